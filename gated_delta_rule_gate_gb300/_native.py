@@ -20,7 +20,9 @@ DEVERR_BAD_SLOT, DEVERR_TIMEOUT, DEVERR_OVERLAP, DEVERR_DECAY_RANGE = 0x1, 0x2, 
 
 EXPORTS = ("gdn_gate", "gdn_recurrent_step", "gdn_chunked_prefill_workspace_size",
            "gdn_chunked_prefill_workspace_size_min", "gdn_chunked_prefill", "gdn_chunked_prefill_noalloc",
-           "gdn_status_string", "gdn_last_error_message")
+           "gdn_status_string", "gdn_last_error_message", "gdn_scan", "gdn_scan_step")
+INPUT_SCALES = {"none": 0, "lerp": 1, "unit": 2}
+SCAN_CHUNK = 64
 
 _vp = ctypes.c_void_p
 
@@ -49,6 +51,20 @@ class GdnGateArgs(ctypes.Structure):
         ("n", ctypes.c_int64), ("heads", ctypes.c_int32), ("dtype", ctypes.c_int32),
         ("a", _vp), ("dt_bias", _vp), ("decay_scale", _vp), ("b", _vp),
         ("decay_out", _vp), ("beta_out", _vp),
+    ]
+
+
+class GdnScanArgs(ctypes.Structure):
+    """Mirror of ``gdn_scan_args`` (include/gdn.h)."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("total_tokens", ctypes.c_int32), ("seq_len", ctypes.c_int32),
+        ("channels", ctypes.c_int32), ("num_state_rows", ctypes.c_int32), ("act_dtype", ctypes.c_int32),
+        ("gate_dtype", ctypes.c_int32), ("input_scale", ctypes.c_int32), ("flags", ctypes.c_uint32),
+        ("x_stride", ctypes.c_int64), ("decay_stride", ctypes.c_int64), ("beta_stride", ctypes.c_int64),
+        ("o_stride", ctypes.c_int64),
+        ("x", _vp), ("decay", _vp), ("beta", _vp), ("o", _vp), ("gate_bias", _vp), ("gate_scale", _vp),
+        ("cu_seqlens", _vp), ("seq_lens", _vp), ("slot_ids", _vp), ("initial_state", _vp),
+        ("final_state", _vp), ("chunk_states", _vp), ("error_word", _vp),
     ]
 
 
@@ -94,6 +110,9 @@ def load():
         lib.gdn_chunked_prefill.restype = ctypes.c_int
         lib.gdn_chunked_prefill_noalloc.argtypes = [ctypes.POINTER(GdnProblem), ctypes.c_int32, _vp]
         lib.gdn_chunked_prefill_noalloc.restype = ctypes.c_int
+        for name, args in (("gdn_scan", GdnScanArgs), ("gdn_scan_step", GdnScanArgs)):
+            getattr(lib, name).argtypes = [ctypes.POINTER(args), _vp]
+            getattr(lib, name).restype = ctypes.c_int
         lib.gdn_status_string.argtypes = [ctypes.c_int]
         lib.gdn_status_string.restype = ctypes.c_char_p
         lib.gdn_last_error_message.argtypes = []

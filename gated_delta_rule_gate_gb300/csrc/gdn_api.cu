@@ -19,10 +19,13 @@
 
 #include "../../include/gdn.h"
 #include "launch.h"
+#include "status.h"
 
 namespace {
-
 thread_local char g_msg[512] = "";
+}  // namespace
+
+namespace gdn {
 
 gdn_status fail(gdn_status st, const char *fmt, ...) {
     va_list ap;
@@ -37,7 +40,19 @@ gdn_status ok() {
     return GDN_OK;
 }
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+gdn_status cuda_status(cudaError_t e) {
+    if (e == cudaSuccess) return ok();
+    return fail(GDN_ERR_CUDA, "CUDA error: %s", cudaGetErrorString(e));
+}
+
+}  // namespace gdn
+
+using gdn::aligned;
+using gdn::cuda_status;
+using gdn::fail;
+using gdn::ok;
+
+namespace {
 
 // Library-owned scratch of gdn_chunked_prefill_noalloc: one per device, set
 // aside when the module loads, so that entry point allocates nothing.  Every
@@ -192,11 +207,6 @@ gdn_status validate(const gdn_problem *p, gdn::Problem *out) {
     return GDN_OK;
 }
 
-gdn_status cuda_status(cudaError_t e) {
-    if (e == cudaSuccess) return ok();
-    return fail(GDN_ERR_CUDA, "CUDA error: %s", cudaGetErrorString(e));
-}
-
 }  // namespace
 
 namespace gdn {
@@ -239,6 +249,18 @@ cudaError_t blocks_per_sm(const void *fn, int threads, size_t smem, int *n) {
     g_attr[key] = per_sm;
     *n = per_sm;
     return cudaSuccess;
+}
+
+cudaError_t large_clusters(const void *fn) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(g_attr_mu);
+    const auto key = std::make_tuple(dev, fn, (size_t)1 << 61);
+    if (g_attr.count(key)) return cudaSuccess;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) g_attr[key] = 0;
+    return e;
 }
 
 int sm_count() {

@@ -27,6 +27,8 @@ int sm_count();
 cudaError_t smem_attr(const void *fn, int bytes);
 // Resident blocks per SM of a kernel at a launch shape (at least 1; cached).
 cudaError_t blocks_per_sm(const void *fn, int threads, size_t smem, int *n);
+// Allows a kernel clusters of up to 16 blocks, once per (device, kernel).
+cudaError_t large_clusters(const void *fn);
 
 cudaError_t launch_gate(const GateLaunch &g, cudaStream_t stream);
 cudaError_t launch_recurrent(const Problem &p, cudaStream_t stream);

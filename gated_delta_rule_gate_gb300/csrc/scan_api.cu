@@ -1,0 +1,143 @@
+// scan_api.cu -- the C entry points of the gated linear recurrence: host-side
+// validation and dispatch.  Every check runs before anything is enqueued.
+#include "launch.h"
+#include "scan_launch.h"
+#include "status.h"
+
+namespace {
+
+using gdn::aligned;
+using gdn::fail;
+using gdn::scan::Args;
+
+size_t size_of(int dt) { return dt == GDN_DTYPE_F32 ? 4 : 2; }
+
+gdn_status check_types(const gdn_scan_args *a) {
+    if (a->act_dtype != GDN_DTYPE_F32 && a->act_dtype != GDN_DTYPE_F16 && a->act_dtype != GDN_DTYPE_BF16)
+        return fail(GDN_ERR_INVALID, "act_dtype: unknown dtype %d", a->act_dtype);
+    if (a->gate_dtype != GDN_DTYPE_F32 && a->gate_dtype != a->act_dtype)
+        return fail(GDN_ERR_INVALID, "gate_dtype must be F32 or the activation dtype");
+    if (a->input_scale < GDN_INPUT_SCALE_NONE || a->input_scale > GDN_INPUT_SCALE_UNIT)
+        return fail(GDN_ERR_INVALID, "unknown input_scale %d", a->input_scale);
+    if (a->flags & ~GDN_FLAG_BETA_SIGMOID) return fail(GDN_ERR_INVALID, "unknown flag bits 0x%x", a->flags);
+    if ((a->flags & GDN_FLAG_BETA_SIGMOID) && !a->beta)
+        return fail(GDN_ERR_INVALID, "GDN_FLAG_BETA_SIGMOID given without beta");
+    return GDN_OK;
+}
+
+gdn_status check_stride(int64_t stride, int channels, const char *what, int64_t *out) {
+    if (stride != 0 && stride < channels)
+        return fail(GDN_ERR_INVALID, "%s_stride (%lld) is less than channels (%d)", what, (long long)stride, channels);
+    *out = stride ? stride : channels;
+    return GDN_OK;
+}
+
+// Sizes, token layout, gates, states and alignment, shared by every entry point.
+// `needs_o`: the call writes o.
+gdn_status validate(const gdn_scan_args *a, bool needs_o, Args *out) {
+    if (!a) return fail(GDN_ERR_INVALID, "args is NULL");
+    if (a->batch < 0) return fail(GDN_ERR_INVALID, "batch must be >= 0 (got %d)", a->batch);
+    if (a->total_tokens < 0) return fail(GDN_ERR_INVALID, "total_tokens must be >= 0");
+    if (a->channels <= 0) return fail(GDN_ERR_INVALID, "channels must be positive (got %d)", a->channels);
+    if (a->channels > (1 << 24)) return fail(GDN_ERR_UNSUPPORTED, "more than 2^24 channels are not supported");
+    gdn_status st = check_types(a);
+    if (st != GDN_OK) return st;
+    if (a->seq_len < 0) return fail(GDN_ERR_INVALID, "seq_len must be >= 0");
+    if (a->seq_len > 0) {
+        if (a->cu_seqlens) return fail(GDN_ERR_INVALID, "cu_seqlens requires the packed form; seq_len must be 0");
+        if ((long long)a->batch * a->seq_len != a->total_tokens)
+            return fail(GDN_ERR_INVALID, "uniform form: total_tokens (%d) != batch * seq_len (%d * %d)",
+                        a->total_tokens, a->batch, a->seq_len);
+    } else if (a->seq_lens) {
+        return fail(GDN_ERR_INVALID, "seq_lens requires the uniform form; seq_len must be > 0");
+    } else if (!a->cu_seqlens && a->batch > 0 && a->total_tokens % a->batch != 0) {
+        return fail(GDN_ERR_INVALID, "uniform packing: total_tokens (%d) is not a multiple of batch (%d)",
+                    a->total_tokens, a->batch);
+    }
+    if ((a->gate_bias == nullptr) != (a->gate_scale == nullptr))
+        return fail(GDN_ERR_INVALID, "gate_bias and gate_scale must be given together (raw-gate arm) or not at all");
+    if (a->num_state_rows < 0) return fail(GDN_ERR_INVALID, "num_state_rows must be >= 0");
+    const int rows = a->num_state_rows ? a->num_state_rows : a->batch;
+    if (!a->slot_ids && rows < a->batch)
+        return fail(GDN_ERR_INVALID, "num_state_rows (%d) < batch (%d) without slot_ids", rows, a->batch);
+    if (a->batch > 0 && a->total_tokens > 0 && (!a->x || !a->decay || (needs_o && !a->o)))
+        return fail(GDN_ERR_INVALID, needs_o ? "x, decay and o are required" : "x and decay are required");
+    Args &p = *out;
+    if ((st = check_stride(a->x_stride, a->channels, "x", &p.xs)) != GDN_OK) return st;
+    if ((st = check_stride(a->decay_stride, a->channels, "decay", &p.gs)) != GDN_OK) return st;
+    if ((st = check_stride(a->beta_stride, a->channels, "beta", &p.bs)) != GDN_OK) return st;
+    if ((st = check_stride(a->o_stride, a->channels, "o", &p.os)) != GDN_OK) return st;
+    const size_t ea = size_of(a->act_dtype), eg = size_of(a->gate_dtype);
+    if (!aligned(a->x, ea) || !aligned(a->o, ea) || !aligned(a->decay, eg) || !aligned(a->beta, eg) ||
+        !aligned(a->gate_bias, 4) || !aligned(a->gate_scale, 4) || !aligned(a->cu_seqlens, 4) ||
+        !aligned(a->seq_lens, 4) || !aligned(a->slot_ids, 4) || !aligned(a->initial_state, 4) ||
+        !aligned(a->final_state, 4) || !aligned(a->chunk_states, 4) || !aligned(a->error_word, 4))
+        return fail(GDN_ERR_INVALID, "a pointer is not aligned to its element size");
+    p.B = a->batch;
+    p.T = a->total_tokens;
+    p.L = a->seq_len ? a->seq_len : (a->cu_seqlens || a->batch == 0 ? 0 : a->total_tokens / a->batch);
+    p.D = a->channels;
+    p.rows = rows;
+    p.mode = a->input_scale;
+    p.sigmoid = (a->flags & GDN_FLAG_BETA_SIGMOID) != 0;
+    p.x = a->x, p.decay = a->decay, p.beta = a->beta, p.o = a->o;
+    p.bias = a->gate_bias, p.scale = a->gate_scale;
+    p.cu = a->cu_seqlens, p.seqlens = a->seq_lens, p.slots = a->slot_ids;
+    p.init = a->initial_state, p.fin = a->final_state, p.chunk = a->chunk_states;
+    p.err = a->error_word;
+    auto word = [](const void *q, size_t e, int64_t stride, int n) {
+        return q == nullptr || (aligned(q, n * e) && stride % n == 0);
+    };
+    p.vec = p.D % 2 == 0 && word(a->x, ea, p.xs, 2) && word(a->o, ea, p.os, 2) && word(a->decay, eg, p.gs, 2) &&
+            word(a->beta, eg, p.bs, 2);
+    return GDN_OK;
+}
+
+// Groups of four channels can be read and written as one word (gdn_scan_step).
+bool four_wide(const Args &p, const gdn_scan_args *a) {
+    const size_t ea = size_of(a->act_dtype), eg = size_of(a->gate_dtype);
+    auto word = [](const void *q, size_t e, int64_t stride) {
+        return q == nullptr || (aligned(q, 4 * e) && stride % 4 == 0);
+    };
+    return p.D % 4 == 0 && word(a->x, ea, p.xs) && word(a->o, ea, p.os) && word(a->decay, eg, p.gs) &&
+           word(a->beta, eg, p.bs) && word(a->gate_bias, 4, 0) && word(a->gate_scale, 4, 0) &&
+           word(a->initial_state, 4, 0) && word(a->final_state, 4, 0);
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_scan(const gdn_scan_args *a, gdn_stream stream) {
+    Args p;
+    const gdn_status st = validate(a, true, &p);
+    if (st != GDN_OK) return st;
+    if (p.B == 0) return gdn::ok();
+    return gdn::cuda_status(gdn::scan::launch_scan(p, a->act_dtype, a->gate_dtype, (cudaStream_t)stream));
+}
+
+gdn_status gdn_scan_step(const gdn_scan_args *a, gdn_stream stream) {
+    Args p;
+    const gdn_status st = validate(a, true, &p);
+    if (st != GDN_OK) return st;
+    if (a->chunk_states) return fail(GDN_ERR_INVALID, "chunk_states are kept by gdn_scan only");
+    if ((long long)p.B * p.D > (1LL << 37))
+        return fail(GDN_ERR_UNSUPPORTED, "batch * channels exceeds 2^37");
+    if (p.B == 0) return gdn::ok();
+    return gdn::cuda_status(
+        gdn::scan::launch_step(p, a->act_dtype, a->gate_dtype, four_wide(p, a), (cudaStream_t)stream));
+}
+
+}  // extern "C"
+
+namespace gdn {
+namespace scan {
+
+cudaError_t launch_scan(const Args &p, int act, int gate, cudaStream_t stream) {
+    if (act == GDN_DTYPE_F32) return launch_scan_f32(p, stream);
+    return act == GDN_DTYPE_F16 ? launch_scan_f16(p, gate == GDN_DTYPE_F32, stream)
+                                : launch_scan_bf16(p, gate == GDN_DTYPE_F32, stream);
+}
+
+}  // namespace scan
+}  // namespace gdn

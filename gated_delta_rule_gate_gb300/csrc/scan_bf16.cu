@@ -1,0 +1,12 @@
+// scan_bf16.cu -- gdn_scan for bf16 activations.
+#include "scan_fwd.cuh"
+
+namespace gdn {
+namespace scan {
+
+cudaError_t launch_scan_bf16(const Args &p, bool gate_f32, cudaStream_t stream) {
+    return gate_f32 ? launch_types<__nv_bfloat16, float>(p, stream) : launch_types<__nv_bfloat16, __nv_bfloat16>(p, stream);
+}
+
+}  // namespace scan
+}  // namespace gdn

@@ -1,0 +1,12 @@
+// scan_f16.cu -- gdn_scan for f16 activations.
+#include "scan_fwd.cuh"
+
+namespace gdn {
+namespace scan {
+
+cudaError_t launch_scan_f16(const Args &p, bool gate_f32, cudaStream_t stream) {
+    return gate_f32 ? launch_types<__half, float>(p, stream) : launch_types<__half, __half>(p, stream);
+}
+
+}  // namespace scan
+}  // namespace gdn

@@ -1,0 +1,163 @@
+"""Python binding of the recurrent-layer operators, over torch tensors.
+
+As in the rest of the binding, these functions read shapes, strides, dtypes and
+pointers, fill the C structs of include/gdn.h and call the library on the current
+stream (or ``stream``); what they allocate when an output is not given is torch
+memory of that stream.  float32, float16 and bfloat16 tensors are taken.
+"""
+import contextlib
+import ctypes
+
+import torch
+
+from . import _native as N
+
+_DT = {torch.float32: N.DTYPE_F32, torch.float16: N.DTYPE_F16, torch.bfloat16: N.DTYPE_BF16}
+
+
+def _handle(stream):
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(stream):
+    """Memory made inside belongs to the stream that the kernels run on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _dtype(t, what):
+    try:
+        return _DT[t.dtype]
+    except KeyError:
+        raise TypeError("%s: unsupported dtype %s" % (what, t.dtype)) from None
+
+
+def _ptr(t, dtype, what, shape=None):
+    """Address of a contiguous device tensor of the given dtype, or None."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("libgdn takes device tensors; %s is on %s" % (what, t.device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s" % (what, dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _rows(t, shape, what):
+    """(address, elements between rows) of a device tensor whose last dimension
+    is contiguous and whose leading ones lie in it as one."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError("libgdn takes device tensors; %s is on %s" % (what, t.device))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    if t.stride(-1) != 1 and shape[-1] != 1:
+        raise ValueError("%s must have contiguous channels" % what)
+    step = t.stride(-2)
+    if t.dim() == 3 and shape[0] > 1:
+        if shape[1] == 1:
+            step = t.stride(0)
+        elif t.stride(0) != shape[1] * step:
+            raise ValueError("%s must have one stride over all tokens" % what)
+    return t.data_ptr(), step
+
+
+def _scan_args(x, decay, beta, gate_bias, gate_scale, beta_sigmoid, input_scale, cu_seqlens, seq_lens, slot_ids,
+               initial_state, final_state, out, chunk_states, error_word):
+    shape = x.shape
+    dim = len(shape)
+    act, gate = _dtype(x, "x"), _dtype(decay, "decay")
+    if dim == 2:
+        T, D = shape
+        seq_len = 0
+        B = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+        if B < 0:
+            raise ValueError("cu_seqlens must have batch + 1 entries")
+    elif dim == 3:
+        B, seq_len, D = shape
+        T = B * seq_len
+        if cu_seqlens is not None:
+            raise ValueError("cu_seqlens goes with packed tokens, x [tokens, channels]")
+    else:
+        raise ValueError("x must be [tokens, channels] or [batch, tokens, channels]")
+    if input_scale not in N.INPUT_SCALES:
+        raise ValueError("input_scale must be one of %s" % ", ".join(N.INPUT_SCALES))
+    if beta is not None and beta.dtype != decay.dtype:
+        raise TypeError("beta must have the dtype of decay")
+    if out is not None and out.dtype != x.dtype:
+        raise TypeError("out must have the dtype of x")
+    xp, xs = _rows(x, shape, "x")
+    gp, gs = _rows(decay, shape, "decay")
+    bp, bs = _rows(beta, shape, "beta")
+    op, os = _rows(out, shape, "out")
+    state = initial_state if initial_state is not None else final_state
+    rows = 0
+    if state is not None:
+        if state.dim() != 2 or state.shape[1] != D:
+            raise ValueError("states must be [rows, %d]" % D)
+        rows = state.shape[0]
+    f32, i32 = torch.float32, torch.int32
+    return N.GdnScanArgs(
+        B, T, seq_len, D, rows, act, gate, N.INPUT_SCALES[input_scale],
+        N.FLAG_BETA_SIGMOID if beta_sigmoid else 0, xs, gs, bs, os, xp, gp, bp, op,
+        _ptr(gate_bias, f32, "gate_bias", (D,)), _ptr(gate_scale, f32, "gate_scale", (D,)),
+        _ptr(cu_seqlens, i32, "cu_seqlens"), _ptr(seq_lens, i32, "seq_lens", (B,)),
+        _ptr(slot_ids, i32, "slot_ids", (B,)), _ptr(initial_state, f32, "initial_state"),
+        _ptr(final_state, f32, "final_state", None if state is None else state.shape),
+        _ptr(chunk_states, f32, "chunk_states", (-(-T // N.SCAN_CHUNK), D)), _ptr(error_word, i32, "error_word"))
+
+
+def gdn_scan(x, decay, *, beta=None, gate_bias=None, gate_scale=None, beta_sigmoid=False, input_scale="none",
+             cu_seqlens=None, seq_lens=None, slot_ids=None, initial_state=None, final_state=None, out=None,
+             want_chunk_states=False, error_word=None, stream=None):
+    """The gated linear recurrence over whole sequences, per channel
+
+        g = decay, or gate_scale * softplus(decay + gate_bias);  a = exp(g)
+        h_t = a h_{t-1} + n i x_t;  out_t = h_t
+
+    with i = 1, ``beta`` or sigmoid(``beta``) and n = 1, 1 - a ("lerp") or
+    sqrt(1 - a^2) ("unit").  x, decay and beta are [T, D] packed (requests by
+    ``cu_seqlens``, else one) or [B, S, D] (``seq_lens`` bounds the rows); they may
+    be columns of wider tensors.  States are fp32 [rows, D], row ``slot_ids[b]`` or
+    b; ``final_state`` is written if given and may be ``initial_state``.  Returns
+    out (allocated when not given; tokens of no request are not written), or (out,
+    chunk_states) with ``want_chunk_states``, for gdn_scan_backward."""
+    chunks = None
+    if out is None or want_chunk_states:
+        with _on(stream):
+            if out is None:
+                out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            if want_chunk_states:
+                D = x.shape[-1]
+                chunks = torch.empty(-(-x.numel() // max(D, 1) // N.SCAN_CHUNK), D, device=x.device)
+    args = _scan_args(x, decay, beta, gate_bias, gate_scale, beta_sigmoid, input_scale, cu_seqlens, seq_lens,
+                      slot_ids, initial_state, final_state, out, chunks, error_word)
+    N.check(N.load().gdn_scan(args, _handle(stream)))
+    return (out, chunks) if want_chunk_states else out
+
+
+def gdn_scan_step(x, decay, *, beta=None, gate_bias=None, gate_scale=None, beta_sigmoid=False, input_scale="none",
+                  cu_seqlens=None, seq_lens=None, slot_ids=None, initial_state=None, final_state=None, out=None,
+                  error_word=None, stream=None):
+    """gdn_scan for one or a few tokens a request (time grows with the longest):
+    the serving step, usually with ``initial_state`` and ``final_state`` one slab
+    that ``slot_ids`` address."""
+    if out is None:
+        with _on(stream):
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    args = _scan_args(x, decay, beta, gate_bias, gate_scale, beta_sigmoid, input_scale, cu_seqlens, seq_lens,
+                      slot_ids, initial_state, final_state, out, None, error_word)
+    N.check(N.load().gdn_scan_step(args, _handle(stream)))
+    return out

@@ -314,6 +314,98 @@ gdn_status gdn_chunked_prefill(const gdn_problem *p, int32_t chunk_size, void *w
  */
 gdn_status gdn_chunked_prefill_noalloc(const gdn_problem *p, int32_t chunk_size, gdn_stream stream);
 
+/*
+ * Recurrent-layer operators: what a layer runs around and instead of the
+ * matrix-state recurrence -- a gated linear recurrence of vector state with its
+ * gradient, the norm at the layer's entry, the clipping of the gradients.  The
+ * reference pages define none of them (the gate's raw arm is theirs).  They
+ * take F32, F16 and BF16 tensors.
+ */
+
+/* Scale n of a token's input in gdn_scan. */
+typedef enum gdn_input_scale {
+    GDN_INPUT_SCALE_NONE = 0, /* n = 1 */
+    GDN_INPUT_SCALE_LERP = 1, /* n = 1 - a: the state is a running mean */
+    GDN_INPUT_SCALE_UNIT = 2  /* n = sqrt(1 - a^2): unit-variance inputs keep the state at unit variance */
+} gdn_input_scale;
+
+/* Tokens between two entries of gdn_scan's chunk_states. */
+#define GDN_SCAN_CHUNK 64
+
+/*
+ * One call of the gated linear recurrence, per token t and channel c:
+ *
+ *     g   = decay                                  (gate_bias == gate_scale == NULL)
+ *     g   = gate_scale[c] * softplus(decay + gate_bias[c])   (both given: the raw arm)
+ *     a   = exp(g)
+ *     i   = 1 | beta | sigmoid(beta)               (beta NULL | given | GDN_FLAG_BETA_SIGMOID)
+ *     n   = 1 | 1 - a | sqrt(max(0, 1 - a^2))      (input_scale)
+ *     h_t = a h_{t-1} + n i x_t,   o_t = h_t
+ *
+ * The state h is fp32; o is rounded once.  g <= 0 is expected (g = -inf forgets
+ * the past; g > 0 grows the state and makes n <= 0 with LERP and 0 with UNIT).
+ *
+ * Tokens and requests are those of gdn_problem: seq_len == 0 is the packed form
+ * ([total_tokens, channels]; request b owns tokens [cu_seqlens[b],
+ * cu_seqlens[b + 1]), each clamped to [0, total_tokens]; cu_seqlens NULL: batch
+ * requests of total_tokens / batch), seq_len > 0 the uniform form ([batch,
+ * seq_len, channels]), which seq_lens makes padded.  Here the clamped offsets
+ * must not decrease (equal ones: an empty request); a decreasing pair sets
+ * GDN_DEVERR_OVERLAP and the results of that call are unspecified (in bounds).
+ * Tokens of no request are neither read nor written.
+ *
+ * x, decay, beta and o have channels contiguous and *_stride elements from one
+ * token to the next (0: channels), so that they may be columns of a wider
+ * matrix; a stride must be at least channels.  o overlaps no input.
+ *
+ * States are [num_state_rows, channels] fp32, rows by slot_ids or by request, as
+ * in gdn_problem: initial_state NULL is zero; final_state may be NULL, may equal
+ * initial_state, and receives an empty request's initial state.  A bad slot id
+ * skips the request and sets GDN_DEVERR_BAD_SLOT.
+ *
+ * chunk_states (gdn_scan only; NULL: not kept) is fp32
+ * [ceil(total_tokens / GDN_SCAN_CHUNK), channels]: entry j receives the state
+ * before token j * GDN_SCAN_CHUNK, which gdn_scan_backward reads; entries whose
+ * token begins a request, or belongs to none, hold no meaning.
+ */
+typedef struct gdn_scan_args {
+    int32_t batch;
+    int32_t total_tokens;
+    int32_t seq_len;        /* 0: packed; > 0: uniform */
+    int32_t channels;
+    int32_t num_state_rows; /* 0 means batch */
+    int32_t act_dtype;      /* of x and o */
+    int32_t gate_dtype;     /* of decay and beta: F32 or act_dtype */
+    int32_t input_scale;    /* gdn_input_scale */
+    uint32_t flags;         /* GDN_FLAG_BETA_SIGMOID or 0 */
+    int64_t x_stride;
+    int64_t decay_stride;
+    int64_t beta_stride;
+    int64_t o_stride;
+    const void *x;
+    const void *decay;
+    const void *beta;        /* or NULL */
+    void *o;
+    const float *gate_bias;  /* [channels], with gate_scale, or NULL */
+    const float *gate_scale; /* [channels] */
+    const int32_t *cu_seqlens;
+    const int32_t *seq_lens;
+    const int32_t *slot_ids;
+    const float *initial_state;
+    float *final_state;
+    float *chunk_states;
+    int32_t *error_word;
+} gdn_scan_args;
+
+/* gdn_scan -- the recurrence, parallel over channels and along time: one launch,
+ * no workspace, the same bits on every run.  For prefill and training. */
+gdn_status gdn_scan(const gdn_scan_args *args, gdn_stream stream);
+
+/* gdn_scan_step -- the same result with the tokens of a request taken one after
+ * another, for calls of one or a few tokens a request (chunk_states must be
+ * NULL).  The arithmetic of a token is gdn_scan's. */
+gdn_status gdn_scan_step(const gdn_scan_args *args, gdn_stream stream);
+
 /* Static description of a status code ("ok", "invalid argument", ...). */
 const char *gdn_status_string(gdn_status status);
 
