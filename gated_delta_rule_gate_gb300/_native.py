@@ -20,7 +20,8 @@ DEVERR_BAD_SLOT, DEVERR_TIMEOUT, DEVERR_OVERLAP, DEVERR_DECAY_RANGE = 0x1, 0x2, 
 
 EXPORTS = ("gdn_gate", "gdn_recurrent_step", "gdn_chunked_prefill_workspace_size",
            "gdn_chunked_prefill_workspace_size_min", "gdn_chunked_prefill", "gdn_chunked_prefill_noalloc",
-           "gdn_status_string", "gdn_last_error_message", "gdn_scan", "gdn_scan_step")
+           "gdn_status_string", "gdn_last_error_message", "gdn_scan", "gdn_scan_step",
+           "gdn_scan_backward")
 INPUT_SCALES = {"none": 0, "lerp": 1, "unit": 2}
 SCAN_CHUNK = 64
 
@@ -68,6 +69,17 @@ class GdnScanArgs(ctypes.Structure):
     ]
 
 
+class GdnScanGradArgs(ctypes.Structure):
+    """Mirror of ``gdn_scan_grad_args`` (include/gdn.h)."""
+    _fields_ = [
+        ("forward", GdnScanArgs),
+        ("d_o_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64), ("d_decay_stride", ctypes.c_int64),
+        ("d_beta_stride", ctypes.c_int64),
+        ("d_o", _vp), ("d_final_state", _vp), ("dx", _vp), ("d_decay", _vp), ("d_beta", _vp),
+        ("d_gate_bias", _vp), ("d_gate_scale", _vp), ("d_initial_state", _vp),
+    ]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status, message):
         self.status = status
@@ -110,7 +122,8 @@ def load():
         lib.gdn_chunked_prefill.restype = ctypes.c_int
         lib.gdn_chunked_prefill_noalloc.argtypes = [ctypes.POINTER(GdnProblem), ctypes.c_int32, _vp]
         lib.gdn_chunked_prefill_noalloc.restype = ctypes.c_int
-        for name, args in (("gdn_scan", GdnScanArgs), ("gdn_scan_step", GdnScanArgs)):
+        for name, args in (("gdn_scan", GdnScanArgs), ("gdn_scan_step", GdnScanArgs),
+                           ("gdn_scan_backward", GdnScanGradArgs)):
             getattr(lib, name).argtypes = [ctypes.POINTER(args), _vp]
             getattr(lib, name).restype = ctypes.c_int
         lib.gdn_status_string.argtypes = [ctypes.c_int]

@@ -30,6 +30,16 @@ struct Args {
     int32_t *err;
 };
 
+// A validated call of gdn_scan_backward.
+struct GradArgs {
+    Args f;  // the forward call; chunk is read
+    int64_t dos, dxs, dgs, dbs;
+    const void *d_o;
+    const float *dfin;
+    void *dx, *dg, *db;
+    float *dbias, *dscale, *dinit;
+};
+
 // Two adjacent channels of one token, as stored.
 template <typename T>
 struct Pair;
@@ -197,6 +207,43 @@ template <bool RAW>
 __device__ __forceinline__ float log_decay(float z, float bias, float scale) {
     return RAW ? scale * softplus(z + bias) : z;
 }
+// What the gradient needs of one token's gates: a, n, dn/dg, i, di/dbeta,
+// softplus, dg/ddecay.
+struct Terms {
+    float a, n, dn, i, di, soft, dgdz;
+};
+template <bool RAW, bool BETA, int MODE>
+__device__ __forceinline__ Terms gate_terms(float z, float y, float bias, float scale, bool sig) {
+    Terms t;
+    float g = z;
+    t.soft = 0.f;
+    t.dgdz = 1.f;
+    if constexpr (RAW) {
+        z += bias;
+        t.soft = softplus(z);
+        g = scale * t.soft;
+        t.dgdz = scale * sigmoid(z);
+    }
+    t.a = expf(g);
+    t.n = 1.f;
+    t.dn = 0.f;
+    if constexpr (MODE == kLerp) {
+        t.n = -expm1f(g);
+        t.dn = -t.a;
+    }
+    if constexpr (MODE == kUnit) {  // where n is 0 (a >= 1) its slope is taken as 0
+        t.n = sqrtf(fmaxf(0.f, -expm1f(2.f * g)));
+        t.dn = t.n > 0.f ? -t.a * t.a / t.n : 0.f;
+    }
+    t.i = 1.f;
+    t.di = 0.f;
+    if constexpr (BETA) {
+        t.i = sig ? sigmoid(y) : y;
+        t.di = sig ? t.i * (1.f - t.i) : 1.f;
+    }
+    return t;
+}
+
 // n of the input x; a = exp(g).
 template <int MODE>
 __device__ __forceinline__ float input_scale(float g, float a) {

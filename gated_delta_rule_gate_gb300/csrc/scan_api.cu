@@ -32,6 +32,9 @@ gdn_status check_stride(int64_t stride, int channels, const char *what, int64_t 
     return GDN_OK;
 }
 
+// Pairs of elements at even places of q's rows are aligned words.
+bool pairs(const void *q, size_t e, int64_t stride) { return q == nullptr || (aligned(q, 2 * e) && stride % 2 == 0); }
+
 // Sizes, token layout, gates, states and alignment, shared by every entry point.
 // `needs_o`: the call writes o.
 gdn_status validate(const gdn_scan_args *a, bool needs_o, Args *out) {
@@ -85,11 +88,8 @@ gdn_status validate(const gdn_scan_args *a, bool needs_o, Args *out) {
     p.cu = a->cu_seqlens, p.seqlens = a->seq_lens, p.slots = a->slot_ids;
     p.init = a->initial_state, p.fin = a->final_state, p.chunk = a->chunk_states;
     p.err = a->error_word;
-    auto word = [](const void *q, size_t e, int64_t stride, int n) {
-        return q == nullptr || (aligned(q, n * e) && stride % n == 0);
-    };
-    p.vec = p.D % 2 == 0 && word(a->x, ea, p.xs, 2) && word(a->o, ea, p.os, 2) && word(a->decay, eg, p.gs, 2) &&
-            word(a->beta, eg, p.bs, 2);
+    p.vec = p.D % 2 == 0 && pairs(a->x, ea, p.xs) && (!needs_o || pairs(a->o, ea, p.os)) &&
+            pairs(a->decay, eg, p.gs) && pairs(a->beta, eg, p.bs);
     return GDN_OK;
 }
 
@@ -128,6 +128,41 @@ gdn_status gdn_scan_step(const gdn_scan_args *a, gdn_stream stream) {
         gdn::scan::launch_step(p, a->act_dtype, a->gate_dtype, four_wide(p, a), (cudaStream_t)stream));
 }
 
+gdn_status gdn_scan_backward(const gdn_scan_grad_args *a, gdn_stream stream) {
+    if (!a) return fail(GDN_ERR_INVALID, "args is NULL");
+    gdn::scan::GradArgs q;
+    gdn_status st = validate(&a->forward, false, &q.f);
+    if (st != GDN_OK) return st;
+    Args &p = q.f;
+    if ((st = check_stride(a->d_o_stride, p.D, "d_o", &q.dos)) != GDN_OK) return st;
+    if ((st = check_stride(a->dx_stride, p.D, "dx", &q.dxs)) != GDN_OK) return st;
+    if ((st = check_stride(a->d_decay_stride, p.D, "d_decay", &q.dgs)) != GDN_OK) return st;
+    if ((st = check_stride(a->d_beta_stride, p.D, "d_beta", &q.dbs)) != GDN_OK) return st;
+    if ((a->d_beta != nullptr) != (p.beta != nullptr))
+        return fail(GDN_ERR_INVALID, p.beta ? "d_beta is required" : "d_beta given without beta");
+    if ((a->d_gate_bias || a->d_gate_scale) && !p.bias)
+        return fail(GDN_ERR_INVALID, "d_gate_bias and d_gate_scale belong to the raw-gate arm");
+    if (p.B > 0 && p.T > 0) {
+        if (!a->d_o || !a->dx || !a->d_decay) return fail(GDN_ERR_INVALID, "d_o, dx and d_decay are required");
+        if (!p.chunk) return fail(GDN_ERR_INVALID, "chunk_states of the forward call are required");
+    }
+    const size_t ea = size_of(a->forward.act_dtype), eg = size_of(a->forward.gate_dtype);
+    if (!aligned(a->d_o, ea) || !aligned(a->dx, ea) || !aligned(a->d_decay, eg) || !aligned(a->d_beta, eg) ||
+        !aligned(a->d_final_state, 4) || !aligned(a->d_gate_bias, 4) || !aligned(a->d_gate_scale, 4) ||
+        !aligned(a->d_initial_state, 4))
+        return fail(GDN_ERR_INVALID, "a pointer is not aligned to its element size");
+    q.d_o = a->d_o, q.dfin = a->d_final_state;
+    q.dx = a->dx, q.dg = a->d_decay, q.db = a->d_beta;
+    q.dbias = a->d_gate_bias, q.dscale = a->d_gate_scale, q.dinit = a->d_initial_state;
+    p.fin = nullptr;
+    p.o = nullptr;
+    p.vec = p.vec && pairs(a->d_o, ea, q.dos) && pairs(a->dx, ea, q.dxs) && pairs(a->d_decay, eg, q.dgs) &&
+            pairs(a->d_beta, eg, q.dbs);
+    if (p.B == 0 && !q.dbias && !q.dscale) return gdn::ok();
+    return gdn::cuda_status(
+        gdn::scan::launch_grad(q, a->forward.act_dtype, a->forward.gate_dtype, (cudaStream_t)stream));
+}
+
 }  // extern "C"
 
 namespace gdn {
@@ -137,6 +172,12 @@ cudaError_t launch_scan(const Args &p, int act, int gate, cudaStream_t stream) {
     if (act == GDN_DTYPE_F32) return launch_scan_f32(p, stream);
     return act == GDN_DTYPE_F16 ? launch_scan_f16(p, gate == GDN_DTYPE_F32, stream)
                                 : launch_scan_bf16(p, gate == GDN_DTYPE_F32, stream);
+}
+
+cudaError_t launch_grad(const GradArgs &p, int act, int gate, cudaStream_t stream) {
+    if (act == GDN_DTYPE_F32) return launch_grad_f32(p, stream);
+    return act == GDN_DTYPE_F16 ? launch_grad_f16(p, gate == GDN_DTYPE_F32, stream)
+                                : launch_grad_bf16(p, gate == GDN_DTYPE_F32, stream);
 }
 
 }  // namespace scan

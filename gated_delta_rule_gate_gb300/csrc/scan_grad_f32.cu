@@ -1,0 +1,12 @@
+// scan_grad_f32.cu -- gdn_scan_backward for f32 activations.
+#include "scan_bwd.cuh"
+
+namespace gdn {
+namespace scan {
+
+cudaError_t launch_grad_f32(const GradArgs &p, cudaStream_t stream) {
+    return launch_grad_types<float, float>(p, stream);
+}
+
+}  // namespace scan
+}  // namespace gdn

@@ -13,6 +13,10 @@ cudaError_t launch_scan(const Args &p, int act, int gate, cudaStream_t stream);
 cudaError_t launch_scan_f32(const Args &p, cudaStream_t stream);
 cudaError_t launch_scan_f16(const Args &p, bool gate_f32, cudaStream_t stream);
 cudaError_t launch_scan_bf16(const Args &p, bool gate_f32, cudaStream_t stream);
+cudaError_t launch_grad(const GradArgs &p, int act, int gate, cudaStream_t stream);
+cudaError_t launch_grad_f32(const GradArgs &p, cudaStream_t stream);
+cudaError_t launch_grad_f16(const GradArgs &p, bool gate_f32, cudaStream_t stream);
+cudaError_t launch_grad_bf16(const GradArgs &p, bool gate_f32, cudaStream_t stream);
 
 }  // namespace scan
 }  // namespace gdn

@@ -6,13 +6,15 @@ stream (or ``stream``); what they allocate when an output is not given is torch
 memory of that stream.  float32, float16 and bfloat16 tensors are taken.
 """
 import contextlib
-import ctypes
+from collections import namedtuple
 
 import torch
 
 from . import _native as N
 
 _DT = {torch.float32: N.DTYPE_F32, torch.float16: N.DTYPE_F16, torch.bfloat16: N.DTYPE_BF16}
+
+ScanGradients = namedtuple("ScanGradients", "dx d_decay d_beta d_gate_bias d_gate_scale d_initial_state")
 
 
 def _handle(stream):
@@ -161,3 +163,51 @@ def gdn_scan_step(x, decay, *, beta=None, gate_bias=None, gate_scale=None, beta_
                       slot_ids, initial_state, final_state, out, None, error_word)
     N.check(N.load().gdn_scan_step(args, _handle(stream)))
     return out
+
+
+def gdn_scan_backward(d_out, x, decay, chunk_states, *, beta=None, gate_bias=None, gate_scale=None,
+                      beta_sigmoid=False, input_scale="none", cu_seqlens=None, seq_lens=None, slot_ids=None,
+                      initial_state=None, d_final_state=None, dx=None, d_decay=None, d_beta=None, d_gate_bias=None,
+                      d_gate_scale=None, d_initial_state=None, error_word=None, stream=None):
+    """Gradients of gdn_scan for the gradient ``d_out`` of its output (and
+    ``d_final_state`` of its final states): the forward call's arguments and the
+    chunk_states that it returned.  Returns ScanGradients(dx, d_decay, d_beta,
+    d_gate_bias, d_gate_scale, d_initial_state), None where there is no such input.
+    Outputs are allocated when not given (zeros where tokens or state rows may belong
+    to no request); a given one is not written there."""
+    like = initial_state if initial_state is not None else d_final_state
+    # every token and row is written unless requests may leave some out
+    token = torch.empty_like if cu_seqlens is None and seq_lens is None and slot_ids is None else torch.zeros_like
+    with _on(stream):
+        if dx is None:
+            dx = token(x, memory_format=torch.contiguous_format)
+        if d_decay is None:
+            d_decay = token(decay, memory_format=torch.contiguous_format)
+        if d_beta is None and beta is not None:
+            d_beta = token(beta, memory_format=torch.contiguous_format)
+        if gate_bias is not None:
+            if d_gate_bias is None:
+                d_gate_bias = torch.empty_like(gate_bias)
+            if d_gate_scale is None:
+                d_gate_scale = torch.empty_like(gate_scale)
+        if d_initial_state is None and initial_state is not None:
+            d_initial_state = torch.zeros_like(initial_state)
+    f32, D = torch.float32, x.shape[-1]
+    for t, of, what in ((d_out, x, "d_out"), (dx, x, "dx"), (d_decay, decay, "d_decay"), (d_beta, beta, "d_beta")):
+        if t is not None and of is not None and t.dtype != of.dtype:
+            raise TypeError("%s must be %s" % (what, of.dtype))
+    forward = _scan_args(x, decay, beta, gate_bias, gate_scale, beta_sigmoid, input_scale, cu_seqlens, seq_lens,
+                         slot_ids, like, None, None, chunk_states, error_word)
+    if initial_state is None:
+        forward.initial_state = None
+    dop, dos = _rows(d_out, x.shape, "d_out")
+    dxp, dxs = _rows(dx, x.shape, "dx")
+    dgp, dgs = _rows(d_decay, x.shape, "d_decay")
+    dbp, dbs = _rows(d_beta, x.shape, "d_beta")
+    rows = None if like is None else like.shape
+    args = N.GdnScanGradArgs(
+        forward, dos, dxs, dgs, dbs, dop, _ptr(d_final_state, f32, "d_final_state", rows), dxp, dgp, dbp,
+        _ptr(d_gate_bias, f32, "d_gate_bias", (D,)), _ptr(d_gate_scale, f32, "d_gate_scale", (D,)),
+        _ptr(d_initial_state, f32, "d_initial_state", rows))
+    N.check(N.load().gdn_scan_backward(args, _handle(stream)))
+    return ScanGradients(dx, d_decay, d_beta, d_gate_bias, d_gate_scale, d_initial_state)

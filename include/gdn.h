@@ -406,6 +406,43 @@ gdn_status gdn_scan(const gdn_scan_args *args, gdn_stream stream);
  * NULL).  The arithmetic of a token is gdn_scan's. */
 gdn_status gdn_scan_step(const gdn_scan_args *args, gdn_stream stream);
 
+/*
+ * gdn_scan_backward -- the gradient of gdn_scan, in one launch, with the same
+ * bits on every run.  `forward` is the forward call: its o and final_state are
+ * not used, its chunk_states are read (required when there are tokens).  dh
+ * being the gradient that reaches a token's state,
+ *
+ *     dh_t = d_o_t + a_{t+1} dh_{t+1}   (+ d_final_state[row] at a request's last token)
+ *     dx   = n i dh,   d_beta = n x dh i'(beta)
+ *     dg   = a h_{t-1} dh + n'(g) i x dh       (n'(g) taken as 0 where UNIT's n is 0)
+ *     d_decay = dg,  or in the raw arm  dg gate_scale sigmoid(decay + gate_bias),
+ *     d_gate_bias = sum over tokens of d_decay,  d_gate_scale = sum of dg softplus(decay + gate_bias)
+ *     d_initial_state[row] = a dh at a request's first token (an empty request: d_final_state[row])
+ *
+ * The sums are kept in fp32 and written whole, over the tokens that requests own.
+ * dx and d_o have act_dtype, d_decay and d_beta gate_dtype, the rest fp32.
+ * d_final_state NULL is zero.  d_gate_bias, d_gate_scale and d_initial_state may
+ * be NULL; dx, d_decay, and d_beta where there is a beta, are required.  Tokens
+ * of no request and rows of none are not written.  Outputs overlap no input.
+ */
+typedef struct gdn_scan_grad_args {
+    gdn_scan_args forward;
+    int64_t d_o_stride; /* 0: channels, as in gdn_scan_args */
+    int64_t dx_stride;
+    int64_t d_decay_stride;
+    int64_t d_beta_stride;
+    const void *d_o;
+    const float *d_final_state;
+    void *dx;
+    void *d_decay;
+    void *d_beta;
+    float *d_gate_bias;
+    float *d_gate_scale;
+    float *d_initial_state;
+} gdn_scan_grad_args;
+
+gdn_status gdn_scan_backward(const gdn_scan_grad_args *args, gdn_stream stream);
+
 /* Static description of a status code ("ok", "invalid argument", ...). */
 const char *gdn_status_string(gdn_status status);
 

@@ -68,6 +68,7 @@ def scan(p, grad=None):
         g = {k: torch.full((T, D), math.nan, dtype=torch.double) for k in ("dx", "d_decay", "d_beta")}
         g["d_gate_bias"] = torch.zeros(D, dtype=torch.double)
         g["d_gate_scale"] = torch.zeros(D, dtype=torch.double)
+        g["sum_of_sizes"] = torch.zeros(2, D, dtype=torch.double)  # of the terms of the two sums
         g["d_initial_state"] = torch.full((p["nrows"], D), math.nan, dtype=torch.double)
     for (t0, t1), row in zip(p["spans"], p["rows"]):
         if row is None:
@@ -94,6 +95,7 @@ def scan(p, grad=None):
             if soft is not None:
                 g["d_gate_scale"] += dg * soft
                 g["d_gate_bias"] += dg * dgdz
+                g["sum_of_sizes"] += torch.stack([(dg * dgdz).abs(), (dg * soft).abs()])
             c = a * dh
         g["d_initial_state"][row] = c
     return (out, fin) if g is None else (out, fin, g)
