@@ -6,11 +6,12 @@ Entry points (same names as the C ABI):
     gdn_chunked_prefill_workspace_size, gdn_chunked_prefill_workspace_size_min,
     gdn_chunked_prefill_noalloc, gdn_status_string
 Recurrent-layer operators:
-    gdn_scan, gdn_scan_step, gdn_scan_backward
+    gdn_scan, gdn_scan_step, gdn_scan_backward, gdn_rmsnorm, gdn_rmsnorm_backward, gdn_grad_clip
 """
 from ._native import GdnError, library_path, load  # noqa: F401
 from .api import (gdn_chunked_prefill, gdn_chunked_prefill_noalloc,  # noqa: F401
                   gdn_chunked_prefill_workspace_size, gdn_chunked_prefill_workspace_size_min, gdn_gate,
                   gdn_recurrent_step,
                   gdn_status_string, make_problem)
-from .layer import gdn_scan, gdn_scan_backward, gdn_scan_step  # noqa: F401
+from .layer import (gdn_grad_clip, gdn_rmsnorm, gdn_rmsnorm_backward, gdn_scan,  # noqa: F401
+                    gdn_scan_backward, gdn_scan_step)

@@ -11,17 +11,19 @@ import threading
 from . import build as _build
 
 GDN_OK, GDN_ERR_INVALID, GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE, GDN_ERR_CUDA = range(5)
-DTYPE_F32, DTYPE_F16, DTYPE_BF16 = 0, 1, 2
+DTYPE_F32, DTYPE_F16, DTYPE_BF16, DTYPE_E4M3 = 0, 1, 2, 3
 RULES = {"linear": 0, "gated": 1, "delta": 2, "gated_delta": 3, "gdn2": 4}
 FLAG_L2NORM_Q, FLAG_L2NORM_K, FLAG_BETA_SIGMOID, FLAG_DECAY_PER_KEY = 0x1, 0x2, 0x4, 0x8
 FLAG_BETA_SHARED = 0x10
 FLAG_STATE_KMAJOR = 0x20
 DEVERR_BAD_SLOT, DEVERR_TIMEOUT, DEVERR_OVERLAP, DEVERR_DECAY_RANGE = 0x1, 0x2, 0x4, 0x8
+DEVERR_NONFINITE = 0x10
 
 EXPORTS = ("gdn_gate", "gdn_recurrent_step", "gdn_chunked_prefill_workspace_size",
            "gdn_chunked_prefill_workspace_size_min", "gdn_chunked_prefill", "gdn_chunked_prefill_noalloc",
            "gdn_status_string", "gdn_last_error_message", "gdn_scan", "gdn_scan_step",
-           "gdn_scan_backward")
+           "gdn_scan_backward", "gdn_rmsnorm", "gdn_rmsnorm_backward", "gdn_rmsnorm_backward_workspace_size",
+           "gdn_grad_clip", "gdn_grad_clip_workspace_size")
 INPUT_SCALES = {"none": 0, "lerp": 1, "unit": 2}
 SCAN_CHUNK = 64
 
@@ -80,6 +82,36 @@ class GdnScanGradArgs(ctypes.Structure):
     ]
 
 
+class GdnRmsnormArgs(ctypes.Structure):
+    """Mirror of ``gdn_rmsnorm_args`` (include/gdn.h)."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("dim", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+        ("group", ctypes.c_int32), ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64),
+        ("x", _vp), ("residual", _vp), ("weight", _vp), ("out", _vp), ("residual_out", _vp), ("scales", _vp),
+        ("rstd", _vp),
+    ]
+
+
+class GdnRmsnormGradArgs(ctypes.Structure):
+    """Mirror of ``gdn_rmsnorm_grad_args`` (include/gdn.h)."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("dim", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+        ("r_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("d_out_stride", ctypes.c_int64),
+        ("d_out", _vp), ("r", _vp), ("weight", _vp), ("rstd", _vp), ("d_residual", _vp), ("dx", _vp),
+        ("d_weight", _vp),
+    ]
+
+
+class GdnGradClipArgs(ctypes.Structure):
+    """Mirror of ``gdn_grad_clip_args`` (include/gdn.h)."""
+    _fields_ = [
+        ("count", ctypes.c_int32), ("max_norm", ctypes.c_float), ("eps", ctypes.c_float),
+        ("grads", ctypes.POINTER(_vp)), ("outs", ctypes.POINTER(_vp)), ("sizes", ctypes.POINTER(ctypes.c_int64)),
+        ("dtypes", ctypes.POINTER(ctypes.c_int32)), ("norm", _vp), ("error_word", _vp),
+    ]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status, message):
         self.status = status
@@ -123,9 +155,14 @@ def load():
         lib.gdn_chunked_prefill_noalloc.argtypes = [ctypes.POINTER(GdnProblem), ctypes.c_int32, _vp]
         lib.gdn_chunked_prefill_noalloc.restype = ctypes.c_int
         for name, args in (("gdn_scan", GdnScanArgs), ("gdn_scan_step", GdnScanArgs),
-                           ("gdn_scan_backward", GdnScanGradArgs)):
+                           ("gdn_scan_backward", GdnScanGradArgs), ("gdn_rmsnorm", GdnRmsnormArgs)):
             getattr(lib, name).argtypes = [ctypes.POINTER(args), _vp]
             getattr(lib, name).restype = ctypes.c_int
+        for name, args in (("gdn_rmsnorm_backward", GdnRmsnormGradArgs), ("gdn_grad_clip", GdnGradClipArgs)):
+            getattr(lib, name).argtypes = [ctypes.POINTER(args), _vp, ctypes.c_size_t, _vp]
+            getattr(lib, name).restype = ctypes.c_int
+            getattr(lib, name + "_workspace_size").argtypes = [ctypes.POINTER(args)]
+            getattr(lib, name + "_workspace_size").restype = ctypes.c_size_t
         lib.gdn_status_string.argtypes = [ctypes.c_int]
         lib.gdn_status_string.restype = ctypes.c_char_p
         lib.gdn_last_error_message.argtypes = []

@@ -14,7 +14,7 @@ namespace gdn {
 enum : int { kLinear = 0, kGated = 1, kDelta = 2, kGatedDelta = 3, kGdn2 = 4 };
 enum : unsigned { kL2q = 0x1u, kL2k = 0x2u, kBetaSigmoid = 0x4u, kPerKey = 0x8u, kBetaShared = 0x10u, kKMajor = 0x20u };
 // Device error bits, mirrored from include/gdn.h.
-enum : int { kErrBadSlot = 0x1, kErrTimeout = 0x2, kErrOverlap = 0x4, kErrDecayRange = 0x8 };
+enum : int { kErrBadSlot = 0x1, kErrTimeout = 0x2, kErrOverlap = 0x4, kErrDecayRange = 0x8, kErrNonfinite = 0x10 };
 
 __host__ __device__ inline bool rule_has_decay(int r) {
     return r == kGated || r == kGatedDelta || r == kGdn2;

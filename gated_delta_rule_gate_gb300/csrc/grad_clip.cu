@@ -1,0 +1,267 @@
+// grad_clip.cu -- gdn_grad_clip: the norm over many tensors, and their scaling.
+//
+// Two kernels a group of tensors (up to kMany, whose table travels as a kernel
+// argument, so nothing is copied to the device first): every block sums the
+// squares of its chunks into one partial, and then every block adds up all
+// partials in one order and scales its chunks.  Bound by HBM: the gradients are
+// read for the norm and, since it has to be known first, once more to be scaled;
+// the second kernel takes the chunks from the end, where the L2 still holds what
+// the first one read last.
+#include <math.h>
+
+#include "launch.h"
+#include "status.h"
+#include "values.cuh"
+
+namespace gdn {
+namespace clip {
+
+constexpr int kThreads = 256;
+constexpr int kChunk = 8192;    // elements that a block takes at a time
+constexpr int kBlocks = 152 * 8;
+constexpr int kMany = 512;
+
+struct Tensor {
+    const void *in;
+    void *out;
+    int64_t n;
+    int32_t first;  // its first chunk, counted over the table
+    int32_t type;   // gdn_dtype
+};
+template <int MAX>
+struct Table {
+    Tensor t[MAX];
+    int count, chunks;
+};
+
+template <int MAX>
+__device__ __forceinline__ int find_tensor(const Table<MAX> &tab, int chunk) {
+    int lo = 0, hi = tab.count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (tab.t[mid].first <= chunk) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+template <typename T>
+__device__ __forceinline__ float chunk_squares(const T *p, int n) {
+    float sum = 0.f;
+    constexpr int V = sizeof(T) == 4 ? 4 : 8;
+    if (reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+        float part[V] = {};
+#pragma unroll 4
+        for (int i = threadIdx.x * V; i + V <= n; i += kThreads * V) {
+            float v[V];
+            load_values<T, V>(p + i, v);
+#pragma unroll
+            for (int k = 0; k < V; ++k) part[k] = fmaf(v[k], v[k], part[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) sum += part[k];
+        const int i = n / V * V + threadIdx.x;
+        if (i < n) {
+            const float v = static_cast<float>(p[i]);
+            sum = fmaf(v, v, sum);
+        }
+    } else {
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const float v = static_cast<float>(p[i]);
+            sum = fmaf(v, v, sum);
+        }
+    }
+    return sum;
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const T *p, T *o, int n, float k) {
+    constexpr int V = sizeof(T) == 4 ? 4 : 8;
+    if ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(o)) % 16 == 0) {
+#pragma unroll 4
+        for (int i = threadIdx.x * V; i + V <= n; i += kThreads * V) {
+            float v[V];
+            load_values<T, V>(p + i, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] *= k;
+            store_values<T, V>(o + i, v);
+        }
+        const int i = n / V * V + threadIdx.x;
+        if (i < n) o[i] = static_cast<T>(static_cast<float>(p[i]) * k);
+    } else {
+        for (int i = threadIdx.x; i < n; i += kThreads) o[i] = static_cast<T>(static_cast<float>(p[i]) * k);
+    }
+}
+
+template <int MAX>
+__global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ Table<MAX> tab, float *partial) {
+    __shared__ float s[kThreads / 32];
+    float sum = 0.f;
+    for (int chunk = blockIdx.x; chunk < tab.chunks; chunk += gridDim.x) {
+        const Tensor &t = tab.t[find_tensor(tab, chunk)];
+        const int64_t at = (int64_t)(chunk - t.first) * kChunk;
+        const int n = (int)(t.n - at < kChunk ? t.n - at : kChunk);
+        if (t.type == GDN_DTYPE_F32) sum += chunk_squares(static_cast<const float *>(t.in) + at, n);
+        else if (t.type == GDN_DTYPE_F16) sum += chunk_squares(static_cast<const __half *>(t.in) + at, n);
+        else sum += chunk_squares(static_cast<const __nv_bfloat16 *>(t.in) + at, n);
+    }
+    sum = warp_sum(sum);
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kThreads / 32; ++w) sum += s[w];
+        partial[blockIdx.x] = sum;
+    }
+}
+
+template <int MAX>
+__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<MAX> tab,
+                                                        const float *partial, int partials, float max_norm, float eps,
+                                                        float *norm_out, int32_t *err) {
+    __shared__ double s[kThreads / 32];
+    double sum = 0.;
+    for (int i = threadIdx.x; i < partials; i += kThreads) sum += (double)partial[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = 0.;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) sum += s[w];
+    const float norm = (float)sqrt(sum);
+    float k = max_norm / (norm + eps);
+    k = k < 1.f ? k : 1.f;
+    if (!isfinite(norm)) k = 1.f;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        if (norm_out) *norm_out = norm;
+        if (!isfinite(norm) && err) atomicOr(err, kErrNonfinite);
+    }
+    for (int chunk = tab.chunks - 1 - (int)blockIdx.x; chunk >= 0; chunk -= (int)gridDim.x) {
+        const Tensor &t = tab.t[find_tensor(tab, chunk)];
+        if (k == 1.f && t.in == t.out) continue;
+        const int64_t at = (int64_t)(chunk - t.first) * kChunk;
+        const int n = (int)(t.n - at < kChunk ? t.n - at : kChunk);
+        if (t.type == GDN_DTYPE_F32)
+            chunk_scale(static_cast<const float *>(t.in) + at, static_cast<float *>(t.out) + at, n, k);
+        else if (t.type == GDN_DTYPE_F16)
+            chunk_scale(static_cast<const __half *>(t.in) + at, static_cast<__half *>(t.out) + at, n, k);
+        else
+            chunk_scale(static_cast<const __nv_bfloat16 *>(t.in) + at, static_cast<__nv_bfloat16 *>(t.out) + at, n, k);
+    }
+}
+
+// Fills a table with tensors i, i + 1, ...; returns the first that is not in it.
+template <int MAX>
+int fill(const gdn_grad_clip_args *a, int i, Table<MAX> *tab) {
+    tab->count = tab->chunks = 0;
+    for (; i < a->count && tab->count < MAX; ++i) {
+        if (a->sizes[i] == 0) continue;
+        const int64_t chunks = (a->sizes[i] + kChunk - 1) / kChunk;
+        if (tab->chunks + chunks > (1LL << 30)) break;
+        Tensor &t = tab->t[tab->count++];
+        t.in = a->grads[i];
+        t.out = a->outs ? a->outs[i] : const_cast<void *>(a->grads[i]);
+        t.n = a->sizes[i];
+        t.first = tab->chunks;
+        t.type = a->dtypes[i];
+        tab->chunks += (int)chunks;
+    }
+    return i;
+}
+
+// Partials of all tables: one table's blocks after the other's.
+template <int MAX>
+int partial_count(const gdn_grad_clip_args *a) {
+    Table<MAX> tab;
+    int total = 0;
+    for (int i = 0; i < a->count;) {
+        i = fill<MAX>(a, i, &tab);
+        total += tab.chunks < kBlocks ? tab.chunks : kBlocks;
+    }
+    return total;
+}
+
+template <int MAX>
+cudaError_t run(const gdn_grad_clip_args *a, float *ws, cudaStream_t stream) {
+    Table<MAX> tab;
+    int total = 0;
+    for (int i = 0; i < a->count;) {
+        i = fill<MAX>(a, i, &tab);
+        const int blocks = tab.chunks < kBlocks ? tab.chunks : kBlocks;
+        if (blocks == 0) continue;
+        squares_kernel<MAX><<<blocks, kThreads, 0, stream>>>(tab, ws + total);
+        total += blocks;
+    }
+    bool first = true;
+    for (int i = 0; i < a->count || first; first = false) {
+        i = fill<MAX>(a, i, &tab);
+        const int blocks = tab.chunks < kBlocks ? tab.chunks : kBlocks;
+        if (blocks == 0 && !first) continue;
+        scale_kernel<MAX><<<blocks ? blocks : 1, kThreads, 0, stream>>>(
+            tab, ws, total, a->max_norm, a->eps, first ? a->norm : nullptr, first ? a->error_word : nullptr);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace clip
+}  // namespace gdn
+
+namespace {
+
+using gdn::aligned;
+using gdn::fail;
+
+gdn_status validate(const gdn_grad_clip_args *a) {
+    if (!a) return fail(GDN_ERR_INVALID, "args is NULL");
+    if (a->count < 0) return fail(GDN_ERR_INVALID, "count must be >= 0");
+    if (!(a->max_norm >= 0.f) || !isfinite(a->max_norm))
+        return fail(GDN_ERR_INVALID, "max_norm must be >= 0 and finite");
+    if (!(a->eps >= 0.f) || !isfinite(a->eps)) return fail(GDN_ERR_INVALID, "eps must be >= 0 and finite");
+    if (a->count > 0 && (!a->grads || !a->sizes || !a->dtypes))
+        return fail(GDN_ERR_INVALID, "grads, sizes and dtypes are required");
+    for (int i = 0; i < a->count; ++i) {
+        const int dt = a->dtypes[i];
+        if (dt != GDN_DTYPE_F32 && dt != GDN_DTYPE_F16 && dt != GDN_DTYPE_BF16)
+            return fail(GDN_ERR_INVALID, "tensor %d: unknown dtype %d", i, dt);
+        if (a->sizes[i] < 0) return fail(GDN_ERR_INVALID, "tensor %d: size must be >= 0", i);
+        if (a->sizes[i] > (1LL << 42)) return fail(GDN_ERR_UNSUPPORTED, "tensor %d: more than 2^42 elements", i);
+        if (a->sizes[i] == 0) continue;
+        const size_t e = dt == GDN_DTYPE_F32 ? 4 : 2;
+        if (!a->grads[i] || (a->outs && !a->outs[i])) return fail(GDN_ERR_INVALID, "tensor %d: NULL", i);
+        if (!aligned(a->grads[i], e) || (a->outs && !aligned(a->outs[i], e)))
+            return fail(GDN_ERR_INVALID, "tensor %d is not aligned to its element size", i);
+    }
+    if (!aligned(a->norm, 4) || !aligned(a->error_word, 4))
+        return fail(GDN_ERR_INVALID, "a pointer is not aligned to its element size");
+    return GDN_OK;
+}
+
+// A table for few tensors keeps the launch's argument small.
+constexpr int kFew = 32;
+size_t workspace(const gdn_grad_clip_args *a) {
+    const int n = a->count <= kFew ? gdn::clip::partial_count<kFew>(a) : gdn::clip::partial_count<gdn::clip::kMany>(a);
+    return (size_t)(n + 3) / 4 * 16;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_grad_clip_workspace_size(const gdn_grad_clip_args *a) {
+    if (validate(a) != GDN_OK) return (size_t)-1;
+    gdn::ok();
+    return workspace(a);
+}
+
+gdn_status gdn_grad_clip(const gdn_grad_clip_args *a, void *ws, size_t ws_bytes, gdn_stream stream) {
+    const gdn_status st = validate(a);
+    if (st != GDN_OK) return st;
+    const size_t need = workspace(a);
+    if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned(ws, 16)))
+        return fail(GDN_ERR_WORKSPACE, "workspace needs %zu bytes, 16-byte aligned (got %zu)", need, ws_bytes);
+    float *w = static_cast<float *>(ws);
+    cudaStream_t s = (cudaStream_t)stream;
+    return gdn::cuda_status(a->count <= kFew ? gdn::clip::run<kFew>(a, w, s)
+                                             : gdn::clip::run<gdn::clip::kMany>(a, w, s));
+}
+
+}  // extern "C"

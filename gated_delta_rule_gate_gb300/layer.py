@@ -6,6 +6,7 @@ stream (or ``stream``); what they allocate when an output is not given is torch
 memory of that stream.  float32, float16 and bfloat16 tensors are taken.
 """
 import contextlib
+import ctypes
 from collections import namedtuple
 
 import torch
@@ -15,6 +16,9 @@ from . import _native as N
 _DT = {torch.float32: N.DTYPE_F32, torch.float16: N.DTYPE_F16, torch.bfloat16: N.DTYPE_BF16}
 
 ScanGradients = namedtuple("ScanGradients", "dx d_decay d_beta d_gate_bias d_gate_scale d_initial_state")
+
+NormResult = namedtuple("NormResult", "out residual scales rstd")
+NormGradients = namedtuple("NormGradients", "dx dweight")
 
 
 def _handle(stream):
@@ -211,3 +215,109 @@ def gdn_scan_backward(d_out, x, decay, chunk_states, *, beta=None, gate_bias=Non
         _ptr(d_initial_state, f32, "d_initial_state", rows))
     N.check(N.load().gdn_scan_backward(args, _handle(stream)))
     return ScanGradients(dx, d_decay, d_beta, d_gate_bias, d_gate_scale, d_initial_state)
+
+
+def gdn_rmsnorm(x, weight, *, residual=None, eps=1e-6, out_dtype=None, group=0, want_rstd=False, out=None,
+                residual_out=None, scales=None, stream=None):
+    """r = x + residual; out = r / sqrt(mean(r^2) + eps) * weight over the last
+    dimension, in fp32.  ``out_dtype`` is x's, or torch.float8_e4m3fn with fp32 scales
+    (out * scale is the value): one per row (``group`` 0) or per 128 columns (128).
+    Returns NormResult(out, residual, scales, rstd): residual is r in residual's dtype
+    (float32 or x's; ``residual_out`` may be ``residual``), rstd is for
+    gdn_rmsnorm_backward; None where there is none or it was not asked for."""
+    shape = x.shape
+    D = shape[-1] if x.dim() else 0
+    n = x.numel() // D if D else 0
+    e4m3 = out_dtype is torch.float8_e4m3fn
+    if out_dtype is None:
+        out_dtype = x.dtype
+    rstd = None
+    with _on(stream):
+        if out is None:
+            out = torch.empty(shape, dtype=out_dtype, device=x.device)
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
+        if e4m3 and scales is None:
+            cols = () if group == 0 else (-(-D // 128),)
+            scales = torch.empty(shape[:-1] + cols, device=x.device)
+        if want_rstd:
+            rstd = torch.empty(shape[:-1], device=x.device)
+    xp, xs = _rows(x, shape, "x")
+    res = None if residual is None else residual.dtype
+    code = _dtype(x, "x")
+    args = N.GdnRmsnormArgs(
+        n, D, code, code if residual is None else _dtype(residual, "residual"), _dtype(weight, "weight"),
+        N.DTYPE_E4M3 if e4m3 else _DT.get(out_dtype, -1), group, eps, xs, xp,
+        _ptr(residual, res, "residual", shape), _ptr(weight, weight.dtype, "weight", (D,)),
+        _ptr(out, out_dtype, "out", shape), _ptr(residual_out, res, "residual_out", shape),
+        _ptr(scales, torch.float32, "scales", shape[:-1] + (() if group == 0 else (-(-D // 128),))),
+        _ptr(rstd, torch.float32, "rstd"))
+    N.check(N.load().gdn_rmsnorm(args, _handle(stream)))
+    return NormResult(out, residual_out if residual is not None else None, scales, rstd)
+
+
+def gdn_rmsnorm_backward(d_out, r, weight, rstd, *, d_residual=None, dx=None, d_weight=None, workspace=None,
+                         stream=None):
+    """Gradients of gdn_rmsnorm for the gradient ``d_out`` of its (unquantised)
+    output and ``d_residual`` of the residual that it returned; r is that residual (x
+    where there was none), rstd what it returned.  Returns NormGradients(dx, dweight): dx, in r's dtype, is the
+    gradient of x and of residual alike (``dx`` may be ``d_residual``); dweight is
+    float32."""
+    shape = r.shape
+    D = shape[-1] if r.dim() else 0
+    n = r.numel() // D if D else 0
+    with _on(stream):
+        if dx is None:
+            dx = torch.empty(shape, dtype=r.dtype, device=r.device)
+        if d_weight is None:
+            d_weight = torch.empty(D, device=r.device)
+    dp, ds = _rows(d_out, shape, "d_out")
+    args = N.GdnRmsnormGradArgs(
+        n, D, _dtype(d_out, "d_out"), _dtype(r, "r"), _dtype(weight, "weight"), ds, dp, _ptr(r, r.dtype, "r"),
+        _ptr(weight, weight.dtype, "weight", (D,)), _ptr(rstd, torch.float32, "rstd", shape[:-1]),
+        _ptr(d_residual, r.dtype, "d_residual", shape), _ptr(dx, r.dtype, "dx", shape),
+        _ptr(d_weight, torch.float32, "d_weight", (D,)))
+    _with_workspace("gdn_rmsnorm_backward", args, workspace, r.device, stream)
+    return NormGradients(dx, d_weight)
+
+
+def _with_workspace(name, args, workspace, device, stream):
+    lib = N.load()
+    if workspace is None:
+        need = getattr(lib, name + "_workspace_size")(args)
+        if need == ctypes.c_size_t(-1).value:
+            need = 0  # the call says what is wrong
+        with _on(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    N.check(getattr(lib, name)(args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                               _handle(stream)))
+
+
+def gdn_grad_clip(grads, max_norm, *, eps=1e-6, out=None, norm=None, error_word=None, workspace=None, stream=None):
+    """The 2-norm of all elements of the tensors ``grads`` together, and each scaled
+    by min(1, max_norm / (norm + eps)): in place, or into the tensors ``out``.  Returns
+    the norm, float32 [1] on the device (no synchronisation).  A norm that is not
+    finite scales nothing and sets DEVERR_NONFINITE in ``error_word``."""
+    grads = list(grads)
+    count = len(grads)
+    device = grads[0].device if count else torch.device("cuda", torch.cuda.current_device())
+    with _on(stream):
+        if norm is None:
+            norm = torch.empty(1, device=device)
+    table = (ctypes.c_void_p * count)()
+    sizes = (ctypes.c_int64 * count)()
+    types = (ctypes.c_int32 * count)()
+    outs = None
+    for i, t in enumerate(grads):
+        table[i], sizes[i], types[i] = _ptr(t, t.dtype, "a gradient"), t.numel(), _dtype(t, "a gradient")
+    if out is not None:
+        out = list(out)
+        if len(out) != count:
+            raise ValueError("out must have a tensor for each of the %d gradients" % count)
+        outs = (ctypes.c_void_p * count)()
+        for i, t in enumerate(out):
+            outs[i] = _ptr(t, grads[i].dtype, "an output", grads[i].shape)
+    args = N.GdnGradClipArgs(count, max_norm, eps, table, outs, sizes, types, _ptr(norm, torch.float32, "norm", (1,)),
+                             _ptr(error_word, torch.int32, "error_word"))
+    _with_workspace("gdn_grad_clip", args, workspace, device, stream)
+    return norm

@@ -62,7 +62,8 @@ typedef enum gdn_status {
 typedef enum gdn_dtype {
     GDN_DTYPE_F32 = 0,
     GDN_DTYPE_F16 = 1,
-    GDN_DTYPE_BF16 = 2 /* named so it can be declined: GDN_ERR_UNSUPPORTED */
+    GDN_DTYPE_BF16 = 2, /* the recurrent-layer operators; the others decline it: GDN_ERR_UNSUPPORTED */
+    GDN_DTYPE_E4M3 = 3  /* 8 bits (4 of exponent, 3 of mantissa, largest 448): output of gdn_rmsnorm only */
 } gdn_dtype;
 
 /* "com.microsoft.GatedDeltaNet", Attributes, update_rule; GDN2 is the rule
@@ -92,6 +93,8 @@ typedef enum gdn_rule {
 #define GDN_DEVERR_DECAY_RANGE 0x8 /* chunked prefill, per-key decay on the tensor cores: a log decay above 0
                                       (a decay above 1) was given; that path needs decays in (0, 1] and the
                                       results of the chunks concerned are not valid */
+
+#define GDN_DEVERR_NONFINITE 0x10 /* gdn_grad_clip: the norm is infinite or NaN; the gradients were not scaled */
 
 /*
  * One call of the recurrence over a batch of requests.
@@ -442,6 +445,107 @@ typedef struct gdn_scan_grad_args {
 } gdn_scan_grad_args;
 
 gdn_status gdn_scan_backward(const gdn_scan_grad_args *args, gdn_stream stream);
+
+/*
+ * gdn_rmsnorm -- residual addition and root-mean-square norm of each of `rows`
+ * rows of `dim` values, all of it in fp32:
+ *
+ *     r = x + residual   (r = x without one),   residual_out = r in residual_dtype
+ *     rstd = 1 / sqrt(mean(r^2) + eps),   y = r rstd weight
+ *     out = y in x_dtype, or in E4M3 with scales:  s = max(|y|) / 448 over a row
+ *     (group 0) or over each 128 columns (group 128; the last group of a row may be
+ *     short), out = y / s, the maximum floored at 2^-100 so that s > 0.
+ *
+ * The norm takes r before residual_out is rounded.  x has x_stride elements from
+ * row to row (0: dim); the other tensors are contiguous.  scales is fp32 [rows],
+ * or [rows, ceil(dim / 128)]; rstd (NULL: not kept) is fp32 [rows], for
+ * gdn_rmsnorm_backward.  residual_out may be residual.  dim is at most 2^20.
+ */
+typedef struct gdn_rmsnorm_args {
+    int64_t rows;
+    int32_t dim;
+    int32_t x_dtype;
+    int32_t residual_dtype; /* F32 or x_dtype */
+    int32_t weight_dtype;   /* F32 or x_dtype */
+    int32_t out_dtype;      /* x_dtype or E4M3 */
+    int32_t group;          /* E4M3: 0 (a scale per row) or 128; else 0 */
+    float eps;              /* >= 0 */
+    int64_t x_stride;
+    const void *x;
+    const void *residual; /* or NULL */
+    const void *weight;   /* [dim] */
+    void *out;
+    void *residual_out; /* with residual */
+    float *scales;      /* with E4M3 */
+    float *rstd;        /* or NULL */
+} gdn_rmsnorm_args;
+
+gdn_status gdn_rmsnorm(const gdn_rmsnorm_args *args, gdn_stream stream);
+
+/*
+ * gdn_rmsnorm_backward -- with r the norm's input as it was kept (residual_out, or
+ * x), xhat = r rstd and d_residual the gradient that reaches residual_out from
+ * elsewhere (NULL: none):
+ *
+ *     dx = rstd (weight d_out - xhat mean(weight d_out xhat)) + d_residual
+ *     d_weight = sum over rows of d_out xhat
+ *
+ * dx is the gradient of x and of residual alike.  r, d_residual and dx have
+ * r_dtype, d_out x_dtype (d_out_stride elements from row to row; 0: dim), d_weight
+ * is fp32.  dx may be d_residual.  Sums are fp32 and in a fixed order.  The
+ * workspace is device memory of gdn_rmsnorm_backward_workspace_size() bytes,
+ * 16-byte aligned (GDN_ERR_WORKSPACE otherwise); its contents are scratch.
+ */
+typedef struct gdn_rmsnorm_grad_args {
+    int64_t rows;
+    int32_t dim;
+    int32_t x_dtype;
+    int32_t r_dtype;      /* F32 or x_dtype */
+    int32_t weight_dtype; /* F32 or x_dtype */
+    int64_t d_out_stride;
+    const void *d_out;
+    const void *r;
+    const void *weight;
+    const float *rstd;
+    const void *d_residual; /* or NULL */
+    void *dx;
+    float *d_weight; /* [dim] */
+} gdn_rmsnorm_grad_args;
+
+/* (size_t)-1 when the arguments are rejected (see gdn_last_error_message). */
+size_t gdn_rmsnorm_backward_workspace_size(const gdn_rmsnorm_grad_args *args);
+gdn_status gdn_rmsnorm_backward(const gdn_rmsnorm_grad_args *args, void *workspace, size_t workspace_bytes,
+                                gdn_stream stream);
+
+/*
+ * gdn_grad_clip -- the norm of all elements of `count` tensors together, and the
+ * tensors scaled to at most max_norm:
+ *
+ *     norm = sqrt(sum g^2),   out = g min(1, max_norm / (norm + eps))
+ *
+ * The arrays grads, outs, sizes and dtypes are HOST memory, read before the call
+ * returns: device pointers, element counts (0: skipped) and gdn_dtypes (F32, F16,
+ * BF16; an output has its gradient's).  outs[i] may be grads[i] (outs NULL: all in
+ * place); a tensor in place is written only if it is scaled.  The sum is fp32 in
+ * a fixed order (joined in 64 bits): the same bits on every run.  norm is a device
+ * float (or NULL).  A norm that is not finite scales nothing and sets
+ * GDN_DEVERR_NONFINITE.  The workspace is device memory of
+ * gdn_grad_clip_workspace_size() bytes, 16-byte aligned.
+ */
+typedef struct gdn_grad_clip_args {
+    int32_t count;
+    float max_norm; /* >= 0 */
+    float eps;      /* >= 0 */
+    const void *const *grads;
+    void *const *outs;
+    const int64_t *sizes;
+    const int32_t *dtypes;
+    float *norm;
+    int32_t *error_word;
+} gdn_grad_clip_args;
+
+size_t gdn_grad_clip_workspace_size(const gdn_grad_clip_args *args);
+gdn_status gdn_grad_clip(const gdn_grad_clip_args *args, void *workspace, size_t workspace_bytes, gdn_stream stream);
 
 /* Static description of a status code ("ok", "invalid argument", ...). */
 const char *gdn_status_string(gdn_status status);
