@@ -263,6 +263,35 @@ cudaError_t large_clusters(const void *fn) {
     return e;
 }
 
+cudaError_t resident_clusters(const void *fn, int threads, size_t smem, int size, int *n) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(g_attr_mu);
+    const auto key = std::make_tuple(dev, fn, ((size_t)1 << 60) + (smem * 4096 + (size_t)threads) * 32 + (size_t)size);
+    auto it = g_attr.find(key);
+    if (it != g_attr.end()) {
+        *n = it->second;
+        return cudaSuccess;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)size);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)size;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    e = cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg);
+    if (e != cudaSuccess) return e;
+    g_attr[key] = clusters;
+    *n = clusters;
+    return cudaSuccess;
+}
+
 int sm_count() {
     static std::mutex mu;
     static std::vector<int> cache;

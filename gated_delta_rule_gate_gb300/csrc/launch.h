@@ -29,6 +29,8 @@ cudaError_t smem_attr(const void *fn, int bytes);
 cudaError_t blocks_per_sm(const void *fn, int threads, size_t smem, int *n);
 // Allows a kernel clusters of up to 16 blocks, once per (device, kernel).
 cudaError_t large_clusters(const void *fn);
+// Clusters of `size` blocks of a kernel that are resident at once (cached).
+cudaError_t resident_clusters(const void *fn, int threads, size_t smem, int size, int *n);
 
 cudaError_t launch_gate(const GateLaunch &g, cudaStream_t stream);
 cudaError_t launch_recurrent(const Problem &p, cudaStream_t stream);

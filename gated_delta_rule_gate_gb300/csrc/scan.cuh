@@ -20,6 +20,7 @@ struct Args {
     int B, T, L, D, rows;  // L: tokens of a request's row in the uniform forms, 0 with cu
     int mode, sigmoid;
     int vec;               // pairs of channels can be read and written as one word
+    int wide;              // the inputs' rows begin on 16-byte addresses
     int64_t xs, gs, bs, os;
     const void *x, *decay, *beta;
     void *o;
@@ -198,58 +199,134 @@ __device__ __forceinline__ Tokens look_up(const Args &p, int t, int n, int lane,
     return k;
 }
 
-// ---------------------------------------------------------------- gates
-// softplus(z) = max(z, 0) + log1p(e^-|z|).
-__device__ __forceinline__ float softplus(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+// ---------------------------------------------------------------- arithmetic
+// Two channels at a time.  The gates' functions are the larger part of the
+// kernels' instructions, so they are written for packed fp32 and few special
+// function units; their relative errors stay within a few 2^-24 where the state
+// remembers (a near 1), since a state of M tokens' memory carries M times a's.
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 operator+(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 operator*(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
-template <bool RAW>
-__device__ __forceinline__ float log_decay(float z, float bias, float scale) {
-    return RAW ? scale * softplus(z + bias) : z;
+__device__ __forceinline__ float ex2(float v) {  // 2^v
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float root(float v) {
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// sigmoid(z) = 1 / (1 + e^-z).
+__device__ __forceinline__ float2 sigmoid(float2 z) {
+    const float2 d = make_float2(ex2(-kLog2e * z.x), ex2(-kLog2e * z.y)) + splat(1.f);
+    return make_float2(reciprocal(d.x), reciprocal(d.y));
+}
+
+// softplus(z) = max(z, 0) + log1p(u), u = e^-|z| in (0, 1].  log1p(u) / u is a
+// polynomial of degree 8 fitted on [0, 1] (weighted least squares at Chebyshev
+// nodes, toward the least largest relative error): 1.7e-7 with fp32 rounding.
+__device__ __forceinline__ float2 softplus(float2 z, float2 &u) {
+    u = make_float2(ex2(-kLog2e * fabsf(z.x)), ex2(-kLog2e * fabsf(z.y)));
+    float2 r = splat(0.00523266801610589f);
+    r = fma2(r, u, splat(-0.029505133628845215f));
+    r = fma2(r, u, splat(0.07822578400373459f));
+    r = fma2(r, u, splat(-0.1366323083639145f));
+    r = fma2(r, u, splat(0.19106000661849976f));
+    r = fma2(r, u, splat(-0.2484298050403595f));
+    r = fma2(r, u, splat(0.3331909775733948f));
+    r = fma2(r, u, splat(-0.4999949336051941f));
+    r = fma2(r, u, splat(0.9999999403953552f));
+    return fma2(r, u, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
+}
+
+// e^g - 1: for |g| <= 1/2 a polynomial times g (degree 6, fitted as above, 1.2e-7),
+// else 2^(g log2 e) - 1.  1 + it is then e^g without a bias where g is near 0.
+__device__ __forceinline__ float2 exp_minus_1(float2 g) {
+    float2 r = splat(0.00019841187167912722f);
+    r = fma2(r, g, splat(0.0013997324276715517f));
+    r = fma2(r, g, splat(0.008333634585142136f));
+    r = fma2(r, g, splat(0.041665319353342056f));
+    r = fma2(r, g, splat(0.16666662693023682f));
+    r = fma2(r, g, splat(0.5000000596046448f));
+    r = fma2(r, g, splat(1.f)) * g;
+    const float2 t = g * splat(kLog2e);
+    const float2 e = make_float2(ex2(t.x), ex2(t.y)) + splat(-1.f);
+    return make_float2(fabsf(g.x) <= 0.5f ? r.x : e.x, fabsf(g.y) <= 0.5f ? r.y : e.y);
+}
+
+// What a token's gates come to: a = exp(g), the input's scale n, and m = a - 1.
+template <bool RAW>
+__device__ __forceinline__ float2 log_decay(float2 z, float2 bias, float2 scale) {
+    float2 u;
+    return RAW ? scale * softplus(z + bias, u) : z;
+}
+// n^2 = 1 - a^2 = -m (2 + m) with m = a - 1, and 0 where a > 1.
+__device__ __forceinline__ float2 unit_scale(float2 m) {
+    const float2 q = m * (splat(-2.f) + make_float2(-m.x, -m.y));
+    return make_float2(root(fmaxf(q.x, 0.f)), root(fmaxf(q.y, 0.f)));
+}
+// a and u = n i x of a token.
+template <bool RAW, bool BETA, int MODE>
+__device__ __forceinline__ void token_map(float2 x, float2 z, float2 y, float2 bias, float2 scale, bool sig, float2 &a,
+                                          float2 &u) {
+    const float2 m = exp_minus_1(log_decay<RAW>(z, bias, scale));
+    a = m + splat(1.f);
+    u = x;
+    if constexpr (BETA) u = u * (sig ? sigmoid(y) : y);
+    if constexpr (MODE == kLerp) u = u * make_float2(-m.x, -m.y);
+    if constexpr (MODE == kUnit) u = u * unit_scale(m);
+}
+
 // What the gradient needs of one token's gates: a, n, dn/dg, i, di/dbeta,
 // softplus, dg/ddecay.
 struct Terms {
-    float a, n, dn, i, di, soft, dgdz;
+    float2 a, n, dn, i, di, soft, dgdz;
 };
 template <bool RAW, bool BETA, int MODE>
-__device__ __forceinline__ Terms gate_terms(float z, float y, float bias, float scale, bool sig) {
+__device__ __forceinline__ Terms gate_terms(float2 z, float2 y, float2 bias, float2 scale, bool sig) {
     Terms t;
-    float g = z;
-    t.soft = 0.f;
-    t.dgdz = 1.f;
+    float2 g = z;
+    t.soft = splat(0.f);
+    t.dgdz = splat(1.f);
     if constexpr (RAW) {
-        z += bias;
-        t.soft = softplus(z);
+        float2 u;
+        z = z + bias;
+        t.soft = softplus(z, u);
         g = scale * t.soft;
-        t.dgdz = scale * sigmoid(z);
+        // sigmoid(z) = 1 / (1 + u) for z >= 0, u / (1 + u) below
+        const float2 d = u + splat(1.f), r = make_float2(reciprocal(d.x), reciprocal(d.y)), l = u * r;
+        t.dgdz = scale * make_float2(z.x >= 0.f ? r.x : l.x, z.y >= 0.f ? r.y : l.y);
     }
-    t.a = expf(g);
-    t.n = 1.f;
-    t.dn = 0.f;
+    const float2 m = exp_minus_1(g);
+    t.a = m + splat(1.f);
+    t.n = splat(1.f);
+    t.dn = splat(0.f);
     if constexpr (MODE == kLerp) {
-        t.n = -expm1f(g);
-        t.dn = -t.a;
+        t.n = make_float2(-m.x, -m.y);
+        t.dn = make_float2(-t.a.x, -t.a.y);
     }
     if constexpr (MODE == kUnit) {  // where n is 0 (a >= 1) its slope is taken as 0
-        t.n = sqrtf(fmaxf(0.f, -expm1f(2.f * g)));
-        t.dn = t.n > 0.f ? -t.a * t.a / t.n : 0.f;
+        t.n = unit_scale(m);
+        const float2 q = t.a * t.a;
+        t.dn = make_float2(t.n.x > 0.f ? -q.x * reciprocal(t.n.x) : 0.f, t.n.y > 0.f ? -q.y * reciprocal(t.n.y) : 0.f);
     }
-    t.i = 1.f;
-    t.di = 0.f;
+    t.i = splat(1.f);
+    t.di = splat(0.f);
     if constexpr (BETA) {
         t.i = sig ? sigmoid(y) : y;
-        t.di = sig ? t.i * (1.f - t.i) : 1.f;
+        t.di = sig ? t.i * (splat(1.f) + make_float2(-t.i.x, -t.i.y)) : splat(1.f);
     }
     return t;
-}
-
-// n of the input x; a = exp(g).
-template <int MODE>
-__device__ __forceinline__ float input_scale(float g, float a) {
-    if constexpr (MODE == kLerp) return -expm1f(g);
-    if constexpr (MODE == kUnit) return sqrtf(fmaxf(0.f, -expm1f(2.f * g)));
-    return 1.f;
 }
 
 }  // namespace scan

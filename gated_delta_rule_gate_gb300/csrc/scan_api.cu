@@ -35,6 +35,11 @@ gdn_status check_stride(int64_t stride, int channels, const char *what, int64_t 
 // Pairs of elements at even places of q's rows are aligned words.
 bool pairs(const void *q, size_t e, int64_t stride) { return q == nullptr || (aligned(q, 2 * e) && stride % 2 == 0); }
 
+// q's rows begin on 16-byte addresses.
+bool lines(const void *q, size_t e, int64_t stride) {
+    return q == nullptr || (aligned(q, 16) && stride * (int64_t)e % 16 == 0);
+}
+
 // Sizes, token layout, gates, states and alignment, shared by every entry point.
 // `needs_o`: the call writes o.
 gdn_status validate(const gdn_scan_args *a, bool needs_o, Args *out) {
@@ -90,6 +95,7 @@ gdn_status validate(const gdn_scan_args *a, bool needs_o, Args *out) {
     p.err = a->error_word;
     p.vec = p.D % 2 == 0 && pairs(a->x, ea, p.xs) && (!needs_o || pairs(a->o, ea, p.os)) &&
             pairs(a->decay, eg, p.gs) && pairs(a->beta, eg, p.bs);
+    p.wide = lines(a->x, ea, p.xs) && lines(a->decay, eg, p.gs) && lines(a->beta, eg, p.bs);
     return GDN_OK;
 }
 

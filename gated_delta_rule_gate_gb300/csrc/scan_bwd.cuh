@@ -9,7 +9,7 @@
 // right: a run of tokens takes c to A c + C, with the product A of the forward
 // run.  h_{t-1} is formed anew from the state that the forward pass kept before
 // every 64th token: a block's tile is 64 tokens, so the forward runs meet in the
-// block alone, and only c crosses blocks (one cluster barrier a window, as in the
+// block alone, and only c crosses blocks (one exchange a window, as in the
 // forward pass).  x, decay, beta and d_o cross HBM once.  The sums over tokens are
 // kept in registers by channel and joined in a fixed order at the end.
 #pragma once
@@ -73,23 +73,22 @@ struct Backward {
     static __device__ __forceinline__ void run(const GradArgs &q, Sums &sums) {
         __shared__ float4 s_fwd[2][kWarps][32];  // (A, H) of each warp's run
         __shared__ float2 s_rev[2][kWarps][32];  // C of each warp's run
-        __shared__ float4 s_rank[2][kMaxCluster][32];
+        __shared__ Exchange s_x;
         const Args &p = q.f;
         const int S = cluster_size(), rank = cluster_rank();
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         const int c = (int)(blockIdx.x / S) * 64 + 2 * lane;
         const bool ok0 = c < p.D, ok1 = c + 1 < p.D;
-        if (S > 1) cluster_arrive();  // waited for before the first remote store
         gradient_duties(q, S * kWarps, rank * kWarps + warp, lane, c, blockIdx.x < S);
         float2 bias = make_float2(0.f, 0.f), scale = bias;
         if (RAW) bias = load_state(p.bias, c, p.D), scale = load_state(p.scale, c, p.D);
-        if (S > 1) cluster_wait();
+        if (S > 1) exchange_init(s_x);
 
         const int window = S * kTile, steps = (p.T + window - 1) / window;
         Seen seen;
         float2 carry = make_float2(0.f, 0.f);  // c behind the window
-        for (int step = steps - 1; step >= 0; --step) {
-            const int par = step & 1;
+        for (int turn = 0; turn < steps; ++turn) {
+            const int step = steps - 1 - turn, par = turn & 1;
             const int tile = step * window + rank * kTile, t = tile + warp * kTokens;
             const Tokens tok = look_up(p, t, kTokens, lane, seen);
             Raw raw;
@@ -98,27 +97,19 @@ struct Backward {
             if (tile < p.T) h = load_state(p.chunk + (size_t)(tile / kChunk) * p.D, c, p.D);
 
             float2 a[kTokens], u[kTokens];
-            float4 fwd = make_float4(1.f, 0.f, 1.f, 0.f);
+            float2 A = splat(1.f), H = splat(0.f);
 #pragma unroll
             for (int k = 0; k < kTokens; ++k) {
-                a[k] = make_float2(1.f, 1.f), u[k] = make_float2(0.f, 0.f);
+                a[k] = splat(1.f), u[k] = splat(0.f);
                 if (tok.own >> k & 1u) {
                     const float2 z = unpack<TG>(raw.z[k]), y = BETA ? unpack<TG>(raw.y[k]) : z;
-                    const float2 x = unpack<TA>(raw.x[k]);
-                    const Terms t0 = gate_terms<RAW, BETA, MODE>(z.x, y.x, bias.x, scale.x, p.sigmoid);
-                    const Terms t1 = gate_terms<RAW, BETA, MODE>(z.y, y.y, bias.y, scale.y, p.sigmoid);
-                    a[k] = make_float2(t0.a, t1.a);
-                    u[k] = make_float2(t0.n * t0.i * x.x, t1.n * t1.i * x.y);
+                    token_map<RAW, BETA, MODE>(unpack<TA>(raw.x[k]), z, y, bias, scale, p.sigmoid, a[k], u[k]);
                 }
                 if (tok.first >> k & 1u) {
-                    const float2 h0 = first_state(p, tok, k, c);
-                    fwd.y = fmaf(a[k].x, h0.x, u[k].x);
-                    fwd.w = fmaf(a[k].y, h0.y, u[k].y);
+                    H = fma2(a[k], first_state(p, tok, k, c), u[k]);
                 } else {
-                    fwd.y = fmaf(a[k].x, fwd.y, u[k].x);
-                    fwd.w = fmaf(a[k].y, fwd.w, u[k].y);
-                    fwd.x *= a[k].x;
-                    fwd.z *= a[k].y;
+                    H = fma2(a[k], H, u[k]);
+                    A = A * a[k];
                 }
             }
             float2 rev = make_float2(0.f, 0.f);
@@ -126,30 +117,29 @@ struct Backward {
             for (int k = kTokens - 1; k >= 0; --k) {
                 float2 d = unpack<TA>(raw.d[k]);
                 if (tok.last >> k & 1u) add_final(q, tok, k, c, d);
-                rev = make_float2(a[k].x * (d.x + rev.x), a[k].y * (d.y + rev.y));
-                if (tok.first >> k & 1u) rev = make_float2(0.f, 0.f);
+                rev = a[k] * (d + rev);
+                if (tok.first >> k & 1u) rev = splat(0.f);
             }
-            if (tok.first) fwd.x = fwd.z = kBegins;
-            s_fwd[par][warp][lane] = fwd;
+            if (tok.first) A = splat(kBegins);
+            s_fwd[par][warp][lane] = map_of(A, H);
             s_rev[par][warp][lane] = rev;
             __syncthreads();
             for (int w = 0; w < warp; ++w) h = apply(s_fwd[par][w][lane], h);
-            float4 after = make_float4(1.f, 0.f, 1.f, 0.f), whole = after;
+            float2 wholeA = splat(1.f), wholeC = splat(0.f), afterA = wholeA, afterC = wholeC;
 #pragma unroll
             for (int w = kWarps - 1; w >= 0; --w) {
-                if (w == warp) after = whole;
-                const float4 f = s_fwd[par][w][lane];
-                const float2 r = s_rev[par][w][lane];
-                fold(whole, make_float4(f.x, r.x, f.z, r.y));
+                if (w == warp) afterA = wholeA, afterC = wholeC;
+                fold<true>(wholeA, wholeC, map_of(map_a(s_fwd[par][w][lane]), s_rev[par][w][lane]));
             }
+            const float4 whole = map_of(wholeA, wholeC), after = map_of(afterA, afterC);
             float2 dc = carry;
             if (S > 1) {
-                for (int r = warp; r < S; r += kWarps) store_remote(&s_rank[par][rank][lane], r, whole);
-                cluster_arrive();
-                cluster_wait();
+                if (threadIdx.x == 0) exchange_expect(s_x, par, S);
+                for (int r = warp; r < S; r += kWarps) exchange_send(s_x, par, rank, r, lane, whole);
+                exchange_wait(s_x, par, turn >> 1, p.err);
                 for (int r = S - 1; r >= 0; --r) {
                     if (r == rank) dc = carry;
-                    carry = apply(s_rank[par][r][lane], carry);
+                    carry = apply(s_x.map[par][r][lane], carry);
                 }
             } else {
                 carry = apply(whole, carry);
@@ -161,7 +151,7 @@ struct Backward {
             for (int k = 0; k < kTokens; ++k) {
                 if (tok.first >> k & 1u) h = first_state(p, tok, k, c);
                 prev[k] = h;
-                h = make_float2(fmaf(a[k].x, h.x, u[k].x), fmaf(a[k].y, h.y, u[k].y));
+                h = fma2(a[k], h, u[k]);
             }
             TA *dx = static_cast<TA *>(q.dx) + (int64_t)t * q.dxs + c;
             TG *dg = static_cast<TG *>(q.dg) + (int64_t)t * q.dgs + c;
@@ -171,37 +161,28 @@ struct Backward {
                 if (!(tok.own >> k & 1u)) continue;  // hands c on
                 float2 dh = unpack<TA>(raw.d[k]);
                 if (tok.last >> k & 1u) add_final(q, tok, k, c, dh);
-                dh.x += dc.x;
-                dh.y += dc.y;
+                dh = dh + dc;
                 const float2 z = unpack<TG>(raw.z[k]), y = BETA ? unpack<TG>(raw.y[k]) : z;
                 const float2 x = unpack<TA>(raw.x[k]);
-                const Terms t0 = gate_terms<RAW, BETA, MODE>(z.x, y.x, bias.x, scale.x, p.sigmoid);
-                const Terms t1 = gate_terms<RAW, BETA, MODE>(z.y, y.y, bias.y, scale.y, p.sigmoid);
-                dc = make_float2(t0.a * dh.x, t1.a * dh.y);
-                float g0 = dc.x * prev[k].x, g1 = dc.y * prev[k].y;
-                if (MODE != kNone) {
-                    g0 = fmaf(t0.dn * t0.i * x.x, dh.x, g0);
-                    g1 = fmaf(t1.dn * t1.i * x.y, dh.y, g1);
-                }
+                const Terms g = gate_terms<RAW, BETA, MODE>(z, y, bias, scale, p.sigmoid);
+                dc = a[k] * dh;
+                float2 d = dc * prev[k];
+                if (MODE != kNone) d = fma2(g.dn * g.i * x, dh, d);
                 if (RAW) {
-                    sums.scale.x = fmaf(g0, t0.soft, sums.scale.x);
-                    sums.scale.y = fmaf(g1, t1.soft, sums.scale.y);
-                    g0 *= t0.dgdz;
-                    g1 *= t1.dgdz;
-                    sums.bias.x += g0;
-                    sums.bias.y += g1;
+                    sums.scale = fma2(d, g.soft, sums.scale);
+                    d = d * g.dgdz;
+                    sums.bias = sums.bias + d;
                 }
                 if (ok0) {
-                    store_pair<TA>(dx + k * q.dxs, make_float2(t0.n * t0.i * dh.x, t1.n * t1.i * dh.y), p.vec, ok1);
-                    store_pair<TG>(dg + k * q.dgs, make_float2(g0, g1), p.vec, ok1);
-                    if (BETA)
-                        store_pair<TG>(db + k * q.dbs,
-                                       make_float2(t0.n * x.x * dh.x * t0.di, t1.n * x.y * dh.y * t1.di), p.vec, ok1);
+                    const float2 w = g.n * dh;
+                    store_pair<TA>(dx + k * q.dxs, w * g.i, p.vec, ok1);
+                    store_pair<TG>(dg + k * q.dgs, d, p.vec, ok1);
+                    if (BETA) store_pair<TG>(db + k * q.dbs, w * x * g.di, p.vec, ok1);
                 }
                 if (tok.first >> k & 1u) {
                     const int row = __shfl_sync(0xffffffffu, tok.row, k);
                     if (q.dinit) store_state(q.dinit + (size_t)row * p.D, c, p.D, dc);
-                    dc = make_float2(0.f, 0.f);
+                    dc = splat(0.f);
                 }
             }
         }
@@ -209,29 +190,34 @@ struct Backward {
             __syncthreads();
             s_fwd[0][warp][lane] = make_float4(sums.bias.x, sums.bias.y, sums.scale.x, sums.scale.y);
             __syncthreads();
+            const int par = steps & 1;  // one turn more of the exchange
+            if (S > 1 && threadIdx.x == 0) exchange_expect(s_x, par, S);
             if (warp == 0) {
                 float4 v = s_fwd[0][0][lane];
                 for (int w = 1; w < kWarps; ++w) {
                     const float4 o = s_fwd[0][w][lane];
                     v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
                 }
-                // the buffer that the last window did not use; no block writes it any more
-                if (S > 1) store_remote(&s_rank[1][rank][lane], 0, v);
-                else s_rank[1][0][lane] = v;
-            }
-            if (S > 1) {
-                cluster_arrive();
-                cluster_wait();
+                if (S > 1) {
+                    for (int r = 0; r < S; ++r) exchange_send(s_x, par, rank, r, lane, v);
+                    exchange_wait(s_x, par, steps >> 1, p.err);
+                } else {
+                    s_x.map[par][0][lane] = v;
+                }
             }
             if (rank == 0 && warp == 0) {
-                float4 v = s_rank[1][0][lane];
+                float4 v = s_x.map[par][0][lane];
                 for (int r = 1; r < S; ++r) {
-                    const float4 o = s_rank[1][r][lane];
+                    const float4 o = s_x.map[par][r][lane];
                     v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
                 }
                 if (q.dbias) store_state(q.dbias, c, p.D, make_float2(v.x, v.y));
                 if (q.dscale) store_state(q.dscale, c, p.D, make_float2(v.z, v.w));
             }
+        }
+        if (S > 1) {  // no block leaves while another may still send to it
+            cluster_arrive();
+            cluster_wait();
         }
     }
 
@@ -257,13 +243,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_grad_kernel(const __grid_
 template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
 cudaError_t launch_grad_one(const GradArgs &q, cudaStream_t stream) {
     auto kernel = scan_grad_kernel<TA, TG, RAW, BETA, MODE>;
-    int per_sm = 1;
-    cudaError_t e = blocks_per_sm((const void *)kernel, kWarps * 32, 0, &per_sm);
-    if (e == cudaSuccess) e = large_clusters((const void *)kernel);
-    if (e != cudaSuccess) return e;
     const int cb = (q.f.D + 63) / 64, tile = Backward<TA, TG, RAW, BETA>::kTile;
-    const int S = cluster_blocks(cb, (q.f.T + tile - 1) / tile, per_sm * sm_count());
-    return launch_clusters(kernel, q, cb, S, stream);
+    int S = 1;
+    const cudaError_t e = cluster_blocks((const void *)kernel, 0, cb, (q.f.T + tile - 1) / tile, &S);
+    if (e != cudaSuccess) return e;
+    return launch_clusters(kernel, q, cb, S, 0, stream);
 }
 
 template <typename TA, typename TG, bool RAW, bool BETA>

@@ -2,7 +2,9 @@
 // along time, maps of runs of tokens, the launch.
 #pragma once
 
+#include "common.cuh"
 #include "launch.h"
+#include "ptx.cuh"
 #include "scan_launch.h"
 
 namespace gdn {
@@ -18,57 +20,140 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// Writes v to the same place of block `rank`'s shared memory.
-__device__ __forceinline__ void store_remote(float4 *p, uint32_t rank, float4 v) {
-    uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(p)), to;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                 : "memory");
-}
-
+// All blocks of the cluster have come here.  Orders no memory accesses.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 constexpr int kWarps = 8;
 constexpr int kMaxCluster = 16;
 
-// (A, H) of a run of two channels: x, y the first's, z, w the second's.  A run
-// in which a request begins has A = -0 and takes nothing of what is before it,
-// not even a NaN or an infinity (every other A is a product of exponentials, +0
-// at least).  Both channels of a run agree on it.
+// (A, H) of a run of two channels: x, y the A of both, z, w the H.  A run in which
+// a request begins has A = -0 and takes nothing of what is before it, not even a
+// NaN or an infinity (every other A is a product of exponentials, +0 at least).
 constexpr float kBegins = -0.f;
+__device__ __forceinline__ float4 map_of(float2 A, float2 H) { return make_float4(A.x, A.y, H.x, H.y); }
+__device__ __forceinline__ float2 map_a(const float4 r) { return make_float2(r.x, r.y); }
+__device__ __forceinline__ float2 map_h(const float4 r) { return make_float2(r.z, r.w); }
 __device__ __forceinline__ bool begins(const float4 r) { return __float_as_uint(r.x) == 0x80000000u; }
-// k followed by r.
-__device__ __forceinline__ void fold(float4 &k, const float4 r) {
-    if (begins(r)) {
-        k = r;
+// The run (A, H) followed by r.  RESETS: a request may begin in r.
+template <bool RESETS>
+__device__ __forceinline__ void fold(float2 &A, float2 &H, const float4 r) {
+    const float2 h = fma2(map_a(r), H, map_h(r)), a = A * map_a(r);
+    if (RESETS && begins(r)) {
+        A = map_a(r);
+        H = map_h(r);
     } else {
-        const bool b = begins(k);
-        k.y = fmaf(r.x, k.y, r.y);
-        k.x = b ? kBegins : k.x * r.x;
-        k.w = fmaf(r.z, k.w, r.w);
-        k.z *= r.z;
+        const bool b = RESETS && __float_as_uint(A.x) == 0x80000000u;
+        A = b ? A : a;
+        H = h;
     }
 }
 __device__ __forceinline__ float2 apply(const float4 r, float2 h) {
-    return begins(r) ? make_float2(r.y, r.w) : make_float2(fmaf(r.x, h.x, r.y), fmaf(r.z, h.y, r.w));
+    const float2 v = fma2(map_a(r), h, map_h(r));
+    return begins(r) ? map_h(r) : v;
+}
+
+// ---------------------------------------------------------------- staging
+// A warp's tokens of one tensor wait in shared memory of its own: `tokens` rows of
+// 64 channels.  Copies of 16 bytes run asynchronously where rows begin on 16-byte
+// addresses; otherwise the lanes load their channels and store them here.  Tokens of
+// no request and channels past the last are zeros.
+template <typename T, int TOKENS>
+struct Stage {
+    pair_t<T> v[TOKENS][32];
+
+    __device__ __forceinline__ void fill(const void *base, int64_t stride, int t, int block, unsigned own, int D,
+                                         bool wide, bool vec, int lane) {
+        constexpr int kRow = 64 * (int)sizeof(T), kPer = kRow / 16, kCopies = TOKENS * kPer / 32;
+        const T *p = static_cast<const T *>(base) + (int64_t)t * stride + block * 64;
+        if (wide) {
+            const int off = lane % kPer, row0 = lane / kPer;
+            int bytes = (D - block * 64) * (int)sizeof(T) - off * 16;
+            bytes = bytes < 0 ? 0 : (bytes > 16 ? 16 : bytes);
+            const char *src = reinterpret_cast<const char *>(p + row0 * stride) + off * 16;
+            char *dst = reinterpret_cast<char *>(&v[0][0]) + lane * 16;
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int n = (own >> (row0 + i * (32 / kPer)) & 1u) ? bytes : 0;
+                ptx::cp_async16(dst + i * 512, n ? src + (int64_t)i * (32 / kPer) * stride * (int)sizeof(T) : base, n);
+            }
+        } else {
+            const int c = block * 64 + 2 * lane;
+            if (c >= D) own = 0u;
+#pragma unroll
+            for (int k = 0; k < TOKENS; ++k)
+                v[k][lane] = (own >> k & 1u) ? load_pair<T>(p + k * stride + 2 * lane, vec, c + 1 < D) : zero_pair<T>();
+        }
+    }
+    __device__ __forceinline__ float2 at(int k, int lane) const { return unpack<T>(v[k][lane]); }
+};
+__device__ __forceinline__ void stage_wait() {
+    ptx::cp_async_wait_all();
+    __syncwarp();
+}
+
+// The exchange of the blocks' maps, one a window: a block sends its own to every
+// block of the cluster by asynchronous stores that count on the receiver's
+// mbarrier.  Nothing is fenced: a release at cluster scope would wait for the
+// outputs that the block has just stored to HBM (measured: 3.9 us a window with a
+// cluster barrier in place of this, 16 warps an SM).  Two buffers in turn suffice:
+// a block sends for window i + 2 once it has every block's map of window i + 1,
+// which a block sends after all its warps have read those of window i.
+struct Exchange {
+    float4 map[2][kMaxCluster][32];
+    uint64_t bar[2];
+};
+__device__ __forceinline__ void exchange_init(Exchange &x) {
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(&x.bar[0], 1);
+        ptx::mbar_init(&x.bar[1], 1);
+        ptx::fence_mbar_init();
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// One thread, once a window, before it waits.
+__device__ __forceinline__ void exchange_expect(Exchange &x, int par, int S) {
+    ptx::mbar_arrive_expect_tx(&x.bar[par], (uint32_t)S * 32u * sizeof(float4));
+}
+// A warp sends v (a lane's two channels) to block `to`, in this block's place.
+__device__ __forceinline__ void exchange_send(Exchange &x, int par, int from, int to, int lane, float4 v) {
+    uint32_t at, bar;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(&x.map[par][from][lane])), "r"(to));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(ptx::smem_u32(&x.bar[par])), "r"(to));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+                 : "memory");
+}
+// Waits for the maps of the window that uses this buffer for the n-th time (from 0).
+// The wait is bounded; a block that gave up goes on (with wrong results, reported),
+// so that the others' stores still find its memory.
+__device__ __forceinline__ void exchange_wait(Exchange &x, int par, int n, int32_t *err) {
+    if (!ptx::mbar_wait(&x.bar[par], n & 1, 1u << 20) && err) atomicOr(err, kErrTimeout);
 }
 
 // The blocks along time of one channel block: the most, up to a cluster's limit,
 // with which all clusters are resident at once, and no more than there are tiles.
-inline int cluster_blocks(int channel_blocks, int tiles, int resident) {
-    int S = 1;
-    while (S < kMaxCluster && S < tiles && 2 * S * channel_blocks <= resident) S *= 2;
-    return S;
+inline cudaError_t cluster_blocks(const void *kernel, size_t smem, int channel_blocks, int tiles, int *S) {
+    cudaError_t e = smem_attr(kernel, (int)smem);
+    if (e == cudaSuccess) e = large_clusters(kernel);
+    int s = tiles < kMaxCluster ? tiles : kMaxCluster;
+    for (; e == cudaSuccess && s > 1; --s) {
+        int n = 0;
+        e = resident_clusters(kernel, kWarps * 32, smem, s, &n);
+        if (n >= channel_blocks) break;
+    }
+    *S = s < 1 ? 1 : s;
+    return e;
 }
 
 // Launches a kernel in clusters of S blocks.
 template <typename P>
-cudaError_t launch_clusters(void (*kernel)(P), const P &p, int channel_blocks, int S, cudaStream_t stream) {
+cudaError_t launch_clusters(void (*kernel)(P), const P &p, int channel_blocks, int S, size_t smem,
+                            cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)channel_blocks * (unsigned)S);
     cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

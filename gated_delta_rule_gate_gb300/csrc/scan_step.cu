@@ -59,19 +59,24 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(const __grid_consta
         load_channels<float, V>(p.scale + c, scale);
     }
     for (int t = t0; t < t1; ++t) {
-        float x[V], z[V], y[V];
+        float x[V], z[V], y[V] = {};
         load_channels<TA, V>(static_cast<const TA *>(p.x) + t * p.xs + c, x);
         load_channels<TG, V>(static_cast<const TG *>(p.decay) + t * p.gs + c, z);
         if (p.beta) load_channels<TG, V>(static_cast<const TG *>(p.beta) + t * p.bs + c, y);
+        constexpr int W = V > 1 ? V / 2 : 1;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float g = p.bias ? log_decay<true>(z[v], bias[v], scale[v]) : z[v];
-            const float a = expf(g);
-            float u = x[v];
-            if (p.beta) u *= p.sigmoid ? sigmoid(y[v]) : y[v];
-            if (p.mode == kLerp) u *= input_scale<kLerp>(g, a);
-            if (p.mode == kUnit) u *= input_scale<kUnit>(g, a);
-            h[v] = fmaf(a, h[v], u);
+        for (int w = 0; w < W; ++w) {
+            const int i = 2 * w, j = V > 1 ? i + 1 : i;
+            const float2 zz = make_float2(z[i], z[j]), yy = make_float2(y[i], y[j]);
+            const float2 bb = make_float2(bias[i], bias[j]), ss = make_float2(scale[i], scale[j]);
+            const float2 m = exp_minus_1(p.bias ? log_decay<true>(zz, bb, ss) : zz), a = m + splat(1.f);
+            float2 u = make_float2(x[i], x[j]);
+            if (p.beta) u = u * (p.sigmoid ? sigmoid(yy) : yy);
+            if (p.mode == kLerp) u = u * make_float2(-m.x, -m.y);
+            if (p.mode == kUnit) u = u * unit_scale(m);
+            const float2 r = fma2(a, make_float2(h[i], h[j]), u);
+            h[i] = r.x;
+            h[j] = V > 1 ? r.y : r.x;
         }
         store_channels<TA, V>(static_cast<TA *>(p.o) + t * p.os + c, h);
     }
