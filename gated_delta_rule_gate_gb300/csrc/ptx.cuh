@@ -389,5 +389,15 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const void *tmap, int c0,
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
         : "memory");
 }
+// Tiled tensor store (TMA) of a 2-D box, in the issuing thread's bulk group.
+__device__ __forceinline__ void tma_store_2d(const void *tmap, int c0, int c1, const void *src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(tmap)),
+                 "r"(c0), "r"(c1), "r"(smem_u32(src))
+                 : "memory");
+}
+// Shared memory written by this thread's generic stores, and by those it has
+// synchronised with, is seen by the asynchronous copies that follow.
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 }  // namespace ptx
 }  // namespace gdn

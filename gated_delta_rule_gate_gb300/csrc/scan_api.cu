@@ -1,6 +1,9 @@
 // scan_api.cu -- the C entry points of the gated linear recurrence: host-side
 // validation and dispatch.  Every check runs before anything is enqueued.
+#include <cuda.h>  // CUtensorMap (the encoder is fetched through the runtime)
+
 #include "launch.h"
+#include "scan_cluster.cuh"
 #include "scan_launch.h"
 #include "status.h"
 
@@ -95,7 +98,8 @@ gdn_status validate(const gdn_scan_args *a, bool needs_o, Args *out) {
     p.err = a->error_word;
     p.vec = p.D % 2 == 0 && pairs(a->x, ea, p.xs) && (!needs_o || pairs(a->o, ea, p.os)) &&
             pairs(a->decay, eg, p.gs) && pairs(a->beta, eg, p.bs);
-    p.wide = lines(a->x, ea, p.xs) && lines(a->decay, eg, p.gs) && lines(a->beta, eg, p.bs);
+    p.wide = p.T > 0 && lines(a->x, ea, p.xs) && (!needs_o || lines(a->o, ea, p.os)) && lines(a->decay, eg, p.gs) &&
+             lines(a->beta, eg, p.bs);
     return GDN_OK;
 }
 
@@ -173,6 +177,28 @@ gdn_status gdn_scan_backward(const gdn_scan_grad_args *a, gdn_stream stream) {
 
 namespace gdn {
 namespace scan {
+
+bool make_token_map(CUtensorMap *m, const void *base, int type, int64_t stride, int channels, int rows, int tokens) {
+    typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e =
+            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
+        return reinterpret_cast<Encode>(e == cudaSuccess && q == cudaDriverEntryPointSuccess ? ptr : nullptr);
+    }();
+    if (!encode) return false;
+    const CUtensorMapDataType types[3] = {CU_TENSOR_MAP_DATA_TYPE_FLOAT32, CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                                          CU_TENSOR_MAP_DATA_TYPE_BFLOAT16};
+    const cuuint64_t dims[2] = {(cuuint64_t)channels, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)stride * (type == 0 ? 4 : 2)};
+    const cuuint32_t box[2] = {64, (cuuint32_t)tokens}, step[2] = {1, 1};
+    return encode(m, types[type], 2, const_cast<void *>(base), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 cudaError_t launch_scan(const Args &p, int act, int gate, cudaStream_t stream) {
     if (act == GDN_DTYPE_F32) return launch_scan_f32(p, stream);

@@ -247,7 +247,7 @@ cudaError_t launch_grad_one(const GradArgs &q, cudaStream_t stream) {
     int S = 1;
     const cudaError_t e = cluster_blocks((const void *)kernel, 0, cb, (q.f.T + tile - 1) / tile, &S);
     if (e != cudaSuccess) return e;
-    return launch_clusters(kernel, q, cb, S, 0, stream);
+    return launch_clusters(cb, S, 0, stream, kernel, q);
 }
 
 template <typename TA, typename TG, bool RAW, bool BETA>

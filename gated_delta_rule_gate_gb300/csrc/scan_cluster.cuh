@@ -2,6 +2,10 @@
 // along time, maps of runs of tokens, the launch.
 #pragma once
 
+#include <cuda.h>  // CUtensorMap
+
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.h"
 #include "ptx.cuh"
@@ -52,44 +56,62 @@ __device__ __forceinline__ float2 apply(const float4 r, float2 h) {
     return begins(r) ? map_h(r) : v;
 }
 
-// ---------------------------------------------------------------- staging
-// A warp's tokens of one tensor wait in shared memory of its own: `tokens` rows of
-// 64 channels.  Copies of 16 bytes run asynchronously where rows begin on 16-byte
-// addresses; otherwise the lanes load their channels and store them here.  Tokens of
-// no request and channels past the last are zeros.
-template <typename T, int TOKENS>
-struct Stage {
-    pair_t<T> v[TOKENS][32];
-
-    __device__ __forceinline__ void fill(const void *base, int64_t stride, int t, int block, unsigned own, int D,
-                                         bool wide, bool vec, int lane) {
-        constexpr int kRow = 64 * (int)sizeof(T), kPer = kRow / 16, kCopies = TOKENS * kPer / 32;
-        const T *p = static_cast<const T *>(base) + (int64_t)t * stride + block * 64;
-        if (wide) {
-            const int off = lane % kPer, row0 = lane / kPer;
-            int bytes = (D - block * 64) * (int)sizeof(T) - off * 16;
-            bytes = bytes < 0 ? 0 : (bytes > 16 ? 16 : bytes);
-            const char *src = reinterpret_cast<const char *>(p + row0 * stride) + off * 16;
-            char *dst = reinterpret_cast<char *>(&v[0][0]) + lane * 16;
+// The state after the runs r[0], r[32], ... r[32 (n - 1)] of a lane, and in `at` the
+// one before run `me`.  Four maps are on their way at a time.
+__device__ __forceinline__ float2 apply_all(const float4 *r, int n, int me, float2 h, float2 &at) {
+    const float2 h0 = h;
+    uint32_t any = 0u;
+    for (int i = 0; i < n; i += 4) {
+        float4 k[4];
 #pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-                const int n = (own >> (row0 + i * (32 / kPer)) & 1u) ? bytes : 0;
-                ptx::cp_async16(dst + i * 512, n ? src + (int64_t)i * (32 / kPer) * stride * (int)sizeof(T) : base, n);
-            }
-        } else {
-            const int c = block * 64 + 2 * lane;
-            if (c >= D) own = 0u;
+        for (int j = 0; j < 4; ++j) k[j] = r[32 * (i + j < n ? i + j : n - 1)];
 #pragma unroll
-            for (int k = 0; k < TOKENS; ++k)
-                v[k][lane] = (own >> k & 1u) ? load_pair<T>(p + k * stride + 2 * lane, vec, c + 1 < D) : zero_pair<T>();
+        for (int j = 0; j < 4; ++j) {
+            if (i + j >= n) break;
+            if (i + j == me) at = h;
+            any |= __float_as_uint(k[j].x);
+            h = fma2(map_a(k[j]), h, map_h(k[j]));
         }
+    }
+    if (any >> 31) {  // a request begins in one of them
+        h = h0;
+        for (int i = 0; i < n; ++i) {
+            const float4 k = r[32 * i];
+            if (i == me) at = h;
+            h = __float_as_uint(k.x) >> 31 ? map_h(k) : fma2(map_a(k), h, map_h(k));
+        }
+    }
+    return h;
+}
+
+// ---------------------------------------------------------------- staging
+// A warp's tokens of one tensor wait in shared memory of its own: TOKENS rows of 64
+// channels, one box of a tensor map, which completes on the warp's mbarrier.  (By
+// cp.async, 16 bytes a lane, a warp was held up 160 cycles a copy on the way.)
+// Without a tensor map -- rows that do not begin on 16-byte addresses -- the lanes
+// load their channels and store them here.
+template <typename T, int TOKENS>
+struct alignas(128) Stage {
+    pair_t<T> v[TOKENS][32];
+    static constexpr uint32_t kBytes = TOKENS * 64 * sizeof(T);
+
+    __device__ __forceinline__ void fill(const CUtensorMap &map, int t, int block, uint64_t *bar) {
+        ptx::tma_load_2d(&v[0][0], &map, block * 64, t, bar);
+    }
+    __device__ __forceinline__ void fill_plain(const void *base, int64_t stride, int t, int block, unsigned own, int D,
+                                               bool vec, int lane) {
+        const int c = block * 64 + 2 * lane;
+        const T *p = static_cast<const T *>(base) + (int64_t)t * stride + c;
+        if (c >= D) own = 0u;
+#pragma unroll
+        for (int k = 0; k < TOKENS; ++k)
+            v[k][lane] = (own >> k & 1u) ? load_pair<T>(p + k * stride, vec, c + 1 < D) : zero_pair<T>();
     }
     __device__ __forceinline__ float2 at(int k, int lane) const { return unpack<T>(v[k][lane]); }
 };
-__device__ __forceinline__ void stage_wait() {
-    ptx::cp_async_wait_all();
-    __syncwarp();
-}
+
+// [rows, channels] of elements of type T, boxes of 64 channels x `tokens` rows.
+bool make_token_map(CUtensorMap *m, const void *base, int type, int64_t stride, int channels, int rows, int tokens);
 
 // The exchange of the blocks' maps, one a window: a block sends its own to every
 // block of the cluster by asynchronous stores that count on the receiver's
@@ -147,9 +169,9 @@ inline cudaError_t cluster_blocks(const void *kernel, size_t smem, int channel_b
 }
 
 // Launches a kernel in clusters of S blocks.
-template <typename P>
-cudaError_t launch_clusters(void (*kernel)(P), const P &p, int channel_blocks, int S, size_t smem,
-                            cudaStream_t stream) {
+template <typename... P, typename... A>
+cudaError_t launch_clusters(int channel_blocks, int S, size_t smem, cudaStream_t stream, void (*kernel)(P...),
+                            const A &...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)channel_blocks * (unsigned)S);
     cfg.blockDim = dim3(kWarps * 32);
@@ -161,7 +183,12 @@ cudaError_t launch_clusters(void (*kernel)(P), const P &p, int channel_blocks, i
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T>
+constexpr int type_of() {
+    return std::is_same<T, float>::value ? 0 : (std::is_same<T, __half>::value ? 1 : 2);
 }
 
 }  // namespace scan

@@ -39,6 +39,10 @@ __device__ __forceinline__ void request_duties(const Args &p, int warps, int war
     }
 }
 
+struct Maps {
+    CUtensorMap x, z, y, o;
+};
+
 template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
 struct Forward {
     static constexpr int kTokens = sizeof(TA) == 2 ? 16 : 8;
@@ -48,16 +52,29 @@ struct Forward {
         Stage<TA, kTokens> x;
         Stage<TG, kTokens> z, y[BETA ? 1 : 0];
     };
-    struct Shared {
+    struct alignas(128) Shared {
+        Input in[kWarps];
+        Stage<TA, kTokens> out[kWarps];
         Exchange x;
         float4 map[2][kWarps][32];
-        Input in[kWarps];
+        uint64_t bar[kWarps];
     };
 
-    static __device__ __forceinline__ void fill(const Args &p, Input &in, int t, int block, unsigned own, int lane) {
-        in.x.fill(p.x, p.xs, t, block, own, p.D, p.wide, p.vec, lane);
-        in.z.fill(p.decay, p.gs, t, block, own, p.D, p.wide, p.vec, lane);
-        if constexpr (BETA) in.y[0].fill(p.beta, p.bs, t, block, own, p.D, p.wide, p.vec, lane);
+    // The warp's tokens t, ... on their way to its stage.
+    static __device__ __forceinline__ void fill(const Args &p, const Maps &m, Input &in, uint64_t *bar, int t, int block,
+                                                unsigned own, int lane) {
+        if (p.wide) {
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(bar, sizeof(Input));
+                in.x.fill(m.x, t, block, bar);
+                in.z.fill(m.z, t, block, bar);
+                if constexpr (BETA) in.y[0].fill(m.y, t, block, bar);
+            }
+        } else {
+            in.x.fill_plain(p.x, p.xs, t, block, own, p.D, p.vec, lane);
+            in.z.fill_plain(p.decay, p.gs, t, block, own, p.D, p.vec, lane);
+            if constexpr (BETA) in.y[0].fill_plain(p.beta, p.bs, t, block, own, p.D, p.vec, lane);
+        }
     }
 
     // a, u of the warp's tokens and its map.  PLAIN: all of them inside one request.
@@ -86,17 +103,27 @@ struct Forward {
         return map_of(A, H);
     }
 
+    // o of the warp's tokens, which a plain run hands to an asynchronous copy.
     template <bool PLAIN>
-    static __device__ __forceinline__ void second_walk(const Args &p, const Tokens &tok, int t, int c,
+    static __device__ __forceinline__ void second_walk(const Args &p, const Maps &m, Stage<TA, kTokens> &out,
+                                                       const Tokens &tok, int t, int c, int lane,
                                                        const float2 (&a)[kTokens], const float2 (&u)[kTokens],
                                                        float2 h) {
         TA *o = static_cast<TA *>(p.o) + (int64_t)t * p.os + c;
         const bool ok0 = c < p.D, ok1 = c + 1 < p.D;
-        if (PLAIN && p.vec) {
+        if (PLAIN && p.wide) {
+            if (lane == 0) ptx::bulk_wait_read();  // the last copy has left the stage
+            __syncwarp();
 #pragma unroll
             for (int k = 0; k < kTokens; ++k) {
                 h = fma2(a[k], h, u[k]);
-                if (ok0) *reinterpret_cast<pair_t<TA> *>(o + k * p.os) = pack<TA>(h);
+                out.v[k][lane] = pack<TA>(h);
+            }
+            ptx::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                ptx::tma_store_2d(&m.o, c, t, &out.v[0][0]);
+                ptx::bulk_commit();
             }
             return;
         }
@@ -111,7 +138,7 @@ struct Forward {
         }
     }
 
-    static __device__ __forceinline__ void run(const Args &p, Shared &s) {
+    static __device__ __forceinline__ void run(const Args &p, const Maps &m, Shared &s) {
         const int S = cluster_size(), rank = cluster_rank();
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         const int block = (int)(blockIdx.x / S), c = block * 64 + 2 * lane;
@@ -119,63 +146,71 @@ struct Forward {
 
         const int window = S * kTile, steps = (p.T + window - 1) / window;
         int t = rank * kTile + warp * kTokens;
-        Seen seen;
         Input &in = s.in[warp];
+        uint64_t *bar = &s.bar[warp];
+        if (lane == 0) {
+            ptx::mbar_init(bar, 1);
+            ptx::fence_mbar_init();
+        }
+        __syncwarp();
+        Seen seen;
         Tokens tok = look_up(p, t, kTokens, lane, seen);
-        fill(p, in, t, block, tok.own, lane);
+        if (steps > 0) fill(p, m, in, bar, t, block, tok.own, lane);
         float2 bias = splat(0.f), scale = bias;
         if (RAW) bias = load_state(p.bias, c, p.D), scale = load_state(p.scale, c, p.D);
         request_duties(p, S * kWarps, rank * kWarps + warp, lane, c, blockIdx.x < S);
         if (S > 1) exchange_init(s.x);
 
         float2 carry = splat(0.f);  // the state before the window
-        for (int step = 0; step < steps; ++step) {
+        for (int step = 0; step < steps; ++step, t += window) {
             const int par = step & 1;
             float2 a[kTokens], u[kTokens];
             const Tokens now = tok;
-            const int tn = t;
             const bool plain = now.own == kAll && !(now.first | now.last);
-            stage_wait();
-            s.map[par][warp][lane] = plain ? first_walk<true>(p, in, now, c, lane, bias, scale, a, u)
-                                           : first_walk<false>(p, in, now, c, lane, bias, scale, a, u);
-            t += window;
+            if (p.wide) {
+                if (!ptx::mbar_wait(bar, par) && p.err) atomicOr(p.err, kErrTimeout);
+            } else {
+                __syncwarp();
+            }
+            const float4 mine = plain ? first_walk<true>(p, in, now, c, lane, bias, scale, a, u)
+                                      : first_walk<false>(p, in, now, c, lane, bias, scale, a, u);
+            s.map[par][warp][lane] = mine;
             __syncwarp();
             if (step + 1 < steps) {
-                tok = look_up(p, t, kTokens, lane, seen);
-                fill(p, in, t, block, tok.own, lane);
+                tok = look_up(p, t + window, kTokens, lane, seen);
+                fill(p, m, in, bar, t + window, block, tok.own, lane);
             }
-            // the runs of the block's warps: those before this warp's, and all
             const bool resets = __syncthreads_or(now.first);
-            float2 A = splat(1.f), H = splat(0.f), beforeA = A, beforeH = H;
+            // the runs of the block before this warp's
+            float2 A = splat(1.f), H = splat(0.f);
             if (!resets) {
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    if (w == warp) beforeA = A, beforeH = H;
-                    fold<false>(A, H, s.map[par][w][lane]);
-                }
+                for (int w = 0; w < kWarps - 1; ++w)
+                    if (w < warp) fold<false>(A, H, s.map[par][w][lane]);
             } else {
-                for (int w = 0; w < kWarps; ++w) {
-                    if (w == warp) beforeA = A, beforeH = H;
-                    fold<true>(A, H, s.map[par][w][lane]);
-                }
+                for (int w = 0; w < warp; ++w) fold<true>(A, H, s.map[par][w][lane]);
             }
+            const float4 before = map_of(A, H);
             float2 h = carry;
             if (S > 1) {
                 if (threadIdx.x == 0) exchange_expect(s.x, par, S);
-                for (int r = warp; r < S; r += kWarps) exchange_send(s.x, par, rank, r, lane, map_of(A, H));
+                if (warp == kWarps - 1) {  // has the whole tile's map
+                    fold<true>(A, H, mine);
+                    const float4 tile = map_of(A, H);
+                    for (int r = 0; r < S; ++r) exchange_send(s.x, par, rank, r, lane, tile);
+                }
                 exchange_wait(s.x, par, step >> 1, p.err);
-                for (int r = 0; r < rank; ++r) carry = apply(s.x.map[par][r][lane], carry);
-                h = carry;
-                for (int r = rank; r < S; ++r) carry = apply(s.x.map[par][r][lane], carry);
+                carry = apply_all(&s.x.map[par][0][lane], S, rank, carry, h);
+                h = apply(before, h);
             } else {
-                carry = apply(map_of(A, H), carry);
+                carry = apply_all(&s.map[par][0][lane], kWarps, warp, carry, h);
             }
-            h = apply(map_of(beforeA, beforeH), h);
-            if (p.chunk && tn % kChunk == 0 && tn < p.T)
-                store_state(p.chunk + (size_t)(tn / kChunk) * p.D, c, p.D, h);
-            if (plain) second_walk<true>(p, now, tn, c, a, u, h);
-            else second_walk<false>(p, now, tn, c, a, u, h);
+            if (p.chunk && t % kChunk == 0 && t < p.T)
+                store_state(p.chunk + (size_t)(t / kChunk) * p.D, c, p.D, h);
+            if (plain) second_walk<true>(p, m, s.out[warp], now, t, c, lane, a, u, h);
+            else second_walk<false>(p, m, s.out[warp], now, t, c, lane, a, u, h);
         }
+        if (lane == 0) ptx::bulk_wait();
         if (S > 1) {  // no block leaves while another may still send to it
             cluster_arrive();
             cluster_wait();
@@ -184,10 +219,11 @@ struct Forward {
 };
 
 template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
-__global__ void __launch_bounds__(kWarps * 32, 2) scan_kernel(const __grid_constant__ Args p) {
+__global__ void __launch_bounds__(kWarps * 32, 2) scan_kernel(const __grid_constant__ Args p,
+                                                             const __grid_constant__ Maps m) {
     using F = Forward<TA, TG, RAW, BETA, MODE>;
-    extern __shared__ __align__(16) unsigned char smem[];
-    F::run(p, *reinterpret_cast<typename F::Shared *>(smem));
+    extern __shared__ __align__(128) unsigned char smem[];
+    F::run(p, m, *reinterpret_cast<typename F::Shared *>(smem));
 }
 
 template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
@@ -199,7 +235,14 @@ cudaError_t launch_one(const Args &p, cudaStream_t stream) {
     const cudaError_t e =
         cluster_blocks((const void *)kernel, sizeof(typename F::Shared), cb, (p.T + F::kTile - 1) / F::kTile, &S);
     if (e != cudaSuccess) return e;
-    return launch_clusters(kernel, p, cb, S, sizeof(typename F::Shared), stream);
+    Maps m = {};
+    Args q = p;
+    if (q.wide && !(make_token_map(&m.x, p.x, type_of<TA>(), p.xs, p.D, p.T, F::kTokens) &&
+                    make_token_map(&m.z, p.decay, type_of<TG>(), p.gs, p.D, p.T, F::kTokens) &&
+                    (!BETA || make_token_map(&m.y, p.beta, type_of<TG>(), p.bs, p.D, p.T, F::kTokens)) &&
+                    make_token_map(&m.o, p.o, type_of<TA>(), p.os, p.D, p.T, F::kTokens)))
+        q.wide = 0;
+    return launch_clusters(cb, S, sizeof(typename F::Shared), stream, kernel, q, m);
 }
 
 template <typename TA, typename TG, bool RAW, bool BETA>

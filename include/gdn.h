@@ -355,7 +355,7 @@ typedef enum gdn_input_scale {
  * seq_len, channels]), which seq_lens makes padded.  Here the clamped offsets
  * must not decrease (equal ones: an empty request); a decreasing pair sets
  * GDN_DEVERR_OVERLAP and the results of that call are unspecified (in bounds).
- * Tokens of no request are neither read nor written.
+ * Tokens of no request take no part in any result and are not written.
  *
  * x, decay, beta and o have channels contiguous and *_stride elements from one
  * token to the next (0: channels), so that they may be columns of a wider
