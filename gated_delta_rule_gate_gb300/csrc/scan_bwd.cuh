@@ -71,8 +71,8 @@ struct Backward {
 
     template <int MODE>
     static __device__ __forceinline__ void run(const GradArgs &q, Sums &sums) {
-        __shared__ float4 s_fwd[2][kWarps][32];  // (A, H) of each warp's run
-        __shared__ float2 s_rev[2][kWarps][32];  // C of each warp's run
+        __shared__ float2 s_fwd[kWarps][64];  // (A, H) of each warp's run; at the end its sums
+        __shared__ Meeting s_rev;
         __shared__ Exchange s_x;
         const Args &p = q.f;
         const int S = cluster_size(), rank = cluster_rank();
@@ -86,15 +86,13 @@ struct Backward {
 
         const int window = S * kTile, steps = (p.T + window - 1) / window;
         Seen seen;
-        float2 carry = make_float2(0.f, 0.f);  // c behind the window
+        float carry = 0.f;  // threads 0 to 63: c of a channel behind the window
         for (int turn = 0; turn < steps; ++turn) {
-            const int step = steps - 1 - turn, par = turn & 1;
+            const int step = steps - 1 - turn;
             const int tile = step * window + rank * kTile, t = tile + warp * kTokens;
             const Tokens tok = look_up(p, t, kTokens, lane, seen);
             Raw raw;
             load(q, t, c, tok.own, raw);
-            float2 h = make_float2(0.f, 0.f);
-            if (tile < p.T) h = load_state(p.chunk + (size_t)(tile / kChunk) * p.D, c, p.D);
 
             float2 a[kTokens], u[kTokens];
             float2 A = splat(1.f), H = splat(0.f);
@@ -121,30 +119,24 @@ struct Backward {
                 if (tok.first >> k & 1u) rev = splat(0.f);
             }
             if (tok.first) A = splat(kBegins);
-            s_fwd[par][warp][lane] = map_of(A, H);
-            s_rev[par][warp][lane] = rev;
+            *reinterpret_cast<float4 *>(&s_fwd[warp][2 * lane]) = make_float4(A.x, H.x, A.y, H.y);
+            *reinterpret_cast<float4 *>(&s_rev.map[warp][2 * lane]) = make_float4(A.x, rev.x, A.y, rev.y);
             __syncthreads();
-            for (int w = 0; w < warp; ++w) h = apply(s_fwd[par][w][lane], h);
-            float2 wholeA = splat(1.f), wholeC = splat(0.f), afterA = wholeA, afterC = wholeC;
-#pragma unroll
-            for (int w = kWarps - 1; w >= 0; --w) {
-                if (w == warp) afterA = wholeA, afterC = wholeC;
-                fold<true>(wholeA, wholeC, map_of(map_a(s_fwd[par][w][lane]), s_rev[par][w][lane]));
-            }
-            const float4 whole = map_of(wholeA, wholeC), after = map_of(afterA, afterC);
-            float2 dc = carry;
-            if (S > 1) {
-                if (threadIdx.x == 0) exchange_expect(s_x, par, S);
-                for (int r = warp; r < S; r += kWarps) exchange_send(s_x, par, rank, r, lane, whole);
-                exchange_wait(s_x, par, turn >> 1, p.err);
-                for (int r = S - 1; r >= 0; --r) {
-                    if (r == rank) dc = carry;
-                    carry = apply(s_x.map[par][r][lane], carry);
+            if (threadIdx.x < 64) {
+                meet<true>(s_rev, s_x, S, rank, turn, threadIdx.x, carry, p.err);
+            } else if (threadIdx.x < 128) {  // the states before the runs, in their place
+                const int k = threadIdx.x - 64, ch = (int)(blockIdx.x / S) * 64 + k;
+                float v = tile < p.T && ch < p.D ? p.chunk[(size_t)(tile / kChunk) * p.D + ch] : 0.f;
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 r = s_fwd[w][k];
+                    s_fwd[w][k].x = v;
+                    v = apply(r, v);
                 }
-            } else {
-                carry = apply(whole, carry);
             }
-            dc = apply(after, dc);
+            __syncthreads();
+            float2 dc = *reinterpret_cast<const float2 *>(&s_rev.h[warp][2 * lane]);
+            const float4 hh = *reinterpret_cast<const float4 *>(&s_fwd[warp][2 * lane]);
+            float2 h = make_float2(hh.x, hh.z);
 
             float2 prev[kTokens];
 #pragma unroll
@@ -187,32 +179,26 @@ struct Backward {
             }
         }
         if (RAW) {  // sums over the block's warps, then over the cluster's blocks
-            __syncthreads();
-            s_fwd[0][warp][lane] = make_float4(sums.bias.x, sums.bias.y, sums.scale.x, sums.scale.y);
-            __syncthreads();
             const int par = steps & 1;  // one turn more of the exchange
-            if (S > 1 && threadIdx.x == 0) exchange_expect(s_x, par, S);
-            if (warp == 0) {
-                float4 v = s_fwd[0][0][lane];
-                for (int w = 1; w < kWarps; ++w) {
-                    const float4 o = s_fwd[0][w][lane];
-                    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-                }
+            float4 *mine = reinterpret_cast<float4 *>(&s_fwd[warp][2 * lane]);
+            __syncthreads();
+            *mine = make_float4(sums.bias.x, sums.scale.x, sums.bias.y, sums.scale.y);
+            __syncthreads();
+            if (threadIdx.x < 64) {
+                const int k = threadIdx.x, ch = (int)(blockIdx.x / S) * 64 + k;
+                float2 v = s_fwd[0][k];
+                for (int w = 1; w < kWarps; ++w) v = v + s_fwd[w][k];
                 if (S > 1) {
-                    for (int r = 0; r < S; ++r) exchange_send(s_x, par, rank, r, lane, v);
+                    if (k == 0) exchange_expect(s_x, par, S);
+                    for (int r = 0; r < S; ++r) exchange_send(s_x, par, rank, r, k, v);
                     exchange_wait(s_x, par, steps >> 1, p.err);
-                } else {
-                    s_x.map[par][0][lane] = v;
+                    v = s_x.map[par][0][k];
+                    for (int r = 1; r < S; ++r) v = v + s_x.map[par][r][k];
                 }
-            }
-            if (rank == 0 && warp == 0) {
-                float4 v = s_x.map[par][0][lane];
-                for (int r = 1; r < S; ++r) {
-                    const float4 o = s_x.map[par][r][lane];
-                    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+                if (rank == 0 && ch < p.D) {
+                    if (q.dbias) q.dbias[ch] = v.x;
+                    if (q.dscale) q.dscale[ch] = v.y;
                 }
-                if (q.dbias) store_state(q.dbias, c, p.D, make_float2(v.x, v.y));
-                if (q.dscale) store_state(q.dscale, c, p.D, make_float2(v.z, v.w));
             }
         }
         if (S > 1) {  // no block leaves while another may still send to it

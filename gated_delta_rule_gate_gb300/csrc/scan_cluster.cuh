@@ -30,58 +30,17 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 constexpr int kWarps = 8;
 constexpr int kMaxCluster = 16;
 
-// (A, H) of a run of two channels: x, y the A of both, z, w the H.  A run in which
-// a request begins has A = -0 and takes nothing of what is before it, not even a
-// NaN or an infinity (every other A is a product of exponentials, +0 at least).
+// (A, H) of a run of one channel.  A run in which a request begins has A = -0 and
+// takes nothing of what is before it, not even a NaN or an infinity (every other A
+// is a product of exponentials, +0 at least).
 constexpr float kBegins = -0.f;
-__device__ __forceinline__ float4 map_of(float2 A, float2 H) { return make_float4(A.x, A.y, H.x, H.y); }
-__device__ __forceinline__ float2 map_a(const float4 r) { return make_float2(r.x, r.y); }
-__device__ __forceinline__ float2 map_h(const float4 r) { return make_float2(r.z, r.w); }
-__device__ __forceinline__ bool begins(const float4 r) { return __float_as_uint(r.x) == 0x80000000u; }
-// The run (A, H) followed by r.  RESETS: a request may begin in r.
-template <bool RESETS>
-__device__ __forceinline__ void fold(float2 &A, float2 &H, const float4 r) {
-    const float2 h = fma2(map_a(r), H, map_h(r)), a = A * map_a(r);
-    if (RESETS && begins(r)) {
-        A = map_a(r);
-        H = map_h(r);
-    } else {
-        const bool b = RESETS && __float_as_uint(A.x) == 0x80000000u;
-        A = b ? A : a;
-        H = h;
-    }
-}
-__device__ __forceinline__ float2 apply(const float4 r, float2 h) {
-    const float2 v = fma2(map_a(r), h, map_h(r));
-    return begins(r) ? map_h(r) : v;
-}
-
-// The state after the runs r[0], r[32], ... r[32 (n - 1)] of a lane, and in `at` the
-// one before run `me`.  Four maps are on their way at a time.
-__device__ __forceinline__ float2 apply_all(const float4 *r, int n, int me, float2 h, float2 &at) {
-    const float2 h0 = h;
-    uint32_t any = 0u;
-    for (int i = 0; i < n; i += 4) {
-        float4 k[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) k[j] = r[32 * (i + j < n ? i + j : n - 1)];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (i + j >= n) break;
-            if (i + j == me) at = h;
-            any |= __float_as_uint(k[j].x);
-            h = fma2(map_a(k[j]), h, map_h(k[j]));
-        }
-    }
-    if (any >> 31) {  // a request begins in one of them
-        h = h0;
-        for (int i = 0; i < n; ++i) {
-            const float4 k = r[32 * i];
-            if (i == me) at = h;
-            h = __float_as_uint(k.x) >> 31 ? map_h(k) : fma2(map_a(k), h, map_h(k));
-        }
-    }
-    return h;
+__device__ __forceinline__ bool begins(float A) { return __float_as_uint(A) == 0x80000000u; }
+// What the run makes of the state h.
+__device__ __forceinline__ float apply(float2 r, float h) { return begins(r.x) ? r.y : fmaf(r.x, h, r.y); }
+// The run k followed by r.
+__device__ __forceinline__ float2 fold(float2 k, float2 r) {
+    const float A = begins(k.x) ? kBegins : k.x * r.x;
+    return make_float2(begins(r.x) ? kBegins : A, apply(r, k.y));
 }
 
 // ---------------------------------------------------------------- staging
@@ -116,12 +75,11 @@ bool make_token_map(CUtensorMap *m, const void *base, int type, int64_t stride, 
 // The exchange of the blocks' maps, one a window: a block sends its own to every
 // block of the cluster by asynchronous stores that count on the receiver's
 // mbarrier.  Nothing is fenced: a release at cluster scope would wait for the
-// outputs that the block has just stored to HBM (measured: 3.9 us a window with a
-// cluster barrier in place of this, 16 warps an SM).  Two buffers in turn suffice:
-// a block sends for window i + 2 once it has every block's map of window i + 1,
-// which a block sends after all its warps have read those of window i.
+// outputs that the block has just stored to HBM.  Two buffers in turn suffice: a
+// block sends for window i + 2 once it has every block's map of window i + 1, which
+// a block sends after it has read those of window i.
 struct Exchange {
-    float4 map[2][kMaxCluster][32];
+    float2 map[2][kMaxCluster][64];
     uint64_t bar[2];
 };
 __device__ __forceinline__ void exchange_init(Exchange &x) {
@@ -135,15 +93,15 @@ __device__ __forceinline__ void exchange_init(Exchange &x) {
 }
 // One thread, once a window, before it waits.
 __device__ __forceinline__ void exchange_expect(Exchange &x, int par, int S) {
-    ptx::mbar_arrive_expect_tx(&x.bar[par], (uint32_t)S * 32u * sizeof(float4));
+    ptx::mbar_arrive_expect_tx(&x.bar[par], (uint32_t)S * 64u * sizeof(float2));
 }
-// A warp sends v (a lane's two channels) to block `to`, in this block's place.
-__device__ __forceinline__ void exchange_send(Exchange &x, int par, int from, int to, int lane, float4 v) {
+// Sends channel c's v to block `to`, in block `from`'s place.
+__device__ __forceinline__ void exchange_send(Exchange &x, int par, int from, int to, int c, float2 v) {
     uint32_t at, bar;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(&x.map[par][from][lane])), "r"(to));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(&x.map[par][from][c])), "r"(to));
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(ptx::smem_u32(&x.bar[par])), "r"(to));
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
-                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(at),
+                 "f"(v.x), "f"(v.y), "r"(bar)
                  : "memory");
 }
 // Waits for the maps of the window that uses this buffer for the n-th time (from 0).
@@ -151,6 +109,54 @@ __device__ __forceinline__ void exchange_send(Exchange &x, int par, int from, in
 // so that the others' stores still find its memory.
 __device__ __forceinline__ void exchange_wait(Exchange &x, int par, int n, int32_t *err) {
     if (!ptx::mbar_wait(&x.bar[par], n & 1, 1u << 20) && err) atomicOr(err, kErrTimeout);
+}
+
+// The maps of a block's warps, of 64 channels each, and the states before them.
+struct Meeting {
+    float2 map[kWarps][64];
+    float h[kWarps][64];
+};
+// One of 64 threads, for channel c, between two barriers of the block: the states
+// before the warps' runs, from `carry`, the state before the window, which moves on
+// by a window.  Warps and blocks follow one another upwards, or (REVERSE) downwards.
+// One thread a channel instead of every warp for itself: the maps are read once (the
+// warps' own folding took 1,700 cycles a window of 8 blocks, of 6,800).
+template <bool REVERSE>
+__device__ __forceinline__ void meet(Meeting &m, Exchange &x, int S, int rank, int turn, int c, float &carry,
+                                     int32_t *err) {
+    const int par = turn & 1;
+    float2 run = make_float2(1.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        float2 *at = &m.map[REVERSE ? kWarps - 1 - i : i][c];
+        const float2 k = *at;
+        *at = run;
+        run = fold(run, k);
+    }
+    float h = carry;
+    if (S > 1) {
+        if (c == 0) exchange_expect(x, par, S);
+        for (int r = 0; r < S; ++r) exchange_send(x, par, rank, r, c, run);
+        exchange_wait(x, par, turn >> 1, err);
+        for (int i = 0; i < S; i += 4) {  // four maps on their way at a time
+            float2 k[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = i + j < S ? i + j : S - 1;
+                k[j] = x.map[par][REVERSE ? S - 1 - r : r][c];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (i + j >= S) break;
+                if ((REVERSE ? S - 1 - (i + j) : i + j) == rank) h = carry;
+                carry = apply(k[j], carry);
+            }
+        }
+    } else {
+        carry = apply(run, carry);
+    }
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) m.h[w][c] = apply(m.map[w][c], h);
 }
 
 // The blocks along time of one channel block: the most, up to a cluster's limit,

@@ -8,7 +8,7 @@
 // walks the whole token axis of its channels in windows of S tiles and carries
 // the state from window to window in registers.  Per window: every warp folds
 // its run to (A, H); the block's warps exchange theirs in shared memory, the
-// blocks theirs in distributed shared memory; every warp
+// blocks theirs in distributed shared memory (meet()); every warp
 // then has the state before its run, in the same order of operations on every
 // run, and walks its tokens, which have stayed in registers, a second time to
 // write o.  The loads of the next window are in flight meanwhile, so x, decay and
@@ -17,6 +17,11 @@
 #pragma once
 
 #include "scan_cluster.cuh"
+#ifndef SCAN_TOK
+#define SCAN_TOK 16
+#define SCAN_TOK32 8
+#define SCAN_MINB 2
+#endif
 
 namespace gdn {
 namespace scan {
@@ -45,7 +50,7 @@ struct Maps {
 
 template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
 struct Forward {
-    static constexpr int kTokens = sizeof(TA) == 2 ? 16 : 8;
+    static constexpr int kTokens = sizeof(TA) == 2 ? SCAN_TOK : SCAN_TOK32;
     static constexpr int kTile = kWarps * kTokens;
 
     struct Input {
@@ -56,7 +61,7 @@ struct Forward {
         Input in[kWarps];
         Stage<TA, kTokens> out[kWarps];
         Exchange x;
-        float4 map[2][kWarps][32];
+        Meeting meet;
         uint64_t bar[kWarps];
     };
 
@@ -100,7 +105,7 @@ struct Forward {
             A = A * a[k];
         }
         if (!PLAIN && tok.first) A = splat(kBegins);
-        return map_of(A, H);
+        return make_float4(A.x, H.x, A.y, H.y);
     }
 
     // o of the warp's tokens, which a plain run hands to an asynchronous copy.
@@ -161,7 +166,7 @@ struct Forward {
         request_duties(p, S * kWarps, rank * kWarps + warp, lane, c, blockIdx.x < S);
         if (S > 1) exchange_init(s.x);
 
-        float2 carry = splat(0.f);  // the state before the window
+        float carry = 0.f;  // threads 0 to 63: the state of a channel before the window
         for (int step = 0; step < steps; ++step, t += window) {
             const int par = step & 1;
             float2 a[kTokens], u[kTokens];
@@ -172,39 +177,18 @@ struct Forward {
             } else {
                 __syncwarp();
             }
-            const float4 mine = plain ? first_walk<true>(p, in, now, c, lane, bias, scale, a, u)
-                                      : first_walk<false>(p, in, now, c, lane, bias, scale, a, u);
-            s.map[par][warp][lane] = mine;
+            *reinterpret_cast<float4 *>(&s.meet.map[warp][2 * lane]) =
+                plain ? first_walk<true>(p, in, now, c, lane, bias, scale, a, u)
+                      : first_walk<false>(p, in, now, c, lane, bias, scale, a, u);
             __syncwarp();
             if (step + 1 < steps) {
                 tok = look_up(p, t + window, kTokens, lane, seen);
                 fill(p, m, in, bar, t + window, block, tok.own, lane);
             }
-            const bool resets = __syncthreads_or(now.first);
-            // the runs of the block before this warp's
-            float2 A = splat(1.f), H = splat(0.f);
-            if (!resets) {
-#pragma unroll
-                for (int w = 0; w < kWarps - 1; ++w)
-                    if (w < warp) fold<false>(A, H, s.map[par][w][lane]);
-            } else {
-                for (int w = 0; w < warp; ++w) fold<true>(A, H, s.map[par][w][lane]);
-            }
-            const float4 before = map_of(A, H);
-            float2 h = carry;
-            if (S > 1) {
-                if (threadIdx.x == 0) exchange_expect(s.x, par, S);
-                if (warp == kWarps - 1) {  // has the whole tile's map
-                    fold<true>(A, H, mine);
-                    const float4 tile = map_of(A, H);
-                    for (int r = 0; r < S; ++r) exchange_send(s.x, par, rank, r, lane, tile);
-                }
-                exchange_wait(s.x, par, step >> 1, p.err);
-                carry = apply_all(&s.x.map[par][0][lane], S, rank, carry, h);
-                h = apply(before, h);
-            } else {
-                carry = apply_all(&s.map[par][0][lane], kWarps, warp, carry, h);
-            }
+            __syncthreads();
+            if (threadIdx.x < 64) meet<false>(s.meet, s.x, S, rank, step, threadIdx.x, carry, p.err);
+            __syncthreads();
+            const float2 h = *reinterpret_cast<const float2 *>(&s.meet.h[warp][2 * lane]);
             if (p.chunk && t % kChunk == 0 && t < p.T)
                 store_state(p.chunk + (size_t)(t / kChunk) * p.D, c, p.D, h);
             if (plain) second_walk<true>(p, m, s.out[warp], now, t, c, lane, a, u, h);
@@ -219,7 +203,7 @@ struct Forward {
 };
 
 template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
-__global__ void __launch_bounds__(kWarps * 32, 2) scan_kernel(const __grid_constant__ Args p,
+__global__ void __launch_bounds__(kWarps * 32, SCAN_MINB) scan_kernel(const __grid_constant__ Args p,
                                                              const __grid_constant__ Maps m) {
     using F = Forward<TA, TG, RAW, BETA, MODE>;
     extern __shared__ __align__(128) unsigned char smem[];
