@@ -168,6 +168,8 @@ gdn_status gdn_scan_backward(const gdn_scan_grad_args *a, gdn_stream stream) {
     p.o = nullptr;
     p.vec = p.vec && pairs(a->d_o, ea, q.dos) && pairs(a->dx, ea, q.dxs) && pairs(a->d_decay, eg, q.dgs) &&
             pairs(a->d_beta, eg, q.dbs);
+    p.wide = p.wide && lines(a->d_o, ea, q.dos) && lines(a->dx, ea, q.dxs) && lines(a->d_decay, eg, q.dgs) &&
+             lines(a->d_beta, eg, q.dbs);
     if (p.B == 0 && !q.dbias && !q.dscale) return gdn::ok();
     return gdn::cuda_status(
         gdn::scan::launch_grad(q, a->forward.act_dtype, a->forward.gate_dtype, (cudaStream_t)stream));

@@ -36,164 +36,255 @@ __device__ __forceinline__ void gradient_duties(const GradArgs &q, int warps, in
     }
 }
 
-template <typename TA, typename TG, bool RAW, bool BETA>
+struct GradMaps {
+    CUtensorMap x, z, y, d, dx, dz, dy;
+};
+
+template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
 struct Backward {
     static constexpr int kTokens = 8;
     static constexpr int kTile = kWarps * kTokens;
     static_assert(kTile == kChunk, "a tile begins where the forward pass kept a state");
 
-    struct Raw {
-        pair_t<TA> x[kTokens], d[kTokens];
-        pair_t<TG> z[kTokens], y[BETA ? kTokens : 1];
+    // A warp's tokens; the gradients take the places of x, decay and beta.
+    struct Input {
+        Stage<TA, kTokens> x, d;
+        Stage<TG, kTokens> z, y[BETA ? 1 : 0];
     };
-
-    static __device__ __forceinline__ void load(const GradArgs &q, int t, int c, unsigned own, Raw &r) {
-        const Args &p = q.f;
-        const TA *x = static_cast<const TA *>(p.x) + (int64_t)t * p.xs + c;
-        const TA *d = static_cast<const TA *>(q.d_o) + (int64_t)t * q.dos + c;
-        const TG *z = static_cast<const TG *>(p.decay) + (int64_t)t * p.gs + c;
-        const TG *y = BETA ? static_cast<const TG *>(p.beta) + (int64_t)t * p.bs + c : nullptr;
-        const bool vec = p.vec, ok1 = c + 1 < p.D;
-        if (c >= p.D) own = 0u;
-#pragma unroll
-        for (int k = 0; k < kTokens; ++k) {
-            const bool on = own >> k & 1u;
-            r.x[k] = on ? load_pair<TA>(x + k * p.xs, vec, ok1) : zero_pair<TA>();
-            r.d[k] = on ? load_pair<TA>(d + k * q.dos, vec, ok1) : zero_pair<TA>();
-            r.z[k] = on ? load_pair<TG>(z + k * p.gs, vec, ok1) : zero_pair<TG>();
-            if (BETA) r.y[k] = on ? load_pair<TG>(y + k * p.bs, vec, ok1) : zero_pair<TG>();
-        }
-    }
-
+    struct Rest {
+        Exchange x;
+        Meeting rev;               // (A, C) of each warp's run, and c behind it
+        float2 fwd[kWarps][64];    // (A, H) of each warp's run, then the state before it; at the end its sums
+        uint64_t bar[kWarps][2];
+    };
+    // Two stages where two blocks an SM have room for them, so that a window's loads
+    // are on their way during the one before.
+    static constexpr int kRing = 2 * kWarps * sizeof(Input) + sizeof(Rest) <= 113 * 1024 ? 2 : 1;
+    struct alignas(128) Shared {
+        Input in[kWarps][kRing];
+        Rest r;
+    };
     struct Sums {
         float2 bias, scale;
     };
 
-    template <int MODE>
-    static __device__ __forceinline__ void run(const GradArgs &q, Sums &sums) {
-        __shared__ float2 s_fwd[kWarps][64];  // (A, H) of each warp's run; at the end its sums
-        __shared__ Meeting s_rev;
-        __shared__ Exchange s_x;
+    static __device__ __forceinline__ void fill(const GradArgs &q, const GradMaps &m, Input &in, uint64_t *bar, int t,
+                                                int block, unsigned own, int lane) {
         const Args &p = q.f;
-        const int S = cluster_size(), rank = cluster_rank();
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const int c = (int)(blockIdx.x / S) * 64 + 2 * lane;
+        if (p.wide) {
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(bar, sizeof(Input));
+                in.x.fill(m.x, t, block, bar);
+                in.d.fill(m.d, t, block, bar);
+                in.z.fill(m.z, t, block, bar);
+                if constexpr (BETA) in.y[0].fill(m.y, t, block, bar);
+            }
+        } else {
+            in.x.fill_plain(p.x, p.xs, t, block, own, p.D, p.vec, lane);
+            in.d.fill_plain(q.d_o, q.dos, t, block, own, p.D, p.vec, lane);
+            in.z.fill_plain(p.decay, p.gs, t, block, own, p.D, p.vec, lane);
+            if constexpr (BETA) in.y[0].fill_plain(p.beta, p.bs, t, block, own, p.D, p.vec, lane);
+        }
+    }
+
+    static __device__ __forceinline__ float2 first_state(const Args &p, const Tokens &tok, int k, int c) {
+        const int row = __shfl_sync(0xffffffffu, tok.row, k);
+        return p.init ? load_state(p.init + (size_t)row * p.D, c, p.D) : splat(0.f);
+    }
+    static __device__ __forceinline__ float2 last_gradient(const GradArgs &q, const Tokens &tok, int k, int c) {
+        const int row = __shfl_sync(0xffffffffu, tok.row, k);
+        return q.dfin ? load_state(q.dfin + (size_t)row * q.f.D, c, q.f.D) : splat(0.f);
+    }
+
+    // a, u of the warp's tokens and its maps, (A, H) and C.  PLAIN: all of them inside
+    // one request, neither its first nor its last token among them.
+    template <bool PLAIN>
+    static __device__ __forceinline__ void first_walk(const GradArgs &q, const Input &in, const Tokens &tok, int c,
+                                                      int lane, float2 bias, float2 scale, float2 (&a)[kTokens],
+                                                      float2 (&u)[kTokens], float2 &A, float2 &H, float2 &C) {
+        const Args &p = q.f;
+        A = splat(1.f), H = splat(0.f), C = splat(0.f);
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) {
+            float2 y = splat(0.f);
+            if constexpr (BETA) y = in.y[0].at(k, lane);
+            token_map<RAW, BETA, MODE>(in.x.at(k, lane), in.z.at(k, lane), y, bias, scale, p.sigmoid, a[k], u[k]);
+            if (!PLAIN) {
+                if (!(tok.own >> k & 1u)) a[k] = splat(1.f), u[k] = splat(0.f);
+                if (tok.first >> k & 1u) H = first_state(p, tok, k, c);
+            }
+            H = fma2(a[k], H, u[k]);
+            A = A * a[k];
+        }
+#pragma unroll
+        for (int k = kTokens - 1; k >= 0; --k) {
+            float2 d = in.d.at(k, lane);
+            if (!PLAIN) {
+                if (!(tok.own >> k & 1u)) d = splat(0.f);
+                if (tok.last >> k & 1u) d = d + last_gradient(q, tok, k, c);
+            }
+            C = a[k] * (d + C);
+            if (!PLAIN && (tok.first >> k & 1u)) C = splat(0.f);
+        }
+        if (!PLAIN && tok.first) A = splat(kBegins);
+    }
+
+    // The gradients of the warp's tokens, from the state before and c behind them.
+    template <bool PLAIN>
+    static __device__ __forceinline__ void second_walk(const GradArgs &q, const GradMaps &m, Input &in,
+                                                       const Tokens &tok, int t, int c, int lane, float2 bias,
+                                                       float2 scale, const float2 (&a)[kTokens],
+                                                       const float2 (&u)[kTokens], float2 h, float2 dc, Sums &sums) {
+        const Args &p = q.f;
+        float2 prev[kTokens];
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) {
+            if (!PLAIN && (tok.first >> k & 1u)) h = first_state(p, tok, k, c);
+            prev[k] = h;
+            h = fma2(a[k], h, u[k]);
+        }
         const bool ok0 = c < p.D, ok1 = c + 1 < p.D;
-        gradient_duties(q, S * kWarps, rank * kWarps + warp, lane, c, blockIdx.x < S);
-        float2 bias = make_float2(0.f, 0.f), scale = bias;
-        if (RAW) bias = load_state(p.bias, c, p.D), scale = load_state(p.scale, c, p.D);
-        if (S > 1) exchange_init(s_x);
-
-        const int window = S * kTile, steps = (p.T + window - 1) / window;
-        Seen seen;
-        float carry = 0.f;  // threads 0 to 63: c of a channel behind the window
-        for (int turn = 0; turn < steps; ++turn) {
-            const int step = steps - 1 - turn;
-            const int tile = step * window + rank * kTile, t = tile + warp * kTokens;
-            const Tokens tok = look_up(p, t, kTokens, lane, seen);
-            Raw raw;
-            load(q, t, c, tok.own, raw);
-
-            float2 a[kTokens], u[kTokens];
-            float2 A = splat(1.f), H = splat(0.f);
 #pragma unroll
-            for (int k = 0; k < kTokens; ++k) {
-                a[k] = splat(1.f), u[k] = splat(0.f);
-                if (tok.own >> k & 1u) {
-                    const float2 z = unpack<TG>(raw.z[k]), y = BETA ? unpack<TG>(raw.y[k]) : z;
-                    token_map<RAW, BETA, MODE>(unpack<TA>(raw.x[k]), z, y, bias, scale, p.sigmoid, a[k], u[k]);
-                }
-                if (tok.first >> k & 1u) {
-                    H = fma2(a[k], first_state(p, tok, k, c), u[k]);
-                } else {
-                    H = fma2(a[k], H, u[k]);
-                    A = A * a[k];
-                }
+        for (int k = kTokens - 1; k >= 0; --k) {
+            if (!PLAIN && !(tok.own >> k & 1u)) continue;  // hands c on
+            float2 dh = in.d.at(k, lane) + dc;
+            if (!PLAIN && (tok.last >> k & 1u)) dh = dh + last_gradient(q, tok, k, c);
+            const float2 x = in.x.at(k, lane), z = in.z.at(k, lane);
+            float2 y = splat(0.f);
+            if constexpr (BETA) y = in.y[0].at(k, lane);
+            const Terms g = gate_terms<RAW, BETA, MODE>(z, y, bias, scale, p.sigmoid);
+            dc = a[k] * dh;
+            float2 d = dc * prev[k];
+            if (MODE != kNone) d = fma2(g.dn * g.i * x, dh, d);
+            if (RAW) {
+                sums.scale = fma2(d, g.soft, sums.scale);
+                d = d * g.dgdz;
+                sums.bias = sums.bias + d;
             }
-            float2 rev = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int k = kTokens - 1; k >= 0; --k) {
-                float2 d = unpack<TA>(raw.d[k]);
-                if (tok.last >> k & 1u) add_final(q, tok, k, c, d);
-                rev = a[k] * (d + rev);
-                if (tok.first >> k & 1u) rev = splat(0.f);
+            const float2 w = g.n * dh;
+            if (PLAIN && p.wide) {
+                in.x.v[k][lane] = pack<TA>(w * g.i);
+                in.z.v[k][lane] = pack<TG>(d);
+                if constexpr (BETA) in.y[0].v[k][lane] = pack<TG>(w * x * g.di);
+            } else if (ok0) {
+                store_pair<TA>(static_cast<TA *>(q.dx) + (t + k) * q.dxs + c, w * g.i, p.vec, ok1);
+                store_pair<TG>(static_cast<TG *>(q.dg) + (t + k) * q.dgs + c, d, p.vec, ok1);
+                if constexpr (BETA)
+                    store_pair<TG>(static_cast<TG *>(q.db) + (t + k) * q.dbs + c, w * x * g.di, p.vec, ok1);
             }
-            if (tok.first) A = splat(kBegins);
-            *reinterpret_cast<float4 *>(&s_fwd[warp][2 * lane]) = make_float4(A.x, H.x, A.y, H.y);
-            *reinterpret_cast<float4 *>(&s_rev.map[warp][2 * lane]) = make_float4(A.x, rev.x, A.y, rev.y);
-            __syncthreads();
-            if (threadIdx.x < 64) {
-                meet<true>(s_rev, s_x, S, rank, turn, threadIdx.x, carry, p.err);
-            } else if (threadIdx.x < 128) {  // the states before the runs, in their place
-                const int k = threadIdx.x - 64, ch = (int)(blockIdx.x / S) * 64 + k;
-                float v = tile < p.T && ch < p.D ? p.chunk[(size_t)(tile / kChunk) * p.D + ch] : 0.f;
-                for (int w = 0; w < kWarps; ++w) {
-                    const float2 r = s_fwd[w][k];
-                    s_fwd[w][k].x = v;
-                    v = apply(r, v);
-                }
-            }
-            __syncthreads();
-            float2 dc = *reinterpret_cast<const float2 *>(&s_rev.h[warp][2 * lane]);
-            const float4 hh = *reinterpret_cast<const float4 *>(&s_fwd[warp][2 * lane]);
-            float2 h = make_float2(hh.x, hh.z);
-
-            float2 prev[kTokens];
-#pragma unroll
-            for (int k = 0; k < kTokens; ++k) {
-                if (tok.first >> k & 1u) h = first_state(p, tok, k, c);
-                prev[k] = h;
-                h = fma2(a[k], h, u[k]);
-            }
-            TA *dx = static_cast<TA *>(q.dx) + (int64_t)t * q.dxs + c;
-            TG *dg = static_cast<TG *>(q.dg) + (int64_t)t * q.dgs + c;
-            TG *db = BETA ? static_cast<TG *>(q.db) + (int64_t)t * q.dbs + c : nullptr;
-#pragma unroll
-            for (int k = kTokens - 1; k >= 0; --k) {
-                if (!(tok.own >> k & 1u)) continue;  // hands c on
-                float2 dh = unpack<TA>(raw.d[k]);
-                if (tok.last >> k & 1u) add_final(q, tok, k, c, dh);
-                dh = dh + dc;
-                const float2 z = unpack<TG>(raw.z[k]), y = BETA ? unpack<TG>(raw.y[k]) : z;
-                const float2 x = unpack<TA>(raw.x[k]);
-                const Terms g = gate_terms<RAW, BETA, MODE>(z, y, bias, scale, p.sigmoid);
-                dc = a[k] * dh;
-                float2 d = dc * prev[k];
-                if (MODE != kNone) d = fma2(g.dn * g.i * x, dh, d);
-                if (RAW) {
-                    sums.scale = fma2(d, g.soft, sums.scale);
-                    d = d * g.dgdz;
-                    sums.bias = sums.bias + d;
-                }
-                if (ok0) {
-                    const float2 w = g.n * dh;
-                    store_pair<TA>(dx + k * q.dxs, w * g.i, p.vec, ok1);
-                    store_pair<TG>(dg + k * q.dgs, d, p.vec, ok1);
-                    if (BETA) store_pair<TG>(db + k * q.dbs, w * x * g.di, p.vec, ok1);
-                }
-                if (tok.first >> k & 1u) {
-                    const int row = __shfl_sync(0xffffffffu, tok.row, k);
-                    if (q.dinit) store_state(q.dinit + (size_t)row * p.D, c, p.D, dc);
-                    dc = splat(0.f);
-                }
+            if (!PLAIN && (tok.first >> k & 1u)) {
+                const int row = __shfl_sync(0xffffffffu, tok.row, k);
+                if (q.dinit) store_state(q.dinit + (size_t)row * p.D, c, p.D, dc);
+                dc = splat(0.f);
             }
         }
-        if (RAW) {  // sums over the block's warps, then over the cluster's blocks
-            const int par = steps & 1;  // one turn more of the exchange
-            float4 *mine = reinterpret_cast<float4 *>(&s_fwd[warp][2 * lane]);
-            __syncthreads();
-            *mine = make_float4(sums.bias.x, sums.scale.x, sums.bias.y, sums.scale.y);
+        if (PLAIN && p.wide) {
+            ptx::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                ptx::tma_store_2d(&m.dx, c, t, &in.x.v[0][0]);
+                ptx::tma_store_2d(&m.dz, c, t, &in.z.v[0][0]);
+                if constexpr (BETA) ptx::tma_store_2d(&m.dy, c, t, &in.y[0].v[0][0]);
+                ptx::bulk_commit();
+            }
+        }
+    }
+
+    static __device__ __forceinline__ void run(const GradArgs &q, const GradMaps &m, Shared &s) {
+        const Args &p = q.f;
+        Rest &r = s.r;
+        const int S = cluster_size(), rank = cluster_rank();
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int block = (int)(blockIdx.x / S), c = block * 64 + 2 * lane;
+        constexpr unsigned kAll = (1u << kTokens) - 1u;
+        const int window = S * kTile, steps = (p.T + window - 1) / window;
+        if (lane == 0) {
+            ptx::mbar_init(&r.bar[warp][0], 1);
+            ptx::mbar_init(&r.bar[warp][1], 1);
+            ptx::fence_mbar_init();
+        }
+        __syncwarp();
+        // the windows from the last to the first
+        int t = (steps - 1) * window + rank * kTile + warp * kTokens;
+        Seen seen;
+        Tokens tok = {}, next = {};
+        if (steps > 0) {
+            tok = look_up(p, t, kTokens, lane, seen);
+            fill(q, m, s.in[warp][0], &r.bar[warp][0], t, block, tok.own, lane);
+        }
+        gradient_duties(q, S * kWarps, rank * kWarps + warp, lane, c, blockIdx.x < S);
+        float2 bias = splat(0.f), scale = bias;
+        if (RAW) bias = load_state(p.bias, c, p.D), scale = load_state(p.scale, c, p.D);
+        if (S > 1) exchange_init(r.x);
+
+        Sums sums = {};
+        float carry = 0.f;  // threads 0 to 63: c of a channel behind the window
+        for (int turn = 0; turn < steps; ++turn, t -= window) {
+            const int stage = turn % kRing;
+            Input &in = s.in[warp][stage];
+            if (kRing == 2 && turn + 1 < steps) {
+                next = look_up(p, t - window, kTokens, lane, seen);
+                if (lane == 0) ptx::bulk_wait_read();  // the other stage's gradients have left it
+                __syncwarp();
+                fill(q, m, s.in[warp][stage ^ 1], &r.bar[warp][stage ^ 1], t - window, block, next.own, lane);
+            }
+            // the state that the forward pass kept before the tile, early
+            const int tile = t - warp * kTokens, ch = block * 64 + (threadIdx.x & 63);
+            float kept = 0.f;
+            if (threadIdx.x >= 64 && threadIdx.x < 128 && tile < p.T && ch < p.D)
+                kept = p.chunk[(size_t)(tile / kChunk) * p.D + ch];
+            if (p.wide) {
+                if (!ptx::mbar_wait(&r.bar[warp][stage], turn / kRing & 1) && p.err) atomicOr(p.err, kErrTimeout);
+            } else {
+                __syncwarp();
+            }
+            const bool plain = tok.own == kAll && !(tok.first | tok.last);
+            float2 a[kTokens], u[kTokens], A, H, C;
+            if (plain) first_walk<true>(q, in, tok, c, lane, bias, scale, a, u, A, H, C);
+            else first_walk<false>(q, in, tok, c, lane, bias, scale, a, u, A, H, C);
+            *reinterpret_cast<float4 *>(&r.fwd[warp][2 * lane]) = make_float4(A.x, H.x, A.y, H.y);
+            *reinterpret_cast<float4 *>(&r.rev.map[warp][2 * lane]) = make_float4(A.x, C.x, A.y, C.y);
             __syncthreads();
             if (threadIdx.x < 64) {
-                const int k = threadIdx.x, ch = (int)(blockIdx.x / S) * 64 + k;
-                float2 v = s_fwd[0][k];
-                for (int w = 1; w < kWarps; ++w) v = v + s_fwd[w][k];
+                meet<true>(r.rev, r.x, S, rank, turn, threadIdx.x, carry, p.err);
+            } else if (threadIdx.x < 128) {
+                const int k = threadIdx.x - 64;
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 run = r.fwd[w][k];
+                    r.fwd[w][k].x = kept;
+                    kept = apply(run, kept);
+                }
+            }
+            __syncthreads();
+            const float2 dc = *reinterpret_cast<const float2 *>(&r.rev.h[warp][2 * lane]);
+            const float4 hh = *reinterpret_cast<const float4 *>(&r.fwd[warp][2 * lane]);
+            const float2 h = make_float2(hh.x, hh.z);
+            if (plain) second_walk<true>(q, m, in, tok, t, c, lane, bias, scale, a, u, h, dc, sums);
+            else second_walk<false>(q, m, in, tok, t, c, lane, bias, scale, a, u, h, dc, sums);
+            if (kRing == 1 && turn + 1 < steps) {
+                next = look_up(p, t - window, kTokens, lane, seen);
+                if (lane == 0) ptx::bulk_wait_read();
+                __syncwarp();
+                fill(q, m, in, &r.bar[warp][0], t - window, block, next.own, lane);
+            }
+            tok = next;
+        }
+        if (lane == 0) ptx::bulk_wait();
+        if (RAW) {  // sums over the block's warps, then over the cluster's blocks
+            __syncthreads();
+            *reinterpret_cast<float4 *>(&r.fwd[warp][2 * lane]) =
+                make_float4(sums.bias.x, sums.scale.x, sums.bias.y, sums.scale.y);
+            __syncthreads();
+            if (threadIdx.x < 64) {
+                const int k = threadIdx.x, ch = block * 64 + k, par = steps & 1;  // one turn more of the exchange
+                float2 v = r.fwd[0][k];
+                for (int w = 1; w < kWarps; ++w) v = v + r.fwd[w][k];
                 if (S > 1) {
-                    if (k == 0) exchange_expect(s_x, par, S);
-                    for (int r = 0; r < S; ++r) exchange_send(s_x, par, rank, r, k, v);
-                    exchange_wait(s_x, par, steps >> 1, p.err);
-                    v = s_x.map[par][0][k];
-                    for (int r = 1; r < S; ++r) v = v + s_x.map[par][r][k];
+                    if (k == 0) exchange_expect(r.x, par, S);
+                    for (int i = 0; i < S; ++i) exchange_send(r.x, par, rank, i, k, v);
+                    exchange_wait(r.x, par, steps >> 1, p.err);
+                    v = r.x.map[par][0][k];
+                    for (int i = 1; i < S; ++i) v = v + r.x.map[par][i][k];
                 }
                 if (rank == 0 && ch < p.D) {
                     if (q.dbias) q.dbias[ch] = v.x;
@@ -206,34 +297,38 @@ struct Backward {
             cluster_wait();
         }
     }
-
-    static __device__ __forceinline__ float2 first_state(const Args &p, const Tokens &tok, int k, int c) {
-        const int row = __shfl_sync(0xffffffffu, tok.row, k);
-        return p.init ? load_state(p.init + (size_t)row * p.D, c, p.D) : make_float2(0.f, 0.f);
-    }
-    static __device__ __forceinline__ void add_final(const GradArgs &q, const Tokens &tok, int k, int c, float2 &d) {
-        const int row = __shfl_sync(0xffffffffu, tok.row, k);
-        if (!q.dfin) return;
-        const float2 f = load_state(q.dfin + (size_t)row * q.f.D, c, q.f.D);
-        d.x += f.x;
-        d.y += f.y;
-    }
 };
 
 template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
-__global__ void __launch_bounds__(kWarps * 32, 2) scan_grad_kernel(const __grid_constant__ GradArgs q) {
-    typename Backward<TA, TG, RAW, BETA>::Sums sums = {};
-    Backward<TA, TG, RAW, BETA>::template run<MODE>(q, sums);
+__global__ void __launch_bounds__(kWarps * 32, 2) scan_grad_kernel(const __grid_constant__ GradArgs q,
+                                                                  const __grid_constant__ GradMaps m) {
+    using G = Backward<TA, TG, RAW, BETA, MODE>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    G::run(q, m, *reinterpret_cast<typename G::Shared *>(smem));
 }
 
 template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
-cudaError_t launch_grad_one(const GradArgs &q, cudaStream_t stream) {
+cudaError_t launch_grad_one(const GradArgs &args, cudaStream_t stream) {
+    using G = Backward<TA, TG, RAW, BETA, MODE>;
     auto kernel = scan_grad_kernel<TA, TG, RAW, BETA, MODE>;
-    const int cb = (q.f.D + 63) / 64, tile = Backward<TA, TG, RAW, BETA>::kTile;
+    GradArgs q = args;
+    const Args &p = q.f;
+    const int cb = (p.D + 63) / 64;
     int S = 1;
-    const cudaError_t e = cluster_blocks((const void *)kernel, 0, cb, (q.f.T + tile - 1) / tile, &S);
+    const cudaError_t e =
+        cluster_blocks((const void *)kernel, sizeof(typename G::Shared), cb, (p.T + G::kTile - 1) / G::kTile, &S);
     if (e != cudaSuccess) return e;
-    return launch_clusters(cb, S, 0, stream, kernel, q);
+    GradMaps m = {};
+    constexpr int ta = type_of<TA>(), tg = type_of<TG>(), n = G::kTokens;
+    if (p.wide && !(make_token_map(&m.x, p.x, ta, p.xs, p.D, p.T, n) &&
+                    make_token_map(&m.d, q.d_o, ta, q.dos, p.D, p.T, n) &&
+                    make_token_map(&m.z, p.decay, tg, p.gs, p.D, p.T, n) &&
+                    make_token_map(&m.dx, q.dx, ta, q.dxs, p.D, p.T, n) &&
+                    make_token_map(&m.dz, q.dg, tg, q.dgs, p.D, p.T, n) &&
+                    (!BETA || (make_token_map(&m.y, p.beta, tg, p.bs, p.D, p.T, n) &&
+                               make_token_map(&m.dy, q.db, tg, q.dbs, p.D, p.T, n)))))
+        q.f.wide = 0;
+    return launch_clusters(cb, S, sizeof(typename G::Shared), stream, kernel, q, m);
 }
 
 template <typename TA, typename TG, bool RAW, bool BETA>

@@ -17,11 +17,6 @@
 #pragma once
 
 #include "scan_cluster.cuh"
-#ifndef SCAN_TOK
-#define SCAN_TOK 16
-#define SCAN_TOK32 8
-#define SCAN_MINB 2
-#endif
 
 namespace gdn {
 namespace scan {
@@ -50,7 +45,7 @@ struct Maps {
 
 template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
 struct Forward {
-    static constexpr int kTokens = sizeof(TA) == 2 ? SCAN_TOK : SCAN_TOK32;
+    static constexpr int kTokens = sizeof(TA) == 2 ? 16 : 8;
     static constexpr int kTile = kWarps * kTokens;
 
     struct Input {
@@ -203,7 +198,7 @@ struct Forward {
 };
 
 template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
-__global__ void __launch_bounds__(kWarps * 32, SCAN_MINB) scan_kernel(const __grid_constant__ Args p,
+__global__ void __launch_bounds__(kWarps * 32, 2) scan_kernel(const __grid_constant__ Args p,
                                                              const __grid_constant__ Maps m) {
     using F = Forward<TA, TG, RAW, BETA, MODE>;
     extern __shared__ __align__(128) unsigned char smem[];
