@@ -21,19 +21,37 @@ NormResult = namedtuple("NormResult", "out residual scales rstd")
 NormGradients = namedtuple("NormGradients", "dx dweight")
 
 
-def _handle(stream):
+# The current stream's handle without building a stream object (3 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _handle(stream, t):
     if stream is None:
+        if _raw_stream is not None and t.is_cuda:
+            return _raw_stream(t.get_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_here = contextlib.nullcontext()
 
 
 def _on(stream):
     """Memory made inside belongs to the stream that the kernels run on."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _here
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
+
+
+def _lib():
+    return N._lib or N.load()
+
+
+def _call(status):
+    if status:
+        N.check(status)
 
 
 def _dtype(t, what):
@@ -47,36 +65,38 @@ def _ptr(t, dtype, what, shape=None):
     """Address of a contiguous device tensor of the given dtype, or None."""
     if t is None:
         return None
+    if t.is_cuda and t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError("libgdn takes device tensors; %s is on %s" % (what, t.device))
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s" % (what, dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % what)
-    if shape is not None and t.shape != shape:
-        raise ValueError("%s must be %s, got %s" % (what, tuple(shape), tuple(t.shape)))
-    return t.data_ptr()
+    raise ValueError("%s must be %s, got %s" % (what, tuple(shape), tuple(t.shape)))
 
 
-def _rows(t, shape, what):
+def _rows(t, dtype, shape, what):
     """(address, elements between rows) of a device tensor whose last dimension
     is contiguous and whose leading ones lie in it as one."""
     if t is None:
         return None, 0
     if not t.is_cuda:
         raise ValueError("libgdn takes device tensors; %s is on %s" % (what, t.device))
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s" % (what, dtype))
     if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (what, tuple(shape), tuple(t.shape)))
     if t.is_contiguous():
         return t.data_ptr(), shape[-1]
     if t.stride(-1) != 1 and shape[-1] != 1:
         raise ValueError("%s must have contiguous channels" % what)
-    step = t.stride(-2)
-    if t.dim() == 3 and shape[0] > 1:
-        if shape[1] == 1:
-            step = t.stride(0)
-        elif t.stride(0) != shape[1] * step:
-            raise ValueError("%s must have one stride over all tokens" % what)
+    step = t.stride(-2) if t.dim() > 1 else shape[-1]
+    for d in range(t.dim() - 3, -1, -1):  # the leading dimensions as one
+        if shape[d + 1] == 1:
+            step = t.stride(d)
+        elif shape[d] > 1 and t.stride(d) != shape[d + 1] * t.stride(d + 1):
+            raise ValueError("%s must have one stride over all its rows" % what)
     return t.data_ptr(), step
 
 
@@ -98,30 +118,29 @@ def _scan_args(x, decay, beta, gate_bias, gate_scale, beta_sigmoid, input_scale,
             raise ValueError("cu_seqlens goes with packed tokens, x [tokens, channels]")
     else:
         raise ValueError("x must be [tokens, channels] or [batch, tokens, channels]")
-    if input_scale not in N.INPUT_SCALES:
+    scale = N.INPUT_SCALES.get(input_scale)
+    if scale is None:
         raise ValueError("input_scale must be one of %s" % ", ".join(N.INPUT_SCALES))
-    if beta is not None and beta.dtype != decay.dtype:
-        raise TypeError("beta must have the dtype of decay")
-    if out is not None and out.dtype != x.dtype:
-        raise TypeError("out must have the dtype of x")
-    xp, xs = _rows(x, shape, "x")
-    gp, gs = _rows(decay, shape, "decay")
-    bp, bs = _rows(beta, shape, "beta")
-    op, os = _rows(out, shape, "out")
+    act_dtype, gate_dtype = x.dtype, decay.dtype
+    xp, xs = _rows(x, act_dtype, shape, "x")
+    gp, gs = _rows(decay, gate_dtype, shape, "decay")
+    bp, bs = _rows(beta, gate_dtype, shape, "beta")
+    op, os = _rows(out, act_dtype, shape, "out")
     state = initial_state if initial_state is not None else final_state
-    rows = 0
+    rows, state_shape = 0, None
     if state is not None:
-        if state.dim() != 2 or state.shape[1] != D:
+        state_shape = state.shape
+        if len(state_shape) != 2 or state_shape[1] != D:
             raise ValueError("states must be [rows, %d]" % D)
-        rows = state.shape[0]
+        rows = state_shape[0]
     f32, i32 = torch.float32, torch.int32
     return N.GdnScanArgs(
-        B, T, seq_len, D, rows, act, gate, N.INPUT_SCALES[input_scale],
+        B, T, seq_len, D, rows, act, gate, scale,
         N.FLAG_BETA_SIGMOID if beta_sigmoid else 0, xs, gs, bs, os, xp, gp, bp, op,
         _ptr(gate_bias, f32, "gate_bias", (D,)), _ptr(gate_scale, f32, "gate_scale", (D,)),
         _ptr(cu_seqlens, i32, "cu_seqlens"), _ptr(seq_lens, i32, "seq_lens", (B,)),
         _ptr(slot_ids, i32, "slot_ids", (B,)), _ptr(initial_state, f32, "initial_state"),
-        _ptr(final_state, f32, "final_state", None if state is None else state.shape),
+        _ptr(final_state, f32, "final_state", state_shape),
         _ptr(chunk_states, f32, "chunk_states", (-(-T // N.SCAN_CHUNK), D)), _ptr(error_word, i32, "error_word"))
 
 
@@ -150,7 +169,7 @@ def gdn_scan(x, decay, *, beta=None, gate_bias=None, gate_scale=None, beta_sigmo
                 chunks = torch.empty(-(-x.numel() // max(D, 1) // N.SCAN_CHUNK), D, device=x.device)
     args = _scan_args(x, decay, beta, gate_bias, gate_scale, beta_sigmoid, input_scale, cu_seqlens, seq_lens,
                       slot_ids, initial_state, final_state, out, chunks, error_word)
-    N.check(N.load().gdn_scan(args, _handle(stream)))
+    _call(_lib().gdn_scan(args, _handle(stream, x)))
     return (out, chunks) if want_chunk_states else out
 
 
@@ -165,7 +184,7 @@ def gdn_scan_step(x, decay, *, beta=None, gate_bias=None, gate_scale=None, beta_
             out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     args = _scan_args(x, decay, beta, gate_bias, gate_scale, beta_sigmoid, input_scale, cu_seqlens, seq_lens,
                       slot_ids, initial_state, final_state, out, None, error_word)
-    N.check(N.load().gdn_scan_step(args, _handle(stream)))
+    _call(_lib().gdn_scan_step(args, _handle(stream, x)))
     return out
 
 
@@ -197,23 +216,21 @@ def gdn_scan_backward(d_out, x, decay, chunk_states, *, beta=None, gate_bias=Non
         if d_initial_state is None and initial_state is not None:
             d_initial_state = torch.zeros_like(initial_state)
     f32, D = torch.float32, x.shape[-1]
-    for t, of, what in ((d_out, x, "d_out"), (dx, x, "dx"), (d_decay, decay, "d_decay"), (d_beta, beta, "d_beta")):
-        if t is not None and of is not None and t.dtype != of.dtype:
-            raise TypeError("%s must be %s" % (what, of.dtype))
     forward = _scan_args(x, decay, beta, gate_bias, gate_scale, beta_sigmoid, input_scale, cu_seqlens, seq_lens,
                          slot_ids, like, None, None, chunk_states, error_word)
     if initial_state is None:
         forward.initial_state = None
-    dop, dos = _rows(d_out, x.shape, "d_out")
-    dxp, dxs = _rows(dx, x.shape, "dx")
-    dgp, dgs = _rows(d_decay, x.shape, "d_decay")
-    dbp, dbs = _rows(d_beta, x.shape, "d_beta")
+    shape = x.shape
+    dop, dos = _rows(d_out, x.dtype, shape, "d_out")
+    dxp, dxs = _rows(dx, x.dtype, shape, "dx")
+    dgp, dgs = _rows(d_decay, decay.dtype, shape, "d_decay")
+    dbp, dbs = _rows(d_beta, decay.dtype, shape, "d_beta")
     rows = None if like is None else like.shape
     args = N.GdnScanGradArgs(
         forward, dos, dxs, dgs, dbs, dop, _ptr(d_final_state, f32, "d_final_state", rows), dxp, dgp, dbp,
         _ptr(d_gate_bias, f32, "d_gate_bias", (D,)), _ptr(d_gate_scale, f32, "d_gate_scale", (D,)),
         _ptr(d_initial_state, f32, "d_initial_state", rows))
-    N.check(N.load().gdn_scan_backward(args, _handle(stream)))
+    _call(_lib().gdn_scan_backward(args, _handle(stream, x)))
     return ScanGradients(dx, d_decay, d_beta, d_gate_bias, d_gate_scale, d_initial_state)
 
 
@@ -225,34 +242,34 @@ def gdn_rmsnorm(x, weight, *, residual=None, eps=1e-6, out_dtype=None, group=0, 
     Returns NormResult(out, residual, scales, rstd): residual is r in residual's dtype
     (float32 or x's; ``residual_out`` may be ``residual``), rstd is for
     gdn_rmsnorm_backward; None where there is none or it was not asked for."""
-    shape = x.shape
-    D = shape[-1] if x.dim() else 0
+    shape, dtype, device = x.shape, x.dtype, x.device
+    D = shape[-1] if shape else 0
     n = x.numel() // D if D else 0
     e4m3 = out_dtype is torch.float8_e4m3fn
     if out_dtype is None:
-        out_dtype = x.dtype
-    rstd = None
+        out_dtype = dtype
+    f32, res = torch.float32, None if residual is None else residual.dtype
+    rstd, sshape = None, None
+    if e4m3:
+        sshape = shape[:-1] if group == 0 else shape[:-1] + (-(-D // 128),)
     with _on(stream):
         if out is None:
-            out = torch.empty(shape, dtype=out_dtype, device=x.device)
+            out = torch.empty(shape, dtype=out_dtype, device=device)
         if residual is not None and residual_out is None:
-            residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
+            residual_out = torch.empty(shape, dtype=res, device=device)
         if e4m3 and scales is None:
-            cols = () if group == 0 else (-(-D // 128),)
-            scales = torch.empty(shape[:-1] + cols, device=x.device)
+            scales = torch.empty(sshape, dtype=f32, device=device)
         if want_rstd:
-            rstd = torch.empty(shape[:-1], device=x.device)
-    xp, xs = _rows(x, shape, "x")
-    res = None if residual is None else residual.dtype
+            rstd = torch.empty(shape[:-1], dtype=f32, device=device)
+    xp, xs = _rows(x, dtype, shape, "x")
     code = _dtype(x, "x")
     args = N.GdnRmsnormArgs(
         n, D, code, code if residual is None else _dtype(residual, "residual"), _dtype(weight, "weight"),
         N.DTYPE_E4M3 if e4m3 else _DT.get(out_dtype, -1), group, eps, xs, xp,
         _ptr(residual, res, "residual", shape), _ptr(weight, weight.dtype, "weight", (D,)),
         _ptr(out, out_dtype, "out", shape), _ptr(residual_out, res, "residual_out", shape),
-        _ptr(scales, torch.float32, "scales", shape[:-1] + (() if group == 0 else (-(-D // 128),))),
-        _ptr(rstd, torch.float32, "rstd"))
-    N.check(N.load().gdn_rmsnorm(args, _handle(stream)))
+        _ptr(scales, f32, "scales", sshape), None if rstd is None else rstd.data_ptr())
+    _call(_lib().gdn_rmsnorm(args, _handle(stream, x)))
     return NormResult(out, residual_out if residual is not None else None, scales, rstd)
 
 
@@ -263,34 +280,37 @@ def gdn_rmsnorm_backward(d_out, r, weight, rstd, *, d_residual=None, dx=None, d_
     where there was none), rstd what it returned.  Returns NormGradients(dx, dweight): dx, in r's dtype, is the
     gradient of x and of residual alike (``dx`` may be ``d_residual``); dweight is
     float32."""
-    shape = r.shape
-    D = shape[-1] if r.dim() else 0
+    shape, dtype, device = r.shape, r.dtype, r.device
+    D = shape[-1] if shape else 0
     n = r.numel() // D if D else 0
+    f32 = torch.float32
     with _on(stream):
         if dx is None:
-            dx = torch.empty(shape, dtype=r.dtype, device=r.device)
+            dx = torch.empty(shape, dtype=dtype, device=device)
         if d_weight is None:
-            d_weight = torch.empty(D, device=r.device)
-    dp, ds = _rows(d_out, shape, "d_out")
+            d_weight = torch.empty(D, dtype=f32, device=device)
+    dp, ds = _rows(d_out, d_out.dtype, shape, "d_out")
     args = N.GdnRmsnormGradArgs(
-        n, D, _dtype(d_out, "d_out"), _dtype(r, "r"), _dtype(weight, "weight"), ds, dp, _ptr(r, r.dtype, "r"),
-        _ptr(weight, weight.dtype, "weight", (D,)), _ptr(rstd, torch.float32, "rstd", shape[:-1]),
-        _ptr(d_residual, r.dtype, "d_residual", shape), _ptr(dx, r.dtype, "dx", shape),
-        _ptr(d_weight, torch.float32, "d_weight", (D,)))
-    _with_workspace("gdn_rmsnorm_backward", args, workspace, r.device, stream)
+        n, D, _dtype(d_out, "d_out"), _dtype(r, "r"), _dtype(weight, "weight"), ds, dp, _ptr(r, dtype, "r"),
+        _ptr(weight, weight.dtype, "weight", (D,)), _ptr(rstd, f32, "rstd", shape[:-1]),
+        _ptr(d_residual, dtype, "d_residual", shape), _ptr(dx, dtype, "dx", shape),
+        _ptr(d_weight, f32, "d_weight", (D,)))
+    lib = _lib()
+    _with_workspace(lib.gdn_rmsnorm_backward, lib.gdn_rmsnorm_backward_workspace_size, args, workspace, r, stream)
     return NormGradients(dx, d_weight)
 
 
-def _with_workspace(name, args, workspace, device, stream):
-    lib = N.load()
+_TOO_LARGE = ctypes.c_size_t(-1).value
+
+
+def _with_workspace(call, size, args, workspace, like, stream):
     if workspace is None:
-        need = getattr(lib, name + "_workspace_size")(args)
-        if need == ctypes.c_size_t(-1).value:
+        need = size(args)
+        if need == _TOO_LARGE:
             need = 0  # the call says what is wrong
         with _on(stream):
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    N.check(getattr(lib, name)(args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                               _handle(stream)))
+            workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    _call(call(args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _handle(stream, like)))
 
 
 def gdn_grad_clip(grads, max_norm, *, eps=1e-6, out=None, norm=None, error_word=None, workspace=None, stream=None):
@@ -300,24 +320,25 @@ def gdn_grad_clip(grads, max_norm, *, eps=1e-6, out=None, norm=None, error_word=
     finite scales nothing and sets DEVERR_NONFINITE in ``error_word``."""
     grads = list(grads)
     count = len(grads)
-    device = grads[0].device if count else torch.device("cuda", torch.cuda.current_device())
+    f32, outs = torch.float32, None
+    types = [t.dtype for t in grads]
     with _on(stream):
         if norm is None:
-            norm = torch.empty(1, device=device)
-    table = (ctypes.c_void_p * count)()
-    sizes = (ctypes.c_int64 * count)()
-    types = (ctypes.c_int32 * count)()
-    outs = None
-    for i, t in enumerate(grads):
-        table[i], sizes[i], types[i] = _ptr(t, t.dtype, "a gradient"), t.numel(), _dtype(t, "a gradient")
+            norm = torch.empty(1, dtype=f32, device=grads[0].device if count else "cuda")
+    table = [_ptr(t, d, "a gradient") for t, d in zip(grads, types)]
+    try:
+        codes = [_DT[d] for d in types]
+    except KeyError as e:
+        raise TypeError("a gradient: unsupported dtype %s" % e) from None
+    pointers = ctypes.c_void_p * count
     if out is not None:
         out = list(out)
         if len(out) != count:
             raise ValueError("out must have a tensor for each of the %d gradients" % count)
-        outs = (ctypes.c_void_p * count)()
-        for i, t in enumerate(out):
-            outs[i] = _ptr(t, grads[i].dtype, "an output", grads[i].shape)
-    args = N.GdnGradClipArgs(count, max_norm, eps, table, outs, sizes, types, _ptr(norm, torch.float32, "norm", (1,)),
-                             _ptr(error_word, torch.int32, "error_word"))
-    _with_workspace("gdn_grad_clip", args, workspace, device, stream)
+        outs = pointers(*[_ptr(o, d, "an output", t.shape) for o, d, t in zip(out, types, grads)])
+    args = N.GdnGradClipArgs(count, max_norm, eps, pointers(*table), outs,
+                             (ctypes.c_int64 * count)(*[t.numel() for t in grads]), (ctypes.c_int32 * count)(*codes),
+                             _ptr(norm, f32, "norm", (1,)), _ptr(error_word, torch.int32, "error_word"))
+    lib = _lib()
+    _with_workspace(lib.gdn_grad_clip, lib.gdn_grad_clip_workspace_size, args, workspace, norm, stream)
     return norm
