@@ -13,5 +13,13 @@ from .api import (gdn_chunked_prefill, gdn_chunked_prefill_noalloc,  # noqa: F40
                   gdn_chunked_prefill_workspace_size, gdn_chunked_prefill_workspace_size_min, gdn_gate,
                   gdn_recurrent_step,
                   gdn_status_string, make_problem)
-from .layer import (gdn_grad_clip, gdn_rmsnorm, gdn_rmsnorm_backward, gdn_scan,  # noqa: F401
-                    gdn_scan_backward, gdn_scan_step)
+from .layer import OPERATORS as _LAYER, NormGradients, NormResult, ScanGradients  # noqa: F401
+
+
+def __getattr__(name):
+    """The recurrent-layer operators, loaded at their first use."""
+    if name in _LAYER:
+        from . import layer
+        globals()[name] = getattr(layer, name)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
