@@ -54,7 +54,8 @@ struct Backward {
     struct Rest {
         Exchange x;
         Meeting rev;               // (A, C) of each warp's run, and c behind it
-        float2 fwd[kWarps][64];    // (A, H) of each warp's run, then the state before it; at the end its sums
+        float2 fwd[kWarps][64];    // (A, H) of each warp's run; at the end its sums
+        float h[kWarps][64];       // the state before it
         uint64_t bar[kWarps][2];
     };
     // Two stages where two blocks an SM have room for them, so that a window's loads
@@ -218,7 +219,7 @@ struct Backward {
         if (S > 1) exchange_init(r.x);
 
         Sums sums = {};
-        float carry = 0.f;  // threads 0 to 63: c of a channel behind the window
+        float carry = 0.f;  // c of this thread's channel (see Meet) behind the window
         for (int turn = 0; turn < steps; ++turn, t -= window) {
             const int stage = turn % kRing;
             Input &in = s.in[warp][stage];
@@ -231,7 +232,7 @@ struct Backward {
             // the state that the forward pass kept before the tile, early
             const int tile = t - warp * kTokens, ch = block * 64 + (threadIdx.x & 63);
             float kept = 0.f;
-            if (threadIdx.x >= 64 && threadIdx.x < 128 && tile < p.T && ch < p.D)
+            if (tile < p.T && ch < p.D)
                 kept = p.chunk[(size_t)(tile / kChunk) * p.D + ch];
             if (p.wide) {
                 if (!ptx::mbar_wait(&r.bar[warp][stage], turn / kRing & 1) && p.err) atomicOr(p.err, kErrTimeout);
@@ -245,20 +246,20 @@ struct Backward {
             *reinterpret_cast<float4 *>(&r.fwd[warp][2 * lane]) = make_float4(A.x, H.x, A.y, H.y);
             *reinterpret_cast<float4 *>(&r.rev.map[warp][2 * lane]) = make_float4(A.x, C.x, A.y, C.y);
             __syncthreads();
-            if (threadIdx.x < 64) {
-                meet<true>(r.rev, r.x, S, rank, turn, threadIdx.x, carry, p.err);
-            } else if (threadIdx.x < 128) {
-                const int k = threadIdx.x - 64;
+            Meet<true> meet;
+            const float2 whole = meet.send(r.rev, r.x, S, rank, turn);
+            {  // while the maps are on their way: the states before the warps' runs
+                float h = kept;
+#pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    const float2 run = r.fwd[w][k];
-                    r.fwd[w][k].x = kept;
-                    kept = apply(run, kept);
+                    if (w / kMine == meet.part) r.h[w][meet.c] = h;
+                    h = apply(r.fwd[w][meet.c], h);
                 }
             }
+            meet.receive(r.rev, r.x, S, rank, turn, whole, carry, p.err);
             __syncthreads();
             const float2 dc = *reinterpret_cast<const float2 *>(&r.rev.h[warp][2 * lane]);
-            const float4 hh = *reinterpret_cast<const float4 *>(&r.fwd[warp][2 * lane]);
-            const float2 h = make_float2(hh.x, hh.z);
+            const float2 h = *reinterpret_cast<const float2 *>(&r.h[warp][2 * lane]);
             if (plain) second_walk<true>(q, m, in, tok, t, c, lane, bias, scale, a, u, h, dc, sums);
             else second_walk<false>(q, m, in, tok, t, c, lane, bias, scale, a, u, h, dc, sums);
             if (kRing == 1 && turn + 1 < steps) {

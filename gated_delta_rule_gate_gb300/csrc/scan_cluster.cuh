@@ -4,6 +4,8 @@
 
 #include <cuda.h>  // CUtensorMap
 
+#include <stddef.h>
+
 #include <type_traits>
 
 #include "common.cuh"
@@ -97,9 +99,10 @@ __device__ __forceinline__ void exchange_expect(Exchange &x, int par, int S) {
 }
 // Sends channel c's v to block `to`, in block `from`'s place.
 __device__ __forceinline__ void exchange_send(Exchange &x, int par, int from, int to, int c, float2 v) {
-    uint32_t at, bar;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(&x.map[par][from][c])), "r"(to));
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(ptx::smem_u32(&x.bar[par])), "r"(to));
+    uint32_t base;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(base) : "r"(ptx::smem_u32(&x)), "r"(to));
+    const uint32_t at = base + (uint32_t)offsetof(Exchange, map) + ((par * kMaxCluster + from) * 64 + c) * 8u;
+    const uint32_t bar = base + (uint32_t)offsetof(Exchange, bar) + par * 8u;
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(at),
                  "f"(v.x), "f"(v.y), "r"(bar)
                  : "memory");
@@ -111,53 +114,87 @@ __device__ __forceinline__ void exchange_wait(Exchange &x, int par, int n, int32
     if (!ptx::mbar_wait(&x.bar[par], n & 1, 1u << 20) && err) atomicOr(err, kErrTimeout);
 }
 
-// The maps of a block's warps, of 64 channels each, and the states before them.
+// The maps of a block's warps, of 64 channels each, and the states before their runs.
 struct Meeting {
     float2 map[kWarps][64];
     float h[kWarps][64];
 };
-// One of 64 threads, for channel c, between two barriers of the block: the states
-// before the warps' runs, from `carry`, the state before the window, which moves on
-// by a window.  Warps and blocks follow one another upwards, or (REVERSE) downwards.
-// One thread a channel instead of every warp for itself: the maps are read once (the
-// warps' own folding took 1,700 cycles a window of 8 blocks, of 6,800).
+// Between two barriers of the block its 256 threads turn the warps' maps into the
+// states before the warps' runs: a thread takes one channel, for two of the warps.
+// Every thread folds all maps of its channel itself: with 64 threads doing it for the
+// block, the others waited 3,100 cycles a window of 8 blocks for 300 dependent
+// instructions.  Warps and blocks follow one another upwards, or (REVERSE) downwards.
+constexpr int kParts = kWarps * 32 / 64, kMine = kWarps / kParts;
 template <bool REVERSE>
-__device__ __forceinline__ void meet(Meeting &m, Exchange &x, int S, int rank, int turn, int c, float &carry,
-                                     int32_t *err) {
-    const int par = turn & 1;
-    float2 run = make_float2(1.f, 0.f);
+struct Meet {
+    int c, part;
+    float2 before[kMine];  // the run before each of this thread's warps
+
+    // First: the block's map, to every block of the cluster.
+    __device__ __forceinline__ float2 send(const Meeting &m, Exchange &x, int S, int rank, int turn) {
+        c = threadIdx.x & 63, part = threadIdx.x >> 6;
+        float2 run = make_float2(1.f, 0.f);
+        uint32_t any = 0u;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        float2 *at = &m.map[REVERSE ? kWarps - 1 - i : i][c];
-        const float2 k = *at;
-        *at = run;
-        run = fold(run, k);
-    }
-    float h = carry;
-    if (S > 1) {
-        if (c == 0) exchange_expect(x, par, S);
-        for (int r = 0; r < S; ++r) exchange_send(x, par, rank, r, c, run);
-        exchange_wait(x, par, turn >> 1, err);
-        for (int i = 0; i < S; i += 4) {  // four maps on their way at a time
-            float2 k[4];
+        for (int i = 0; i < kWarps; ++i) {
+            const float2 k = m.map[REVERSE ? kWarps - 1 - i : i][c];
+            if (i / kMine == part) before[i % kMine] = run;
+            any |= __float_as_uint(k.x);
+            run = make_float2(run.x * k.x, fmaf(k.x, run.y, k.y));
+        }
+        if (any >> 31) {  // a request begins in one of them
+            run = make_float2(1.f, 0.f);
+            for (int i = 0; i < kWarps; ++i) {
+                const float2 k = m.map[REVERSE ? kWarps - 1 - i : i][c];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = i + j < S ? i + j : S - 1;
-                k[j] = x.map[par][REVERSE ? S - 1 - r : r][c];
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (i + j >= S) break;
-                if ((REVERSE ? S - 1 - (i + j) : i + j) == rank) h = carry;
-                carry = apply(k[j], carry);
+                for (int j = 0; j < kMine; ++j)
+                    if (i == part * kMine + j) before[j] = run;
+                run = fold(run, k);
             }
         }
-    } else {
-        carry = apply(run, carry);
+        if (S > 1) {
+            if (threadIdx.x == 0) exchange_expect(x, turn & 1, S);
+            for (int r = part; r < S; r += kParts) exchange_send(x, turn & 1, rank, r, c, run);
+        }
+        return run;
     }
+    // Then: the states before the runs, from `carry`, the one before the window,
+    // which moves on by a window.
+    __device__ __forceinline__ void receive(Meeting &m, Exchange &x, int S, int rank, int turn, float2 run,
+                                            float &carry, int32_t *err) {
+        float h = carry;
+        if (S > 1) {
+            const int par = turn & 1;
+            exchange_wait(x, par, turn >> 1, err);
+            const float2 *map = &x.map[par][REVERSE ? S - 1 : 0][c];
+            constexpr int kNext = REVERSE ? -64 : 64;
+            const int me = REVERSE ? S - 1 - rank : rank;
+            const float c0 = carry;
+            uint32_t any = 0u;
+#pragma unroll 4
+            for (int i = 0; i < S; ++i) {
+                const float2 k = map[i * kNext];
+                if (i == me) h = carry;
+                any |= __float_as_uint(k.x);
+                carry = fmaf(k.x, carry, k.y);
+            }
+            if (any >> 31) {
+                carry = c0;
+                for (int i = 0; i < S; ++i) {
+                    if (i == me) h = carry;
+                    carry = apply(map[i * kNext], carry);
+                }
+            }
+        } else {
+            carry = apply(run, carry);
+        }
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m.h[w][c] = apply(m.map[w][c], h);
-}
+        for (int j = 0; j < kMine; ++j) {
+            const int w = part * kMine + j;
+            m.h[REVERSE ? kWarps - 1 - w : w][c] = apply(before[j], h);
+        }
+    }
+};
 
 // The blocks along time of one channel block: the most, up to a cluster's limit,
 // with which all clusters are resident at once, and no more than there are tiles.

@@ -8,7 +8,7 @@
 // walks the whole token axis of its channels in windows of S tiles and carries
 // the state from window to window in registers.  Per window: every warp folds
 // its run to (A, H); the block's warps exchange theirs in shared memory, the
-// blocks theirs in distributed shared memory (meet()); every warp
+// blocks theirs in distributed shared memory (Meet); every warp
 // then has the state before its run, in the same order of operations on every
 // run, and walks its tokens, which have stayed in registers, a second time to
 // write o.  The loads of the next window are in flight meanwhile, so x, decay and
@@ -161,7 +161,7 @@ struct Forward {
         request_duties(p, S * kWarps, rank * kWarps + warp, lane, c, blockIdx.x < S);
         if (S > 1) exchange_init(s.x);
 
-        float carry = 0.f;  // threads 0 to 63: the state of a channel before the window
+        float carry = 0.f;  // the state of this thread's channel (see Meet) before the window
         for (int step = 0; step < steps; ++step, t += window) {
             const int par = step & 1;
             float2 a[kTokens], u[kTokens];
@@ -175,13 +175,14 @@ struct Forward {
             *reinterpret_cast<float4 *>(&s.meet.map[warp][2 * lane]) =
                 plain ? first_walk<true>(p, in, now, c, lane, bias, scale, a, u)
                       : first_walk<false>(p, in, now, c, lane, bias, scale, a, u);
-            __syncwarp();
-            if (step + 1 < steps) {
+            __syncthreads();
+            Meet<false> meet;
+            const float2 tile = meet.send(s.meet, s.x, S, rank, step);
+            if (step + 1 < steps) {  // while the maps are on their way
                 tok = look_up(p, t + window, kTokens, lane, seen);
                 fill(p, m, in, bar, t + window, block, tok.own, lane);
             }
-            __syncthreads();
-            if (threadIdx.x < 64) meet<false>(s.meet, s.x, S, rank, step, threadIdx.x, carry, p.err);
+            meet.receive(s.meet, s.x, S, rank, step, tile, carry, p.err);
             __syncthreads();
             const float2 h = *reinterpret_cast<const float2 *>(&s.meet.h[warp][2 * lane]);
             if (p.chunk && t % kChunk == 0 && t < p.T)
