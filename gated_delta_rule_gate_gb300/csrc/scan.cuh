@@ -226,17 +226,20 @@ __device__ __forceinline__ float root(float v) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
+__device__ __forceinline__ float2 operator-(float2 a) { return a * splat(-1.f); }
+
 // sigmoid(z) = 1 / (1 + e^-z).
 __device__ __forceinline__ float2 sigmoid(float2 z) {
-    const float2 d = make_float2(ex2(-kLog2e * z.x), ex2(-kLog2e * z.y)) + splat(1.f);
+    const float2 t = z * splat(-kLog2e);
+    const float2 d = make_float2(ex2(t.x), ex2(t.y)) + splat(1.f);
     return make_float2(reciprocal(d.x), reciprocal(d.y));
 }
 
 // softplus(z) = max(z, 0) + log1p(u), u = e^-|z| in (0, 1].  log1p(u) / u is a
 // polynomial of degree 8 fitted on [0, 1] (weighted least squares at Chebyshev
 // nodes, toward the least largest relative error): 1.7e-7 with fp32 rounding.
-__device__ __forceinline__ float2 softplus(float2 z, float2 &u) {
-    u = make_float2(ex2(-kLog2e * fabsf(z.x)), ex2(-kLog2e * fabsf(z.y)));
+__device__ __forceinline__ float2 softplus(float2 z) {
+    const float2 u = make_float2(ex2(-kLog2e * fabsf(z.x)), ex2(-kLog2e * fabsf(z.y)));
     float2 r = splat(0.00523266801610589f);
     r = fma2(r, u, splat(-0.029505133628845215f));
     r = fma2(r, u, splat(0.07822578400373459f));
@@ -249,84 +252,49 @@ __device__ __forceinline__ float2 softplus(float2 z, float2 &u) {
     return fma2(r, u, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
 }
 
-// e^g - 1: for |g| <= 1/2 a polynomial times g (degree 6, fitted as above, 1.2e-7),
+// e^g - 1: for |g| <= 1/5 a polynomial times g (degree 4, fitted as above, 1.4e-7),
 // else 2^(g log2 e) - 1.  1 + it is then e^g without a bias where g is near 0.
 __device__ __forceinline__ float2 exp_minus_1(float2 g) {
-    float2 r = splat(0.00019841187167912722f);
-    r = fma2(r, g, splat(0.0013997324276715517f));
-    r = fma2(r, g, splat(0.008333634585142136f));
-    r = fma2(r, g, splat(0.041665319353342056f));
-    r = fma2(r, g, splat(0.16666662693023682f));
-    r = fma2(r, g, splat(0.5000000596046448f));
+    float2 r = splat(0.008333331905305386f);
+    r = fma2(r, g, splat(0.04173609986901283f));
+    r = fma2(r, g, splat(0.16666696965694427f));
+    r = fma2(r, g, splat(0.4999993145465851f));
     r = fma2(r, g, splat(1.f)) * g;
     const float2 t = g * splat(kLog2e);
     const float2 e = make_float2(ex2(t.x), ex2(t.y)) + splat(-1.f);
-    return make_float2(fabsf(g.x) <= 0.5f ? r.x : e.x, fabsf(g.y) <= 0.5f ? r.y : e.y);
+    return make_float2(fabsf(g.x) <= 0.2f ? r.x : e.x, fabsf(g.y) <= 0.2f ? r.y : e.y);
 }
 
-// What a token's gates come to: a = exp(g), the input's scale n, and m = a - 1.
 template <bool RAW>
 __device__ __forceinline__ float2 log_decay(float2 z, float2 bias, float2 scale) {
-    float2 u;
-    return RAW ? scale * softplus(z + bias, u) : z;
+    return RAW ? scale * softplus(z + bias) : z;
 }
 // n^2 = 1 - a^2 = -m (2 + m) with m = a - 1, and 0 where a > 1.
 __device__ __forceinline__ float2 unit_scale(float2 m) {
-    const float2 q = m * (splat(-2.f) + make_float2(-m.x, -m.y));
+    const float2 q = m * fma2(m, splat(-1.f), splat(-2.f));
     return make_float2(root(fmaxf(q.x, 0.f)), root(fmaxf(q.y, 0.f)));
 }
-// a and u = n i x of a token.
-template <bool RAW, bool BETA, int MODE>
-__device__ __forceinline__ void token_map(float2 x, float2 z, float2 y, float2 bias, float2 scale, bool sig, float2 &a,
-                                          float2 &u) {
-    const float2 m = exp_minus_1(log_decay<RAW>(z, bias, scale));
-    a = m + splat(1.f);
-    u = x;
-    if constexpr (BETA) u = u * (sig ? sigmoid(y) : y);
-    if constexpr (MODE == kLerp) u = u * make_float2(-m.x, -m.y);
-    if constexpr (MODE == kUnit) u = u * unit_scale(m);
-}
 
-// What the gradient needs of one token's gates: a, n, dn/dg, i, di/dbeta,
-// softplus, dg/ddecay.
-struct Terms {
-    float2 a, n, dn, i, di, soft, dgdz;
+// What a token's gates come to: a = exp(g), the input's scale n, its gate i, and in
+// the raw arm softplus(z).
+struct Gates {
+    float2 a, n, i, soft;
 };
 template <bool RAW, bool BETA, int MODE>
-__device__ __forceinline__ Terms gate_terms(float2 z, float2 y, float2 bias, float2 scale, bool sig) {
-    Terms t;
-    float2 g = z;
-    t.soft = splat(0.f);
-    t.dgdz = splat(1.f);
-    if constexpr (RAW) {
-        float2 u;
-        z = z + bias;
-        t.soft = softplus(z, u);
-        g = scale * t.soft;
-        // sigmoid(z) = 1 / (1 + u) for z >= 0, u / (1 + u) below
-        const float2 d = u + splat(1.f), r = make_float2(reciprocal(d.x), reciprocal(d.y)), l = u * r;
-        t.dgdz = scale * make_float2(z.x >= 0.f ? r.x : l.x, z.y >= 0.f ? r.y : l.y);
-    }
-    const float2 m = exp_minus_1(g);
+__device__ __forceinline__ Gates token_gates(float2 z, float2 y, float2 bias, float2 scale, bool sig) {
+    Gates t;
+    t.soft = RAW ? softplus(z + bias) : splat(0.f);
+    const float2 m = exp_minus_1(RAW ? scale * t.soft : z);
     t.a = m + splat(1.f);
-    t.n = splat(1.f);
-    t.dn = splat(0.f);
-    if constexpr (MODE == kLerp) {
-        t.n = make_float2(-m.x, -m.y);
-        t.dn = make_float2(-t.a.x, -t.a.y);
-    }
-    if constexpr (MODE == kUnit) {  // where n is 0 (a >= 1) its slope is taken as 0
-        t.n = unit_scale(m);
-        const float2 q = t.a * t.a;
-        t.dn = make_float2(t.n.x > 0.f ? -q.x * reciprocal(t.n.x) : 0.f, t.n.y > 0.f ? -q.y * reciprocal(t.n.y) : 0.f);
-    }
-    t.i = splat(1.f);
-    t.di = splat(0.f);
-    if constexpr (BETA) {
-        t.i = sig ? sigmoid(y) : y;
-        t.di = sig ? t.i * (splat(1.f) + make_float2(-t.i.x, -t.i.y)) : splat(1.f);
-    }
+    t.n = MODE == kLerp ? -m : (MODE == kUnit ? unit_scale(m) : splat(1.f));
+    t.i = BETA ? (sig ? sigmoid(y) : y) : splat(1.f);
     return t;
+}
+// n i x.
+template <bool BETA, int MODE>
+__device__ __forceinline__ float2 scaled(float2 x, float2 n, float2 i) {
+    if (BETA) x = x * i;
+    return MODE == kNone ? x : x * n;
 }
 
 }  // namespace scan

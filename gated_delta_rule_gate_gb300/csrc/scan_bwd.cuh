@@ -97,25 +97,33 @@ struct Backward {
         return q.dfin ? load_state(q.dfin + (size_t)row * q.f.D, c, q.f.D) : splat(0.f);
     }
 
-    // a, u of the warp's tokens and its maps, (A, H) and C.  PLAIN: all of them inside
-    // one request, neither its first nor its last token among them.
+    // What a warp keeps of its tokens' gates between the walks (the compiler drops what
+    // the arm at hand does not have).
+    struct Held {
+        float2 a[kTokens], n[kTokens], i[kTokens], soft[kTokens];
+    };
+
+    // The gates of the warp's tokens and its maps, (A, H) and C.  PLAIN: all of them
+    // inside one request, neither its first nor its last token among them.
     template <bool PLAIN>
     static __device__ __forceinline__ void first_walk(const GradArgs &q, const Input &in, const Tokens &tok, int c,
-                                                      int lane, float2 bias, float2 scale, float2 (&a)[kTokens],
-                                                      float2 (&u)[kTokens], float2 &A, float2 &H, float2 &C) {
+                                                      int lane, float2 bias, float2 scale, Held &held, float2 &A,
+                                                      float2 &H, float2 &C) {
         const Args &p = q.f;
         A = splat(1.f), H = splat(0.f), C = splat(0.f);
 #pragma unroll
         for (int k = 0; k < kTokens; ++k) {
             float2 y = splat(0.f);
             if constexpr (BETA) y = in.y[0].at(k, lane);
-            token_map<RAW, BETA, MODE>(in.x.at(k, lane), in.z.at(k, lane), y, bias, scale, p.sigmoid, a[k], u[k]);
+            const Gates g = token_gates<RAW, BETA, MODE>(in.z.at(k, lane), y, bias, scale, p.sigmoid);
+            held.a[k] = g.a, held.n[k] = g.n, held.i[k] = g.i, held.soft[k] = g.soft;
+            float2 u = scaled<BETA, MODE>(in.x.at(k, lane), g.n, g.i);
             if (!PLAIN) {
-                if (!(tok.own >> k & 1u)) a[k] = splat(1.f), u[k] = splat(0.f);
+                if (!(tok.own >> k & 1u)) held.a[k] = splat(1.f), u = splat(0.f);
                 if (tok.first >> k & 1u) H = first_state(p, tok, k, c);
             }
-            H = fma2(a[k], H, u[k]);
-            A = A * a[k];
+            H = fma2(held.a[k], H, u);
+            A = A * held.a[k];
         }
 #pragma unroll
         for (int k = kTokens - 1; k >= 0; --k) {
@@ -124,7 +132,7 @@ struct Backward {
                 if (!(tok.own >> k & 1u)) d = splat(0.f);
                 if (tok.last >> k & 1u) d = d + last_gradient(q, tok, k, c);
             }
-            C = a[k] * (d + C);
+            C = held.a[k] * (d + C);
             if (!PLAIN && (tok.first >> k & 1u)) C = splat(0.f);
         }
         if (!PLAIN && tok.first) A = splat(kBegins);
@@ -133,45 +141,56 @@ struct Backward {
     // The gradients of the warp's tokens, from the state before and c behind them.
     template <bool PLAIN>
     static __device__ __forceinline__ void second_walk(const GradArgs &q, const GradMaps &m, Input &in,
-                                                       const Tokens &tok, int t, int c, int lane, float2 bias,
-                                                       float2 scale, const float2 (&a)[kTokens],
-                                                       const float2 (&u)[kTokens], float2 h, float2 dc, Sums &sums) {
+                                                       const Tokens &tok, int t, int c, int lane, float2 scale,
+                                                       const Held &held, float2 h, float2 dc, Sums &sums) {
         const Args &p = q.f;
         float2 prev[kTokens];
 #pragma unroll
         for (int k = 0; k < kTokens; ++k) {
             if (!PLAIN && (tok.first >> k & 1u)) h = first_state(p, tok, k, c);
             prev[k] = h;
-            h = fma2(a[k], h, u[k]);
+            if (PLAIN || (tok.own >> k & 1u))
+                h = fma2(held.a[k], h, scaled<BETA, MODE>(in.x.at(k, lane), held.n[k], held.i[k]));
         }
         const bool ok0 = c < p.D, ok1 = c + 1 < p.D;
 #pragma unroll
         for (int k = kTokens - 1; k >= 0; --k) {
             if (!PLAIN && !(tok.own >> k & 1u)) continue;  // hands c on
+            const float2 a = held.a[k], n = held.n[k], i = held.i[k];
             float2 dh = in.d.at(k, lane) + dc;
             if (!PLAIN && (tok.last >> k & 1u)) dh = dh + last_gradient(q, tok, k, c);
-            const float2 x = in.x.at(k, lane), z = in.z.at(k, lane);
-            float2 y = splat(0.f);
-            if constexpr (BETA) y = in.y[0].at(k, lane);
-            const Terms g = gate_terms<RAW, BETA, MODE>(z, y, bias, scale, p.sigmoid);
-            dc = a[k] * dh;
+            const float2 x = in.x.at(k, lane);
+            dc = a * dh;
             float2 d = dc * prev[k];
-            if (MODE != kNone) d = fma2(g.dn * g.i * x, dh, d);
-            if (RAW) {
-                sums.scale = fma2(d, g.soft, sums.scale);
-                d = d * g.dgdz;
+            if (MODE != kNone) {  // n'(g) i x dh
+                float2 w = dh * x;
+                if (BETA) w = w * i;
+                if (MODE == kLerp) {
+                    d = fma2(w, -a, d);
+                } else {  // n' = -a^2 / n; where n is 0 (a >= 1) it is taken as 0
+                    const float2 r = make_float2(n.x > 0.f ? reciprocal(n.x) : 0.f, n.y > 0.f ? reciprocal(n.y) : 0.f);
+                    d = fma2(w, -(a * a * r), d);
+                }
+            }
+            if (RAW) {  // sigmoid(z) = 1 - e^-softplus(z)
+                sums.scale = fma2(d, held.soft[k], sums.scale);
+                d = d * (-scale * exp_minus_1(-held.soft[k]));
                 sums.bias = sums.bias + d;
             }
-            const float2 w = g.n * dh;
+            const float2 w = MODE == kNone ? dh : n * dh, dx = BETA ? w * i : w;
+            float2 dy = splat(0.f);
+            if (BETA) {
+                dy = w * x;
+                if (p.sigmoid) dy = dy * fma2(i, -i, i);
+            }
             if (PLAIN && p.wide) {
-                in.x.v[k][lane] = pack<TA>(w * g.i);
+                in.x.v[k][lane] = pack<TA>(dx);
                 in.z.v[k][lane] = pack<TG>(d);
-                if constexpr (BETA) in.y[0].v[k][lane] = pack<TG>(w * x * g.di);
+                if constexpr (BETA) in.y[0].v[k][lane] = pack<TG>(dy);
             } else if (ok0) {
-                store_pair<TA>(static_cast<TA *>(q.dx) + (t + k) * q.dxs + c, w * g.i, p.vec, ok1);
+                store_pair<TA>(static_cast<TA *>(q.dx) + (t + k) * q.dxs + c, dx, p.vec, ok1);
                 store_pair<TG>(static_cast<TG *>(q.dg) + (t + k) * q.dgs + c, d, p.vec, ok1);
-                if constexpr (BETA)
-                    store_pair<TG>(static_cast<TG *>(q.db) + (t + k) * q.dbs + c, w * x * g.di, p.vec, ok1);
+                if constexpr (BETA) store_pair<TG>(static_cast<TG *>(q.db) + (t + k) * q.dbs + c, dy, p.vec, ok1);
             }
             if (!PLAIN && (tok.first >> k & 1u)) {
                 const int row = __shfl_sync(0xffffffffu, tok.row, k);
@@ -240,9 +259,10 @@ struct Backward {
                 __syncwarp();
             }
             const bool plain = tok.own == kAll && !(tok.first | tok.last);
-            float2 a[kTokens], u[kTokens], A, H, C;
-            if (plain) first_walk<true>(q, in, tok, c, lane, bias, scale, a, u, A, H, C);
-            else first_walk<false>(q, in, tok, c, lane, bias, scale, a, u, A, H, C);
+            Held held;
+            float2 A, H, C;
+            if (plain) first_walk<true>(q, in, tok, c, lane, bias, scale, held, A, H, C);
+            else first_walk<false>(q, in, tok, c, lane, bias, scale, held, A, H, C);
             *reinterpret_cast<float4 *>(&r.fwd[warp][2 * lane]) = make_float4(A.x, H.x, A.y, H.y);
             *reinterpret_cast<float4 *>(&r.rev.map[warp][2 * lane]) = make_float4(A.x, C.x, A.y, C.y);
             __syncthreads();
@@ -260,8 +280,8 @@ struct Backward {
             __syncthreads();
             const float2 dc = *reinterpret_cast<const float2 *>(&r.rev.h[warp][2 * lane]);
             const float2 h = *reinterpret_cast<const float2 *>(&r.h[warp][2 * lane]);
-            if (plain) second_walk<true>(q, m, in, tok, t, c, lane, bias, scale, a, u, h, dc, sums);
-            else second_walk<false>(q, m, in, tok, t, c, lane, bias, scale, a, u, h, dc, sums);
+            if (plain) second_walk<true>(q, m, in, tok, t, c, lane, scale, held, h, dc, sums);
+            else second_walk<false>(q, m, in, tok, t, c, lane, scale, held, h, dc, sums);
             if (kRing == 1 && turn + 1 < steps) {
                 next = look_up(p, t - window, kTokens, lane, seen);
                 if (lane == 0) ptx::bulk_wait_read();

@@ -87,7 +87,9 @@ struct Forward {
         for (int k = 0; k < kTokens; ++k) {
             float2 y = splat(0.f);
             if constexpr (BETA) y = in.y[0].at(k, lane);
-            token_map<RAW, BETA, MODE>(in.x.at(k, lane), in.z.at(k, lane), y, bias, scale, p.sigmoid, a[k], u[k]);
+            const Gates g = token_gates<RAW, BETA, MODE>(in.z.at(k, lane), y, bias, scale, p.sigmoid);
+            a[k] = g.a;
+            u[k] = scaled<BETA, MODE>(in.x.at(k, lane), g.n, g.i);
             if (!PLAIN) {  // tokens of no request hand the state on
                 if (!(tok.own >> k & 1u)) a[k] = splat(1.f), u[k] = splat(0.f);
                 if (tok.first >> k & 1u) {  // takes in the request's initial state

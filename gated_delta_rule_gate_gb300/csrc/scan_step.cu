@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(const __grid_consta
             const float2 m = exp_minus_1(p.bias ? log_decay<true>(zz, bb, ss) : zz), a = m + splat(1.f);
             float2 u = make_float2(x[i], x[j]);
             if (p.beta) u = u * (p.sigmoid ? sigmoid(yy) : yy);
-            if (p.mode == kLerp) u = u * make_float2(-m.x, -m.y);
+            if (p.mode == kLerp) u = u * -m;
             if (p.mode == kUnit) u = u * unit_scale(m);
             const float2 r = fma2(a, make_float2(h[i], h[j]), u);
             h[i] = r.x;
