@@ -21,6 +21,7 @@ struct Args {
     int mode, sigmoid;
     int vec;               // pairs of channels can be read and written as one word
     int wide;              // the inputs' rows begin on 16-byte addresses
+    int groups, per;       // groups of requests that a cluster takes side by side, requests in one
     int64_t xs, gs, bs, os;
     const void *x, *decay, *beta;
     void *o;
@@ -160,9 +161,9 @@ __device__ __forceinline__ bool find_request(const Args &p, int t, int &t0, int 
 }
 
 // The tokens of a warp's tile [t, t + n), n <= 32, as masks of their places:
-// owned by a request, first and last of it; lane k holds the state row of token
-// t + k.  `in0`, `in1` carry the last request seen, so that a tile inside it
-// takes no search.
+// owned by a request and in [lo, hi), first and last of it; lane k holds the state
+// row of token t + k.  `seen` is the last request met, so that a tile inside it takes
+// no search.
 struct Tokens {
     unsigned own, first, last;
     int row;
@@ -170,7 +171,7 @@ struct Tokens {
 struct Seen {
     int t0 = 0, t1 = 0, row = -1;
 };
-__device__ __forceinline__ Tokens look_up(const Args &p, int t, int n, int lane, Seen &seen) {
+__device__ __forceinline__ Tokens look_up(const Args &p, int lo, int hi, int t, int n, int lane, Seen &seen) {
     Tokens k;
     if (t > seen.t0 && t + n < seen.t1 && t >= 0) {
         k.own = seen.row >= 0 ? (n == 32 ? ~0u : (1u << n) - 1u) : 0u;
@@ -181,7 +182,7 @@ __device__ __forceinline__ Tokens look_up(const Args &p, int t, int n, int lane,
     bool own = false, first = false, last = false;
     int t0 = 0, t1 = 0, row = -1;
     const int tk = t + lane;
-    if (lane < n && tk >= 0 && tk < p.T) {
+    if (lane < n && tk >= lo && tk < hi) {
         own = find_request(p, tk, t0, t1, row);
         first = own && tk == t0;
         last = own && tk + 1 == t1;

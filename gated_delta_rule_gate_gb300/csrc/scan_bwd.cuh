@@ -54,7 +54,7 @@ struct Backward {
     struct Rest {
         Exchange x;
         Meeting rev;               // (A, C) of each warp's run, and c behind it
-        float2 fwd[kWarps][64];    // (A, H) of each warp's run; at the end its sums
+        alignas(16) float2 fwd[kWarps][64];  // (A, H) of each warp's run; at the end its sums
         float h[kWarps][64];       // the state before it
         uint64_t bar[kWarps][2];
     };
@@ -213,11 +213,11 @@ struct Backward {
     static __device__ __forceinline__ void run(const GradArgs &q, const GradMaps &m, Shared &s) {
         const Args &p = q.f;
         Rest &r = s.r;
-        const int S = cluster_size(), rank = cluster_rank();
+        const Place at = place_of(p);
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const int block = (int)(blockIdx.x / S), c = block * 64 + 2 * lane;
+        const int block = (int)(blockIdx.x / at.size), c = block * 64 + 2 * lane;
         constexpr unsigned kAll = (1u << kTokens) - 1u;
-        const int window = S * kTile, steps = (p.T + window - 1) / window;
+        const int window = at.S * kTile, steps = windows(at, window);
         if (lane == 0) {
             ptx::mbar_init(&r.bar[warp][0], 1);
             ptx::mbar_init(&r.bar[warp][1], 1);
@@ -225,17 +225,17 @@ struct Backward {
         }
         __syncwarp();
         // the windows from the last to the first
-        int t = (steps - 1) * window + rank * kTile + warp * kTokens;
+        int t = at.base + (steps - 1) * window + at.rank * kTile + warp * kTokens;
         Seen seen;
         Tokens tok = {}, next = {};
         if (steps > 0) {
-            tok = look_up(p, t, kTokens, lane, seen);
+            tok = look_up(p, at.lo, at.hi, t, kTokens, lane, seen);
             fill(q, m, s.in[warp][0], &r.bar[warp][0], t, block, tok.own, lane);
         }
-        gradient_duties(q, S * kWarps, rank * kWarps + warp, lane, c, blockIdx.x < S);
+        gradient_duties(q, at.size * kWarps, at.me * kWarps + warp, lane, c, blockIdx.x < at.size);
         float2 bias = splat(0.f), scale = bias;
         if (RAW) bias = load_state(p.bias, c, p.D), scale = load_state(p.scale, c, p.D);
-        if (S > 1) exchange_init(r.x);
+        if (at.size > 1) exchange_init(r.x);
 
         Sums sums = {};
         float carry = 0.f;  // c of this thread's channel (see Meet) behind the window
@@ -243,7 +243,7 @@ struct Backward {
             const int stage = turn % kRing;
             Input &in = s.in[warp][stage];
             if (kRing == 2 && turn + 1 < steps) {
-                next = look_up(p, t - window, kTokens, lane, seen);
+                next = look_up(p, at.lo, at.hi, t - window, kTokens, lane, seen);
                 if (lane == 0) ptx::bulk_wait_read();  // the other stage's gradients have left it
                 __syncwarp();
                 fill(q, m, s.in[warp][stage ^ 1], &r.bar[warp][stage ^ 1], t - window, block, next.own, lane);
@@ -251,7 +251,7 @@ struct Backward {
             // the state that the forward pass kept before the tile, early
             const int tile = t - warp * kTokens, ch = block * 64 + (threadIdx.x & 63);
             float kept = 0.f;
-            if (tile < p.T && ch < p.D)
+            if (tile < at.hi && ch < p.D)
                 kept = p.chunk[(size_t)(tile / kChunk) * p.D + ch];
             if (p.wide) {
                 if (!ptx::mbar_wait(&r.bar[warp][stage], turn / kRing & 1) && p.err) atomicOr(p.err, kErrTimeout);
@@ -267,7 +267,7 @@ struct Backward {
             *reinterpret_cast<float4 *>(&r.rev.map[warp][2 * lane]) = make_float4(A.x, C.x, A.y, C.y);
             __syncthreads();
             Meet<true> meet;
-            const float2 whole = meet.send(r.rev, r.x, S, rank, turn);
+            const float2 whole = meet.send(r.rev, r.x, at, turn);
             {  // while the maps are on their way: the states before the warps' runs
                 float h = kept;
 #pragma unroll
@@ -276,14 +276,14 @@ struct Backward {
                     h = apply(r.fwd[w][meet.c], h);
                 }
             }
-            meet.receive(r.rev, r.x, S, rank, turn, whole, carry, p.err);
+            meet.receive(r.rev, r.x, at, turn, whole, carry, p.err);
             __syncthreads();
             const float2 dc = *reinterpret_cast<const float2 *>(&r.rev.h[warp][2 * lane]);
             const float2 h = *reinterpret_cast<const float2 *>(&r.h[warp][2 * lane]);
             if (plain) second_walk<true>(q, m, in, tok, t, c, lane, scale, held, h, dc, sums);
             else second_walk<false>(q, m, in, tok, t, c, lane, scale, held, h, dc, sums);
             if (kRing == 1 && turn + 1 < steps) {
-                next = look_up(p, t - window, kTokens, lane, seen);
+                next = look_up(p, at.lo, at.hi, t - window, kTokens, lane, seen);
                 if (lane == 0) ptx::bulk_wait_read();
                 __syncwarp();
                 fill(q, m, in, &r.bar[warp][0], t - window, block, next.own, lane);
@@ -296,24 +296,30 @@ struct Backward {
             *reinterpret_cast<float4 *>(&r.fwd[warp][2 * lane]) =
                 make_float4(sums.bias.x, sums.scale.x, sums.bias.y, sums.scale.y);
             __syncthreads();
+            if (at.size > 1) {  // no group uses its buffers any more
+                cluster_arrive();
+                cluster_wait();
+            }
             if (threadIdx.x < 64) {
-                const int k = threadIdx.x, ch = block * 64 + k, par = steps & 1;  // one turn more of the exchange
+                const int k = threadIdx.x, ch = block * 64 + k;
                 float2 v = r.fwd[0][k];
                 for (int w = 1; w < kWarps; ++w) v = v + r.fwd[w][k];
-                if (S > 1) {
-                    if (k == 0) exchange_expect(r.x, par, S);
-                    for (int i = 0; i < S; ++i) exchange_send(r.x, par, rank, i, k, v);
-                    exchange_wait(r.x, par, steps >> 1, p.err);
-                    v = r.x.map[par][0][k];
-                    for (int i = 1; i < S; ++i) v = v + r.x.map[par][i][k];
+                if (at.size > 1) {
+                    if (at.me == 0 && k == 0) exchange_expect(r.x, 2, at.size);
+                    exchange_send(r.x, 0, 2, at.me, 0, k, v);
+                    if (at.me == 0) {
+                        if (!ptx::mbar_wait(&r.x.bar[2], 0, 1u << 20) && p.err) atomicOr(p.err, kErrTimeout);
+                        v = r.x.map[0][0][k];
+                        for (int i = 1; i < at.size; ++i) v = v + r.x.map[0][i][k];
+                    }
                 }
-                if (rank == 0 && ch < p.D) {
+                if (at.me == 0 && ch < p.D) {
                     if (q.dbias) q.dbias[ch] = v.x;
                     if (q.dscale) q.dscale[ch] = v.y;
                 }
             }
         }
-        if (S > 1) {  // no block leaves while another may still send to it
+        if (at.size > 1) {  // no block leaves while another may still send to it
             cluster_arrive();
             cluster_wait();
         }
@@ -339,6 +345,7 @@ cudaError_t launch_grad_one(const GradArgs &args, cudaStream_t stream) {
     const cudaError_t e =
         cluster_blocks((const void *)kernel, sizeof(typename G::Shared), cb, (p.T + G::kTile - 1) / G::kTile, &S);
     if (e != cudaSuccess) return e;
+    share_out(q.f, S, G::kTile);
     GradMaps m = {};
     constexpr int ta = type_of<TA>(), tg = type_of<TG>(), n = G::kTokens;
     if (p.wide && !(make_token_map(&m.x, p.x, ta, p.xs, p.D, p.T, n) &&

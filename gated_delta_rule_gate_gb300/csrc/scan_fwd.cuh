@@ -141,13 +141,13 @@ struct Forward {
     }
 
     static __device__ __forceinline__ void run(const Args &p, const Maps &m, Shared &s) {
-        const int S = cluster_size(), rank = cluster_rank();
+        const Place at = place_of(p);
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const int block = (int)(blockIdx.x / S), c = block * 64 + 2 * lane;
+        const int block = (int)(blockIdx.x / at.size), c = block * 64 + 2 * lane;
         constexpr unsigned kAll = (1u << kTokens) - 1u;
 
-        const int window = S * kTile, steps = (p.T + window - 1) / window;
-        int t = rank * kTile + warp * kTokens;
+        const int window = at.S * kTile, steps = windows(at, window);
+        int t = at.base + at.rank * kTile + warp * kTokens;
         Input &in = s.in[warp];
         uint64_t *bar = &s.bar[warp];
         if (lane == 0) {
@@ -156,12 +156,12 @@ struct Forward {
         }
         __syncwarp();
         Seen seen;
-        Tokens tok = look_up(p, t, kTokens, lane, seen);
+        Tokens tok = look_up(p, at.lo, at.hi, t, kTokens, lane, seen);
         if (steps > 0) fill(p, m, in, bar, t, block, tok.own, lane);
         float2 bias = splat(0.f), scale = bias;
         if (RAW) bias = load_state(p.bias, c, p.D), scale = load_state(p.scale, c, p.D);
-        request_duties(p, S * kWarps, rank * kWarps + warp, lane, c, blockIdx.x < S);
-        if (S > 1) exchange_init(s.x);
+        request_duties(p, at.size * kWarps, at.me * kWarps + warp, lane, c, blockIdx.x < at.size);
+        if (at.size > 1) exchange_init(s.x);
 
         float carry = 0.f;  // the state of this thread's channel (see Meet) before the window
         for (int step = 0; step < steps; ++step, t += window) {
@@ -179,21 +179,21 @@ struct Forward {
                       : first_walk<false>(p, in, now, c, lane, bias, scale, a, u);
             __syncthreads();
             Meet<false> meet;
-            const float2 tile = meet.send(s.meet, s.x, S, rank, step);
+            const float2 tile = meet.send(s.meet, s.x, at, step);
             if (step + 1 < steps) {  // while the maps are on their way
-                tok = look_up(p, t + window, kTokens, lane, seen);
+                tok = look_up(p, at.lo, at.hi, t + window, kTokens, lane, seen);
                 fill(p, m, in, bar, t + window, block, tok.own, lane);
             }
-            meet.receive(s.meet, s.x, S, rank, step, tile, carry, p.err);
+            meet.receive(s.meet, s.x, at, step, tile, carry, p.err);
             __syncthreads();
             const float2 h = *reinterpret_cast<const float2 *>(&s.meet.h[warp][2 * lane]);
-            if (p.chunk && t % kChunk == 0 && t < p.T)
+            if (p.chunk && t % kChunk == 0 && t >= at.lo && t < at.hi)
                 store_state(p.chunk + (size_t)(t / kChunk) * p.D, c, p.D, h);
             if (plain) second_walk<true>(p, m, s.out[warp], now, t, c, lane, a, u, h);
             else second_walk<false>(p, m, s.out[warp], now, t, c, lane, a, u, h);
         }
         if (lane == 0) ptx::bulk_wait();
-        if (S > 1) {  // no block leaves while another may still send to it
+        if (at.size > 1) {  // no block leaves while another may still send to it
             cluster_arrive();
             cluster_wait();
         }
@@ -219,6 +219,7 @@ cudaError_t launch_one(const Args &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     Maps m = {};
     Args q = p;
+    share_out(q, S, F::kTile);
     if (q.wide && !(make_token_map(&m.x, p.x, type_of<TA>(), p.xs, p.D, p.T, F::kTokens) &&
                     make_token_map(&m.z, p.decay, type_of<TG>(), p.gs, p.D, p.T, F::kTokens) &&
                     (!BETA || make_token_map(&m.y, p.beta, type_of<TG>(), p.bs, p.D, p.T, F::kTokens)) &&

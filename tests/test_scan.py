@@ -102,6 +102,11 @@ CASES = [
     dict(D=40, cu=[7, 20, 20, 50], T=77),  # tokens of no request at both ends
     dict(D=72, lengths=[5, 40, 0, 9], rows=11, slots=[7, 0, 10, 3], mode="lerp"),
     dict(D=72, lengths=[5, 40, 0, 9], rows=4, slots=[3, -1, 4, 0], act="f16"),  # two bad slots
+    # equal rows, which a cluster shares out in groups of requests
+    dict(D=70, S=600, seq_lens=[600, 599, 0, 300], act="f16", mode="unit"),
+    dict(D=130, S=321, seq_lens=[321] * 8, mode="lerp"),
+    dict(D=34, S=1100, seq_lens=[1100, 1], act="bf16", rows=3, slots=[2, 0]),
+    dict(D=66, S=2048, seq_lens=[2048, 2047, 2048], act="f16", gate="f32", beta="plain"),
 ]
 
 
