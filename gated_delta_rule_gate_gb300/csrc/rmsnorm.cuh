@@ -272,8 +272,8 @@ cudaError_t launch_rmsnorm_as(const Args &p, int q, bool vec, cudaStream_t strea
 // ---------------------------------------------------------------- gradient
 // xhat = r rstd, m = mean(weight d_out xhat): dx = rstd (weight d_out - xhat m) +
 // d_residual.  A block takes rows b, b + blocks, ...; a thread has the same
-// columns of each, so that its share of d_weight stays in registers; the blocks'
-// shares meet in the workspace, which a second kernel adds up in their order.
+// columns of each, so that its share of d_weight stays in registers, and the next
+// row's tensors are loaded while this one's sum is formed; the blocks' shares meet in the workspace, which a second kernel adds up in their order.
 template <typename TA, typename TR, int V, int N>
 __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constant__ GradArgs p, float *partial) {
     __shared__ float s_red[2][64];
@@ -286,30 +286,50 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constan
         for (int v = 0; v < V; ++v) w[i][v] = dw[i][v] = 0.f;
         if (c < D) load_as<TA, V>(p.weight, p.w_f32, c, w[i]);
     }
-    int par = 0;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
-        float d[N][V], x[N][V];
-        const float rstd = p.rstd[row];
-        float dot = 0.f, none = 0.f;
+    // a row's tensors, on their way while the row before is reduced and written (where
+    // 64 registers, of blocks of up to 1024 threads, hold both)
+    constexpr bool kAhead = V * N <= 4 || (V == 8 && sizeof(TR) == 2);
+    struct Row {
+        Words<TA, V> d[N];
+        Words<TR, V> r[N], g[N];
+        float rstd;
+    };
+    auto fetch = [&](int64_t row, Row &w) {
+        if (row >= p.rows) return;
+        w.rstd = p.rstd[row];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-#pragma unroll
-            for (int v = 0; v < V; ++v) d[i][v] = x[i][v] = 0.f;
             if (c < D) {
-                load_values<TA, V>(static_cast<const TA *>(p.d_out) + row * p.dos + c, d[i]);
-                load_values<TR, V>(static_cast<const TR *>(p.r) + row * D + c, x[i]);
+                w.d[i].load(static_cast<const TA *>(p.d_out) + row * p.dos + c);
+                w.r[i].load(static_cast<const TR *>(p.r) + row * D + c);
+                if (p.d_res) w.g[i].load(static_cast<const TR *>(p.d_res) + row * D + c);
             }
         }
+    };
+    Row next;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+    for (int i = 0; i < N; ++i) next.d[i].zero(), next.r[i].zero(), next.g[i].zero();
+    if (kAhead) fetch(blockIdx.x, next);
+    int par = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
+        if (!kAhead) fetch(row, next);
+        const Row now = next;
+        if (kAhead) fetch(row + gridDim.x, next);
+        float d[N][V], x[N][V];
+        float dot = 0.f, none = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            now.d[i].get(d[i]);
+            now.r[i].get(x[i]);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                x[i][v] *= rstd;
+                x[i][v] *= now.rstd;
                 dw[i][v] = fmaf(d[i][v], x[i][v], dw[i][v]);
                 d[i][v] *= w[i][v];
                 dot = fmaf(d[i][v], x[i][v], dot);
             }
+        }
         block_sum_max(dot, none, s_red[par]);
         const float m = dot / (float)D;
 #pragma unroll
@@ -317,11 +337,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constan
             const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
             if (c >= D) continue;
             float g[V];
+            now.g[i].get(g);  // zeros without d_residual
 #pragma unroll
-            for (int v = 0; v < V; ++v) g[v] = 0.f;
-            if (p.d_res) load_values<TR, V>(static_cast<const TR *>(p.d_res) + row * D + c, g);
-#pragma unroll
-            for (int v = 0; v < V; ++v) g[v] += rstd * (d[i][v] - x[i][v] * m);
+            for (int v = 0; v < V; ++v) g[v] += now.rstd * (d[i][v] - x[i][v] * m);
             store_values<TR, V>(static_cast<TR *>(p.dx) + row * D + c, g);
         }
     }

@@ -10,35 +10,52 @@
 
 namespace gdn {
 
+// V adjacent values as they are stored: one word of up to 16 bytes (fp32: V / 4 of
+// them), so that they can be on their way while others are worked on.
+template <typename T, int V>
+struct Words {
+    static constexpr int kBytes = V * (int)sizeof(T) > 16 ? 16 : V * (int)sizeof(T);
+    static constexpr int kCount = V * (int)sizeof(T) / kBytes;
+    using type = std::conditional_t<
+        V == 1, T, std::conditional_t<sizeof(T) == 4, float4, std::conditional_t<V == 8, uint4, uint2>>>;
+    type w[kCount];
+
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) w[i] = reinterpret_cast<const type *>(p)[i];
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) w[i] = type{};
+    }
+    __device__ __forceinline__ void get(float (&v)[V]) const {
+        if constexpr (V == 1) {
+            v[0] = static_cast<float>(w[0]);
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < kCount; ++i)
+                v[4 * i] = w[i].x, v[4 * i + 1] = w[i].y, v[4 * i + 2] = w[i].z, v[4 * i + 3] = w[i].w;
+        } else {
+            static_assert(V == 8 || V == 4, "16-bit groups");
+            const uint32_t *u = reinterpret_cast<const uint32_t *>(&w[0]);
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                uint32_t q = u[i];
+                float2 f;
+                if constexpr (std::is_same<T, __half>::value) f = __half22float2(*reinterpret_cast<__half2 *>(&q));
+                else f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&q));
+                v[2 * i] = f.x, v[2 * i + 1] = f.y;
+            }
+        }
+    }
+};
+
 // V values of type T at p (V > 1: 16 bytes, or 32 as two, aligned to 16).
 template <typename T, int V>
 __device__ __forceinline__ void load_values(const T *p, float (&v)[V]) {
-    if constexpr (V == 1) {
-        v[0] = static_cast<float>(*p);
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const float4 r = *reinterpret_cast<const float4 *>(p + i);
-            v[i] = r.x, v[i + 1] = r.y, v[i + 2] = r.z, v[i + 3] = r.w;
-        }
-    } else {
-        static_assert(V == 8 || V == 4, "16-bit groups");
-        uint32_t w[V / 2];
-        if constexpr (V == 8) {
-            const uint4 r = *reinterpret_cast<const uint4 *>(p);
-            w[0] = r.x, w[1] = r.y, w[2] = r.z, w[3] = r.w;
-        } else {
-            const uint2 r = *reinterpret_cast<const uint2 *>(p);
-            w[0] = r.x, w[1] = r.y;
-        }
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            float2 f;
-            if constexpr (std::is_same<T, __half>::value) f = __half22float2(*reinterpret_cast<__half2 *>(&w[i]));
-            else f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&w[i]));
-            v[2 * i] = f.x, v[2 * i + 1] = f.y;
-        }
-    }
+    Words<T, V> w;
+    w.load(p);
+    w.get(v);
 }
 
 template <typename T, int V>
