@@ -399,5 +399,11 @@ __device__ __forceinline__ void tma_store_2d(const void *tmap, int c0, int c1, c
 // Shared memory written by this thread's generic stores, and by those it has
 // synchronised with, is seen by the asynchronous copies that follow.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// Brings a 2-D box of a tensor map into L2 ahead of its load.
+__device__ __forceinline__ void tma_prefetch_2d(const void *tmap, int c0, int c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+                 "r"(c0), "r"(c1)
+                 : "memory");
+}
 }  // namespace ptx
 }  // namespace gdn

@@ -91,10 +91,11 @@ __device__ __forceinline__ pair_t<T> zero_pair() {
 template <typename T>
 __device__ __forceinline__ pair_t<T> load_pair(const T *p, bool vec, bool ok1) {
     if (vec) return __ldg(reinterpret_cast<const pair_t<T> *>(p));
-    float2 v;
-    v.x = static_cast<float>(p[0]);
-    v.y = ok1 ? static_cast<float>(p[1]) : 0.f;
-    return pack<T>(v);  // exact: the values come from T
+    pair_t<T> v;
+    T *e = reinterpret_cast<T *>(&v);
+    e[0] = __ldg(p);
+    e[1] = __ldg(p + (ok1 ? 1 : 0));  // unused where there is none
+    return v;
 }
 template <typename T>
 __device__ __forceinline__ void store_pair(T *p, float2 v, bool vec, bool ok1) {

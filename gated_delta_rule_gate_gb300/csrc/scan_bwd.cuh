@@ -88,6 +88,13 @@ struct Backward {
         }
     }
 
+    static __device__ __forceinline__ void prefetch(const GradMaps &m, int t, int block) {
+        Stage<TA, kTokens>::prefetch(m.x, t, block);
+        Stage<TA, kTokens>::prefetch(m.d, t, block);
+        Stage<TG, kTokens>::prefetch(m.z, t, block);
+        if constexpr (BETA) Stage<TG, kTokens>::prefetch(m.y, t, block);
+    }
+
     static __device__ __forceinline__ float2 first_state(const Args &p, const Tokens &tok, int k, int c) {
         const int row = __shfl_sync(0xffffffffu, tok.row, k);
         return p.init ? load_state(p.init + (size_t)row * p.D, c, p.D) : splat(0.f);
@@ -232,10 +239,10 @@ struct Backward {
             tok = look_up(p, at.lo, at.hi, t, kTokens, lane, seen);
             fill(q, m, s.in[warp][0], &r.bar[warp][0], t, block, tok.own, lane);
         }
-        gradient_duties(q, at.size * kWarps, at.me * kWarps + warp, lane, c, blockIdx.x < at.size);
         float2 bias = splat(0.f), scale = bias;
         if (RAW) bias = load_state(p.bias, c, p.D), scale = load_state(p.scale, c, p.D);
         if (at.size > 1) exchange_init(r.x);
+        gradient_duties(q, at.size * kWarps, at.me * kWarps + warp, lane, c, blockIdx.x < at.size);
 
         Sums sums = {};
         float carry = 0.f;  // c of this thread's channel (see Meet) behind the window
@@ -248,6 +255,7 @@ struct Backward {
                 __syncwarp();
                 fill(q, m, s.in[warp][stage ^ 1], &r.bar[warp][stage ^ 1], t - window, block, next.own, lane);
             }
+            if (kRing == 1 && turn + 1 < steps && p.wide && lane == 0) prefetch(m, t - window, block);
             // the state that the forward pass kept before the tile, early
             const int tile = t - warp * kTokens, ch = block * 64 + (threadIdx.x & 63);
             float kept = 0.f;

@@ -59,14 +59,20 @@ struct alignas(128) Stage {
     __device__ __forceinline__ void fill(const CUtensorMap &map, int t, int block, uint64_t *bar) {
         ptx::tma_load_2d(&v[0][0], &map, block * 64, t, bar);
     }
+    static __device__ __forceinline__ void prefetch(const CUtensorMap &map, int t, int block) {
+        ptx::tma_prefetch_2d(&map, block * 64, t);
+    }
     __device__ __forceinline__ void fill_plain(const void *base, int64_t stride, int t, int block, unsigned own, int D,
                                                bool vec, int lane) {
         const int c = block * 64 + 2 * lane;
         const T *p = static_cast<const T *>(base) + (int64_t)t * stride + c;
         if (c >= D) own = 0u;
+        pair_t<T> r[TOKENS];  // all on their way before the first is stored
 #pragma unroll
         for (int k = 0; k < TOKENS; ++k)
-            v[k][lane] = (own >> k & 1u) ? load_pair<T>(p + k * stride, vec, c + 1 < D) : zero_pair<T>();
+            r[k] = (own >> k & 1u) ? load_pair<T>(p + k * stride, vec, c + 1 < D) : zero_pair<T>();
+#pragma unroll
+        for (int k = 0; k < TOKENS; ++k) v[k][lane] = r[k];
     }
     __device__ __forceinline__ float2 at(int k, int lane) const { return unpack<T>(v[k][lane]); }
 };

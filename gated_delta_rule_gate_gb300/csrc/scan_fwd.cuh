@@ -160,8 +160,8 @@ struct Forward {
         if (steps > 0) fill(p, m, in, bar, t, block, tok.own, lane);
         float2 bias = splat(0.f), scale = bias;
         if (RAW) bias = load_state(p.bias, c, p.D), scale = load_state(p.scale, c, p.D);
-        request_duties(p, at.size * kWarps, at.me * kWarps + warp, lane, c, blockIdx.x < at.size);
         if (at.size > 1) exchange_init(s.x);
+        request_duties(p, at.size * kWarps, at.me * kWarps + warp, lane, c, blockIdx.x < at.size);
 
         float carry = 0.f;  // the state of this thread's channel (see Meet) before the window
         for (int step = 0; step < steps; ++step, t += window) {
