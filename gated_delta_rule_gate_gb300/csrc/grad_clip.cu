@@ -10,6 +10,7 @@
 #include <math.h>
 
 #include "launch.h"
+#include "ptx.cuh"
 #include "status.h"
 #include "values.cuh"
 
@@ -95,6 +96,7 @@ __device__ __forceinline__ void chunk_scale(const T *p, T *o, int n, float k) {
 template <int MAX>
 __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ Table<MAX> tab, float *partial) {
     __shared__ float s[kThreads / 32];
+    ptx::grid_wait();
     float sum = 0.f;
     for (int chunk = blockIdx.x; chunk < tab.chunks; chunk += gridDim.x) {
         const Tensor &t = tab.t[find_tensor(tab, chunk)];
@@ -118,6 +120,7 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
                                                         const float *partial, int partials, float max_norm, float eps,
                                                         float *norm_out, int32_t *err) {
     __shared__ double s[kThreads / 32];
+    ptx::grid_wait();
     double sum = 0.;
     for (int i = threadIdx.x; i < partials; i += kThreads) sum += (double)partial[i];
 #pragma unroll
@@ -188,7 +191,8 @@ cudaError_t run(const gdn_grad_clip_args *a, float *ws, cudaStream_t stream) {
         i = fill<MAX>(a, i, &tab);
         const int blocks = tab.chunks < kBlocks ? tab.chunks : kBlocks;
         if (blocks == 0) continue;
-        squares_kernel<MAX><<<blocks, kThreads, 0, stream>>>(tab, ws + total);
+        const cudaError_t e = launch_early(squares_kernel<MAX>, blocks, kThreads, 0, stream, tab, ws + total);
+        if (e != cudaSuccess) return e;
         total += blocks;
     }
     bool first = true;
@@ -196,10 +200,13 @@ cudaError_t run(const gdn_grad_clip_args *a, float *ws, cudaStream_t stream) {
         i = fill<MAX>(a, i, &tab);
         const int blocks = tab.chunks < kBlocks ? tab.chunks : kBlocks;
         if (blocks == 0 && !first) continue;
-        scale_kernel<MAX><<<blocks ? blocks : 1, kThreads, 0, stream>>>(
-            tab, ws, total, a->max_norm, a->eps, first ? a->norm : nullptr, first ? a->error_word : nullptr);
+        float *norm = first ? a->norm : nullptr;
+        int32_t *err = first ? a->error_word : nullptr;
+        const cudaError_t e = launch_early(scale_kernel<MAX>, blocks ? blocks : 1, kThreads, 0, stream, tab, ws, total,
+                                           a->max_norm, a->eps, norm, err);
+        if (e != cudaSuccess) return e;
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace clip

@@ -405,5 +405,12 @@ __device__ __forceinline__ void tma_prefetch_2d(const void *tmap, int c0, int c1
                  "r"(c0), "r"(c1)
                  : "memory");
 }
+// ---------------------------------------------------------------- dependent launch
+// Until the kernels before this one on the stream have ended and what they wrote is
+// seen; the next kernel may be set up meanwhile.
+__device__ __forceinline__ void grid_wait() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 }  // namespace ptx
 }  // namespace gdn

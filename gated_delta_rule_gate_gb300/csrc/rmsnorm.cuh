@@ -8,6 +8,7 @@
 #include <cuda_fp8.h>
 
 #include "launch.h"
+#include "ptx.cuh"
 #include "rmsnorm_launch.h"
 #include "values.cuh"
 
@@ -89,6 +90,7 @@ __device__ __forceinline__ void load_r(const Args &p, size_t row, int c, float (
 
 template <typename TA, int Q, int V, int N>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(const __grid_constant__ Args p) {
+    ptx::grid_wait();
     __shared__ float s_red[64];
     extern __shared__ int s_peak[];  // V == 1: the largest |y| of each group, as bits
     const size_t row = blockIdx.x;
@@ -181,6 +183,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const __grid_constant__ A
 // walk is also the one that writes, so that residual_out may be residual.
 template <typename TA, int Q>
 __global__ void __launch_bounds__(1024) rmsnorm_wide_kernel(const __grid_constant__ Args p) {
+    ptx::grid_wait();
     __shared__ float s_red[64], s_group[64];
     const size_t row = blockIdx.x;
     const int D = p.D;
@@ -244,22 +247,16 @@ cudaError_t launch_out(const Args &p, bool vec, cudaStream_t stream) {
     if (vec) {
         const int groups = p.D / V;
         if (groups <= 512) {
-            rmsnorm_kernel<TA, Q, V, 1><<<rows, threads_for(groups, 1), 0, stream>>>(p);
-            return cudaGetLastError();
+            return launch_early(rmsnorm_kernel<TA, Q, V, 1>, rows, threads_for(groups, 1), 0, stream, p);
         }
         if (groups <= 2048) {
-            rmsnorm_kernel<TA, Q, V, 2><<<rows, threads_for(groups, 2), 0, stream>>>(p);
-            return cudaGetLastError();
+            return launch_early(rmsnorm_kernel<TA, Q, V, 2>, rows, threads_for(groups, 2), 0, stream, p);
         }
     }
     const size_t peaks = (size_t)((p.D + kGroup - 1) / kGroup) * sizeof(int);
-    if (p.D <= 2048)
-        rmsnorm_kernel<TA, Q, 1, 4><<<rows, threads_for(p.D, 4), peaks, stream>>>(p);
-    else if (p.D <= 8192)
-        rmsnorm_kernel<TA, Q, 1, 8><<<rows, threads_for(p.D, 8), peaks, stream>>>(p);
-    else
-        rmsnorm_wide_kernel<TA, Q><<<rows, 1024, 0, stream>>>(p);
-    return cudaGetLastError();
+    if (p.D <= 2048) return launch_early(rmsnorm_kernel<TA, Q, 1, 4>, rows, threads_for(p.D, 4), peaks, stream, p);
+    if (p.D <= 8192) return launch_early(rmsnorm_kernel<TA, Q, 1, 8>, rows, threads_for(p.D, 8), peaks, stream, p);
+    return launch_early(rmsnorm_wide_kernel<TA, Q>, rows, 1024, 0, stream, p);
 }
 
 template <typename TA>
@@ -276,6 +273,7 @@ cudaError_t launch_rmsnorm_as(const Args &p, int q, bool vec, cudaStream_t strea
 // row's tensors are loaded while this one's sum is formed; the blocks' shares meet in the workspace, which a second kernel adds up in their order.
 template <typename TA, typename TR, int V, int N>
 __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constant__ GradArgs p, float *partial) {
+    ptx::grid_wait();
     __shared__ float s_red[2][64];
     const int D = p.D;
     float w[N][V], dw[N][V];
@@ -355,6 +353,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constan
 // can be almost nothing, of which fp32 would keep rounding errors alone.
 template <typename TA, typename TR>
 __global__ void __launch_bounds__(32) rmsnorm_grad_narrow_kernel(const __grid_constant__ GradArgs p, float *partial) {
+    ptx::grid_wait();
     const int c = threadIdx.x;
     const bool on = c < p.D;
     float w[1] = {0.f}, dw = 0.f;
@@ -381,6 +380,7 @@ __global__ void __launch_bounds__(32) rmsnorm_grad_narrow_kernel(const __grid_co
 // Wide rows: the mean of each row first, then columns over a stretch of rows.
 template <typename TA, typename TR>
 __global__ void __launch_bounds__(1024) rmsnorm_grad_mean_kernel(const __grid_constant__ GradArgs p, float *mean) {
+    ptx::grid_wait();
     __shared__ float s_red[64];
     const int64_t row = blockIdx.x;
     float dot = 0.f, none = 0.f;
@@ -398,6 +398,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_mean_kernel(const __grid_co
 template <typename TA, typename TR>
 __global__ void __launch_bounds__(256) rmsnorm_grad_columns_kernel(const __grid_constant__ GradArgs p,
                                                                   const float *mean, float *partial, int column_blocks) {
+    ptx::grid_wait();
     const int c = (int)(blockIdx.x % column_blocks) * 256 + (int)threadIdx.x;
     const int part = blockIdx.x / column_blocks, parts = gridDim.x / column_blocks;
     if (c >= p.D) return;
@@ -421,21 +422,21 @@ cudaError_t launch_grad_as(const GradArgs &p, bool vec, int parts, float *ws, cu
     const unsigned grid = (unsigned)parts;
     if (p.D > kFit) {
         float *mean = ws + (size_t)parts * p.Dp;
-        rmsnorm_grad_mean_kernel<TA, TR><<<(unsigned)p.rows, 1024, 0, stream>>>(p, mean);
+        const cudaError_t e =
+            launch_early(rmsnorm_grad_mean_kernel<TA, TR>, (unsigned)p.rows, 1024, 0, stream, p, mean);
+        if (e != cudaSuccess) return e;
         const int cb = (p.D + 255) / 256;
-        rmsnorm_grad_columns_kernel<TA, TR><<<grid * cb, 256, 0, stream>>>(p, mean, ws, cb);
-    } else if (p.D <= kNarrow) {
-        rmsnorm_grad_narrow_kernel<TA, TR><<<grid, 32, 0, stream>>>(p, ws);
-    } else if (vec && p.D <= 1024 * V) {
-        rmsnorm_grad_kernel<TA, TR, V, 1><<<grid, threads_for(p.D / V, 1), 0, stream>>>(p, ws);
-    } else if (vec) {
-        rmsnorm_grad_kernel<TA, TR, V, kFit / 1024 / V><<<grid, threads_for(p.D / V, kFit / 1024 / V), 0, stream>>>(p, ws);
-    } else if (p.D <= 2048) {
-        rmsnorm_grad_kernel<TA, TR, 1, 4><<<grid, threads_for(p.D, 4), 0, stream>>>(p, ws);
-    } else {
-        rmsnorm_grad_kernel<TA, TR, 1, 8><<<grid, threads_for(p.D, 8), 0, stream>>>(p, ws);
+        return launch_early(rmsnorm_grad_columns_kernel<TA, TR>, grid * cb, 256, 0, stream, p, mean, ws, cb);
     }
-    return cudaGetLastError();
+    if (p.D <= kNarrow) return launch_early(rmsnorm_grad_narrow_kernel<TA, TR>, grid, 32, 0, stream, p, ws);
+    constexpr int kTwo = kFit / 1024 / V;
+    if (vec && p.D <= 1024 * V)
+        return launch_early(rmsnorm_grad_kernel<TA, TR, V, 1>, grid, threads_for(p.D / V, 1), 0, stream, p, ws);
+    if (vec)
+        return launch_early(rmsnorm_grad_kernel<TA, TR, V, kTwo>, grid, threads_for(p.D / V, kTwo), 0, stream, p, ws);
+    if (p.D <= 2048)
+        return launch_early(rmsnorm_grad_kernel<TA, TR, 1, 4>, grid, threads_for(p.D, 4), 0, stream, p, ws);
+    return launch_early(rmsnorm_grad_kernel<TA, TR, 1, 8>, grid, threads_for(p.D, 8), 0, stream, p, ws);
 }
 
 }  // namespace norm

@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include "launch.h"
+#include "ptx.cuh"
 #include "rmsnorm_launch.h"
 #include "status.h"
 
@@ -10,9 +11,10 @@ namespace gdn {
 namespace norm {
 
 // 32 columns by 32 stretches of blocks a block; each column's sum in one order.
-__global__ void __launch_bounds__(1024) weight_sum_kernel(const float *__restrict__ partial, int parts, int D, int Dp,
-                                                          float *__restrict__ dw) {
+__global__ void __launch_bounds__(1024) weight_sum_kernel(const float *partial, int parts, int D, int Dp,
+                                                          float *dw) {
     __shared__ float s[32][33];
+    ptx::grid_wait();
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
     float sum = 0.f;
     if (c < D) {
@@ -28,8 +30,7 @@ __global__ void __launch_bounds__(1024) weight_sum_kernel(const float *__restric
 }
 
 cudaError_t launch_weight_sum(const float *partial, int parts, int D, int Dp, float *dw, cudaStream_t stream) {
-    weight_sum_kernel<<<(unsigned)((D + 31) / 32), 1024, 0, stream>>>(partial, parts, D, Dp, dw);
-    return cudaGetLastError();
+    return launch_early(weight_sum_kernel, (unsigned)((D + 31) / 32), 1024, 0, stream, partial, parts, D, Dp, dw);
 }
 
 }  // namespace norm

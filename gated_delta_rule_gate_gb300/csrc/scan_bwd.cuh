@@ -231,6 +231,7 @@ struct Backward {
             ptx::fence_mbar_init();
         }
         __syncwarp();
+        ptx::grid_wait();
         // the windows from the last to the first
         int t = at.base + (steps - 1) * window + at.rank * kTile + warp * kTokens;
         Seen seen;

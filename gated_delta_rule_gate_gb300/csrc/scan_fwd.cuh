@@ -155,6 +155,7 @@ struct Forward {
             ptx::fence_mbar_init();
         }
         __syncwarp();
+        ptx::grid_wait();
         Seen seen;
         Tokens tok = look_up(p, at.lo, at.hi, t, kTokens, lane, seen);
         if (steps > 0) fill(p, m, in, bar, t, block, tok.own, lane);

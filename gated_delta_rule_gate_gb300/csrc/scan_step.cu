@@ -6,6 +6,7 @@
 // row in and out, 8 bytes a channel, beside the token's tensors) and by launch
 // and memory latency at few; all loads of a token are issued together.
 #include "launch.h"
+#include "ptx.cuh"
 #include "scan_launch.h"
 
 namespace gdn {
@@ -40,6 +41,7 @@ constexpr int kThreads = 128;
 
 template <typename TA, typename TG, int V>
 __global__ void __launch_bounds__(kThreads) scan_step_kernel(const __grid_constant__ Args p, int blocks) {
+    ptx::grid_wait();
     const int b = blockIdx.x / blocks;
     const int c = ((blockIdx.x % blocks) * kThreads + threadIdx.x) * V;
     int t0, t1;
@@ -88,11 +90,8 @@ static cudaError_t launch(const Args &p, bool vec4, cudaStream_t stream) {
     const int per = kThreads * (vec4 ? 4 : 1);
     const int blocks = (p.D + per - 1) / per;
     const unsigned grid = (unsigned)blocks * (unsigned)p.B;
-    if (vec4)
-        scan_step_kernel<TA, TG, 4><<<grid, kThreads, 0, stream>>>(p, blocks);
-    else
-        scan_step_kernel<TA, TG, 1><<<grid, kThreads, 0, stream>>>(p, blocks);
-    return cudaGetLastError();
+    return launch_early(vec4 ? scan_step_kernel<TA, TG, 4> : scan_step_kernel<TA, TG, 1>, grid, kThreads, 0, stream, p,
+                        blocks);
 }
 
 cudaError_t launch_step(const Args &p, int act, int gate, bool vec4, cudaStream_t stream) {
