@@ -11,6 +11,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -198,7 +199,10 @@ class Stream {
 };
 
 at::TensorOptions on(const Tensor &like, ScalarType type) { return at::TensorOptions().device(like.device()).dtype(type); }
-Tensor make(IntArrayRef shape, const Tensor &like, ScalarType type) { return at::empty(shape, on(like, type)); }
+// Device memory by torch's allocator (past the dispatcher, 0.3 us a tensor).
+Tensor make(IntArrayRef shape, const Tensor &like, ScalarType type) {
+    return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
+}
 
 PyObject *wrap(const Tensor &t) { return t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None); }
 // A named tuple of the tensors (None where undefined).
@@ -366,7 +370,7 @@ PyObject *py_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
     Stream stream(v[21], x);
     // every token and row is written unless requests may leave some out
     const bool whole = !c.cu && !c.seq_lens && !c.slots;
-    auto token = [&](ScalarType t) { return whole ? at::empty(shape, on(x, t)) : at::zeros(shape, on(x, t)); };
+    auto token = [&](ScalarType t) { return whole ? make(shape, x, t) : at::zeros(shape, on(x, t)); };
     auto given = [&](int i, const char *what) {
         const Tensor *t = tensor(v[i], what);
         return t ? *t : Tensor();

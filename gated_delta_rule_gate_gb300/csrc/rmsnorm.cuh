@@ -10,6 +10,7 @@
 #include "launch.h"
 #include "ptx.cuh"
 #include "rmsnorm_launch.h"
+#include "twofloat.cuh"
 #include "values.cuh"
 
 namespace gdn {
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constan
     }
 }
 
-// Rows of up to kNarrow values, a warp each, in 64 bits: dx is what is left of
+// Rows of up to kNarrow values, a warp each, in pairs of fp32: dx is what is left of
 // weight d_out once its part along x is taken away, and of one value or a few that
 // can be almost nothing, of which fp32 would keep rounding errors alone.
 template <typename TA, typename TR>
@@ -359,20 +360,18 @@ __global__ void __launch_bounds__(32) rmsnorm_grad_narrow_kernel(const __grid_co
     float w[1] = {0.f}, dw = 0.f;
     if (on) load_as<TA, 1>(p.weight, p.w_f32, c, w);
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const double rstd = p.rstd[row];
-        double d = 0., x = 0.;
+        const float rstd = p.rstd[row];
+        float d = 0.f, r = 0.f;
         if (on) {
             d = static_cast<float>(static_cast<const TA *>(p.d_out)[row * p.dos + c]);
-            x = static_cast<float>(static_cast<const TR *>(p.r)[row * p.D + c]) * rstd;
+            r = static_cast<float>(static_cast<const TR *>(p.r)[row * p.D + c]);
         }
-        dw += (float)(d * x);
-        d *= w[0];
-        double dot = d * x;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        double g = rstd * (d - x * (dot / p.D));
-        if (on && p.d_res) g += static_cast<float>(static_cast<const TR *>(p.d_res)[row * p.D + c]);
-        if (on) static_cast<TR *>(p.dx)[row * p.D + c] = static_cast<TR>((float)g);
+        const TwoFloat x = two_product(r, rstd), wd = two_product(d, w[0]);
+        dw = fmaf(d, x.hi, dw);
+        const TwoFloat m = warp_sum(wd * x) / (float)p.D, g = TwoFloat{rstd, 0.f} * (wd + -(x * m));
+        float res = 0.f;
+        if (on && p.d_res) res = static_cast<float>(static_cast<const TR *>(p.d_res)[row * p.D + c]);
+        if (on) static_cast<TR *>(p.dx)[row * p.D + c] = static_cast<TR>(g.hi + res);
     }
     if (on) partial[(size_t)blockIdx.x * p.Dp + c] = dw;
 }

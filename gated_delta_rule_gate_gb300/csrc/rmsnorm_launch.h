@@ -8,7 +8,7 @@ namespace gdn {
 namespace norm {
 
 constexpr int kFit = 8192;   // values of a row that the gradient keeps in registers
-constexpr int kNarrow = 32;  // rows that the gradient takes in 64 bits
+constexpr int kNarrow = 32;  // longest rows that the gradient takes in pairs of fp32
 
 struct Args {
     int64_t rows, xs;
