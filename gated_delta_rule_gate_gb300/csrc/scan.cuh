@@ -19,8 +19,7 @@ constexpr int kChunk = 64;                       // GDN_SCAN_CHUNK
 struct Args {
     int B, T, L, D, rows;  // L: tokens of a request's row in the uniform forms, 0 with cu
     int mode, sigmoid;
-    int vec;               // pairs of channels can be read and written as one word
-    int wide;              // the inputs' rows begin on 16-byte addresses
+    int wide;              // every tensor's rows begin on 16-byte addresses
     int groups, per;       // groups of requests that a cluster takes side by side, requests in one
     int64_t xs, gs, bs, os;
     const void *x, *decay, *beta;
@@ -86,24 +85,35 @@ template <typename T>
 __device__ __forceinline__ pair_t<T> zero_pair() {
     return pack<T>(make_float2(0.f, 0.f));
 }
-// Channels c, c + 1 at p: one word where `vec`, else element by element, the
-// second only where ok1 (the caller checks the first).
+// Channels c, c + 1 at p (the second where ok1), one by one.
 template <typename T>
-__device__ __forceinline__ pair_t<T> load_pair(const T *p, bool vec, bool ok1) {
-    if (vec) return __ldg(reinterpret_cast<const pair_t<T> *>(p));
+__device__ __forceinline__ pair_t<T> load_pair(const T *p, bool ok1) {
     pair_t<T> v;
     T *e = reinterpret_cast<T *>(&v);
     e[0] = __ldg(p);
     e[1] = __ldg(p + (ok1 ? 1 : 0));  // unused where there is none
     return v;
 }
+// A warp writes the first n of a row's 64 channels at p, a lane two of them, whatever
+// the row's alignment: of a 16-bit row that begins between two words a lane writes its
+// second channel and its neighbour's first as one.
 template <typename T>
-__device__ __forceinline__ void store_pair(T *p, float2 v, bool vec, bool ok1) {
-    if (vec) {
-        *reinterpret_cast<pair_t<T> *>(p) = pack<T>(v);
+__device__ __forceinline__ void store_row(T *p, float2 v, int lane, int n) {
+    if constexpr (sizeof(T) == 4) {
+        if (2 * lane < n) p[2 * lane] = v.x;
+        if (2 * lane + 1 < n) p[2 * lane + 1] = v.y;
     } else {
-        p[0] = static_cast<T>(v.x);
-        if (ok1) p[1] = static_cast<T>(v.y);
+        const uint32_t mine = pack<T>(v);
+        uint16_t *e = reinterpret_cast<uint16_t *>(p);
+        if (!(reinterpret_cast<uintptr_t>(p) & 2u)) {
+            if (2 * lane + 1 < n) reinterpret_cast<uint32_t *>(p)[lane] = mine;
+            else if (2 * lane < n) e[2 * lane] = (uint16_t)mine;
+        } else {
+            const uint32_t w = __funnelshift_r(mine, __shfl_down_sync(0xffffffffu, mine, 1), 16);
+            if (lane < 31 && 2 * lane + 2 < n) *reinterpret_cast<uint32_t *>(e + 2 * lane + 1) = w;
+            else if (2 * lane + 1 < n) e[2 * lane + 1] = (uint16_t)w;
+            if (lane == 0 && n > 0) e[0] = (uint16_t)mine;
+        }
     }
 }
 // The same for fp32 state rows, whose alignment follows the channel count alone.

@@ -35,9 +35,6 @@ gdn_status check_stride(int64_t stride, int channels, const char *what, int64_t 
     return GDN_OK;
 }
 
-// Pairs of elements at even places of q's rows are aligned words.
-bool pairs(const void *q, size_t e, int64_t stride) { return q == nullptr || (aligned(q, 2 * e) && stride % 2 == 0); }
-
 // q's rows begin on 16-byte addresses.
 bool lines(const void *q, size_t e, int64_t stride) {
     return q == nullptr || (aligned(q, 16) && stride * (int64_t)e % 16 == 0);
@@ -96,8 +93,6 @@ gdn_status validate(const gdn_scan_args *a, bool needs_o, Args *out) {
     p.cu = a->cu_seqlens, p.seqlens = a->seq_lens, p.slots = a->slot_ids;
     p.init = a->initial_state, p.fin = a->final_state, p.chunk = a->chunk_states;
     p.err = a->error_word;
-    p.vec = p.D % 2 == 0 && pairs(a->x, ea, p.xs) && (!needs_o || pairs(a->o, ea, p.os)) &&
-            pairs(a->decay, eg, p.gs) && pairs(a->beta, eg, p.bs);
     p.wide = p.T > 0 && lines(a->x, ea, p.xs) && (!needs_o || lines(a->o, ea, p.os)) && lines(a->decay, eg, p.gs) &&
              lines(a->beta, eg, p.bs);
     return GDN_OK;
@@ -166,8 +161,6 @@ gdn_status gdn_scan_backward(const gdn_scan_grad_args *a, gdn_stream stream) {
     q.dbias = a->d_gate_bias, q.dscale = a->d_gate_scale, q.dinit = a->d_initial_state;
     p.fin = nullptr;
     p.o = nullptr;
-    p.vec = p.vec && pairs(a->d_o, ea, q.dos) && pairs(a->dx, ea, q.dxs) && pairs(a->d_decay, eg, q.dgs) &&
-            pairs(a->d_beta, eg, q.dbs);
     p.wide = p.wide && lines(a->d_o, ea, q.dos) && lines(a->dx, ea, q.dxs) && lines(a->d_decay, eg, q.dgs) &&
              lines(a->d_beta, eg, q.dbs);
     if (p.B == 0 && !q.dbias && !q.dscale) return gdn::ok();
@@ -203,15 +196,17 @@ bool make_token_map(CUtensorMap *m, const void *base, int type, int64_t stride, 
 }
 
 cudaError_t launch_scan(const Args &p, int act, int gate, cudaStream_t stream) {
-    if (act == GDN_DTYPE_F32) return launch_scan_f32(p, stream);
-    return act == GDN_DTYPE_F16 ? launch_scan_f16(p, gate == GDN_DTYPE_F32, stream)
-                                : launch_scan_bf16(p, gate == GDN_DTYPE_F32, stream);
+    const bool f = gate == GDN_DTYPE_F32;
+    if (act == GDN_DTYPE_F32) return p.wide ? launch_scan_f32(p, stream) : launch_scan_f32_loose(p, stream);
+    if (act == GDN_DTYPE_F16) return p.wide ? launch_scan_f16(p, f, stream) : launch_scan_f16_loose(p, f, stream);
+    return p.wide ? launch_scan_bf16(p, f, stream) : launch_scan_bf16_loose(p, f, stream);
 }
 
 cudaError_t launch_grad(const GradArgs &p, int act, int gate, cudaStream_t stream) {
-    if (act == GDN_DTYPE_F32) return launch_grad_f32(p, stream);
-    return act == GDN_DTYPE_F16 ? launch_grad_f16(p, gate == GDN_DTYPE_F32, stream)
-                                : launch_grad_bf16(p, gate == GDN_DTYPE_F32, stream);
+    const bool f = gate == GDN_DTYPE_F32, wide = p.f.wide;
+    if (act == GDN_DTYPE_F32) return wide ? launch_grad_f32(p, stream) : launch_grad_f32_loose(p, stream);
+    if (act == GDN_DTYPE_F16) return wide ? launch_grad_f16(p, f, stream) : launch_grad_f16_loose(p, f, stream);
+    return wide ? launch_grad_bf16(p, f, stream) : launch_grad_bf16_loose(p, f, stream);
 }
 
 }  // namespace scan

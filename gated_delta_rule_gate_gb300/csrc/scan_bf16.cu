@@ -1,11 +1,11 @@
-// scan_bf16.cu -- gdn_scan for bf16 activations.
+// scan_bf16.cu -- gdn_scan for bf16 activations, rows on 16-byte addresses.
 #include "scan_fwd.cuh"
 
 namespace gdn {
 namespace scan {
 
 cudaError_t launch_scan_bf16(const Args &p, bool gate_f32, cudaStream_t stream) {
-    return gate_f32 ? launch_types<__nv_bfloat16, float>(p, stream) : launch_types<__nv_bfloat16, __nv_bfloat16>(p, stream);
+    return gate_f32 ? launch_types<true, __nv_bfloat16, float>(p, stream) : launch_types<true, __nv_bfloat16, __nv_bfloat16>(p, stream);
 }
 
 }  // namespace scan

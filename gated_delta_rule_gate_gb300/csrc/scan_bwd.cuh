@@ -40,7 +40,7 @@ struct GradMaps {
     CUtensorMap x, z, y, d, dx, dz, dy;
 };
 
-template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
+template <bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
 struct Backward {
     static constexpr int kTokens = 8;
     static constexpr int kTile = kWarps * kTokens;
@@ -69,10 +69,12 @@ struct Backward {
         float2 bias, scale;
     };
 
+    // The warp's tokens t, ... to its stage, by the asynchronous copies of WIDE rows on
+    // their way there; otherwise the tokens of the window before on their way to L2.
     static __device__ __forceinline__ void fill(const GradArgs &q, const GradMaps &m, Input &in, uint64_t *bar, int t,
-                                                int block, unsigned own, int lane) {
+                                                int window, int block, unsigned own, int lane) {
         const Args &p = q.f;
-        if (p.wide) {
+        if (WIDE) {
             if (lane == 0) {
                 ptx::mbar_arrive_expect_tx(bar, sizeof(Input));
                 in.x.fill(m.x, t, block, bar);
@@ -80,11 +82,24 @@ struct Backward {
                 in.z.fill(m.z, t, block, bar);
                 if constexpr (BETA) in.y[0].fill(m.y, t, block, bar);
             }
+            return;
+        }
+        if (t >= window) {
+            in.x.prefetch_row(p.x, p.xs, t - window, p.T, block, p.D, lane);
+            in.x.prefetch_row(q.d_o, q.dos, t - window, p.T, block, p.D, lane);
+            in.z.prefetch_row(p.decay, p.gs, t - window, p.T, block, p.D, lane);
+            if constexpr (BETA) in.z.prefetch_row(p.beta, p.bs, t - window, p.T, block, p.D, lane);
+        }
+        if (inside(p, t, kTokens, block)) {
+            in.x.fill_words(p.x, p.xs, t, block, own, p.D, lane);
+            in.d.fill_words(q.d_o, q.dos, t, block, own, p.D, lane);
+            in.z.fill_words(p.decay, p.gs, t, block, own, p.D, lane);
+            if constexpr (BETA) in.y[0].fill_words(p.beta, p.bs, t, block, own, p.D, lane);
         } else {
-            in.x.fill_plain(p.x, p.xs, t, block, own, p.D, p.vec, lane);
-            in.d.fill_plain(q.d_o, q.dos, t, block, own, p.D, p.vec, lane);
-            in.z.fill_plain(p.decay, p.gs, t, block, own, p.D, p.vec, lane);
-            if constexpr (BETA) in.y[0].fill_plain(p.beta, p.bs, t, block, own, p.D, p.vec, lane);
+            in.x.fill_each(p.x, p.xs, t, block, own, p.D, lane);
+            in.d.fill_each(q.d_o, q.dos, t, block, own, p.D, lane);
+            in.z.fill_each(p.decay, p.gs, t, block, own, p.D, lane);
+            if constexpr (BETA) in.y[0].fill_each(p.beta, p.bs, t, block, own, p.D, lane);
         }
     }
 
@@ -159,7 +174,7 @@ struct Backward {
             if (PLAIN || (tok.own >> k & 1u))
                 h = fma2(held.a[k], h, scaled<BETA, MODE>(in.x.at(k, lane), held.n[k], held.i[k]));
         }
-        const bool ok0 = c < p.D, ok1 = c + 1 < p.D;
+        const int first = c - 2 * lane, n_row = p.D - first;  // of the block's channels
 #pragma unroll
         for (int k = kTokens - 1; k >= 0; --k) {
             if (!PLAIN && !(tok.own >> k & 1u)) continue;  // hands c on
@@ -190,14 +205,14 @@ struct Backward {
                 dy = w * x;
                 if (p.sigmoid) dy = dy * fma2(i, -i, i);
             }
-            if (PLAIN && p.wide) {
+            if (PLAIN && WIDE) {
                 in.x.v[k][lane] = pack<TA>(dx);
                 in.z.v[k][lane] = pack<TG>(d);
                 if constexpr (BETA) in.y[0].v[k][lane] = pack<TG>(dy);
-            } else if (ok0) {
-                store_pair<TA>(static_cast<TA *>(q.dx) + (t + k) * q.dxs + c, dx, p.vec, ok1);
-                store_pair<TG>(static_cast<TG *>(q.dg) + (t + k) * q.dgs + c, d, p.vec, ok1);
-                if constexpr (BETA) store_pair<TG>(static_cast<TG *>(q.db) + (t + k) * q.dbs + c, dy, p.vec, ok1);
+            } else {
+                store_row<TA>(static_cast<TA *>(q.dx) + (t + k) * q.dxs + first, dx, lane, n_row);
+                store_row<TG>(static_cast<TG *>(q.dg) + (t + k) * q.dgs + first, d, lane, n_row);
+                if constexpr (BETA) store_row<TG>(static_cast<TG *>(q.db) + (t + k) * q.dbs + first, dy, lane, n_row);
             }
             if (!PLAIN && (tok.first >> k & 1u)) {
                 const int row = __shfl_sync(0xffffffffu, tok.row, k);
@@ -205,13 +220,13 @@ struct Backward {
                 dc = splat(0.f);
             }
         }
-        if (PLAIN && p.wide) {
+        if (PLAIN && WIDE) {
             ptx::fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-                ptx::tma_store_2d(&m.dx, c, t, &in.x.v[0][0]);
-                ptx::tma_store_2d(&m.dz, c, t, &in.z.v[0][0]);
-                if constexpr (BETA) ptx::tma_store_2d(&m.dy, c, t, &in.y[0].v[0][0]);
+                ptx::tma_store_2d(&m.dx, c, t, in.x.v);
+                ptx::tma_store_2d(&m.dz, c, t, in.z.v);
+                if constexpr (BETA) ptx::tma_store_2d(&m.dy, c, t, in.y[0].v);
                 ptx::bulk_commit();
             }
         }
@@ -238,7 +253,7 @@ struct Backward {
         Tokens tok = {}, next = {};
         if (steps > 0) {
             tok = look_up(p, at.lo, at.hi, t, kTokens, lane, seen);
-            fill(q, m, s.in[warp][0], &r.bar[warp][0], t, block, tok.own, lane);
+            fill(q, m, s.in[warp][0], &r.bar[warp][0], t, window, block, tok.own, lane);
         }
         float2 bias = splat(0.f), scale = bias;
         if (RAW) bias = load_state(p.bias, c, p.D), scale = load_state(p.scale, c, p.D);
@@ -250,19 +265,19 @@ struct Backward {
         for (int turn = 0; turn < steps; ++turn, t -= window) {
             const int stage = turn % kRing;
             Input &in = s.in[warp][stage];
-            if (kRing == 2 && turn + 1 < steps) {
+            if (kRing == 2 && WIDE && turn + 1 < steps) {
                 next = look_up(p, at.lo, at.hi, t - window, kTokens, lane, seen);
                 if (lane == 0) ptx::bulk_wait_read();  // the other stage's gradients have left it
                 __syncwarp();
-                fill(q, m, s.in[warp][stage ^ 1], &r.bar[warp][stage ^ 1], t - window, block, next.own, lane);
+                fill(q, m, s.in[warp][stage ^ 1], &r.bar[warp][stage ^ 1], t - window, window, block, next.own, lane);
             }
-            if (kRing == 1 && turn + 1 < steps && p.wide && lane == 0) prefetch(m, t - window, block);
+            if (kRing == 1 && turn + 1 < steps && WIDE && lane == 0) prefetch(m, t - window, block);
             // the state that the forward pass kept before the tile, early
             const int tile = t - warp * kTokens, ch = block * 64 + (threadIdx.x & 63);
             float kept = 0.f;
             if (tile < at.hi && ch < p.D)
                 kept = p.chunk[(size_t)(tile / kChunk) * p.D + ch];
-            if (p.wide) {
+            if (WIDE) {
                 if (!ptx::mbar_wait(&r.bar[warp][stage], turn / kRing & 1) && p.err) atomicOr(p.err, kErrTimeout);
             } else {
                 __syncwarp();
@@ -291,11 +306,11 @@ struct Backward {
             const float2 h = *reinterpret_cast<const float2 *>(&r.h[warp][2 * lane]);
             if (plain) second_walk<true>(q, m, in, tok, t, c, lane, scale, held, h, dc, sums);
             else second_walk<false>(q, m, in, tok, t, c, lane, scale, held, h, dc, sums);
-            if (kRing == 1 && turn + 1 < steps) {
+            if ((kRing == 1 || !WIDE) && turn + 1 < steps) {
                 next = look_up(p, at.lo, at.hi, t - window, kTokens, lane, seen);
                 if (lane == 0) ptx::bulk_wait_read();
                 __syncwarp();
-                fill(q, m, in, &r.bar[warp][0], t - window, block, next.own, lane);
+                fill(q, m, s.in[warp][(turn + 1) % kRing], &r.bar[warp][0], t - window, window, block, next.own, lane);
             }
             tok = next;
         }
@@ -335,18 +350,18 @@ struct Backward {
     }
 };
 
-template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
+template <bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
 __global__ void __launch_bounds__(kWarps * 32, 2) scan_grad_kernel(const __grid_constant__ GradArgs q,
                                                                   const __grid_constant__ GradMaps m) {
-    using G = Backward<TA, TG, RAW, BETA, MODE>;
+    using G = Backward<WIDE, TA, TG, RAW, BETA, MODE>;
     extern __shared__ __align__(128) unsigned char smem[];
     G::run(q, m, *reinterpret_cast<typename G::Shared *>(smem));
 }
 
-template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
+template <bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
 cudaError_t launch_grad_one(const GradArgs &args, cudaStream_t stream) {
-    using G = Backward<TA, TG, RAW, BETA, MODE>;
-    auto kernel = scan_grad_kernel<TA, TG, RAW, BETA, MODE>;
+    using G = Backward<WIDE, TA, TG, RAW, BETA, MODE>;
+    auto kernel = scan_grad_kernel<WIDE, TA, TG, RAW, BETA, MODE>;
     GradArgs q = args;
     const Args &p = q.f;
     const int cb = (p.D + 63) / 64;
@@ -357,31 +372,31 @@ cudaError_t launch_grad_one(const GradArgs &args, cudaStream_t stream) {
     share_out(q.f, S, G::kTile);
     GradMaps m = {};
     constexpr int ta = type_of<TA>(), tg = type_of<TG>(), n = G::kTokens;
-    if (p.wide && !(make_token_map(&m.x, p.x, ta, p.xs, p.D, p.T, n) &&
+    if (WIDE && !(make_token_map(&m.x, p.x, ta, p.xs, p.D, p.T, n) &&
                     make_token_map(&m.d, q.d_o, ta, q.dos, p.D, p.T, n) &&
                     make_token_map(&m.z, p.decay, tg, p.gs, p.D, p.T, n) &&
                     make_token_map(&m.dx, q.dx, ta, q.dxs, p.D, p.T, n) &&
                     make_token_map(&m.dz, q.dg, tg, q.dgs, p.D, p.T, n) &&
                     (!BETA || (make_token_map(&m.y, p.beta, tg, p.bs, p.D, p.T, n) &&
                                make_token_map(&m.dy, q.db, tg, q.dbs, p.D, p.T, n)))))
-        q.f.wide = 0;
+        return cudaErrorInvalidValue;
     return launch_clusters(cb, S, sizeof(typename G::Shared), stream, kernel, q, m);
 }
 
-template <typename TA, typename TG, bool RAW, bool BETA>
+template <bool WIDE, typename TA, typename TG, bool RAW, bool BETA>
 cudaError_t launch_grad_mode(const GradArgs &q, cudaStream_t stream) {
-    if (q.f.mode == kNone) return launch_grad_one<TA, TG, RAW, BETA, kNone>(q, stream);
-    if (q.f.mode == kLerp) return launch_grad_one<TA, TG, RAW, BETA, kLerp>(q, stream);
-    return launch_grad_one<TA, TG, RAW, BETA, kUnit>(q, stream);
+    if (q.f.mode == kNone) return launch_grad_one<WIDE, TA, TG, RAW, BETA, kNone>(q, stream);
+    if (q.f.mode == kLerp) return launch_grad_one<WIDE, TA, TG, RAW, BETA, kLerp>(q, stream);
+    return launch_grad_one<WIDE, TA, TG, RAW, BETA, kUnit>(q, stream);
 }
 
-template <typename TA, typename TG>
+template <bool WIDE, typename TA, typename TG>
 cudaError_t launch_grad_types(const GradArgs &q, cudaStream_t stream) {
     if (q.f.bias)
-        return q.f.beta ? launch_grad_mode<TA, TG, true, true>(q, stream)
-                        : launch_grad_mode<TA, TG, true, false>(q, stream);
-    return q.f.beta ? launch_grad_mode<TA, TG, false, true>(q, stream)
-                    : launch_grad_mode<TA, TG, false, false>(q, stream);
+        return q.f.beta ? launch_grad_mode<WIDE, TA, TG, true, true>(q, stream)
+                        : launch_grad_mode<WIDE, TA, TG, true, false>(q, stream);
+    return q.f.beta ? launch_grad_mode<WIDE, TA, TG, false, true>(q, stream)
+                    : launch_grad_mode<WIDE, TA, TG, false, false>(q, stream);
 }
 
 }  // namespace scan

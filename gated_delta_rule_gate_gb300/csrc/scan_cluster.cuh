@@ -47,35 +47,95 @@ __device__ __forceinline__ float2 fold(float2 k, float2 r) {
 
 // ---------------------------------------------------------------- staging
 // A warp's tokens of one tensor wait in shared memory of its own: TOKENS rows of 64
-// channels, one box of a tensor map, which completes on the warp's mbarrier.  (By
-// cp.async, 16 bytes a lane, a warp was held up 160 cycles a copy on the way.)
-// Without a tensor map -- rows that do not begin on 16-byte addresses -- the lanes
-// load their channels and store them here.
+// channels.  Rows that begin on 16-byte addresses are one box of a tensor map, which
+// completes on the warp's mbarrier (by cp.async, 16 bytes a lane, a warp was held up
+// 160 cycles a copy).  Others are read by 4-byte words, which are shifted together
+// where a 16-bit row begins between two words, after a prefetch to L2 a window
+// earlier; tiles whose words would reach past the tensor's ends, channel by channel.
+// (Bulk copies of the words of 16 bytes that such rows touch, shifted when they are
+// read, were slower: 250 us for 16384 x 2046 bf16.)
 template <typename T, int TOKENS>
 struct alignas(128) Stage {
+    static constexpr int kRow = 64 * (int)sizeof(T);
+    static constexpr uint32_t kBytes = TOKENS * kRow;
     pair_t<T> v[TOKENS][32];
-    static constexpr uint32_t kBytes = TOKENS * 64 * sizeof(T);
 
     __device__ __forceinline__ void fill(const CUtensorMap &map, int t, int block, uint64_t *bar) {
-        ptx::tma_load_2d(&v[0][0], &map, block * 64, t, bar);
+        ptx::tma_load_2d(v, &map, block * 64, t, bar);
     }
     static __device__ __forceinline__ void prefetch(const CUtensorMap &map, int t, int block) {
         ptx::tma_prefetch_2d(&map, block * 64, t);
     }
-    __device__ __forceinline__ void fill_plain(const void *base, int64_t stride, int t, int block, unsigned own, int D,
-                                               bool vec, int lane) {
+    // Token t + lane's row on its way to L2.
+    static __device__ __forceinline__ void prefetch_row(const void *base, int64_t stride, int t, int end, int block,
+                                                        int D, int lane) {
+        const char *row = static_cast<const char *>(base) + ((int64_t)(t + lane) * stride + block * 64) * (int)sizeof(T);
+        const int left = (D - block * 64) * (int)sizeof(T);
+        if (lane >= TOKENS || t + lane >= end || left <= 0) return;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
+        if (left > 128 && kRow > 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 128));
+    }
+    __device__ __forceinline__ void fill_words(const void *base, int64_t stride, int t, int block, unsigned own, int D,
+                                               int lane) {
+        const T *row = static_cast<const T *>(base) + (int64_t)t * stride + block * 64;
+        const int n = D - block * 64 < 64 ? D - block * 64 : 64;
+        pair_t<T> r[TOKENS];  // all on their way before the first is stored
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int k = 0; k < TOKENS; ++k) {
+                const bool on = own >> k & 1u;
+                r[k].x = on && 2 * lane < n ? __ldg(row + k * stride + 2 * lane) : 0.f;
+                r[k].y = on && 2 * lane + 1 < n ? __ldg(row + k * stride + 2 * lane + 1) : 0.f;
+            }
+        } else {
+            const uintptr_t first = reinterpret_cast<uintptr_t>(row);
+            const bool odd = stride & 1;
+            if (!odd && !(first & 2u)) {  // no row begins between words
+#pragma unroll
+                for (int k = 0; k < TOKENS; ++k) {
+                    const bool on = own >> k & 1u && 2 * lane < n;
+                    r[k] = on ? __ldg(reinterpret_cast<const uint32_t *>(row + k * stride) + lane) : 0u;
+                }
+            } else {
+                // of two rows in turn both or one; the word behind lane 31's comes with a
+                // load of its own
+                uint32_t last[TOKENS];
+#pragma unroll
+                for (int k = 0; k < TOKENS; ++k) {
+                    const bool split = ((first >> 1) + (odd ? k : 0)) & 1u, on = own >> k & 1u;
+                    const uint32_t *w = reinterpret_cast<const uint32_t *>(row + k * stride - (split ? 1 : 0)) + lane;
+                    r[k] = on && 2 * lane < n + (split ? 1 : 0) ? __ldg(w) : 0u;
+                    last[k] = on && split && lane == 31 && n == 64 ? __ldg(w + 1) : 0u;
+                }
+#pragma unroll
+                for (int k = 0; k < TOKENS; ++k) {
+                    const bool split = ((first >> 1) + (odd ? k : 0)) & 1u;
+                    const uint32_t next = __shfl_down_sync(0xffffffffu, r[k], 1);
+                    if (split) r[k] = __funnelshift_r(r[k], lane == 31 ? last[k] : next, 16);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < TOKENS; ++k) v[k][lane] = r[k];
+    }
+    __device__ __forceinline__ void fill_each(const void *base, int64_t stride, int t, int block, unsigned own, int D,
+                                              int lane) {
         const int c = block * 64 + 2 * lane;
         const T *p = static_cast<const T *>(base) + (int64_t)t * stride + c;
         if (c >= D) own = 0u;
-        pair_t<T> r[TOKENS];  // all on their way before the first is stored
+        pair_t<T> r[TOKENS];
 #pragma unroll
         for (int k = 0; k < TOKENS; ++k)
-            r[k] = (own >> k & 1u) ? load_pair<T>(p + k * stride, vec, c + 1 < D) : zero_pair<T>();
+            r[k] = (own >> k & 1u) ? load_pair<T>(p + k * stride, c + 1 < D) : zero_pair<T>();
 #pragma unroll
         for (int k = 0; k < TOKENS; ++k) v[k][lane] = r[k];
     }
     __device__ __forceinline__ float2 at(int k, int lane) const { return unpack<T>(v[k][lane]); }
 };
+// Whether the words that a tile's rows touch lie inside the tensor.
+__device__ __forceinline__ bool inside(const Args &p, int t, int tokens, int block) {
+    return !(t == 0 && block == 0) && !(t + tokens >= p.T && (block + 1) * 64 >= p.D);
+}
 
 // [rows, channels] of elements of type T, boxes of 64 channels x `tokens` rows.
 bool make_token_map(CUtensorMap *m, const void *base, int type, int64_t stride, int channels, int rows, int tokens);

@@ -43,7 +43,7 @@ struct Maps {
     CUtensorMap x, z, y, o;
 };
 
-template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
+template <bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
 struct Forward {
     static constexpr int kTokens = sizeof(TA) == 2 ? 16 : 8;
     static constexpr int kTile = kWarps * kTokens;
@@ -60,20 +60,30 @@ struct Forward {
         uint64_t bar[kWarps];
     };
 
-    // The warp's tokens t, ... on their way to its stage.
-    static __device__ __forceinline__ void fill(const Args &p, const Maps &m, Input &in, uint64_t *bar, int t, int block,
-                                                unsigned own, int lane) {
-        if (p.wide) {
+    // The warp's tokens t, ... to its stage, by the asynchronous copies of WIDE rows on
+    // their way there; otherwise the tokens of the window after on their way to L2.
+    static __device__ __forceinline__ void fill(const Args &p, const Maps &m, Input &in, uint64_t *bar, int t, int window,
+                                                int block, unsigned own, int lane) {
+        if (WIDE) {
             if (lane == 0) {
                 ptx::mbar_arrive_expect_tx(bar, sizeof(Input));
                 in.x.fill(m.x, t, block, bar);
                 in.z.fill(m.z, t, block, bar);
                 if constexpr (BETA) in.y[0].fill(m.y, t, block, bar);
             }
+            return;
+        }
+        in.x.prefetch_row(p.x, p.xs, t + window, p.T, block, p.D, lane);
+        in.z.prefetch_row(p.decay, p.gs, t + window, p.T, block, p.D, lane);
+        if constexpr (BETA) in.z.prefetch_row(p.beta, p.bs, t + window, p.T, block, p.D, lane);
+        if (inside(p, t, kTokens, block)) {
+            in.x.fill_words(p.x, p.xs, t, block, own, p.D, lane);
+            in.z.fill_words(p.decay, p.gs, t, block, own, p.D, lane);
+            if constexpr (BETA) in.y[0].fill_words(p.beta, p.bs, t, block, own, p.D, lane);
         } else {
-            in.x.fill_plain(p.x, p.xs, t, block, own, p.D, p.vec, lane);
-            in.z.fill_plain(p.decay, p.gs, t, block, own, p.D, p.vec, lane);
-            if constexpr (BETA) in.y[0].fill_plain(p.beta, p.bs, t, block, own, p.D, p.vec, lane);
+            in.x.fill_each(p.x, p.xs, t, block, own, p.D, lane);
+            in.z.fill_each(p.decay, p.gs, t, block, own, p.D, lane);
+            if constexpr (BETA) in.y[0].fill_each(p.beta, p.bs, t, block, own, p.D, lane);
         }
     }
 
@@ -108,12 +118,11 @@ struct Forward {
     // o of the warp's tokens, which a plain run hands to an asynchronous copy.
     template <bool PLAIN>
     static __device__ __forceinline__ void second_walk(const Args &p, const Maps &m, Stage<TA, kTokens> &out,
-                                                       const Tokens &tok, int t, int c, int lane,
+                                                       const Tokens &tok, int t, int block, int lane,
                                                        const float2 (&a)[kTokens], const float2 (&u)[kTokens],
                                                        float2 h) {
-        TA *o = static_cast<TA *>(p.o) + (int64_t)t * p.os + c;
-        const bool ok0 = c < p.D, ok1 = c + 1 < p.D;
-        if (PLAIN && p.wide) {
+        const int c = block * 64 + 2 * lane;
+        if (PLAIN && WIDE) {
             if (lane == 0) ptx::bulk_wait_read();  // the last copy has left the stage
             __syncwarp();
 #pragma unroll
@@ -124,16 +133,18 @@ struct Forward {
             ptx::fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-                ptx::tma_store_2d(&m.o, c, t, &out.v[0][0]);
+                ptx::tma_store_2d(&m.o, c, t, out.v);
                 ptx::bulk_commit();
             }
             return;
         }
+        TA *o = static_cast<TA *>(p.o) + (int64_t)t * p.os + block * 64;
+        const int n = p.D - block * 64;
 #pragma unroll
         for (int k = 0; k < kTokens; ++k) {
-            h = tok.first >> k & 1u ? u[k] : fma2(a[k], h, u[k]);
-            if ((tok.own >> k & 1u) && ok0) store_pair<TA>(o + k * p.os, h, p.vec, ok1);
-            if ((tok.last >> k & 1u) && p.fin) {
+            h = !PLAIN && (tok.first >> k & 1u) ? u[k] : fma2(a[k], h, u[k]);
+            if (PLAIN || (tok.own >> k & 1u)) store_row<TA>(o + k * p.os, h, lane, n);
+            if (!PLAIN && (tok.last >> k & 1u) && p.fin) {
                 const int row = __shfl_sync(0xffffffffu, tok.row, k);
                 store_state(p.fin + (size_t)row * p.D, c, p.D, h);
             }
@@ -158,7 +169,7 @@ struct Forward {
         ptx::grid_wait();
         Seen seen;
         Tokens tok = look_up(p, at.lo, at.hi, t, kTokens, lane, seen);
-        if (steps > 0) fill(p, m, in, bar, t, block, tok.own, lane);
+        if (steps > 0) fill(p, m, in, bar, t, window, block, tok.own, lane);
         float2 bias = splat(0.f), scale = bias;
         if (RAW) bias = load_state(p.bias, c, p.D), scale = load_state(p.scale, c, p.D);
         if (at.size > 1) exchange_init(s.x);
@@ -170,7 +181,7 @@ struct Forward {
             float2 a[kTokens], u[kTokens];
             const Tokens now = tok;
             const bool plain = now.own == kAll && !(now.first | now.last);
-            if (p.wide) {
+            if (WIDE) {
                 if (!ptx::mbar_wait(bar, par) && p.err) atomicOr(p.err, kErrTimeout);
             } else {
                 __syncwarp();
@@ -183,15 +194,17 @@ struct Forward {
             const float2 tile = meet.send(s.meet, s.x, at, step);
             if (step + 1 < steps) {  // while the maps are on their way
                 tok = look_up(p, at.lo, at.hi, t + window, kTokens, lane, seen);
-                fill(p, m, in, bar, t + window, block, tok.own, lane);
+                if (WIDE) fill(p, m, in, bar, t + window, window, block, tok.own, lane);
             }
             meet.receive(s.meet, s.x, at, step, tile, carry, p.err);
             __syncthreads();
             const float2 h = *reinterpret_cast<const float2 *>(&s.meet.h[warp][2 * lane]);
             if (p.chunk && t % kChunk == 0 && t >= at.lo && t < at.hi)
                 store_state(p.chunk + (size_t)(t / kChunk) * p.D, c, p.D, h);
-            if (plain) second_walk<true>(p, m, s.out[warp], now, t, c, lane, a, u, h);
-            else second_walk<false>(p, m, s.out[warp], now, t, c, lane, a, u, h);
+            if (plain) second_walk<true>(p, m, s.out[warp], now, t, block, lane, a, u, h);
+            else second_walk<false>(p, m, s.out[warp], now, t, block, lane, a, u, h);
+            // through registers, which a and u have left
+            if (!WIDE && step + 1 < steps) fill(p, m, in, bar, t + window, window, block, tok.own, lane);
         }
         if (lane == 0) ptx::bulk_wait();
         if (at.size > 1) {  // no block leaves while another may still send to it
@@ -201,18 +214,18 @@ struct Forward {
     }
 };
 
-template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
+template <bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
 __global__ void __launch_bounds__(kWarps * 32, 2) scan_kernel(const __grid_constant__ Args p,
                                                              const __grid_constant__ Maps m) {
-    using F = Forward<TA, TG, RAW, BETA, MODE>;
+    using F = Forward<WIDE, TA, TG, RAW, BETA, MODE>;
     extern __shared__ __align__(128) unsigned char smem[];
     F::run(p, m, *reinterpret_cast<typename F::Shared *>(smem));
 }
 
-template <typename TA, typename TG, bool RAW, bool BETA, int MODE>
+template <bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
 cudaError_t launch_one(const Args &p, cudaStream_t stream) {
-    using F = Forward<TA, TG, RAW, BETA, MODE>;
-    auto kernel = scan_kernel<TA, TG, RAW, BETA, MODE>;
+    using F = Forward<WIDE, TA, TG, RAW, BETA, MODE>;
+    auto kernel = scan_kernel<WIDE, TA, TG, RAW, BETA, MODE>;
     const int cb = (p.D + 63) / 64;
     int S = 1;
     const cudaError_t e =
@@ -221,26 +234,26 @@ cudaError_t launch_one(const Args &p, cudaStream_t stream) {
     Maps m = {};
     Args q = p;
     share_out(q, S, F::kTile);
-    if (q.wide && !(make_token_map(&m.x, p.x, type_of<TA>(), p.xs, p.D, p.T, F::kTokens) &&
-                    make_token_map(&m.z, p.decay, type_of<TG>(), p.gs, p.D, p.T, F::kTokens) &&
-                    (!BETA || make_token_map(&m.y, p.beta, type_of<TG>(), p.bs, p.D, p.T, F::kTokens)) &&
-                    make_token_map(&m.o, p.o, type_of<TA>(), p.os, p.D, p.T, F::kTokens)))
-        q.wide = 0;
+    if (WIDE && !(make_token_map(&m.x, p.x, type_of<TA>(), p.xs, p.D, p.T, F::kTokens) &&
+                  make_token_map(&m.z, p.decay, type_of<TG>(), p.gs, p.D, p.T, F::kTokens) &&
+                  (!BETA || make_token_map(&m.y, p.beta, type_of<TG>(), p.bs, p.D, p.T, F::kTokens)) &&
+                  make_token_map(&m.o, p.o, type_of<TA>(), p.os, p.D, p.T, F::kTokens)))
+        return cudaErrorInvalidValue;
     return launch_clusters(cb, S, sizeof(typename F::Shared), stream, kernel, q, m);
 }
 
-template <typename TA, typename TG, bool RAW, bool BETA>
+template <bool WIDE, typename TA, typename TG, bool RAW, bool BETA>
 cudaError_t launch_mode(const Args &p, cudaStream_t stream) {
-    if (p.mode == kNone) return launch_one<TA, TG, RAW, BETA, kNone>(p, stream);
-    if (p.mode == kLerp) return launch_one<TA, TG, RAW, BETA, kLerp>(p, stream);
-    return launch_one<TA, TG, RAW, BETA, kUnit>(p, stream);
+    if (p.mode == kNone) return launch_one<WIDE, TA, TG, RAW, BETA, kNone>(p, stream);
+    if (p.mode == kLerp) return launch_one<WIDE, TA, TG, RAW, BETA, kLerp>(p, stream);
+    return launch_one<WIDE, TA, TG, RAW, BETA, kUnit>(p, stream);
 }
 
-template <typename TA, typename TG>
+template <bool WIDE, typename TA, typename TG>
 cudaError_t launch_types(const Args &p, cudaStream_t stream) {
     if (p.bias)
-        return p.beta ? launch_mode<TA, TG, true, true>(p, stream) : launch_mode<TA, TG, true, false>(p, stream);
-    return p.beta ? launch_mode<TA, TG, false, true>(p, stream) : launch_mode<TA, TG, false, false>(p, stream);
+        return p.beta ? launch_mode<WIDE, TA, TG, true, true>(p, stream) : launch_mode<WIDE, TA, TG, true, false>(p, stream);
+    return p.beta ? launch_mode<WIDE, TA, TG, false, true>(p, stream) : launch_mode<WIDE, TA, TG, false, false>(p, stream);
 }
 
 }  // namespace scan

@@ -1,11 +1,11 @@
-// scan_grad_bf16.cu -- gdn_scan_backward for bf16 activations.
+// scan_grad_bf16.cu -- gdn_scan_backward for bf16 activations, rows on 16-byte addresses.
 #include "scan_bwd.cuh"
 
 namespace gdn {
 namespace scan {
 
 cudaError_t launch_grad_bf16(const GradArgs &p, bool gate_f32, cudaStream_t stream) {
-    return gate_f32 ? launch_grad_types<__nv_bfloat16, float>(p, stream) : launch_grad_types<__nv_bfloat16, __nv_bfloat16>(p, stream);
+    return gate_f32 ? launch_grad_types<true, __nv_bfloat16, float>(p, stream) : launch_grad_types<true, __nv_bfloat16, __nv_bfloat16>(p, stream);
 }
 
 }  // namespace scan
