@@ -526,8 +526,9 @@ gdn_status gdn_rmsnorm_backward(const gdn_rmsnorm_grad_args *args, void *workspa
  * The arrays grads, outs, sizes and dtypes are HOST memory, read before the call
  * returns: device pointers, element counts (0: skipped) and gdn_dtypes (F32, F16,
  * BF16; an output has its gradient's).  outs[i] may be grads[i] (outs NULL: all in
- * place); a tensor in place is written only if it is scaled.  The sum is fp32 in
- * a fixed order (joined in 64 bits): the same bits on every run.  norm is a device
+ * place); a tensor in place is written only if it is scaled.  The squares and a
+ * block's sum are fp32, joined in pairs of fp32, in a fixed order: the same bits on
+ * every run (a norm above 1.8e19 counts as infinite).  norm is a device
  * float (or NULL).  A norm that is not finite scales nothing and sets
  * GDN_DEVERR_NONFINITE.  The workspace is device memory of
  * gdn_grad_clip_workspace_size() bytes, 16-byte aligned.

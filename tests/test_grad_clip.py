@@ -78,6 +78,22 @@ def test_parts_of_a_buffer_and_odd_addresses():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_gradient_and_result_at_any_address(dt):
+    """Every pair of offsets from a 16-byte address, shorter than a word and longer."""
+    import gated_delta_rule_gate_gb300 as g
+    for n in (1, 5, 8, 15, 9001):
+        for a in range(8):
+            for b in (0, a, (a + 3) % 8):
+                flat = draw(n + a, [n + 16], (dt,))[0]
+                out = torch.full_like(flat, 7.0)
+                bound = 0.3 * norm_of([flat[a:a + n]])
+                norm = g.gdn_grad_clip([flat[a:a + n]], bound, out=[out[b:b + n]])
+                check([out[b:b + n]], [flat[a:a + n]], norm, bound)
+                assert bool((out[:b] == 7.0).all()) and bool((out[b + n:] == 7.0).all())
+
+
+@pytest.mark.gpu
 def test_norms_that_are_zero_or_not_finite():
     import gated_delta_rule_gate_gb300 as g
     zero = [torch.zeros(100, device="cuda")]
