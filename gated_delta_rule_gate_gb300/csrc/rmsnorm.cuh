@@ -1,8 +1,16 @@
 // rmsnorm.cuh -- gdn_rmsnorm and its gradient: the kernels.
 //
-// A block takes a row, a thread N groups of V adjacent values of it, which stay in
-// registers from the load to the store: every tensor crosses HBM once.  Rows that
-// do not fit (more than kFit values) are walked a second time instead.
+// r = x + residual, y = r rsqrt(mean(r^2) + eps) weight.  A block takes a row, a
+// thread N groups of V adjacent values of it, which stay in registers from the load
+// to the store: every tensor crosses HBM once, and HBM is the bound.  One row to a
+// block needs no loop and no wait between rows; the blocks of an SM overlap one
+// another's sums.  The scale of a whole row needs max |r weight| before the row's
+// rstd is known, so both reductions are one: |y| is that times rstd >= 0.
+// Rows that do not fit (more than kFit values, or 16384 in words of 8) are walked a
+// second time instead.
+//
+// 16384 x 4096 bf16, residual, e4m3 by groups of 128: 112 us, 6.6 TB/s of 6.8.
+// 256 x 2048: 5.5 us, a launch and two trips to memory.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -41,33 +49,36 @@ __device__ __forceinline__ void block_sum_max(float &a, float &b, float *s) {
     }
 }
 
+// Columns c, ... of a row (or the weight) in fp32 or TA.
 template <typename TA, int V>
-__device__ __forceinline__ void load_as(const void *p, bool f32, size_t at, float (&v)[V]) {
-    if (f32) load_values<float, V>(static_cast<const float *>(p) + at, v);
-    else load_values<TA, V>(static_cast<const TA *>(p) + at, v);
+__device__ __forceinline__ void load_as(const void *p, bool f32, size_t row, int c, int n, float (&v)[V]) {
+    if (f32) load_columns<float, V>(static_cast<const float *>(p) + row, c, n, v);
+    else load_columns<TA, V>(static_cast<const TA *>(p) + row, c, n, v);
 }
 template <typename TA, int V>
-__device__ __forceinline__ void store_as(void *p, bool f32, size_t at, const float (&v)[V]) {
-    if (f32) store_values<float, V>(static_cast<float *>(p) + at, v);
-    else store_values<TA, V>(static_cast<TA *>(p) + at, v);
+__device__ __forceinline__ void store_as(void *p, bool f32, size_t row, int c, int n, const float (&v)[V]) {
+    if (f32) store_columns<float, V>(static_cast<float *>(p) + row, c, n, v);
+    else store_columns<TA, V>(static_cast<TA *>(p) + row, c, n, v);
 }
 
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+// Columns c, ... of a row of n bytes.
 template <int V>
-__device__ __forceinline__ void store_e4m3(unsigned char *p, const float (&v)[V], float inv) {
+__device__ __forceinline__ void store_e4m3(unsigned char *row, int c, int n, const float (&v)[V], float inv) {
+    if (c >= n) return;
     if constexpr (V == 1) {
-        *p = __nv_cvt_float_to_fp8(v[0] * inv, __NV_SATFINITE, __NV_E4M3);
+        row[c] = __nv_cvt_float_to_fp8(v[0] * inv, __NV_SATFINITE, __NV_E4M3);
+    } else if constexpr (V == 2) {
+        *reinterpret_cast<uint16_t *>(row + c) = (uint16_t)e4m3_pair(v[0] * inv, v[1] * inv);
     } else {
         uint32_t w[V / 4];
 #pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i] * inv, v[4 * i + 1] * inv),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2] * inv, v[4 * i + 3] * inv),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            w[i] = lo | hi << 16;
-        }
-        if constexpr (V == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
-        else *reinterpret_cast<uint32_t *>(p) = w[0];
+        for (int i = 0; i < V / 4; ++i)
+            w[i] = e4m3_pair(v[4 * i] * inv, v[4 * i + 1] * inv) | e4m3_pair(v[4 * i + 2] * inv, v[4 * i + 3] * inv) << 16;
+        if constexpr (V == 8) *reinterpret_cast<uint2 *>(row + c) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t *>(row + c) = w[0];
     }
 }
 // Scale of a row or group whose largest |y| is m, and its reciprocal.
@@ -77,107 +88,147 @@ __device__ __forceinline__ float scale_of(float m, float &inv) {
     return m / kE4m3Max;
 }
 
-// Loads r = x + residual of V values at column c.
-template <typename TA, int V>
-__device__ __forceinline__ void load_r(const Args &p, size_t row, int c, float (&r)[V]) {
-    load_values<TA, V>(static_cast<const TA *>(p.x) + row * p.xs + c, r);
-    if (p.res) {
-        float q[V];
-        load_as<TA, V>(p.res, p.res_f32, row * p.D + c, q);
+// N times V columns of a row in fp32 or TA, all on their way before the first is
+// looked at; `column(i)` gives the i-th's first.
+template <typename TA, int V, int N, typename C>
+__device__ __forceinline__ void load_row(const void *p, bool f32, size_t row, int n, C column, float (&v)[N][V]) {
+    if (f32) {
+        Columns<float, V> q[N];
+        const float *r = static_cast<const float *>(p) + row;
 #pragma unroll
-        for (int v = 0; v < V; ++v) r[v] += q[v];
+        for (int i = 0; i < N; ++i) q[i].load(r, column(i), n);
+#pragma unroll
+        for (int i = 0; i < N; ++i) q[i].get(v[i]);
+    } else {
+        Columns<TA, V> q[N];
+        const TA *r = static_cast<const TA *>(p) + row;
+#pragma unroll
+        for (int i = 0; i < N; ++i) q[i].load(r, column(i), n);
+#pragma unroll
+        for (int i = 0; i < N; ++i) q[i].get(v[i]);
+    }
+}
+// r = x + residual.
+template <typename TA, int V, int N, typename C>
+__device__ __forceinline__ void load_sum(const Args &p, size_t row, C column, float (&v)[N][V]) {
+    Columns<TA, V> x[N];
+    const TA *r = static_cast<const TA *>(p.x) + row * p.xs;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i].load(r, column(i), p.D);
+    float q[N][V];
+    if (p.res) {
+        load_row<TA, V, N>(p.res, p.res_f32, row * p.D, p.D, column, q);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int k = 0; k < V; ++k) q[i][k] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i].get(v[i]);
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[i][k] += q[i][k];
     }
 }
 
+// V: 8 or 4, words of 16 bytes; 2, rows whose values pair up; 1, rows at any alignment.
+// 16384 rows of bf16 with a residual and scales by group: 2048 wide (V = 8) 49 us,
+// 2046 (V = 2) 86, against 143 by single values; 2047 (V = 1) 129; fp32 77, 84, 126.
+// Eight values a thread at every V: four at V = 1 took 142 us, with fewer bytes on
+// their way.  Rows of up to 512 words take one a thread and four blocks an SM at 32
+// registers; longer ones two.
 template <typename TA, int Q, int V, int N>
-__global__ void __launch_bounds__(1024) rmsnorm_kernel(const __grid_constant__ Args p) {
-    ptx::grid_wait();
+__global__ void __launch_bounds__(V > 2 && N == 1 ? 512 : 1024, V > 2 && N == 1 ? 4 : 1) rmsnorm_kernel(const __grid_constant__ Args p) {
     __shared__ float s_red[64];
-    extern __shared__ int s_peak[];  // V == 1: the largest |y| of each group, as bits
+    extern __shared__ int s_peak[];  // V <= 2: the largest |y| of each group, as bits
+    ptx::grid_wait();
     const size_t row = blockIdx.x;
     const int D = p.D;
-    float r[N][V], w[N][V];
+    auto column = [&](int i) { return (i * (int)blockDim.x + (int)threadIdx.x) * V; };
+    float r[N][V];
     float sum = 0.f, peak = 0.f;
+    load_sum<TA, V, N>(p, row, column, r);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
+        if (p.res_out) store_as<TA, V>(p.res_out, p.res_f32, row * D, column(i), D, r[i]);
 #pragma unroll
-        for (int v = 0; v < V; ++v) r[i][v] = w[i][v] = 0.f;
-        if (c < D) {
-            load_r<TA, V>(p, row, c, r[i]);
-            load_as<TA, V>(p.weight, p.w_f32, c, w[i]);
-        }
+        for (int v = 0; v < V; ++v) sum = fmaf(r[i][v], r[i][v], sum);
     }
+    if (Q == kRowScale) {
+        float w[N][V];
+        load_row<TA, V, N>(p.weight, p.w_f32, 0, D, column, w);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-        if (p.res_out && c < D) store_as<TA, V>(p.res_out, p.res_f32, row * D + c, r[i]);
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            sum = fmaf(r[i][v], r[i][v], sum);
-            if (Q == kRowScale) peak = fmaxf(peak, fabsf(r[i][v] * w[i][v]));
-        }
+            for (int v = 0; v < V; ++v) peak = fmaxf(peak, fabsf(r[i][v] * w[i][v]));
     }
-    if (Q == kGroupScale && V == 1) {
+    if (Q == kGroupScale && V <= 2) {
         for (int g = threadIdx.x; g < (D + kGroup - 1) / kGroup; g += blockDim.x) s_peak[g] = 0;
     }
     block_sum_max(sum, peak, s_red);
     const float rstd = rsqrtf(sum / (float)D + p.eps);
     if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+    {
+        float w[N][V];
+        load_row<TA, V, N>(p.weight, p.w_f32, 0, D, column, w);
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int v = 0; v < V; ++v) r[i][v] *= rstd * w[i][v];
+            for (int v = 0; v < V; ++v) r[i][v] *= rstd * w[i][v];
+    }
+    unsigned char *bytes = static_cast<unsigned char *>(p.out) + row * D;
     if constexpr (Q == kPlain) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-            if (c < D) store_values<TA, V>(static_cast<TA *>(p.out) + row * D + c, r[i]);
-        }
+        for (int i = 0; i < N; ++i) store_columns<TA, V>(static_cast<TA *>(p.out) + row * D, column(i), D, r[i]);
     } else if constexpr (Q == kRowScale) {
         float inv;
         const float scale = scale_of(peak * rstd, inv);
         if (threadIdx.x == 0) p.scales[row] = scale;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-            if (c < D) store_e4m3<V>(static_cast<unsigned char *>(p.out) + row * D + c, r[i], inv);
-        }
+        for (int i = 0; i < N; ++i) store_e4m3<V>(bytes, column(i), D, r[i], inv);
     } else {
         const int groups = (D + kGroup - 1) / kGroup;
-        if (V == 1) {
+        float m[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            m[i] = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) m[i] = fmaxf(m[i], fabsf(r[i][v]));
+            // of whole words the lanes of a group are part of a warp
+            constexpr int kLanes = V <= 2 ? 32 : kGroup / V;
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+        }
+        if (V <= 2) {
             if (blockDim.x <= 32) __syncwarp();
 #pragma unroll
-            for (int i = 0; i < N; ++i) {  // 32 adjacent values lie in one group
-                const int c = i * (int)blockDim.x + (int)threadIdx.x;
-                float m = fabsf(r[i][0]);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            for (int i = 0; i < N; ++i) {  // a warp's columns lie in one group
                 // numbers >= 0 order as their bits; a maximum does not depend on the order
-                if ((threadIdx.x & 31) == 0 && c < D) atomicMax(&s_peak[c / kGroup], __float_as_int(m));
+                if ((threadIdx.x & 31) == 0 && column(i) < D)
+                    atomicMax(&s_peak[column(i) / kGroup], __float_as_int(m[i]));
             }
             __syncthreads();
+#pragma unroll
+            for (int i = 0; i < N; ++i) m[i] = column(i) < D ? __int_as_float(s_peak[column(i) / kGroup]) : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-            float m = 0.f;
-            if (V == 1) {
-                if (c < D) m = __int_as_float(s_peak[c / kGroup]);
-            } else {
-#pragma unroll
-                for (int v = 0; v < V; ++v) m = fmaxf(m, fabsf(r[i][v]));
-#pragma unroll
-                for (int o = kGroup / V / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            }
+            const int c = column(i);
             float inv;
-            const float scale = scale_of(m, inv);
-            if (c < D) {
-                if (c % kGroup == 0) p.scales[row * groups + c / kGroup] = scale;
-                store_e4m3<V>(static_cast<unsigned char *>(p.out) + row * D + c, r[i], inv);
-            }
+            const float scale = scale_of(m[i], inv);
+            if (c < D && c % kGroup == 0) p.scales[row * groups + c / kGroup] = scale;
+            store_e4m3<V>(bytes, c, D, r[i], inv);
         }
     }
+}
+
+template <typename TA>
+__device__ __forceinline__ float sum_at(const Args &p, size_t row, int c) {
+    float r = static_cast<float>(static_cast<const TA *>(p.x)[row * p.xs + c]), q[1];
+    if (!p.res) return r;
+    load_as<TA, 1>(p.res, p.res_f32, row * p.D, c, p.D, q);
+    return r + q[0];
 }
 
 // Rows that do not fit in registers: x and residual are read again.  The second
@@ -191,10 +242,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_wide_kernel(const __grid_constan
     float sum = 0.f, peak = 0.f;
     for (int c = threadIdx.x; c < D; c += blockDim.x) {
         float r[1], w[1];
-        load_r<TA, 1>(p, row, c, r);
+        r[0] = sum_at<TA>(p, row, c);
         sum = fmaf(r[0], r[0], sum);
         if (Q == kRowScale) {
-            load_as<TA, 1>(p.weight, p.w_f32, c, w);
+            load_as<TA, 1>(p.weight, p.w_f32, 0, c, D, w);
             peak = fmaxf(peak, fabsf(r[0] * w[0]));
         }
     }
@@ -211,9 +262,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_wide_kernel(const __grid_constan
         const int c = base + threadIdx.x;
         float r[1] = {0.f}, w[1] = {0.f};
         if (c < D) {
-            load_r<TA, 1>(p, row, c, r);
-            load_as<TA, 1>(p.weight, p.w_f32, c, w);
-            if (p.res_out) store_as<TA, 1>(p.res_out, p.res_f32, row * D + c, r);
+            r[0] = sum_at<TA>(p, row, c);
+            load_as<TA, 1>(p.weight, p.w_f32, 0, c, D, w);
+            if (p.res_out) store_as<TA, 1>(p.res_out, p.res_f32, row * D, c, D, r);
         }
         float y[1] = {r[0] * (rstd * w[0])};
         if constexpr (Q == kPlain) {
@@ -231,7 +282,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_wide_kernel(const __grid_constan
                 const float scale = scale_of(m, inv);
                 if (c < D && c % kGroup == 0) p.scales[row * ((D + kGroup - 1) / kGroup) + c / kGroup] = scale;
             }
-            if (c < D) store_e4m3<1>(static_cast<unsigned char *>(p.out) + row * D + c, y, inv);
+            store_e4m3<1>(static_cast<unsigned char *>(p.out) + row * D, c, D, y, inv);
         }
     }
 }
@@ -242,10 +293,10 @@ inline unsigned threads_for(int groups, int n) {
 }
 
 template <typename TA, int Q>
-cudaError_t launch_out(const Args &p, bool vec, cudaStream_t stream) {
+cudaError_t launch_out(const Args &p, int width, cudaStream_t stream) {
     constexpr int V = sizeof(TA) == 4 ? 4 : 8;
     const unsigned rows = (unsigned)p.rows;
-    if (vec) {
+    if (width == V) {
         const int groups = p.D / V;
         if (groups <= 512) {
             return launch_early(rmsnorm_kernel<TA, Q, V, 1>, rows, threads_for(groups, 1), 0, stream, p);
@@ -255,23 +306,30 @@ cudaError_t launch_out(const Args &p, bool vec, cudaStream_t stream) {
         }
     }
     const size_t peaks = (size_t)((p.D + kGroup - 1) / kGroup) * sizeof(int);
-    if (p.D <= 2048) return launch_early(rmsnorm_kernel<TA, Q, 1, 4>, rows, threads_for(p.D, 4), peaks, stream, p);
-    if (p.D <= 8192) return launch_early(rmsnorm_kernel<TA, Q, 1, 8>, rows, threads_for(p.D, 8), peaks, stream, p);
+    if (p.D <= kFit && width >= 2)
+        return launch_early(rmsnorm_kernel<TA, Q, 2, 4>, rows, threads_for(p.D / 2, 4), peaks, stream, p);
+    if (p.D <= kFit) return launch_early(rmsnorm_kernel<TA, Q, 1, 8>, rows, threads_for(p.D, 8), peaks, stream, p);
     return launch_early(rmsnorm_wide_kernel<TA, Q>, rows, 1024, 0, stream, p);
 }
 
 template <typename TA>
-cudaError_t launch_rmsnorm_as(const Args &p, int q, bool vec, cudaStream_t stream) {
-    if (q == kPlain) return launch_out<TA, kPlain>(p, vec, stream);
-    if (q == kRowScale) return launch_out<TA, kRowScale>(p, vec, stream);
-    return launch_out<TA, kGroupScale>(p, vec, stream);
+cudaError_t launch_rmsnorm_as(const Args &p, int q, int width, cudaStream_t stream) {
+    if (q == kPlain) return launch_out<TA, kPlain>(p, width, stream);
+    if (q == kRowScale) return launch_out<TA, kRowScale>(p, width, stream);
+    return launch_out<TA, kGroupScale>(p, width, stream);
 }
 
 // ---------------------------------------------------------------- gradient
 // xhat = r rstd, m = mean(weight d_out xhat): dx = rstd (weight d_out - xhat m) +
-// d_residual.  A block takes rows b, b + blocks, ...; a thread has the same
-// columns of each, so that its share of d_weight stays in registers, and the next
-// row's tensors are loaded while this one's sum is formed; the blocks' shares meet in the workspace, which a second kernel adds up in their order.
+// d_residual, d_weight = sum of d_out xhat over the rows.  A block takes rows b, b +
+// blocks, ...; a thread has the same columns of each, so that its share of d_weight
+// stays in registers, and the next row's tensors are loaded while this one's sum is
+// formed.  The blocks' shares meet in the workspace, and a second kernel adds them up
+// in their order: no atomics, the same sum every time.
+//
+// Bound by HBM, and by the wait for each row's sum: forward and gradient of 16384 x
+// 4096 bf16 186 us, 5.1 TB/s; of 2046 wide by pairs 126 against 206 by single values,
+// 2048 wide 100.
 template <typename TA, typename TR, int V, int N>
 __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constant__ GradArgs p, float *partial) {
     ptx::grid_wait();
@@ -283,14 +341,14 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constan
         const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
 #pragma unroll
         for (int v = 0; v < V; ++v) w[i][v] = dw[i][v] = 0.f;
-        if (c < D) load_as<TA, V>(p.weight, p.w_f32, c, w[i]);
+        load_as<TA, V>(p.weight, p.w_f32, 0, c, D, w[i]);
     }
     // a row's tensors, on their way while the row before is reduced and written (where
     // 64 registers, of blocks of up to 1024 threads, hold both)
     constexpr bool kAhead = V * N <= 4 || (V == 8 && sizeof(TR) == 2);
     struct Row {
-        Words<TA, V> d[N];
-        Words<TR, V> r[N], g[N];
+        Columns<TA, V> d[N];
+        Columns<TR, V> r[N], g[N];
         float rstd;
     };
     auto fetch = [&](int64_t row, Row &w) {
@@ -299,16 +357,12 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-            if (c < D) {
-                w.d[i].load(static_cast<const TA *>(p.d_out) + row * p.dos + c);
-                w.r[i].load(static_cast<const TR *>(p.r) + row * D + c);
-                if (p.d_res) w.g[i].load(static_cast<const TR *>(p.d_res) + row * D + c);
-            }
+            w.d[i].load(static_cast<const TA *>(p.d_out) + row * p.dos, c, D);
+            w.r[i].load(static_cast<const TR *>(p.r) + row * D, c, D);
+            if (p.d_res) w.g[i].load(static_cast<const TR *>(p.d_res) + row * D, c, D);
         }
     };
     Row next;
-#pragma unroll
-    for (int i = 0; i < N; ++i) next.d[i].zero(), next.r[i].zero(), next.g[i].zero();
     if (kAhead) fetch(blockIdx.x, next);
     int par = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
@@ -319,6 +373,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constan
         float dot = 0.f, none = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+            const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
             now.d[i].get(d[i]);
             now.r[i].get(x[i]);
 #pragma unroll
@@ -334,18 +389,17 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-            if (c >= D) continue;
-            float g[V];
-            now.g[i].get(g);  // zeros without d_residual
+            float g[V] = {};
+            if (p.d_res) now.g[i].get(g);
 #pragma unroll
             for (int v = 0; v < V; ++v) g[v] += now.rstd * (d[i][v] - x[i][v] * m);
-            store_values<TR, V>(static_cast<TR *>(p.dx) + row * D + c, g);
+            store_columns<TR, V>(static_cast<TR *>(p.dx) + row * D, c, D, g);
         }
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int c = (i * (int)blockDim.x + (int)threadIdx.x) * V;
-        if (c < D) store_values<float, V>(partial + (size_t)blockIdx.x * p.Dp + c, dw[i]);
+        store_columns<float, V>(partial + (size_t)blockIdx.x * p.Dp, c, D, dw[i]);
     }
 }
 
@@ -358,7 +412,7 @@ __global__ void __launch_bounds__(32) rmsnorm_grad_narrow_kernel(const __grid_co
     const int c = threadIdx.x;
     const bool on = c < p.D;
     float w[1] = {0.f}, dw = 0.f;
-    if (on) load_as<TA, 1>(p.weight, p.w_f32, c, w);
+    load_as<TA, 1>(p.weight, p.w_f32, 0, c, p.D, w);
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const float rstd = p.rstd[row];
         float d = 0.f, r = 0.f;
@@ -386,7 +440,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_mean_kernel(const __grid_co
     const float rstd = p.rstd[row];
     for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
         float w[1];
-        load_as<TA, 1>(p.weight, p.w_f32, c, w);
+        load_as<TA, 1>(p.weight, p.w_f32, 0, c, p.D, w);
         const float d = static_cast<float>(static_cast<const TA *>(p.d_out)[row * p.dos + c]);
         const float r = static_cast<float>(static_cast<const TR *>(p.r)[row * p.D + c]);
         dot = fmaf(d * w[0], r * rstd, dot);
@@ -402,7 +456,7 @@ __global__ void __launch_bounds__(256) rmsnorm_grad_columns_kernel(const __grid_
     const int part = blockIdx.x / column_blocks, parts = gridDim.x / column_blocks;
     if (c >= p.D) return;
     float w[1], dw = 0.f;
-    load_as<TA, 1>(p.weight, p.w_f32, c, w);
+    load_as<TA, 1>(p.weight, p.w_f32, 0, c, p.D, w);
     for (int64_t row = part; row < p.rows; row += parts) {
         const float rstd = p.rstd[row], m = mean[row];
         const float d = static_cast<float>(static_cast<const TA *>(p.d_out)[row * p.dos + c]);
@@ -416,7 +470,7 @@ __global__ void __launch_bounds__(256) rmsnorm_grad_columns_kernel(const __grid_
 }
 
 template <typename TA, typename TR>
-cudaError_t launch_grad_as(const GradArgs &p, bool vec, int parts, float *ws, cudaStream_t stream) {
+cudaError_t launch_grad_as(const GradArgs &p, int width, int parts, float *ws, cudaStream_t stream) {
     constexpr int V = sizeof(TA) == 4 || sizeof(TR) == 4 ? 4 : 8;
     const unsigned grid = (unsigned)parts;
     if (p.D > kFit) {
@@ -429,12 +483,15 @@ cudaError_t launch_grad_as(const GradArgs &p, bool vec, int parts, float *ws, cu
     }
     if (p.D <= kNarrow) return launch_early(rmsnorm_grad_narrow_kernel<TA, TR>, grid, 32, 0, stream, p, ws);
     constexpr int kTwo = kFit / 1024 / V;
-    if (vec && p.D <= 1024 * V)
+    if (width == V && p.D <= 1024 * V)
         return launch_early(rmsnorm_grad_kernel<TA, TR, V, 1>, grid, threads_for(p.D / V, 1), 0, stream, p, ws);
-    if (vec)
+    if (width == V)
         return launch_early(rmsnorm_grad_kernel<TA, TR, V, kTwo>, grid, threads_for(p.D / V, kTwo), 0, stream, p, ws);
-    if (p.D <= 2048)
-        return launch_early(rmsnorm_grad_kernel<TA, TR, 1, 4>, grid, threads_for(p.D, 4), 0, stream, p, ws);
+    if (width == 2 && p.D <= 2048)
+        return launch_early(rmsnorm_grad_kernel<TA, TR, 2, 2>, grid, threads_for(p.D / 2, 2), 0, stream, p, ws);
+    if (width == 2)
+        return launch_early(rmsnorm_grad_kernel<TA, TR, 2, 4>, grid, threads_for(p.D / 2, 4), 0, stream, p, ws);
+    if (p.D <= 2048) return launch_early(rmsnorm_grad_kernel<TA, TR, 1, 4>, grid, threads_for(p.D, 4), 0, stream, p, ws);
     return launch_early(rmsnorm_grad_kernel<TA, TR, 1, 8>, grid, threads_for(p.D, 8), 0, stream, p, ws);
 }
 

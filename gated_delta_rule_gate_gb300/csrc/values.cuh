@@ -17,7 +17,9 @@ struct Words {
     static constexpr int kBytes = V * (int)sizeof(T) > 16 ? 16 : V * (int)sizeof(T);
     static constexpr int kCount = V * (int)sizeof(T) / kBytes;
     using type = std::conditional_t<
-        V == 1, T, std::conditional_t<sizeof(T) == 4, float4, std::conditional_t<V == 8, uint4, uint2>>>;
+        V == 1, T,
+        std::conditional_t<sizeof(T) == 4, std::conditional_t<V == 2, float2, float4>,
+                           std::conditional_t<V == 8, uint4, std::conditional_t<V == 4, uint2, uint32_t>>>>;
     type w[kCount];
 
     __device__ __forceinline__ void load(const T *p) {
@@ -31,12 +33,14 @@ struct Words {
     __device__ __forceinline__ void get(float (&v)[V]) const {
         if constexpr (V == 1) {
             v[0] = static_cast<float>(w[0]);
+        } else if constexpr (sizeof(T) == 4 && V == 2) {
+            v[0] = w[0].x, v[1] = w[0].y;
         } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
             for (int i = 0; i < kCount; ++i)
                 v[4 * i] = w[i].x, v[4 * i + 1] = w[i].y, v[4 * i + 2] = w[i].z, v[4 * i + 3] = w[i].w;
         } else {
-            static_assert(V == 8 || V == 4, "16-bit groups");
+            static_assert(V == 8 || V == 4 || V == 2, "16-bit groups");
             const uint32_t *u = reinterpret_cast<const uint32_t *>(&w[0]);
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
@@ -50,7 +54,7 @@ struct Words {
     }
 };
 
-// V values of type T at p (V > 1: 16 bytes, or 32 as two, aligned to 16).
+// V values of type T at p, which is aligned to V of them (to 16 bytes from there on).
 template <typename T, int V>
 __device__ __forceinline__ void load_values(const T *p, float (&v)[V]) {
     Words<T, V> w;
@@ -62,6 +66,8 @@ template <typename T, int V>
 __device__ __forceinline__ void store_values(T *p, const float (&v)[V]) {
     if constexpr (V == 1) {
         *p = static_cast<T>(v[0]);
+    } else if constexpr (sizeof(T) == 4 && V == 2) {
+        *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int i = 0; i < V; i += 4)
@@ -79,8 +85,28 @@ __device__ __forceinline__ void store_values(T *p, const float (&v)[V]) {
             }
         }
         if constexpr (V == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        else if constexpr (V == 4) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t *>(p) = w[0];
     }
+}
+
+// V adjacent columns c, ... of a row of n values (n % V == 0); zeros from column n on.
+template <typename T, int V>
+struct Columns : Words<T, V> {
+    __device__ __forceinline__ void load(const T *row, int c, int n) {
+        this->zero();
+        if (c < n) Words<T, V>::load(row + c);
+    }
+};
+template <typename T, int V>
+__device__ __forceinline__ void load_columns(const T *row, int c, int n, float (&v)[V]) {
+    Columns<T, V> q;
+    q.load(row, c, n);
+    q.get(v);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_columns(T *row, int c, int n, const float (&v)[V]) {
+    if (c < n) store_values<T, V>(row + c, v);
 }
 
 }  // namespace gdn
