@@ -407,7 +407,9 @@ __device__ __forceinline__ void tma_prefetch_2d(const void *tmap, int c0, int c1
 }
 // ---------------------------------------------------------------- dependent launch
 // Until the kernels before this one on the stream have ended and what they wrote is
-// seen; the next kernel may be set up meanwhile.
+// seen; the next kernel may be set up meanwhile.  A kernel that waits so reads global
+// memory by plain loads: what the one before wrote is not read-only while it runs, and
+// __ldg could be moved ahead of the wait.
 __device__ __forceinline__ void grid_wait() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");

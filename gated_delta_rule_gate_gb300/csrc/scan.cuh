@@ -90,8 +90,8 @@ template <typename T>
 __device__ __forceinline__ pair_t<T> load_pair(const T *p, bool ok1) {
     pair_t<T> v;
     T *e = reinterpret_cast<T *>(&v);
-    e[0] = __ldg(p);
-    e[1] = __ldg(p + (ok1 ? 1 : 0));  // unused where there is none
+    e[0] = *p;
+    e[1] = p[ok1 ? 1 : 0];  // unused where there is none
     return v;
 }
 // A warp writes the first n of a row's 64 channels at p, a lane two of them, whatever

@@ -84,8 +84,8 @@ struct alignas(128) Stage {
 #pragma unroll
             for (int k = 0; k < TOKENS; ++k) {
                 const bool on = own >> k & 1u;
-                r[k].x = on && 2 * lane < n ? __ldg(row + k * stride + 2 * lane) : 0.f;
-                r[k].y = on && 2 * lane + 1 < n ? __ldg(row + k * stride + 2 * lane + 1) : 0.f;
+                r[k].x = on && 2 * lane < n ? row[k * stride + 2 * lane] : 0.f;
+                r[k].y = on && 2 * lane + 1 < n ? row[k * stride + 2 * lane + 1] : 0.f;
             }
         } else {
             const uintptr_t first = reinterpret_cast<uintptr_t>(row);
@@ -94,7 +94,7 @@ struct alignas(128) Stage {
 #pragma unroll
                 for (int k = 0; k < TOKENS; ++k) {
                     const bool on = own >> k & 1u && 2 * lane < n;
-                    r[k] = on ? __ldg(reinterpret_cast<const uint32_t *>(row + k * stride) + lane) : 0u;
+                    r[k] = on ? reinterpret_cast<const uint32_t *>(row + k * stride)[lane] : 0u;
                 }
             } else {
                 // of two rows in turn both or one; the word behind lane 31's comes with a
@@ -104,8 +104,8 @@ struct alignas(128) Stage {
                 for (int k = 0; k < TOKENS; ++k) {
                     const bool split = ((first >> 1) + (odd ? k : 0)) & 1u, on = own >> k & 1u;
                     const uint32_t *w = reinterpret_cast<const uint32_t *>(row + k * stride - (split ? 1 : 0)) + lane;
-                    r[k] = on && 2 * lane < n + (split ? 1 : 0) ? __ldg(w) : 0u;
-                    last[k] = on && split && lane == 31 && n == 64 ? __ldg(w + 1) : 0u;
+                    r[k] = on && 2 * lane < n + (split ? 1 : 0) ? *w : 0u;
+                    last[k] = on && split && lane == 31 && n == 64 ? w[1] : 0u;
                 }
 #pragma unroll
                 for (int k = 0; k < TOKENS; ++k) {

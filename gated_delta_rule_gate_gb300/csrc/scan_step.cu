@@ -17,10 +17,10 @@ __device__ __forceinline__ void load_channels(const T *p, float (&v)[V]) {
     if constexpr (V == 1) {
         v[0] = static_cast<float>(*p);
     } else if constexpr (sizeof(T) == 4) {
-        const float4 r = __ldg(reinterpret_cast<const float4 *>(p));
+        const float4 r = *reinterpret_cast<const float4 *>(p);
         v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
     } else {
-        const uint2 r = __ldg(reinterpret_cast<const uint2 *>(p));
+        const uint2 r = *reinterpret_cast<const uint2 *>(p);
         const float2 a = unpack<T>(r.x), b = unpack<T>(r.y);
         v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
     }
