@@ -19,6 +19,8 @@
 namespace gdn {
 namespace scan {
 
+constexpr int kWarps = 8;
+
 __device__ __forceinline__ void gradient_duties(const GradArgs &q, int warps, int warp, int lane, int c, bool report) {
     const Args &p = q.f;
     for (int b = warp; b < p.B; b += warps) {
@@ -53,7 +55,7 @@ struct Backward {
     };
     struct Rest {
         Exchange x;
-        Meeting rev;               // (A, C) of each warp's run, and c behind it
+        Meeting<kWarps> rev;               // (A, C) of each warp's run, and c behind it
         alignas(16) float2 fwd[kWarps][64];  // (A, H) of each warp's run; at the end its sums
         float h[kWarps][64];       // the state before it
         uint64_t bar[kWarps][2];
@@ -290,13 +292,13 @@ struct Backward {
             *reinterpret_cast<float4 *>(&r.fwd[warp][2 * lane]) = make_float4(A.x, H.x, A.y, H.y);
             *reinterpret_cast<float4 *>(&r.rev.map[warp][2 * lane]) = make_float4(A.x, C.x, A.y, C.y);
             __syncthreads();
-            Meet<true> meet;
+            Meet<true, kWarps> meet;
             const float2 whole = meet.send(r.rev, r.x, at, turn);
             {  // while the maps are on their way: the states before the warps' runs
                 float h = kept;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    if (w / kMine == meet.part) r.h[w][meet.c] = h;
+                    if (w / meet.kMine == meet.part) r.h[w][meet.c] = h;
                     h = apply(r.fwd[w][meet.c], h);
                 }
             }
@@ -367,7 +369,7 @@ cudaError_t launch_grad_one(const GradArgs &args, cudaStream_t stream) {
     const int cb = (p.D + 63) / 64;
     int S = 1;
     const cudaError_t e =
-        cluster_blocks((const void *)kernel, sizeof(typename G::Shared), cb, (p.T + G::kTile - 1) / G::kTile, &S);
+        cluster_blocks((const void *)kernel, kWarps, sizeof(typename G::Shared), cb, (p.T + G::kTile - 1) / G::kTile, &S);
     if (e != cudaSuccess) return e;
     share_out(q.f, S, G::kTile);
     GradMaps m = {};
@@ -380,7 +382,7 @@ cudaError_t launch_grad_one(const GradArgs &args, cudaStream_t stream) {
                     (!BETA || (make_token_map(&m.y, p.beta, tg, p.bs, p.D, p.T, n) &&
                                make_token_map(&m.dy, q.db, tg, q.dbs, p.D, p.T, n)))))
         return cudaErrorInvalidValue;
-    return launch_clusters(cb, S, sizeof(typename G::Shared), stream, kernel, q, m);
+    return launch_clusters(cb, S, kWarps, sizeof(typename G::Shared), true, stream, kernel, q, m);
 }
 
 template <bool WIDE, typename TA, typename TG, bool RAW, bool BETA>

@@ -29,7 +29,6 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // All blocks of the cluster have come here.  Orders no memory accesses.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
-constexpr int kWarps = 8;
 constexpr int kMaxCluster = 16;
 
 // (A, H) of a run of one channel.  A run in which a request begins has A = -0 and
@@ -205,37 +204,38 @@ __device__ __forceinline__ int windows(const Place &a, int window) {
 }
 
 // The maps of a block's warps, of 64 channels each, and the states before their runs.
+template <int WARPS>
 struct alignas(16) Meeting {  // a warp writes its maps 16 bytes a lane
-    float2 map[kWarps][64];
-    float h[kWarps][64];
+    float2 map[WARPS][64];
+    float h[WARPS][64];
 };
-// Between two barriers of the block its 256 threads turn the warps' maps into the
+// Between two barriers of the block its threads turn the warps' maps into the
 // states before the warps' runs: a thread takes one channel, for two of the warps.
 // Every thread folds all maps of its channel itself: with 64 threads doing it for the
 // block, the others waited 3,100 cycles a window of 8 blocks for 300 dependent
 // instructions.  Warps and blocks follow one another upwards, or (REVERSE) downwards.
-constexpr int kParts = kWarps * 32 / 64, kMine = kWarps / kParts;
-template <bool REVERSE>
+template <bool REVERSE, int WARPS>
 struct Meet {
+    static constexpr int kParts = WARPS * 32 / 64, kMine = WARPS / kParts;
     int c, part;
     float2 before[kMine];  // the run before each of this thread's warps
 
     // First: the block's map, to every block of its group.
-    __device__ __forceinline__ float2 send(const Meeting &m, Exchange &x, const Place &at, int turn) {
+    __device__ __forceinline__ float2 send(const Meeting<WARPS> &m, Exchange &x, const Place &at, int turn) {
         c = threadIdx.x & 63, part = threadIdx.x >> 6;
         float2 run = make_float2(1.f, 0.f);
         uint32_t any = 0u;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            const float2 k = m.map[REVERSE ? kWarps - 1 - i : i][c];
+        for (int i = 0; i < WARPS; ++i) {
+            const float2 k = m.map[REVERSE ? WARPS - 1 - i : i][c];
             if (i / kMine == part) before[i % kMine] = run;
             any |= __float_as_uint(k.x);
             run = make_float2(run.x * k.x, fmaf(k.x, run.y, k.y));
         }
         if (any >> 31) {  // a request begins in one of them
             run = make_float2(1.f, 0.f);
-            for (int i = 0; i < kWarps; ++i) {
-                const float2 k = m.map[REVERSE ? kWarps - 1 - i : i][c];
+            for (int i = 0; i < WARPS; ++i) {
+                const float2 k = m.map[REVERSE ? WARPS - 1 - i : i][c];
 #pragma unroll
                 for (int j = 0; j < kMine; ++j)
                     if (i == part * kMine + j) before[j] = run;
@@ -251,7 +251,7 @@ struct Meet {
     }
     // Then: the states before the runs, from `carry`, the one before the window,
     // which moves on by a window.
-    __device__ __forceinline__ void receive(Meeting &m, Exchange &x, const Place &at, int turn, float2 run,
+    __device__ __forceinline__ void receive(Meeting<WARPS> &m, Exchange &x, const Place &at, int turn, float2 run,
                                             float &carry, int32_t *err) {
         float h = carry;
         const int S = at.S, rank = at.rank;
@@ -283,20 +283,23 @@ struct Meet {
 #pragma unroll
         for (int j = 0; j < kMine; ++j) {
             const int w = part * kMine + j;
-            m.h[REVERSE ? kWarps - 1 - w : w][c] = apply(before[j], h);
+            m.h[REVERSE ? WARPS - 1 - w : w][c] = apply(before[j], h);
         }
     }
 };
 
 // The blocks along time of one channel block: the most, up to a cluster's limit,
 // with which all clusters are resident at once, and no more than there are tiles.
-inline cudaError_t cluster_blocks(const void *kernel, size_t smem, int channel_blocks, int tiles, int *S) {
+inline cudaError_t cluster_blocks(const void *kernel, int warps, size_t smem, int channel_blocks, int tiles, int *S) {
     cudaError_t e = smem_attr(kernel, (int)smem);
     if (e == cudaSuccess) e = large_clusters(kernel);
-    int s = tiles < kMaxCluster ? tiles : kMaxCluster;
+    int s = tiles < kMaxCluster ? tiles : kMaxCluster, n = 0;
+    if (e == cudaSuccess && s > 1) {
+        e = resident_clusters(kernel, warps * 32, smem, 1, &n);
+        if (s > n / channel_blocks) s = n / channel_blocks;
+    }
     for (; e == cudaSuccess && s > 1; --s) {
-        int n = 0;
-        e = resident_clusters(kernel, kWarps * 32, smem, s, &n);
+        e = resident_clusters(kernel, warps * 32, smem, s, &n);
         if (n >= channel_blocks) break;
     }
     *S = s < 1 ? 1 : s;
@@ -324,23 +327,23 @@ inline void share_out(Args &p, int size, int tile) {
     }
 }
 
-// Launches a kernel in clusters of S blocks.
+// Launches a kernel in clusters of S blocks; `early`: as launch_early().
 template <typename... P, typename... A>
-cudaError_t launch_clusters(int channel_blocks, int S, size_t smem, cudaStream_t stream, void (*kernel)(P...),
-                            const A &...args) {
+cudaError_t launch_clusters(int channel_blocks, int S, int warps, size_t smem, bool early, cudaStream_t stream,
+                            void (*kernel)(P...), const A &...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)channel_blocks * (unsigned)S);
-    cfg.blockDim = dim3(kWarps * 32);
+    cfg.blockDim = dim3(warps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)S;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_early()
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = early ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

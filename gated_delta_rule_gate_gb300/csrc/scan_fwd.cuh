@@ -14,6 +14,11 @@
 // write o.  The loads of the next window are in flight meanwhile, so x, decay and
 // beta cross HBM once.  A request's first token takes in the request's initial
 // state and nothing of the token before it, so that ragged requests need nothing else.
+//
+// The bound is the issue of instructions, of which the gates' functions are the most:
+// 8 ragged requests of 16384 tokens together x 4096 channels fp16 with raw gates, input
+// gate and states 158 us, where HBM alone would take 79; with the decay given as its
+// logarithm and no input gate 32768 x 2048 bf16 takes 89 us, 66 % of HBM.
 #pragma once
 
 #include "scan_cluster.cuh"
@@ -43,24 +48,24 @@ struct Maps {
     CUtensorMap x, z, y, o;
 };
 
-template <bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
+template <int WARPS, bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
 struct Forward {
     // Long runs cost less of the exchange; with fp32 tensors they would leave room for
-    // one block an SM (4 x 32768 x 2048 bf16 with fp32 gates: 164 us at 8, 190 at 16; with
-    // bf16 gates 16).
+    // one block an SM (32768 tokens x 2048 bf16 with fp32 gates: 164 us at 8, 190 at 16; with
+    // bf16 gates 16 are the faster).
     static constexpr int kTokens = sizeof(TA) == 2 && sizeof(TG) == 2 ? 16 : 8;
-    static constexpr int kTile = kWarps * kTokens;
+    static constexpr int kTile = WARPS * kTokens;
 
     struct Input {
         Stage<TA, kTokens> x;
         Stage<TG, kTokens> z, y[BETA ? 1 : 0];
     };
     struct alignas(128) Shared {
-        Input in[kWarps];
-        Stage<TA, kTokens> out[kWarps];
+        Input in[WARPS];
+        Stage<TA, kTokens> out[WARPS];
         Exchange x;
-        Meeting meet;
-        uint64_t bar[kWarps];
+        Meeting<WARPS> meet;
+        uint64_t bar[WARPS];
     };
 
     // The warp's tokens t, ... to its stage, by the asynchronous copies of WIDE rows on
@@ -176,7 +181,7 @@ struct Forward {
         float2 bias = splat(0.f), scale = bias;
         if (RAW) bias = load_state(p.bias, c, p.D), scale = load_state(p.scale, c, p.D);
         if (at.size > 1) exchange_init(s.x);
-        request_duties(p, at.size * kWarps, at.me * kWarps + warp, lane, c, blockIdx.x < at.size);
+        request_duties(p, at.size * WARPS, at.me * WARPS + warp, lane, c, blockIdx.x < at.size);
 
         float carry = 0.f;  // the state of this thread's channel (see Meet) before the window
         for (int step = 0; step < steps; ++step, t += window) {
@@ -193,7 +198,7 @@ struct Forward {
                 plain ? first_walk<true>(p, in, now, c, lane, bias, scale, a, u)
                       : first_walk<false>(p, in, now, c, lane, bias, scale, a, u);
             __syncthreads();
-            Meet<false> meet;
+            Meet<false, WARPS> meet;
             const float2 tile = meet.send(s.meet, s.x, at, step);
             if (step + 1 < steps) {  // while the maps are on their way
                 tok = look_up(p, at.lo, at.hi, t + window, kTokens, lane, seen);
@@ -217,23 +222,24 @@ struct Forward {
     }
 };
 
-template <bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
-__global__ void __launch_bounds__(kWarps * 32, 2) scan_kernel(const __grid_constant__ Args p,
-                                                             const __grid_constant__ Maps m) {
-    using F = Forward<WIDE, TA, TG, RAW, BETA, MODE>;
+// 16 warps an SM.
+template <int WARPS, bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) scan_kernel(const __grid_constant__ Args p,
+                                                                     const __grid_constant__ Maps m) {
+    using F = Forward<WARPS, WIDE, TA, TG, RAW, BETA, MODE>;
     extern __shared__ __align__(128) unsigned char smem[];
     F::run(p, m, *reinterpret_cast<typename F::Shared *>(smem));
 }
 
-template <bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
-cudaError_t launch_one(const Args &p, cudaStream_t stream) {
-    using F = Forward<WIDE, TA, TG, RAW, BETA, MODE>;
-    auto kernel = scan_kernel<WIDE, TA, TG, RAW, BETA, MODE>;
-    const int cb = (p.D + 63) / 64;
-    int S = 1;
-    const cudaError_t e =
-        cluster_blocks((const void *)kernel, sizeof(typename F::Shared), cb, (p.T + F::kTile - 1) / F::kTile, &S);
-    if (e != cudaSuccess) return e;
+template <int WARPS, bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
+cudaError_t blocks_for(const Args &p, int *S) {
+    using F = Forward<WARPS, WIDE, TA, TG, RAW, BETA, MODE>;
+    return cluster_blocks((const void *)scan_kernel<WARPS, WIDE, TA, TG, RAW, BETA, MODE>, WARPS,
+                          sizeof(typename F::Shared), (p.D + 63) / 64, (p.T + F::kTile - 1) / F::kTile, S);
+}
+template <int WARPS, bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
+cudaError_t launch_blocks(const Args &p, int S, cudaStream_t stream) {
+    using F = Forward<WARPS, WIDE, TA, TG, RAW, BETA, MODE>;
     Maps m = {};
     Args q = p;
     share_out(q, S, F::kTile);
@@ -242,7 +248,39 @@ cudaError_t launch_one(const Args &p, cudaStream_t stream) {
                   (!BETA || make_token_map(&m.y, p.beta, type_of<TG>(), p.bs, p.D, p.T, F::kTokens)) &&
                   make_token_map(&m.o, p.o, type_of<TA>(), p.os, p.D, p.T, F::kTokens)))
         return cudaErrorInvalidValue;
-    return launch_clusters(cb, S, sizeof(typename F::Shared), stream, kernel, q, m);
+    // A pass that keeps states is one of training, between gradients that fill the SMs'
+    // shared memory: set up while one still runs, its blocks take the places that come
+    // free first, and the whole grid is slower than one set up afterwards (a training
+    // pass of 4096 x 2048 bf16 102 us, 92 so; 32768 x 2048 462 and 452), but for one
+    // window or two, where the launch counts (1024 x 2048 36.0 and 36.4, 999 x 1000 fp32
+    // 31.8 and 33.1).  Without states always early (4096 x 1024 22.2 us, 24.5 not).
+    const int64_t window = (int64_t)(S / q.groups) * F::kTile;
+    const bool early = !p.chunk || p.T <= 2 * q.groups * window;
+    return launch_clusters((p.D + 63) / 64, S, WARPS, sizeof(typename F::Shared), early, stream,
+                           scan_kernel<WARPS, WIDE, TA, TG, RAW, BETA, MODE>, q, m);
+}
+
+// Of 16-bit tensors blocks of 4 warps are shared out more evenly and wait for fewer
+// others, but a cluster has 16 at most: blocks of 8 where it gets more warps from
+// them.  us with 4 and 8, bf16, raw gates: 16384 x 4096 ragged 158 and 162, 16384 x 2560
+// 97 and 108, 32768 x 2048 136 and 138, 32768 x 512 84 and 77.  Tiles of fp32 tensors are
+// half as long, and rows that are read by words want more of them on their way: 8
+// (16384 x 2048 fp32 99 and 97; 16384 x 2047 bf16 237 and 188).  A pass that keeps states
+// takes 8 too: the small blocks leave a gradient that is set up beside them no room for
+// two on an SM (a training pass of 32768 x 2048 520 us, 462 with 8).
+template <bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
+cudaError_t launch_one(const Args &p, cudaStream_t stream) {
+    int eights = 1;
+    cudaError_t e = blocks_for<8, WIDE, TA, TG, RAW, BETA, MODE>(p, &eights);
+    if constexpr (WIDE && sizeof(TA) == 2 && sizeof(TG) == 2) {
+        if (e == cudaSuccess && !p.chunk) {
+            int fours = 1;
+            e = blocks_for<4, WIDE, TA, TG, RAW, BETA, MODE>(p, &fours);
+            if (e == cudaSuccess && eights * 8 <= fours * 4)
+                return launch_blocks<4, WIDE, TA, TG, RAW, BETA, MODE>(p, fours, stream);
+        }
+    }
+    return e == cudaSuccess ? launch_blocks<8, WIDE, TA, TG, RAW, BETA, MODE>(p, eights, stream) : e;
 }
 
 template <bool WIDE, typename TA, typename TG, bool RAW, bool BETA>
