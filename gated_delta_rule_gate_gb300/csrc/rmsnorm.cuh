@@ -139,7 +139,8 @@ __device__ __forceinline__ void load_sum(const Args &p, size_t row, C column, fl
 // their way.  Rows of up to 512 words take one a thread and four blocks an SM at 32
 // registers; longer ones two.
 template <typename TA, int Q, int V, int N>
-__global__ void __launch_bounds__(V > 2 && N == 1 ? 512 : 1024, V > 2 && N == 1 ? 4 : 1) rmsnorm_kernel(const __grid_constant__ Args p) {
+__global__ void __launch_bounds__(V > 2 && N == 1 ? 512 : 1024, V > 2 && N == 1 ? 4 : 1)
+    rmsnorm_kernel(const __grid_constant__ Args p) {
     __shared__ float s_red[64];
     extern __shared__ int s_peak[];  // V <= 2: the largest |y| of each group, as bits
     ptx::grid_wait();

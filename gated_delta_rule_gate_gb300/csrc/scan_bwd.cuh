@@ -12,6 +12,10 @@
 // block alone, and only c crosses blocks (one exchange a window, as in the
 // forward pass).  x, decay, beta and d_o cross HBM once.  The sums over tokens are
 // kept in registers by channel and joined in a fixed order at the end.
+//
+// Bound by the issue of instructions (178 a token and 64 channels with raw and input
+// gates) and by the exchange of each window: 4 x 8192 x 2048 bf16 with them 311 us, 2.9
+// TB/s; the pass with its forward 455, with the decay given as its logarithm 255.
 #pragma once
 
 #include "scan_cluster.cuh"

@@ -293,8 +293,10 @@ cudaError_t launch_mode(const Args &p, cudaStream_t stream) {
 template <bool WIDE, typename TA, typename TG>
 cudaError_t launch_types(const Args &p, cudaStream_t stream) {
     if (p.bias)
-        return p.beta ? launch_mode<WIDE, TA, TG, true, true>(p, stream) : launch_mode<WIDE, TA, TG, true, false>(p, stream);
-    return p.beta ? launch_mode<WIDE, TA, TG, false, true>(p, stream) : launch_mode<WIDE, TA, TG, false, false>(p, stream);
+        return p.beta ? launch_mode<WIDE, TA, TG, true, true>(p, stream)
+                      : launch_mode<WIDE, TA, TG, true, false>(p, stream);
+    return p.beta ? launch_mode<WIDE, TA, TG, false, true>(p, stream)
+                  : launch_mode<WIDE, TA, TG, false, false>(p, stream);
 }
 
 }  // namespace scan
