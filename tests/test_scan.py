@@ -131,6 +131,21 @@ def test_matches_the_token_loop(i):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("layout", [dict(lengths=[300, 0, 1, 399]), dict(S=350, seq_lens=[350, 349])])
+def test_wide_rows_in_several_windows(act, layout):
+    """So many channels that few blocks walk each: several windows, with the blocks of a
+    pass that keeps states and of one that does not."""
+    import gated_delta_rule_gate_gb300 as g
+    p = draw(250, 8192, act=act, mode="unit", **layout)
+    for keep in (False, True):
+        out, fin = call(p, g.gdn_scan, want_chunk_states=keep)
+        check(p, out, fin)
+        again = call(p, g.gdn_scan, want_chunk_states=keep)
+        assert torch.equal(out.nan_to_num(9.0), again[0].nan_to_num(9.0)) and torch.equal(fin, again[1])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("mode", ["none", "lerp", "unit"])
 @pytest.mark.parametrize("raw", [True, False])
