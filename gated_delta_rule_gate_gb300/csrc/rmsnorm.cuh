@@ -9,8 +9,8 @@
 // Rows that do not fit (more than kFit values, or 16384 in words of 8) are walked a
 // second time instead.
 //
-// 16384 x 4096 bf16, residual, e4m3 by groups of 128: 112 us, 6.6 TB/s of 6.8.
-// 256 x 2048: 5.5 us, a launch and two trips to memory.
+// 32768 x 2048 bf16, fp32 residual, e4m3 by groups of 128: 109 us, 6.8 TB/s.
+// 256 x 4096 fp16: 6.3 us, a launch and two trips to memory.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -328,9 +328,9 @@ cudaError_t launch_rmsnorm_as(const Args &p, int q, int width, cudaStream_t stre
 // formed.  The blocks' shares meet in the workspace, and a second kernel adds them up
 // in their order: no atomics, the same sum every time.
 //
-// Bound by HBM, and by the wait for each row's sum: forward and gradient of 16384 x
-// 4096 bf16 186 us, 5.1 TB/s; of 2046 wide by pairs 126 against 206 by single values,
-// 2048 wide 100.
+// Bound by HBM, and by the wait for each row's sum: forward and gradient of 32768 x
+// 2048 bf16 181 us, 5.2 TB/s; of 16384 x 2046 by pairs 126 against 206 by single values,
+// 16384 x 2048 100.
 template <typename TA, typename TR, int V, int N>
 __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constant__ GradArgs p, float *partial) {
     ptx::grid_wait();

@@ -80,7 +80,7 @@ gdn_status validate_grad(const gdn_rmsnorm_grad_args *a) {
 }
 
 // Blocks that share the rows out: enough to fill the device at the row's size.  Four
-// on each of 152 SMs: forward and gradient of 16384 x 4096 bf16 take 255, 206, 185,
+// on each of 152 SMs: forward and gradient of 32768 x 2048 bf16 take 255, 206, 185,
 // 202, 189 us with two, three, four, six, eight.
 int grad_parts(const gdn_rmsnorm_grad_args *a) {
     if (a->rows == 0) return 0;
