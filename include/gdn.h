@@ -454,7 +454,9 @@ gdn_status gdn_scan_backward(const gdn_scan_grad_args *args, gdn_stream stream);
  *     rstd = 1 / sqrt(mean(r^2) + eps),   y = r rstd weight
  *     out = y in x_dtype, or in E4M3 with scales:  s = max(|y|) / 448 over a row
  *     (group 0) or over each 128 columns (group 128; the last group of a row may be
- *     short), out = y / s, the maximum floored at 2^-100 so that s > 0.
+ *     short), out = y / s, the maximum floored at 2^-100 so that s > 0.  y is formed as
+ *     (r rstd) weight and the quotient rounded as a division's; the maximum of a whole row
+ *     is max |r weight| times rstd (within three roundings of fp32 of max |y|).
  *
  * The norm takes r before residual_out is rounded.  x has x_stride elements from
  * row to row (0: dim); the other tensors are contiguous.  scales is fp32 [rows],
