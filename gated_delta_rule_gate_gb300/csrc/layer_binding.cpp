@@ -155,7 +155,7 @@ struct Rows {
     int64_t stride;
 };
 // Address and elements between rows of a device tensor whose last dimension is
-// contiguous and whose leading ones lie in it as one.
+// contiguous and whose leading ones lie in it as one; rows do not overlap.
 Rows rows(const Tensor *t, ScalarType type, IntArrayRef shape, const char *what) {
     if (!t) return {nullptr, 0};
     check(*t, type, what);
@@ -169,6 +169,8 @@ Rows rows(const Tensor *t, ScalarType type, IntArrayRef shape, const char *what)
         else if (shape[d] > 1 && t->stride(d) != shape[d + 1] * t->stride(d + 1))
             refuse(PyExc_ValueError, "%s must have one stride over all its rows", what);
     }
+    // a step of 0 is the library's word for rows without a gap
+    if (step < last) refuse(PyExc_ValueError, "%s has rows that overlap (an expanded tensor?): pass a copy", what);
     return {t->data_ptr(), step};
 }
 Rows rows(const Tensor &t, ScalarType type, IntArrayRef shape, const char *what) { return rows(&t, type, shape, what); }
@@ -367,25 +369,30 @@ PyObject *py_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
     a.forward.final_state = nullptr;
     const IntArrayRef shape = x.sizes();
     const ScalarType act = x.scalar_type(), gate = decay.scalar_type();
-    Stream stream(v[21], x);
-    // every token and row is written unless requests may leave some out
-    const bool whole = !c.cu && !c.seq_lens && !c.slots;
-    auto token = [&](ScalarType t) { return whole ? make(shape, x, t) : at::zeros(shape, on(x, t)); };
     auto given = [&](int i, const char *what) {
         const Tensor *t = tensor(v[i], what);
         return t ? *t : Tensor();
     };
+    auto some = [](const Tensor &t) { return t.defined() ? &t : nullptr; };
     Tensor dx = given(14, "dx"), dg = given(15, "d_decay"), db = given(16, "d_beta");
     Tensor dbias = given(17, "d_gate_bias"), dscale = given(18, "d_gate_scale"), dinit = given(19, "d_initial_state");
-    if (!dx.defined()) dx = token(act);
-    if (!dg.defined()) dg = token(gate);
-    if (!db.defined() && c.beta) db = token(gate);
+    const Rows dor = rows(dout, act, shape, "d_out");
+    Rows dxr = rows(some(dx), act, shape, "dx"), dgr = rows(some(dg), gate, shape, "d_decay");
+    Rows dbr = rows(some(db), gate, shape, "d_beta");
+    Stream stream(v[21], x);
+    // every token and row is written unless requests may leave some out
+    const bool whole = !c.cu && !c.seq_lens && !c.slots;
+    auto token = [&](Tensor &t, Rows &r, ScalarType type) {
+        if (t.defined()) return;
+        t = whole ? make(shape, x, type) : at::zeros(shape, on(x, type));
+        r.at = t.data_ptr();
+    };
+    token(dx, dxr, act);
+    token(dg, dgr, gate);
+    if (c.beta) token(db, dbr, gate);
     if (c.bias && !dbias.defined()) dbias = make(c.bias->sizes(), x, f32);
     if (c.bias && !dscale.defined()) dscale = make(c.bias->sizes(), x, f32);
     if (c.init && !dinit.defined()) dinit = at::zeros(c.init->sizes(), on(x, f32));
-    auto some = [](const Tensor &t) { return t.defined() ? &t : nullptr; };
-    const Rows dor = rows(dout, act, shape, "d_out"), dxr = rows(dx, act, shape, "dx");
-    const Rows dgr = rows(dg, gate, shape, "d_decay"), dbr = rows(some(db), gate, shape, "d_beta");
     a.d_o = dor.at, a.d_o_stride = dor.stride;
     a.dx = dxr.at, a.dx_stride = dxr.stride;
     a.d_decay = dgr.at, a.d_decay_stride = dgr.stride;
