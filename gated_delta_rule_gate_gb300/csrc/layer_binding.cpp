@@ -163,11 +163,12 @@ Rows rows(const Tensor *t, ScalarType type, IntArrayRef shape, const char *what)
     const int64_t dim = t->dim(), last = dim ? shape[dim - 1] : 1;
     if (t->is_contiguous()) return {t->data_ptr(), last};
     if (t->stride(-1) != 1 && last != 1) refuse(PyExc_ValueError, "%s must have contiguous channels", what);
-    int64_t step = dim > 1 ? t->stride(-2) : last;
-    for (int64_t d = dim - 3; d >= 0; --d) {
-        if (shape[d + 1] == 1) step = t->stride(d);
-        else if (shape[d] > 1 && t->stride(d) != shape[d + 1] * t->stride(d + 1))
-            refuse(PyExc_ValueError, "%s must have one stride over all its rows", what);
+    int64_t step = last, count = 1;  // of the dimensions so far; those of one have no stride
+    for (int64_t d = dim - 2; d >= 0; --d) {
+        if (shape[d] == 1) continue;
+        if (count == 1) step = t->stride(d);
+        else if (t->stride(d) != count * step) refuse(PyExc_ValueError, "%s must have one stride over all its rows", what);
+        count *= shape[d];
     }
     // a step of 0 is the library's word for rows without a gap
     if (step < last) refuse(PyExc_ValueError, "%s has rows that overlap (an expanded tensor?): pass a copy", what);

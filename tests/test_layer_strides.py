@@ -74,3 +74,45 @@ def test_an_expanded_gradient_is_refused_and_its_copy_taken():
     for t in range(50):
         h = decay.double().exp() * h + x[t].double()
     assert float((out[-1].double() - h).abs().max() / h.abs().max()) <= 1e-5
+
+
+def lead_steps(lead, width):
+    """Strides of [*lead, D] columns of a wider contiguous tensor [*lead, width]."""
+    strides, step = [], width
+    for n in reversed(lead):
+        strides.insert(0, step)
+        step *= n
+    return tuple(strides)
+
+
+@pytest.mark.parametrize("lead", [(2, 1, 3), (2, 3, 1), (1, 2, 3), (2, 1, 1), (2, 1, 3, 1, 2), (1, 1, 3)])
+def test_leading_dimensions_of_one_are_passed_over(lead):
+    """Rows in one step are accepted wherever a dimension of one stands and whatever its
+    stride, and rows that are not in one are refused."""
+    import gated_delta_rule_gate_gb300 as g
+    strides = lead_steps(lead, D + 4)
+    odd = tuple(12345 if n == 1 else s for n, s in zip(lead, strides))
+    for st in (strides, odd):
+        with pytest.raises(Exception) as e:  # past the checks of strides, at the missing device
+            g.gdn_rmsnorm(Standin((*lead, D), (*st, 1)), W, out_dtype=torch.float16, scales=X)
+        assert "stride" not in str(e.value) and "overlap" not in str(e.value)
+    wide = [k for k, n in enumerate(lead) if n > 1]
+    if len(wide) > 1:
+        bad = list(strides)
+        bad[wide[0]] += D + 4
+        with pytest.raises(ValueError, match="one stride"):
+            g.gdn_rmsnorm(Standin((*lead, D), (*bad, 1)), W)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lead", [(2, 1, 3), (4, 1, 5, 1, 2), (1, 3, 1), (3, 1, 1)])
+def test_columns_of_a_wider_tensor_with_dimensions_of_one(lead):
+    import gated_delta_rule_gate_gb300 as g
+    wide = torch.randn(*lead, 40, generator=torch.Generator().manual_seed(7)).cuda()
+    w = torch.ones(24, device="cuda")
+    x = wide[..., 8:32]
+    f, whole = g.gdn_rmsnorm(x, w, want_rstd=True), g.gdn_rmsnorm(x.contiguous(), w, want_rstd=True)
+    assert torch.equal(f.out, whole.out) and torch.equal(f.rstd, whole.rstd)
+    b = g.gdn_rmsnorm_backward(x, x.contiguous(), w, f.rstd)
+    want = g.gdn_rmsnorm_backward(x.contiguous(), x.contiguous(), w, f.rstd)
+    assert torch.equal(b.dx, want.dx) and torch.equal(b.dweight, want.dweight)
