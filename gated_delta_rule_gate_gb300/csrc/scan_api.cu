@@ -82,7 +82,7 @@ gdn_status validate(const gdn_scan_args *a, bool needs_o, Args *out) {
         !aligned(a->final_state, 4) || !aligned(a->chunk_states, 4) || !aligned(a->error_word, 4))
         return fail(GDN_ERR_INVALID, "a pointer is not aligned to its element size");
     p.B = a->batch;
-    p.T = a->total_tokens;
+    p.T = a->batch ? a->total_tokens : 0;  // without requests no kernel looks for a token's
     p.L = a->seq_len ? a->seq_len : (a->cu_seqlens || a->batch == 0 ? 0 : a->total_tokens / a->batch);
     p.D = a->channels;
     p.rows = rows;

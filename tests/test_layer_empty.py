@@ -1,0 +1,41 @@
+"""Calls with nothing in them: no requests, no tokens."""
+import ctypes
+
+import pytest
+import torch
+
+from gated_delta_rule_gate_gb300 import _native as N
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("states", [False, True])
+def test_gradient_of_no_requests(states):
+    """Offsets of one entry beside tokens: no token belongs to a request, and the sums are zero."""
+    import gated_delta_rule_gate_gb300 as g
+    for T, D in ((130, 70), (1, 64), (0, 16)):
+        x, z, d, b = (torch.randn(T, D, device="cuda") for _ in range(4))
+        bias = torch.randn(D, device="cuda")
+        # what lies behind the one offset would be a request of all tokens
+        cu = torch.tensor([0, T, T], dtype=torch.int32, device="cuda")[:1]
+        h = torch.randn(3, D, device="cuda") if states else None
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        kw = dict(beta=b, gate_bias=bias, gate_scale=-bias.exp(), cu_seqlens=cu, initial_state=h, error_word=err)
+        _, chunks = g.gdn_scan(x, z, want_chunk_states=True, **kw)
+        got = g.gdn_scan_backward(d, x, z, chunks, d_final_state=h, **kw)
+        torch.cuda.synchronize()
+        for t in got:
+            assert t is None or not bool(t.any())
+        assert int(err) == 0
+
+
+@pytest.mark.gpu
+def test_gradient_of_no_requests_through_the_library():
+    """Without offsets, and without the tensors that no token needs."""
+    dbias, dscale, bias = (torch.full((16,), 7.0, device="cuda") for _ in range(3))
+    f = N.GdnScanArgs(0, 8, 0, 16, 0, N.DTYPE_F32, N.DTYPE_F32, 0, 0)
+    f.gate_bias = f.gate_scale = bias.data_ptr()
+    a = N.GdnScanGradArgs(f)
+    a.d_gate_bias, a.d_gate_scale = dbias.data_ptr(), dscale.data_ptr()
+    assert N.load().gdn_scan_backward(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == N.GDN_OK
+    torch.cuda.synchronize()
+    assert not bool(dbias.any()) and not bool(dscale.any())
