@@ -108,6 +108,13 @@ bool flag(PyObject *o) {
     if (v < 0) throw python_error();
     return v != 0;
 }
+int32_t whole(PyObject *o, const char *what) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred() && !PyErr_ExceptionMatches(PyExc_OverflowError)) throw python_error();
+    PyErr_Clear();
+    if (v < 1 || v > INT32_MAX) refuse(PyExc_ValueError, "%s must be in [1, 2^31)", what);
+    return (int32_t)v;
+}
 double number(PyObject *o, double otherwise) {
     if (!o) return otherwise;
     const double v = PyFloat_AsDouble(o);
@@ -274,6 +281,8 @@ gdn_scan_args scan_args(const ScanCall &c, const Tensor *out, const Tensor *chun
         a.num_state_rows = (int32_t)state->size(0);
         a.initial_state = address<const float>(c.init, f32, "initial_state");
         a.final_state = address<float>(c.fin, f32, "final_state", state->sizes());
+    } else if (c.slots) {
+        a.num_state_rows = INT32_MAX;  // no states, no rows for an id to be beyond
     }
     const int64_t d[1] = {D}, b[1] = {B}, ch[2] = {(T + kChunk - 1) / kChunk, D};
     a.gate_bias = address<const float>(c.bias, f32, "gate_bias", d);
@@ -348,7 +357,7 @@ PyObject *py_step(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
 Signature backward_signature = {"gdn_scan_backward", 4, 4, {"d_out", "x", "decay", "chunk_states", "beta", "gate_bias",
                                 "gate_scale", "beta_sigmoid", "input_scale", "cu_seqlens", "seq_lens", "slot_ids",
                                 "initial_state", "d_final_state", "dx", "d_decay", "d_beta", "d_gate_bias",
-                                "d_gate_scale", "d_initial_state", "error_word", "stream"}, {}};
+                                "d_gate_scale", "d_initial_state", "error_word", "stream", "num_state_rows"}, {}};
 
 PyObject *py_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwnames) {
     HANDLE_TH_ERRORS
@@ -368,6 +377,13 @@ PyObject *py_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
     gdn_scan_grad_args a = {};
     a.forward = scan_args(c, nullptr, chunks);
     a.forward.final_state = nullptr;
+    const Tensor *state = c.init ? c.init : dfin ? dfin : tensor(v[19], "d_initial_state");
+    if (v[22]) {
+        const int32_t n = whole(v[22], "num_state_rows");
+        if (state && state->dim() == 2 && state->size(0) != n)
+            refuse(PyExc_ValueError, "num_state_rows is %d, the states have %lld", n, (long long)state->size(0));
+        a.forward.num_state_rows = n;
+    }
     const IntArrayRef shape = x.sizes();
     const ScalarType act = x.scalar_type(), gate = decay.scalar_type();
     auto given = [&](int i, const char *what) {
@@ -398,11 +414,10 @@ PyObject *py_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
     a.dx = dxr.at, a.dx_stride = dxr.stride;
     a.d_decay = dgr.at, a.d_decay_stride = dgr.stride;
     a.d_beta = dbr.at, a.d_beta_stride = dbr.stride;
-    const Tensor *state = c.init ? c.init : dfin;
     const int64_t d[1] = {shape.back()};
     a.d_gate_bias = address<float>(some(dbias), f32, "d_gate_bias", d);
     a.d_gate_scale = address<float>(some(dscale), f32, "d_gate_scale", d);
-    if (state) {
+    if (c.init || dfin) {
         a.d_final_state = address<const float>(dfin, f32, "d_final_state", state->sizes());
         a.d_initial_state = address<float>(some(dinit), f32, "d_initial_state", state->sizes());
     } else if (dinit.defined()) {
@@ -631,7 +646,8 @@ PyMethodDef methods[] = {
      "(\"unit\").  x, decay and beta are [T, D] packed (requests by cu_seqlens, else one)\n"
      "or [B, S, D] (seq_lens bounds the rows); they may be columns of wider tensors.\n"
      "States are fp32 [rows, D], row slot_ids[b] or b; final_state is written if given\n"
-     "and may be initial_state.  Returns out (allocated when not given; tokens of no\n"
+     "and may be initial_state; without states slot_ids only tell which requests to skip\n"
+     "(negative ones).  Returns out (allocated when not given; tokens of no\n"
      "request are not written), or (out, chunk_states) with want_chunk_states, for\n"
      "gdn_scan_backward."},
     {"gdn_scan_step", FAST(py_step),
@@ -645,13 +661,15 @@ PyMethodDef methods[] = {
      "gdn_scan_backward($module, d_out, x, decay, chunk_states, *, beta=None, gate_bias=None, gate_scale=None, "
      "beta_sigmoid=False, input_scale='none', cu_seqlens=None, seq_lens=None, slot_ids=None, initial_state=None, "
      "d_final_state=None, dx=None, d_decay=None, d_beta=None, d_gate_bias=None, d_gate_scale=None, "
-     "d_initial_state=None, error_word=None, stream=None)\n--\n\n"
+     "d_initial_state=None, error_word=None, stream=None, num_state_rows=None)\n--\n\n"
      "Gradients of gdn_scan for the gradient d_out of its output (and d_final_state of\n"
      "its final states): the forward call's arguments and the chunk_states that it\n"
      "returned.  Returns ScanGradients(dx, d_decay, d_beta, d_gate_bias, d_gate_scale,\n"
      "d_initial_state), None where there is no such input.  Outputs are allocated when\n"
      "not given (zeros where tokens or state rows may belong to no request); a given\n"
-     "one is not written there."},
+     "one is not written there.  num_state_rows says how many rows the forward call's\n"
+     "states had where none are given here: without it only a negative slot id is a bad\n"
+     "one, as in a forward call without states."},
     {"gdn_rmsnorm", FAST(py_norm),
      "gdn_rmsnorm($module, x, weight, *, residual=None, eps=1e-06, out_dtype=None, group=0, want_rstd=False, "
      "out=None, residual_out=None, scales=None, stream=None)\n--\n\n"
