@@ -277,6 +277,7 @@ gdn_scan_args scan_args(const ScanCall &c, const Tensor *out, const Tensor *chun
     if (state) {
         if (state->dim() != 2 || state->size(1) != D)
             refuse(PyExc_ValueError, "states must be [rows, %lld]", (long long)D);
+        if (state->size(0) == 0 && B > 0) refuse(PyExc_ValueError, "states of %lld requests have no rows", (long long)B);
         if (state->size(0) > INT32_MAX) refuse(PyExc_ValueError, "more than 2^31 - 1 state rows");
         a.num_state_rows = (int32_t)state->size(0);
         a.initial_state = address<const float>(c.init, f32, "initial_state");
@@ -378,6 +379,8 @@ PyObject *py_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
     a.forward = scan_args(c, nullptr, chunks);
     a.forward.final_state = nullptr;
     const Tensor *state = c.init ? c.init : dfin ? dfin : tensor(v[19], "d_initial_state");
+    if (state && state->dim() == 2 && state->size(0) == 0 && a.forward.batch > 0)
+        refuse(PyExc_ValueError, "states of %d requests have no rows", a.forward.batch);
     if (v[22]) {
         const int32_t n = whole(v[22], "num_state_rows");
         if (state && state->dim() == 2 && state->size(0) != n)

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from gated_delta_rule_gate_gb300 import _native as N
+from layer_standins import Standin
 
 
 @pytest.mark.gpu
@@ -39,3 +40,15 @@ def test_gradient_of_no_requests_through_the_library():
     assert N.load().gdn_scan_backward(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == N.GDN_OK
     torch.cuda.synchronize()
     assert not bool(dbias.any()) and not bool(dscale.any())
+
+
+def test_states_of_no_rows_are_refused():
+    """Zero rows are the library's word for a row a request."""
+    import gated_delta_rule_gate_gb300 as g
+    x, none, ch = Standin((4, 8)), Standin((0, 8)), Standin((1, 8))
+    for call in (lambda: g.gdn_scan(x, x, initial_state=none), lambda: g.gdn_scan_step(x, x, final_state=none),
+                 lambda: g.gdn_scan_backward(x, x, x, ch, initial_state=none),
+                 lambda: g.gdn_scan_backward(x, x, x, ch, d_final_state=none),
+                 lambda: g.gdn_scan_backward(x, x, x, ch, dx=x, d_decay=x, d_initial_state=none)):
+        with pytest.raises(ValueError, match="no rows"):
+            call()
