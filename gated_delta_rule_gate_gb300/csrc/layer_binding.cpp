@@ -290,6 +290,8 @@ gdn_scan_args scan_args(const ScanCall &c, const Tensor *out, const Tensor *chun
     a.gate_scale = address<const float>(c.scale, f32, "gate_scale", d);
     a.cu_seqlens = address<const int32_t>(c.cu, i32, "cu_seqlens");
     a.seq_lens = address<const int32_t>(c.seq_lens, i32, "seq_lens", b);
+    // rows of no tokens the library knows as packed ones; all requests are empty
+    if (shape.size() == 3 && !a.seq_len) a.seq_lens = nullptr;
     a.slot_ids = address<const int32_t>(c.slots, i32, "slot_ids", b);
     a.chunk_states = address<float>(chunks, f32, "chunk_states", ch);
     a.error_word = address<int32_t>(c.err, i32, "error_word");

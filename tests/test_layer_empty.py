@@ -52,3 +52,23 @@ def test_states_of_no_rows_are_refused():
                  lambda: g.gdn_scan_backward(x, x, x, ch, dx=x, d_decay=x, d_initial_state=none)):
         with pytest.raises(ValueError, match="no rows"):
             call()
+
+
+@pytest.mark.gpu
+def test_padded_rows_of_no_tokens():
+    """[B, 0, D] with seq_lens: every request is empty and hands its state on."""
+    import gated_delta_rule_gate_gb300 as g
+    x = torch.empty(3, 0, 20, device="cuda")
+    bias = torch.randn(20, device="cuda")
+    h = torch.randn(5, 20, device="cuda")
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    for seq_lens in (None, i32([0, 4, -1])):
+        kw = dict(gate_bias=bias, gate_scale=-bias.exp(), seq_lens=seq_lens, slot_ids=i32([4, 0, 2]))
+        for fn in (g.gdn_scan, g.gdn_scan_step):
+            fin = torch.full_like(h, 7.0)
+            assert fn(x, x, initial_state=h, final_state=fin, **kw).shape == x.shape
+            assert torch.equal(fin[[4, 0, 2]], h[[4, 0, 2]]) and bool((fin[[1, 3]] == 7.0).all())
+        chunks = torch.empty(0, 20, device="cuda")
+        got = g.gdn_scan_backward(x, x, x, chunks, initial_state=h, d_final_state=h, **kw)
+        assert torch.equal(got.d_initial_state[[4, 0, 2]], h[[4, 0, 2]])
+        assert not bool(got.d_gate_bias.any()) and not bool(got.d_gate_scale.any()) and got.dx.shape == x.shape
