@@ -135,9 +135,12 @@ std::string text(IntArrayRef v) {
     for (size_t i = 0; i < v.size(); ++i) s += (i ? ", " : "") + std::to_string(v[i]);
     return s + ")";
 }
-void check(const Tensor &t, ScalarType type, const char *what) {
+void check_device(const Tensor &t, const char *what) {
     if (!t.is_cuda())
         refuse(PyExc_ValueError, "libgdn takes device tensors; %s is on %s", what, t.device().str().c_str());
+}
+void check(const Tensor &t, ScalarType type, const char *what) {
+    check_device(t, what);
     if (t.scalar_type() != type) refuse(PyExc_TypeError, "%s must be %s", what, c10::toString(type));
 }
 void check_shape(const Tensor &t, IntArrayRef shape, const char *what) {
@@ -496,6 +499,14 @@ PyObject *py_norm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
     END_HANDLE_TH_ERRORS
 }
 
+// A workspace may have any type and shape.
+const Tensor *workspace(PyObject *o) {
+    const Tensor *t = tensor(o, "workspace");
+    if (!t) return nullptr;
+    check_device(*t, "workspace");
+    if (!t->is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
+    return t;
+}
 // Device memory of `need` bytes where `given` is none.
 struct Workspace {
     Tensor t;
@@ -535,11 +546,11 @@ PyObject *py_norm_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyOb
     a.weight = address(&weight, weight.scalar_type(), "weight", d);
     a.rstd = address<const float>(&rstd, f32, "rstd", shape.empty() ? shape : shape.slice(0, shape.size() - 1));
     a.d_residual = address(dres, rt, "d_residual", shape);
+    const Tensor *given = workspace(v[7]);
     Stream stream(v[8], r);
     Tensor dx = dxg ? *dxg : make(shape, r, rt), dw = dwg ? *dwg : make(d, r, f32);
     a.dx = address(&dx, rt, "dx", shape);
     a.d_weight = address<float>(&dw, f32, "d_weight", d);
-    const Tensor *given = tensor(v[7], "workspace");
     const Workspace ws(given, given ? 0 : lib.norm_workspace(&a), r);
     done(lib.norm_backward(&a, ws.at, ws.bytes, stream.get()));
     return tuple_of(norm_gradients, {&dx, &dw});
@@ -586,7 +597,7 @@ PyObject *py_clip(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
         sizes[i] = g.numel();
         if (outs) to[i] = address(&outs->at(i, "an output"), g.scalar_type(), "an output", g.sizes());
     }
-    const Tensor *given_norm = tensor(v[4], "norm");
+    const Tensor *given_norm = tensor(v[4], "norm"), *given = workspace(v[6]);
     Tensor norm = given_norm ? *given_norm : Tensor();
     if (!given_norm && !grads.n)
         norm = at::empty({1}, at::TensorOptions().device(at::kCUDA, c10::cuda::current_device()).dtype(at::kFloat));
@@ -601,7 +612,6 @@ PyObject *py_clip(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
     const int64_t one[1] = {1};
     a.norm = address<float>(&norm, ScalarType::Float, "norm", one);
     a.error_word = address<int32_t>(tensor(v[5], "error_word"), ScalarType::Int, "error_word");
-    const Tensor *given = tensor(v[6], "workspace");
     const Workspace ws(given, given ? 0 : lib.clip_workspace(&a), norm);
     done(lib.clip(&a, ws.at, ws.bytes, stream.get()));
     return THPVariable_Wrap(norm);
