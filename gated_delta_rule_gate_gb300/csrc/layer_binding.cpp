@@ -139,6 +139,20 @@ void check_device(const Tensor &t, const char *what) {
     if (!t.is_cuda())
         refuse(PyExc_ValueError, "libgdn takes device tensors; %s is on %s", what, t.device().str().c_str());
 }
+// All tensors of a call lie where `first` does (which is refused with a message of its
+// own where that is no device).
+struct Named {
+    const Tensor *t;
+    const char *what;
+};
+void one_device(const Tensor &first, std::initializer_list<Named> others) {
+    if (!first.is_cuda()) return;
+    const c10::Device device = first.device();
+    for (const Named &o : others)
+        if (o.t && o.t->device() != device && o.t->is_cuda())
+            refuse(PyExc_ValueError, "%s is on %s, not on %s as the rest of the call's device tensors", o.what,
+                   o.t->device().str().c_str(), device.str().c_str());
+}
 void check(const Tensor &t, ScalarType type, const char *what) {
     check_device(t, what);
     if (t.scalar_type() != type) refuse(PyExc_TypeError, "%s must be %s", what, c10::toString(type));
@@ -187,13 +201,16 @@ Rows rows(const Tensor *t, ScalarType type, IntArrayRef shape, const char *what)
 Rows rows(const Tensor &t, ScalarType type, IntArrayRef shape, const char *what) { return rows(&t, type, shape, what); }
 
 // The stream of a call: the current one of the tensors' device, a torch stream, or a
-// handle.  While it lives, memory is made for that stream.
+// handle.  While it lives, that device is the current one and memory is made for that stream.
 class Stream {
   public:
     Stream(PyObject *o, const Tensor &like) {
         if (!like.is_cuda()) return;  // refused with a message of its own
+        const c10::DeviceIndex device = like.device().index();
         if (!o) {
-            handle_ = c10::cuda::getCurrentCUDAStream(like.device().index()).stream();
+            handle_ = c10::cuda::getCurrentCUDAStream(device).stream();
+            // the library launches on the current device
+            if (device != c10::cuda::current_device()) device_.emplace(device);
             return;
         }
         PyObject *held = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttr(o, stream_handle_name);
@@ -202,13 +219,14 @@ class Stream {
         Py_DECREF(held);
         if (!h && PyErr_Occurred()) throw python_error();
         handle_ = static_cast<cudaStream_t>(h);
-        guard_.emplace(c10::cuda::getStreamFromExternal(handle_, like.device().index()));
+        guard_.emplace(c10::cuda::getStreamFromExternal(handle_, device));
     }
     gdn_stream get() const { return reinterpret_cast<gdn_stream>(handle_); }
 
   private:
     cudaStream_t handle_ = nullptr;
     std::optional<c10::cuda::CUDAStreamGuard> guard_;
+    std::optional<c10::cuda::CUDAGuard> device_;
 };
 
 at::TensorOptions on(const Tensor &like, ScalarType type) { return at::TensorOptions().device(like.device()).dtype(type); }
@@ -240,6 +258,9 @@ struct ScanCall {
 gdn_scan_args scan_args(const ScanCall &c, const Tensor *out, const Tensor *chunks) {
     constexpr ScalarType f32 = ScalarType::Float, i32 = ScalarType::Int;
     const Tensor &x = *c.x, &decay = *c.decay;
+    one_device(x, {{&decay, "decay"}, {c.beta, "beta"}, {c.bias, "gate_bias"}, {c.scale, "gate_scale"},
+                   {c.cu, "cu_seqlens"}, {c.seq_lens, "seq_lens"}, {c.slots, "slot_ids"}, {c.init, "initial_state"},
+                   {c.fin, "final_state"}, {c.err, "error_word"}, {out, "out"}, {chunks, "chunk_states"}});
     gdn_scan_args a = {};
     a.act_dtype = code(x, "x");
     a.gate_dtype = code(decay, "decay");
@@ -401,6 +422,9 @@ PyObject *py_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
     auto some = [](const Tensor &t) { return t.defined() ? &t : nullptr; };
     Tensor dx = given(14, "dx"), dg = given(15, "d_decay"), db = given(16, "d_beta");
     Tensor dbias = given(17, "d_gate_bias"), dscale = given(18, "d_gate_scale"), dinit = given(19, "d_initial_state");
+    one_device(x, {{&dout, "d_out"}, {dfin, "d_final_state"}, {some(dx), "dx"}, {some(dg), "d_decay"},
+                   {some(db), "d_beta"}, {some(dbias), "d_gate_bias"}, {some(dscale), "d_gate_scale"},
+                   {some(dinit), "d_initial_state"}});
     const Rows dor = rows(dout, act, shape, "d_out");
     Rows dxr = rows(some(dx), act, shape, "dx"), dgr = rows(some(dg), gate, shape, "d_decay");
     Rows dbr = rows(some(db), gate, shape, "d_beta");
@@ -468,6 +492,8 @@ PyObject *py_norm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
     if (D > INT32_MAX) refuse(PyExc_ValueError, "x has more than 2^31 - 1 columns");
     a.dim = (int32_t)D;
     a.rows = D ? x.numel() / D : 0;
+    const Tensor *o = tensor(v[7], "out"), *ro = tensor(v[8], "residual_out"), *sc = tensor(v[9], "scales");
+    one_device(x, {{&weight, "weight"}, {residual, "residual"}, {o, "out"}, {ro, "residual_out"}, {sc, "scales"}});
     const Rows xr = rows(x, type, shape, "x");
     a.x = xr.at, a.x_stride = xr.stride;
     const int64_t d[1] = {D};
@@ -477,7 +503,6 @@ PyObject *py_norm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
     if (a.group) scales_shape.push_back((D + 127) / 128);
     Stream stream(v[10], x);
     Tensor out, res_out, scales, rstd;
-    const Tensor *o = tensor(v[7], "out"), *ro = tensor(v[8], "residual_out"), *sc = tensor(v[9], "scales");
     out = o ? *o : make(shape, x, out_type);
     if (residual) {
         const ScalarType rt = residual->scalar_type();
@@ -531,6 +556,9 @@ PyObject *py_norm_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyOb
     const Tensor &dout = needed(v[0], "d_out"), &r = needed(v[1], "r"), &weight = needed(v[2], "weight");
     const Tensor &rstd = needed(v[3], "rstd"), *dres = tensor(v[4], "d_residual"), *dxg = tensor(v[5], "dx");
     const Tensor *dwg = tensor(v[6], "d_weight");
+    const Tensor *given = workspace(v[7]);
+    one_device(r, {{&dout, "d_out"}, {&weight, "weight"}, {&rstd, "rstd"}, {dres, "d_residual"}, {dxg, "dx"},
+                   {dwg, "d_weight"}, {given, "workspace"}});
     gdn_rmsnorm_grad_args a = {};
     const IntArrayRef shape = r.sizes();
     const ScalarType rt = r.scalar_type();
@@ -546,7 +574,6 @@ PyObject *py_norm_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyOb
     a.weight = address(&weight, weight.scalar_type(), "weight", d);
     a.rstd = address<const float>(&rstd, f32, "rstd", shape.empty() ? shape : shape.slice(0, shape.size() - 1));
     a.d_residual = address(dres, rt, "d_residual", shape);
-    const Tensor *given = workspace(v[7]);
     Stream stream(v[8], r);
     Tensor dx = dxg ? *dxg : make(shape, r, rt), dw = dwg ? *dwg : make(d, r, f32);
     a.dx = address(&dx, rt, "dx", shape);
@@ -590,14 +617,19 @@ PyObject *py_clip(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
     std::vector<void *> to(grads.n);
     std::vector<int64_t> sizes(grads.n);
     std::vector<int32_t> types(grads.n);
+    const Tensor *given_norm = tensor(v[4], "norm"), *given = workspace(v[6]), *err = tensor(v[5], "error_word");
+    if (grads.n)
+        one_device(grads.at(0, "a gradient"), {{given_norm, "norm"}, {err, "error_word"}, {given, "workspace"}});
+    else if (given_norm)
+        one_device(*given_norm, {{err, "error_word"}, {given, "workspace"}});
     for (Py_ssize_t i = 0; i < grads.n; ++i) {
         const Tensor &g = grads.at(i, "a gradient");
+        one_device(grads.at(0, "a gradient"), {{&g, "a gradient"}, {outs ? &outs->at(i, "an output") : nullptr, "an output"}});
         types[i] = code(g, "a gradient");
         in[i] = address(&g, g.scalar_type(), "a gradient");
         sizes[i] = g.numel();
         if (outs) to[i] = address(&outs->at(i, "an output"), g.scalar_type(), "an output", g.sizes());
     }
-    const Tensor *given_norm = tensor(v[4], "norm"), *given = workspace(v[6]);
     Tensor norm = given_norm ? *given_norm : Tensor();
     if (!given_norm && !grads.n)
         norm = at::empty({1}, at::TensorOptions().device(at::kCUDA, c10::cuda::current_device()).dtype(at::kFloat));
@@ -611,7 +643,7 @@ PyObject *py_clip(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
     a.grads = in.data(), a.outs = outs ? to.data() : nullptr, a.sizes = sizes.data(), a.dtypes = types.data();
     const int64_t one[1] = {1};
     a.norm = address<float>(&norm, ScalarType::Float, "norm", one);
-    a.error_word = address<int32_t>(tensor(v[5], "error_word"), ScalarType::Int, "error_word");
+    a.error_word = address<int32_t>(err, ScalarType::Int, "error_word");
     const Workspace ws(given, given ? 0 : lib.clip_workspace(&a), norm);
     done(lib.clip(&a, ws.at, ws.bytes, stream.get()));
     return THPVariable_Wrap(norm);
