@@ -606,6 +606,8 @@ PyObject *py_clip(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
     PyObject *v[kMost];
     parse(clip_signature, args, n, kwnames, v);
     if (!v[0]) refuse(PyExc_TypeError, "grads must be a sequence of tensors");
+    if (!v[1]) refuse(PyExc_TypeError, "max_norm must be a number");
+    const double max_norm = number(v[1], 0), eps = number(v[2], 1e-6);
     const Sequence grads(v[0], "grads must be a sequence of tensors");
     std::optional<Sequence> outs;
     if (v[3]) {
@@ -638,8 +640,8 @@ PyObject *py_clip(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
     if (!norm.defined()) norm = make({1}, like, ScalarType::Float);
     gdn_grad_clip_args a = {};
     a.count = (int32_t)grads.n;
-    a.max_norm = (float)number(v[1], 0);
-    a.eps = (float)number(v[2], 1e-6);
+    a.max_norm = (float)max_norm;
+    a.eps = (float)eps;
     a.grads = in.data(), a.outs = outs ? to.data() : nullptr, a.sizes = sizes.data(), a.dtypes = types.data();
     const int64_t one[1] = {1};
     a.norm = address<float>(&norm, ScalarType::Float, "norm", one);
