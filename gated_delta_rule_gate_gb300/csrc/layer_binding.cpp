@@ -12,7 +12,6 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/cuda/EmptyTensor.h>
-#include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -204,9 +203,10 @@ Rows rows(const Tensor &t, ScalarType type, IntArrayRef shape, const char *what)
 // handle.  While it lives, that device is the current one and memory is made for that stream.
 class Stream {
   public:
-    Stream(PyObject *o, const Tensor &like) {
-        if (!like.is_cuda()) return;  // refused with a message of its own
-        const c10::DeviceIndex device = like.device().index();
+    Stream(PyObject *o, const Tensor &like) : Stream(o, like.device()) {}
+    Stream(PyObject *o, c10::Device home) {
+        if (!home.is_cuda()) return;  // refused with a message of its own
+        const c10::DeviceIndex device = home.index();
         if (!o) {
             handle_ = c10::cuda::getCurrentCUDAStream(device).stream();
             // the library launches on the current device
@@ -231,9 +231,10 @@ class Stream {
 
 at::TensorOptions on(const Tensor &like, ScalarType type) { return at::TensorOptions().device(like.device()).dtype(type); }
 // Device memory by torch's allocator (past the dispatcher, 0.3 us a tensor).
-Tensor make(IntArrayRef shape, const Tensor &like, ScalarType type) {
-    return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
+Tensor make(IntArrayRef shape, c10::Device device, ScalarType type) {
+    return at::detail::empty_cuda(shape, type, device, std::nullopt);
 }
+Tensor make(IntArrayRef shape, const Tensor &like, ScalarType type) { return make(shape, like.device(), type); }
 
 PyObject *wrap(const Tensor &t) { return t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None); }
 // A named tuple of the tensors (None where undefined).
@@ -632,12 +633,11 @@ PyObject *py_clip(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
         sizes[i] = g.numel();
         if (outs) to[i] = address(&outs->at(i, "an output"), g.scalar_type(), "an output", g.sizes());
     }
-    Tensor norm = given_norm ? *given_norm : Tensor();
-    if (!given_norm && !grads.n)
-        norm = at::empty({1}, at::TensorOptions().device(at::kCUDA, c10::cuda::current_device()).dtype(at::kFloat));
-    const Tensor like = grads.n ? grads.at(0, "a gradient") : norm;
-    Stream stream(v[7], like);
-    if (!norm.defined()) norm = make({1}, like, ScalarType::Float);
+    const c10::Device device = grads.n      ? grads.at(0, "a gradient").device()
+                               : given_norm ? given_norm->device()
+                                            : c10::Device(at::kCUDA, c10::cuda::current_device());
+    Stream stream(v[7], device);
+    Tensor norm = given_norm ? *given_norm : make({1}, device, ScalarType::Float);
     gdn_grad_clip_args a = {};
     a.count = (int32_t)grads.n;
     a.max_norm = (float)max_norm;
