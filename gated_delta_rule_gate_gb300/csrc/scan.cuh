@@ -215,7 +215,8 @@ __device__ __forceinline__ Tokens look_up(const Args &p, int lo, int hi, int t, 
 // Two channels at a time.  The gates' functions are the larger part of the
 // kernels' instructions, so they are written for packed fp32 and few special
 // function units; their relative errors stay within a few 2^-24 where the state
-// remembers (a near 1), since a state of M tokens' memory carries M times a's.
+// remembers (a near 1), since a state of M tokens' memory carries M times a's, and
+// grow with |g| (see exponential) where it forgets.
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 operator+(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 operator*(float2 a, float2 b) { return __fmul2_rn(a, b); }
@@ -264,17 +265,23 @@ __device__ __forceinline__ float2 softplus(float2 z) {
     return fma2(r, u, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
 }
 
-// e^g - 1: for |g| <= 1/5 a polynomial times g (degree 4, fitted as above, 1.4e-7),
-// else 2^(g log2 e) - 1.  1 + it is then e^g without a bias where g is near 0.
-__device__ __forceinline__ float2 exp_minus_1(float2 g) {
+// e^g, and m = e^g - 1 without cancellation: for |g| <= 1/5 a polynomial times g (degree 4,
+// fitted as above, 1.4e-7) and 1 + it, which has no bias where g is near 0; else 2^(g log2 e),
+// whose error is (4 + 1.25 |g|) 2^-24 of itself (ex2.approx, the product's rounding), and that
+// less 1.  Below 2^-126 it is 0.  1 + m for all g would leave a small decay on steps of 2^-24.
+struct Exp {
+    float2 a, m;
+};
+__device__ __forceinline__ Exp exponential(float2 g) {
     float2 r = splat(0.008333331905305386f);
     r = fma2(r, g, splat(0.04173609986901283f));
     r = fma2(r, g, splat(0.16666696965694427f));
     r = fma2(r, g, splat(0.4999993145465851f));
     r = fma2(r, g, splat(1.f)) * g;
-    const float2 t = g * splat(kLog2e);
-    const float2 e = make_float2(ex2(t.x), ex2(t.y)) + splat(-1.f);
-    return make_float2(fabsf(g.x) <= 0.2f ? r.x : e.x, fabsf(g.y) <= 0.2f ? r.y : e.y);
+    const float2 t = g * splat(kLog2e), e = make_float2(ex2(t.x), ex2(t.y));
+    const float2 a = r + splat(1.f), m = e + splat(-1.f);
+    const bool x = fabsf(g.x) <= 0.2f, y = fabsf(g.y) <= 0.2f;
+    return {make_float2(x ? a.x : e.x, y ? a.y : e.y), make_float2(x ? r.x : m.x, y ? r.y : m.y)};
 }
 
 template <bool RAW>
@@ -296,9 +303,9 @@ template <bool RAW, bool BETA, int MODE>
 __device__ __forceinline__ Gates token_gates(float2 z, float2 y, float2 bias, float2 scale, bool sig) {
     Gates t;
     t.soft = RAW ? softplus(z + bias) : splat(0.f);
-    const float2 m = exp_minus_1(RAW ? scale * t.soft : z);
-    t.a = m + splat(1.f);
-    t.n = MODE == kLerp ? -m : (MODE == kUnit ? unit_scale(m) : splat(1.f));
+    const Exp e = exponential(RAW ? scale * t.soft : z);
+    t.a = e.a;
+    t.n = MODE == kLerp ? -e.m : (MODE == kUnit ? unit_scale(e.m) : splat(1.f));
     t.i = BETA ? (sig ? sigmoid(y) : y) : splat(1.f);
     return t;
 }

@@ -202,7 +202,7 @@ struct Backward {
             }
             if (RAW) {  // sigmoid(z) = 1 - e^-softplus(z)
                 sums.scale = fma2(d, held.soft[k], sums.scale);
-                d = d * (-scale * exp_minus_1(-held.soft[k]));
+                d = d * (-scale * exponential(-held.soft[k]).m);
                 sums.bias = sums.bias + d;
             }
             const float2 w = MODE == kNone ? dh : n * dh, dx = BETA ? w * i : w;

@@ -72,12 +72,12 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(const __grid_consta
             const int i = 2 * w, j = V > 1 ? i + 1 : i;
             const float2 zz = make_float2(z[i], z[j]), yy = make_float2(y[i], y[j]);
             const float2 bb = make_float2(bias[i], bias[j]), ss = make_float2(scale[i], scale[j]);
-            const float2 m = exp_minus_1(p.bias ? log_decay<true>(zz, bb, ss) : zz), a = m + splat(1.f);
+            const Exp e = exponential(p.bias ? log_decay<true>(zz, bb, ss) : zz);
             float2 u = make_float2(x[i], x[j]);
             if (p.beta) u = u * (p.sigmoid ? sigmoid(yy) : yy);
-            if (p.mode == kLerp) u = u * -m;
-            if (p.mode == kUnit) u = u * unit_scale(m);
-            const float2 r = fma2(a, make_float2(h[i], h[j]), u);
+            if (p.mode == kLerp) u = u * -e.m;
+            if (p.mode == kUnit) u = u * unit_scale(e.m);
+            const float2 r = fma2(e.a, make_float2(h[i], h[j]), u);
             h[i] = r.x;
             h[j] = V > 1 ? r.y : r.x;
         }

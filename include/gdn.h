@@ -345,7 +345,8 @@ typedef enum gdn_input_scale {
  *     n   = 1 | 1 - a | sqrt(max(0, 1 - a^2))      (input_scale)
  *     h_t = a h_{t-1} + n i x_t,   o_t = h_t
  *
- * The state h is fp32; o is rounded once.  g <= 0 is expected (g = -inf forgets
+ * The state h is fp32; o is rounded once.  a is good to (4 + 1.25 |g|) 2^-24 of itself,
+ * and 0 where it is below 2^-126.  g <= 0 is expected (g = -inf forgets
  * the past; g > 0 grows the state and makes n <= 0 with LERP and 0 with UNIT).
  *
  * Tokens and requests are those of gdn_problem: seq_len == 0 is the packed form
