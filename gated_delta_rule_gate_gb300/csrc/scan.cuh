@@ -294,16 +294,17 @@ __device__ __forceinline__ float2 unit_scale(float2 m) {
     return make_float2(root(fmaxf(q.x, 0.f)), root(fmaxf(q.y, 0.f)));
 }
 
-// What a token's gates come to: a = exp(g), the input's scale n, its gate i, and in
+// What a token's gates come to: g, a = exp(g), the input's scale n, its gate i, and in
 // the raw arm softplus(z).
 struct Gates {
-    float2 a, n, i, soft;
+    float2 g, a, n, i, soft;
 };
 template <bool RAW, bool BETA, int MODE>
 __device__ __forceinline__ Gates token_gates(float2 z, float2 y, float2 bias, float2 scale, bool sig) {
     Gates t;
     t.soft = RAW ? softplus(z + bias) : splat(0.f);
-    const Exp e = exponential(RAW ? scale * t.soft : z);
+    t.g = RAW ? scale * t.soft : z;
+    const Exp e = exponential(t.g);
     t.a = e.a;
     t.n = MODE == kLerp ? -e.m : (MODE == kUnit ? unit_scale(e.m) : splat(1.f));
     t.i = BETA ? (sig ? sigmoid(y) : y) : splat(1.f);

@@ -59,8 +59,8 @@ struct Backward {
     };
     struct Rest {
         Exchange x;
-        Meeting<kWarps> rev;               // (A, C) of each warp's run, and c behind it
-        alignas(16) float2 fwd[kWarps][64];  // (A, H) of each warp's run; at the end its sums
+        Meeting<kWarps> rev;               // (R, C) of each warp's run, and c behind it
+        alignas(16) float2 fwd[kWarps][64];  // (R, H) of each warp's run; at the end its sums
         float h[kWarps][64];       // the state before it
         uint64_t bar[kWarps][2];
     };
@@ -131,27 +131,28 @@ struct Backward {
         float2 a[kTokens], n[kTokens], i[kTokens], soft[kTokens];
     };
 
-    // The gates of the warp's tokens and its maps, (A, H) and C.  PLAIN: all of them
+    // The gates of the warp's tokens and its maps, (R, H) and C.  PLAIN: all of them
     // inside one request, neither its first nor its last token among them.
     template <bool PLAIN>
     static __device__ __forceinline__ void first_walk(const GradArgs &q, const Input &in, const Tokens &tok, int c,
-                                                      int lane, float2 bias, float2 scale, Held &held, float2 &A,
+                                                      int lane, float2 bias, float2 scale, Held &held, float2 &R,
                                                       float2 &H, float2 &C) {
         const Args &p = q.f;
-        A = splat(1.f), H = splat(0.f), C = splat(0.f);
+        float2 sum = splat(0.f);
+        H = splat(0.f), C = splat(0.f);
 #pragma unroll
         for (int k = 0; k < kTokens; ++k) {
             float2 y = splat(0.f);
             if constexpr (BETA) y = in.y[0].at(k, lane);
             const Gates g = token_gates<RAW, BETA, MODE>(in.z.at(k, lane), y, bias, scale, p.sigmoid);
             held.a[k] = g.a, held.n[k] = g.n, held.i[k] = g.i, held.soft[k] = g.soft;
-            float2 u = scaled<BETA, MODE>(in.x.at(k, lane), g.n, g.i);
+            float2 u = scaled<BETA, MODE>(in.x.at(k, lane), g.n, g.i), own_g = g.g;
             if (!PLAIN) {
-                if (!(tok.own >> k & 1u)) held.a[k] = splat(1.f), u = splat(0.f);
+                if (!(tok.own >> k & 1u)) held.a[k] = splat(1.f), own_g = u = splat(0.f);
                 if (tok.first >> k & 1u) H = first_state(p, tok, k, c);
             }
             H = fma2(held.a[k], H, u);
-            A = A * held.a[k];
+            sum = sum + own_g;
         }
 #pragma unroll
         for (int k = kTokens - 1; k >= 0; --k) {
@@ -163,7 +164,7 @@ struct Backward {
             C = held.a[k] * (d + C);
             if (!PLAIN && (tok.first >> k & 1u)) C = splat(0.f);
         }
-        if (!PLAIN && tok.first) A = splat(kBegins);
+        R = !PLAIN && tok.first ? splat(kBegins) : root_of(sum);
     }
 
     // The gradients of the warp's tokens, from the state before and c behind them.
@@ -290,11 +291,11 @@ struct Backward {
             }
             const bool plain = tok.own == kAll && !(tok.first | tok.last);
             Held held;
-            float2 A, H, C;
-            if (plain) first_walk<true>(q, in, tok, c, lane, bias, scale, held, A, H, C);
-            else first_walk<false>(q, in, tok, c, lane, bias, scale, held, A, H, C);
-            *reinterpret_cast<float4 *>(&r.fwd[warp][2 * lane]) = make_float4(A.x, H.x, A.y, H.y);
-            *reinterpret_cast<float4 *>(&r.rev.map[warp][2 * lane]) = make_float4(A.x, C.x, A.y, C.y);
+            float2 R, H, C;
+            if (plain) first_walk<true>(q, in, tok, c, lane, bias, scale, held, R, H, C);
+            else first_walk<false>(q, in, tok, c, lane, bias, scale, held, R, H, C);
+            *reinterpret_cast<float4 *>(&r.fwd[warp][2 * lane]) = make_float4(R.x, H.x, R.y, H.y);
+            *reinterpret_cast<float4 *>(&r.rev.map[warp][2 * lane]) = make_float4(R.x, C.x, R.y, C.y);
             __syncthreads();
             Meet<true, kWarps> meet;
             const float2 whole = meet.send(r.rev, r.x, at, turn);

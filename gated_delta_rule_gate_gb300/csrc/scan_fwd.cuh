@@ -2,12 +2,13 @@
 // and along time, in one launch.
 //
 // h_t = a_t h_{t-1} + u_t is a composition of affine maps: a run of tokens takes
-// h to A h + H with A the product of its a and H its result from a zero state.
+// h to A h + H with A the product of its a (kept as its root, see scan_cluster.cuh) and
+// H its result from a zero state.
 // A warp takes kTokens tokens of 64 channels (a lane two of them), a block the
 // runs of its warps, a cluster of S blocks the tiles of its blocks; the cluster
 // walks the whole token axis of its channels in windows of S tiles and carries
 // the state from window to window in registers.  Per window: every warp folds
-// its run to (A, H); the block's warps exchange theirs in shared memory, the
+// its run to its map; the block's warps exchange theirs in shared memory, the
 // blocks theirs in distributed shared memory (Meet); every warp
 // then has the state before its run, in the same order of operations on every
 // run, and walks its tokens, which have stayed in registers, a second time to
@@ -100,16 +101,17 @@ struct Forward {
     static __device__ __forceinline__ float4 first_walk(const Args &p, const Input &in, const Tokens &tok, int c,
                                                         int lane, float2 bias, float2 scale, float2 (&a)[kTokens],
                                                         float2 (&u)[kTokens]) {
-        float2 A = splat(1.f), H = splat(0.f);
+        float2 sum = splat(0.f), H = splat(0.f);
 #pragma unroll
         for (int k = 0; k < kTokens; ++k) {
             float2 y = splat(0.f);
             if constexpr (BETA) y = in.y[0].at(k, lane);
             const Gates g = token_gates<RAW, BETA, MODE>(in.z.at(k, lane), y, bias, scale, p.sigmoid);
+            float2 own_g = g.g;
             a[k] = g.a;
             u[k] = scaled<BETA, MODE>(in.x.at(k, lane), g.n, g.i);
             if (!PLAIN) {  // tokens of no request hand the state on
-                if (!(tok.own >> k & 1u)) a[k] = splat(1.f), u[k] = splat(0.f);
+                if (!(tok.own >> k & 1u)) a[k] = splat(1.f), own_g = u[k] = splat(0.f);
                 if (tok.first >> k & 1u) {  // takes in the request's initial state
                     const int row = __shfl_sync(0xffffffffu, tok.row, k);
                     if (p.init) u[k] = fma2(a[k], load_state(p.init + (size_t)row * p.D, c, p.D), u[k]);
@@ -117,10 +119,10 @@ struct Forward {
                 }
             }
             H = !PLAIN && (tok.first >> k & 1u) ? u[k] : fma2(a[k], H, u[k]);
-            A = A * a[k];
+            sum = sum + own_g;
         }
-        if (!PLAIN && tok.first) A = splat(kBegins);
-        return make_float4(A.x, H.x, A.y, H.y);
+        const float2 R = !PLAIN && tok.first ? splat(kBegins) : root_of(sum);
+        return make_float4(R.x, H.x, R.y, H.y);
     }
 
     // o of the warp's tokens, which a plain run hands to an asynchronous copy.

@@ -347,7 +347,9 @@ typedef enum gdn_input_scale {
  *
  * The state h is fp32; o is rounded once.  a is good to (4 + 1.25 |g|) 2^-24 of itself,
  * and 0 where it is below 2^-126.  g <= 0 is expected (g = -inf forgets
- * the past; g > 0 grows the state and makes n <= 0 with LERP and 0 with UNIT).
+ * the past; g > 0 grows the state and makes n <= 0 with LERP and 0 with UNIT).  Runs of
+ * tokens may grow or shrink by more than fp32 holds; a state that is a number
+ * after every token comes out as one.
  *
  * Tokens and requests are those of gdn_problem: seq_len == 0 is the packed form
  * ([total_tokens, channels]; request b owns tokens [cu_seqlens[b],
