@@ -495,7 +495,9 @@ gdn_status gdn_rmsnorm(const gdn_rmsnorm_args *args, gdn_stream stream);
  *     dx = rstd (weight d_out - xhat mean(weight d_out xhat)) + d_residual
  *     d_weight = sum over rows of d_out xhat
  *
- * dx is the gradient of x and of residual alike.  r, d_residual and dx have
+ * dx is the gradient of x and of residual alike, for the rstd that is given: an fp32
+ * rstd is up to 2^-22 off, which moves dx by up to 2^-22 (1 + 3 sqrt(dim)) rstd |weight d_out|
+ * (on rows of one value that may be all of it).  r, d_residual and dx have
  * r_dtype, d_out x_dtype (d_out_stride elements from row to row; 0: dim), d_weight
  * is fp32.  dx may be d_residual.  Sums are fp32 and in a fixed order.  The
  * workspace is device memory of gdn_rmsnorm_backward_workspace_size() bytes,
