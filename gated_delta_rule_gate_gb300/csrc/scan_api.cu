@@ -98,6 +98,13 @@ gdn_status validate(const gdn_scan_args *a, bool needs_o, Args *out) {
     return GDN_OK;
 }
 
+// The walks along time add up to three windows to a token's place.
+gdn_status check_tokens(const Args &p) {
+    constexpr int kMost = INT32_MAX - 4 * gdn::scan::kMaxWindow;
+    if (p.T > kMost) return fail(GDN_ERR_UNSUPPORTED, "total_tokens above %d is not supported", kMost);
+    return GDN_OK;
+}
+
 // Groups of four channels can be read and written as one word (gdn_scan_step).
 bool four_wide(const Args &p, const gdn_scan_args *a) {
     const size_t ea = size_of(a->act_dtype), eg = size_of(a->gate_dtype);
@@ -115,8 +122,8 @@ extern "C" {
 
 gdn_status gdn_scan(const gdn_scan_args *a, gdn_stream stream) {
     Args p;
-    const gdn_status st = validate(a, true, &p);
-    if (st != GDN_OK) return st;
+    gdn_status st = validate(a, true, &p);
+    if (st != GDN_OK || (st = check_tokens(p)) != GDN_OK) return st;
     if (p.B == 0) return gdn::ok();
     return gdn::cuda_status(gdn::scan::launch_scan(p, a->act_dtype, a->gate_dtype, (cudaStream_t)stream));
 }
@@ -137,7 +144,7 @@ gdn_status gdn_scan_backward(const gdn_scan_grad_args *a, gdn_stream stream) {
     if (!a) return fail(GDN_ERR_INVALID, "args is NULL");
     gdn::scan::GradArgs q;
     gdn_status st = validate(&a->forward, false, &q.f);
-    if (st != GDN_OK) return st;
+    if (st != GDN_OK || (st = check_tokens(q.f)) != GDN_OK) return st;
     Args &p = q.f;
     if ((st = check_stride(a->d_o_stride, p.D, "d_o", &q.dos)) != GDN_OK) return st;
     if ((st = check_stride(a->dx_stride, p.D, "dx", &q.dxs)) != GDN_OK) return st;

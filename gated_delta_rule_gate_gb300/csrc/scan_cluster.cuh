@@ -30,6 +30,7 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 constexpr int kMaxCluster = 16;
+constexpr int kMaxWindow = kMaxCluster * 128;  // tokens that a cluster takes at a time, at most
 
 // (R, H) of a run of one channel: it takes h to R^2 h + H, R^2 being the product of its a.
 // That product itself may leave fp32's range both ways (128 tokens of |g| = 0.7), and a state
@@ -54,7 +55,7 @@ __device__ __forceinline__ float2 fold(float2 k, float2 r) {
 }
 // R of a run whose g add up to sum: without a bias near 1, where runs are many.
 __device__ __forceinline__ float2 root_of(float2 sum) {
-    constexpr float kLog = 88.02969f;  // log of kLargest, rounded down
+    constexpr float kLog = 88.02969f;  // log of kLargest
     return exponential(make_float2(fminf(0.5f * sum.x, kLog), fminf(0.5f * sum.y, kLog))).a;
 }
 

@@ -56,6 +56,7 @@ struct Forward {
     // bf16 gates 16 are the faster).
     static constexpr int kTokens = sizeof(TA) == 2 && sizeof(TG) == 2 ? 16 : 8;
     static constexpr int kTile = WARPS * kTokens;
+    static_assert(kTile * kMaxCluster <= kMaxWindow, "token counts are checked against the largest window");
 
     struct Input {
         Stage<TA, kTokens> x;

@@ -404,7 +404,8 @@ typedef struct gdn_scan_args {
 } gdn_scan_args;
 
 /* gdn_scan -- the recurrence, parallel over channels and along time: one launch,
- * no workspace, the same bits on every run.  For prefill and training. */
+ * no workspace, the same bits on every run.  For prefill and training.  total_tokens is at
+ * most 2^31 - 8193 here and in gdn_scan_backward. */
 gdn_status gdn_scan(const gdn_scan_args *args, gdn_stream stream);
 
 /* gdn_scan_step -- the same result with the tokens of a request taken one after
