@@ -2,8 +2,9 @@
 gdn_rmsnorm, gdn_rmsnorm_backward, gdn_grad_clip (documented in their docstrings).
 
 Their Python entry points are native (csrc/layer_binding.cpp), because a decode step
-is over in the time that Python takes to look at its tensors.  The module is built
-with the library and loaded at the first use of a name.
+is over in the time that Python takes to look at its tensors.  The module is built (by g++,
+against the installed torch) and loaded at the first use of a name; the library and the
+other entry points do without it.
 """
 import ctypes
 import importlib.machinery
@@ -34,6 +35,7 @@ def load():
         if _module is None:
             import torch  # noqa: F401  (the module's symbols come from it)
             lib = N.load()
+            _build.build_binding()  # one of another torch is not loaded
             name = __package__ + "._layer"
             loader = importlib.machinery.ExtensionFileLoader(name, _build.BINDING)
             spec = importlib.util.spec_from_file_location(name, _build.BINDING, loader=loader)
