@@ -236,6 +236,12 @@ Tensor make(IntArrayRef shape, c10::Device device, ScalarType type) {
 }
 Tensor make(IntArrayRef shape, const Tensor &like, ScalarType type) { return make(shape, like.device(), type); }
 
+// The call wrote into these given tensors: autograd is to notice where it has kept one.
+void written(std::initializer_list<const Tensor *> ts) {
+    for (const Tensor *t : ts)
+        if (t && t->defined() && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject *wrap(const Tensor &t) { return t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None); }
 // A named tuple of the tensors (None where undefined).
 PyObject *tuple_of(PyObject *cls, std::initializer_list<const Tensor *> ts) {
@@ -359,6 +365,7 @@ PyObject *py_scan(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
         a.chunk_states = chunks.data_ptr<float>();
     }
     done(lib.scan(&a, stream.get()));
+    written({given, c.fin});
     PyObject *o = given ? Py_NewRef(v[12]) : THPVariable_Wrap(out);
     return keep ? Py_BuildValue("(NN)", o, THPVariable_Wrap(chunks)) : o;
     END_HANDLE_TH_ERRORS
@@ -378,6 +385,7 @@ PyObject *py_step(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
         a.o = out.data_ptr(), a.o_stride = 0;
     }
     done(lib.step(&a, stream.get()));
+    written({given, c.fin});
     return given ? Py_NewRef(v[12]) : THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
 }
@@ -460,6 +468,7 @@ PyObject *py_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
         a.d_initial_state = address<float>(&dinit, f32, "d_initial_state");
     }
     done(lib.backward(&a, stream.get()));
+    for (int i = 14; i < 20; ++i) written({tensor(v[i], "a gradient")});
     return tuple_of(scan_gradients, {&dx, &dg, &db, &dbias, &dscale, &dinit});
     END_HANDLE_TH_ERRORS
 }
@@ -521,6 +530,7 @@ PyObject *py_norm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
     }
     a.out = address(&out, out_type, "out", shape);
     done(lib.norm(&a, stream.get()));
+    written({o, residual ? ro : nullptr, sc});
     return tuple_of(norm_result, {&out, &res_out, &scales, &rstd});
     END_HANDLE_TH_ERRORS
 }
@@ -581,6 +591,7 @@ PyObject *py_norm_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyOb
     a.d_weight = address<float>(&dw, f32, "d_weight", d);
     const Workspace ws(given, given ? 0 : lib.norm_workspace(&a), r);
     done(lib.norm_backward(&a, ws.at, ws.bytes, stream.get()));
+    written({dxg, dwg});
     return tuple_of(norm_gradients, {&dx, &dw});
     END_HANDLE_TH_ERRORS
 }
@@ -648,6 +659,8 @@ PyObject *py_clip(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
     a.error_word = address<int32_t>(err, ScalarType::Int, "error_word");
     const Workspace ws(given, given ? 0 : lib.clip_workspace(&a), norm);
     done(lib.clip(&a, ws.at, ws.bytes, stream.get()));
+    for (Py_ssize_t i = 0; i < grads.n; ++i) written({outs ? &outs->at(i, "an output") : &grads.at(i, "a gradient")});
+    written({given_norm});
     return THPVariable_Wrap(norm);
     END_HANDLE_TH_ERRORS
 }
