@@ -726,7 +726,8 @@ PyMethodDef methods[] = {
      "d_initial_state=None, error_word=None, stream=None, num_state_rows=None)\n--\n\n"
      "Gradients of gdn_scan for the gradient d_out of its output (and d_final_state of\n"
      "its final states): the forward call's arguments and the chunk_states that it\n"
-     "returned.  Returns ScanGradients(dx, d_decay, d_beta, d_gate_bias, d_gate_scale,\n"
+     "returned (initial_state as that call found it: keep a copy of one that it wrote its\n"
+     "final states over).  Returns ScanGradients(dx, d_decay, d_beta, d_gate_bias, d_gate_scale,\n"
      "d_initial_state), None where there is no such input.  Outputs are allocated when\n"
      "not given (zeros where tokens or state rows may belong to no request); a given\n"
      "one is not written there.  num_state_rows says how many rows the forward call's\n"
@@ -753,7 +754,8 @@ PyMethodDef methods[] = {
      "gdn_grad_clip($module, grads, max_norm, *, eps=1e-06, out=None, norm=None, error_word=None, workspace=None, "
      "stream=None)\n--\n\n"
      "The 2-norm of all elements of the tensors grads together, and each scaled by\n"
-     "min(1, max_norm / (norm + eps)): in place, or into the tensors out.  Returns the\n"
+     "min(1, max_norm / (norm + eps)): in place, or into the tensors out.  No tensor\n"
+     "overlaps another.  Returns the\n"
      "norm, float32 [1] on the device (no synchronisation).  A norm that is not finite\n"
      "scales nothing and sets DEVERR_NONFINITE in error_word."},
     {"bind", py_bind, METH_VARARGS, nullptr},

@@ -5,6 +5,10 @@ Their Python entry points are native (csrc/layer_binding.cpp), because a decode 
 is over in the time that Python takes to look at its tensors.  The module is built (by g++,
 against the installed torch) and loaded at the first use of a name; the library and the
 other entry points do without it.
+
+The calls record nothing for autograd: results are plain tensors, whatever the inputs
+require.  examples/recurrent_layer.py wraps forward and gradient calls in
+torch.autograd.Function.
 """
 import ctypes
 import importlib.machinery

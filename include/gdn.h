@@ -416,7 +416,9 @@ gdn_status gdn_scan_step(const gdn_scan_args *args, gdn_stream stream);
 /*
  * gdn_scan_backward -- the gradient of gdn_scan, in one launch, with the same
  * bits on every run.  `forward` is the forward call: its o and final_state are
- * not used, its chunk_states are read (required when there are tokens).  dh
+ * not used, its chunk_states are read (required when there are tokens).  Its
+ * initial_state is read again and has to hold what the forward call found there: where
+ * that call wrote its final states over it, pass a copy made before.  dh
  * being the gradient that reaches a token's state,
  *
  *     dh_t = d_o_t + a_{t+1} dh_{t+1}   (+ d_final_state[row] at a request's last token)
@@ -534,7 +536,8 @@ gdn_status gdn_rmsnorm_backward(const gdn_rmsnorm_grad_args *args, void *workspa
  * The arrays grads, outs, sizes and dtypes are HOST memory, read before the call
  * returns: device pointers, element counts (0: skipped) and gdn_dtypes (F32, F16,
  * BF16; an output has its gradient's).  outs[i] may be grads[i] (outs NULL: all in
- * place); a tensor in place is written only if it is scaled.  The squares and a
+ * place), and else overlaps neither it nor another; a tensor in place is written only if
+ * it is scaled.  The squares and a
  * block's sum are fp32, joined in pairs of fp32, in a fixed order: the same bits on
  * every run (a norm above 1.8e19 counts as infinite).  norm is a device
  * float (or NULL).  A norm that is not finite scales nothing and sets
