@@ -132,7 +132,8 @@ struct Backward {
     };
 
     // The gates of the warp's tokens and its maps, (R, H) and C.  PLAIN: all of them
-    // inside one request, neither its first nor its last token among them.
+    // inside one request, neither its first nor its last token among them, and their channels
+    // whole words where they are stored as such.
     template <bool PLAIN>
     static __device__ __forceinline__ void first_walk(const GradArgs &q, const Input &in, const Tokens &tok, int c,
                                                       int lane, float2 bias, float2 scale, Held &held, float2 &R,
@@ -267,6 +268,7 @@ struct Backward {
         if (at.size > 1) exchange_init(r.x);
         gradient_duties(q, at.size * kWarps, at.me * kWarps + warp, lane, c, blockIdx.x < at.size);
 
+        const bool whole = !WIDE || (whole_words<TA>(p.D, block) && whole_words<TG>(p.D, block));
         Sums sums = {};
         float carry = 0.f;  // c of this thread's channel (see Meet) behind the window
         for (int turn = 0; turn < steps; ++turn, t -= window) {
@@ -289,7 +291,7 @@ struct Backward {
             } else {
                 __syncwarp();
             }
-            const bool plain = tok.own == kAll && !(tok.first | tok.last);
+            const bool plain = tok.own == kAll && !(tok.first | tok.last) && whole;
             Held held;
             float2 R, H, C;
             if (plain) first_walk<true>(q, in, tok, c, lane, bias, scale, held, R, H, C);

@@ -151,6 +151,13 @@ __device__ __forceinline__ bool inside(const Args &p, int t, int tokens, int blo
     return !(t == 0 && block == 0) && !(t + tokens >= p.T && (block + 1) * 64 >= p.D);
 }
 
+// Whether the block's channels end on a 16-byte boundary: a bulk store of a box that ends
+// inside one writes the rest of it too, over what lies behind the row's channels there.
+template <typename T>
+__device__ __forceinline__ bool whole_words(int D, int block) {
+    return (block + 1) * 64 <= D || D * (int)sizeof(T) % 16 == 0;
+}
+
 // [rows, channels] of elements of type T, boxes of 64 channels x `tokens` rows.
 bool make_token_map(CUtensorMap *m, const void *base, int type, int64_t stride, int channels, int rows, int tokens);
 

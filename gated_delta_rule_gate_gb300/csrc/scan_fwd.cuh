@@ -97,7 +97,8 @@ struct Forward {
         }
     }
 
-    // a, u of the warp's tokens and its map.  PLAIN: all of them inside one request.
+    // a, u of the warp's tokens and its map.  PLAIN: all of them inside one request, and their
+    // channels whole words where they are stored as such.
     template <bool PLAIN>
     static __device__ __forceinline__ float4 first_walk(const Args &p, const Input &in, const Tokens &tok, int c,
                                                         int lane, float2 bias, float2 scale, float2 (&a)[kTokens],
@@ -126,7 +127,7 @@ struct Forward {
         return make_float4(R.x, H.x, R.y, H.y);
     }
 
-    // o of the warp's tokens, which a plain run hands to an asynchronous copy.
+    // o of the warp's tokens, which a plain run of whole words hands to an asynchronous copy.
     template <bool PLAIN>
     static __device__ __forceinline__ void second_walk(const Args &p, const Maps &m, Stage<TA, kTokens> &out,
                                                        const Tokens &tok, int t, int block, int lane,
@@ -186,12 +187,13 @@ struct Forward {
         if (at.size > 1) exchange_init(s.x);
         request_duties(p, at.size * WARPS, at.me * WARPS + warp, lane, c, blockIdx.x < at.size);
 
+        const bool whole = !WIDE || whole_words<TA>(p.D, block);
         float carry = 0.f;  // the state of this thread's channel (see Meet) before the window
         for (int step = 0; step < steps; ++step, t += window) {
             const int par = step & 1;
             float2 a[kTokens], u[kTokens];
             const Tokens now = tok;
-            const bool plain = now.own == kAll && !(now.first | now.last);
+            const bool plain = now.own == kAll && !(now.first | now.last) && whole;
             if (WIDE) {
                 if (!ptx::mbar_wait(bar, par) && p.err) atomicOr(p.err, kErrTimeout);
             } else {
