@@ -503,6 +503,7 @@ PyObject *py_norm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
     a.dim = (int32_t)D;
     a.rows = D ? x.numel() / D : 0;
     const Tensor *o = tensor(v[7], "out"), *ro = tensor(v[8], "residual_out"), *sc = tensor(v[9], "scales");
+    if (ro && !residual) refuse(PyExc_ValueError, "residual_out given without residual");
     one_device(x, {{&weight, "weight"}, {residual, "residual"}, {o, "out"}, {ro, "residual_out"}, {sc, "scales"}});
     const Rows xr = rows(x, type, shape, "x");
     a.x = xr.at, a.x_stride = xr.stride;
@@ -530,7 +531,7 @@ PyObject *py_norm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
     }
     a.out = address(&out, out_type, "out", shape);
     done(lib.norm(&a, stream.get()));
-    written({o, residual ? ro : nullptr, sc});
+    written({o, ro, sc});
     return tuple_of(norm_result, {&out, &res_out, &scales, &rstd});
     END_HANDLE_TH_ERRORS
 }
