@@ -10,7 +10,9 @@
 // second time instead.
 //
 // 32768 x 2048 bf16, fp32 residual, e4m3 by groups of 128: 111 us, 6.7 TB/s.
-// 256 x 4096 fp16: 6.3 us, a launch and two trips to memory.
+// 256 x 4096 fp16: 5.3 to 8.0 us, with the buffers' places in memory; a launch and two trips
+// there.  Rows that do not fit, value by value and read twice: 4096 x 16384 fp32 392 us, where
+// HBM would take 129.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -146,8 +148,8 @@ __device__ __forceinline__ void load_sum(const Args &p, size_t row, C column, fl
 }
 
 // V: 8 or 4, words of 16 bytes; 2, rows whose values pair up; 1, rows at any alignment.
-// 16384 rows of bf16 with a residual and scales by group: 2048 wide (V = 8) 49 us,
-// 2046 (V = 2) 86, against 143 by single values; 2047 (V = 1) 129; fp32 77, 84, 126.
+// 16384 rows of bf16 with a residual and scales by group: 2048 wide (V = 8) 46 us,
+// 2046 (V = 2) 85, against 143 by single values; 2047 (V = 1) 129; fp32 74, 81, 125.
 // Eight values a thread at every V: four at V = 1 took 142 us, with fewer bytes on
 // their way.  Rows of up to 512 words take one a thread and four blocks an SM at 32
 // registers; longer ones two.
@@ -337,8 +339,9 @@ cudaError_t launch_rmsnorm_as(const Args &p, int q, int width, cudaStream_t stre
 // in their order: no atomics, the same sum every time.
 //
 // Bound by HBM, and by the wait for each row's sum: forward and gradient of 32768 x
-// 2048 bf16 181 us, 5.2 TB/s; of 16384 x 2046 by pairs 126 against 206 by single values,
-// 16384 x 2048 100.
+// 2048 bf16 181 us, 5.2 TB/s; of 16384 x 2046 by pairs 122 against 206 by single values,
+// 16384 x 2048 96.  Wide rows take two kernels, value by value, that read everything twice:
+// 4096 x 16384 fp32 with its forward 689 us, where HBM would take 277.
 template <typename TA, typename TR, int V, int N>
 __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constant__ GradArgs p, float *partial) {
     ptx::grid_wait();

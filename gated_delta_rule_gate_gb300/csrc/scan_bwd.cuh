@@ -13,9 +13,12 @@
 // forward pass).  x, decay, beta and d_o cross HBM once.  The sums over tokens are
 // kept in registers by channel and joined in a fixed order at the end.
 //
-// Bound by the issue of instructions (178 a token and 64 channels with raw and input
-// gates) and by the exchange of each window: 4 x 8192 x 2048 bf16 with them 311 us, 2.9
-// TB/s; the pass with its forward 455, with the decay given as its logarithm 255.
+// 4 x 8192 x 2048 bf16 with raw and input gates 312 us, 2.9 TB/s; the pass with its forward
+// 466, with the decay given as its logarithm and no input gate 249.  The issue of
+// instructions (183 a token and 64 channels, 53 % of the slots) takes half of it, the waits of
+// each window for its loads and the exchange the rest.  What a warp holds of its tokens
+// between the walks is 64 registers of 128: with raw and input gates and an input scale 112 to
+// 140 bytes a thread are spilled (64 to 164 where rows are read by words).
 #pragma once
 
 #include "scan_cluster.cuh"

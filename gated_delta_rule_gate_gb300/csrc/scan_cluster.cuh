@@ -38,9 +38,10 @@ constexpr int kMaxWindow = kMaxCluster * 128;  // tokens that a cluster takes at
 // small, and what they have grown is forgotten again.  Its root, multiplied by twice, is in
 // range wherever the result is; where it would not be it stops at 2^127, so that a state of
 // zero stays one.  (With the product a window of 16-bit gates of 1 turned zeros to NaN.  The
-// root costs 16384 x 4096 ragged fp16 161 us for 158, a training pass of 4 x 8192 x 2048
-// bf16 471 for 461, and halves the error of long memories.)  A run in which a request begins has R = -0 and takes nothing of what is
-// before it, not even a NaN or an infinity (every other R is +0 at least).
+// root costs 16384 x 4096 ragged fp16 163 us for 158, a training pass of 4 x 8192 x 2048
+// bf16 466 for 461, and halves the error of long memories.)
+// A run in which a request begins has R = -0 and takes nothing of what is before it, not
+// even a NaN or an infinity (every other R is +0 at least).
 constexpr float kBegins = -0.f, kLargest = 0x1p127f;
 __device__ __forceinline__ bool begins(float R) { return __float_as_uint(R) == 0x80000000u; }
 // What the run makes of the state h, if no request begins in it, and if one may.
@@ -332,7 +333,7 @@ inline cudaError_t cluster_blocks(const void *kernel, int warps, size_t smem, in
 // take groups of them side by side, each with fewer blocks: the exchange then joins
 // fewer of them.  As many groups as keep the number of windows within an eighth (rows
 // that do not share out evenly, tiles that two groups cut).  4 x 8192 x 2048 bf16 in
-// clusters of 8: in four groups 144 us, in one 165 us; its training pass 480 and 532.
+// clusters of 8: in four groups 142 us, in one 162 us; its training pass 466 and 539.
 inline void share_out(Args &p, int size, int tile) {
     p.groups = 1, p.per = p.B;
     if (p.cu || p.B < 2) return;

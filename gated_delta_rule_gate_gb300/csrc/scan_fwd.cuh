@@ -16,10 +16,12 @@
 // beta cross HBM once.  A request's first token takes in the request's initial
 // state and nothing of the token before it, so that ragged requests need nothing else.
 //
-// The bound is the issue of instructions, of which the gates' functions are the most:
 // 8 ragged requests of 16384 tokens together x 4096 channels fp16 with raw gates, input
-// gate and states 158 us, where HBM alone would take 79; with the decay given as its
-// logarithm and no input gate 32768 x 2048 bf16 takes 89 us, 66 % of HBM.
+// gate and states take 163 us, where HBM alone would take 79.  Half of it is the issue of
+// instructions, of which the gates' functions are the most (88 a token and 64 channels, 52 %
+// of the slots), the other half each window's wait for its loads and for the exchange, with
+// 3 warps a scheduler to fill it.  With the decay given as its logarithm and no input gate
+// 32768 x 2048 bf16 takes 85 us, 70 % of HBM.
 #pragma once
 
 #include "scan_cluster.cuh"
@@ -52,7 +54,7 @@ struct Maps {
 template <int WARPS, bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
 struct Forward {
     // Long runs cost less of the exchange; with fp32 tensors they would leave room for
-    // one block an SM (32768 tokens x 2048 bf16 with fp32 gates: 164 us at 8, 190 at 16; with
+    // one block an SM (32768 tokens x 2048 bf16 with fp32 gates: 169 us at 8, 190 at 16; with
     // bf16 gates 16 are the faster).
     static constexpr int kTokens = sizeof(TA) == 2 && sizeof(TG) == 2 ? 16 : 8;
     static constexpr int kTile = WARPS * kTokens;
@@ -256,9 +258,9 @@ cudaError_t launch_blocks(const Args &p, int S, cudaStream_t stream) {
     // A pass that keeps states is one of training, between gradients that fill the SMs'
     // shared memory: set up while one still runs, its blocks take the places that come
     // free first, and the whole grid is slower than one set up afterwards (a training
-    // pass of 4096 x 2048 bf16 102 us, 92 so; 32768 x 2048 462 and 452), but for one
-    // window or two, where the launch counts (1024 x 2048 36.0 and 36.4, 999 x 1000 fp32
-    // 31.8 and 33.1).  Without states always early (4096 x 1024 22.2 us, 24.5 not).
+    // pass of 4096 x 2048 bf16 105 us, 97 so; 32768 x 2048 472 and 466), but for one
+    // window or two, where the launch counts (999 x 1000 fp32 33.1 us, 34.4 not early).
+    // Without states always early (4096 x 1024 23.0 us, 24.7 not).
     const int64_t window = (int64_t)(S / q.groups) * F::kTile;
     const bool early = !p.chunk || p.T <= 2 * q.groups * window;
     return launch_clusters((p.D + 63) / 64, S, WARPS, sizeof(typename F::Shared), early, stream,
@@ -267,12 +269,12 @@ cudaError_t launch_blocks(const Args &p, int S, cudaStream_t stream) {
 
 // Of 16-bit tensors blocks of 4 warps are shared out more evenly and wait for fewer
 // others, but a cluster has 16 at most: blocks of 8 where it gets more warps from
-// them.  us with 4 and 8, bf16, raw gates: 16384 x 4096 ragged 158 and 162, 16384 x 2560
-// 97 and 108, 32768 x 2048 136 and 138, 32768 x 512 84 and 77.  Tiles of fp32 tensors are
+// them.  us with 4 and 8, bf16, raw gates: 16384 x 4096 ragged 163 and 165, 16384 x 2560
+// 102 and 112, 32768 x 2048 142 and 143, 32768 x 512 88 and 80.  Tiles of fp32 tensors are
 // half as long, and rows that are read by words want more of them on their way: 8
-// (16384 x 2048 fp32 99 and 97; 16384 x 2047 bf16 237 and 188).  A pass that keeps states
+// (16384 x 2048 fp32 104 and 103; 16384 x 2047 bf16 240 and 196).  A pass that keeps states
 // takes 8 too: the small blocks leave a gradient that is set up beside them no room for
-// two on an SM (a training pass of 32768 x 2048 520 us, 462 with 8).
+// two on an SM (a training pass of 32768 x 2048 471 us, 466 with 8).
 template <bool WIDE, typename TA, typename TG, bool RAW, bool BETA, int MODE>
 cudaError_t launch_one(const Args &p, cudaStream_t stream) {
     int eights = 1;

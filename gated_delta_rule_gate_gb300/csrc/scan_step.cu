@@ -5,7 +5,7 @@
 // and walks its tokens: h = a h + n i x.  Bound by HBM at many requests (a state
 // row in and out, 8 bytes a channel, beside the token's tensors) and by launch
 // and memory latency at few; all loads of a token are issued together.  256 x 4096
-// fp16 with raw and input gates 4.3 us, of which HBM takes 2.5; 1 x 2048 3.0 us.
+// fp16 with raw and input gates 4.4 us, of which HBM takes 2.5; 1 x 2048 3.1 us.
 #include "launch.h"
 #include "ptx.cuh"
 #include "scan_launch.h"
