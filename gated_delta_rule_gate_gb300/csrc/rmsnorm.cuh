@@ -69,19 +69,20 @@ __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
 // Scale of a row or group whose largest |y| is m, and the quotients by it.  y / s itself: a
 // product with 1 / s puts values at the edge of two steps on the other one.  A division
 // for each value made 32768 x 2048 bf16 with scales by group 115 us, this 111 (110 by the
-// product alone): the product's remainder is exact in one fma, and a second one rounds the quotient as a division does
-// (Markstein 1990; 1 / s is rounded once, and neither it nor the remainder underflows where a
-// step of e4m3 could tell).
+// product alone): the product's remainder is exact in one fma, and a second one rounds the
+// quotient as a division does (Markstein 1990; 1 / s is rounded once, and neither it nor the
+// remainder underflows where a step of e4m3 could tell).  The remainder is taken as s q - y,
+// so that a y of -0 gives -0.
 struct Scale {
-    float s, inv, minus;
+    float s, inv, times;
     __device__ __forceinline__ explicit Scale(float m) {
         s = fmaxf(m, 0x1p-100f) / kE4m3Max;
         inv = 1.f / s;
-        minus = isfinite(s) ? -s : 0.f;
+        times = isfinite(s) ? s : 0.f;
     }
     __device__ __forceinline__ float under(float y) const {
         const float q = y * inv;
-        return fmaf(fmaf(minus, q, y), inv, q);
+        return fmaf(fmaf(times, q, -y), -inv, q);
     }
 };
 // Columns c, ... of a row of n bytes.
@@ -137,7 +138,7 @@ __device__ __forceinline__ void load_sum(const Args &p, size_t row, C column, fl
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int k = 0; k < V; ++k) q[i][k] = 0.f;
+            for (int k = 0; k < V; ++k) q[i][k] = -0.f;  // x + -0 is x, of either zero
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {

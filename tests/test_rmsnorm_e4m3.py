@@ -31,3 +31,20 @@ def test_out_is_y_over_s(n, D, act, group):
     peak = torch.stack([p.abs().amax(1) for p in y.split(group or D, dim=1)], 1) / 448
     # the scale of a row is formed of max |r weight|, times rstd: three roundings of fp32 apart
     assert bool(((scales.view(n, -1) - peak).abs() <= 4 * 2.0 ** -24 * peak).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [520, 518, 517, 8201])
+@pytest.mark.parametrize("group", [0, 128])
+def test_zeros_keep_their_signs(D, group):
+    import gated_delta_rule_gate_gb300 as g
+    gen = torch.Generator().manual_seed(D)
+    x = torch.randn(20, D, generator=gen)
+    x[:, ::7] = 0.0
+    x[:, 1::7] = -0.0
+    x[0] = -0.0  # a whole row
+    w = torch.randn(D, generator=gen)
+    out = g.gdn_rmsnorm(x.cuda(), w.cuda(), out_dtype=E4M3, group=group).out.cpu()
+    zero = x == 0
+    want = torch.where(torch.signbit(x) != torch.signbit(w), 128, 0)[zero].to(torch.uint8)
+    assert torch.equal(out.view(torch.uint8)[zero], want)
