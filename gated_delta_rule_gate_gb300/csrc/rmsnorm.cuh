@@ -9,7 +9,7 @@
 // Rows that do not fit (more than kFit values, or 16384 in words of 8) are walked a
 // second time instead.
 //
-// 32768 x 2048 bf16, fp32 residual, e4m3 by groups of 128: 111 us, 6.7 TB/s.
+// 32768 x 2048 bf16, fp32 residual, e4m3 by groups of 128: 110 us, 6.7 TB/s.
 // 256 x 4096 fp16: 5.3 to 8.0 us, with the buffers' places in memory; a launch and two trips
 // there.  Rows that do not fit, value by value and read twice: 4096 x 16384 fp32 392 us, where
 // HBM would take 129.
@@ -68,8 +68,8 @@ __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
 }
 // Scale of a row or group whose largest |y| is m, and the quotients by it.  y / s itself: a
 // product with 1 / s puts values at the edge of two steps on the other one.  A division
-// for each value made 32768 x 2048 bf16 with scales by group 115 us, this 111 (110 by the
-// product alone): the product's remainder is exact in one fma, and a second one rounds the
+// for each value made 32768 x 2048 bf16 with scales by group 115 us, this 110, as the
+// product alone: the product's remainder is exact in one fma, and a second one rounds the
 // quotient as a division does (Markstein 1990; 1 / s is rounded once, and neither it nor the
 // remainder underflows where a step of e4m3 could tell).  The remainder is taken as s q - y,
 // so that a y of -0 gives -0.
