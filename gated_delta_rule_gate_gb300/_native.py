@@ -23,7 +23,10 @@ EXPORTS = ("gdn_gate", "gdn_recurrent_step", "gdn_chunked_prefill_workspace_size
            "gdn_chunked_prefill_workspace_size_min", "gdn_chunked_prefill", "gdn_chunked_prefill_noalloc",
            "gdn_status_string", "gdn_last_error_message", "gdn_scan", "gdn_scan_step",
            "gdn_scan_backward", "gdn_rmsnorm", "gdn_rmsnorm_backward", "gdn_rmsnorm_backward_workspace_size",
-           "gdn_grad_clip", "gdn_grad_clip_workspace_size")
+           "gdn_grad_clip", "gdn_grad_clip_workspace_size", "gdn_glu", "gdn_glu_workspace_size", "gdn_glu_backward",
+           "gdn_glu_backward_workspace_size", "gdn_adamw")
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
+ADAMW_BLOCK = 256
 INPUT_SCALES = {"none": 0, "lerp": 1, "unit": 2}
 SCAN_CHUNK = 64
 
@@ -112,6 +115,40 @@ class GdnGradClipArgs(ctypes.Structure):
     ]
 
 
+class GdnGluArgs(ctypes.Structure):
+    """Mirror of ``gdn_glu_args`` (include/gdn.h)."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("dim", ctypes.c_int32), ("inner", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32), ("x_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+        ("x", _vp), ("w_gate", _vp), ("w_up", _vp), ("out", _vp), ("gates", _vp), ("error_word", _vp),
+    ]
+
+
+class GdnGluGradArgs(ctypes.Structure):
+    """Mirror of ``gdn_glu_grad_args`` (include/gdn.h)."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("dim", ctypes.c_int32), ("inner", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32), ("x_stride", ctypes.c_int64), ("d_out_stride", ctypes.c_int64),
+        ("dx_stride", ctypes.c_int64), ("d_out", _vp), ("x", _vp), ("w_gate", _vp), ("w_up", _vp), ("gates", _vp),
+        ("dx", _vp), ("d_w_gate", _vp), ("d_w_up", _vp), ("error_word", _vp),
+    ]
+
+
+class GdnAdamwArgs(ctypes.Structure):
+    """Mirror of ``gdn_adamw_args`` (include/gdn.h)."""
+    _fields_ = [
+        ("count", ctypes.c_int32), ("state_dtype", ctypes.c_int32), ("step", ctypes.c_int64), ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+        ("weight_decay", ctypes.c_double), ("max_norm", ctypes.c_double), ("norm_eps", ctypes.c_double),
+        ("params", ctypes.POINTER(_vp)), ("grads", ctypes.POINTER(_vp)), ("exp_avg", ctypes.POINTER(_vp)),
+        ("exp_avg_sq", ctypes.POINTER(_vp)), ("exp_avg_scales", ctypes.POINTER(_vp)),
+        ("exp_avg_sq_scales", ctypes.POINTER(_vp)), ("master", ctypes.POINTER(_vp)),
+        ("sizes", ctypes.POINTER(ctypes.c_int64)), ("param_dtypes", ctypes.POINTER(ctypes.c_int32)),
+        ("grad_dtypes", ctypes.POINTER(ctypes.c_int32)), ("step_device", _vp), ("lr_device", _vp),
+        ("grad_norm", _vp), ("error_word", _vp),
+    ]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status, message):
         self.status = status
@@ -155,10 +192,12 @@ def load():
         lib.gdn_chunked_prefill_noalloc.argtypes = [ctypes.POINTER(GdnProblem), ctypes.c_int32, _vp]
         lib.gdn_chunked_prefill_noalloc.restype = ctypes.c_int
         for name, args in (("gdn_scan", GdnScanArgs), ("gdn_scan_step", GdnScanArgs),
-                           ("gdn_scan_backward", GdnScanGradArgs), ("gdn_rmsnorm", GdnRmsnormArgs)):
+                           ("gdn_scan_backward", GdnScanGradArgs), ("gdn_rmsnorm", GdnRmsnormArgs),
+                           ("gdn_adamw", GdnAdamwArgs)):
             getattr(lib, name).argtypes = [ctypes.POINTER(args), _vp]
             getattr(lib, name).restype = ctypes.c_int
-        for name, args in (("gdn_rmsnorm_backward", GdnRmsnormGradArgs), ("gdn_grad_clip", GdnGradClipArgs)):
+        for name, args in (("gdn_rmsnorm_backward", GdnRmsnormGradArgs), ("gdn_grad_clip", GdnGradClipArgs),
+                           ("gdn_glu", GdnGluArgs), ("gdn_glu_backward", GdnGluGradArgs)):
             getattr(lib, name).argtypes = [ctypes.POINTER(args), _vp, ctypes.c_size_t, _vp]
             getattr(lib, name).restype = ctypes.c_int
             getattr(lib, name + "_workspace_size").argtypes = [ctypes.POINTER(args)]

@@ -1,0 +1,313 @@
+// glu_api.cu -- the C entry points of the gated feed-forward: host-side validation,
+// the operands' tensor maps, and copies of operands whose rows are no words of 16 bytes.
+#include <cuda.h>
+
+#include "glu_launch.h"
+#include "launch.h"
+#include "ptx.cuh"
+#include "status.h"
+
+namespace gdn {
+namespace glu {
+
+bool make_map(CUtensorMap *m, const void *base, bool bf16, int64_t stride, int64_t cols, int64_t rows, int box) {
+    typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e =
+            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
+        return reinterpret_cast<Encode>(e == cudaSuccess && q == cudaDriverEntryPointSuccess ? ptr : nullptr);
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t boxes[2] = {64, (cuuint32_t)box}, step[2] = {1, 1};
+    return encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                  const_cast<void *>(base), dims, strides, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A thread a value: what is copied so is little beside the product that follows.
+__global__ void __launch_bounds__(256) spread_kernel(const uint16_t *src, uint16_t *dst, int64_t n, int cols,
+                                                     int64_t from, int64_t to) {
+    ptx::grid_wait();
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / cols;
+        const int c = (int)(i - row * cols);
+        dst[row * to + c] = src[row * from + c];
+    }
+}
+cudaError_t launch_spread(const void *src, void *dst, int64_t rows, int cols, int64_t from, int64_t to,
+                          cudaStream_t stream) {
+    const int64_t n = rows * cols, blocks = (n + 255) / 256, most = (int64_t)sm_count() * 16;
+    return launch_early(spread_kernel, (unsigned)(blocks < most ? blocks : most), 256, 0, stream,
+                        static_cast<const uint16_t *>(src), static_cast<uint16_t *>(dst), n, cols, from, to);
+}
+
+}  // namespace glu
+}  // namespace gdn
+
+namespace {
+
+using namespace gdn::glu;
+using gdn::aligned;
+using gdn::fail;
+
+constexpr int kMost = 1 << 20;
+
+int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
+// Rows that a tensor map takes: words of 16 bytes.
+bool lines(const void *p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; }
+int64_t or_dense(int64_t stride, int64_t dense) { return stride ? stride : dense; }
+
+gdn_status check_stride(int64_t stride, int least, const char *what) {
+    if (stride != 0 && stride < least)
+        return fail(GDN_ERR_INVALID, "%s (%lld) is less than a row (%d)", what, (long long)stride, least);
+    return GDN_OK;
+}
+gdn_status check_sizes(int64_t rows, int dim, int inner, int dtype, int act) {
+    if (rows < 0) return fail(GDN_ERR_INVALID, "rows must be >= 0");
+    if (rows > (1LL << 31) - 512) return fail(GDN_ERR_UNSUPPORTED, "more than 2^31 - 512 rows are not supported");
+    if (dim <= 0 || inner <= 0) return fail(GDN_ERR_INVALID, "dim and inner must be positive (got %d, %d)", dim, inner);
+    if (dim > kMost || inner > kMost) return fail(GDN_ERR_UNSUPPORTED, "dim and inner above %d are not supported", kMost);
+    if (dtype == GDN_DTYPE_F32) return fail(GDN_ERR_UNSUPPORTED, "dtype: the products take 16-bit operands, not float32");
+    if (dtype != GDN_DTYPE_F16 && dtype != GDN_DTYPE_BF16) return fail(GDN_ERR_INVALID, "unknown dtype %d", dtype);
+    if (act < GDN_ACT_SILU || act > GDN_ACT_SIGMOID) return fail(GDN_ERR_INVALID, "unknown activation %d", act);
+    return GDN_OK;
+}
+
+gdn_status validate(const gdn_glu_args *a) {
+    if (!a) return fail(GDN_ERR_INVALID, "args is NULL");
+    gdn_status st;
+    if ((st = check_sizes(a->rows, a->dim, a->inner, a->dtype, a->activation)) != GDN_OK) return st;
+    if ((st = check_stride(a->x_stride, a->dim, "x_stride")) != GDN_OK) return st;
+    if ((st = check_stride(a->out_stride, a->inner, "out_stride")) != GDN_OK) return st;
+    if (a->rows > 0 && (!a->x || !a->w_gate || !a->w_up || !a->out))
+        return fail(GDN_ERR_INVALID, "x, w_gate, w_up and out are required");
+    if (!aligned(a->x, 2) || !aligned(a->w_gate, 2) || !aligned(a->w_up, 2) || !aligned(a->out, 2) ||
+        !aligned(a->gates, 2) || !aligned(a->error_word, 4))
+        return fail(GDN_ERR_INVALID, "a pointer is not aligned to its element size");
+    return GDN_OK;
+}
+gdn_status validate_grad(const gdn_glu_grad_args *a) {
+    if (!a) return fail(GDN_ERR_INVALID, "args is NULL");
+    gdn_status st;
+    if ((st = check_sizes(a->rows, a->dim, a->inner, a->dtype, a->activation)) != GDN_OK) return st;
+    if ((st = check_stride(a->x_stride, a->dim, "x_stride")) != GDN_OK) return st;
+    if ((st = check_stride(a->d_out_stride, a->inner, "d_out_stride")) != GDN_OK) return st;
+    if ((st = check_stride(a->dx_stride, a->dim, "dx_stride")) != GDN_OK) return st;
+    if ((a->d_w_gate == nullptr) != (a->d_w_up == nullptr))
+        return fail(GDN_ERR_INVALID, "d_w_gate and d_w_up go together");
+    if (!a->dx && !a->d_w_gate) return fail(GDN_ERR_INVALID, "dx, or d_w_gate and d_w_up, are required");
+    if (a->rows > 0 && (!a->d_out || !a->gates)) return fail(GDN_ERR_INVALID, "d_out and gates are required");
+    if (a->rows > 0 && a->dx && (!a->w_gate || !a->w_up)) return fail(GDN_ERR_INVALID, "w_gate and w_up are required");
+    if (a->rows > 0 && a->d_w_gate && !a->x) return fail(GDN_ERR_INVALID, "x is required");
+    if (!aligned(a->x, 2) || !aligned(a->w_gate, 2) || !aligned(a->w_up, 2) || !aligned(a->d_out, 2) ||
+        !aligned(a->gates, 2) || !aligned(a->dx, 2) || !aligned(a->d_w_gate, 2) || !aligned(a->d_w_up, 2) ||
+        !aligned(a->error_word, 4))
+        return fail(GDN_ERR_INVALID, "a pointer is not aligned to its element size");
+    return GDN_OK;
+}
+
+// A workspace given out piece by piece, in multiples of 256 bytes; without memory it counts.
+struct Pieces {
+    unsigned char *base;
+    size_t used = 0;
+    void *take(int64_t values) {
+        void *p = base ? base + used : nullptr;
+        used += ((size_t)values * 2 + 255) / 256 * 256;
+        return p;
+    }
+};
+// An operand as a tensor map takes it: itself, or a copy.
+struct Operand {
+    const void *at;
+    int64_t stride, cols, rows;
+    const void *from = nullptr;  // what is copied, and its rows' distance
+    int64_t from_stride = 0;
+};
+Operand operand(const void *p, int64_t rows, int64_t cols, int64_t stride, Pieces *ws) {
+    Operand o = {p, stride, cols, rows};
+    if (lines(p, stride)) return o;
+    o.from = p, o.from_stride = stride, o.stride = padded(cols);
+    o.at = ws->take(rows * o.stride);
+    return o;
+}
+cudaError_t bring(const Operand &o, cudaStream_t s) {
+    if (!o.from) return cudaSuccess;
+    return launch_spread(o.from, const_cast<void *>(o.at), o.rows, (int)o.cols, o.from_stride, o.stride, s);
+}
+bool map_of(CUtensorMap *m, const Operand &o, bool bf16, int box) {
+    return make_map(m, o.at, bf16, o.stride, o.cols, o.rows, box);
+}
+Result result_of(void *at, int64_t stride) {
+    Result r = {};
+    r.at = at, r.stride = stride;
+    return r;
+}
+bool map_results(Product *p, int count, bool bf16) {
+    p->by_map = 1;
+    for (int i = 0; i < count; ++i) p->by_map = p->by_map && lines(p->c[i].at, p->c[i].stride);
+    for (int i = 0; p->by_map && i < count; ++i)
+        if (!make_map(&p->c[i].map, p->c[i].at, bf16, p->c[i].stride, p->cols, p->rows, 32)) return false;
+    return true;
+}
+void tiles_of(Product *p, int64_t rows, int cols, int width, int results, int64_t depth) {
+    p->rows = rows, p->cols = cols;
+    p->tiles_m = (rows + 255) / 256, p->tiles_n = (cols + width - 1) / width;
+    p->tiles = p->tiles_m * p->tiles_n * results;
+    p->blocks_k = (int)((depth + 63) / 64);
+}
+cudaError_t launch(const Product &p, Mode mode, bool bf16, cudaStream_t s) {
+    return bf16 ? launch_product_bf16(p, mode, s) : launch_product_f16(p, mode, s);
+}
+gdn_status no_map() { return fail(GDN_ERR_CUDA, "a tensor map could not be made"); }
+
+struct Forward {
+    bool few;
+    Operand x, wg, wu;
+    size_t bytes;
+};
+Forward plan(const gdn_glu_args *a, void *ws) {
+    Forward f = {};
+    f.few = a->rows <= kFewTokens;
+    if (f.few || a->rows == 0) return f;
+    Pieces pieces = {static_cast<unsigned char *>(ws)};
+    f.x = operand(a->x, a->rows, a->dim, or_dense(a->x_stride, a->dim), &pieces);
+    f.wg = operand(a->w_gate, a->inner, a->dim, a->dim, &pieces);
+    f.wu = operand(a->w_up, a->inner, a->dim, a->dim, &pieces);
+    f.bytes = pieces.used;
+    return f;
+}
+
+struct Backward {
+    Operand x, wg, wu, dg, du;
+    size_t bytes;
+};
+Backward plan_grad(const gdn_glu_grad_args *a, void *ws) {
+    Backward b = {};
+    if (a->rows == 0) return b;
+    Pieces pieces = {static_cast<unsigned char *>(ws)};
+    const int64_t F = a->inner, Fp = padded(F);
+    b.dg = {pieces.take(a->rows * Fp), Fp, F, a->rows};
+    b.du = {pieces.take(a->rows * Fp), Fp, F, a->rows};
+    if (a->d_w_gate) b.x = operand(a->x, a->rows, a->dim, or_dense(a->x_stride, a->dim), &pieces);
+    if (a->dx) {
+        b.wg = operand(a->w_gate, F, a->dim, a->dim, &pieces);
+        b.wu = operand(a->w_up, F, a->dim, a->dim, &pieces);
+    }
+    b.bytes = pieces.used;
+    return b;
+}
+
+gdn_status check_workspace(const void *ws, size_t have, size_t need) {
+    if (need > 0 && (ws == nullptr || have < need || !aligned(ws, 16)))
+        return fail(GDN_ERR_WORKSPACE, "workspace needs %zu bytes, 16-byte aligned (got %zu)", need, have);
+    return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_glu_workspace_size(const gdn_glu_args *a) {
+    if (validate(a) != GDN_OK) return (size_t)-1;
+    gdn::ok();
+    return plan(a, nullptr).bytes;
+}
+
+gdn_status gdn_glu(const gdn_glu_args *a, void *ws, size_t ws_bytes, gdn_stream stream) {
+    gdn_status st = validate(a);
+    if (st != GDN_OK) return st;
+    if ((st = check_workspace(ws, ws_bytes, plan(a, nullptr).bytes)) != GDN_OK) return st;
+    if (a->rows == 0) return gdn::ok();
+    const Forward f = plan(a, ws);
+    const bool bf16 = a->dtype == GDN_DTYPE_BF16;
+    const int64_t os = or_dense(a->out_stride, a->inner);
+    cudaStream_t s = (cudaStream_t)stream;
+    if (f.few) {
+        Few p = {};
+        p.x = a->x, p.wg = a->w_gate, p.wu = a->w_up, p.out = a->out, p.gates = a->gates;
+        p.xs = or_dense(a->x_stride, a->dim), p.os = os;
+        p.T = (int)a->rows, p.D = a->dim, p.F = a->inner, p.act = a->activation;
+        p.words = lines(a->x, p.xs) && lines(a->w_gate, a->dim) && lines(a->w_up, a->dim);
+        return gdn::cuda_status(bf16 ? launch_few_bf16(p, s) : launch_few_f16(p, s));
+    }
+    Product p = {};
+    tiles_of(&p, a->rows, a->inner, 128, 1, a->dim);
+    p.act = a->activation, p.gates = a->gates != nullptr, p.err = a->error_word;
+    p.c[0] = result_of(a->out, os);
+    if (a->gates) {
+        p.c[1] = result_of(a->gates, 2 * (int64_t)a->inner);
+        p.c[2] = result_of(static_cast<uint16_t *>(a->gates) + a->inner, 2 * (int64_t)a->inner);
+    }
+    if (!map_of(&p.a[0], f.x, bf16, 128) || !map_of(&p.b[0], f.wg, bf16, 128) || !map_of(&p.b[1], f.wu, bf16, 128) ||
+        !map_results(&p, a->gates ? 3 : 1, bf16))
+        return no_map();
+    cudaError_t e = bring(f.x, s);
+    if (e == cudaSuccess) e = bring(f.wg, s);
+    if (e == cudaSuccess) e = bring(f.wu, s);
+    if (e == cudaSuccess) e = launch(p, kForward, bf16, s);
+    return gdn::cuda_status(e);
+}
+
+size_t gdn_glu_backward_workspace_size(const gdn_glu_grad_args *a) {
+    if (validate_grad(a) != GDN_OK) return (size_t)-1;
+    gdn::ok();
+    return plan_grad(a, nullptr).bytes;
+}
+
+gdn_status gdn_glu_backward(const gdn_glu_grad_args *a, void *ws, size_t ws_bytes, gdn_stream stream) {
+    gdn_status st = validate_grad(a);
+    if (st != GDN_OK) return st;
+    if ((st = check_workspace(ws, ws_bytes, plan_grad(a, nullptr).bytes)) != GDN_OK) return st;
+    cudaStream_t s = (cudaStream_t)stream;
+    const int64_t T = a->rows;
+    const int D = a->dim, F = a->inner;
+    cudaError_t e = cudaSuccess;
+    if (T == 0) {  // sums over nothing
+        const size_t bytes = (size_t)F * D * 2;
+        if (a->d_w_gate) e = cudaMemsetAsync(a->d_w_gate, 0, bytes, s);
+        if (a->d_w_up && e == cudaSuccess) e = cudaMemsetAsync(a->d_w_up, 0, bytes, s);
+        return gdn::cuda_status(e);
+    }
+    const Backward b = plan_grad(a, ws);
+    const bool bf16 = a->dtype == GDN_DTYPE_BF16;
+    Product in = {}, w = {};
+    if (a->dx) {
+        tiles_of(&in, T, D, 256, 1, F);
+        in.err = a->error_word;
+        in.c[0] = result_of(a->dx, or_dense(a->dx_stride, D));
+        if (!map_of(&in.a[0], b.dg, bf16, 128) || !map_of(&in.a[1], b.du, bf16, 128) ||
+            !map_of(&in.b[0], b.wg, bf16, 64) || !map_of(&in.b[1], b.wu, bf16, 64) || !map_results(&in, 1, bf16))
+            return no_map();
+    }
+    if (a->d_w_gate) {
+        tiles_of(&w, F, D, 256, 2, T);
+        w.err = a->error_word;
+        w.c[0] = result_of(a->d_w_gate, D), w.c[1] = result_of(a->d_w_up, D);
+        if (!map_of(&w.a[0], b.dg, bf16, 64) || !map_of(&w.a[1], b.du, bf16, 64) || !map_of(&w.b[0], b.x, bf16, 64) ||
+            !map_results(&w, 2, bf16))
+            return no_map();
+    }
+    GateGrad g = {};
+    g.d_out = a->d_out, g.gates = a->gates, g.dg = const_cast<void *>(b.dg.at), g.du = const_cast<void *>(b.du.at);
+    g.rows = T, g.dos = or_dense(a->d_out_stride, F), g.ds = b.dg.stride, g.F = F, g.act = a->activation;
+    g.words = F % 8 == 0 && lines(a->d_out, g.dos) && aligned(a->gates, 16);
+    e = bf16 ? launch_gate_grad_bf16(g, s) : launch_gate_grad_f16(g, s);
+    if (e == cudaSuccess && a->dx) {
+        e = bring(b.wg, s);
+        if (e == cudaSuccess) e = bring(b.wu, s);
+        if (e == cudaSuccess) e = launch(in, kInput, bf16, s);
+    }
+    if (e == cudaSuccess && a->d_w_gate) {
+        e = bring(b.x, s);
+        if (e == cudaSuccess) e = launch(w, kWeights, bf16, s);
+    }
+    return gdn::cuda_status(e);
+}
+
+}  // extern "C"

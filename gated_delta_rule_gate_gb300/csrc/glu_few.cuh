@@ -1,0 +1,155 @@
+// glu_few.cuh -- the gated feed-forward of few tokens, and the element-wise part of
+// its gradient.
+//
+// Few tokens: bound by the weights' way from HBM.  A block has 8 output features, whose
+// 8 rows of w_gate and 8 of w_up are the 16 rows of a warp-level product (m16n8k16), so
+// that a thread's accumulators hold gate and up of the same outputs.  The order of k
+// within a product is free: a lane takes 8 adjacent values (16 bytes) of its two weight
+// rows and of its token, which are its operands of two products over 32 k's.  The 8
+// warps share the k's out and add their sums up at the end, in one order.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "glu_launch.h"
+#include "glu_math.cuh"
+#include "launch.h"
+#include "ptx.cuh"
+#include "values.cuh"
+
+namespace gdn {
+namespace glu {
+
+constexpr int kFewWarps = 8, kFeatures = 8;
+constexpr int kAhead = 4;  // loads of a weight row in flight per lane
+
+template <typename T>
+__device__ __forceinline__ void product16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same<T, __half>::value) ptx::mma16816(d, a, b0, b1);
+    else ptx::mma16816_bf16(d, a, b0, b1);
+}
+// 8 values of a row of D from k on, zeros beyond it; WORDS: rows are words of 16 bytes.
+template <bool WORDS>
+__device__ __forceinline__ uint4 load8(const uint16_t *row, int k, int D) {
+    if constexpr (WORDS) {
+        return k < D ? *reinterpret_cast<const uint4 *>(row + k) : make_uint4(0, 0, 0, 0);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = k + 2 * i < D ? row[k + 2 * i] : 0, hi = k + 2 * i + 1 < D ? row[k + 2 * i + 1] : 0;
+            w[i] = lo | hi << 16;
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// NT: groups of 8 tokens.
+template <typename T, int NT, bool WORDS>
+__global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const __grid_constant__ Few p) {
+    __shared__ float sums[kFewWarps][NT][16][9];
+    ptx::grid_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int f = blockIdx.x * kFeatures + g;
+    const int fr = f < p.F ? f : p.F - 1;  // rows beyond the last are not kept
+    const uint16_t *wg = static_cast<const uint16_t *>(p.wg) + (int64_t)fr * p.D;
+    const uint16_t *wu = static_cast<const uint16_t *>(p.wu) + (int64_t)fr * p.D;
+    const uint16_t *x[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int tok = 8 * n + g;
+        x[n] = tok < p.T ? static_cast<const uint16_t *>(p.x) + tok * p.xs : nullptr;
+    }
+    float acc[NT][4] = {};
+    // a warp's steps of 32 k's: kAhead adjacent ones at a time
+    const int steps = (p.D + 31) / 32;
+    for (int s0 = warp * kAhead; s0 < steps; s0 += kFewWarps * kAhead) {
+        uint4 a[kAhead], b[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int k = (s0 + i) * 32 + 8 * t;
+            a[i] = load8<WORDS>(wg, k, p.D);
+            b[i] = load8<WORDS>(wu, k, p.D);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int k = (s0 + i) * 32 + 8 * t;
+            const uint32_t first[4] = {a[i].x, b[i].x, a[i].y, b[i].y}, second[4] = {a[i].z, b[i].z, a[i].w, b[i].w};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint4 v = x[n] ? load8<WORDS>(x[n], k, p.D) : make_uint4(0, 0, 0, 0);
+                product16<T>(acc[n], first, v.x, v.y);
+                product16<T>(acc[n], second, v.z, v.w);
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        sums[warp][n][g][2 * t] = acc[n][0], sums[warp][n][g][2 * t + 1] = acc[n][1];
+        sums[warp][n][8 + g][2 * t] = acc[n][2], sums[warp][n][8 + g][2 * t + 1] = acc[n][3];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 64 * NT; i += 32 * kFewWarps) {
+        const int e = i & 7, tok = i >> 3, n = tok >> 3, c = tok & 7, at = blockIdx.x * kFeatures + e;
+        if (tok >= p.T || at >= p.F) continue;
+        float gate = 0.f, up = 0.f;
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) gate += sums[w][n][e][c], up += sums[w][n][8 + e][c];
+        static_cast<T *>(p.out)[tok * p.os + at] = static_cast<T>(activation(gate, p.act) * up);
+        if (p.gates) {
+            T *row = static_cast<T *>(p.gates) + (int64_t)tok * 2 * p.F + at;
+            row[0] = static_cast<T>(gate);
+            row[p.F] = static_cast<T>(up);
+        }
+    }
+}
+
+template <typename T, int NT>
+cudaError_t launch_few_of(const Few &p, cudaStream_t stream) {
+    const unsigned blocks = (unsigned)((p.F + kFeatures - 1) / kFeatures);
+    return p.words ? launch_early(few_kernel<T, NT, true>, blocks, 32 * kFewWarps, 0, stream, p)
+                   : launch_early(few_kernel<T, NT, false>, blocks, 32 * kFewWarps, 0, stream, p);
+}
+template <typename T>
+cudaError_t launch_few(const Few &p, cudaStream_t stream) {
+    static_assert(kFewTokens == 16, "groups of 8 tokens");
+    return p.T <= 8 ? launch_few_of<T, 1>(p, stream) : launch_few_of<T, 2>(p, stream);
+}
+
+// ---------------------------------------------------------------- gradient, element by element
+// d_g = d_out u act'(g) and d_u = d_out act(g), V adjacent values a thread.  Bound by HBM.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) gate_grad_kernel(const __grid_constant__ GateGrad p) {
+    ptx::grid_wait();
+    const int per = p.F / V;
+    const int64_t n = p.rows * per;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / per;
+        const int c = (int)(i - row * per) * V;
+        float d[V], g[V], u[V], dg[V], du[V];
+        load_values<T, V>(static_cast<const T *>(p.d_out) + row * p.dos + c, d);
+        load_values<T, V>(static_cast<const T *>(p.gates) + row * 2 * p.F + c, g);
+        load_values<T, V>(static_cast<const T *>(p.gates) + row * 2 * p.F + p.F + c, u);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float2 a = activation_slope(g[e], p.act);
+            dg[e] = d[e] * u[e] * a.y;
+            du[e] = d[e] * a.x;
+        }
+        store_values<T, V>(static_cast<T *>(p.dg) + row * p.ds + c, dg);
+        store_values<T, V>(static_cast<T *>(p.du) + row * p.ds + c, du);
+    }
+}
+template <typename T>
+cudaError_t launch_gate_grad(const GateGrad &p, cudaStream_t stream) {
+    const int v = p.words ? 8 : 1;
+    const int64_t blocks = (p.rows * (p.F / v) + 255) / 256, most = (int64_t)sm_count() * 16;
+    if (blocks == 0) return cudaSuccess;
+    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+    return v == 8 ? launch_early(gate_grad_kernel<T, 8>, grid, 256, 0, stream, p)
+                  : launch_early(gate_grad_kernel<T, 1>, grid, 256, 0, stream, p);
+}
+
+}  // namespace glu
+}  // namespace gdn

@@ -1,0 +1,61 @@
+// glu_launch.h -- what the host side of the gated feed-forward hands to its kernels.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gdn {
+namespace glu {
+
+// The products, by the operands' order in memory and what is done with the result:
+// kForward: out = act(x w_gate^T) (x w_up^T); kInput: dx = d_g w_gate + d_u w_up;
+// kWeights: d_w = d^T x, of both weights.
+enum Mode { kForward, kInput, kWeights };
+
+// A result's rows: by tensor map where they are words of 16 bytes, else element by element.
+struct Result {
+    CUtensorMap map;
+    void *at;
+    int64_t stride;
+};
+struct Product {
+    CUtensorMap a[2], b[2];
+    Result c[3];
+    int64_t rows, tiles_m, tiles;  // tiles: of all results
+    int cols, tiles_n, blocks_k;   // blocks_k: of 64, of one pair of operands
+    int act, gates, by_map;
+    int32_t *err;
+};
+// Fewer tokens than the tensor cores' tiles are made for.
+struct Few {
+    const void *x, *wg, *wu;
+    void *out, *gates;  // gates may be null
+    int64_t xs, os;
+    int T, D, F, act, words;
+};
+// d_g and d_u of d_out and the gates that the forward pass kept.
+struct GateGrad {
+    const void *d_out, *gates;
+    void *dg, *du;
+    int64_t rows, dos, ds;  // ds: elements between rows of dg and du
+    int F, act, words;
+};
+
+constexpr int kFewTokens = 16;
+
+// 2-D map of 16-bit rows for boxes of 64 columns x `box` rows, 128-byte swizzle.
+bool make_map(CUtensorMap *m, const void *base, bool bf16, int64_t stride, int64_t cols, int64_t rows, int box);
+
+cudaError_t launch_product_f16(const Product &p, Mode mode, cudaStream_t stream);
+cudaError_t launch_product_bf16(const Product &p, Mode mode, cudaStream_t stream);
+cudaError_t launch_few_f16(const Few &p, cudaStream_t stream);
+cudaError_t launch_few_bf16(const Few &p, cudaStream_t stream);
+cudaError_t launch_gate_grad_f16(const GateGrad &p, cudaStream_t stream);
+cudaError_t launch_gate_grad_bf16(const GateGrad &p, cudaStream_t stream);
+// Rows of `cols` 16-bit values, `from` elements apart, to rows `to` elements apart.
+cudaError_t launch_spread(const void *src, void *dst, int64_t rows, int cols, int64_t from, int64_t to,
+                          cudaStream_t stream);
+
+}  // namespace glu
+}  // namespace gdn

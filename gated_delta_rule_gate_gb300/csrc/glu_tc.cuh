@@ -1,0 +1,324 @@
+// glu_tc.cuh -- the matrix products of the gated feed-forward on the tensor cores
+// (tcgen05, 16-bit operands, fp32 accumulators), with what is done to their results.
+//
+// A pair of blocks on two SMs works on one tile of 256 x 256 (cta_group::2): each has
+// 128 of the tile's rows in its tensor memory and half of either operand in its shared
+// memory, so that a K-step of 64 takes 32 KB of each block for 16.8 MFLOP: half the
+// operand bytes of two single blocks.  Persistent; per block a warp that loads
+// (TMA, six stages), a warp whose first thread issues the products (in the pair's first
+// block) and four warps that take the finished accumulators (two of them, so that the
+// next tile's products run meanwhile) out of tensor memory.
+//
+// kForward: the 256 columns are 128 of the gate and the same 128 of the up projection (the
+// first block of the pair loads w_gate's rows, the second w_up's), so both factors of an
+// output meet in one thread.  kInput sums over two pairs of operands, d_g w_gate and
+// d_u w_up, in one accumulator.  kWeights takes d^T and x as they lie in memory: both
+// operands have K (the tokens) as their outer dimension.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "glu_launch.h"
+#include "glu_math.cuh"
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace gdn {
+namespace glu {
+
+constexpr int kStages = 6, kHalf = 16384;  // bytes of a block's share of an operand's stage
+constexpr int kStageBytes = 2 * kHalf;
+constexpr int kEpilogueWarps = 4, kProductThreads = 32 * (2 + kEpilogueWarps);
+constexpr int kBox = 4096;  // 32 rows of 64 results
+constexpr int kProductSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * 2 * kBox + 256;
+constexpr int kGroup = 8;  // tiles along the rows that are taken side by side
+
+struct Barriers {
+    uint64_t full[kStages], empty[kStages], done[2], taken[2];
+    uint32_t tmem;
+};
+
+struct TileAt {
+    int64_t m;
+    int n, z;
+};
+// Tiles in groups of kGroup along the rows, so that those worked on at once share their
+// operands in L2.
+template <Mode MODE>
+__device__ __forceinline__ TileAt tile_at(const Product &p, int64_t i) {
+    TileAt t;
+    const int64_t per = p.tiles_m * p.tiles_n;
+    t.z = MODE == kWeights ? (int)(i / per) : 0;
+    i -= t.z * per;
+    const int64_t group = i / ((int64_t)kGroup * p.tiles_n), first = group * kGroup;
+    const int64_t rows = p.tiles_m - first < kGroup ? p.tiles_m - first : kGroup;
+    i -= first * p.tiles_n;
+    t.m = first + i % rows;
+    t.n = (int)(i / rows);
+    return t;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Half of a lane's row of 64 results, 16-byte pieces where the 128-byte swizzle has them.
+template <typename T>
+__device__ __forceinline__ void put_half(unsigned char *box, int lane, int half, const float (&v)[32]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const uint4 w = make_uint4(pack2<T>(v[8 * c], v[8 * c + 1]), pack2<T>(v[8 * c + 2], v[8 * c + 3]),
+                                   pack2<T>(v[8 * c + 4], v[8 * c + 5]), pack2<T>(v[8 * c + 6], v[8 * c + 7]));
+        *reinterpret_cast<uint4 *>(box + lane * 128 + (((4 * half + c) ^ (lane & 7)) << 4)) = w;
+    }
+}
+
+// The staged boxes of a warp, two in turn.
+struct Stage {
+    unsigned char *base;
+    int turn;
+    __device__ __forceinline__ unsigned char *next(bool by_map, int lane) {
+        unsigned char *box = base + (turn ^= 1) * kBox;
+        if (by_map && lane == 0) ptx::bulk_wait_read_all_but_last();  // the store before the last one has read it
+        __syncwarp();
+        return box;
+    }
+};
+// Sends a box of 32 rows x 64 columns to its place; what lies outside is left out.
+__device__ __forceinline__ void send(const Product &p, const Result &c, const unsigned char *box, int64_t row, int col,
+                                     int lane) {
+    if (p.by_map) {
+        ptx::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            ptx::tma_store_2d(&c.map, col, (int)row, box);
+            ptx::bulk_commit();
+        }
+        return;
+    }
+    __syncwarp();
+    const int rows = p.rows - row < 32 ? (int)(p.rows - row) : 32, cols = p.cols - col < 64 ? p.cols - col : 64;
+    for (int r = 0; r < rows; ++r) {
+        uint16_t *to = static_cast<uint16_t *>(c.at) + (row + r) * c.stride + col;
+        for (int e = lane; e < cols; e += 32)
+            to[e] = *reinterpret_cast<const uint16_t *>(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + (e & 7) * 2);
+    }
+    __syncwarp();
+}
+
+template <Mode MODE, typename T>
+__device__ __forceinline__ void take(const Product &p, const TileAt &t, uint32_t acc, int64_t row, Stage &stage,
+                                     int lane) {
+    float v[32];
+    if (MODE == kForward) {
+        const int col0 = t.n * 128;
+        for (int h = 0; h < 2; ++h) {
+            const int col = col0 + 64 * h;
+            if (col >= p.cols) break;
+            unsigned char *box = stage.next(p.by_map, lane);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float u[32];
+                tc::ld32(acc + 64 * h + 32 * q, v);
+                tc::ld32(acc + 128 + 64 * h + 32 * q, u);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = activation(v[i], p.act) * u[i];
+                put_half<T>(box, lane, q, v);
+            }
+            send(p, p.c[0], box, row, col, lane);
+            if (!p.gates) continue;
+            for (int k = 0; k < 2; ++k) {
+                box = stage.next(p.by_map, lane);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    tc::ld32(acc + 128 * k + 64 * h + 32 * q, v);
+                    put_half<T>(box, lane, q, v);
+                }
+                send(p, p.c[1 + k], box, row, col, lane);
+            }
+        }
+    } else {
+        const int col0 = t.n * 256;
+        for (int h = 0; h < 4; ++h) {
+            const int col = col0 + 64 * h;
+            if (col >= p.cols) break;
+            unsigned char *box = stage.next(p.by_map, lane);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                tc::ld32(acc + 64 * h + 32 * q, v);
+                put_half<T>(box, lane, q, v);
+            }
+            send(p, p.c[t.z], box, row, col, lane);
+        }
+    }
+}
+
+template <Mode MODE, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
+    product_kernel(const __grid_constant__ Product p) {
+    extern __shared__ unsigned char raw[];
+    constexpr bool A_MN = MODE == kWeights, B_MN = MODE != kForward;
+    constexpr int PAIRS = MODE == kInput ? 2 : 1;  // of operands that one result sums over
+    unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    unsigned char *boxes = sm + kStages * kStageBytes;
+    Barriers &bar = *reinterpret_cast<Barriers *>(boxes + kEpilogueWarps * 2 * kBox);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            ptx::mbar_init(&bar.full[s], 1);
+            ptx::mbar_init(&bar.empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(&bar.done[a], 1);
+            ptx::mbar_init(&bar.taken[a], 2 * kEpilogueWarps);
+        }
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) tc::tmem_alloc_pair(&bar.tmem, 512);
+    tc::fence_before();
+    __syncthreads();
+    ptx::cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = bar.tmem;
+    ptx::grid_wait();
+
+    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int blocks = PAIRS * p.blocks_k;
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            int64_t filled = 0;
+            for (int64_t i = first; ok && i < p.tiles; i += step) {
+                const TileAt t = tile_at<MODE>(p, i);
+                const int m = (int)(t.m * 256) + 128 * (int)rank;
+                const int n = MODE == kForward ? t.n * 128 : t.n * 256 + 128 * (int)rank;
+                for (int kb = 0; kb < blocks; ++kb) {
+                    if (!ptx::mbar_wait_sleep(&bar.empty[s], ph ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    unsigned char *a = sm + s * kStageBytes, *b = a + kHalf;
+                    const uint32_t full = ptx::cluster_address(&bar.full[s], 0);
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(&bar.full[s], 2 * kStageBytes);
+                    const int pair = PAIRS == 2 && kb >= p.blocks_k ? 1 : 0, k = (kb - pair * p.blocks_k) * 64;
+                    const CUtensorMap *ma = &p.a[MODE == kWeights ? t.z : pair];
+                    const CUtensorMap *mb = &p.b[MODE == kForward ? rank : pair];
+                    if (A_MN) {
+                        ptx::tma_load_2d_pair(a, ma, m, k, full);
+                        ptx::tma_load_2d_pair(a + kHalf / 2, ma, m + 64, k, full);
+                    } else {
+                        ptx::tma_load_2d_pair(a, ma, k, m, full);
+                    }
+                    if (B_MN) {
+                        ptx::tma_load_2d_pair(b, mb, n, k, full);
+                        ptx::tma_load_2d_pair(b + kHalf / 2, mb, n + 64, k, full);
+                    } else {
+                        ptx::tma_load_2d_pair(b, mb, k, n, full);
+                    }
+                    ++filled;
+                    if (++s == kStages) s = 0, ph ^= 1;
+                }
+            }
+            // what was loaded has been read, and the pair's arrivals are in, before either block ends
+            for (int j = 0; j < kStages && j < filled; ++j) {
+                if (--s < 0) s = kStages - 1, ph ^= 1;
+                ok = ptx::mbar_wait_sleep(&bar.empty[s], ph) && ok;
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t id = tc::idesc_f16(256, 256, A_MN, B_MN) |
+                                    (std::is_same<T, __nv_bfloat16>::value ? tc::kIdescBf16 : 0u);
+            constexpr uint32_t sa = A_MN ? 2048 : 32, sb = B_MN ? 2048 : 32;  // bytes of 16 along K
+            const uint64_t da = tc::desc_sw128(ptx::smem_u32(sm), A_MN ? kHalf / 2 : 16);
+            const uint64_t db = tc::desc_sw128(ptx::smem_u32(sm) + kHalf, B_MN ? kHalf / 2 : 16);
+            int s = 0;
+            uint32_t ph = 0, turn = 0;
+            for (int64_t i = first; ok && i < p.tiles; i += step, ++turn) {
+                const uint32_t a = turn & 1;
+                if (!ptx::mbar_wait(&bar.taken[a], ((turn >> 1) & 1) ^ 1, 1u << 22)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                for (int kb = 0; kb < blocks; ++kb) {
+                    if (!ptx::mbar_wait(&bar.full[s], ph, 1u << 22)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc::mma_f16_pair(tmem + a * 256, tc::desc_adv(da, s * kStageBytes + k * sa),
+                                         tc::desc_adv(db, s * kStageBytes + k * sb), id, kb + k > 0);
+                    tc::commit_pair(&bar.empty[s]);
+                    if (++s == kStages) s = 0, ph ^= 1;
+                }
+                tc::commit_pair(&bar.done[a]);
+            }
+        }
+    } else {
+        const int quarter = warp & 3;  // of the tensor memory's lanes, by the warp's number
+        Stage stage = {boxes + (warp - 2) * 2 * kBox, 0};
+        uint32_t turn = 0;
+        const uint32_t taken[2] = {ptx::cluster_address(&bar.taken[0], 0), ptx::cluster_address(&bar.taken[1], 0)};
+        for (int64_t i = first; i < p.tiles; i += step, ++turn) {
+            const TileAt t = tile_at<MODE>(p, i);
+            const uint32_t a = turn & 1;
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&bar.done[a], (turn >> 1) & 1));
+            if (!ok) break;
+            tc::fence_after();
+            const int64_t row = t.m * 256 + 128 * rank + 32 * quarter;
+            if (row < p.rows)
+                take<MODE, T>(p, t, tmem + a * 256 + ((uint32_t)(32 * quarter) << 16), row, stage, lane);
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(taken[a]);
+        }
+        if (lane == 0) ptx::bulk_wait_read();
+    }
+    if (!ok) {
+        if (p.err) atomicOr(p.err, kErrTimeout);
+        // what the block still has in flight ends meanwhile
+        for (int i = 0; i < 100; ++i) __nanosleep(10000);
+    }
+    __syncthreads();
+    ptx::cluster_sync();
+    if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
+}
+
+template <Mode MODE, typename T>
+cudaError_t launch_product_as(const Product &p, cudaStream_t stream) {
+    const auto kernel = product_kernel<MODE, T>;
+    const cudaError_t e = smem_attr((const void *)kernel, kProductSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t pairs = sm_count() / 2;
+    const unsigned blocks = 2 * (unsigned)(p.tiles < pairs ? p.tiles : pairs);
+    return launch_early(kernel, blocks, kProductThreads, kProductSmem, stream, p);
+}
+template <typename T>
+cudaError_t launch_product(const Product &p, Mode mode, cudaStream_t stream) {
+    if (p.tiles == 0) return cudaSuccess;
+    switch (mode) {
+        case kForward: return launch_product_as<kForward, T>(p, stream);
+        case kInput: return launch_product_as<kInput, T>(p, stream);
+        default: return launch_product_as<kWeights, T>(p, stream);
+    }
+}
+
+}  // namespace glu
+}  // namespace gdn

@@ -39,8 +39,13 @@ struct Library {
     decltype(&gdn_rmsnorm_backward_workspace_size) norm_workspace;
     decltype(&gdn_grad_clip) clip;
     decltype(&gdn_grad_clip_workspace_size) clip_workspace;
+    decltype(&gdn_glu) glu;
+    decltype(&gdn_glu_workspace_size) glu_workspace;
+    decltype(&gdn_glu_backward) glu_backward;
+    decltype(&gdn_glu_backward_workspace_size) glu_backward_workspace;
+    decltype(&gdn_adamw) adamw;
 } lib;
-PyObject *check_status, *scan_gradients, *norm_result, *norm_gradients, *stream_handle_name;
+PyObject *check_status, *scan_gradients, *norm_result, *norm_gradients, *glu_gradients, *stream_handle_name;
 
 [[noreturn]] void refuse(PyObject *type, const char *fmt, ...) {
     va_list ap;
@@ -666,14 +671,241 @@ PyObject *py_clip(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwn
     END_HANDLE_TH_ERRORS
 }
 
+// ---------------------------------------------------------------- gated feed-forward
+int32_t activation(PyObject *o) {
+    static const char *const names[] = {"silu", "gelu", "gelu_tanh", "relu", "sigmoid"};
+    if (!o) return GDN_ACT_SILU;
+    const char *s = PyUnicode_Check(o) ? PyUnicode_AsUTF8(o) : "";
+    if (!s) throw python_error();
+    for (int i = 0; i < 5; ++i)
+        if (!strcmp(s, names[i])) return i;
+    refuse(PyExc_ValueError, "activation must be one of silu, gelu, gelu_tanh, relu, sigmoid");
+}
+// The sizes of a call: x [..., dim], weights [inner, dim].
+struct GluShape {
+    int64_t rows, D, F;
+    std::vector<int64_t> out, gates;  // [..., inner], [..., 2 inner]
+};
+GluShape glu_shape(const Tensor &x, const Tensor &w_gate) {
+    const IntArrayRef shape = x.sizes();
+    if (shape.empty()) refuse(PyExc_ValueError, "x must be [..., dim]");
+    if (w_gate.dim() != 2) refuse(PyExc_ValueError, "w_gate must be [inner, dim], got %s", text(w_gate.sizes()).c_str());
+    GluShape s;
+    s.D = shape.back(), s.F = w_gate.size(0);
+    if (s.D > INT32_MAX || s.F > INT32_MAX) refuse(PyExc_ValueError, "x or w_gate has more than 2^31 - 1 columns or rows");
+    s.rows = s.D ? x.numel() / s.D : 0;
+    s.out.assign(shape.begin(), shape.end() - 1);
+    s.gates = s.out;
+    s.out.push_back(s.F);
+    s.gates.push_back(2 * s.F);
+    return s;
+}
+
+Signature glu_signature = {"gdn_glu", 3, 3, {"x", "w_gate", "w_up", "activation", "want_gates", "out", "error_word",
+                           "workspace", "stream"}, {}};
+
+PyObject *py_glu(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwnames) {
+    HANDLE_TH_ERRORS
+    PyObject *v[kMost];
+    parse(glu_signature, args, n, kwnames, v);
+    const Tensor &x = needed(v[0], "x"), &w_gate = needed(v[1], "w_gate"), &w_up = needed(v[2], "w_up");
+    const Tensor *given_out = tensor(v[5], "out"), *err = tensor(v[6], "error_word"), *given = workspace(v[7]);
+    gdn_glu_args a = {};
+    a.activation = activation(v[3]);
+    const bool keep = flag(v[4]);
+    one_device(x, {{&w_gate, "w_gate"}, {&w_up, "w_up"}, {given_out, "out"}, {err, "error_word"}, {given, "workspace"}});
+    const GluShape s = glu_shape(x, w_gate);
+    const ScalarType type = x.scalar_type();
+    a.dtype = code(x, "x");
+    a.rows = s.rows, a.dim = (int32_t)s.D, a.inner = (int32_t)s.F;
+    const int64_t w[2] = {s.F, s.D};
+    const Rows xr = rows(x, type, x.sizes(), "x");
+    a.x = xr.at, a.x_stride = xr.stride;
+    a.w_gate = address(&w_gate, type, "w_gate", w);
+    a.w_up = address(&w_up, type, "w_up", w);
+    a.error_word = address<int32_t>(err, ScalarType::Int, "error_word");
+    const Rows orow = rows(given_out, type, s.out, "out");
+    Stream stream(v[8], x);
+    Tensor out, gates;
+    if (given_out) {
+        a.out = orow.at, a.out_stride = orow.stride;
+    } else {
+        out = make(s.out, x, type);
+        a.out = out.data_ptr();
+    }
+    if (keep) {
+        gates = make(s.gates, x, type);
+        a.gates = gates.data_ptr();
+    }
+    const Workspace ws(given, given ? 0 : lib.glu_workspace(&a), x);
+    done(lib.glu(&a, ws.at, ws.bytes, stream.get()));
+    written({given_out});
+    PyObject *o = given_out ? Py_NewRef(v[5]) : THPVariable_Wrap(out);
+    return keep ? Py_BuildValue("(NN)", o, THPVariable_Wrap(gates)) : o;
+    END_HANDLE_TH_ERRORS
+}
+
+Signature glu_backward_signature = {"gdn_glu_backward", 5, 5, {"d_out", "x", "w_gate", "w_up", "gates", "activation",
+                                    "want_dx", "want_d_weights", "dx", "d_w_gate", "d_w_up", "error_word",
+                                    "workspace", "stream"}, {}};
+
+PyObject *py_glu_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwnames) {
+    HANDLE_TH_ERRORS
+    PyObject *v[kMost];
+    parse(glu_backward_signature, args, n, kwnames, v);
+    const Tensor &dout = needed(v[0], "d_out"), &x = needed(v[1], "x"), &w_gate = needed(v[2], "w_gate");
+    const Tensor &w_up = needed(v[3], "w_up"), &gates = needed(v[4], "gates");
+    const bool want_x = !v[6] || flag(v[6]), want_w = !v[7] || flag(v[7]);
+    const Tensor *dxg = tensor(v[8], "dx"), *dgg = tensor(v[9], "d_w_gate"), *dug = tensor(v[10], "d_w_up");
+    const Tensor *err = tensor(v[11], "error_word"), *given = workspace(v[12]);
+    if (dxg && !want_x) refuse(PyExc_ValueError, "dx given with want_dx False");
+    if ((dgg || dug) && !want_w) refuse(PyExc_ValueError, "d_w_gate or d_w_up given with want_d_weights False");
+    gdn_glu_grad_args a = {};
+    a.activation = activation(v[5]);
+    one_device(x, {{&dout, "d_out"}, {&w_gate, "w_gate"}, {&w_up, "w_up"}, {&gates, "gates"}, {dxg, "dx"},
+                   {dgg, "d_w_gate"}, {dug, "d_w_up"}, {err, "error_word"}, {given, "workspace"}});
+    const GluShape s = glu_shape(x, w_gate);
+    const ScalarType type = x.scalar_type();
+    a.dtype = code(x, "x");
+    a.rows = s.rows, a.dim = (int32_t)s.D, a.inner = (int32_t)s.F;
+    const int64_t w[2] = {s.F, s.D};
+    const Rows xr = rows(x, type, x.sizes(), "x"), dr = rows(dout, type, s.out, "d_out");
+    a.x = xr.at, a.x_stride = xr.stride;
+    a.d_out = dr.at, a.d_out_stride = dr.stride;
+    a.w_gate = address(&w_gate, type, "w_gate", w);
+    a.w_up = address(&w_up, type, "w_up", w);
+    a.gates = address(&gates, type, "gates", s.gates);
+    a.error_word = address<int32_t>(err, ScalarType::Int, "error_word");
+    const Rows dxr = rows(dxg, type, x.sizes(), "dx");
+    Tensor dx, dg, du;
+    if (dgg) dg = *dgg;
+    if (dug) du = *dug;
+    a.d_w_gate = address(dgg, type, "d_w_gate", w);
+    a.d_w_up = address(dug, type, "d_w_up", w);
+    Stream stream(v[13], x);
+    if (want_x) {
+        dx = dxg ? *dxg : make(x.sizes(), x, type);
+        a.dx = dx.data_ptr(), a.dx_stride = dxg ? dxr.stride : 0;
+    }
+    if (want_w) {
+        if (!dgg) dg = make(w, x, type), a.d_w_gate = dg.data_ptr();
+        if (!dug) du = make(w, x, type), a.d_w_up = du.data_ptr();
+    }
+    // rows of no tokens have no address, but are wanted all the same
+    if (s.rows || want_w) {
+        const Workspace ws(given, given ? 0 : lib.glu_backward_workspace(&a), x);
+        done(lib.glu_backward(&a, ws.at, ws.bytes, stream.get()));
+    }
+    written({dxg, dgg, dug});
+    return tuple_of(glu_gradients, {&dx, &dg, &du});
+    END_HANDLE_TH_ERRORS
+}
+
+// ---------------------------------------------------------------- optimizer
+Signature adamw_signature = {"gdn_adamw", 5, 5, {"params", "grads", "exp_avg", "exp_avg_sq", "step", "lr", "beta1",
+                             "beta2", "eps", "weight_decay", "exp_avg_scales", "exp_avg_sq_scales", "master",
+                             "grad_norm", "max_norm", "norm_eps", "error_word", "stream"}, {}};
+
+PyObject *py_adamw(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwnames) {
+    HANDLE_TH_ERRORS
+    constexpr ScalarType f32 = ScalarType::Float, e4m3 = ScalarType::Float8_e4m3fn;
+    PyObject *v[kMost];
+    parse(adamw_signature, args, n, kwnames, v);
+    static const char *const lists[] = {"params", "grads", "exp_avg", "exp_avg_sq"};
+    for (int i = 0; i < 4; ++i)
+        if (!v[i]) refuse(PyExc_TypeError, "%s must be a sequence of tensors", lists[i]);
+    if (!v[4]) refuse(PyExc_TypeError, "step must be an integer or a tensor");
+    const Sequence params(v[0], "params must be a sequence of tensors"), grads(v[1], "grads must be a sequence of tensors");
+    const Sequence ms(v[2], "exp_avg must be a sequence of tensors"), vs(v[3], "exp_avg_sq must be a sequence of tensors");
+    std::optional<Sequence> mss, vss, masters;
+    if (v[10]) mss.emplace(v[10], "exp_avg_scales must be a sequence of tensors");
+    if (v[11]) vss.emplace(v[11], "exp_avg_sq_scales must be a sequence of tensors");
+    if (v[12]) masters.emplace(v[12], "master must be a sequence of tensors");
+    auto as_many = [&](const Sequence *s, const char *what) {
+        if (s && s->n != params.n)
+            refuse(PyExc_ValueError, "%s has %zd tensors, params %zd", what, s->n, params.n);
+    };
+    auto some = [](const std::optional<Sequence> &s) { return s ? &*s : nullptr; };
+    as_many(&grads, "grads"), as_many(&ms, "exp_avg"), as_many(&vs, "exp_avg_sq");
+    as_many(some(mss), "exp_avg_scales"), as_many(some(vss), "exp_avg_sq_scales"), as_many(some(masters), "master");
+    gdn_adamw_args a = {};
+    const Tensor *step = nullptr, *lr = nullptr;
+    if (THPVariable_Check(v[4])) step = &THPVariable_Unpack(v[4]);
+    else a.step = whole(v[4], "step");
+    if (v[5] && THPVariable_Check(v[5])) lr = &THPVariable_Unpack(v[5]);
+    else a.lr = number(v[5], 1e-3);
+    a.beta1 = number(v[6], 0.9), a.beta2 = number(v[7], 0.999), a.eps = number(v[8], 1e-8);
+    a.weight_decay = number(v[9], 0.01);
+    const Tensor *norm = tensor(v[13], "grad_norm"), *err = tensor(v[16], "error_word");
+    if ((norm != nullptr) != (v[14] != nullptr)) refuse(PyExc_ValueError, "grad_norm and max_norm go together");
+    a.max_norm = number(v[14], 0), a.norm_eps = number(v[15], 1e-6);
+    const c10::Device device = params.n ? params.at(0, "a parameter").device()
+                                        : c10::Device(at::kCUDA, c10::cuda::current_device());
+    const bool eight = params.n && ms.at(0, "an exp_avg").scalar_type() == e4m3;
+    const ScalarType state = eight ? e4m3 : f32;
+    a.count = (int32_t)params.n;
+    a.state_dtype = eight ? GDN_DTYPE_E4M3 : GDN_DTYPE_F32;
+    const size_t N = params.n;
+    std::vector<void *> p(N), m(N), q(N);
+    std::vector<const void *> g(N);
+    std::vector<float *> msc(N), vsc(N), master(N);
+    std::vector<int64_t> sizes(N);
+    std::vector<int32_t> ptypes(N), gtypes(N);
+    std::vector<const Tensor *> outputs;
+    auto maybe = [](const std::optional<Sequence> &s, size_t i, const char *what) {
+        return s ? tensor(PySequence_Fast_GET_ITEM(s->s, i) == Py_None ? nullptr : PySequence_Fast_GET_ITEM(s->s, i), what)
+                 : nullptr;
+    };
+    for (size_t i = 0; i < N; ++i) {
+        const Tensor &tp = params.at(i, "a parameter"), &tg = grads.at(i, "a gradient");
+        const Tensor &tm = ms.at(i, "an exp_avg"), &tv = vs.at(i, "an exp_avg_sq");
+        const Tensor *tms = mss ? &mss->at(i, "an exp_avg_scales") : nullptr;
+        const Tensor *tvs = vss ? &vss->at(i, "an exp_avg_sq_scales") : nullptr;
+        const Tensor *tw = maybe(masters, i, "a master copy");
+        one_device(params.at(0, "a parameter"), {{&tp, "a parameter"}, {&tg, "a gradient"}, {&tm, "an exp_avg"},
+                   {&tv, "an exp_avg_sq"}, {tms, "an exp_avg_scales"}, {tvs, "an exp_avg_sq_scales"},
+                   {tw, "a master copy"}, {step, "step"}, {lr, "lr"}, {norm, "grad_norm"}, {err, "error_word"}});
+        const IntArrayRef shape = tp.sizes();
+        ptypes[i] = code(tp, "a parameter"), gtypes[i] = code(tg, "a gradient");
+        sizes[i] = tp.numel();
+        p[i] = address(&tp, tp.scalar_type(), "a parameter");
+        g[i] = address(&tg, tg.scalar_type(), "a gradient", shape);
+        m[i] = address(&tm, state, "an exp_avg", shape);
+        q[i] = address(&tv, state, "an exp_avg_sq", shape);
+        const int64_t blocks[1] = {(tp.numel() + GDN_ADAMW_BLOCK - 1) / GDN_ADAMW_BLOCK};
+        msc[i] = address<float>(tms, f32, "an exp_avg_scales", blocks);
+        vsc[i] = address<float>(tvs, f32, "an exp_avg_sq_scales", blocks);
+        master[i] = address<float>(tw, f32, "a master copy", shape);
+        for (const Tensor *t : {&tp, &tm, &tv, tms, tvs, tw})
+            if (t) outputs.push_back(t);
+    }
+    a.params = p.data(), a.grads = g.data(), a.exp_avg = m.data(), a.exp_avg_sq = q.data();
+    a.exp_avg_scales = mss ? msc.data() : nullptr, a.exp_avg_sq_scales = vss ? vsc.data() : nullptr;
+    a.master = masters ? master.data() : nullptr;
+    a.sizes = sizes.data(), a.param_dtypes = ptypes.data(), a.grad_dtypes = gtypes.data();
+    auto one = [&](const Tensor *t, const char *what) {
+        if (t && t->numel() != 1) refuse(PyExc_ValueError, "%s must have one element", what);
+    };
+    one(step, "step"), one(lr, "lr"), one(norm, "grad_norm"), one(err, "error_word");
+    a.step_device = address<const int64_t>(step, ScalarType::Long, "step");
+    a.lr_device = address<const float>(lr, f32, "lr");
+    a.grad_norm = address<const float>(norm, f32, "grad_norm");
+    a.error_word = address<int32_t>(err, ScalarType::Int, "error_word");
+    Stream stream(v[17], device);
+    done(lib.adamw(&a, stream.get()));
+    for (const Tensor *t : outputs) written({t});
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
 // ---------------------------------------------------------------- module
-// bind(addresses of the library's functions, check, ScanGradients, NormResult, NormGradients)
+// bind(addresses of the library's functions, check, ScanGradients, NormResult, NormGradients, GluGradients)
 PyObject *py_bind(PyObject *, PyObject *args) {
     HANDLE_TH_ERRORS
-    unsigned long long f[8];
-    PyObject *objects[4];
-    if (!PyArg_ParseTuple(args, "(KKKKKKKK)OOOO", f, f + 1, f + 2, f + 3, f + 4, f + 5, f + 6, f + 7, objects,
-                          objects + 1, objects + 2, objects + 3))
+    unsigned long long f[13];
+    PyObject *objects[5];
+    if (!PyArg_ParseTuple(args, "(KKKKKKKKKKKKK)OOOOO", f, f + 1, f + 2, f + 3, f + 4, f + 5, f + 6, f + 7, f + 8,
+                          f + 9, f + 10, f + 11, f + 12, objects, objects + 1, objects + 2, objects + 3, objects + 4))
         return nullptr;
     lib.scan = reinterpret_cast<decltype(lib.scan)>(f[0]);
     lib.step = reinterpret_cast<decltype(lib.step)>(f[1]);
@@ -683,11 +915,18 @@ PyObject *py_bind(PyObject *, PyObject *args) {
     lib.norm_workspace = reinterpret_cast<decltype(lib.norm_workspace)>(f[5]);
     lib.clip = reinterpret_cast<decltype(lib.clip)>(f[6]);
     lib.clip_workspace = reinterpret_cast<decltype(lib.clip_workspace)>(f[7]);
+    lib.glu = reinterpret_cast<decltype(lib.glu)>(f[8]);
+    lib.glu_workspace = reinterpret_cast<decltype(lib.glu_workspace)>(f[9]);
+    lib.glu_backward = reinterpret_cast<decltype(lib.glu_backward)>(f[10]);
+    lib.glu_backward_workspace = reinterpret_cast<decltype(lib.glu_backward_workspace)>(f[11]);
+    lib.adamw = reinterpret_cast<decltype(lib.adamw)>(f[12]);
     check_status = Py_NewRef(objects[0]), scan_gradients = Py_NewRef(objects[1]);
     norm_result = Py_NewRef(objects[2]), norm_gradients = Py_NewRef(objects[3]);
+    glu_gradients = Py_NewRef(objects[4]);
     stream_handle_name = PyUnicode_InternFromString("cuda_stream");
     for (Signature *s : {&scan_signature, &step_signature, &backward_signature, &norm_signature,
-                         &norm_backward_signature, &clip_signature}) {
+                         &norm_backward_signature, &clip_signature, &glu_signature, &glu_backward_signature,
+                         &adamw_signature}) {
         if (!s->interned.empty()) continue;
         for (const char *name : s->names) s->interned.push_back(PyUnicode_InternFromString(name));
     }
@@ -759,6 +998,42 @@ PyMethodDef methods[] = {
      "overlaps another.  Returns the\n"
      "norm, float32 [1] on the device (no synchronisation).  A norm that is not finite\n"
      "scales nothing and sets DEVERR_NONFINITE in error_word."},
+    {"gdn_glu", FAST(py_glu),
+     "gdn_glu($module, x, w_gate, w_up, *, activation='silu', want_gates=False, out=None, error_word=None, "
+     "workspace=None, stream=None)\n--\n\n"
+     "The gated half of a feed-forward block in one kernel: with g = x w_gate^T and\n"
+     "u = x w_up^T, out = act(g) u.  x is [..., dim] (its rows may be columns of wider\n"
+     "ones), the weights [inner, dim] (halves of one fused weight, say), all of one dtype,\n"
+     "float16 or bfloat16; out is [..., inner].  activation is \"silu\", \"gelu\" (by the\n"
+     "error function), \"gelu_tanh\", \"relu\" or \"sigmoid\".  Sums are fp32.  Returns\n"
+     "out, or (out, gates) with want_gates: gates [..., 2 inner] holds g and u for\n"
+     "gdn_glu_backward, in x's dtype.  Calls of a few tokens (serving) are bound by the\n"
+     "weights' way from memory, long ones by the tensor cores."},
+    {"gdn_glu_backward", FAST(py_glu_backward),
+     "gdn_glu_backward($module, d_out, x, w_gate, w_up, gates, *, activation='silu', want_dx=True, "
+     "want_d_weights=True, dx=None, d_w_gate=None, d_w_up=None, error_word=None, workspace=None, stream=None)\n--\n\n"
+     "Gradients of gdn_glu for the gradient d_out of its output, at the gates that it\n"
+     "returned: d_g = d_out u act'(g) and d_u = d_out act(g) (rounded to x's dtype as the\n"
+     "products' operands), dx = d_g w_gate + d_u w_up, d_w_gate = d_g^T x, d_w_up = d_u^T x.\n"
+     "Returns GluGradients(dx, d_w_gate, d_w_up), all in x's dtype; None where not wanted."},
+    {"gdn_adamw", FAST(py_adamw),
+     "gdn_adamw($module, params, grads, exp_avg, exp_avg_sq, step, *, lr=0.001, beta1=0.9, beta2=0.999, eps=1e-08, "
+     "weight_decay=0.01, exp_avg_scales=None, exp_avg_sq_scales=None, master=None, grad_norm=None, max_norm=None, "
+     "norm_eps=1e-06, error_word=None, stream=None)\n--\n\n"
+     "One AdamW step of many tensors, all in place (grads are read), in fp32:\n\n"
+     "    m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2\n"
+     "    p = p - lr (weight_decay p + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps))\n\n"
+     "params and grads are float32, float16 or bfloat16, each its own; master (a list,\n"
+     "None where there is none) are float32 copies on which the step is taken, the\n"
+     "parameter receiving the rounding.  exp_avg and exp_avg_sq are float32, or all of them\n"
+     "float8_e4m3fn with float32 scales [ceil(n / 256)] for blocks of 256 elements (zeros\n"
+     "to begin with): exp_avg_scales, and exp_avg_sq_scales for the root of v, which is\n"
+     "what exp_avg_sq then holds.  grad_norm (float32, one element on the device, as\n"
+     "gdn_grad_clip returns it) clips the gradients to max_norm as they are read:\n"
+     "gdn_grad_clip(grads, 3e38) leaves them as they are and gives it.  A norm that is not finite leaves\n"
+     "everything as it is and sets DEVERR_NONFINITE in error_word.  step (1 at first) may be\n"
+     "an int64 tensor and lr a float32 one, of one element on the device, which a captured\n"
+     "graph reads anew at each replay.  All tensors are contiguous and none overlaps another."},
     {"bind", py_bind, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -1,5 +1,6 @@
 """The recurrent-layer operators: gdn_scan, gdn_scan_step, gdn_scan_backward,
-gdn_rmsnorm, gdn_rmsnorm_backward, gdn_grad_clip (documented in their docstrings).
+gdn_rmsnorm, gdn_rmsnorm_backward, gdn_glu, gdn_glu_backward, gdn_grad_clip, gdn_adamw
+(documented in their docstrings).
 
 Their Python entry points are native (csrc/layer_binding.cpp), because a decode step
 is over in the time that Python takes to look at its tensors.  The module is built (by g++,
@@ -22,11 +23,14 @@ from . import build as _build
 ScanGradients = namedtuple("ScanGradients", "dx d_decay d_beta d_gate_bias d_gate_scale d_initial_state")
 NormResult = namedtuple("NormResult", "out residual scales rstd")
 NormGradients = namedtuple("NormGradients", "dx dweight")
+GluGradients = namedtuple("GluGradients", "dx d_w_gate d_w_up")
 
-OPERATORS = ("gdn_scan", "gdn_scan_step", "gdn_scan_backward", "gdn_rmsnorm", "gdn_rmsnorm_backward", "gdn_grad_clip")
+OPERATORS = ("gdn_scan", "gdn_scan_step", "gdn_scan_backward", "gdn_rmsnorm", "gdn_rmsnorm_backward", "gdn_grad_clip",
+             "gdn_glu", "gdn_glu_backward", "gdn_adamw")
 # what the module calls, in the order that its bind() takes
 _FUNCTIONS = ("gdn_scan", "gdn_scan_step", "gdn_scan_backward", "gdn_rmsnorm", "gdn_rmsnorm_backward",
-              "gdn_rmsnorm_backward_workspace_size", "gdn_grad_clip", "gdn_grad_clip_workspace_size")
+              "gdn_rmsnorm_backward_workspace_size", "gdn_grad_clip", "gdn_grad_clip_workspace_size", "gdn_glu",
+              "gdn_glu_workspace_size", "gdn_glu_backward", "gdn_glu_backward_workspace_size", "gdn_adamw")
 
 _module = None
 _lock = threading.Lock()
@@ -46,7 +50,7 @@ def load():
             module = importlib.util.module_from_spec(spec)
             loader.exec_module(module)
             module.bind(tuple(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in _FUNCTIONS), N.check,
-                        ScanGradients, NormResult, NormGradients)
+                        ScanGradients, NormResult, NormGradients, GluGradients)
             _module = module
         return _module
 

@@ -94,7 +94,8 @@ typedef enum gdn_rule {
                                       (a decay above 1) was given; that path needs decays in (0, 1] and the
                                       results of the chunks concerned are not valid */
 
-#define GDN_DEVERR_NONFINITE 0x10 /* gdn_grad_clip: the norm is infinite or NaN; the gradients were not scaled */
+#define GDN_DEVERR_NONFINITE 0x10 /* gdn_grad_clip: the norm is infinite or NaN; the gradients were not scaled.
+                                     gdn_adamw: grad_norm is; the step was not taken */
 
 /*
  * One call of the recurrence over a batch of requests.
@@ -558,6 +559,150 @@ typedef struct gdn_grad_clip_args {
 
 size_t gdn_grad_clip_workspace_size(const gdn_grad_clip_args *args);
 gdn_status gdn_grad_clip(const gdn_grad_clip_args *args, void *workspace, size_t workspace_bytes, gdn_stream stream);
+
+typedef enum gdn_activation {
+    GDN_ACT_SILU = 0,      /* g sigmoid(g) */
+    GDN_ACT_GELU = 1,      /* g Phi(g), by the error function */
+    GDN_ACT_GELU_TANH = 2, /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+    GDN_ACT_RELU = 3,      /* max(g, 0); its derivative at 0 is 0 */
+    GDN_ACT_SIGMOID = 4    /* sigmoid(g) */
+} gdn_activation;
+
+/*
+ * gdn_glu -- the gated half of a feed-forward block, both projections and what joins
+ * them in one kernel, for each of `rows` tokens:
+ *
+ *     g = x w_gate^T,   u = x w_up^T,   out = act(g) u
+ *
+ * x is [rows, dim] with x_stride elements from row to row (0: dim), out [rows, inner] with
+ * out_stride (0: inner), the weights [inner, dim] contiguous, all of dtype F16 or BF16 (F32
+ * is declined: GDN_ERR_UNSUPPORTED).  Products are summed in fp32 on the tensor cores, and
+ * out is rounded once.  gates (NULL: not kept) receives g and u, [rows, 2 inner] contiguous
+ * with a row's g first, rounded to dtype, for gdn_glu_backward; fp16 ones beyond 65504 are
+ * infinite.  A few tokens (serving) take a kernel of their own.  out and gates overlap no
+ * input.
+ *
+ * The workspace is device memory of gdn_glu_workspace_size() bytes, 16-byte aligned (none
+ * is needed where rows of x and of the weights are whole words of 16 bytes); its contents
+ * are scratch.  dim and inner are at most 2^20.
+ */
+typedef struct gdn_glu_args {
+    int64_t rows;
+    int32_t dim;
+    int32_t inner;
+    int32_t dtype;      /* F16 or BF16 */
+    int32_t activation; /* gdn_activation */
+    int64_t x_stride;
+    int64_t out_stride;
+    const void *x;
+    const void *w_gate;
+    const void *w_up;
+    void *out;
+    void *gates; /* or NULL */
+    int32_t *error_word;
+} gdn_glu_args;
+
+/* (size_t)-1 when the arguments are rejected (see gdn_last_error_message). */
+size_t gdn_glu_workspace_size(const gdn_glu_args *args);
+gdn_status gdn_glu(const gdn_glu_args *args, void *workspace, size_t workspace_bytes, gdn_stream stream);
+
+/*
+ * gdn_glu_backward -- the gradient of gdn_glu for the gradient d_out of its output, at
+ * the gates that it kept:
+ *
+ *     d_g = d_out u act'(g),   d_u = d_out act(g)
+ *     dx = d_g w_gate + d_u w_up,   d_w_gate = d_g^T x,   d_w_up = d_u^T x
+ *
+ * d_g and d_u are formed in fp32 and rounded to dtype, as operands of the products; sums
+ * are fp32, in an order that sizes alone decide.  dx, and d_w_gate with d_w_up, may be NULL
+ * (not wanted; what only they need may then be NULL too).  d_out_stride and dx_stride are
+ * elements from row to row (0: without a gap); gates, the weights and their gradients are
+ * contiguous.  Without rows the weights' gradients are zero.  Outputs overlap no input.
+ */
+typedef struct gdn_glu_grad_args {
+    int64_t rows;
+    int32_t dim;
+    int32_t inner;
+    int32_t dtype;
+    int32_t activation;
+    int64_t x_stride;
+    int64_t d_out_stride;
+    int64_t dx_stride;
+    const void *d_out;
+    const void *x;
+    const void *w_gate;
+    const void *w_up;
+    const void *gates;
+    void *dx;       /* or NULL */
+    void *d_w_gate; /* with d_w_up, or NULL */
+    void *d_w_up;
+    int32_t *error_word;
+} gdn_glu_grad_args;
+
+size_t gdn_glu_backward_workspace_size(const gdn_glu_grad_args *args);
+gdn_status gdn_glu_backward(const gdn_glu_grad_args *args, void *workspace, size_t workspace_bytes, gdn_stream stream);
+
+/* Elements that share a scale in 8-bit optimizer states. */
+#define GDN_ADAMW_BLOCK 256
+
+/*
+ * gdn_adamw -- one AdamW step of `count` tensors.  With t the step's number (the first
+ * is 1) and all of it in fp32:
+ *
+ *     k = min(1, max_norm / (*grad_norm + norm_eps))   (grad_norm given; else 1)
+ *     m = beta1 m + (1 - beta1) k g,   v = beta2 v + (1 - beta2) (k g)^2
+ *     p = p - lr (weight_decay p + (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps))
+ *
+ * grad_norm is a device float, the norm of all gradients: gdn_grad_clip with the largest
+ * max_norm leaves them as they are and gives it, and the clip is then made here, where
+ * they are read anyway.  A norm that is not finite leaves every tensor as it is and sets
+ * GDN_DEVERR_NONFINITE.
+ *
+ * The arrays are HOST memory, read before the call returns: device pointers, element
+ * counts (0: skipped) and gdn_dtypes (F32, F16, BF16).  params, exp_avg (m), exp_avg_sq
+ * (v) and their scales are updated in place; grads are read.  master (NULL: none, or
+ * NULL for a tensor that has none) are fp32 copies of the weights: the step is then
+ * taken on the copy, and params[i], which is not read, receives its rounding.
+ *
+ * state_dtype F32 keeps m and v as they are.  E4M3 keeps m and r = sqrt(v) in blocks of
+ * GDN_ADAMW_BLOCK elements of a tensor (the last may be short), each with an fp32 scale
+ * s = max(largest |m| (r), 2^-100) / 448 in exp_avg_scales[i] (exp_avg_sq_scales[i]),
+ * ceil(size / GDN_ADAMW_BLOCK) of them: the code is the quotient rounded to e4m3, and of
+ * an r above zero at least the smallest, 2^-9, so that no step divides by the eps alone
+ * where there was a gradient.  The step itself takes m and v before they are rounded.
+ * Codes and scales of zero are states of zero.
+ *
+ * step_device (or NULL) is the step's number in device memory, in place of `step`, and
+ * lr_device the rate, in place of `lr`: a captured graph is replayed with new ones.  A
+ * number below 1 there counts as 1.  No tensor overlaps another.
+ */
+typedef struct gdn_adamw_args {
+    int32_t count;
+    int32_t state_dtype; /* F32 or E4M3 */
+    int64_t step;        /* >= 1 */
+    double lr;           /* >= 0 */
+    double beta1, beta2; /* in [0, 1) */
+    double eps;          /* >= 0 */
+    double weight_decay; /* >= 0 */
+    double max_norm;     /* >= 0, with grad_norm */
+    double norm_eps;     /* >= 0, with grad_norm */
+    void *const *params;
+    const void *const *grads;
+    void *const *exp_avg;
+    void *const *exp_avg_sq;
+    float *const *exp_avg_scales;    /* E4M3 */
+    float *const *exp_avg_sq_scales; /* E4M3 */
+    float *const *master;
+    const int64_t *sizes;
+    const int32_t *param_dtypes;
+    const int32_t *grad_dtypes;
+    const int64_t *step_device;
+    const float *lr_device;
+    const float *grad_norm;
+    int32_t *error_word;
+} gdn_adamw_args;
+
+gdn_status gdn_adamw(const gdn_adamw_args *args, gdn_stream stream);
 
 /* Static description of a status code ("ok", "invalid argument", ...). */
 const char *gdn_status_string(gdn_status status);
