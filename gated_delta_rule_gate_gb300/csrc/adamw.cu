@@ -1,11 +1,14 @@
 // adamw.cu -- gdn_adamw: one AdamW step over many tensors.
 //
-// One kernel a group of tensors (up to kMany, whose table travels as a kernel argument,
-// so nothing is copied to the device first).  Elements are taken by rows of 256, a warp
-// a row, 8 elements a lane in two groups of four, which makes every access of fp32,
+// One kernel a group of tensors (up to kMany of one kind, whose table travels as a kernel
+// argument, so nothing is copied to the device first).  Elements are taken by rows of 256,
+// a warp a row, 8 elements a lane in two groups of four, which makes every access of fp32,
 // 16-bit and 8-bit values a whole word over adjacent lanes; a row is also the block of
 // 8-bit states that shares its scales, so that the largest of a block is a maximum over
-// one warp.  Everything is read once and written once.  Bound by HBM.
+// one warp.  Everything is read once and written once.  Bound by HBM: 4.0e8 bf16 elements
+// with fp32 copies and states (28 bytes each) 1639 us, 6.9 TB/s; with 8-bit states (10 bytes
+// each) 790 us, 5.1 TB/s, where issuing 44 instructions an element takes 470 us and
+// the waits of 24 warps an SM are not all hidden.
 #include <math.h>
 
 #include <cuda_fp8.h>
@@ -19,28 +22,25 @@ namespace gdn {
 namespace adamw {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kBlocks = 152 * 8;
-constexpr int kMany = 440, kFew = 32;
+constexpr int kMany = 400, kFew = 32;
+constexpr int kStretch = 8;
 constexpr int kRow = GDN_ADAMW_BLOCK;
 constexpr int kGroups = kRow / 128;  // of four adjacent elements a lane
 static_assert(kRow == 256, "a lane's two groups of four");
-// Rows that a block takes at a time.
-constexpr int kChunk = 4 * kWarps, kSmallChunk = kWarps;
-constexpr int64_t kSmall = 1 << 22;
 
 struct Tensor {
     void *p;
     const void *g;
     void *m, *v;
     float *ms, *vs, *master;
-    int64_t n;
-    int32_t first;  // its first chunk, counted over the table
-    uint8_t p_type, g_type, whole;  // gdn_dtypes; groups of four are words in all its tensors
+    int64_t n, first;  // elements; its first row, counted over the table
+    uint8_t p_type, g_type, whole;  // gdn_dtypes; all its tensors begin at 16-byte addresses
 };
 template <int MAX>
 struct Table {
     Tensor t[MAX];
-    int count, chunks, chunk;  // tensors, chunks, rows of a chunk
+    int64_t rows;
+    int count, stretch;  // tensors, rows of a block
 };
 // What the step is made of, and the two places of which the host need not know.
 struct Step {
@@ -59,221 +59,277 @@ struct Factors {
 };
 
 template <int MAX>
-__device__ __forceinline__ int find_tensor(const Table<MAX> &tab, int chunk) {
+__device__ __forceinline__ int find_tensor(const Table<MAX> &tab, int64_t row) {
     int lo = 0, hi = tab.count;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (tab.t[mid].first <= chunk) lo = mid; else hi = mid;
+        if (tab.t[mid].first <= row) lo = mid; else hi = mid;
     }
     return lo;
 }
 
-// Four values as they are stored (16-bit ones in the first half).
-__device__ __forceinline__ uint4 raw4(const void *base, int type, int64_t at) {
-    if (type == GDN_DTYPE_F32) return *reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + at);
-    const uint2 h = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(base) + at);
-    return make_uint4(h.x, h.y, 0, 0);
-}
 __device__ __forceinline__ uint32_t raw1(const void *base, int type, int64_t at) {
     return type == GDN_DTYPE_F32 ? static_cast<const uint32_t *>(base)[at] : static_cast<const uint16_t *>(base)[at];
 }
-__device__ __forceinline__ void widen2(uint32_t w, int type, float *v) {
-    const float2 f = type == GDN_DTYPE_F16 ? __half22float2(*reinterpret_cast<__half2 *>(&w))
-                                           : __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&w));
-    v[0] = f.x, v[1] = f.y;
-}
-__device__ __forceinline__ void widen4(const uint4 &r, int type, float *v) {
-    if (type == GDN_DTYPE_F32) {
-        v[0] = __uint_as_float(r.x), v[1] = __uint_as_float(r.y);
-        v[2] = __uint_as_float(r.z), v[3] = __uint_as_float(r.w);
-    } else {
-        widen2(r.x, type, v);
-        widen2(r.y, type, v + 2);
-    }
+__device__ __forceinline__ float2 widen2(uint32_t w, int type) {
+    return type == GDN_DTYPE_F16 ? __half22float2(*reinterpret_cast<__half2 *>(&w))
+                                 : __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&w));
 }
 __device__ __forceinline__ float widen1(uint32_t r, int type) {
-    if (type == GDN_DTYPE_F32) return __uint_as_float(r);
-    float v[2];
-    widen2(r, type, v);
-    return v[0];
-}
-__device__ __forceinline__ void put4(void *base, int type, int64_t at, const float (&v)[4]) {
-    if (type == GDN_DTYPE_F32) store_values<float, 4>(static_cast<float *>(base) + at, v);
-    else if (type == GDN_DTYPE_F16) store_values<__half, 4>(static_cast<__half *>(base) + at, v);
-    else store_values<__nv_bfloat16, 4>(static_cast<__nv_bfloat16 *>(base) + at, v);
+    return type == GDN_DTYPE_F32 ? __uint_as_float(r) : widen2(r, type).x;
 }
 __device__ __forceinline__ void put1(void *base, int type, int64_t at, float v) {
     if (type == GDN_DTYPE_F32) static_cast<float *>(base)[at] = v;
     else if (type == GDN_DTYPE_F16) static_cast<__half *>(base)[at] = __float2half_rn(v);
     else static_cast<__nv_bfloat16 *>(base)[at] = __float2bfloat16_rn(v);
 }
-// e4m3 codes, four in a word, first lowest.
-__device__ __forceinline__ void decode4(uint32_t w, float *v) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        v[2 * i] = f.x, v[2 * i + 1] = f.y;
-    }
+// e4m3 codes, two in a half-word, first lowest.
+__device__ __forceinline__ float2 decode2(uint32_t w) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
-__device__ __forceinline__ uint32_t encode4(const float *v) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
-    return lo | hi << 16;
+__device__ __forceinline__ uint32_t encode2(float2 v) { return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3); }
+
+// Pairs of elements throughout (packed fp32).  The root and the reciprocal are the
+// approximate ones, 2 ulp each: what they leave of p is below p's own rounding.  An 8-bit
+// element takes 44 instructions so; one element at a time with rounded roots and
+// quotients took 83, and 2^26 bf16 elements 227 us in place of 177.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float root_of(float v) {
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// Of a number that is not subnormal (a root is above 2^-75, unless it is 0).
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// A pair of elements: p, m and v (in 32 bits) and their gradients.  Returns the roots of v.
+__device__ __forceinline__ float2 update(const Step &st, const Factors &f, float2 g, float2 &p, float2 &m, float2 &v) {
+    g = __fmul2_rn(g, both(f.clip));
+    m = __ffma2_rn(both(st.beta1), m, __fmul2_rn(both(st.rest1), g));
+    v = __ffma2_rn(both(st.beta2), v, __fmul2_rn(__fmul2_rn(both(st.rest2), g), g));
+    const float2 root = make_float2(root_of(v.x), root_of(v.y));
+    const float2 den = __ffma2_rn(root, both(f.unroot), both(f.eps));
+    const float2 q = __fmul2_rn(m, make_float2(reciprocal(den.x), reciprocal(den.y)));
+    p = __ffma2_rn(both(-f.rate), q, __ffma2_rn(both(-f.decay), p, p));
+    return root;
 }
 
 // A block's scale and the reciprocal with which quotients are formed.
 struct Scale {
     float s, inv;
 };
-__device__ __forceinline__ Scale scale_of(const float (&y)[8]) {
+__device__ __forceinline__ Scale scale_of(const float2 (&y)[4]) {
     float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(y[i]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const float s = __fdiv_rn(fmaxf(a, 0x1p-100f), 448.f);
-    return {s, __frcp_rn(s)};
+    for (int i = 0; i < 4; ++i) a = fmaxf(a, fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
+    // numbers that are not negative compare as their bits do
+    a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+    const float s = fmaxf(a, 0x1p-100f) * (1.f / 448.f);
+    return {s, reciprocal(s)};
 }
 // y / s as a division rounds it: one product and two fma.
-__device__ __forceinline__ float quotient(float y, const Scale &s) {
-    const float q = y * s.inv;
-    return fmaf(fmaf(-q, s.s, y), s.inv, q);
+__device__ __forceinline__ float2 quotient(float2 y, const Scale &s) {
+    const float2 q = __fmul2_rn(y, both(s.inv));
+    return __ffma2_rn(__ffma2_rn(q, both(-s.s), y), both(s.inv), q);
+}
+__device__ __forceinline__ float at_least(float q, float root) { return root > 0.f ? fmaxf(q, 0x1p-9f) : q; }
+__device__ __forceinline__ float2 root_code(float2 root, const Scale &s) {
+    const float2 q = quotient(root, s);
+    return make_float2(at_least(q.x, root.x), at_least(q.y, root.y));
 }
 
-// One element: p, m and v (in 32 bits) and its gradient.
-__device__ __forceinline__ void update(const Step &st, const Factors &f, float g, float &p, float &m, float &v,
-                                       float &root) {
-    g *= f.clip;
-    m = fmaf(st.beta1, m, st.rest1 * g);
-    v = fmaf(st.beta2, v, st.rest2 * g * g);
-    root = sqrtf(v);
-    p = fmaf(-f.decay, p, p) - f.rate * (m / fmaf(root, f.unroot, f.eps));
+// Four adjacent values, of a row in shared memory and to one in global memory.
+template <bool WIDE>
+__device__ __forceinline__ void get4(const unsigned char *row, int type, int at, float2 *v) {
+    if constexpr (WIDE) {
+        const float4 w = *reinterpret_cast<const float4 *>(row + 4 * at);
+        v[0] = make_float2(w.x, w.y), v[1] = make_float2(w.z, w.w);
+    } else {
+        const uint2 w = *reinterpret_cast<const uint2 *>(row + 2 * at);
+        v[0] = widen2(w.x, type), v[1] = widen2(w.y, type);
+    }
+}
+__device__ __forceinline__ void put4(float *base, int64_t at, const float2 *v) {
+    *reinterpret_cast<float4 *>(base + at) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+}
+template <bool WIDE>
+__device__ __forceinline__ void put4(void *base, int type, int64_t at, const float2 *v) {
+    if constexpr (WIDE) {
+        put4(static_cast<float *>(base), at, v);
+    } else {
+        const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
+        if (type == GDN_DTYPE_F16) store_values<__half, 4>(static_cast<__half *>(base) + at, f);
+        else store_values<__nv_bfloat16, 4>(static_cast<__nv_bfloat16 *>(base) + at, f);
+    }
 }
 
-// A row of up to 256 elements from `at` on.
-template <bool EIGHT, bool WHOLE>
-__device__ __forceinline__ void row_step(const Step &st, const Factors &f, const Tensor &t, int64_t at) {
-    const int lane = threadIdx.x & 31;
+// Whole rows of 256 elements come through shared memory (cp.async), several on their way
+// a warp, without a register: with the next row in registers 2^26 bf16 elements with
+// 8-bit states took 171 us, for 128 (three rows on their way: 181).  A lane has elements 4 lane + 128 j ... + 3.
+// PW, GW: fp32 parameters, gradients; MASTER: 16-bit parameters with copies.
+template <bool EIGHT, bool PW, bool MASTER, bool GW>
+struct Whole {
+    static constexpr int kP = PW || MASTER ? 4 * kRow : 2 * kRow, kG = GW ? 4 * kRow : 2 * kRow;
+    static constexpr int kState = EIGHT ? kRow : 4 * kRow;
+    static constexpr int kBytes = kP + kG + 2 * kState + 16;  // and the scales
+    // as many rows a warp as leave room for four (fp32 states: three) blocks an SM, two at least
+    static constexpr int kSlots = 72 * 1024 / (kWarps * kBytes);
+    static constexpr int kSmem = EIGHT ? kWarps * kSlots * kBytes : 0;
+
+    template <int N>
+    static __device__ __forceinline__ void copy(unsigned char *to, const void *from, int64_t row, int lane) {
+        static_assert(N % 512 == 0, "16 bytes a lane");
+        const char *src = static_cast<const char *>(from) + row * N;
+#pragma unroll
+        for (int o = 0; o < N; o += 512) ptx::cp_async16(to + o + 16 * lane, src + o + 16 * lane, 16);
+    }
+    static __device__ __forceinline__ void load(unsigned char *slot, const Tensor &t, int64_t row, int lane) {
+        copy<kP>(slot, MASTER ? static_cast<const void *>(t.master) : t.p, row, lane);
+        copy<kG>(slot + kP, t.g, row, lane);
+        unsigned char *m = slot + kP + kG;
+        // half a warp each
+        const char *src = static_cast<const char *>(lane < 16 ? t.m : t.v) + row * kRow;
+        ptx::cp_async16(m + 16 * lane, src + 16 * (lane & 15), 16);
+        if (lane < 2) ptx::cp_async4(m + 2 * kState + 4 * lane, (lane ? t.vs : t.ms) + row);
+    }
+    static __device__ __forceinline__ void step(const unsigned char *slot, const Step &st, const Factors &f,
+                                                const Tensor &t, int64_t row, int lane) {
+        const unsigned char *sp, *sg, *sm, *sv;
+        float2 p[4], m[4], v[4], root[4];
+        float ms = 0.f, vs = 0.f;
+        if constexpr (EIGHT) {
+            sp = slot, sg = sp + kP, sm = sg + kG, sv = sm + kState;
+            ms = *reinterpret_cast<const float *>(sv + kState);
+            vs = *reinterpret_cast<const float *>(sv + kState + 4);
+        } else {
+            sp = static_cast<const unsigned char *>(MASTER ? static_cast<const void *>(t.master) : t.p) + row * kP;
+            sg = static_cast<const unsigned char *>(t.g) + row * kG;
+            sm = static_cast<const unsigned char *>(t.m) + row * kState;
+            sv = static_cast<const unsigned char *>(t.v) + row * kState;
+        }
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+            const int e = 4 * lane + 128 * j;
+            float2 g[2];
+            get4<GW>(sg, t.g_type, e, g);
+            get4<PW || MASTER>(sp, t.p_type, e, p + 2 * j);
+            if constexpr (EIGHT) {
+                const uint32_t cm = *reinterpret_cast<const uint32_t *>(sm + e);
+                const uint32_t cv = *reinterpret_cast<const uint32_t *>(sv + e);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    m[2 * j + h] = __fmul2_rn(decode2(cm >> 16 * h & 0xffff), both(ms));
+                    v[2 * j + h] = __fmul2_rn(decode2(cv >> 16 * h & 0xffff), both(vs));
+                    v[2 * j + h] = __fmul2_rn(v[2 * j + h], v[2 * j + h]);
+                }
+            } else {
+                get4<true>(sm, 0, e, m + 2 * j);
+                get4<true>(sv, 0, e, v + 2 * j);
+            }
+#pragma unroll
+            for (int i = 2 * j; i < 2 * j + 2; ++i) root[i] = update(st, f, g[i - 2 * j], p[i], m[i], v[i]);
+        }
+        if (EIGHT) __syncwarp();  // the slot has been read
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+            const int64_t e = row * kRow + 4 * lane + 128 * j;
+            if (MASTER) put4(t.master, e, p + 2 * j);
+            put4<PW>(t.p, t.p_type, e, p + 2 * j);
+            if constexpr (!EIGHT) {
+                put4(static_cast<float *>(t.m), e, m + 2 * j);
+                put4(static_cast<float *>(t.v), e, v + 2 * j);
+            }
+        }
+        if constexpr (EIGHT) {
+            const Scale qm = scale_of(m), qv = scale_of(root);
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) {
+                const int64_t e = row * (kRow / 4) + lane + 32 * j;
+                static_cast<uint32_t *>(t.m)[e] =
+                    encode2(quotient(m[2 * j], qm)) | encode2(quotient(m[2 * j + 1], qm)) << 16;
+                static_cast<uint32_t *>(t.v)[e] =
+                    encode2(root_code(root[2 * j], qv)) | encode2(root_code(root[2 * j + 1], qv)) << 16;
+            }
+            if (lane == 0) t.ms[row] = qm.s, t.vs[row] = qv.s;
+        }
+    }
+};
+
+// A row of up to 256 elements at any address: a lane has elements lane + 32 i.
+template <bool EIGHT>
+__device__ __forceinline__ void loose_row(const Step &st, const Factors &f, const Tensor &t, int64_t at, int lane) {
     const int n = (int)(t.n - at < kRow ? t.n - at : kRow);
     const int pt = t.master ? GDN_DTYPE_F32 : t.p_type, gt = t.g_type;
     const void *pin = t.master ? t.master : t.p;
-    const uint8_t *mc = static_cast<const uint8_t *>(t.m), *vc = static_cast<const uint8_t *>(t.v);
-    float g[8], p[8], m[8], v[8], root[8];
-    float ms = 0.f, vs = 0.f;
-    if (EIGHT) ms = t.ms[at / kRow], vs = t.vs[at / kRow];
-    // WHOLE: elements 4 lane + 128 j ...; else lane + 32 i, zeros beyond the end
-    if (WHOLE) {
-        uint4 gr[kGroups], pr[kGroups], mr[kGroups], vr[kGroups];
-#pragma unroll
-        for (int j = 0; j < kGroups; ++j) {
-            const int64_t e = at + 4 * lane + 128 * j;
-            gr[j] = raw4(t.g, gt, e);
-            pr[j] = raw4(pin, pt, e);
-            if (EIGHT) {
-                mr[j].x = *reinterpret_cast<const uint32_t *>(mc + e);
-                vr[j].x = *reinterpret_cast<const uint32_t *>(vc + e);
-            } else {
-                mr[j] = raw4(t.m, GDN_DTYPE_F32, e);
-                vr[j] = raw4(t.v, GDN_DTYPE_F32, e);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kGroups; ++j) {
-            widen4(gr[j], gt, g + 4 * j);
-            widen4(pr[j], pt, p + 4 * j);
-            if (EIGHT) {
-                decode4(mr[j].x, m + 4 * j);
-                decode4(vr[j].x, v + 4 * j);
-            } else {
-                widen4(mr[j], GDN_DTYPE_F32, m + 4 * j);
-                widen4(vr[j], GDN_DTYPE_F32, v + 4 * j);
-            }
-        }
-    } else {
-        uint32_t gr[8], pr[8], mr[8], vr[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t e = at + lane + 32 * i;
-            gr[i] = pr[i] = mr[i] = vr[i] = 0;
-            if (lane + 32 * i < n) {
-                gr[i] = raw1(t.g, gt, e);
-                pr[i] = raw1(pin, pt, e);
-                mr[i] = EIGHT ? mc[e] : static_cast<const uint32_t *>(t.m)[e];
-                vr[i] = EIGHT ? vc[e] : static_cast<const uint32_t *>(t.v)[e];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            g[i] = widen1(gr[i], gt);
-            p[i] = widen1(pr[i], pt);
-            if (EIGHT) {
-                float q[4];
-                decode4(mr[i] | vr[i] << 8, q);
-                m[i] = q[0], v[i] = q[1];
-            } else {
-                m[i] = __uint_as_float(mr[i]), v[i] = __uint_as_float(vr[i]);
-            }
-        }
-    }
+    uint8_t *mc = static_cast<uint8_t *>(t.m), *vc = static_cast<uint8_t *>(t.v);
+    uint32_t gr[8], pr[8], mr[8], vr[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (EIGHT) {
-            m[i] *= ms;
-            v[i] *= vs;
-            v[i] *= v[i];
+        const int64_t e = at + lane + 32 * i;
+        gr[i] = pr[i] = mr[i] = vr[i] = 0;
+        if (lane + 32 * i < n) {
+            gr[i] = raw1(t.g, gt, e);
+            pr[i] = raw1(pin, pt, e);
+            mr[i] = EIGHT ? mc[e] : static_cast<const uint32_t *>(t.m)[e];
+            vr[i] = EIGHT ? vc[e] : static_cast<const uint32_t *>(t.v)[e];
         }
-        update(st, f, g[i], p[i], m[i], v[i], root[i]);
-        // beyond the end nothing has a say in the scales (with eps 0 it may be NaN)
-        if (EIGHT && !WHOLE && lane + 32 * i >= n) m[i] = root[i] = 0.f;
     }
-    if (EIGHT) {
-        const Scale sm = scale_of(m), sv = scale_of(root);
+    float2 p[4], m[4], v[4], root[4];
+    const float ms = EIGHT ? t.ms[at / kRow] : 0.f, vs = EIGHT ? t.vs[at / kRow] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            m[i] = quotient(m[i], sm);
-            v[i] = root[i] > 0.f ? fmaxf(quotient(root[i], sv), 0x1p-9f) : root[i];
+    for (int i = 0; i < 4; ++i) {
+        const float2 g = make_float2(widen1(gr[2 * i], gt), widen1(gr[2 * i + 1], gt));
+        p[i] = make_float2(widen1(pr[2 * i], pt), widen1(pr[2 * i + 1], pt));
+        if (EIGHT) {
+            m[i] = __fmul2_rn(decode2(mr[2 * i] | mr[2 * i + 1] << 8), both(ms));
+            v[i] = __fmul2_rn(decode2(vr[2 * i] | vr[2 * i + 1] << 8), both(vs));
+            v[i] = __fmul2_rn(v[i], v[i]);
+        } else {
+            m[i] = make_float2(__uint_as_float(mr[2 * i]), __uint_as_float(mr[2 * i + 1]));
+            v[i] = make_float2(__uint_as_float(vr[2 * i]), __uint_as_float(vr[2 * i + 1]));
         }
+        root[i] = update(st, f, g, p[i], m[i], v[i]);
+    }
+    Scale sm = {0.f, 0.f}, sv = {0.f, 0.f};
+    if (EIGHT) {
+        // zeros beyond the end have states of zero (with an eps of 0 only their p is NaN)
+        sm = scale_of(m), sv = scale_of(root);
         if (lane == 0) t.ms[at / kRow] = sm.s, t.vs[at / kRow] = sv.s;
     }
-    if (WHOLE) {
 #pragma unroll
-        for (int j = 0; j < kGroups; ++j) {
-            const int64_t e = at + 4 * lane + 128 * j;
-            const float(&pj)[4] = *reinterpret_cast<const float(*)[4]>(p + 4 * j);
-            if (t.master) store_values<float, 4>(t.master + e, pj);
-            put4(t.p, t.p_type, e, pj);
-            if (EIGHT) {
-                *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(t.m) + e) = encode4(m + 4 * j);
-                *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(t.v) + e) = encode4(v + 4 * j);
-            } else {
-                store_values<float, 4>(static_cast<float *>(t.m) + e, *reinterpret_cast<const float(*)[4]>(m + 4 * j));
-                store_values<float, 4>(static_cast<float *>(t.v) + e, *reinterpret_cast<const float(*)[4]>(v + 4 * j));
-            }
-        }
-    } else {
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t cm = EIGHT ? encode2(quotient(m[i], sm)) : 0, cv = EIGHT ? encode2(root_code(root[i], sv)) : 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t e = at + lane + 32 * i;
-            if (lane + 32 * i >= n) continue;
-            if (t.master) t.master[e] = p[i];
-            put1(t.p, t.p_type, e, p[i]);
+        for (int h = 0; h < 2; ++h) {
+            const int64_t e = at + lane + 32 * (2 * i + h);
+            if (lane + 32 * (2 * i + h) >= n) continue;
+            const float y = h ? p[i].y : p[i].x;
+            if (t.master) t.master[e] = y;
+            put1(t.p, t.p_type, e, y);
             if (EIGHT) {
-                const float q[4] = {m[i], v[i], 0.f, 0.f};
-                const uint32_t c = encode4(q);
-                static_cast<uint8_t *>(t.m)[e] = (uint8_t)c;
-                static_cast<uint8_t *>(t.v)[e] = (uint8_t)(c >> 8);
+                mc[e] = (uint8_t)(cm >> 8 * h), vc[e] = (uint8_t)(cv >> 8 * h);
             } else {
-                static_cast<float *>(t.m)[e] = m[i];
-                static_cast<float *>(t.v)[e] = v[i];
+                static_cast<float *>(t.m)[e] = h ? m[i].y : m[i].x;
+                static_cast<float *>(t.v)[e] = h ? v[i].y : v[i].x;
             }
         }
     }
 }
 
-template <bool EIGHT, int MAX>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<MAX> tab,
-                                                         const __grid_constant__ Step st) {
+__device__ __forceinline__ bool whole_row(const Tensor &t, int64_t row) { return t.whole && (row + 1) * kRow <= t.n; }
+
+// A block has a stretch of adjacent rows, which its warps take in turn, and the device
+// as many blocks as there are stretches: SMs are not equally fast (equal shares of a
+// persistent grid: 235 us in place of 218 for 2^26 bf16 elements with fp32 states).
+template <bool EIGHT, bool PW, bool MASTER, bool GW, int MAX>
+__global__ void __launch_bounds__(kThreads, EIGHT ? 3 : 2) adamw_kernel(const __grid_constant__ Table<MAX> tab,
+                                                                        const __grid_constant__ Step st) {
+    extern __shared__ __align__(16) unsigned char slots[];
     ptx::grid_wait();
     Factors f;
     f.clip = 1.f;
@@ -297,30 +353,57 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     f.decay = lr * st.weight_decay;
     f.unroot = __fdiv_rn(1.f, root2);
     f.eps = st.eps;
-    const int warp = threadIdx.x >> 5;
-    for (int chunk = blockIdx.x; chunk < tab.chunks; chunk += gridDim.x) {
-        const Tensor &t = tab.t[find_tensor(tab, chunk)];
-        const int64_t row = (int64_t)(chunk - t.first) * tab.chunk;
-        for (int r = warp; r < tab.chunk; r += kWarps) {
-            const int64_t at = (row + r) * kRow;
-            if (at >= t.n) break;
-            if (t.whole && at + kRow <= t.n) row_step<EIGHT, true>(st, f, t, at);
-            else row_step<EIGHT, false>(st, f, t, at);
+    using Rows = Whole<EIGHT, PW, MASTER, GW>;
+    constexpr int N = EIGHT ? Rows::kSlots : 1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t row = (int64_t)blockIdx.x * tab.stretch + warp;
+    const int64_t stop = row - warp + tab.stretch < tab.rows ? row - warp + tab.stretch : tab.rows;
+    int i = find_tensor(tab, row);
+    // slots, of rows ahead of this one (8-bit states)
+    unsigned char *mine = slots + warp * N * Rows::kBytes;
+    int64_t ahead = row;
+    int ia = i, at = 0, to = 0;
+    auto request = [&] {
+        while (ia + 1 < tab.count && tab.t[ia + 1].first <= ahead) ++ia;
+        const Tensor &t = tab.t[ia];
+        if (ahead < stop && whole_row(t, ahead - t.first))
+            Rows::load(mine + to * Rows::kBytes, t, ahead - t.first, lane);
+        ptx::cp_async_commit();
+        ahead += kWarps;
+        to = to + 1 == N ? 0 : to + 1;
+    };
+    if constexpr (EIGHT) {
+#pragma unroll 1
+        for (int k = 0; k < N - 1; ++k) request();
+    }
+    for (; row < stop; row += kWarps) {
+        if constexpr (EIGHT) {
+            request();
+            ptx::cp_async_wait<N - 1>();
+            __syncwarp();
         }
+        while (i + 1 < tab.count && tab.t[i + 1].first <= row) ++i;
+        const Tensor &t = tab.t[i];
+        if (whole_row(t, row - t.first)) Rows::step(mine + at * Rows::kBytes, st, f, t, row - t.first, lane);
+        else loose_row<EIGHT>(st, f, t, (row - t.first) * kRow, lane);
+        at = at + 1 == N ? 0 : at + 1;
     }
 }
 
-bool words(const void *p, int type) { return aligned(p, type == GDN_DTYPE_F32 ? 16 : type == GDN_DTYPE_E4M3 ? 4 : 8); }
+// Tensors of one kind share a kernel: the width of parameters and of gradients, and
+// whether there is a copy.  (An fp32 parameter with a copy goes element by element.)
+int kind_of(const gdn_adamw_args *a, int i) {
+    const bool pw = a->param_dtypes[i] == GDN_DTYPE_F32, gw = a->grad_dtypes[i] == GDN_DTYPE_F32;
+    return (pw ? 0 : a->master && a->master[i] ? 2 : 1) * 2 + gw;
+}
+constexpr int kKinds = 6;
 
-// Fills a table with tensors i, i + 1, ...; returns the first that is not in it.
+// Fills a table with tensors of a kind from i on; returns the first that was not looked at.
 template <int MAX>
-int fill(const gdn_adamw_args *a, int i, int chunk, Table<MAX> *tab) {
-    tab->count = tab->chunks = 0;
-    tab->chunk = chunk;
+int fill(const gdn_adamw_args *a, int i, int kind, Table<MAX> *tab) {
+    tab->count = 0, tab->rows = 0;
     for (; i < a->count && tab->count < MAX; ++i) {
-        if (a->sizes[i] == 0) continue;
-        const int64_t per = (int64_t)chunk * kRow, chunks = (a->sizes[i] + per - 1) / per;
-        if (tab->chunks + chunks > (1LL << 30)) break;
+        if (a->sizes[i] == 0 || kind_of(a, i) != kind) continue;
         Tensor &t = tab->t[tab->count++];
         t.p = a->params[i], t.g = a->grads[i], t.m = a->exp_avg[i], t.v = a->exp_avg_sq[i];
         const bool eight = a->state_dtype == GDN_DTYPE_E4M3;
@@ -328,27 +411,49 @@ int fill(const gdn_adamw_args *a, int i, int chunk, Table<MAX> *tab) {
         t.vs = eight ? a->exp_avg_sq_scales[i] : nullptr;
         t.master = a->master ? a->master[i] : nullptr;
         t.n = a->sizes[i];
-        t.first = tab->chunks;
+        t.first = tab->rows;
         t.p_type = (uint8_t)a->param_dtypes[i], t.g_type = (uint8_t)a->grad_dtypes[i];
-        t.whole = words(t.p, t.p_type) && words(t.g, t.g_type) && words(t.m, a->state_dtype) &&
-                  words(t.v, a->state_dtype) && words(t.master, GDN_DTYPE_F32);
-        tab->chunks += (int)chunks;
+        t.whole = aligned(t.p, 16) && aligned(t.g, 16) && aligned(t.m, 16) && aligned(t.v, 16) &&
+                  aligned(t.master, 16) && !(t.master && t.p_type == GDN_DTYPE_F32);
+        tab->rows += (t.n + kRow - 1) / kRow;
     }
+    // rows of a warp: one of few, so that they reach all SMs, up to kStretch of many
+    int64_t each = tab->rows / (kWarps * 152 * 4);
+    each = each < 1 ? 1 : each > kStretch ? kStretch : each;
+    while (tab->rows / (each * kWarps) >= 1LL << 31) each *= 2;
+    tab->stretch = (int)each * kWarps;
     return i;
+}
+
+template <int KIND, bool EIGHT, int MAX>
+cudaError_t launch(const Table<MAX> &tab, const Step &st, cudaStream_t stream) {
+    constexpr bool PW = KIND / 2 == 0, MASTER = KIND / 2 == 2, GW = KIND % 2 == 1;
+    constexpr int smem = Whole<EIGHT, PW, MASTER, GW>::kSmem;
+    const auto kernel = adamw_kernel<EIGHT, PW, MASTER, GW, MAX>;
+    cudaError_t e = smem_attr((const void *)kernel, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = (tab.rows + tab.stretch - 1) / tab.stretch;
+    return launch_early(kernel, (unsigned)blocks, kThreads, smem, stream, tab, st);
 }
 
 template <bool EIGHT, int MAX>
 cudaError_t run(const gdn_adamw_args *a, const Step &st, cudaStream_t stream) {
-    int64_t elements = 0;
-    for (int j = 0; j < a->count; ++j) elements += a->sizes[j];
-    const int chunk = elements <= kSmall ? kSmallChunk : kChunk;
     Table<MAX> tab;
-    for (int i = 0; i < a->count;) {
-        i = fill<MAX>(a, i, chunk, &tab);
-        if (tab.chunks == 0) continue;
-        const int blocks = tab.chunks < kBlocks ? tab.chunks : kBlocks;
-        const cudaError_t e = launch_early(adamw_kernel<EIGHT, MAX>, blocks, kThreads, 0, stream, tab, st);
-        if (e != cudaSuccess) return e;
+    for (int kind = 0; kind < kKinds; ++kind) {
+        for (int i = 0; i < a->count;) {
+            i = fill<MAX>(a, i, kind, &tab);
+            if (tab.rows == 0) continue;
+            cudaError_t e;
+            switch (kind) {
+                case 0: e = launch<0, EIGHT, MAX>(tab, st, stream); break;
+                case 1: e = launch<1, EIGHT, MAX>(tab, st, stream); break;
+                case 2: e = launch<2, EIGHT, MAX>(tab, st, stream); break;
+                case 3: e = launch<3, EIGHT, MAX>(tab, st, stream); break;
+                case 4: e = launch<4, EIGHT, MAX>(tab, st, stream); break;
+                default: e = launch<5, EIGHT, MAX>(tab, st, stream); break;
+            }
+            if (e != cudaSuccess) return e;
+        }
     }
     return cudaSuccess;
 }
