@@ -88,8 +88,9 @@ gdn_status validate(const gdn_glu_args *a) {
     if (a->rows > 0 && (!a->x || !a->w_gate || !a->w_up || !a->out))
         return fail(GDN_ERR_INVALID, "x, w_gate, w_up and out are required");
     if (!aligned(a->x, 2) || !aligned(a->w_gate, 2) || !aligned(a->w_up, 2) || !aligned(a->out, 2) ||
-        !aligned(a->gates, 2) || !aligned(a->error_word, 4))
+        !aligned(a->error_word, 4))
         return fail(GDN_ERR_INVALID, "a pointer is not aligned to its element size");
+    if (!aligned(a->gates, 16)) return fail(GDN_ERR_INVALID, "gates must be aligned to 16 bytes");
     return GDN_OK;
 }
 gdn_status validate_grad(const gdn_glu_grad_args *a) {
@@ -106,9 +107,10 @@ gdn_status validate_grad(const gdn_glu_grad_args *a) {
     if (a->rows > 0 && a->dx && (!a->w_gate || !a->w_up)) return fail(GDN_ERR_INVALID, "w_gate and w_up are required");
     if (a->rows > 0 && a->d_w_gate && !a->x) return fail(GDN_ERR_INVALID, "x is required");
     if (!aligned(a->x, 2) || !aligned(a->w_gate, 2) || !aligned(a->w_up, 2) || !aligned(a->d_out, 2) ||
-        !aligned(a->gates, 2) || !aligned(a->dx, 2) || !aligned(a->d_w_gate, 2) || !aligned(a->d_w_up, 2) ||
+        !aligned(a->dx, 2) || !aligned(a->d_w_gate, 2) || !aligned(a->d_w_up, 2) ||
         !aligned(a->error_word, 4))
         return fail(GDN_ERR_INVALID, "a pointer is not aligned to its element size");
+    if (!aligned(a->gates, 16)) return fail(GDN_ERR_INVALID, "gates must be aligned to 16 bytes");
     return GDN_OK;
 }
 
@@ -143,17 +145,10 @@ cudaError_t bring(const Operand &o, cudaStream_t s) {
 bool map_of(CUtensorMap *m, const Operand &o, bool bf16, int box) {
     return make_map(m, o.at, bf16, o.stride, o.cols, o.rows, box);
 }
-Result result_of(void *at, int64_t stride) {
-    Result r = {};
-    r.at = at, r.stride = stride;
-    return r;
-}
-bool map_results(Product *p, int count, bool bf16) {
-    p->by_map = 1;
-    for (int i = 0; i < count; ++i) p->by_map = p->by_map && lines(p->c[i].at, p->c[i].stride);
-    for (int i = 0; p->by_map && i < count; ++i)
-        if (!make_map(&p->c[i].map, p->c[i].at, bf16, p->c[i].stride, p->cols, p->rows, 32)) return false;
-    return true;
+// A result of p.rows rows, by tensor map where its rows are words of 16 bytes.
+bool result(Result *r, const Product &p, void *at, int64_t stride, int cols, bool bf16) {
+    r->at = at, r->stride = stride, r->by_map = lines(at, stride);
+    return !r->by_map || make_map(&r->map, at, bf16, stride, cols, p.rows, 32);
 }
 void tiles_of(Product *p, int64_t rows, int cols, int width, int results, int64_t depth) {
     p->rows = rows, p->cols = cols;
@@ -232,21 +227,19 @@ gdn_status gdn_glu(const gdn_glu_args *a, void *ws, size_t ws_bytes, gdn_stream 
         Few p = {};
         p.x = a->x, p.wg = a->w_gate, p.wu = a->w_up, p.out = a->out, p.gates = a->gates;
         p.xs = or_dense(a->x_stride, a->dim), p.os = os;
-        p.T = (int)a->rows, p.D = a->dim, p.F = a->inner, p.act = a->activation;
+        p.T = (int)a->rows, p.D = a->dim, p.F = a->inner, p.Fp = (int)padded(a->inner), p.act = a->activation;
         p.words = lines(a->x, p.xs) && lines(a->w_gate, a->dim) && lines(a->w_up, a->dim);
         return gdn::cuda_status(bf16 ? launch_few_bf16(p, s) : launch_few_f16(p, s));
     }
     Product p = {};
     tiles_of(&p, a->rows, a->inner, 128, 1, a->dim);
     p.act = a->activation, p.gates = a->gates != nullptr, p.err = a->error_word;
-    p.c[0] = result_of(a->out, os);
-    if (a->gates) {
-        p.c[1] = result_of(a->gates, 2 * (int64_t)a->inner);
-        p.c[2] = result_of(static_cast<uint16_t *>(a->gates) + a->inner, 2 * (int64_t)a->inner);
-    }
+    const int Fp = (int)padded(a->inner);
     if (!map_of(&p.a[0], f.x, bf16, 128) || !map_of(&p.b[0], f.wg, bf16, 128) || !map_of(&p.b[1], f.wu, bf16, 128) ||
-        !map_results(&p, a->gates ? 3 : 1, bf16))
+        !result(&p.c[0], p, a->out, os, a->inner, bf16))
         return no_map();
+    for (int i = 0; a->gates && i < 2; ++i)
+        if (!result(&p.c[1 + i], p, static_cast<uint16_t *>(a->gates) + i * Fp, 2 * (int64_t)Fp, Fp, bf16)) return no_map();
     cudaError_t e = bring(f.x, s);
     if (e == cudaSuccess) e = bring(f.wg, s);
     if (e == cudaSuccess) e = bring(f.wu, s);
@@ -280,23 +273,22 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *a, void *ws, size_t ws_byte
     if (a->dx) {
         tiles_of(&in, T, D, 256, 1, F);
         in.err = a->error_word;
-        in.c[0] = result_of(a->dx, or_dense(a->dx_stride, D));
         if (!map_of(&in.a[0], b.dg, bf16, 128) || !map_of(&in.a[1], b.du, bf16, 128) ||
-            !map_of(&in.b[0], b.wg, bf16, 64) || !map_of(&in.b[1], b.wu, bf16, 64) || !map_results(&in, 1, bf16))
+            !map_of(&in.b[0], b.wg, bf16, 64) || !map_of(&in.b[1], b.wu, bf16, 64) ||
+            !result(&in.c[0], in, a->dx, or_dense(a->dx_stride, D), D, bf16))
             return no_map();
     }
     if (a->d_w_gate) {
         tiles_of(&w, F, D, 256, 2, T);
         w.err = a->error_word;
-        w.c[0] = result_of(a->d_w_gate, D), w.c[1] = result_of(a->d_w_up, D);
         if (!map_of(&w.a[0], b.dg, bf16, 64) || !map_of(&w.a[1], b.du, bf16, 64) || !map_of(&w.b[0], b.x, bf16, 64) ||
-            !map_results(&w, 2, bf16))
+            !result(&w.c[0], w, a->d_w_gate, D, D, bf16) || !result(&w.c[1], w, a->d_w_up, D, D, bf16))
             return no_map();
     }
     GateGrad g = {};
     g.d_out = a->d_out, g.gates = a->gates, g.dg = const_cast<void *>(b.dg.at), g.du = const_cast<void *>(b.du.at);
-    g.rows = T, g.dos = or_dense(a->d_out_stride, F), g.ds = b.dg.stride, g.F = F, g.act = a->activation;
-    g.words = F % 8 == 0 && lines(a->d_out, g.dos) && aligned(a->gates, 16);
+    g.rows = T, g.dos = or_dense(a->d_out_stride, F), g.F = F, g.Fp = (int)padded(F), g.act = a->activation;
+    g.words = F % 8 == 0 && lines(a->d_out, g.dos);
     e = bf16 ? launch_gate_grad_bf16(g, s) : launch_gate_grad_f16(g, s);
     if (e == cudaSuccess && a->dx) {
         e = bring(b.wg, s);

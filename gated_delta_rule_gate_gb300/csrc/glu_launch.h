@@ -18,13 +18,14 @@ struct Result {
     CUtensorMap map;
     void *at;
     int64_t stride;
+    int by_map;
 };
 struct Product {
     CUtensorMap a[2], b[2];
     Result c[3];
     int64_t rows, tiles_m, tiles;  // tiles: of all results
     int cols, tiles_n, blocks_k;   // blocks_k: of 64, of one pair of operands
-    int act, gates, by_map;
+    int act, gates;
     int32_t *err;
 };
 // Fewer tokens than the tensor cores' tiles are made for.
@@ -32,14 +33,14 @@ struct Few {
     const void *x, *wg, *wu;
     void *out, *gates;  // gates may be null
     int64_t xs, os;
-    int T, D, F, act, words;
+    int T, D, F, Fp, act, words;
 };
 // d_g and d_u of d_out and the gates that the forward pass kept.
 struct GateGrad {
     const void *d_out, *gates;
     void *dg, *du;
-    int64_t rows, dos, ds;  // ds: elements between rows of dg and du
-    int F, act, words;
+    int64_t rows, dos;
+    int F, Fp, act, words;  // Fp: elements between g and u, and between rows of dg and du; words: of d_out
 };
 
 constexpr int kFewTokens = 16;

@@ -6,7 +6,7 @@
 // memory, so that a K-step of 64 takes 32 KB of each block for 16.8 MFLOP: half the
 // operand bytes of two single blocks.  Persistent; per block a warp that loads
 // (TMA, six stages), a warp whose first thread issues the products (in the pair's first
-// block) and four warps that take the finished accumulators (two of them, so that the
+// block) and eight warps that take the finished accumulators (two of them, so that the
 // next tile's products run meanwhile) out of tensor memory.
 //
 // kForward: the 256 columns are 128 of the gate and the same 128 of the up projection (the
@@ -29,9 +29,9 @@ namespace glu {
 
 constexpr int kStages = 6, kHalf = 16384;  // bytes of a block's share of an operand's stage
 constexpr int kStageBytes = 2 * kHalf;
-constexpr int kEpilogueWarps = 4, kProductThreads = 32 * (2 + kEpilogueWarps);
+constexpr int kEpilogueWarps = 8, kProductThreads = 32 * (2 + kEpilogueWarps);
 constexpr int kBox = 4096;  // 32 rows of 64 results
-constexpr int kProductSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * 2 * kBox + 256;
+constexpr int kProductSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kBox + 256;
 constexpr int kGroup = 8;  // tiles along the rows that are taken side by side
 
 struct Barriers {
@@ -83,21 +83,10 @@ __device__ __forceinline__ void put_half(unsigned char *box, int lane, int half,
     }
 }
 
-// The staged boxes of a warp, two in turn.
-struct Stage {
-    unsigned char *base;
-    int turn;
-    __device__ __forceinline__ unsigned char *next(bool by_map, int lane) {
-        unsigned char *box = base + (turn ^= 1) * kBox;
-        if (by_map && lane == 0) ptx::bulk_wait_read_all_but_last();  // the store before the last one has read it
-        __syncwarp();
-        return box;
-    }
-};
-// Sends a box of 32 rows x 64 columns to its place; what lies outside is left out.
+// Sends a warp's box of 32 rows x 64 columns to its place; what lies outside is left out.
 __device__ __forceinline__ void send(const Product &p, const Result &c, const unsigned char *box, int64_t row, int col,
                                      int lane) {
-    if (p.by_map) {
+    if (c.by_map) {
         ptx::fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -107,55 +96,64 @@ __device__ __forceinline__ void send(const Product &p, const Result &c, const un
         return;
     }
     __syncwarp();
-    const int rows = p.rows - row < 32 ? (int)(p.rows - row) : 32, cols = p.cols - col < 64 ? p.cols - col : 64;
-    for (int r = 0; r < rows; ++r) {
-        uint16_t *to = static_cast<uint16_t *>(c.at) + (row + r) * c.stride + col;
-        for (int e = lane; e < cols; e += 32)
-            to[e] = *reinterpret_cast<const uint16_t *>(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + (e & 7) * 2);
+    const int rows = p.rows - row < 32 ? (int)(p.rows - row) : 32;
+    uint16_t *to = static_cast<uint16_t *>(c.at) + row * c.stride + col;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int e = lane + 32 * h;
+        if (col + e >= p.cols) continue;
+#pragma unroll 16
+        for (int r = 0; r < 32; ++r) {
+            const uint16_t v = *reinterpret_cast<const uint16_t *>(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + (e & 7) * 2);
+            if (r < rows) to[r * c.stride + e] = v;
+        }
     }
     __syncwarp();
 }
+// Before a box is filled anew: its store has read it.
+__device__ __forceinline__ void reuse(int lane) {
+    if (lane == 0) ptx::bulk_wait_read();
+    __syncwarp();
+}
 
+// The accumulator's columns of one of two groups of warps, `half`.
 template <Mode MODE, typename T>
-__device__ __forceinline__ void take(const Product &p, const TileAt &t, uint32_t acc, int64_t row, Stage &stage,
-                                     int lane) {
+__device__ __forceinline__ void take(const Product &p, const TileAt &t, uint32_t acc, int64_t row, unsigned char *box,
+                                     int half, int lane) {
     float v[32];
     if (MODE == kForward) {
-        const int col0 = t.n * 128;
-        for (int h = 0; h < 2; ++h) {
-            const int col = col0 + 64 * h;
-            if (col >= p.cols) break;
-            unsigned char *box = stage.next(p.by_map, lane);
+        const int col = t.n * 128 + 64 * half;
+        if (col >= p.cols) return;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float u[32];
+            tc::ld32(acc + 64 * half + 32 * q, v);
+            tc::ld32(acc + 128 + 64 * half + 32 * q, u);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = activation(v[i], p.act) * u[i];
+            if (q == 0) reuse(lane);
+            put_half<T>(box, lane, q, v);
+        }
+        send(p, p.c[0], box, row, col, lane);
+        if (!p.gates) return;
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                float u[32];
-                tc::ld32(acc + 64 * h + 32 * q, v);
-                tc::ld32(acc + 128 + 64 * h + 32 * q, u);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = activation(v[i], p.act) * u[i];
+                tc::ld32(acc + 128 * k + 64 * half + 32 * q, v);
+                if (q == 0) reuse(lane);
                 put_half<T>(box, lane, q, v);
             }
-            send(p, p.c[0], box, row, col, lane);
-            if (!p.gates) continue;
-            for (int k = 0; k < 2; ++k) {
-                box = stage.next(p.by_map, lane);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    tc::ld32(acc + 128 * k + 64 * h + 32 * q, v);
-                    put_half<T>(box, lane, q, v);
-                }
-                send(p, p.c[1 + k], box, row, col, lane);
-            }
+            send(p, p.c[1 + k], box, row, col, lane);
         }
     } else {
-        const int col0 = t.n * 256;
-        for (int h = 0; h < 4; ++h) {
-            const int col = col0 + 64 * h;
-            if (col >= p.cols) break;
-            unsigned char *box = stage.next(p.by_map, lane);
+        for (int h = 2 * half; h < 2 * half + 2; ++h) {
+            const int col = t.n * 256 + 64 * h;
+            if (col >= p.cols) return;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 tc::ld32(acc + 64 * h + 32 * q, v);
+                if (q == 0) reuse(lane);
                 put_half<T>(box, lane, q, v);
             }
             send(p, p.c[t.z], box, row, col, lane);
@@ -171,7 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     constexpr int PAIRS = MODE == kInput ? 2 : 1;  // of operands that one result sums over
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     unsigned char *boxes = sm + kStages * kStageBytes;
-    Barriers &bar = *reinterpret_cast<Barriers *>(boxes + kEpilogueWarps * 2 * kBox);
+    Barriers &bar = *reinterpret_cast<Barriers *>(boxes + kEpilogueWarps * kBox);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -273,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         }
     } else {
         const int quarter = warp & 3;  // of the tensor memory's lanes, by the warp's number
-        Stage stage = {boxes + (warp - 2) * 2 * kBox, 0};
+        unsigned char *box = boxes + (warp - 2) * kBox;
         uint32_t turn = 0;
         const uint32_t taken[2] = {ptx::cluster_address(&bar.taken[0], 0), ptx::cluster_address(&bar.taken[1], 0)};
         for (int64_t i = first; i < p.tiles; i += step, ++turn) {
@@ -284,7 +282,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             tc::fence_after();
             const int64_t row = t.m * 256 + 128 * rank + 32 * quarter;
             if (row < p.rows)
-                take<MODE, T>(p, t, tmem + a * 256 + ((uint32_t)(32 * quarter) << 16), row, stage, lane);
+                take<MODE, T>(p, t, tmem + a * 256 + ((uint32_t)(32 * quarter) << 16), row, box,
+                              (warp - 2) >> 2, lane);
             tc::fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive_cluster(taken[a]);

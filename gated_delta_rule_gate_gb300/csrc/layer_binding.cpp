@@ -684,7 +684,7 @@ int32_t activation(PyObject *o) {
 // The sizes of a call: x [..., dim], weights [inner, dim].
 struct GluShape {
     int64_t rows, D, F;
-    std::vector<int64_t> out, gates;  // [..., inner], [..., 2 inner]
+    std::vector<int64_t> out, gates;  // [..., inner], [..., 2, inner rounded up to 8]
 };
 GluShape glu_shape(const Tensor &x, const Tensor &w_gate) {
     const IntArrayRef shape = x.sizes();
@@ -697,7 +697,8 @@ GluShape glu_shape(const Tensor &x, const Tensor &w_gate) {
     s.out.assign(shape.begin(), shape.end() - 1);
     s.gates = s.out;
     s.out.push_back(s.F);
-    s.gates.push_back(2 * s.F);
+    s.gates.push_back(2);
+    s.gates.push_back((s.F + 7) / 8 * 8);
     return s;
 }
 
@@ -1006,8 +1007,8 @@ PyMethodDef methods[] = {
      "ones), the weights [inner, dim] (halves of one fused weight, say), all of one dtype,\n"
      "float16 or bfloat16; out is [..., inner].  activation is \"silu\", \"gelu\" (by the\n"
      "error function), \"gelu_tanh\", \"relu\" or \"sigmoid\".  Sums are fp32.  Returns\n"
-     "out, or (out, gates) with want_gates: gates [..., 2 inner] holds g and u for\n"
-     "gdn_glu_backward, in x's dtype.  Calls of a few tokens (serving) are bound by the\n"
+     "out, or (out, gates) with want_gates: gates [..., 2, inner rounded up to a multiple\n"
+     "of 8] holds g and u for gdn_glu_backward, in x's dtype.  Calls of a few tokens (serving) are bound by the\n"
      "weights' way from memory, long ones by the tensor cores."},
     {"gdn_glu_backward", FAST(py_glu_backward),
      "gdn_glu_backward($module, d_out, x, w_gate, w_up, gates, *, activation='silu', want_dx=True, "

@@ -577,10 +577,11 @@ typedef enum gdn_activation {
  * x is [rows, dim] with x_stride elements from row to row (0: dim), out [rows, inner] with
  * out_stride (0: inner), the weights [inner, dim] contiguous, all of dtype F16 or BF16 (F32
  * is declined: GDN_ERR_UNSUPPORTED).  Products are summed in fp32 on the tensor cores, and
- * out is rounded once.  gates (NULL: not kept) receives g and u, [rows, 2 inner] contiguous
- * with a row's g first, rounded to dtype, for gdn_glu_backward; fp16 ones beyond 65504 are
- * infinite.  A few tokens (serving) take a kernel of their own.  out and gates overlap no
- * input.
+ * out is rounded once.  gates (NULL: not kept) receives g and u, rounded to dtype, for
+ * gdn_glu_backward: [rows, 2, padded] contiguous and aligned to 16 bytes, where padded is inner
+ * rounded up to a multiple of 8 (columns from inner on are 0), a row's g first; fp16 ones
+ * beyond 65504 are infinite.  A few tokens (serving) take a kernel of their own.  out and gates
+ * overlap no input.
  *
  * The workspace is device memory of gdn_glu_workspace_size() bytes, 16-byte aligned (none
  * is needed where rows of x and of the weights are whole words of 16 bytes); its contents

@@ -70,7 +70,8 @@ def check_forward(out, gates, x, wg, wu, kind):
     assert bool(((out.double() - want).abs() <= tol).all())
     if gates is not None:
         F = wg.shape[0]
-        for got, y, e in ((gates[..., :F], g, eg), (gates[..., F:], u, eu)):
+        assert gates.shape == (*x.shape[:-1], 2, -(-F // 8) * 8) and not bool(gates[..., F:].any())
+        for got, y, e in ((gates[..., 0, :F], g, eg), (gates[..., 1, :F], u, eu)):
             assert bool(((got.double() - y).abs() <= (1 + r) * e + r * y.abs() + t).all())
 
 
@@ -79,7 +80,7 @@ def reference(d_out, x, wg, wu, gates, kind):
     r, t = ref.ROUND[x.dtype], tiny(x.dtype)
     F = wg.shape[0]
     d, x6, wg6, wu6 = (v.double() for v in (d_out, x, wg, wu))
-    g, u = gates[:, :F].double(), gates[:, F:].double()
+    g, u = gates[:, 0, :F].double(), gates[:, 1, :F].double()
     a, slope, z = act(g, kind)
     dg, du = d * u * slope, d * a
     f = fuzz(g, z)
@@ -228,16 +229,16 @@ def test_leading_dimensions_and_wanted_parts():
     import gated_delta_rule_gate_gb300 as gdn
     x, wg, wu, d = draw(60, 72, 80, "bf16", seed=9)
     out, gates = gdn.gdn_glu(x.view(3, 20, 72), wg, wu, want_gates=True)
-    assert out.shape == (3, 20, 80) and gates.shape == (3, 20, 160)
-    flat = gdn.gdn_glu_backward(d, x, wg, wu, gates.view(60, 160))
+    assert out.shape == (3, 20, 80) and gates.shape == (3, 20, 2, 80)
+    flat = gdn.gdn_glu_backward(d, x, wg, wu, gates.view(60, 2, 80))
     b = gdn.gdn_glu_backward(d.view(3, 20, 80), x.view(3, 20, 72), wg, wu, gates)
     assert b.dx.shape == (3, 20, 72) and torch.equal(b.dx.view(60, 72), flat.dx)
     one = gdn.gdn_glu(x[0], wg, wu)
     assert one.shape == (80,)
     check_forward(one[None], None, x[:1], wg, wu, "silu")
-    only = gdn.gdn_glu_backward(d, x, wg, wu, gates.view(60, 160), want_d_weights=False)
+    only = gdn.gdn_glu_backward(d, x, wg, wu, gates.view(60, 2, 80), want_d_weights=False)
     assert only.d_w_gate is None and only.d_w_up is None and torch.equal(only.dx, flat.dx)
-    only = gdn.gdn_glu_backward(d, x, wg, wu, gates.view(60, 160), want_dx=False)
+    only = gdn.gdn_glu_backward(d, x, wg, wu, gates.view(60, 2, 80), want_dx=False)
     assert only.dx is None and torch.equal(only.d_w_gate, flat.d_w_gate) and torch.equal(only.d_w_up, flat.d_w_up)
 
 
@@ -246,7 +247,7 @@ def test_no_tokens():
     import gated_delta_rule_gate_gb300 as gdn
     x, wg, wu, d = draw(0, 24, 16, "f16")
     out, gates = gdn.gdn_glu(x, wg, wu, want_gates=True)
-    assert out.shape == (0, 16) and gates.shape == (0, 32)
+    assert out.shape == (0, 16) and gates.shape == (0, 2, 16)
     dw = [torch.full_like(wg, 5.0) for _ in range(2)]
     b = gdn.gdn_glu_backward(d, x, wg, wu, gates, d_w_gate=dw[0], d_w_up=dw[1])
     assert b.dx.shape == (0, 24) and not bool(dw[0].any()) and not bool(dw[1].any())
@@ -368,7 +369,7 @@ COMMON = [
     (dict(activation=5), N.GDN_ERR_INVALID, "activation"),
     (dict(x_stride=23), N.GDN_ERR_INVALID, "x_stride"),
     (dict(x=FAKE + 1), N.GDN_ERR_INVALID, "aligned"),
-    (dict(gates=FAKE + 1), N.GDN_ERR_INVALID, "aligned"),
+    (dict(gates=FAKE + 8), N.GDN_ERR_INVALID, "gates"),
     (dict(error_word=FAKE + 2), N.GDN_ERR_INVALID, "aligned"),
     (dict(w_up=None), N.GDN_ERR_INVALID, "w_up"),
 ]
@@ -418,7 +419,7 @@ def test_binding_refuses():
     from layer_standins import Standin
     h = torch.float16
     S = lambda *s, **kw: Standin(s, **{"dtype": h, **kw})
-    x, w, d, gates = S(20, 24), S(16, 24), S(20, 16), S(20, 32)
+    x, w, d, gates = S(20, 24), S(16, 24), S(20, 16), S(20, 2, 16)
     glu, back = gdn.gdn_glu, gdn.gdn_glu_backward
     for call, exc, msg in [
         (lambda: glu(x, w), TypeError, "w_up"),
@@ -440,12 +441,12 @@ def test_binding_refuses():
         (lambda: glu(S(20, 24, dtype=torch.int32), w, w), TypeError, "dtype"),
         (lambda: back(S(20, 17), x, w, w, gates), ValueError, "d_out must be"),
         (lambda: back(d, x, w, w, S(20, 16)), ValueError, "gates must be"),
-        (lambda: back(d, x, w, w, S(20, 32, dtype=torch.float32)), TypeError, "gates"),
+        (lambda: back(d, x, w, w, S(20, 2, 16, dtype=torch.float32)), TypeError, "gates"),
         (lambda: back(d, x, w, w, gates, dx=S(20, 16)), ValueError, "dx must be"),
         (lambda: back(d, x, w, w, gates, want_dx=False, dx=x), ValueError, "want_dx"),
         (lambda: back(d, x, w, w, gates, want_d_weights=False, d_w_up=w), ValueError, "want_d_weights"),
         (lambda: back(d, x, w, w, gates, d_w_gate=S(24, 16)), ValueError, "d_w_gate must be"),
-        (lambda: back(d, x, w, w, S(20, 32, device="cuda:1")), ValueError, "cuda:1"),
+        (lambda: back(d, x, w, w, S(20, 2, 16, device="cuda:1")), ValueError, "cuda:1"),
     ]:
         with pytest.raises(exc, match=msg):
             call()
