@@ -10,7 +10,9 @@
 namespace gdn {
 namespace glu {
 
-bool make_map(CUtensorMap *m, const void *base, bool bf16, int64_t stride, int64_t cols, int64_t rows, int box) {
+// A map of rows for boxes of 128 bytes x `box` rows, 128-byte swizzle.
+static bool make_map(CUtensorMap *m, const void *base, CUtensorMapDataType type, int rank, const cuuint64_t *dims,
+                     const cuuint64_t *strides, int box) {
     typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -22,12 +24,23 @@ bool make_map(CUtensorMap *m, const void *base, bool bf16, int64_t stride, int64
         return reinterpret_cast<Encode>(e == cudaSuccess && q == cudaDriverEntryPointSuccess ? ptr : nullptr);
     }();
     if (!encode) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t boxes[2] = {64, (cuuint32_t)box}, step[2] = {1, 1};
-    return encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                  const_cast<void *>(base), dims, strides, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint32_t boxes[3] = {type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 32u : 64u, (cuuint32_t)box, 1};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return encode(m, type, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, boxes, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Of 16-bit rows.
+static bool make_map(CUtensorMap *m, const void *base, bool bf16, int64_t stride, int64_t cols, int64_t rows, int box) {
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
+    return make_map(m, base, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, dims, strides,
+                    box);
+}
+// Of fp32 shares [planes, rows, cols], for boxes of 32 rows.
+static bool make_share_map(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int planes) {
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)cols * 4, (cuuint64_t)(cols * rows) * 4};
+    return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, dims, strides, 32);
 }
 
 // A thread a value: what is copied so is little beside the product that follows.
@@ -57,6 +70,7 @@ using gdn::aligned;
 using gdn::fail;
 
 constexpr int kMost = 1 << 20;
+constexpr int kMostParts = 32;
 
 int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
 // Rows that a tensor map takes: words of 16 bytes.
@@ -150,14 +164,42 @@ bool result(Result *r, const Product &p, void *at, int64_t stride, int cols, boo
     r->at = at, r->stride = stride, r->by_map = lines(at, stride);
     return !r->by_map || make_map(&r->map, at, bf16, stride, cols, p.rows, 32);
 }
-void tiles_of(Product *p, int64_t rows, int cols, int width, int results, int64_t depth) {
+void tiles_of(Product *p, int64_t rows, int cols, int width, int results, int64_t depth, int pairs, int parts) {
     p->rows = rows, p->cols = cols;
     p->tiles_m = (rows + 255) / 256, p->tiles_n = (cols + width - 1) / width;
-    p->tiles = p->tiles_m * p->tiles_n * results;
     p->blocks_k = (int)((depth + 63) / 64);
+    const int all = pairs * p->blocks_k;
+    p->per_part = (all + parts - 1) / parts;
+    p->parts = parts;
+    p->tiles = p->tiles_m * p->tiles_n * results * parts;
 }
-cudaError_t launch(const Product &p, Mode mode, bool bf16, cudaStream_t s) {
-    return bf16 ? launch_product_bf16(p, mode, s) : launch_product_f16(p, mode, s);
+// The stretches that K of a gradient's result is cut into: as many as make the
+// device's time least, in K-steps (0.27 us) a pair of blocks.  A tile costs some six steps
+// beside its own, shares are written and read in fp32 and a launch is added.
+int parts_of(int64_t rows, int cols, int results, int64_t depth, int pairs) {
+    const int64_t tiles = (rows + 255) / 256 * ((cols + 255) / 256) * results, all = (depth + 63) / 64 * pairs;
+    const int64_t device = gdn::sm_count() / 2;
+    const double values = (double)rows * padded(cols) * results;
+    int best = 1;
+    double least = 0;
+    for (int n = 1; n <= kMostParts && (n == 1 || all / n >= 8); ++n) {
+        const int64_t per = (all + n - 1) / n;
+        if ((all + per - 1) / per != n) continue;  // the last stretch would be empty
+        double t = (double)((tiles * n + device - 1) / device) * (double)(per + 6);
+        if (n > 1) t += 12 + values * n * 8 / 6.5e6 / 0.27;
+        if (n == 1 || t < least) best = n, least = t;
+    }
+    return best;
+}
+cudaError_t launch(const Product &p, Mode mode, bool bf16, const void *shares, cudaStream_t s) {
+    const cudaError_t e = bf16 ? launch_product_bf16(p, mode, s) : launch_product_f16(p, mode, s);
+    if (e != cudaSuccess || p.parts == 1) return e;
+    Join j = {};
+    j.shares = static_cast<const float *>(shares);
+    j.results = mode == kWeights ? 2 : 1;
+    j.out[0] = p.c[0].at, j.out[1] = p.c[1].at;
+    j.rows = p.rows, j.stride = p.c[0].stride, j.cols = p.cols, j.cs = (int)padded(p.cols), j.parts = p.parts;
+    return bf16 ? launch_join_bf16(j, s) : launch_join_f16(j, s);
 }
 gdn_status no_map() { return fail(GDN_ERR_CUDA, "a tensor map could not be made"); }
 
@@ -180,6 +222,8 @@ Forward plan(const gdn_glu_args *a, void *ws) {
 
 struct Backward {
     Operand x, wg, wu, dg, du;
+    int in_parts, w_parts;
+    void *shares;  // of one product after the other
     size_t bytes;
 };
 Backward plan_grad(const gdn_glu_grad_args *a, void *ws) {
@@ -194,6 +238,11 @@ Backward plan_grad(const gdn_glu_grad_args *a, void *ws) {
         b.wg = operand(a->w_gate, F, a->dim, a->dim, &pieces);
         b.wu = operand(a->w_up, F, a->dim, a->dim, &pieces);
     }
+    b.in_parts = a->dx ? parts_of(a->rows, a->dim, 1, F, 2) : 1;
+    b.w_parts = a->d_w_gate ? parts_of(F, a->dim, 2, a->rows, 1) : 1;
+    const int64_t in = b.in_parts > 1 ? a->rows * padded(a->dim) * b.in_parts : 0;
+    const int64_t w = b.w_parts > 1 ? F * padded(a->dim) * b.w_parts * 2 : 0;
+    b.shares = pieces.take(2 * (in > w ? in : w));
     b.bytes = pieces.used;
     return b;
 }
@@ -232,7 +281,7 @@ gdn_status gdn_glu(const gdn_glu_args *a, void *ws, size_t ws_bytes, gdn_stream 
         return gdn::cuda_status(bf16 ? launch_few_bf16(p, s) : launch_few_f16(p, s));
     }
     Product p = {};
-    tiles_of(&p, a->rows, a->inner, 128, 1, a->dim);
+    tiles_of(&p, a->rows, a->inner, 128, 1, a->dim, 1, 1);
     p.act = a->activation, p.gates = a->gates != nullptr, p.err = a->error_word;
     const int Fp = (int)padded(a->inner);
     if (!map_of(&p.a[0], f.x, bf16, 128) || !map_of(&p.b[0], f.wg, bf16, 128) || !map_of(&p.b[1], f.wu, bf16, 128) ||
@@ -243,7 +292,7 @@ gdn_status gdn_glu(const gdn_glu_args *a, void *ws, size_t ws_bytes, gdn_stream 
     cudaError_t e = bring(f.x, s);
     if (e == cudaSuccess) e = bring(f.wg, s);
     if (e == cudaSuccess) e = bring(f.wu, s);
-    if (e == cudaSuccess) e = launch(p, kForward, bf16, s);
+    if (e == cudaSuccess) e = launch(p, kForward, bf16, nullptr, s);
     return gdn::cuda_status(e);
 }
 
@@ -271,18 +320,20 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *a, void *ws, size_t ws_byte
     const bool bf16 = a->dtype == GDN_DTYPE_BF16;
     Product in = {}, w = {};
     if (a->dx) {
-        tiles_of(&in, T, D, 256, 1, F);
+        tiles_of(&in, T, D, 256, 1, F, 2, b.in_parts);
         in.err = a->error_word;
         if (!map_of(&in.a[0], b.dg, bf16, 128) || !map_of(&in.a[1], b.du, bf16, 128) ||
             !map_of(&in.b[0], b.wg, bf16, 64) || !map_of(&in.b[1], b.wu, bf16, 64) ||
-            !result(&in.c[0], in, a->dx, or_dense(a->dx_stride, D), D, bf16))
+            !result(&in.c[0], in, a->dx, or_dense(a->dx_stride, D), D, bf16) ||
+            (b.in_parts > 1 && !make_share_map(&in.shares, b.shares, padded(D), T, b.in_parts)))
             return no_map();
     }
     if (a->d_w_gate) {
-        tiles_of(&w, F, D, 256, 2, T);
+        tiles_of(&w, F, D, 256, 2, T, 1, b.w_parts);
         w.err = a->error_word;
         if (!map_of(&w.a[0], b.dg, bf16, 64) || !map_of(&w.a[1], b.du, bf16, 64) || !map_of(&w.b[0], b.x, bf16, 64) ||
-            !result(&w.c[0], w, a->d_w_gate, D, D, bf16) || !result(&w.c[1], w, a->d_w_up, D, D, bf16))
+            !result(&w.c[0], w, a->d_w_gate, D, D, bf16) || !result(&w.c[1], w, a->d_w_up, D, D, bf16) ||
+            (b.w_parts > 1 && !make_share_map(&w.shares, b.shares, padded(D), F, 2 * b.w_parts)))
             return no_map();
     }
     GateGrad g = {};
@@ -293,11 +344,11 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *a, void *ws, size_t ws_byte
     if (e == cudaSuccess && a->dx) {
         e = bring(b.wg, s);
         if (e == cudaSuccess) e = bring(b.wu, s);
-        if (e == cudaSuccess) e = launch(in, kInput, bf16, s);
+        if (e == cudaSuccess) e = launch(in, kInput, bf16, b.shares, s);
     }
     if (e == cudaSuccess && a->d_w_gate) {
         e = bring(b.x, s);
-        if (e == cudaSuccess) e = launch(w, kWeights, bf16, s);
+        if (e == cudaSuccess) e = launch(w, kWeights, bf16, b.shares, s);
     }
     return gdn::cuda_status(e);
 }

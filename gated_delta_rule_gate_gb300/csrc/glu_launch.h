@@ -22,9 +22,11 @@ struct Result {
 };
 struct Product {
     CUtensorMap a[2], b[2];
+    CUtensorMap shares;  // fp32 [parts x results, rows, cols], where parts > 1
     Result c[3];
     int64_t rows, tiles_m, tiles;  // tiles: of all results
     int cols, tiles_n, blocks_k;   // blocks_k: of 64, of one pair of operands
+    int parts, per_part;           // stretches of K, and their blocks
     int act, gates;
     int32_t *err;
 };
@@ -43,10 +45,15 @@ struct GateGrad {
     int F, Fp, act, words;  // Fp: elements between g and u, and between rows of dg and du; words: of d_out
 };
 
-constexpr int kFewTokens = 16;
+// The shares of `parts` stretches added up and rounded: [parts, results, rows, cs] fp32.
+struct Join {
+    const float *shares;
+    void *out[2];
+    int64_t rows, stride;
+    int cols, cs, parts, results;
+};
 
-// 2-D map of 16-bit rows for boxes of 64 columns x `box` rows, 128-byte swizzle.
-bool make_map(CUtensorMap *m, const void *base, bool bf16, int64_t stride, int64_t cols, int64_t rows, int box);
+constexpr int kFewTokens = 16;
 
 cudaError_t launch_product_f16(const Product &p, Mode mode, cudaStream_t stream);
 cudaError_t launch_product_bf16(const Product &p, Mode mode, cudaStream_t stream);
@@ -54,6 +61,8 @@ cudaError_t launch_few_f16(const Few &p, cudaStream_t stream);
 cudaError_t launch_few_bf16(const Few &p, cudaStream_t stream);
 cudaError_t launch_gate_grad_f16(const GateGrad &p, cudaStream_t stream);
 cudaError_t launch_gate_grad_bf16(const GateGrad &p, cudaStream_t stream);
+cudaError_t launch_join_f16(const Join &p, cudaStream_t stream);
+cudaError_t launch_join_bf16(const Join &p, cudaStream_t stream);
 // Rows of `cols` 16-bit values, `from` elements apart, to rows `to` elements apart.
 cudaError_t launch_spread(const void *src, void *dst, int64_t rows, int cols, int64_t from, int64_t to,
                           cudaStream_t stream);

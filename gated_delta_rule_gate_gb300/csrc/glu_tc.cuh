@@ -5,7 +5,7 @@
 // 128 of the tile's rows in its tensor memory and half of either operand in its shared
 // memory, so that a K-step of 64 takes 32 KB of each block for 16.8 MFLOP: half the
 // operand bytes of two single blocks.  Persistent; per block a warp that loads
-// (TMA, six stages), a warp whose first thread issues the products (in the pair's first
+// (TMA, five stages), a warp whose first thread issues the products (in the pair's first
 // block) and eight warps that take the finished accumulators (two of them, so that the
 // next tile's products run meanwhile) out of tensor memory.
 //
@@ -14,6 +14,9 @@
 // output meet in one thread.  kInput sums over two pairs of operands, d_g w_gate and
 // d_u w_up, in one accumulator.  kWeights takes d^T and x as they lie in memory: both
 // operands have K (the tokens) as their outer dimension.
+//
+// Where a gradient has few tiles, each is cut into stretches of K, whose sums go to
+// memory in fp32 and are added up by a kernel of their own, in one order.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -27,11 +30,11 @@
 namespace gdn {
 namespace glu {
 
-constexpr int kStages = 6, kHalf = 16384;  // bytes of a block's share of an operand's stage
+constexpr int kStages = 5, kHalf = 16384;  // bytes of a block's share of an operand's stage
 constexpr int kStageBytes = 2 * kHalf;
 constexpr int kEpilogueWarps = 8, kProductThreads = 32 * (2 + kEpilogueWarps);
 constexpr int kBox = 4096;  // 32 rows of 64 results
-constexpr int kProductSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kBox + 256;
+constexpr int kProductSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * 2 * kBox + 256;
 constexpr int kGroup = 8;  // tiles along the rows that are taken side by side
 
 struct Barriers {
@@ -41,7 +44,7 @@ struct Barriers {
 
 struct TileAt {
     int64_t m;
-    int n, z;
+    int n, z, part;  // of the results' tiles, which result, which stretch of K
 };
 // Tiles in groups of kGroup along the rows, so that those worked on at once share their
 // operands in L2.
@@ -49,8 +52,10 @@ template <Mode MODE>
 __device__ __forceinline__ TileAt tile_at(const Product &p, int64_t i) {
     TileAt t;
     const int64_t per = p.tiles_m * p.tiles_n;
-    t.z = MODE == kWeights ? (int)(i / per) : 0;
+    t.z = MODE == kForward ? 0 : (int)(i / per);
     i -= t.z * per;
+    constexpr int results = MODE == kWeights ? 2 : 1;
+    t.part = t.z / results, t.z %= results;
     const int64_t group = i / ((int64_t)kGroup * p.tiles_n), first = group * kGroup;
     const int64_t rows = p.tiles_m - first < kGroup ? p.tiles_m - first : kGroup;
     i -= first * p.tiles_n;
@@ -110,20 +115,35 @@ __device__ __forceinline__ void send(const Product &p, const Result &c, const un
     }
     __syncwarp();
 }
-// Before a box is filled anew: its store has read it.
-__device__ __forceinline__ void reuse(int lane) {
-    if (lane == 0) ptx::bulk_wait_read();
-    __syncwarp();
+// A warp's boxes, two in turn; the one that is filled next has been read by its store.
+struct Boxes {
+    unsigned char *base;
+    int turn;
+    __device__ __forceinline__ unsigned char *next(int lane) {
+        if (lane == 0) ptx::bulk_wait_read_all_but_last();
+        __syncwarp();
+        return base + (turn ^= 1) * kBox;
+    }
+};
+
+// 32 fp32 columns of a lane's row: a share of a result that is summed over stretches of K.
+__device__ __forceinline__ void put_share(unsigned char *box, int lane, const float (&v)[32]) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<float4 *>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+            make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
 }
 
 // The accumulator's columns of one of two groups of warps, `half`.
 template <Mode MODE, typename T>
-__device__ __forceinline__ void take(const Product &p, const TileAt &t, uint32_t acc, int64_t row, unsigned char *box,
+__device__ __forceinline__ void take(const Product &p, const TileAt &t, uint32_t acc, int64_t row, Boxes &boxes,
                                      int half, int lane) {
     float v[32];
+    unsigned char *box;
     if (MODE == kForward) {
         const int col = t.n * 128 + 64 * half;
         if (col >= p.cols) return;
+        box = boxes.next(lane);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             float u[32];
@@ -131,29 +151,42 @@ __device__ __forceinline__ void take(const Product &p, const TileAt &t, uint32_t
             tc::ld32(acc + 128 + 64 * half + 32 * q, u);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = activation(v[i], p.act) * u[i];
-            if (q == 0) reuse(lane);
             put_half<T>(box, lane, q, v);
         }
         send(p, p.c[0], box, row, col, lane);
         if (!p.gates) return;
 #pragma unroll 1
         for (int k = 0; k < 2; ++k) {
+            box = boxes.next(lane);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 tc::ld32(acc + 128 * k + 64 * half + 32 * q, v);
-                if (q == 0) reuse(lane);
                 put_half<T>(box, lane, q, v);
             }
             send(p, p.c[1 + k], box, row, col, lane);
+        }
+    } else if (p.parts > 1) {
+        for (int h = 0; h < 4; ++h) {
+            const int col = t.n * 256 + 128 * half + 32 * h;
+            if (col >= p.cols) return;
+            box = boxes.next(lane);
+            tc::ld32(acc + 128 * half + 32 * h, v);
+            put_share(box, lane, v);
+            ptx::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                ptx::tma_store_3d(&p.shares, col, (int)row, t.part * (MODE == kWeights ? 2 : 1) + t.z, box);
+                ptx::bulk_commit();
+            }
         }
     } else {
         for (int h = 2 * half; h < 2 * half + 2; ++h) {
             const int col = t.n * 256 + 64 * h;
             if (col >= p.cols) return;
+            box = boxes.next(lane);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 tc::ld32(acc + 64 * h + 32 * q, v);
-                if (q == 0) reuse(lane);
                 put_half<T>(box, lane, q, v);
             }
             send(p, p.c[t.z], box, row, col, lane);
@@ -169,7 +202,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     constexpr int PAIRS = MODE == kInput ? 2 : 1;  // of operands that one result sums over
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     unsigned char *boxes = sm + kStages * kStageBytes;
-    Barriers &bar = *reinterpret_cast<Barriers *>(boxes + kEpilogueWarps * kBox);
+    Barriers &bar = *reinterpret_cast<Barriers *>(boxes + kEpilogueWarps * 2 * kBox);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -193,7 +226,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     ptx::grid_wait();
 
     const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
-    const int blocks = PAIRS * p.blocks_k;
+    // K-steps of a tile: those of its stretch
+    auto begin_of = [&](const TileAt &t) { return t.part * p.per_part; };
+    auto end_of = [&](const TileAt &t) {
+        const int e = (t.part + 1) * p.per_part, all = PAIRS * p.blocks_k;
+        return e < all ? e : all;
+    };
     bool ok = true;
     if (warp == 0) {
         if (lane == 0) {
@@ -204,7 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                 const TileAt t = tile_at<MODE>(p, i);
                 const int m = (int)(t.m * 256) + 128 * (int)rank;
                 const int n = MODE == kForward ? t.n * 128 : t.n * 256 + 128 * (int)rank;
-                for (int kb = 0; kb < blocks; ++kb) {
+                for (int kb = begin_of(t), e = end_of(t); kb < e; ++kb) {
                     if (!ptx::mbar_wait_sleep(&bar.empty[s], ph ^ 1)) {
                         ok = false;
                         break;
@@ -253,7 +291,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                     break;
                 }
                 tc::fence_after();
-                for (int kb = 0; kb < blocks; ++kb) {
+                const TileAt t = tile_at<MODE>(p, i);
+                const int b0 = begin_of(t), e = end_of(t);
+                for (int kb = b0; kb < e; ++kb) {
                     if (!ptx::mbar_wait(&bar.full[s], ph, 1u << 22)) {
                         ok = false;
                         break;
@@ -262,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         tc::mma_f16_pair(tmem + a * 256, tc::desc_adv(da, s * kStageBytes + k * sa),
-                                         tc::desc_adv(db, s * kStageBytes + k * sb), id, kb + k > 0);
+                                         tc::desc_adv(db, s * kStageBytes + k * sb), id, kb > b0 || k > 0);
                     tc::commit_pair(&bar.empty[s]);
                     if (++s == kStages) s = 0, ph ^= 1;
                 }
@@ -271,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         }
     } else {
         const int quarter = warp & 3;  // of the tensor memory's lanes, by the warp's number
-        unsigned char *box = boxes + (warp - 2) * kBox;
+        Boxes mine = {boxes + (warp - 2) * 2 * kBox, 0};
         uint32_t turn = 0;
         const uint32_t taken[2] = {ptx::cluster_address(&bar.taken[0], 0), ptx::cluster_address(&bar.taken[1], 0)};
         for (int64_t i = first; i < p.tiles; i += step, ++turn) {
@@ -282,7 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             tc::fence_after();
             const int64_t row = t.m * 256 + 128 * rank + 32 * quarter;
             if (row < p.rows)
-                take<MODE, T>(p, t, tmem + a * 256 + ((uint32_t)(32 * quarter) << 16), row, box,
+                take<MODE, T>(p, t, tmem + a * 256 + ((uint32_t)(32 * quarter) << 16), row, mine,
                               (warp - 2) >> 2, lane);
             tc::fence_before();
             __syncwarp();

@@ -414,6 +414,13 @@ __device__ __forceinline__ void tma_store_2d(const void *tmap, int c0, int c1, c
                  "r"(c0), "r"(c1), "r"(smem_u32(src))
                  : "memory");
 }
+// The same of a 3-D box.
+__device__ __forceinline__ void tma_store_3d(const void *tmap, int c0, int c1, int c2, const void *src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(tmap)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
+                 : "memory");
+}
 // Shared memory written by this thread's generic stores, and by those it has
 // synchronised with, is seen by the asynchronous copies that follow.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }

@@ -108,7 +108,7 @@ def check_backward(got, want, dt):
 # rows, dim, inner: few tokens and many, one tile and several, whole words and odd widths
 SHAPES = [(1, 64, 8), (1, 1, 1), (1, 2048, 96), (3, 517, 1001), (8, 96, 40), (9, 40, 24), (16, 200, 130), (16, 2051, 17),
           (17, 64, 128), (17, 65, 1), (100, 1, 3), (129, 72, 136), (256, 64, 128), (257, 520, 264), (300, 1000, 700),
-          (1001, 517, 1531), (513, 128, 8), (40, 8, 520), (2049, 192, 1288)]
+          (1001, 517, 1531), (513, 128, 8), (40, 8, 520), (2049, 192, 1288), (700, 12, 600), (90, 20, 4000)]
 
 
 @pytest.mark.gpu
