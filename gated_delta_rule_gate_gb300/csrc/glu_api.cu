@@ -89,6 +89,9 @@ gdn_status check_sizes(int64_t rows, int dim, int inner, int dtype, int act) {
     if (dim > kMost || inner > kMost) return fail(GDN_ERR_UNSUPPORTED, "dim and inner above %d are not supported", kMost);
     if (dtype == GDN_DTYPE_F32) return fail(GDN_ERR_UNSUPPORTED, "dtype: the products take 16-bit operands, not float32");
     if (dtype != GDN_DTYPE_F16 && dtype != GDN_DTYPE_BF16) return fail(GDN_ERR_INVALID, "unknown dtype %d", dtype);
+    // tiles of 256 x 128 results are counted in 32 bits, with up to 2 kMostParts of each
+    if (((rows + 255) / 256) * ((inner + 127) / 128) >= 1LL << 25 || ((rows + 255) / 256) * ((dim + 127) / 128) >= 1LL << 25)
+        return fail(GDN_ERR_UNSUPPORTED, "rows x inner or rows x dim is beyond 2^40");
     if (act < GDN_ACT_SILU || act > GDN_ACT_SIGMOID) return fail(GDN_ERR_INVALID, "unknown activation %d", act);
     return GDN_OK;
 }
@@ -166,12 +169,12 @@ bool result(Result *r, const Product &p, void *at, int64_t stride, int cols, boo
 }
 void tiles_of(Product *p, int64_t rows, int cols, int width, int results, int64_t depth, int pairs, int parts) {
     p->rows = rows, p->cols = cols;
-    p->tiles_m = (rows + 255) / 256, p->tiles_n = (cols + width - 1) / width;
+    p->tiles_m = (int)((rows + 255) / 256), p->tiles_n = (cols + width - 1) / width;
     p->blocks_k = (int)((depth + 63) / 64);
     const int all = pairs * p->blocks_k;
     p->per_part = (all + parts - 1) / parts;
     p->parts = parts;
-    p->tiles = p->tiles_m * p->tiles_n * results * parts;
+    p->tiles = (uint32_t)p->tiles_m * (uint32_t)p->tiles_n * (uint32_t)(results * parts);
 }
 // The stretches that K of a gradient's result is cut into: as many as make the
 // device's time least, in K-steps (0.27 us) a pair of blocks.  A tile costs some six steps

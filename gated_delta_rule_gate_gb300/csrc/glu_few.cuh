@@ -96,7 +96,10 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const __grid_consta
         float gate = 0.f, up = 0.f;
 #pragma unroll
         for (int w = 0; w < kFewWarps; ++w) gate += sums[w][n][e][c], up += sums[w][n][8 + e][c];
-        if (at < p.F) static_cast<T *>(p.out)[tok * p.os + at] = static_cast<T>(activation(gate, p.act) * up);
+        if (at < p.F)
+            with_activation(p.act, [&](auto act) {
+                static_cast<T *>(p.out)[tok * p.os + at] = static_cast<T>(activation<act>(gate) * up);
+            });
         if (p.gates) {
             T *row = static_cast<T *>(p.gates) + (int64_t)tok * 2 * p.Fp + at;
             row[0] = static_cast<T>(at < p.F ? gate : 0.f);
@@ -141,12 +144,14 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const __grid_constant__ 
 #pragma unroll
             for (int e = 0; e < 8; ++e) d[e] = c + e < p.F ? static_cast<float>(at[e]) : 0.f;
         }
+        with_activation(p.act, [&](auto act) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float2 a = activation_slope(g[e], p.act);
-            dg[e] = d[e] * u[e] * a.y;
-            du[e] = d[e] * a.x;
-        }
+            for (int e = 0; e < 8; ++e) {
+                const float2 a = activation_slope<act>(g[e]);
+                dg[e] = d[e] * u[e] * a.y;
+                du[e] = d[e] * a.x;
+            }
+        });
         store_values<T, 8>(static_cast<T *>(p.dg) + row * p.Fp + c, dg);
         store_values<T, 8>(static_cast<T *>(p.du) + row * p.Fp + c, du);
     }

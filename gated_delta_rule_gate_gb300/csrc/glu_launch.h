@@ -24,9 +24,10 @@ struct Product {
     CUtensorMap a[2], b[2];
     CUtensorMap shares;  // fp32 [parts x results, rows, cols], where parts > 1
     Result c[3];
-    int64_t rows, tiles_m, tiles;  // tiles: of all results
-    int cols, tiles_n, blocks_k;   // blocks_k: of 64, of one pair of operands
-    int parts, per_part;           // stretches of K, and their blocks
+    int64_t rows;
+    uint32_t tiles;                  // of all results and stretches
+    int cols, tiles_m, tiles_n;
+    int blocks_k, parts, per_part;   // K-steps of one pair of operands; stretches of K, and theirs
     int act, gates;
     int32_t *err;
 };

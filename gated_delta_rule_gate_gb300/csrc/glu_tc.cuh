@@ -43,24 +43,27 @@ struct Barriers {
 };
 
 struct TileAt {
-    int64_t m;
-    int n, z, part;  // of the results' tiles, which result, which stretch of K
+    int m, n, z, part;  // of the results' tiles, which result, which stretch of K
 };
 // Tiles in groups of kGroup along the rows, so that those worked on at once share their
-// operands in L2.
+// operands in L2.  (In 32 bits: with 64-bit divisions the place of a tile took longer than
+// its results.)
 template <Mode MODE>
-__device__ __forceinline__ TileAt tile_at(const Product &p, int64_t i) {
+__device__ __forceinline__ TileAt tile_at(const Product &p, uint32_t i) {
     TileAt t;
-    const int64_t per = p.tiles_m * p.tiles_n;
-    t.z = MODE == kForward ? 0 : (int)(i / per);
-    i -= t.z * per;
-    constexpr int results = MODE == kWeights ? 2 : 1;
-    t.part = t.z / results, t.z %= results;
-    const int64_t group = i / ((int64_t)kGroup * p.tiles_n), first = group * kGroup;
-    const int64_t rows = p.tiles_m - first < kGroup ? p.tiles_m - first : kGroup;
-    i -= first * p.tiles_n;
-    t.m = first + i % rows;
+    const uint32_t wide = (uint32_t)p.tiles_n, tall = (uint32_t)p.tiles_m, per = wide * tall;
+    constexpr uint32_t results = MODE == kWeights ? 2 : 1;
+    t.z = t.part = 0;
+    if (MODE != kForward) {
+        const uint32_t plane = i / per;
+        i -= plane * per;
+        t.part = (int)(plane / results), t.z = (int)(plane % results);
+    }
+    const uint32_t group = i / (kGroup * wide), first = group * kGroup;
+    const uint32_t rows = tall - first < kGroup ? tall - first : kGroup;
+    i -= first * wide;
     t.n = (int)(i / rows);
+    t.m = (int)(first + (i - (uint32_t)t.n * rows));
     return t;
 }
 
@@ -77,14 +80,23 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Half of a lane's row of 64 results, 16-byte pieces where the 128-byte swizzle has them.
+// 32 results of a lane's row, rounded, and their place in its row of 64 of a box: 16-byte
+// pieces where the 128-byte swizzle has them.
+struct Packed {
+    uint32_t w[16];
+};
 template <typename T>
-__device__ __forceinline__ void put_half(unsigned char *box, int lane, int half, const float (&v)[32]) {
+__device__ __forceinline__ Packed pack(const uint32_t (&r)[32]) {
+    Packed p;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const uint4 w = make_uint4(pack2<T>(v[8 * c], v[8 * c + 1]), pack2<T>(v[8 * c + 2], v[8 * c + 3]),
-                                   pack2<T>(v[8 * c + 4], v[8 * c + 5]), pack2<T>(v[8 * c + 6], v[8 * c + 7]));
-        *reinterpret_cast<uint4 *>(box + lane * 128 + (((4 * half + c) ^ (lane & 7)) << 4)) = w;
+    for (int i = 0; i < 16; ++i) p.w[i] = pack2<T>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+    return p;
+}
+__device__ __forceinline__ void put(unsigned char *box, int lane, const Packed (&p)[2]) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const uint32_t *w = p[c >> 2].w + 4 * (c & 3);
+        *reinterpret_cast<uint4 *>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -127,69 +139,85 @@ struct Boxes {
 };
 
 // 32 fp32 columns of a lane's row: a share of a result that is summed over stretches of K.
-__device__ __forceinline__ void put_share(unsigned char *box, int lane, const float (&v)[32]) {
+__device__ __forceinline__ void put_share(unsigned char *box, int lane, const uint32_t (&r)[32]) {
 #pragma unroll
     for (int c = 0; c < 8; ++c)
-        *reinterpret_cast<float4 *>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-            make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        *reinterpret_cast<uint4 *>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+            make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
 }
 
-// The accumulator's columns of one of two groups of warps, `half`.
+// An accumulator's 128 columns of one of two groups of warps, `half`: taken into registers,
+// after which it is free for the next tile but one, and sent to their results.
 template <Mode MODE, typename T>
-__device__ __forceinline__ void take(const Product &p, const TileAt &t, uint32_t acc, int64_t row, Boxes &boxes,
-                                     int half, int lane) {
-    float v[32];
-    unsigned char *box;
-    if (MODE == kForward) {
+__device__ __forceinline__ void take(const Product &p, const TileAt &t, uint32_t acc, uint32_t taken, int64_t row,
+                                     Boxes &boxes, int half, int lane) {
+    auto release = [&] {
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(taken);
+    };
+    if constexpr (MODE == kForward) {  // 64 columns of the gate and the same 64 of up
         const int col = t.n * 128 + 64 * half;
-        if (col >= p.cols) return;
-        box = boxes.next(lane);
+        const bool kept = row < p.rows && col < p.cols;
+        Packed out[2], gate[2], up[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            float u[32];
-            tc::ld32(acc + 64 * half + 32 * q, v);
-            tc::ld32(acc + 128 + 64 * half + 32 * q, u);
+            uint32_t r[2][32];
+            tc::ld32_begin(acc + 64 * half + 32 * q, r[0]);
+            tc::ld32_begin(acc + 128 + 64 * half + 32 * q, r[1]);
+            tc::wait_ld(r);
+            if (q == 1) release();
+            if (p.gates) gate[q] = pack<T>(r[0]), up[q] = pack<T>(r[1]);
+            with_activation(p.act, [&](auto act) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = activation(v[i], p.act) * u[i];
-            put_half<T>(box, lane, q, v);
+                for (int i = 0; i < 16; ++i)
+                    out[q].w[i] = pack2<T>(
+                        activation<act>(__uint_as_float(r[0][2 * i])) * __uint_as_float(r[1][2 * i]),
+                        activation<act>(__uint_as_float(r[0][2 * i + 1])) * __uint_as_float(r[1][2 * i + 1]));
+            });
         }
+        if (!kept) return;
+        unsigned char *box = boxes.next(lane);
+        put(box, lane, out);
         send(p, p.c[0], box, row, col, lane);
-        if (!p.gates) return;
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
+        if (p.gates) {
             box = boxes.next(lane);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                tc::ld32(acc + 128 * k + 64 * half + 32 * q, v);
-                put_half<T>(box, lane, q, v);
-            }
-            send(p, p.c[1 + k], box, row, col, lane);
-        }
-    } else if (p.parts > 1) {
-        for (int h = 0; h < 4; ++h) {
-            const int col = t.n * 256 + 128 * half + 32 * h;
-            if (col >= p.cols) return;
+            put(box, lane, gate);
+            send(p, p.c[1], box, row, col, lane);
             box = boxes.next(lane);
-            tc::ld32(acc + 128 * half + 32 * h, v);
-            put_share(box, lane, v);
-            ptx::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                ptx::tma_store_3d(&p.shares, col, (int)row, t.part * (MODE == kWeights ? 2 : 1) + t.z, box);
-                ptx::bulk_commit();
-            }
+            put(box, lane, up);
+            send(p, p.c[2], box, row, col, lane);
         }
     } else {
-        for (int h = 2 * half; h < 2 * half + 2; ++h) {
-            const int col = t.n * 256 + 64 * h;
-            if (col >= p.cols) return;
-            box = boxes.next(lane);
+        const int col = t.n * 256 + 128 * half;
+        uint32_t r[4][32];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                tc::ld32(acc + 64 * h + 32 * q, v);
-                put_half<T>(box, lane, q, v);
+        for (int k = 0; k < 4; ++k) tc::ld32_begin(acc + 128 * half + 32 * k, r[k]);
+        tc::wait_ld(r);
+        release();
+        if (row >= p.rows) return;
+        if (p.parts > 1) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                if (col + 32 * h >= p.cols) return;
+                unsigned char *box = boxes.next(lane);
+                put_share(box, lane, r[h]);
+                ptx::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::tma_store_3d(&p.shares, col + 32 * h, (int)row, t.part * (MODE == kWeights ? 2 : 1) + t.z, box);
+                    ptx::bulk_commit();
+                }
             }
-            send(p, p.c[t.z], box, row, col, lane);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (col + 64 * h >= p.cols) return;
+                const Packed v[2] = {pack<T>(r[2 * h]), pack<T>(r[2 * h + 1])};
+                unsigned char *box = boxes.next(lane);
+                put(box, lane, v);
+                send(p, p.c[t.z], box, row, col + 64 * h, lane);
+            }
         }
     }
 }
@@ -225,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     const uint32_t tmem = bar.tmem;
     ptx::grid_wait();
 
-    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const uint32_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
     // K-steps of a tile: those of its stretch
     auto begin_of = [&](const TileAt &t) { return t.part * p.per_part; };
     auto end_of = [&](const TileAt &t) {
@@ -238,9 +266,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             int s = 0;
             uint32_t ph = 0;
             int64_t filled = 0;
-            for (int64_t i = first; ok && i < p.tiles; i += step) {
+            for (uint32_t i = first; ok && i < p.tiles; i += step) {
                 const TileAt t = tile_at<MODE>(p, i);
-                const int m = (int)(t.m * 256) + 128 * (int)rank;
+                const int m = t.m * 256 + 128 * (int)rank;
                 const int n = MODE == kForward ? t.n * 128 : t.n * 256 + 128 * (int)rank;
                 for (int kb = begin_of(t), e = end_of(t); kb < e; ++kb) {
                     if (!ptx::mbar_wait_sleep(&bar.empty[s], ph ^ 1)) {
@@ -284,7 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             const uint64_t db = tc::desc_sw128(ptx::smem_u32(sm) + kHalf, B_MN ? kHalf / 2 : 16);
             int s = 0;
             uint32_t ph = 0, turn = 0;
-            for (int64_t i = first; ok && i < p.tiles; i += step, ++turn) {
+            for (uint32_t i = first; ok && i < p.tiles; i += step, ++turn) {
                 const uint32_t a = turn & 1;
                 if (!ptx::mbar_wait(&bar.taken[a], ((turn >> 1) & 1) ^ 1, 1u << 22)) {
                     ok = false;
@@ -314,19 +342,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         Boxes mine = {boxes + (warp - 2) * 2 * kBox, 0};
         uint32_t turn = 0;
         const uint32_t taken[2] = {ptx::cluster_address(&bar.taken[0], 0), ptx::cluster_address(&bar.taken[1], 0)};
-        for (int64_t i = first; i < p.tiles; i += step, ++turn) {
+        for (uint32_t i = first; i < p.tiles; i += step, ++turn) {
             const TileAt t = tile_at<MODE>(p, i);
             const uint32_t a = turn & 1;
             ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&bar.done[a], (turn >> 1) & 1));
             if (!ok) break;
             tc::fence_after();
-            const int64_t row = t.m * 256 + 128 * rank + 32 * quarter;
-            if (row < p.rows)
-                take<MODE, T>(p, t, tmem + a * 256 + ((uint32_t)(32 * quarter) << 16), row, mine,
-                              (warp - 2) >> 2, lane);
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(taken[a]);
+            const int64_t row = (int64_t)t.m * 256 + 128 * rank + 32 * quarter;
+            take<MODE, T>(p, t, tmem + a * 256 + ((uint32_t)(32 * quarter) << 16), taken[a], row, mine, (warp - 2) >> 2,
+                          lane);
         }
         if (lane == 0) ptx::bulk_wait_read();
     }
