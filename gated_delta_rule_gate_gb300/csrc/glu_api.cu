@@ -2,6 +2,8 @@
 // the operands' tensor maps, and copies of operands whose rows are no words of 16 bytes.
 #include <cuda.h>
 
+#include <initializer_list>
+
 #include "glu_launch.h"
 #include "launch.h"
 #include "ptx.cuh"
@@ -43,21 +45,36 @@ static bool make_share_map(CUtensorMap *m, const void *base, int64_t cols, int64
     return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, dims, strides, 32);
 }
 
-// A thread a value: what is copied so is little beside the product that follows.
-__global__ void __launch_bounds__(256) spread_kernel(const uint16_t *src, uint16_t *dst, int64_t n, int cols,
-                                                     int64_t from, int64_t to) {
+// Rows of `cols` 16-bit values, `from` elements apart, to rows `to` (a multiple of 8)
+// elements apart at a 16-byte address; up to three operands a launch.
+struct Copies {
+    const uint16_t *src[3];
+    uint16_t *dst[3];
+    int64_t rows[3], from[3];
+    int cols, to, count;
+};
+// 8 values a thread: read one by one (neighbours share their lines), written as a word.
+__global__ void __launch_bounds__(256) spread_kernel(const __grid_constant__ Copies c) {
     ptx::grid_wait();
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / cols;
-        const int c = (int)(i - row * cols);
-        dst[row * to + c] = src[row * from + c];
+    const int per = c.to / 8;
+    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int64_t n = k < c.count ? c.rows[k] * per : 0;
+        for (; i < n; i += (int64_t)gridDim.x * 256) {
+            const int64_t row = i / per;
+            const int at = (int)(i - row * per) * 8;
+            const uint16_t *src = c.src[k] + row * c.from[k] + at;
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t lo = at + 2 * e < c.cols ? src[2 * e] : 0, hi = at + 2 * e + 1 < c.cols ? src[2 * e + 1] : 0;
+                w[e] = lo | hi << 16;
+            }
+            *reinterpret_cast<uint4 *>(c.dst[k] + row * c.to + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        i -= n;
     }
-}
-cudaError_t launch_spread(const void *src, void *dst, int64_t rows, int cols, int64_t from, int64_t to,
-                          cudaStream_t stream) {
-    const int64_t n = rows * cols, blocks = (n + 255) / 256, most = (int64_t)sm_count() * 16;
-    return launch_early(spread_kernel, (unsigned)(blocks < most ? blocks : most), 256, 0, stream,
-                        static_cast<const uint16_t *>(src), static_cast<uint16_t *>(dst), n, cols, from, to);
 }
 
 }  // namespace glu
@@ -155,9 +172,22 @@ Operand operand(const void *p, int64_t rows, int64_t cols, int64_t stride, Piece
     o.at = ws->take(rows * o.stride);
     return o;
 }
-cudaError_t bring(const Operand &o, cudaStream_t s) {
-    if (!o.from) return cudaSuccess;
-    return launch_spread(o.from, const_cast<void *>(o.at), o.rows, (int)o.cols, o.from_stride, o.stride, s);
+// Those of up to three operands of one width that are copies are made.
+cudaError_t bring(std::initializer_list<const Operand *> operands, cudaStream_t s) {
+    Copies c = {};
+    int64_t n = 0;
+    for (const Operand *o : operands) {
+        if (!o->from) continue;
+        const int k = c.count++;
+        c.src[k] = static_cast<const uint16_t *>(o->from);
+        c.dst[k] = static_cast<uint16_t *>(const_cast<void *>(o->at));
+        c.rows[k] = o->rows, c.from[k] = o->from_stride;
+        c.cols = (int)o->cols, c.to = (int)o->stride;
+        n += o->rows * (o->stride / 8);
+    }
+    if (c.count == 0) return cudaSuccess;
+    const int64_t blocks = (n + 255) / 256, most = (int64_t)gdn::sm_count() * 16;
+    return gdn::launch_early(spread_kernel, (unsigned)(blocks < most ? blocks : most), 256, 0, s, c);
 }
 bool map_of(CUtensorMap *m, const Operand &o, bool bf16, int box) {
     return make_map(m, o.at, bf16, o.stride, o.cols, o.rows, box);
@@ -292,9 +322,7 @@ gdn_status gdn_glu(const gdn_glu_args *a, void *ws, size_t ws_bytes, gdn_stream 
         return no_map();
     for (int i = 0; a->gates && i < 2; ++i)
         if (!result(&p.c[1 + i], p, static_cast<uint16_t *>(a->gates) + i * Fp, 2 * (int64_t)Fp, Fp, bf16)) return no_map();
-    cudaError_t e = bring(f.x, s);
-    if (e == cudaSuccess) e = bring(f.wg, s);
-    if (e == cudaSuccess) e = bring(f.wu, s);
+    cudaError_t e = bring({&f.x, &f.wg, &f.wu}, s);
     if (e == cudaSuccess) e = launch(p, kForward, bf16, nullptr, s);
     return gdn::cuda_status(e);
 }
@@ -344,15 +372,9 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *a, void *ws, size_t ws_byte
     g.rows = T, g.dos = or_dense(a->d_out_stride, F), g.F = F, g.Fp = (int)padded(F), g.act = a->activation;
     g.words = F % 8 == 0 && lines(a->d_out, g.dos);
     e = bf16 ? launch_gate_grad_bf16(g, s) : launch_gate_grad_f16(g, s);
-    if (e == cudaSuccess && a->dx) {
-        e = bring(b.wg, s);
-        if (e == cudaSuccess) e = bring(b.wu, s);
-        if (e == cudaSuccess) e = launch(in, kInput, bf16, b.shares, s);
-    }
-    if (e == cudaSuccess && a->d_w_gate) {
-        e = bring(b.x, s);
-        if (e == cudaSuccess) e = launch(w, kWeights, bf16, b.shares, s);
-    }
+    if (e == cudaSuccess) e = bring({&b.x, &b.wg, &b.wu}, s);
+    if (e == cudaSuccess && a->dx) e = launch(in, kInput, bf16, b.shares, s);
+    if (e == cudaSuccess && a->d_w_gate) e = launch(w, kWeights, bf16, b.shares, s);
     return gdn::cuda_status(e);
 }
 

@@ -1,12 +1,20 @@
 // glu_few.cuh -- the gated feed-forward of few tokens, and the element-wise part of
 // its gradient.
 //
-// Few tokens: bound by the weights' way from HBM.  A block has 8 output features, whose
-// 8 rows of w_gate and 8 of w_up are the 16 rows of a warp-level product (m16n8k16), so
-// that a thread's accumulators hold gate and up of the same outputs.  The order of k
-// within a product is free: a lane takes 8 adjacent values (16 bytes) of its two weight
-// rows and of its token, which are its operands of two products over 32 k's.  The 8
-// warps share the k's out and add their sums up at the end, in one order.
+// Few tokens: bound by the weights' way from HBM.  A warp-level product (m16n8k16) has 8
+// rows of w_gate and the same 8 of w_up as its 16 rows, so that a thread's accumulators
+// hold gate and up of the same outputs.  The order of k within a product is free: a lane
+// takes 8 adjacent values (16 bytes) of its two weight rows and of its token, which are its
+// operands of two products over 32 k's.  The block's warps share the k's out and add their
+// sums up at the end, in one order.
+//
+// What counts is bytes on their way: 16 words of 16 bytes a lane, 16 warps an SM, as 16
+// features a block and 4 words of each of their rows.  Where that makes less than a block
+// an SM (up to 2432 features), 8 features and 8 words.  1 token x 4096, in us:
+// features              1536    4864    8192
+// 16 features, 4 words   8.7    14.1    22.1
+//  8 features, 8 words   6.6    14.8    24.8
+//  8 features, 4 words  10.8    15.5    25.8
 #pragma once
 
 #include <cuda_bf16.h>
@@ -21,8 +29,7 @@
 namespace gdn {
 namespace glu {
 
-constexpr int kFewWarps = 8, kFeatures = 8;
-constexpr int kAhead = 4;  // loads of a weight row in flight per lane
+constexpr int kFewWarps = 8;
 
 template <typename T>
 __device__ __forceinline__ void product16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -45,57 +52,71 @@ __device__ __forceinline__ uint4 load8(const uint16_t *row, int k, int D) {
     }
 }
 
-// NT: groups of 8 tokens.
-template <typename T, int NT, bool WORDS>
-__global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const __grid_constant__ Few p) {
-    __shared__ float sums[kFewWarps][NT][16][9];
+// NT: groups of 8 tokens; MT: of 8 features.
+template <typename T, int NT, int MT, bool WORDS>
+__global__ void __launch_bounds__(32 * kFewWarps, 2) few_kernel(const __grid_constant__ Few p) {
+    constexpr int kAhead = 8 / MT;  // words of a weight row on their way to a lane
+    __shared__ float sums[kFewWarps][NT][MT][16][9];
     ptx::grid_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int f = blockIdx.x * kFeatures + g;
-    const int fr = f < p.F ? f : p.F - 1;  // rows beyond the last are not kept
-    const uint16_t *wg = static_cast<const uint16_t *>(p.wg) + (int64_t)fr * p.D;
-    const uint16_t *wu = static_cast<const uint16_t *>(p.wu) + (int64_t)fr * p.D;
-    const uint16_t *x[NT];
+    const uint16_t *wg[MT], *wu[MT], *x[NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int f = (blockIdx.x * MT + m) * 8 + g, row = f < p.F ? f : p.F - 1;  // those beyond the last are not kept
+        wg[m] = static_cast<const uint16_t *>(p.wg) + (int64_t)row * p.D;
+        wu[m] = static_cast<const uint16_t *>(p.wu) + (int64_t)row * p.D;
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int tok = 8 * n + g;
         x[n] = tok < p.T ? static_cast<const uint16_t *>(p.x) + tok * p.xs : nullptr;
     }
-    float acc[NT][4] = {};
+    float acc[NT][MT][4] = {};
     // a warp's steps of 32 k's: kAhead adjacent ones at a time
     const int steps = (p.D + 31) / 32;
     for (int s0 = warp * kAhead; s0 < steps; s0 += kFewWarps * kAhead) {
-        uint4 a[kAhead], b[kAhead];
+        uint4 a[MT][kAhead], b[MT][kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int k = (s0 + i) * 32 + 8 * t;
-            a[i] = load8<WORDS>(wg, k, p.D);
-            b[i] = load8<WORDS>(wu, k, p.D);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                a[m][i] = load8<WORDS>(wg[m], k, p.D);
+                b[m][i] = load8<WORDS>(wu[m], k, p.D);
+            }
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int k = (s0 + i) * 32 + 8 * t;
-            const uint32_t first[4] = {a[i].x, b[i].x, a[i].y, b[i].y}, second[4] = {a[i].z, b[i].z, a[i].w, b[i].w};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const uint4 v = x[n] ? load8<WORDS>(x[n], k, p.D) : make_uint4(0, 0, 0, 0);
-                product16<T>(acc[n], first, v.x, v.y);
-                product16<T>(acc[n], second, v.z, v.w);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const uint32_t first[4] = {a[m][i].x, b[m][i].x, a[m][i].y, b[m][i].y};
+                    const uint32_t second[4] = {a[m][i].z, b[m][i].z, a[m][i].w, b[m][i].w};
+                    product16<T>(acc[n][m], first, v.x, v.y);
+                    product16<T>(acc[n][m], second, v.z, v.w);
+                }
             }
         }
     }
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        sums[warp][n][g][2 * t] = acc[n][0], sums[warp][n][g][2 * t + 1] = acc[n][1];
-        sums[warp][n][8 + g][2 * t] = acc[n][2], sums[warp][n][8 + g][2 * t + 1] = acc[n][3];
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            float(&to)[16][9] = sums[warp][n][m];
+            to[g][2 * t] = acc[n][m][0], to[g][2 * t + 1] = acc[n][m][1];
+            to[8 + g][2 * t] = acc[n][m][2], to[8 + g][2 * t + 1] = acc[n][m][3];
+        }
     __syncthreads();
-    for (int i = threadIdx.x; i < 64 * NT; i += 32 * kFewWarps) {
-        const int e = i & 7, tok = i >> 3, n = tok >> 3, c = tok & 7, at = blockIdx.x * kFeatures + e;
+    for (int i = threadIdx.x; i < 64 * NT * MT; i += 32 * kFewWarps) {
+        const int e = i % (8 * MT), tok = i / (8 * MT), n = tok >> 3, c = tok & 7, at = blockIdx.x * (8 * MT) + e;
         if (tok >= p.T || at >= p.Fp) continue;
         float gate = 0.f, up = 0.f;
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) gate += sums[w][n][e][c], up += sums[w][n][8 + e][c];
+        for (int w = 0; w < kFewWarps; ++w)
+            gate += sums[w][n][e >> 3][e & 7][c], up += sums[w][n][e >> 3][8 + (e & 7)][c];
         if (at < p.F)
             with_activation(p.act, [&](auto act) {
                 static_cast<T *>(p.out)[tok * p.os + at] = static_cast<T>(activation<act>(gate) * up);
@@ -108,16 +129,18 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const __grid_consta
     }
 }
 
-template <typename T, int NT>
+template <typename T, int NT, int MT>
 cudaError_t launch_few_of(const Few &p, cudaStream_t stream) {
-    const unsigned blocks = (unsigned)((p.F + kFeatures - 1) / kFeatures);
-    return p.words ? launch_early(few_kernel<T, NT, true>, blocks, 32 * kFewWarps, 0, stream, p)
-                   : launch_early(few_kernel<T, NT, false>, blocks, 32 * kFewWarps, 0, stream, p);
+    const unsigned blocks = (unsigned)((p.F + 8 * MT - 1) / (8 * MT));
+    return p.words ? launch_early(few_kernel<T, NT, MT, true>, blocks, 32 * kFewWarps, 0, stream, p)
+                   : launch_early(few_kernel<T, NT, MT, false>, blocks, 32 * kFewWarps, 0, stream, p);
 }
 template <typename T>
 cudaError_t launch_few(const Few &p, cudaStream_t stream) {
     static_assert(kFewTokens == 16, "groups of 8 tokens");
-    return p.T <= 8 ? launch_few_of<T, 1>(p, stream) : launch_few_of<T, 2>(p, stream);
+    const bool narrow = p.F <= 16 * sm_count();
+    if (p.T <= 8) return narrow ? launch_few_of<T, 1, 1>(p, stream) : launch_few_of<T, 1, 2>(p, stream);
+    return narrow ? launch_few_of<T, 2, 1>(p, stream) : launch_few_of<T, 2, 2>(p, stream);
 }
 
 // ---------------------------------------------------------------- gradient, element by element

@@ -64,9 +64,6 @@ cudaError_t launch_gate_grad_f16(const GateGrad &p, cudaStream_t stream);
 cudaError_t launch_gate_grad_bf16(const GateGrad &p, cudaStream_t stream);
 cudaError_t launch_join_f16(const Join &p, cudaStream_t stream);
 cudaError_t launch_join_bf16(const Join &p, cudaStream_t stream);
-// Rows of `cols` 16-bit values, `from` elements apart, to rows `to` elements apart.
-cudaError_t launch_spread(const void *src, void *dst, int64_t rows, int cols, int64_t from, int64_t to,
-                          cudaStream_t stream);
 
 }  // namespace glu
 }  // namespace gdn
