@@ -192,57 +192,77 @@ cudaError_t bring(std::initializer_list<const Operand *> operands, cudaStream_t 
 bool map_of(CUtensorMap *m, const Operand &o, bool bf16, int box) {
     return make_map(m, o.at, bf16, o.stride, o.cols, o.rows, box);
 }
-// A result of p.rows rows, by tensor map where its rows are words of 16 bytes.
-bool result(Result *r, const Product &p, void *at, int64_t stride, int cols, bool bf16) {
+// A result of job.rows rows, by tensor map where its rows are words of 16 bytes.
+bool result(Result *r, const Job &job, void *at, int64_t stride, int cols, bool bf16) {
     r->at = at, r->stride = stride, r->by_map = lines(at, stride);
-    return !r->by_map || make_map(&r->map, at, bf16, stride, cols, p.rows, 32);
+    return !r->by_map || make_map(&r->map, at, bf16, stride, cols, job.rows, 32);
 }
-void tiles_of(Product *p, int64_t rows, int cols, int width, int results, int64_t depth, int pairs, int parts) {
-    p->rows = rows, p->cols = cols;
-    p->tiles_m = (int)((rows + 255) / 256), p->tiles_n = (cols + width - 1) / width;
-    p->blocks_k = (int)((depth + 63) / 64);
-    const int all = pairs * p->blocks_k;
-    p->per_part = (all + parts - 1) / parts;
-    p->parts = parts;
-    p->tiles = (uint32_t)p->tiles_m * (uint32_t)p->tiles_n * (uint32_t)(results * parts);
+// `results` results of rows x cols in tiles of 256 x width, sums over `pairs` pairs of operands with
+// `depth` of K each, in `parts` stretches.
+void sizes(Job *j, int64_t rows, int cols, int width, int results, int64_t depth, int pairs, int parts) {
+    j->rows = rows, j->cols = cols, j->results = results, j->pairs = pairs, j->parts = parts;
+    j->tiles_m = (int)((rows + 255) / 256), j->tiles_n = (cols + width - 1) / width;
+    j->blocks_k = (int)((depth + 63) / 64);
+    j->per_part = (pairs * j->blocks_k + parts - 1) / parts;
+    j->tiles = (uint32_t)j->tiles_m * (uint32_t)j->tiles_n * (uint32_t)(results * parts);
 }
-// The stretches that K of a gradient's result is cut into: as many as make the
-// device's time least, in K-steps (0.27 us) a pair of blocks.  A tile costs some six steps
-// beside its own, shares are written and read in fp32 and a launch is added.
-int parts_of(int64_t rows, int cols, int results, int64_t depth, int pairs) {
-    const int64_t tiles = (rows + 255) / 256 * ((cols + 255) / 256) * results, all = (depth + 63) / 64 * pairs;
+// The stretches that K of the gradients' results is cut into: those that make the device's
+// time least, in K-steps (0.27 us) of a pair of blocks.  A tile costs some six steps beside its
+// own; shares are written and read in fp32, and a launch is added.  Pairs of blocks take
+// tiles in turn, the first job's first, so the longest time is that of the first pair, or of
+// the first one that has a tile less of the first job.
+struct Cut {
+    int64_t tiles = 0, steps = 0;  // in one stretch
+    double values = 0;             // of all results
+    bool into(int n) const { return n == 1 || (steps / n >= 8 && (steps + (steps + n - 1) / n - 1) / ((steps + n - 1) / n) == n); }
+};
+void choose_parts(const Cut &first, const Cut &second, int *n1, int *n2) {
+    static const int counts[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, kMostParts};
     const int64_t device = gdn::sm_count() / 2;
-    const double values = (double)rows * padded(cols) * results;
-    int best = 1;
-    double least = 0;
-    for (int n = 1; n <= kMostParts && (n == 1 || all / n >= 8); ++n) {
-        const int64_t per = (all + n - 1) / n;
-        if ((all + per - 1) / per != n) continue;  // the last stretch would be empty
-        double t = (double)((tiles * n + device - 1) / device) * (double)(per + 6);
-        if (n > 1) t += 12 + values * n * 8 / 6.5e6 / 0.27;
-        if (n == 1 || t < least) best = n, least = t;
+    double least = -1;
+    for (const int i : counts) {
+        if (!first.into(i) || (first.tiles == 0 && i > 1)) continue;
+        for (const int j : counts) {
+            if (!second.into(j) || (second.tiles == 0 && j > 1)) continue;
+            const int64_t a = first.tiles * i, all = a + second.tiles * j;
+            const double ta = (double)((first.steps + i - 1) / i + 6), tb = (double)((second.steps + j - 1) / j + 6);
+            double longest = 0;
+            for (const int64_t p : {(int64_t)0, a % device}) {
+                const int64_t mine = (a - p + device - 1) / device, total = (all - p + device - 1) / device;
+                const double t = (double)mine * ta + (double)(total - mine) * tb;
+                if (t > longest) longest = t;
+            }
+            const double shares = (i > 1 ? first.values * i : 0) + (j > 1 ? second.values * j : 0);
+            if (shares > 0) longest += 12 + shares * 8 / 6.5e6 / 0.27;
+            if (least < 0 || longest < least) least = longest, *n1 = i, *n2 = j;
+        }
     }
-    return best;
 }
-cudaError_t launch(const Product &p, Mode mode, bool bf16, const void *shares, cudaStream_t s) {
-    const cudaError_t e = bf16 ? launch_product_bf16(p, mode, s) : launch_product_f16(p, mode, s);
-    if (e != cudaSuccess || p.parts == 1) return e;
-    Join j = {};
-    j.shares = static_cast<const float *>(shares);
-    j.results = mode == kWeights ? 2 : 1;
-    j.out[0] = p.c[0].at, j.out[1] = p.c[1].at;
-    j.rows = p.rows, j.stride = p.c[0].stride, j.cols = p.cols, j.cs = (int)padded(p.cols), j.parts = p.parts;
-    return bf16 ? launch_join_bf16(j, s) : launch_join_f16(j, s);
+Cut cut_of(int64_t rows, int cols, int results, int64_t depth, int pairs) {
+    Cut c;
+    c.tiles = (rows + 255) / 256 * ((cols + 255) / 256) * results;
+    c.steps = (depth + 63) / 64 * pairs;
+    c.values = (double)rows * padded(cols) * results;
+    return c;
+}
+Join join_of(const Job &j, const void *shares) {
+    Join r = {};
+    r.shares = static_cast<const float *>(shares);
+    r.rows = j.rows, r.stride = j.c[0].stride, r.cols = j.cols, r.cs = (int)padded(j.cols);
+    r.parts = j.parts, r.results = j.results;
+    r.words = j.cols % 4 == 0 && r.stride % 4 == 0;
+    for (int z = 0; z < j.results; ++z) r.out[z] = j.c[z].at, r.words = r.words && aligned(j.c[z].at, 8);
+    return r;
 }
 gdn_status no_map() { return fail(GDN_ERR_CUDA, "a tensor map could not be made"); }
 
-struct Forward {
+struct ForwardPlan {
     bool few;
     Operand x, wg, wu;
     size_t bytes;
 };
-Forward plan(const gdn_glu_args *a, void *ws) {
-    Forward f = {};
+ForwardPlan plan(const gdn_glu_args *a, void *ws) {
+    ForwardPlan f = {};
     f.few = a->rows <= kFewTokens;
     if (f.few || a->rows == 0) return f;
     Pieces pieces = {static_cast<unsigned char *>(ws)};
@@ -253,17 +273,17 @@ Forward plan(const gdn_glu_args *a, void *ws) {
     return f;
 }
 
-struct Backward {
+struct BackwardPlan {
     Operand x, wg, wu, dg, du;
     int in_parts, w_parts;
-    void *shares;  // of one product after the other
+    void *in_shares, *w_shares;
     size_t bytes;
 };
-Backward plan_grad(const gdn_glu_grad_args *a, void *ws) {
-    Backward b = {};
+BackwardPlan plan_grad(const gdn_glu_grad_args *a, void *ws) {
+    BackwardPlan b = {};
     if (a->rows == 0) return b;
     Pieces pieces = {static_cast<unsigned char *>(ws)};
-    const int64_t F = a->inner, Fp = padded(F);
+    const int64_t F = a->inner, Fp = padded(F), Dp = padded(a->dim);
     b.dg = {pieces.take(a->rows * Fp), Fp, F, a->rows};
     b.du = {pieces.take(a->rows * Fp), Fp, F, a->rows};
     if (a->d_w_gate) b.x = operand(a->x, a->rows, a->dim, or_dense(a->x_stride, a->dim), &pieces);
@@ -271,11 +291,12 @@ Backward plan_grad(const gdn_glu_grad_args *a, void *ws) {
         b.wg = operand(a->w_gate, F, a->dim, a->dim, &pieces);
         b.wu = operand(a->w_up, F, a->dim, a->dim, &pieces);
     }
-    b.in_parts = a->dx ? parts_of(a->rows, a->dim, 1, F, 2) : 1;
-    b.w_parts = a->d_w_gate ? parts_of(F, a->dim, 2, a->rows, 1) : 1;
-    const int64_t in = b.in_parts > 1 ? a->rows * padded(a->dim) * b.in_parts : 0;
-    const int64_t w = b.w_parts > 1 ? F * padded(a->dim) * b.w_parts * 2 : 0;
-    b.shares = pieces.take(2 * (in > w ? in : w));
+    Cut in, w;
+    if (a->dx) in = cut_of(a->rows, a->dim, 1, F, 2);
+    if (a->d_w_gate) w = cut_of(F, a->dim, 2, a->rows, 1);
+    choose_parts(in, w, &b.in_parts, &b.w_parts);
+    b.in_shares = pieces.take(b.in_parts > 1 ? 2 * a->rows * Dp * b.in_parts : 0);
+    b.w_shares = pieces.take(b.w_parts > 1 ? 4 * F * Dp * b.w_parts : 0);
     b.bytes = pieces.used;
     return b;
 }
@@ -301,7 +322,7 @@ gdn_status gdn_glu(const gdn_glu_args *a, void *ws, size_t ws_bytes, gdn_stream 
     if (st != GDN_OK) return st;
     if ((st = check_workspace(ws, ws_bytes, plan(a, nullptr).bytes)) != GDN_OK) return st;
     if (a->rows == 0) return gdn::ok();
-    const Forward f = plan(a, ws);
+    const ForwardPlan f = plan(a, ws);
     const bool bf16 = a->dtype == GDN_DTYPE_BF16;
     const int64_t os = or_dense(a->out_stride, a->inner);
     cudaStream_t s = (cudaStream_t)stream;
@@ -313,17 +334,18 @@ gdn_status gdn_glu(const gdn_glu_args *a, void *ws, size_t ws_bytes, gdn_stream 
         p.words = lines(a->x, p.xs) && lines(a->w_gate, a->dim) && lines(a->w_up, a->dim);
         return gdn::cuda_status(bf16 ? launch_few_bf16(p, s) : launch_few_f16(p, s));
     }
-    Product p = {};
-    tiles_of(&p, a->rows, a->inner, 128, 1, a->dim, 1, 1);
+    Forward p = {};
+    Job &j = p.job;
+    sizes(&j, a->rows, a->inner, 128, 1, a->dim, 1, 1);
     p.act = a->activation, p.gates = a->gates != nullptr, p.err = a->error_word;
     const int Fp = (int)padded(a->inner);
-    if (!map_of(&p.a[0], f.x, bf16, 128) || !map_of(&p.b[0], f.wg, bf16, 128) || !map_of(&p.b[1], f.wu, bf16, 128) ||
-        !result(&p.c[0], p, a->out, os, a->inner, bf16))
+    if (!map_of(&j.a[0], f.x, bf16, 128) || !map_of(&j.b[0], f.wg, bf16, 128) || !map_of(&j.b[1], f.wu, bf16, 128) ||
+        !result(&j.c[0], j, a->out, os, a->inner, bf16))
         return no_map();
     for (int i = 0; a->gates && i < 2; ++i)
-        if (!result(&p.c[1 + i], p, static_cast<uint16_t *>(a->gates) + i * Fp, 2 * (int64_t)Fp, Fp, bf16)) return no_map();
+        if (!result(&j.c[1 + i], j, static_cast<uint16_t *>(a->gates) + i * Fp, 2 * (int64_t)Fp, Fp, bf16)) return no_map();
     cudaError_t e = bring({&f.x, &f.wg, &f.wu}, s);
-    if (e == cudaSuccess) e = launch(p, kForward, bf16, nullptr, s);
+    if (e == cudaSuccess) e = bf16 ? launch_forward_bf16(p, s) : launch_forward_f16(p, s);
     return gdn::cuda_status(e);
 }
 
@@ -347,25 +369,29 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *a, void *ws, size_t ws_byte
         if (a->d_w_up && e == cudaSuccess) e = cudaMemsetAsync(a->d_w_up, 0, bytes, s);
         return gdn::cuda_status(e);
     }
-    const Backward b = plan_grad(a, ws);
+    const BackwardPlan b = plan_grad(a, ws);
     const bool bf16 = a->dtype == GDN_DTYPE_BF16;
-    Product in = {}, w = {};
+    Backward p = {};
+    Job &in = p.job[0], &w = p.job[1];
+    Joins joins = {};
+    p.err = a->error_word;
     if (a->dx) {
-        tiles_of(&in, T, D, 256, 1, F, 2, b.in_parts);
-        in.err = a->error_word;
+        sizes(&in, T, D, 256, 1, F, 2, b.in_parts);
         if (!map_of(&in.a[0], b.dg, bf16, 128) || !map_of(&in.a[1], b.du, bf16, 128) ||
             !map_of(&in.b[0], b.wg, bf16, 64) || !map_of(&in.b[1], b.wu, bf16, 64) ||
             !result(&in.c[0], in, a->dx, or_dense(a->dx_stride, D), D, bf16) ||
-            (b.in_parts > 1 && !make_share_map(&in.shares, b.shares, padded(D), T, b.in_parts)))
+            (in.parts > 1 && !make_share_map(&in.shares, b.in_shares, padded(D), T, in.parts)))
             return no_map();
+        if (in.parts > 1) joins.j[joins.count++] = join_of(in, b.in_shares);
     }
     if (a->d_w_gate) {
-        tiles_of(&w, F, D, 256, 2, T, 1, b.w_parts);
-        w.err = a->error_word;
+        sizes(&w, F, D, 256, 2, T, 1, b.w_parts);
+        w.a_outer = 1;
         if (!map_of(&w.a[0], b.dg, bf16, 64) || !map_of(&w.a[1], b.du, bf16, 64) || !map_of(&w.b[0], b.x, bf16, 64) ||
             !result(&w.c[0], w, a->d_w_gate, D, D, bf16) || !result(&w.c[1], w, a->d_w_up, D, D, bf16) ||
-            (b.w_parts > 1 && !make_share_map(&w.shares, b.shares, padded(D), F, 2 * b.w_parts)))
+            (w.parts > 1 && !make_share_map(&w.shares, b.w_shares, padded(D), F, 2 * w.parts)))
             return no_map();
+        if (w.parts > 1) joins.j[joins.count++] = join_of(w, b.w_shares);
     }
     GateGrad g = {};
     g.d_out = a->d_out, g.gates = a->gates, g.dg = const_cast<void *>(b.dg.at), g.du = const_cast<void *>(b.du.at);
@@ -373,8 +399,8 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *a, void *ws, size_t ws_byte
     g.words = F % 8 == 0 && lines(a->d_out, g.dos);
     e = bf16 ? launch_gate_grad_bf16(g, s) : launch_gate_grad_f16(g, s);
     if (e == cudaSuccess) e = bring({&b.x, &b.wg, &b.wu}, s);
-    if (e == cudaSuccess && a->dx) e = launch(in, kInput, bf16, b.shares, s);
-    if (e == cudaSuccess && a->d_w_gate) e = launch(w, kWeights, bf16, b.shares, s);
+    if (e == cudaSuccess) e = bf16 ? launch_backward_bf16(p, s) : launch_backward_f16(p, s);
+    if (e == cudaSuccess && joins.count) e = bf16 ? launch_join_bf16(joins, s) : launch_join_f16(joins, s);
     return gdn::cuda_status(e);
 }
 

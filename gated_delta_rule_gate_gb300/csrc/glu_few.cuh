@@ -188,41 +188,46 @@ cudaError_t launch_gate_grad(const GateGrad &p, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------- shares of a result
-// Four adjacent columns a thread, the shares in their order.  WORDS: a result's groups of
-// four are words.
-template <typename T, bool WORDS>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Join p) {
+// Four adjacent columns a thread, the shares in their order.
+template <typename T>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Joins joins) {
     ptx::grid_wait();
-    const int per = p.cs / 4;
-    const int64_t plane = p.rows * p.cs, n = p.results * p.rows * per;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t line = i / per;  // result and row
-        const int c = (int)(i - line * per) * 4, z = line >= p.rows;
-        const int64_t row = z ? line - p.rows : line;
-        float sum[4] = {};
-#pragma unroll 4
-        for (int k = 0; k < p.parts; ++k) {
-            const float4 v = *reinterpret_cast<const float4 *>(p.shares + (int64_t)k * p.results * plane + line * p.cs + c);
-            sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
-        }
-        T *to = static_cast<T *>(p.out[z]) + row * p.stride + c;
-        if constexpr (WORDS) {
-            if (c < p.cols) store_values<T, 4>(to, sum);
-        } else {
+    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < p.cols) to[e] = static_cast<T>(sum[e]);
+    for (int q = 0; q < 2; ++q) {
+        if (q >= joins.count) break;
+        const Join &p = joins.j[q];
+        const int per = p.cs / 4;
+        const int64_t plane = p.rows * p.cs, n = p.results * p.rows * per;
+        for (; i < n; i += (int64_t)gridDim.x * 256) {
+            const int64_t line = i / per;  // result and row
+            const int c = (int)(i - line * per) * 4, z = line >= p.rows;
+            const int64_t row = z ? line - p.rows : line;
+            float sum[4] = {};
+#pragma unroll 4
+            for (int k = 0; k < p.parts; ++k) {
+                const float4 v =
+                    *reinterpret_cast<const float4 *>(p.shares + (int64_t)k * p.results * plane + line * p.cs + c);
+                sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
+            }
+            T *to = static_cast<T *>(p.out[z]) + row * p.stride + c;
+            if (p.words) {
+                if (c < p.cols) store_values<T, 4>(to, sum);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < p.cols) to[e] = static_cast<T>(sum[e]);
+            }
         }
+        i -= n;
     }
 }
 template <typename T>
-cudaError_t launch_join(const Join &p, cudaStream_t stream) {
-    const int64_t blocks = (p.results * p.rows * (p.cs / 4) + 255) / 256, most = (int64_t)sm_count() * 16;
-    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
-    auto words = [&](const void *o) { return reinterpret_cast<uintptr_t>(o) % 8 == 0; };
-    return p.cols % 4 == 0 && p.stride % 4 == 0 && words(p.out[0]) && words(p.out[p.results - 1])
-               ? launch_early(join_kernel<T, true>, grid, 256, 0, stream, p)
-               : launch_early(join_kernel<T, false>, grid, 256, 0, stream, p);
+cudaError_t launch_join(const Joins &p, cudaStream_t stream) {
+    int64_t n = 0;
+    for (int q = 0; q < p.count; ++q) n += p.j[q].results * p.j[q].rows * (p.j[q].cs / 4);
+    const int64_t blocks = (n + 255) / 256, most = (int64_t)sm_count() * 16;
+    return launch_early(join_kernel<T>, (unsigned)(blocks < most ? blocks : most), 256, 0, stream, p);
 }
 
 }  // namespace glu

@@ -5,6 +5,6 @@ namespace gdn {
 namespace glu {
 cudaError_t launch_few_f16(const Few &p, cudaStream_t stream) { return launch_few<__half>(p, stream); }
 cudaError_t launch_gate_grad_f16(const GateGrad &p, cudaStream_t stream) { return launch_gate_grad<__half>(p, stream); }
-cudaError_t launch_join_f16(const Join &p, cudaStream_t stream) { return launch_join<__half>(p, stream); }
+cudaError_t launch_join_f16(const Joins &p, cudaStream_t stream) { return launch_join<__half>(p, stream); }
 }  // namespace glu
 }  // namespace gdn

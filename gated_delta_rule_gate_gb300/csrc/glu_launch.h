@@ -8,11 +8,6 @@
 namespace gdn {
 namespace glu {
 
-// The products, by the operands' order in memory and what is done with the result:
-// kForward: out = act(x w_gate^T) (x w_up^T); kInput: dx = d_g w_gate + d_u w_up;
-// kWeights: d_w = d^T x, of both weights.
-enum Mode { kForward, kInput, kWeights };
-
 // A result's rows: by tensor map where they are words of 16 bytes, else element by element.
 struct Result {
     CUtensorMap map;
@@ -20,15 +15,28 @@ struct Result {
     int64_t stride;
     int by_map;
 };
-struct Product {
+// One kind of product: results of the same sizes, each a sum over `pairs` pairs of operands
+// (result z's are a[z + i], b[i] of pair i).  Tiles of 256 x 256, of 256 x 128 of the forward pass.
+struct Job {
     CUtensorMap a[2], b[2];
     CUtensorMap shares;  // fp32 [parts x results, rows, cols], where parts > 1
     Result c[3];
     int64_t rows;
-    uint32_t tiles;                  // of all results and stretches
-    int cols, tiles_m, tiles_n;
-    int blocks_k, parts, per_part;   // K-steps of one pair of operands; stretches of K, and theirs
+    uint32_t tiles;                 // of all results and stretches
+    int cols, tiles_m, tiles_n, results;
+    int pairs, blocks_k;            // K-steps (of 64) of one pair of operands
+    int parts, per_part;            // stretches of K, and theirs
+    int a_outer;                    // A has K as its outer dimension
+};
+// The forward pass: out = act(x w_gate^T) (x w_up^T).
+struct Forward {
+    Job job;
     int act, gates;
+    int32_t *err;
+};
+// The gradients: dx = d_g w_gate + d_u w_up, and d_w = d^T x of both weights, in one launch.
+struct Backward {
+    Job job[2];
     int32_t *err;
 };
 // Fewer tokens than the tensor cores' tiles are made for.
@@ -51,19 +59,25 @@ struct Join {
     const float *shares;
     void *out[2];
     int64_t rows, stride;
-    int cols, cs, parts, results;
+    int cols, cs, parts, results, words;  // words: groups of four results are
+};
+struct Joins {
+    Join j[2];
+    int count;
 };
 
 constexpr int kFewTokens = 16;
 
-cudaError_t launch_product_f16(const Product &p, Mode mode, cudaStream_t stream);
-cudaError_t launch_product_bf16(const Product &p, Mode mode, cudaStream_t stream);
+cudaError_t launch_forward_f16(const Forward &p, cudaStream_t stream);
+cudaError_t launch_forward_bf16(const Forward &p, cudaStream_t stream);
+cudaError_t launch_backward_f16(const Backward &p, cudaStream_t stream);
+cudaError_t launch_backward_bf16(const Backward &p, cudaStream_t stream);
 cudaError_t launch_few_f16(const Few &p, cudaStream_t stream);
 cudaError_t launch_few_bf16(const Few &p, cudaStream_t stream);
 cudaError_t launch_gate_grad_f16(const GateGrad &p, cudaStream_t stream);
 cudaError_t launch_gate_grad_bf16(const GateGrad &p, cudaStream_t stream);
-cudaError_t launch_join_f16(const Join &p, cudaStream_t stream);
-cudaError_t launch_join_bf16(const Join &p, cudaStream_t stream);
+cudaError_t launch_join_f16(const Joins &p, cudaStream_t stream);
+cudaError_t launch_join_bf16(const Joins &p, cudaStream_t stream);
 
 }  // namespace glu
 }  // namespace gdn

@@ -9,14 +9,15 @@
 // block) and eight warps that take the finished accumulators (two of them, so that the
 // next tile's products run meanwhile) out of tensor memory.
 //
-// kForward: the 256 columns are 128 of the gate and the same 128 of the up projection (the
+// Forward: the 256 columns are 128 of the gate and the same 128 of the up projection (the
 // first block of the pair loads w_gate's rows, the second w_up's), so both factors of an
-// output meet in one thread.  kInput sums over two pairs of operands, d_g w_gate and
-// d_u w_up, in one accumulator.  kWeights takes d^T and x as they lie in memory: both
-// operands have K (the tokens) as their outer dimension.
+// output meet in one thread.  Backward: dx sums over two pairs of operands, d_g w_gate and
+// d_u w_up, in one accumulator; the weights' gradients take d^T and x as they lie in memory,
+// both with K (the tokens) as their outer dimension.  Both are one launch, so that
+// the tiles of one fill what those of the other leave of the device.
 //
-// Where a gradient has few tiles, each is cut into stretches of K, whose sums go to
-// memory in fp32 and are added up by a kernel of their own, in one order.
+// Where there are few tiles, each is cut into stretches of K, whose sums go to memory in
+// fp32 and are added up by a kernel of their own, in one order.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -44,28 +45,34 @@ struct Barriers {
 
 struct TileAt {
     int m, n, z, part;  // of the results' tiles, which result, which stretch of K
+    int begin, end;     // its K-steps
 };
 // Tiles in groups of kGroup along the rows, so that those worked on at once share their
-// operands in L2.  (In 32 bits: with 64-bit divisions the place of a tile took longer than
-// its results.)
-template <Mode MODE>
-__device__ __forceinline__ TileAt tile_at(const Product &p, uint32_t i) {
+// operands in L2.
+__device__ __forceinline__ TileAt tile_at(const Job &p, uint32_t i) {
     TileAt t;
     const uint32_t wide = (uint32_t)p.tiles_n, tall = (uint32_t)p.tiles_m, per = wide * tall;
-    constexpr uint32_t results = MODE == kWeights ? 2 : 1;
-    t.z = t.part = 0;
-    if (MODE != kForward) {
-        const uint32_t plane = i / per;
-        i -= plane * per;
-        t.part = (int)(plane / results), t.z = (int)(plane % results);
-    }
+    const uint32_t plane = i / per;
+    i -= plane * per;
+    t.part = (int)plane / p.results, t.z = (int)plane - t.part * p.results;
     const uint32_t group = i / (kGroup * wide), first = group * kGroup;
     const uint32_t rows = tall - first < kGroup ? tall - first : kGroup;
     i -= first * wide;
     t.n = (int)(i / rows);
     t.m = (int)(first + (i - (uint32_t)t.n * rows));
+    const int all = p.pairs * p.blocks_k, end = (t.part + 1) * p.per_part;
+    t.begin = t.part * p.per_part, t.end = end < all ? end : all;
     return t;
 }
+// The job of a tile, which is then counted from the job's first.
+__device__ __forceinline__ const Job &job_of(const Forward &p, uint32_t &) { return p.job; }
+__device__ __forceinline__ const Job &job_of(const Backward &p, uint32_t &i) {
+    const bool second = i >= p.job[0].tiles;
+    if (second) i -= p.job[0].tiles;
+    return p.job[second];
+}
+__host__ __device__ inline uint32_t tiles_of(const Forward &p) { return p.job.tiles; }
+__host__ __device__ inline uint32_t tiles_of(const Backward &p) { return p.job[0].tiles + p.job[1].tiles; }
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);
@@ -101,7 +108,7 @@ __device__ __forceinline__ void put(unsigned char *box, int lane, const Packed (
 }
 
 // Sends a warp's box of 32 rows x 64 columns to its place; what lies outside is left out.
-__device__ __forceinline__ void send(const Product &p, const Result &c, const unsigned char *box, int64_t row, int col,
+__device__ __forceinline__ void send(const Job &p, const Result &c, const unsigned char *box, int64_t row, int col,
                                      int lane) {
     if (c.by_map) {
         ptx::fence_async_smem();
@@ -148,15 +155,16 @@ __device__ __forceinline__ void put_share(unsigned char *box, int lane, const ui
 
 // An accumulator's 128 columns of one of two groups of warps, `half`: taken into registers,
 // after which it is free for the next tile but one, and sent to their results.
-template <Mode MODE, typename T>
-__device__ __forceinline__ void take(const Product &p, const TileAt &t, uint32_t acc, uint32_t taken, int64_t row,
-                                     Boxes &boxes, int half, int lane) {
+template <typename T, typename Call>
+__device__ __forceinline__ void take(const Call &call, const Job &p, const TileAt &t, uint32_t acc, uint32_t taken,
+                                     int64_t row, Boxes &boxes, int half, int lane) {
+    constexpr bool FORWARD = std::is_same<Call, Forward>::value;
     auto release = [&] {
         tc::fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_cluster(taken);
     };
-    if constexpr (MODE == kForward) {  // 64 columns of the gate and the same 64 of up
+    if constexpr (FORWARD) {  // 64 columns of the gate and the same 64 of up
         const int col = t.n * 128 + 64 * half;
         const bool kept = row < p.rows && col < p.cols;
         Packed out[2], gate[2], up[2];
@@ -167,8 +175,8 @@ __device__ __forceinline__ void take(const Product &p, const TileAt &t, uint32_t
             tc::ld32_begin(acc + 128 + 64 * half + 32 * q, r[1]);
             tc::wait_ld(r);
             if (q == 1) release();
-            if (p.gates) gate[q] = pack<T>(r[0]), up[q] = pack<T>(r[1]);
-            with_activation(p.act, [&](auto act) {
+            if (call.gates) gate[q] = pack<T>(r[0]), up[q] = pack<T>(r[1]);
+            with_activation(call.act, [&](auto act) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     out[q].w[i] = pack2<T>(
@@ -180,7 +188,7 @@ __device__ __forceinline__ void take(const Product &p, const TileAt &t, uint32_t
         unsigned char *box = boxes.next(lane);
         put(box, lane, out);
         send(p, p.c[0], box, row, col, lane);
-        if (p.gates) {
+        if (call.gates) {
             box = boxes.next(lane);
             put(box, lane, gate);
             send(p, p.c[1], box, row, col, lane);
@@ -205,7 +213,7 @@ __device__ __forceinline__ void take(const Product &p, const TileAt &t, uint32_t
                 ptx::fence_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    ptx::tma_store_3d(&p.shares, col + 32 * h, (int)row, t.part * (MODE == kWeights ? 2 : 1) + t.z, box);
+                    ptx::tma_store_3d(&p.shares, col + 32 * h, (int)row, t.part * p.results + t.z, box);
                     ptx::bulk_commit();
                 }
             }
@@ -222,12 +230,11 @@ __device__ __forceinline__ void take(const Product &p, const TileAt &t, uint32_t
     }
 }
 
-template <Mode MODE, typename T>
+template <typename T, typename Call>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
-    product_kernel(const __grid_constant__ Product p) {
+    product_kernel(const __grid_constant__ Call p) {
     extern __shared__ unsigned char raw[];
-    constexpr bool A_MN = MODE == kWeights, B_MN = MODE != kForward;
-    constexpr int PAIRS = MODE == kInput ? 2 : 1;  // of operands that one result sums over
+    constexpr bool FORWARD = std::is_same<Call, Forward>::value;
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     unsigned char *boxes = sm + kStages * kStageBytes;
     Barriers &bar = *reinterpret_cast<Barriers *>(boxes + kEpilogueWarps * 2 * kBox);
@@ -254,23 +261,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     ptx::grid_wait();
 
     const uint32_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
-    // K-steps of a tile: those of its stretch
-    auto begin_of = [&](const TileAt &t) { return t.part * p.per_part; };
-    auto end_of = [&](const TileAt &t) {
-        const int e = (t.part + 1) * p.per_part, all = PAIRS * p.blocks_k;
-        return e < all ? e : all;
-    };
+    const uint32_t tiles = tiles_of(p);
     bool ok = true;
     if (warp == 0) {
         if (lane == 0) {
             int s = 0;
             uint32_t ph = 0;
             int64_t filled = 0;
-            for (uint32_t i = first; ok && i < p.tiles; i += step) {
-                const TileAt t = tile_at<MODE>(p, i);
+            for (uint32_t i = first; ok && i < tiles; i += step) {
+                uint32_t at = i;
+                const Job &job = job_of(p, at);
+                const TileAt t = tile_at(job, at);
                 const int m = t.m * 256 + 128 * (int)rank;
-                const int n = MODE == kForward ? t.n * 128 : t.n * 256 + 128 * (int)rank;
-                for (int kb = begin_of(t), e = end_of(t); kb < e; ++kb) {
+                const int n = FORWARD ? t.n * 128 : t.n * 256 + 128 * (int)rank;
+                for (int kb = t.begin; kb < t.end; ++kb) {
                     if (!ptx::mbar_wait_sleep(&bar.empty[s], ph ^ 1)) {
                         ok = false;
                         break;
@@ -278,20 +282,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                     unsigned char *a = sm + s * kStageBytes, *b = a + kHalf;
                     const uint32_t full = ptx::cluster_address(&bar.full[s], 0);
                     if (rank == 0) ptx::mbar_arrive_expect_tx(&bar.full[s], 2 * kStageBytes);
-                    const int pair = PAIRS == 2 && kb >= p.blocks_k ? 1 : 0, k = (kb - pair * p.blocks_k) * 64;
-                    const CUtensorMap *ma = &p.a[MODE == kWeights ? t.z : pair];
-                    const CUtensorMap *mb = &p.b[MODE == kForward ? rank : pair];
-                    if (A_MN) {
+                    const int pair = kb >= job.blocks_k ? 1 : 0, k = (kb - pair * job.blocks_k) * 64;
+                    const CUtensorMap *ma = &job.a[t.z + pair];
+                    const CUtensorMap *mb = &job.b[FORWARD ? rank : pair];
+                    if (!FORWARD && job.a_outer) {
                         ptx::tma_load_2d_pair(a, ma, m, k, full);
                         ptx::tma_load_2d_pair(a + kHalf / 2, ma, m + 64, k, full);
                     } else {
                         ptx::tma_load_2d_pair(a, ma, k, m, full);
                     }
-                    if (B_MN) {
+                    if (FORWARD) {
+                        ptx::tma_load_2d_pair(b, mb, k, n, full);
+                    } else {
                         ptx::tma_load_2d_pair(b, mb, n, k, full);
                         ptx::tma_load_2d_pair(b + kHalf / 2, mb, n + 64, k, full);
-                    } else {
-                        ptx::tma_load_2d_pair(b, mb, k, n, full);
                     }
                     ++filled;
                     if (++s == kStages) s = 0, ph ^= 1;
@@ -305,23 +309,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            constexpr uint32_t id = tc::idesc_f16(256, 256, A_MN, B_MN) |
-                                    (std::is_same<T, __nv_bfloat16>::value ? tc::kIdescBf16 : 0u);
-            constexpr uint32_t sa = A_MN ? 2048 : 32, sb = B_MN ? 2048 : 32;  // bytes of 16 along K
-            const uint64_t da = tc::desc_sw128(ptx::smem_u32(sm), A_MN ? kHalf / 2 : 16);
-            const uint64_t db = tc::desc_sw128(ptx::smem_u32(sm) + kHalf, B_MN ? kHalf / 2 : 16);
+            constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? tc::kIdescBf16 : 0u;
+            // operands with K as the inner and as the outer dimension, and 16 of K in bytes
+            const uint32_t base = ptx::smem_u32(sm);
+            const uint64_t inner = tc::desc_sw128(base, 16), outer = tc::desc_sw128(base, kHalf / 2);
+            const uint64_t db = tc::desc_adv(FORWARD ? inner : outer, kHalf);
+            constexpr uint32_t sb = FORWARD ? 32 : 2048;
             int s = 0;
             uint32_t ph = 0, turn = 0;
-            for (uint32_t i = first; ok && i < p.tiles; i += step, ++turn) {
+            for (uint32_t i = first; ok && i < tiles; i += step, ++turn) {
                 const uint32_t a = turn & 1;
+                uint32_t at = i;
+                const Job &job = job_of(p, at);
+                const TileAt t = tile_at(job, at);
+                const bool a_outer = !FORWARD && job.a_outer;
+                const uint64_t da = a_outer ? outer : inner;
+                const uint32_t sa = a_outer ? 2048 : 32;
+                const uint32_t id = tc::idesc_f16(256, 256, a_outer, !FORWARD) | type;
                 if (!ptx::mbar_wait(&bar.taken[a], ((turn >> 1) & 1) ^ 1, 1u << 22)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after();
-                const TileAt t = tile_at<MODE>(p, i);
-                const int b0 = begin_of(t), e = end_of(t);
-                for (int kb = b0; kb < e; ++kb) {
+                for (int kb = t.begin; kb < t.end; ++kb) {
                     if (!ptx::mbar_wait(&bar.full[s], ph, 1u << 22)) {
                         ok = false;
                         break;
@@ -330,7 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         tc::mma_f16_pair(tmem + a * 256, tc::desc_adv(da, s * kStageBytes + k * sa),
-                                         tc::desc_adv(db, s * kStageBytes + k * sb), id, kb > b0 || k > 0);
+                                         tc::desc_adv(db, s * kStageBytes + k * sb), id, kb > t.begin || k > 0);
                     tc::commit_pair(&bar.empty[s]);
                     if (++s == kStages) s = 0, ph ^= 1;
                 }
@@ -342,15 +352,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         Boxes mine = {boxes + (warp - 2) * 2 * kBox, 0};
         uint32_t turn = 0;
         const uint32_t taken[2] = {ptx::cluster_address(&bar.taken[0], 0), ptx::cluster_address(&bar.taken[1], 0)};
-        for (uint32_t i = first; i < p.tiles; i += step, ++turn) {
-            const TileAt t = tile_at<MODE>(p, i);
+        for (uint32_t i = first; i < tiles; i += step, ++turn) {
+            uint32_t at = i;
+            const Job &job = job_of(p, at);
+            const TileAt t = tile_at(job, at);
             const uint32_t a = turn & 1;
             ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&bar.done[a], (turn >> 1) & 1));
             if (!ok) break;
             tc::fence_after();
             const int64_t row = (int64_t)t.m * 256 + 128 * rank + 32 * quarter;
-            take<MODE, T>(p, t, tmem + a * 256 + ((uint32_t)(32 * quarter) << 16), taken[a], row, mine, (warp - 2) >> 2,
-                          lane);
+            take<T>(p, job, t, tmem + a * 256 + ((uint32_t)(32 * quarter) << 16), taken[a], row, mine, (warp - 2) >> 2,
+                    lane);
         }
         if (lane == 0) ptx::bulk_wait_read();
     }
@@ -364,23 +376,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
 }
 
-template <Mode MODE, typename T>
-cudaError_t launch_product_as(const Product &p, cudaStream_t stream) {
-    const auto kernel = product_kernel<MODE, T>;
+template <typename T, typename Call>
+cudaError_t launch_product(const Call &p, cudaStream_t stream) {
+    const auto kernel = product_kernel<T, Call>;
     const cudaError_t e = smem_attr((const void *)kernel, kProductSmem);
     if (e != cudaSuccess) return e;
-    const int64_t pairs = sm_count() / 2;
-    const unsigned blocks = 2 * (unsigned)(p.tiles < pairs ? p.tiles : pairs);
-    return launch_early(kernel, blocks, kProductThreads, kProductSmem, stream, p);
-}
-template <typename T>
-cudaError_t launch_product(const Product &p, Mode mode, cudaStream_t stream) {
-    if (p.tiles == 0) return cudaSuccess;
-    switch (mode) {
-        case kForward: return launch_product_as<kForward, T>(p, stream);
-        case kInput: return launch_product_as<kInput, T>(p, stream);
-        default: return launch_product_as<kWeights, T>(p, stream);
-    }
+    const uint32_t tiles = tiles_of(p), pairs = (uint32_t)sm_count() / 2;
+    return launch_early(kernel, 2 * (tiles < pairs ? tiles : pairs), kProductThreads, kProductSmem, stream, p);
 }
 
 }  // namespace glu

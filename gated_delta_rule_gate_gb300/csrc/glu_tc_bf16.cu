@@ -3,8 +3,7 @@
 
 namespace gdn {
 namespace glu {
-cudaError_t launch_product_bf16(const Product &p, Mode mode, cudaStream_t stream) {
-    return launch_product<__nv_bfloat16>(p, mode, stream);
-}
+cudaError_t launch_forward_bf16(const Forward &p, cudaStream_t stream) { return launch_product<__nv_bfloat16>(p, stream); }
+cudaError_t launch_backward_bf16(const Backward &p, cudaStream_t stream) { return launch_product<__nv_bfloat16>(p, stream); }
 }  // namespace glu
 }  // namespace gdn

@@ -3,8 +3,7 @@
 
 namespace gdn {
 namespace glu {
-cudaError_t launch_product_f16(const Product &p, Mode mode, cudaStream_t stream) {
-    return launch_product<__half>(p, mode, stream);
-}
+cudaError_t launch_forward_f16(const Forward &p, cudaStream_t stream) { return launch_product<__half>(p, stream); }
+cudaError_t launch_backward_f16(const Backward &p, cudaStream_t stream) { return launch_product<__half>(p, stream); }
 }  // namespace glu
 }  // namespace gdn
