@@ -334,10 +334,10 @@ gdn_status gdn_glu(const gdn_glu_args *a, void *ws, size_t ws_bytes, gdn_stream 
         p.words = lines(a->x, p.xs) && lines(a->w_gate, a->dim) && lines(a->w_up, a->dim);
         return gdn::cuda_status(bf16 ? launch_few_bf16(p, s) : launch_few_f16(p, s));
     }
-    Forward p = {};
+    ForwardArgs p = {};
     Job &j = p.job;
     sizes(&j, a->rows, a->inner, 128, 1, a->dim, 1, 1);
-    p.act = a->activation, p.gates = a->gates != nullptr, p.err = a->error_word;
+    p.act = a->activation, p.err = a->error_word;
     const int Fp = (int)padded(a->inner);
     if (!map_of(&j.a[0], f.x, bf16, 128) || !map_of(&j.b[0], f.wg, bf16, 128) || !map_of(&j.b[1], f.wu, bf16, 128) ||
         !result(&j.c[0], j, a->out, os, a->inner, bf16))
@@ -345,7 +345,7 @@ gdn_status gdn_glu(const gdn_glu_args *a, void *ws, size_t ws_bytes, gdn_stream 
     for (int i = 0; a->gates && i < 2; ++i)
         if (!result(&j.c[1 + i], j, static_cast<uint16_t *>(a->gates) + i * Fp, 2 * (int64_t)Fp, Fp, bf16)) return no_map();
     cudaError_t e = bring({&f.x, &f.wg, &f.wu}, s);
-    if (e == cudaSuccess) e = bf16 ? launch_forward_bf16(p, s) : launch_forward_f16(p, s);
+    if (e == cudaSuccess) e = bf16 ? launch_forward_bf16(p, a->gates, s) : launch_forward_f16(p, a->gates, s);
     return gdn::cuda_status(e);
 }
 

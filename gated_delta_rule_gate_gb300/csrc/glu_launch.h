@@ -28,12 +28,14 @@ struct Job {
     int parts, per_part;            // stretches of K, and theirs
     int a_outer;                    // A has K as its outer dimension
 };
-// The forward pass: out = act(x w_gate^T) (x w_up^T).
-struct Forward {
+// The forward pass: out = act(x w_gate^T) (x w_up^T); KEEP: the gates are results too.
+struct ForwardArgs {
     Job job;
-    int act, gates;
+    int act;
     int32_t *err;
 };
+template <bool KEEP>
+struct Forward : ForwardArgs {};
 // The gradients: dx = d_g w_gate + d_u w_up, and d_w = d^T x of both weights, in one launch.
 struct Backward {
     Job job[2];
@@ -68,8 +70,8 @@ struct Joins {
 
 constexpr int kFewTokens = 16;
 
-cudaError_t launch_forward_f16(const Forward &p, cudaStream_t stream);
-cudaError_t launch_forward_bf16(const Forward &p, cudaStream_t stream);
+cudaError_t launch_forward_f16(const ForwardArgs &p, bool keep, cudaStream_t stream);
+cudaError_t launch_forward_bf16(const ForwardArgs &p, bool keep, cudaStream_t stream);
 cudaError_t launch_backward_f16(const Backward &p, cudaStream_t stream);
 cudaError_t launch_backward_bf16(const Backward &p, cudaStream_t stream);
 cudaError_t launch_few_f16(const Few &p, cudaStream_t stream);

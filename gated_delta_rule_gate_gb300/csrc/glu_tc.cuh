@@ -5,7 +5,7 @@
 // 128 of the tile's rows in its tensor memory and half of either operand in its shared
 // memory, so that a K-step of 64 takes 32 KB of each block for 16.8 MFLOP: half the
 // operand bytes of two single blocks.  Persistent; per block a warp that loads
-// (TMA, five stages), a warp whose first thread issues the products (in the pair's first
+// (TMA, five or six stages), a warp whose first thread issues the products (in the pair's first
 // block) and eight warps that take the finished accumulators (two of them, so that the
 // next tile's products run meanwhile) out of tensor memory.
 //
@@ -31,15 +31,29 @@
 namespace gdn {
 namespace glu {
 
-constexpr int kStages = 5, kHalf = 16384;  // bytes of a block's share of an operand's stage
+constexpr int kHalf = 16384;  // bytes of a block's share of an operand's stage
 constexpr int kStageBytes = 2 * kHalf;
 constexpr int kEpilogueWarps = 8, kProductThreads = 32 * (2 + kEpilogueWarps);
 constexpr int kBox = 4096;  // 32 rows of 64 results
-constexpr int kProductSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * 2 * kBox + 256;
+// A warp's results are one box a tile in the forward pass, which leaves room for six
+// stages; with kept gates three, in the gradients two to four, two in turn.
+template <typename Call>
+struct Shape {
+    static constexpr bool kForward = false, kKeep = false;
+    static constexpr int kBoxes = 2, kStages = 5;
+};
+template <bool KEEP>
+struct Shape<Forward<KEEP>> {
+    static constexpr bool kForward = true, kKeep = KEEP;
+    static constexpr int kBoxes = KEEP ? 2 : 1, kStages = KEEP ? 5 : 6;
+};
+template <typename Call>
+constexpr int kProductSmem = 1024 + Shape<Call>::kStages * kStageBytes + kEpilogueWarps * Shape<Call>::kBoxes * kBox + 256;
 constexpr int kGroup = 8;  // tiles along the rows that are taken side by side
 
+template <int STAGES>
 struct Barriers {
-    uint64_t full[kStages], empty[kStages], done[2], taken[2];
+    uint64_t full[STAGES], empty[STAGES], done[2], taken[2];
     uint32_t tmem;
 };
 
@@ -65,13 +79,13 @@ __device__ __forceinline__ TileAt tile_at(const Job &p, uint32_t i) {
     return t;
 }
 // The job of a tile, which is then counted from the job's first.
-__device__ __forceinline__ const Job &job_of(const Forward &p, uint32_t &) { return p.job; }
+__device__ __forceinline__ const Job &job_of(const ForwardArgs &p, uint32_t &) { return p.job; }
 __device__ __forceinline__ const Job &job_of(const Backward &p, uint32_t &i) {
     const bool second = i >= p.job[0].tiles;
     if (second) i -= p.job[0].tiles;
     return p.job[second];
 }
-__host__ __device__ inline uint32_t tiles_of(const Forward &p) { return p.job.tiles; }
+__host__ __device__ inline uint32_t tiles_of(const ForwardArgs &p) { return p.job.tiles; }
 __host__ __device__ inline uint32_t tiles_of(const Backward &p) { return p.job[0].tiles + p.job[1].tiles; }
 
 template <typename T>
@@ -134,14 +148,18 @@ __device__ __forceinline__ void send(const Job &p, const Result &c, const unsign
     }
     __syncwarp();
 }
-// A warp's boxes, two in turn; the one that is filled next has been read by its store.
+// A warp's boxes, in turn; the one that is filled next has been read by its store.
+template <int N>
 struct Boxes {
     unsigned char *base;
     int turn;
     __device__ __forceinline__ unsigned char *next(int lane) {
-        if (lane == 0) ptx::bulk_wait_read_all_but_last();
+        if (lane == 0) {
+            if (N == 1) ptx::bulk_wait_read();
+            else ptx::bulk_wait_read_all_but_last();
+        }
         __syncwarp();
-        return base + (turn ^= 1) * kBox;
+        return N == 1 ? base : base + (turn ^= 1) * kBox;
     }
 };
 
@@ -157,8 +175,8 @@ __device__ __forceinline__ void put_share(unsigned char *box, int lane, const ui
 // after which it is free for the next tile but one, and sent to their results.
 template <typename T, typename Call>
 __device__ __forceinline__ void take(const Call &call, const Job &p, const TileAt &t, uint32_t acc, uint32_t taken,
-                                     int64_t row, Boxes &boxes, int half, int lane) {
-    constexpr bool FORWARD = std::is_same<Call, Forward>::value;
+                                     int64_t row, Boxes<Shape<Call>::kBoxes> &boxes, int half, int lane) {
+    constexpr bool FORWARD = Shape<Call>::kForward, KEEP = Shape<Call>::kKeep;
     auto release = [&] {
         tc::fence_before();
         __syncwarp();
@@ -175,7 +193,7 @@ __device__ __forceinline__ void take(const Call &call, const Job &p, const TileA
             tc::ld32_begin(acc + 128 + 64 * half + 32 * q, r[1]);
             tc::wait_ld(r);
             if (q == 1) release();
-            if (call.gates) gate[q] = pack<T>(r[0]), up[q] = pack<T>(r[1]);
+            if (KEEP) gate[q] = pack<T>(r[0]), up[q] = pack<T>(r[1]);
             with_activation(call.act, [&](auto act) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -188,7 +206,7 @@ __device__ __forceinline__ void take(const Call &call, const Job &p, const TileA
         unsigned char *box = boxes.next(lane);
         put(box, lane, out);
         send(p, p.c[0], box, row, col, lane);
-        if (call.gates) {
+        if (KEEP) {
             box = boxes.next(lane);
             put(box, lane, gate);
             send(p, p.c[1], box, row, col, lane);
@@ -234,10 +252,11 @@ template <typename T, typename Call>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     product_kernel(const __grid_constant__ Call p) {
     extern __shared__ unsigned char raw[];
-    constexpr bool FORWARD = std::is_same<Call, Forward>::value;
+    constexpr bool FORWARD = Shape<Call>::kForward;
+    constexpr int kStages = Shape<Call>::kStages, kBoxes = Shape<Call>::kBoxes;
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     unsigned char *boxes = sm + kStages * kStageBytes;
-    Barriers &bar = *reinterpret_cast<Barriers *>(boxes + kEpilogueWarps * 2 * kBox);
+    Barriers<kStages> &bar = *reinterpret_cast<Barriers<kStages> *>(boxes + kEpilogueWarps * kBoxes * kBox);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -349,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         }
     } else {
         const int quarter = warp & 3;  // of the tensor memory's lanes, by the warp's number
-        Boxes mine = {boxes + (warp - 2) * 2 * kBox, 0};
+        Boxes<kBoxes> mine = {boxes + (warp - 2) * kBoxes * kBox, 0};
         uint32_t turn = 0;
         const uint32_t taken[2] = {ptx::cluster_address(&bar.taken[0], 0), ptx::cluster_address(&bar.taken[1], 0)};
         for (uint32_t i = first; i < tiles; i += step, ++turn) {
@@ -379,10 +398,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 template <typename T, typename Call>
 cudaError_t launch_product(const Call &p, cudaStream_t stream) {
     const auto kernel = product_kernel<T, Call>;
-    const cudaError_t e = smem_attr((const void *)kernel, kProductSmem);
+    constexpr int smem = kProductSmem<Call>;
+    const cudaError_t e = smem_attr((const void *)kernel, smem);
     if (e != cudaSuccess) return e;
     const uint32_t tiles = tiles_of(p), pairs = (uint32_t)sm_count() / 2;
-    return launch_early(kernel, 2 * (tiles < pairs ? tiles : pairs), kProductThreads, kProductSmem, stream, p);
+    return launch_early(kernel, 2 * (tiles < pairs ? tiles : pairs), kProductThreads, smem, stream, p);
+}
+
+template <typename T>
+cudaError_t launch_forward(const ForwardArgs &p, bool keep, cudaStream_t stream) {
+    return keep ? launch_product<T>(Forward<true>{p}, stream) : launch_product<T>(Forward<false>{p}, stream);
 }
 
 }  // namespace glu
