@@ -13,6 +13,8 @@
 
 #include <cuda_fp8.h>
 
+#include <utility>
+
 #include "launch.h"
 #include "ptx.cuh"
 #include "status.h"
@@ -40,7 +42,7 @@ template <int MAX>
 struct Table {
     Tensor t[MAX];
     int64_t rows;
-    int count, stretch;  // tensors, rows of a block
+    int count, stretch, slots;  // tensors, rows of a block, slots of a warp (fewer than its ring where its rows are)
 };
 // What the step is made of, and the two places of which the host need not know.
 struct Step {
@@ -143,42 +145,36 @@ __device__ __forceinline__ float2 root_code(float2 root, const Scale &s) {
     return make_float2(at_least(q.x, root.x), at_least(q.y, root.y));
 }
 
-// Four adjacent values, of a row in shared memory and to one in global memory.
-template <bool WIDE>
-__device__ __forceinline__ void get4(const unsigned char *row, int type, int at, float2 *v) {
-    if constexpr (WIDE) {
+// Four adjacent values, of a row in shared or global memory and to one in global memory.
+template <typename T>
+__device__ __forceinline__ void get4(const unsigned char *row, int at, float2 *v) {
+    if constexpr (sizeof(T) == 4) {
         const float4 w = *reinterpret_cast<const float4 *>(row + 4 * at);
         v[0] = make_float2(w.x, w.y), v[1] = make_float2(w.z, w.w);
     } else {
         const uint2 w = *reinterpret_cast<const uint2 *>(row + 2 * at);
+        constexpr int type = std::is_same<T, __half>::value ? GDN_DTYPE_F16 : GDN_DTYPE_BF16;
         v[0] = widen2(w.x, type), v[1] = widen2(w.y, type);
     }
 }
-__device__ __forceinline__ void put4(float *base, int64_t at, const float2 *v) {
-    *reinterpret_cast<float4 *>(base + at) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-}
-template <bool WIDE>
-__device__ __forceinline__ void put4(void *base, int type, int64_t at, const float2 *v) {
-    if constexpr (WIDE) {
-        put4(static_cast<float *>(base), at, v);
-    } else {
-        const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
-        if (type == GDN_DTYPE_F16) store_values<__half, 4>(static_cast<__half *>(base) + at, f);
-        else store_values<__nv_bfloat16, 4>(static_cast<__nv_bfloat16 *>(base) + at, f);
-    }
+template <typename T>
+__device__ __forceinline__ void put4(void *base, int64_t at, const float2 *v) {
+    const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
+    store_values<T, 4>(static_cast<T *>(base) + at, f);
 }
 
 // Whole rows of 256 elements come through shared memory (cp.async), several on their way
 // a warp, without a register: with the next row in registers 2^26 bf16 elements with
 // 8-bit states took 171 us, for 128 (three rows on their way: 181).  A lane has elements 4 lane + 128 j ... + 3.
-// PW, GW: fp32 parameters, gradients; MASTER: 16-bit parameters with copies.
-template <bool EIGHT, bool PW, bool MASTER, bool GW>
+// P, G: the types of parameters and gradients; MASTER: there are fp32 copies.
+template <bool EIGHT, typename P, bool MASTER, typename G>
 struct Whole {
-    static constexpr int kP = PW || MASTER ? 4 * kRow : 2 * kRow, kG = GW ? 4 * kRow : 2 * kRow;
+    using Kept = std::conditional_t<MASTER, float, P>;  // what the step is taken on
+    static constexpr int kP = sizeof(Kept) * kRow, kG = sizeof(G) * kRow;
     static constexpr int kState = EIGHT ? kRow : 4 * kRow;
     static constexpr int kBytes = kP + kG + 2 * kState + 16;  // and the scales
-    // as many rows a warp as leave room for four (fp32 states: three) blocks an SM, two at least
-    static constexpr int kSlots = 72 * 1024 / (kWarps * kBytes);
+    // as many rows a warp as leave room for four blocks an SM
+    static constexpr int kSlots = 54 * 1024 / (kWarps * kBytes);
     static constexpr int kSmem = EIGHT ? kWarps * kSlots * kBytes : 0;
 
     template <int N>
@@ -216,8 +212,8 @@ struct Whole {
         for (int j = 0; j < kGroups; ++j) {
             const int e = 4 * lane + 128 * j;
             float2 g[2];
-            get4<GW>(sg, t.g_type, e, g);
-            get4<PW || MASTER>(sp, t.p_type, e, p + 2 * j);
+            get4<G>(sg, e, g);
+            get4<Kept>(sp, e, p + 2 * j);
             if constexpr (EIGHT) {
                 const uint32_t cm = *reinterpret_cast<const uint32_t *>(sm + e);
                 const uint32_t cv = *reinterpret_cast<const uint32_t *>(sv + e);
@@ -228,8 +224,8 @@ struct Whole {
                     v[2 * j + h] = __fmul2_rn(v[2 * j + h], v[2 * j + h]);
                 }
             } else {
-                get4<true>(sm, 0, e, m + 2 * j);
-                get4<true>(sv, 0, e, v + 2 * j);
+                get4<float>(sm, e, m + 2 * j);
+                get4<float>(sv, e, v + 2 * j);
             }
 #pragma unroll
             for (int i = 2 * j; i < 2 * j + 2; ++i) root[i] = update(st, f, g[i - 2 * j], p[i], m[i], v[i]);
@@ -238,11 +234,11 @@ struct Whole {
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) {
             const int64_t e = row * kRow + 4 * lane + 128 * j;
-            if (MASTER) put4(t.master, e, p + 2 * j);
-            put4<PW>(t.p, t.p_type, e, p + 2 * j);
+            if (MASTER) put4<float>(t.master, e, p + 2 * j);
+            put4<P>(t.p, e, p + 2 * j);
             if constexpr (!EIGHT) {
-                put4(static_cast<float *>(t.m), e, m + 2 * j);
-                put4(static_cast<float *>(t.v), e, v + 2 * j);
+                put4<float>(t.m, e, m + 2 * j);
+                put4<float>(t.v, e, v + 2 * j);
             }
         }
         if constexpr (EIGHT) {
@@ -326,8 +322,8 @@ __device__ __forceinline__ bool whole_row(const Tensor &t, int64_t row) { return
 // A block has a stretch of adjacent rows, which its warps take in turn, and the device
 // as many blocks as there are stretches: SMs are not equally fast (equal shares of a
 // persistent grid: 235 us in place of 218 for 2^26 bf16 elements with fp32 states).
-template <bool EIGHT, bool PW, bool MASTER, bool GW, int MAX>
-__global__ void __launch_bounds__(kThreads, EIGHT ? 3 : 2) adamw_kernel(const __grid_constant__ Table<MAX> tab,
+template <bool EIGHT, typename P, bool MASTER, typename G, int MAX>
+__global__ void __launch_bounds__(kThreads, EIGHT ? 4 : 2) adamw_kernel(const __grid_constant__ Table<MAX> tab,
                                                                         const __grid_constant__ Step st) {
     extern __shared__ __align__(16) unsigned char slots[];
     ptx::grid_wait();
@@ -353,14 +349,14 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? 3 : 2) adamw_kernel(const __
     f.decay = lr * st.weight_decay;
     f.unroot = __fdiv_rn(1.f, root2);
     f.eps = st.eps;
-    using Rows = Whole<EIGHT, PW, MASTER, GW>;
+    using Rows = Whole<EIGHT, P, MASTER, G>;
     constexpr int N = EIGHT ? Rows::kSlots : 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t row = (int64_t)blockIdx.x * tab.stretch + warp;
     const int64_t stop = row - warp + tab.stretch < tab.rows ? row - warp + tab.stretch : tab.rows;
     int i = find_tensor(tab, row);
     // slots, of rows ahead of this one (8-bit states)
-    unsigned char *mine = slots + warp * N * Rows::kBytes;
+    unsigned char *mine = slots + warp * tab.slots * Rows::kBytes;
     int64_t ahead = row;
     int ia = i, at = 0, to = 0;
     auto request = [&] {
@@ -390,13 +386,16 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? 3 : 2) adamw_kernel(const __
     }
 }
 
-// Tensors of one kind share a kernel: the width of parameters and of gradients, and
+// Tensors of one kind share a kernel: the types of parameters and of gradients, and
 // whether there is a copy.  (An fp32 parameter with a copy goes element by element.)
+constexpr int kKinds = 15;
 int kind_of(const gdn_adamw_args *a, int i) {
-    const bool pw = a->param_dtypes[i] == GDN_DTYPE_F32, gw = a->grad_dtypes[i] == GDN_DTYPE_F32;
-    return (pw ? 0 : a->master && a->master[i] ? 2 : 1) * 2 + gw;
+    const int p = a->param_dtypes[i], copied = p != GDN_DTYPE_F32 && a->master && a->master[i];
+    return (p + 2 * copied) * 3 + a->grad_dtypes[i];
 }
-constexpr int kKinds = 6;
+static_assert(GDN_DTYPE_F32 == 0 && GDN_DTYPE_F16 == 1 && GDN_DTYPE_BF16 == 2, "kinds count types");
+template <int TYPE>
+using TypeOf = std::conditional_t<TYPE == GDN_DTYPE_F32, float, std::conditional_t<TYPE == GDN_DTYPE_F16, __half, __nv_bfloat16>>;
 
 // Fills a table with tensors of a kind from i on; returns the first that was not looked at.
 template <int MAX>
@@ -417,8 +416,8 @@ int fill(const gdn_adamw_args *a, int i, int kind, Table<MAX> *tab) {
                   aligned(t.master, 16) && !(t.master && t.p_type == GDN_DTYPE_F32);
         tab->rows += (t.n + kRow - 1) / kRow;
     }
-    // rows of a warp: one of few, so that they reach all SMs, up to kStretch of many
-    int64_t each = tab->rows / (kWarps * 152 * 4);
+    // rows of a warp: so few that they reach all SMs (six blocks each), up to kStretch
+    int64_t each = (tab->rows + kWarps * 152 * 6 - 1) / (kWarps * 152 * 6);
     each = each < 1 ? 1 : each > kStretch ? kStretch : each;
     while (tab->rows / (each * kWarps) >= 1LL << 31) each *= 2;
     tab->stretch = (int)each * kWarps;
@@ -426,36 +425,43 @@ int fill(const gdn_adamw_args *a, int i, int kind, Table<MAX> *tab) {
 }
 
 template <int KIND, bool EIGHT, int MAX>
-cudaError_t launch(const Table<MAX> &tab, const Step &st, cudaStream_t stream) {
-    constexpr bool PW = KIND / 2 == 0, MASTER = KIND / 2 == 2, GW = KIND % 2 == 1;
-    constexpr int smem = Whole<EIGHT, PW, MASTER, GW>::kSmem;
-    const auto kernel = adamw_kernel<EIGHT, PW, MASTER, GW, MAX>;
-    cudaError_t e = smem_attr((const void *)kernel, smem);
+cudaError_t launch(Table<MAX> &tab, const Step &st, cudaStream_t stream) {
+    constexpr int p = KIND / 3;
+    constexpr bool copied = p > 2;
+    using P = TypeOf<(copied ? p - 2 : p)>;
+    using G = TypeOf<KIND % 3>;
+    using Rows = Whole<EIGHT, P, copied, G>;
+    const auto kernel = adamw_kernel<EIGHT, P, copied, G, MAX>;
+    const cudaError_t e = smem_attr((const void *)kernel, Rows::kSmem);
     if (e != cudaSuccess) return e;
+    const int each = tab.stretch / kWarps;
+    tab.slots = each < Rows::kSlots ? each : Rows::kSlots;
+    const size_t smem = EIGHT ? kWarps * tab.slots * Rows::kBytes : 0;
     const int64_t blocks = (tab.rows + tab.stretch - 1) / tab.stretch;
     return launch_early(kernel, (unsigned)blocks, kThreads, smem, stream, tab, st);
 }
 
-template <bool EIGHT, int MAX>
-cudaError_t run(const gdn_adamw_args *a, const Step &st, cudaStream_t stream) {
+template <bool EIGHT, int MAX, int... KINDS>
+cudaError_t run(const gdn_adamw_args *a, const Step &st, cudaStream_t stream, std::integer_sequence<int, KINDS...>) {
+    cudaError_t (*const launchers[])(Table<MAX> &, const Step &, cudaStream_t) = {launch<KINDS, EIGHT, MAX>...};
+    bool present[kKinds] = {};
+    for (int i = 0; i < a->count; ++i)
+        if (a->sizes[i] > 0) present[kind_of(a, i)] = true;
     Table<MAX> tab;
     for (int kind = 0; kind < kKinds; ++kind) {
-        for (int i = 0; i < a->count;) {
+        for (int i = 0; present[kind] && i < a->count;) {
             i = fill<MAX>(a, i, kind, &tab);
             if (tab.rows == 0) continue;
-            cudaError_t e;
-            switch (kind) {
-                case 0: e = launch<0, EIGHT, MAX>(tab, st, stream); break;
-                case 1: e = launch<1, EIGHT, MAX>(tab, st, stream); break;
-                case 2: e = launch<2, EIGHT, MAX>(tab, st, stream); break;
-                case 3: e = launch<3, EIGHT, MAX>(tab, st, stream); break;
-                case 4: e = launch<4, EIGHT, MAX>(tab, st, stream); break;
-                default: e = launch<5, EIGHT, MAX>(tab, st, stream); break;
-            }
+            const cudaError_t e = launchers[kind](tab, st, stream);
             if (e != cudaSuccess) return e;
         }
     }
     return cudaSuccess;
+}
+template <bool EIGHT>
+cudaError_t run(const gdn_adamw_args *a, const Step &st, cudaStream_t stream) {
+    const auto kinds = std::make_integer_sequence<int, kKinds>();
+    return a->count <= kFew ? run<EIGHT, kFew>(a, st, stream, kinds) : run<EIGHT, kMany>(a, st, stream, kinds);
 }
 
 }  // namespace adamw
@@ -532,10 +538,6 @@ extern "C" gdn_status gdn_adamw(const gdn_adamw_args *a, gdn_stream stream) {
     }
     s.step = a->step_device, s.lr_at = a->lr_device, s.norm = a->grad_norm, s.err = a->error_word;
     cudaStream_t q = (cudaStream_t)stream;
-    const bool eight = a->state_dtype == GDN_DTYPE_E4M3, few = a->count <= gdn::adamw::kFew;
-    if (eight)
-        return gdn::cuda_status(few ? gdn::adamw::run<true, gdn::adamw::kFew>(a, s, q)
-                                    : gdn::adamw::run<true, gdn::adamw::kMany>(a, s, q));
-    return gdn::cuda_status(few ? gdn::adamw::run<false, gdn::adamw::kFew>(a, s, q)
-                                : gdn::adamw::run<false, gdn::adamw::kMany>(a, s, q));
+    return gdn::cuda_status(a->state_dtype == GDN_DTYPE_E4M3 ? gdn::adamw::run<true>(a, s, q)
+                                                             : gdn::adamw::run<false>(a, s, q));
 }
