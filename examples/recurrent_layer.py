@@ -5,8 +5,10 @@
 Each block adds its input to a float32 residual stream and normalises it
 (gdn_rmsnorm), projects to x, a decay gate and an input gate in one product, runs the
 gated linear recurrence over the packed requests (gdn_scan, on column slices of that
-product) and projects back.  Training takes the operators' gradients through
-torch.autograd.Function and clips them all together (gdn_grad_clip).  Serving
+product) and projects back.  With `inner` a block has a second half: norm, gated
+feed-forward (gdn_glu) and projection back.  Training takes the operators' gradients
+through torch.autograd.Function and clips them all together (gdn_grad_clip), by plain
+descent, or as they are read by the AdamW step (gdn_adamw), whose states may be in 8 bits.  Serving
 prefills a slab of states (gdn_scan) and decodes one token a request in it
 (gdn_scan_step), with the norm's output in 8 bits with a scale for each 128 columns.
 
@@ -66,23 +68,48 @@ class Scan(torch.autograd.Function):
         return d, g.d_gate_bias, g.d_gate_scale, None
 
 
+class Glu(torch.autograd.Function):
+    """gdn_glu with the gates kept for its gradient."""
+
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up):
+        out, gates = gdn.gdn_glu(x, w_gate, w_up, want_gates=True)
+        ctx.save_for_backward(x, w_gate, w_up, gates)
+        return out
+
+    @staticmethod
+    def backward(ctx, d_out):
+        x, w_gate, w_up, gates = ctx.saved_tensors
+        g = gdn.gdn_glu_backward(d_out.contiguous(), x, w_gate, w_up, gates, want_dx=ctx.needs_input_grad[0])
+        return g.dx, g.d_w_gate, g.d_w_up
+
+
 class Block:
-    def __init__(self, dim, channels, gen, dtype=torch.bfloat16, device="cuda"):
+    def __init__(self, dim, channels, gen, dtype=torch.bfloat16, device="cuda", inner=0):
         rand = lambda *s: torch.randn(*s, generator=gen, device=device)
         self.norm = torch.ones(dim, dtype=dtype, device=device)
         self.w_in = (rand(dim, 3 * channels) * dim ** -0.5).to(dtype)
         self.w_out = (rand(channels, dim) * channels ** -0.5 * 0.5).to(dtype)
         self.bias = torch.rand(channels, generator=gen, device=device) * 4 - 2
         self.log_scale = torch.rand(channels, generator=gen, device=device) * 4 - 3
-        self.channels = channels
+        self.channels, self.inner = channels, inner
+        if inner:
+            self.norm2 = torch.ones(dim, dtype=dtype, device=device)
+            self.w_gate, self.w_up = ((rand(inner, dim) * dim ** -0.5).to(dtype) for _ in range(2))
+            self.w_down = (rand(inner, dim) * inner ** -0.5 * 0.5).to(dtype)
 
     def parameters(self):
-        return [self.norm, self.w_in, self.w_out, self.bias, self.log_scale]
+        own = [self.norm, self.w_in, self.w_out, self.bias, self.log_scale]
+        return own + [self.norm2, self.w_gate, self.w_up, self.w_down] if self.inner else own
 
     def train(self, x, residual, cu):
         y, residual = Norm.apply(x, residual, self.norm)
         out = Scan.apply(y @ self.w_in, self.bias, -torch.exp(self.log_scale), cu)
-        return out @ self.w_out, residual
+        x = out @ self.w_out
+        if self.inner:
+            y, residual = Norm.apply(x, residual, self.norm2)
+            x = Glu.apply(y, self.w_gate, self.w_up) @ self.w_down
+        return x, residual
 
     def serve(self, x, residual, recurrence, cu, slots, slab):
         """The same without gradients; the states of the requests are slab rows, and
@@ -95,13 +122,17 @@ class Block:
         x_, z, g = (y @ self.w_in).split(self.channels, dim=1)
         out = recurrence(x_, z, beta=g, beta_sigmoid=True, gate_bias=self.bias, gate_scale=-torch.exp(self.log_scale),
                          input_scale="unit", cu_seqlens=cu, slot_ids=slots, initial_state=slab, final_state=slab)
-        return out @ self.w_out, residual
+        x = out @ self.w_out
+        if self.inner:
+            y = gdn.gdn_rmsnorm(x, self.norm2, residual=residual, eps=EPS, residual_out=residual).out
+            x = gdn.gdn_glu(y, self.w_gate, self.w_up) @ self.w_down
+        return x, residual
 
 
 class Stack:
-    def __init__(self, blocks=2, dim=256, channels=384, seed=0):
+    def __init__(self, blocks=2, dim=256, channels=384, seed=0, inner=0):
         gen = torch.Generator(device="cuda").manual_seed(seed)
-        self.blocks = [Block(dim, channels, gen) for _ in range(blocks)]
+        self.blocks = [Block(dim, channels, gen, inner=inner) for _ in range(blocks)]
         self.dim, self.channels = dim, channels
 
     def parameters(self):
@@ -138,14 +169,49 @@ def draw(lengths, dim, gen, mix):
     return x.bfloat16(), 3 * y
 
 
-def train(stack, steps=30, lengths=(100, 37, 1, 118), rate=0.5, max_norm=1.0, seed=1):
-    """Losses and gradient norms of `steps` steps of gradient descent."""
+class Descent:
+    """Plain gradient descent on fp32 copies, the gradients clipped in place."""
+
+    def __init__(self, params, rate):
+        self.params, self.rate = params, rate
+        self.master = [p.float() for p in params]
+
+    def step(self, grads, max_norm):
+        norm = gdn.gdn_grad_clip(grads, max_norm)
+        for p, m, g in zip(self.params, self.master, grads):
+            m -= self.rate * g.float()
+            p.copy_(m)
+        return norm
+
+
+class AdamW:
+    """gdn_adamw on fp32 copies of 16-bit parameters, states of `bits`; the gradients are
+    clipped as they are read, and a norm that is not finite takes no step."""
+
+    def __init__(self, params, rate, bits=32):
+        self.params, self.rate, self.count = params, rate, 0
+        self.master = [p.float() if p.dtype != torch.float32 else None for p in params]
+        dtype = torch.float8_e4m3fn if bits == 8 else torch.float32
+        self.m, self.v = ([torch.zeros(p.shape, device=p.device).to(dtype) for p in params] for _ in range(2))
+        scales = lambda: [torch.zeros(-(-p.numel() // 256), device=p.device) for p in params]
+        self.scales = dict(exp_avg_scales=scales(), exp_avg_sq_scales=scales()) if bits == 8 else {}
+
+    def step(self, grads, max_norm):
+        self.count += 1
+        norm = gdn.gdn_grad_clip(grads, 3e38)  # measures, and leaves them as they are
+        gdn.gdn_adamw(self.params, grads, self.m, self.v, self.count, lr=self.rate, master=self.master, grad_norm=norm,
+                      max_norm=max_norm, **self.scales)
+        return norm
+
+
+def train(stack, steps=30, lengths=(100, 37, 1, 118), rate=0.5, max_norm=1.0, seed=1, optimizer=Descent):
+    """Losses and gradient norms of `steps` steps."""
     gen = torch.Generator(device="cuda").manual_seed(seed)
     mix = torch.randn(stack.dim, stack.dim, generator=gen, device="cuda") * stack.dim ** -0.5
     cu = offsets(lengths)
     x, y = draw(lengths, stack.dim, gen, mix)
     params = stack.parameters()
-    master = [p.float() for p in params]
+    opt = optimizer(params, rate)
     losses, norms = [], []
     for _ in range(steps):
         for p in params:
@@ -154,12 +220,10 @@ def train(stack, steps=30, lengths=(100, 37, 1, 118), rate=0.5, max_norm=1.0, se
         loss = (stack.train(x, cu) - y).square().mean()
         loss.backward()
         grads = [p.grad for p in params]
-        norms.append(gdn.gdn_grad_clip(grads, max_norm))
         with torch.no_grad():
-            for p, m, g in zip(params, master, grads):
-                m -= rate * g.float()
+            for p in params:
                 p.requires_grad_(False)
-                p.copy_(m)
+            norms.append(opt.step(grads, max_norm))
         losses.append(loss.detach())
     return [float(v) for v in losses], [float(v) for v in norms]
 
@@ -185,11 +249,12 @@ def serve(stack, lengths=(23, 64, 5), tokens=4, rows=8, seed=2):
 
 
 def main():
-    stack = Stack()
-    losses, norms = train(stack)
-    print("loss %.4f -> %.4f, gradient norm %.3f -> %.3f" % (losses[0], losses[-1], norms[0], norms[-1]))
-    got, want = serve(stack)
-    print("decode against prefill: %.2g of the largest output" % float((got - want).abs().max() / want.abs().max()))
+    for stack, kw in ((Stack(), {}), (Stack(inner=512), dict(optimizer=AdamW, rate=3e-3)),
+                      (Stack(inner=512), dict(optimizer=lambda p, rate: AdamW(p, rate, bits=8), rate=3e-3))):
+        losses, norms = train(stack, **kw)
+        print("loss %.4f -> %.4f, gradient norm %.3f -> %.3f" % (losses[0], losses[-1], norms[0], norms[-1]))
+        got, want = serve(stack)
+        print("decode against prefill: %.2g of the largest output" % float((got - want).abs().max() / want.abs().max()))
 
 
 if __name__ == "__main__":

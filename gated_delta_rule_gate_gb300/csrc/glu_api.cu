@@ -136,6 +136,7 @@ gdn_status validate_grad(const gdn_glu_grad_args *a) {
     if ((st = check_stride(a->dx_stride, a->dim, "dx_stride")) != GDN_OK) return st;
     if ((a->d_w_gate == nullptr) != (a->d_w_up == nullptr))
         return fail(GDN_ERR_INVALID, "d_w_gate and d_w_up go together");
+    if (a->d_w_gate && a->d_w_gate == a->d_w_up) return fail(GDN_ERR_INVALID, "d_w_gate and d_w_up are one tensor");
     if (!a->dx && !a->d_w_gate) return fail(GDN_ERR_INVALID, "dx, or d_w_gate and d_w_up, are required");
     if (a->rows > 0 && (!a->d_out || !a->gates)) return fail(GDN_ERR_INVALID, "d_out and gates are required");
     if (a->rows > 0 && a->dx && (!a->w_gate || !a->w_up)) return fail(GDN_ERR_INVALID, "w_gate and w_up are required");

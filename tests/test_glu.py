@@ -351,8 +351,9 @@ def _forward(**over):
 def _backward(**over):
     a = N.GdnGluGradArgs()
     a.rows, a.dim, a.inner, a.dtype = 20, 24, 16, N.DTYPE_F16
-    for f in ("x", "w_gate", "w_up", "d_out", "gates", "dx", "d_w_gate", "d_w_up"):
+    for f in ("x", "w_gate", "w_up", "d_out", "gates", "dx", "d_w_gate"):
         setattr(a, f, FAKE)
+    a.d_w_up = 2 * FAKE
     for k, v in over.items():
         setattr(a, k, v)
     return a
@@ -395,6 +396,7 @@ def test_forward_refuses(over, status, msg):
     (dict(d_out=None), N.GDN_ERR_INVALID, "d_out"),
     (dict(x=None), N.GDN_ERR_INVALID, "x is"),
     (dict(d_w_up=None), N.GDN_ERR_INVALID, "go together"),
+    (dict(d_w_up=FAKE), N.GDN_ERR_INVALID, "one tensor"),
     (dict(dx=None, d_w_gate=None, d_w_up=None), N.GDN_ERR_INVALID, "required"),
     (dict(), N.GDN_ERR_WORKSPACE, "workspace"),
 ])
