@@ -49,6 +49,7 @@ struct Step {
     float beta1, rest1, beta2, rest2;  // rest = 1 - beta, rounded from 64 bits
     float log_beta1, log_beta2;
     float lr, weight_decay, eps, max_norm, norm_eps;
+    float zero;       // -0
     float c1, root2;  // 1 - beta1^t and sqrt(1 - beta2^t) where step is NULL
     const int64_t *step;
     const float *lr_at;
@@ -92,10 +93,11 @@ __device__ __forceinline__ float2 decode2(uint32_t w) {
 }
 __device__ __forceinline__ uint32_t encode2(float2 v) { return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3); }
 
-// Pairs of elements throughout (packed fp32).  The root and the reciprocal are the
-// approximate ones, 2 ulp each: what they leave of p is below p's own rounding.  An 8-bit
-// element takes 44 instructions so; one element at a time with rounded roots and
-// quotients took 83, and 2^26 bf16 elements 227 us in place of 177.
+// Pairs of elements throughout (packed fp32).  What 8-bit codes depend on is rounded one by
+// one, in the formula's order: codes and scales are then a function of the definition
+// alone, and a value that lies between two codes falls where it does for anyone who
+// evaluates it so.  What only p takes (root and reciprocal) is approximate, 2 ulp each, which leaves
+// less than p's own rounding.
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float root_of(float v) {
     float r;
@@ -108,12 +110,27 @@ __device__ __forceinline__ float reciprocal(float v) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+// a b + c d with each product and the sum rounded.  Of packed products and a sum the compiler
+// makes an fma, whatever rounding they name; so each product is an fma with a -0 that it
+// does not know to be one.
+__device__ __forceinline__ float2 mix(float a, float2 b, float c, float2 d, float zero) {
+    return __fadd2_rn(__ffma2_rn(both(a), b, both(zero)), __ffma2_rn(both(c), d, both(zero)));
+}
+// A root that is up to 2 ulp off, rounded: one step of Newton's method, whose residual
+// v - s^2 an fma gives without error (Markstein 1990).  (With the rounded root of the library
+// 4.0e8 elements took 800 us in place of XX.)
+__device__ __forceinline__ float2 rounded_root(float2 s, float2 v) {
+    const float2 r = __ffma2_rn(make_float2(-s.x, -s.y), s, v);
+    const float2 h = make_float2(reciprocal(fmaxf(s.x, 0x1p-80f)), reciprocal(fmaxf(s.y, 0x1p-80f)));
+    return __ffma2_rn(r, __fmul2_rn(both(0.5f), h), s);
+}
 
-// A pair of elements: p, m and v (in 32 bits) and their gradients.  Returns the roots of v.
+// A pair of elements: p, m and v (in 32 bits) and their gradients.  Returns the roots of v,
+// approximate ones.
 __device__ __forceinline__ float2 update(const Step &st, const Factors &f, float2 g, float2 &p, float2 &m, float2 &v) {
     g = __fmul2_rn(g, both(f.clip));
-    m = __ffma2_rn(both(st.beta1), m, __fmul2_rn(both(st.rest1), g));
-    v = __ffma2_rn(both(st.beta2), v, __fmul2_rn(__fmul2_rn(both(st.rest2), g), g));
+    m = mix(st.beta1, m, st.rest1, g, st.zero);
+    v = mix(st.beta2, v, st.rest2, __fmul2_rn(g, g), st.zero);
     const float2 root = make_float2(root_of(v.x), root_of(v.y));
     const float2 den = __ffma2_rn(root, both(f.unroot), both(f.eps));
     const float2 q = __fmul2_rn(m, make_float2(reciprocal(den.x), reciprocal(den.y)));
@@ -132,9 +149,9 @@ __device__ __forceinline__ Scale scale_of(const float2 (&y)[4]) {
     // numbers that are not negative compare as their bits do
     a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
     const float s = fmaxf(a, 0x1p-100f) * (1.f / 448.f);
-    return {s, reciprocal(s)};
+    return {s, __frcp_rn(s)};
 }
-// y / s as a division rounds it: one product and two fma.
+// y / s as a division rounds it: one product and two fma (Markstein), s.inv being rounded.
 __device__ __forceinline__ float2 quotient(float2 y, const Scale &s) {
     const float2 q = __fmul2_rn(y, both(s.inv));
     return __ffma2_rn(__ffma2_rn(q, both(-s.s), y), both(s.inv), q);
@@ -228,7 +245,10 @@ struct Whole {
                 get4<float>(sv, e, v + 2 * j);
             }
 #pragma unroll
-            for (int i = 2 * j; i < 2 * j + 2; ++i) root[i] = update(st, f, g[i - 2 * j], p[i], m[i], v[i]);
+            for (int i = 2 * j; i < 2 * j + 2; ++i) {
+                root[i] = update(st, f, g[i - 2 * j], p[i], m[i], v[i]);
+                if (EIGHT) root[i] = rounded_root(root[i], v[i]);
+            }
         }
         if (EIGHT) __syncwarp();  // the slot has been read
 #pragma unroll
@@ -290,6 +310,7 @@ __device__ __forceinline__ void loose_row(const Step &st, const Factors &f, cons
             v[i] = make_float2(__uint_as_float(vr[2 * i]), __uint_as_float(vr[2 * i + 1]));
         }
         root[i] = update(st, f, g, p[i], m[i], v[i]);
+        if (EIGHT) root[i] = rounded_root(root[i], v[i]);
     }
     Scale sm = {0.f, 0.f}, sv = {0.f, 0.f};
     if (EIGHT) {
@@ -335,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? 4 : 2) adamw_kernel(const __
             if (blockIdx.x == 0 && threadIdx.x == 0 && st.err) atomicOr(st.err, kErrNonfinite);
             return;
         }
-        f.clip = fminf(1.f, __fdiv_rn(st.max_norm, norm + st.norm_eps));
+        f.clip = fminf(1.f, st.max_norm * __frcp_rn(norm + st.norm_eps));
     }
     const float lr = st.lr_at ? *st.lr_at : st.lr;
     float c1 = st.c1, root2 = st.root2;
@@ -529,6 +550,7 @@ extern "C" gdn_status gdn_adamw(const gdn_adamw_args *a, gdn_stream stream) {
     s.beta1 = (float)a->beta1, s.rest1 = (float)(1 - a->beta1);
     s.beta2 = (float)a->beta2, s.rest2 = (float)(1 - a->beta2);
     s.lr = (float)a->lr, s.weight_decay = (float)a->weight_decay, s.eps = (float)a->eps;
+    s.zero = -0.f;
     s.max_norm = (float)a->max_norm, s.norm_eps = (float)a->norm_eps;
     // beta = 0 has logarithm -inf, and 1 - beta^t = 1
     s.log_beta1 = (float)log(a->beta1), s.log_beta2 = (float)log(a->beta2);

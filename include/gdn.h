@@ -667,11 +667,13 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *args, void *workspace, size
  *
  * state_dtype F32 keeps m and v as they are.  E4M3 keeps m and r = sqrt(v) in blocks of
  * GDN_ADAMW_BLOCK elements of a tensor (the last may be short), each with an fp32 scale
- * s = max(largest |m| (r), 2^-100) / 448 in exp_avg_scales[i] (exp_avg_sq_scales[i]),
- * ceil(size / GDN_ADAMW_BLOCK) of them: the code is the quotient rounded to e4m3, and of
- * an r above zero at least the smallest, 2^-9, so that no step divides by the eps alone
- * where there was a gradient.  The step itself takes m and v before they are rounded.
- * Codes and scales of zero are states of zero.
+ * s = max(largest |m| (r), 2^-100) (1 / 448) in exp_avg_scales[i] (exp_avg_sq_scales[i]),
+ * ceil(size / GDN_ADAMW_BLOCK) of them: the code is the quotient by s rounded to e4m3, and
+ * of an r above zero at least the smallest, 2^-9, so that no step divides by the eps alone
+ * where there was a gradient.  Each product, sum, root and quotient on the way there is
+ * rounded to fp32 (k as max_norm times the reciprocal).  The step itself takes m and v
+ * before they are codes.  Codes and scales of zero are states of zero.  (A gradient that is
+ * infinite makes its block's states NaN; grad_norm keeps such a step from being taken.)
  *
  * step_device (or NULL) is the step's number in device memory, in place of `step`, and
  * lr_device the rate, in place of `lr`: a captured graph is replayed with new ones.  A
