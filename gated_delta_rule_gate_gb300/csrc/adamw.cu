@@ -120,7 +120,7 @@ __device__ __forceinline__ float2 mix(float a, float2 b, float c, float2 d, floa
 // v - s^2 an fma gives without error (Markstein 1990).  (With the rounded root of the library
 // 4.0e8 elements took 800 us in place of XX.)
 __device__ __forceinline__ float2 rounded_root(float2 s, float2 v) {
-    const float2 r = __ffma2_rn(make_float2(-s.x, -s.y), s, v);
+    const float2 r = __ffma2_rn(__fmul2_rn(both(-1.f), s), s, v);
     const float2 h = make_float2(reciprocal(fmaxf(s.x, 0x1p-80f)), reciprocal(fmaxf(s.y, 0x1p-80f)));
     return __ffma2_rn(r, __fmul2_rn(both(0.5f), h), s);
 }
