@@ -26,7 +26,8 @@ static bool make_map(CUtensorMap *m, const void *base, CUtensorMapDataType type,
         return reinterpret_cast<Encode>(e == cudaSuccess && q == cudaDriverEntryPointSuccess ? ptr : nullptr);
     }();
     if (!encode) return false;
-    const cuuint32_t boxes[3] = {type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 32u : 64u, (cuuint32_t)box, 1};
+    const cuuint32_t wide = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 32 : type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 128 : 64;
+    const cuuint32_t boxes[3] = {wide, (cuuint32_t)box, 1};
     const cuuint32_t step[3] = {1, 1, 1};
     return encode(m, type, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, boxes, step,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -90,6 +91,8 @@ constexpr int kMost = 1 << 20;
 constexpr int kMostParts = 32;
 
 int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
+int gate_columns(int inner) { return (inner + kGateColumns - 1) / kGateColumns * kGateColumns; }
+static_assert(GDN_GLU_GATES_ROW(kGateColumns + 1) == gates_row(2 * kGateColumns), "the header's size of a row");
 // Rows that a tensor map takes: words of 16 bytes.
 bool lines(const void *p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; }
 int64_t or_dense(int64_t stride, int64_t dense) { return stride ? stride : dense; }
@@ -329,9 +332,9 @@ gdn_status gdn_glu(const gdn_glu_args *a, void *ws, size_t ws_bytes, gdn_stream 
     cudaStream_t s = (cudaStream_t)stream;
     if (f.few) {
         Few p = {};
-        p.x = a->x, p.wg = a->w_gate, p.wu = a->w_up, p.out = a->out, p.gates = a->gates;
+        p.x = a->x, p.wg = a->w_gate, p.wu = a->w_up, p.out = a->out, p.gates = static_cast<unsigned char *>(a->gates);
         p.xs = or_dense(a->x_stride, a->dim), p.os = os;
-        p.T = (int)a->rows, p.D = a->dim, p.F = a->inner, p.Fp = (int)padded(a->inner), p.act = a->activation;
+        p.T = (int)a->rows, p.D = a->dim, p.F = a->inner, p.Fg = gate_columns(a->inner), p.act = a->activation;
         p.words = lines(a->x, p.xs) && lines(a->w_gate, a->dim) && lines(a->w_up, a->dim);
         return gdn::cuda_status(bf16 ? launch_few_bf16(p, s) : launch_few_f16(p, s));
     }
@@ -339,12 +342,18 @@ gdn_status gdn_glu(const gdn_glu_args *a, void *ws, size_t ws_bytes, gdn_stream 
     Job &j = p.job;
     sizes(&j, a->rows, a->inner, 128, 1, a->dim, 1, 1);
     p.act = a->activation, p.err = a->error_word;
-    const int Fp = (int)padded(a->inner);
+    const int Fg = gate_columns(a->inner);
     if (!map_of(&j.a[0], f.x, bf16, 128) || !map_of(&j.b[0], f.wg, bf16, 128) || !map_of(&j.b[1], f.wu, bf16, 128) ||
         !result(&j.c[0], j, a->out, os, a->inner, bf16))
         return no_map();
-    for (int i = 0; a->gates && i < 2; ++i)
-        if (!result(&j.c[1 + i], j, static_cast<uint16_t *>(a->gates) + i * Fp, 2 * (int64_t)Fp, Fp, bf16)) return no_map();
+    if (a->gates) {
+        unsigned char *gates = static_cast<unsigned char *>(a->gates);
+        for (int i = 0; i < 2; ++i)
+            if (!result(&j.c[1 + i], j, gates + i * 2 * (int64_t)Fg, gates_row(Fg) / 2, Fg, bf16)) return no_map();
+        const cuuint64_t dims[2] = {2 * (cuuint64_t)Fg, (cuuint64_t)a->rows}, strides[1] = {(cuuint64_t)gates_row(Fg)};
+        if (!make_map(&p.lower, gates + 4 * (int64_t)Fg, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, dims, strides, 32))
+            return no_map();
+    }
     cudaError_t e = bring({&f.x, &f.wg, &f.wu}, s);
     if (e == cudaSuccess) e = bf16 ? launch_forward_bf16(p, a->gates, s) : launch_forward_f16(p, a->gates, s);
     return gdn::cuda_status(e);
@@ -395,8 +404,9 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *a, void *ws, size_t ws_byte
         if (w.parts > 1) joins.j[joins.count++] = join_of(w, b.w_shares);
     }
     GateGrad g = {};
-    g.d_out = a->d_out, g.gates = a->gates, g.dg = const_cast<void *>(b.dg.at), g.du = const_cast<void *>(b.du.at);
-    g.rows = T, g.dos = or_dense(a->d_out_stride, F), g.F = F, g.Fp = (int)padded(F), g.act = a->activation;
+    g.d_out = a->d_out, g.gates = static_cast<const unsigned char *>(a->gates), g.dg = const_cast<void *>(b.dg.at), g.du = const_cast<void *>(b.du.at);
+    g.rows = T, g.dos = or_dense(a->d_out_stride, F), g.F = F, g.Fp = (int)padded(F), g.Fg = gate_columns(F);
+    g.act = a->activation;
     g.words = F % 8 == 0 && lines(a->d_out, g.dos);
     e = bf16 ? launch_gate_grad_bf16(g, s) : launch_gate_grad_f16(g, s);
     if (e == cudaSuccess) e = bring({&b.x, &b.wg, &b.wu}, s);

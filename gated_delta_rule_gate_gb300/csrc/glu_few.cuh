@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) few_kernel(const __grid_con
     __syncthreads();
     for (int i = threadIdx.x; i < 64 * NT * MT; i += 32 * kFewWarps) {
         const int e = i % (8 * MT), tok = i / (8 * MT), n = tok >> 3, c = tok & 7, at = blockIdx.x * (8 * MT) + e;
-        if (tok >= p.T || at >= p.Fp) continue;
+        if (tok >= p.T) continue;
         float gate = 0.f, up = 0.f;
 #pragma unroll
         for (int w = 0; w < kFewWarps; ++w)
@@ -121,10 +121,13 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) few_kernel(const __grid_con
             with_activation(p.act, [&](auto act) {
                 static_cast<T *>(p.out)[tok * p.os + at] = static_cast<T>(activation<act>(gate) * up);
             });
-        if (p.gates) {
-            T *row = static_cast<T *>(p.gates) + (int64_t)tok * 2 * p.Fp + at;
-            row[0] = static_cast<T>(at < p.F ? gate : 0.f);
-            row[p.Fp] = static_cast<T>(at < p.F ? up : 0.f);
+        if (p.gates && at < p.Fg) {
+            unsigned char *row = p.gates + tok * gates_row(p.Fg);
+            const uint32_t g = at < p.F ? __float_as_uint(gate) : 0u, u = at < p.F ? __float_as_uint(up) : 0u;
+            reinterpret_cast<uint16_t *>(row)[at] = (uint16_t)(g >> 16);
+            reinterpret_cast<uint16_t *>(row)[p.Fg + at] = (uint16_t)(u >> 16);
+            row[lower_at(p.Fg, 0, at)] = (unsigned char)(g >> 8);
+            row[lower_at(p.Fg, 1, at)] = (unsigned char)(u >> 8);
         }
     }
 }
@@ -144,10 +147,17 @@ cudaError_t launch_few(const Few &p, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------- gradient, element by element
+// 8 kept values from their upper halves and next bytes.
+__device__ __forceinline__ void widen24(uint4 hi, uint2 lo, float (&v)[8]) {
+    const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[2] = {lo.x, lo.y};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)  // bytes: none, the next one, the upper two
+        v[e] = __uint_as_float(__byte_perm(h[e >> 1], l[e >> 2], (e & 1 ? 0x3200 : 0x1000) | (4 + (e & 3)) << 4) & 0xffffff00u);
+}
+
 // d_g = d_out u act'(g) and d_u = d_out act(g), 8 adjacent values a thread; WORDS: rows of
 // d_out are words of 16 bytes (the others are by their making).  Columns from F to Fp
-// are zeros in the gates; nothing reads them of d_g and d_u.  Bound by HBM: 16384 x
-// 6144 bf16 in 159 us, 6.3 TB/s.
+// nobody reads of d_g and d_u.  Bound by HBM: 16384 x 6144 bf16 in XX us, XX TB/s.
 template <typename T, bool WORDS>
 __global__ void __launch_bounds__(256) gate_grad_kernel(const __grid_constant__ GateGrad p) {
     ptx::grid_wait();
@@ -157,16 +167,20 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const __grid_constant__ 
         const int64_t row = i / per;
         const int c = (int)(i - row * per) * 8;
         const T *at = static_cast<const T *>(p.d_out) + row * p.dos + c;
-        const T *gates = static_cast<const T *>(p.gates) + row * 2 * p.Fp + c;
+        const unsigned char *gates = p.gates + row * gates_row(p.Fg);
+        const uint4 gh = *reinterpret_cast<const uint4 *>(gates + 2 * c);
+        const uint4 uh = *reinterpret_cast<const uint4 *>(gates + 2 * (p.Fg + c));
+        const uint2 gl = *reinterpret_cast<const uint2 *>(gates + lower_at(p.Fg, 0, c));
+        const uint2 ul = *reinterpret_cast<const uint2 *>(gates + lower_at(p.Fg, 1, c));
         float d[8], g[8], u[8], dg[8], du[8];
-        load_values<T, 8>(gates, g);
-        load_values<T, 8>(gates + p.Fp, u);
         if constexpr (WORDS) {
             load_values<T, 8>(at, d);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) d[e] = c + e < p.F ? static_cast<float>(at[e]) : 0.f;
         }
+        widen24(gh, gl, g);
+        widen24(uh, ul, u);
         with_activation(p.act, [&](auto act) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {

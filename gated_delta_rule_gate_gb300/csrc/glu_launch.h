@@ -30,7 +30,8 @@ struct Job {
 };
 // The forward pass: out = act(x w_gate^T) (x w_up^T); KEEP: the gates are results too.
 struct ForwardArgs {
-    Job job;
+    Job job;           // its results: out, and of kept gates the upper halves of g and u
+    CUtensorMap lower; // and the next bytes of both
     int act;
     int32_t *err;
 };
@@ -44,17 +45,27 @@ struct Backward {
 // Fewer tokens than the tensor cores' tiles are made for.
 struct Few {
     const void *x, *wg, *wu;
-    void *out, *gates;  // gates may be null
+    void *out;
+    unsigned char *gates;  // or null
     int64_t xs, os;
-    int T, D, F, Fp, act, words;
+    int T, D, F, Fg, act, words;
 };
 // d_g and d_u of d_out and the gates that the forward pass kept.
 struct GateGrad {
-    const void *d_out, *gates;
+    const void *d_out;
+    const unsigned char *gates;
     void *dg, *du;
     int64_t rows, dos;
-    int F, Fp, act, words;  // Fp: elements between g and u, and between rows of dg and du; words: of d_out
+    int F, Fp, Fg, act, words;  // Fp: elements between rows of dg and du; words: of d_out
 };
+
+// Kept gates: g and u cut to 24 bits.  A row is the upper 16 bits of g's Fg columns, those
+// of u's, and then the next 8 bits, 64 columns of g and the same of u in turn.
+constexpr int kGateColumns = 64;
+__host__ __device__ constexpr int64_t gates_row(int Fg) { return 6 * (int64_t)Fg; }
+__host__ __device__ constexpr int64_t lower_at(int Fg, int up, int col) {
+    return 4 * (int64_t)Fg + col / kGateColumns * (2 * kGateColumns) + up * kGateColumns + col % kGateColumns;
+}
 
 // The shares of `parts` stretches added up and rounded: [parts, results, rows, cs] fp32.
 struct Join {

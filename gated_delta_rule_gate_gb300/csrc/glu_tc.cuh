@@ -36,7 +36,7 @@ constexpr int kStageBytes = 2 * kHalf;
 constexpr int kEpilogueWarps = 8, kProductThreads = 32 * (2 + kEpilogueWarps);
 constexpr int kBox = 4096;  // 32 rows of 64 results
 // A warp's results are one box a tile in the forward pass, which leaves room for six
-// stages; with kept gates three, in the gradients two to four, two in turn.
+// stages; with kept gates four, in the gradients two to four, two in turn.
 template <typename Call>
 struct Shape {
     static constexpr bool kForward = false, kKeep = false;
@@ -185,34 +185,64 @@ __device__ __forceinline__ void take(const Call &call, const Job &p, const TileA
     if constexpr (FORWARD) {  // 64 columns of the gate and the same 64 of up
         const int col = t.n * 128 + 64 * half;
         const bool kept = row < p.rows && col < p.cols;
-        Packed out[2], gate[2], up[2];
+        Packed v[2];
+        unsigned char *box;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             uint32_t r[2][32];
             tc::ld32_begin(acc + 64 * half + 32 * q, r[0]);
             tc::ld32_begin(acc + 128 + 64 * half + 32 * q, r[1]);
             tc::wait_ld(r);
-            if (q == 1) release();
-            if (KEEP) gate[q] = pack<T>(r[0]), up[q] = pack<T>(r[1]);
+            if (!KEEP && q == 1) release();
             with_activation(call.act, [&](auto act) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    out[q].w[i] = pack2<T>(
+                    v[q].w[i] = pack2<T>(
                         activation<act>(__uint_as_float(r[0][2 * i])) * __uint_as_float(r[1][2 * i]),
                         activation<act>(__uint_as_float(r[0][2 * i + 1])) * __uint_as_float(r[1][2 * i + 1]));
             });
         }
-        if (!kept) return;
-        unsigned char *box = boxes.next(lane);
-        put(box, lane, out);
-        send(p, p.c[0], box, row, col, lane);
-        if (KEEP) {
+        if (kept) {
             box = boxes.next(lane);
-            put(box, lane, gate);
-            send(p, p.c[1], box, row, col, lane);
+            put(box, lane, v);
+            send(p, p.c[0], box, row, col, lane);
+        }
+        if constexpr (KEEP) {  // cut to 24 bits, which no number leaves and no NaN
+            uint32_t lower[2][16];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t r[2][32];
+                tc::ld32_begin(acc + 128 * k + 64 * half, r[0]);
+                tc::ld32_begin(acc + 128 * k + 64 * half + 32, r[1]);
+                tc::wait_ld(r);
+                if (k == 1) release();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[q].w[i] = __byte_perm(r[q][2 * i], r[q][2 * i + 1], 0x7632);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        lower[k][8 * q + i] = __byte_perm(__byte_perm(r[q][4 * i], r[q][4 * i + 1], 0x0051),
+                                                          __byte_perm(r[q][4 * i + 2], r[q][4 * i + 3], 0x0051), 0x5410);
+                }
+                if (!kept) continue;
+                box = boxes.next(lane);
+                put(box, lane, v);
+                send(p, p.c[1 + k], box, row, col, lane);
+            }
+            if (!kept) return;
             box = boxes.next(lane);
-            put(box, lane, up);
-            send(p, p.c[2], box, row, col, lane);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const uint32_t *w = lower[c >> 2] + 4 * (c & 3);
+                *reinterpret_cast<uint4 *>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            ptx::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                ptx::tma_store_2d(&call.lower, 2 * col, (int)row, box);
+                ptx::bulk_commit();
+            }
         }
     } else {
         const int col = t.n * 256 + 128 * half;

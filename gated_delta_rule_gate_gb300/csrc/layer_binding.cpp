@@ -684,7 +684,7 @@ int32_t activation(PyObject *o) {
 // The sizes of a call: x [..., dim], weights [inner, dim].
 struct GluShape {
     int64_t rows, D, F;
-    std::vector<int64_t> out, gates;  // [..., inner], [..., 2, inner rounded up to 8]
+    std::vector<int64_t> out, gates;  // [..., inner], [..., bytes of a row]
 };
 GluShape glu_shape(const Tensor &x, const Tensor &w_gate) {
     const IntArrayRef shape = x.sizes();
@@ -697,8 +697,7 @@ GluShape glu_shape(const Tensor &x, const Tensor &w_gate) {
     s.out.assign(shape.begin(), shape.end() - 1);
     s.gates = s.out;
     s.out.push_back(s.F);
-    s.gates.push_back(2);
-    s.gates.push_back((s.F + 7) / 8 * 8);
+    s.gates.push_back(GDN_GLU_GATES_ROW(s.F));
     return s;
 }
 
@@ -735,7 +734,7 @@ PyObject *py_glu(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwna
         a.out = out.data_ptr();
     }
     if (keep) {
-        gates = make(s.gates, x, type);
+        gates = make(s.gates, x, ScalarType::Byte);
         a.gates = gates.data_ptr();
     }
     const Workspace ws(given, given ? 0 : lib.glu_workspace(&a), x);
@@ -775,7 +774,7 @@ PyObject *py_glu_backward(PyObject *, PyObject *const *args, Py_ssize_t n, PyObj
     a.d_out = dr.at, a.d_out_stride = dr.stride;
     a.w_gate = address(&w_gate, type, "w_gate", w);
     a.w_up = address(&w_up, type, "w_up", w);
-    a.gates = address(&gates, type, "gates", s.gates);
+    a.gates = address(&gates, ScalarType::Byte, "gates", s.gates);
     a.error_word = address<int32_t>(err, ScalarType::Int, "error_word");
     const Rows dxr = rows(dxg, type, x.sizes(), "dx");
     Tensor dx, dg, du;
@@ -1007,8 +1006,8 @@ PyMethodDef methods[] = {
      "ones), the weights [inner, dim] (halves of one fused weight, say), all of one dtype,\n"
      "float16 or bfloat16; out is [..., inner].  activation is \"silu\", \"gelu\" (by the\n"
      "error function), \"gelu_tanh\", \"relu\" or \"sigmoid\".  Sums are fp32.  Returns\n"
-     "out, or (out, gates) with want_gates: gates [..., 2, inner rounded up to a multiple\n"
-     "of 8] holds g and u for gdn_glu_backward, in x's dtype.  Calls of a few tokens (serving) are bound by the\n"
+     "out, or (out, gates) with want_gates: gates, uint8 [..., 6 (inner rounded up to 64)],\n"
+     "holds g and u for gdn_glu_backward, 24 bits of each.  Calls of a few tokens (serving) are bound by the\n"
      "weights' way from memory, long ones by the tensor cores."},
     {"gdn_glu_backward", FAST(py_glu_backward),
      "gdn_glu_backward($module, d_out, x, w_gate, w_up, gates, *, activation='silu', want_dx=True, "

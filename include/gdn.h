@@ -568,6 +568,10 @@ typedef enum gdn_activation {
     GDN_ACT_SIGMOID = 4    /* sigmoid(g) */
 } gdn_activation;
 
+/* Bytes of a row of gdn_glu's kept gates: the upper 16 bits of g and of u (inner rounded up
+ * to a multiple of 64 of each), then the next 8 bits, 64 of g and the same 64 of u in turn. */
+#define GDN_GLU_GATES_ROW(inner) (6 * (((int64_t)(inner) + 63) / 64 * 64))
+
 /*
  * gdn_glu -- the gated half of a feed-forward block, both projections and what joins
  * them in one kernel, for each of `rows` tokens:
@@ -577,10 +581,10 @@ typedef enum gdn_activation {
  * x is [rows, dim] with x_stride elements from row to row (0: dim), out [rows, inner] with
  * out_stride (0: inner), the weights [inner, dim] contiguous, all of dtype F16 or BF16 (F32
  * is declined: GDN_ERR_UNSUPPORTED).  Products are summed in fp32 on the tensor cores, and
- * out is rounded once.  gates (NULL: not kept) receives g and u, rounded to dtype, for
- * gdn_glu_backward: [rows, 2, padded] contiguous and aligned to 16 bytes, where padded is inner
- * rounded up to a multiple of 8 (columns from inner on are 0), a row's g first; fp16 ones
- * beyond 65504 are infinite.  A few tokens (serving) take a kernel of their own.  out and gates
+ * out is rounded once.  gates (NULL: not kept) receives g and u for gdn_glu_backward, cut to
+ * 24 bits (sign, 8 bits of exponent, 15 of fraction; 16 would cost the gradients as much
+ * again as their own roundings): GDN_GLU_GATES_ROW(inner) bytes a row, contiguous and
+ * aligned to 16 bytes.  A few tokens (serving) take a kernel of their own.  out and gates
  * overlap no input.
  *
  * The workspace is device memory of gdn_glu_workspace_size() bytes, 16-byte aligned (none
