@@ -5,7 +5,7 @@
 // 128 of the tile's rows in its tensor memory and half of either operand in its shared
 // memory, so that a K-step of 64 takes 32 KB of each block for 16.8 MFLOP: half the
 // operand bytes of two single blocks.  Persistent; per block a warp that loads
-// (TMA, five or six stages), a warp whose first thread issues the products (in the pair's first
+// (TMA, six stages), a warp whose first thread issues the products (in the pair's first
 // block) and eight warps that take the finished accumulators (two of them, so that the
 // next tile's products run meanwhile) out of tensor memory.
 //
@@ -35,25 +35,22 @@ constexpr int kHalf = 16384;  // bytes of a block's share of an operand's stage
 constexpr int kStageBytes = 2 * kHalf;
 constexpr int kEpilogueWarps = 8, kProductThreads = 32 * (2 + kEpilogueWarps);
 constexpr int kBox = 4096;  // 32 rows of 64 results
-// A warp's results are one box a tile in the forward pass, which leaves room for six
-// stages; with kept gates four, in the gradients two to four, two in turn.
+// Six stages leave each of these warps one box, which is what a tile needs: with two, and
+// five stages, 16384 x 2048 x 6144 with kept gates took 486 us in place of 471.
+constexpr int kStages = 6;
+constexpr int kProductSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kBox + 256;
 template <typename Call>
 struct Shape {
     static constexpr bool kForward = false, kKeep = false;
-    static constexpr int kBoxes = 2, kStages = 5;
 };
 template <bool KEEP>
 struct Shape<Forward<KEEP>> {
     static constexpr bool kForward = true, kKeep = KEEP;
-    static constexpr int kBoxes = KEEP ? 2 : 1, kStages = KEEP ? 5 : 6;
 };
-template <typename Call>
-constexpr int kProductSmem = 1024 + Shape<Call>::kStages * kStageBytes + kEpilogueWarps * Shape<Call>::kBoxes * kBox + 256;
 constexpr int kGroup = 8;  // tiles along the rows that are taken side by side
 
-template <int STAGES>
 struct Barriers {
-    uint64_t full[STAGES], empty[STAGES], done[2], taken[2];
+    uint64_t full[kStages], empty[kStages], done[2], taken[2];
     uint32_t tmem;
 };
 
@@ -148,20 +145,11 @@ __device__ __forceinline__ void send(const Job &p, const Result &c, const unsign
     }
     __syncwarp();
 }
-// A warp's boxes, in turn; the one that is filled next has been read by its store.
-template <int N>
-struct Boxes {
-    unsigned char *base;
-    int turn;
-    __device__ __forceinline__ unsigned char *next(int lane) {
-        if (lane == 0) {
-            if (N == 1) ptx::bulk_wait_read();
-            else ptx::bulk_wait_read_all_but_last();
-        }
-        __syncwarp();
-        return N == 1 ? base : base + (turn ^= 1) * kBox;
-    }
-};
+// Before a warp's box is filled anew: its store has read it.
+__device__ __forceinline__ void reuse(int lane) {
+    if (lane == 0) ptx::bulk_wait_read();
+    __syncwarp();
+}
 
 // 32 fp32 columns of a lane's row: a share of a result that is summed over stretches of K.
 __device__ __forceinline__ void put_share(unsigned char *box, int lane, const uint32_t (&r)[32]) {
@@ -175,7 +163,7 @@ __device__ __forceinline__ void put_share(unsigned char *box, int lane, const ui
 // after which it is free for the next tile but one, and sent to their results.
 template <typename T, typename Call>
 __device__ __forceinline__ void take(const Call &call, const Job &p, const TileAt &t, uint32_t acc, uint32_t taken,
-                                     int64_t row, Boxes<Shape<Call>::kBoxes> &boxes, int half, int lane) {
+                                     int64_t row, unsigned char *box, int half, int lane) {
     constexpr bool FORWARD = Shape<Call>::kForward, KEEP = Shape<Call>::kKeep;
     auto release = [&] {
         tc::fence_before();
@@ -186,7 +174,6 @@ __device__ __forceinline__ void take(const Call &call, const Job &p, const TileA
         const int col = t.n * 128 + 64 * half;
         const bool kept = row < p.rows && col < p.cols;
         Packed v[2];
-        unsigned char *box;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             uint32_t r[2][32];
@@ -203,7 +190,7 @@ __device__ __forceinline__ void take(const Call &call, const Job &p, const TileA
             });
         }
         if (kept) {
-            box = boxes.next(lane);
+            reuse(lane);
             put(box, lane, v);
             send(p, p.c[0], box, row, col, lane);
         }
@@ -226,12 +213,12 @@ __device__ __forceinline__ void take(const Call &call, const Job &p, const TileA
                                                           __byte_perm(r[q][4 * i + 2], r[q][4 * i + 3], 0x0051), 0x5410);
                 }
                 if (!kept) continue;
-                box = boxes.next(lane);
+                reuse(lane);
                 put(box, lane, v);
                 send(p, p.c[1 + k], box, row, col, lane);
             }
             if (!kept) return;
-            box = boxes.next(lane);
+            reuse(lane);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const uint32_t *w = lower[c >> 2] + 4 * (c & 3);
@@ -256,7 +243,7 @@ __device__ __forceinline__ void take(const Call &call, const Job &p, const TileA
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
                 if (col + 32 * h >= p.cols) return;
-                unsigned char *box = boxes.next(lane);
+                reuse(lane);
                 put_share(box, lane, r[h]);
                 ptx::fence_async_smem();
                 __syncwarp();
@@ -270,7 +257,7 @@ __device__ __forceinline__ void take(const Call &call, const Job &p, const TileA
             for (int h = 0; h < 2; ++h) {
                 if (col + 64 * h >= p.cols) return;
                 const Packed v[2] = {pack<T>(r[2 * h]), pack<T>(r[2 * h + 1])};
-                unsigned char *box = boxes.next(lane);
+                reuse(lane);
                 put(box, lane, v);
                 send(p, p.c[t.z], box, row, col + 64 * h, lane);
             }
@@ -283,10 +270,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     product_kernel(const __grid_constant__ Call p) {
     extern __shared__ unsigned char raw[];
     constexpr bool FORWARD = Shape<Call>::kForward;
-    constexpr int kStages = Shape<Call>::kStages, kBoxes = Shape<Call>::kBoxes;
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     unsigned char *boxes = sm + kStages * kStageBytes;
-    Barriers<kStages> &bar = *reinterpret_cast<Barriers<kStages> *>(boxes + kEpilogueWarps * kBoxes * kBox);
+    Barriers &bar = *reinterpret_cast<Barriers *>(boxes + kEpilogueWarps * kBox);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -398,7 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         }
     } else {
         const int quarter = warp & 3;  // of the tensor memory's lanes, by the warp's number
-        Boxes<kBoxes> mine = {boxes + (warp - 2) * kBoxes * kBox, 0};
+        unsigned char *mine = boxes + (warp - 2) * kBox;
         uint32_t turn = 0;
         const uint32_t taken[2] = {ptx::cluster_address(&bar.taken[0], 0), ptx::cluster_address(&bar.taken[1], 0)};
         for (uint32_t i = first; i < tiles; i += step, ++turn) {
@@ -428,11 +414,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 template <typename T, typename Call>
 cudaError_t launch_product(const Call &p, cudaStream_t stream) {
     const auto kernel = product_kernel<T, Call>;
-    constexpr int smem = kProductSmem<Call>;
-    const cudaError_t e = smem_attr((const void *)kernel, smem);
+    const cudaError_t e = smem_attr((const void *)kernel, kProductSmem);
     if (e != cudaSuccess) return e;
     const uint32_t tiles = tiles_of(p), pairs = (uint32_t)sm_count() / 2;
-    return launch_early(kernel, 2 * (tiles < pairs ? tiles : pairs), kProductThreads, smem, stream, p);
+    return launch_early(kernel, 2 * (tiles < pairs ? tiles : pairs), kProductThreads, kProductSmem, stream, p);
 }
 
 template <typename T>
