@@ -390,6 +390,28 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? 4 : 2) adamw_kernel(const __
         to = to + 1 == N ? 0 : to + 1;
     };
     if constexpr (EIGHT) {
+        const Tensor t = tab.t[i];
+        if (row < stop && whole_row(t, stop - 1 - t.first)) {  // a stretch of one tensor's whole rows
+            const int rows = (int)((stop - row + kWarps - 1) / kWarps);
+            const int64_t r0 = row - t.first;
+#pragma unroll 1
+            for (int k = 0; k < N - 1; ++k) {
+                if (k < rows) Rows::load(mine + k * Rows::kBytes, t, r0 + k * kWarps, lane);
+                ptx::cp_async_commit();
+            }
+            to = N - 1;
+#pragma unroll 1
+            for (int k = 0; k < rows; ++k) {
+                if (k + N - 1 < rows) Rows::load(mine + to * Rows::kBytes, t, r0 + (k + N - 1) * kWarps, lane);
+                ptx::cp_async_commit();
+                ptx::cp_async_wait<N - 1>();
+                __syncwarp();
+                Rows::step(mine + at * Rows::kBytes, st, f, t, r0 + k * kWarps, lane);
+                at = at + 1 == N ? 0 : at + 1;
+                to = to + 1 == N ? 0 : to + 1;
+            }
+            return;
+        }
 #pragma unroll 1
         for (int k = 0; k < N - 1; ++k) request();
     }
