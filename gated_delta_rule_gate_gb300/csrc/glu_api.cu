@@ -196,9 +196,10 @@ cudaError_t bring(std::initializer_list<const Operand *> operands, cudaStream_t 
 bool map_of(CUtensorMap *m, const Operand &o, bool bf16, int box) {
     return make_map(m, o.at, bf16, o.stride, o.cols, o.rows, box);
 }
-// A result of job.rows rows, by tensor map where its rows are words of 16 bytes.
+// A result of job.rows rows, by tensor map where its rows are words of 16 bytes and end with
+// one: a store that is cut inside a word writes all of it.  (A load is cut where it should be.)
 bool result(Result *r, const Job &job, void *at, int64_t stride, int cols, bool bf16) {
-    r->at = at, r->stride = stride, r->by_map = lines(at, stride);
+    r->at = at, r->stride = stride, r->by_map = lines(at, stride) && cols % 8 == 0;
     return !r->by_map || make_map(&r->map, at, bf16, stride, cols, job.rows, 32);
 }
 // `results` results of rows x cols in tiles of 256 x width, sums over `pairs` pairs of operands with

@@ -218,6 +218,26 @@ def test_columns_of_wider_tensors(T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [7, 150])
+def test_rows_that_end_inside_a_word(T):
+    """Widths that are no multiple of 8 in rows that are whole words apart: what is behind a row
+    in its last word (NaN) has no say, and is left alone."""
+    import gated_delta_rule_gate_gb300 as gdn
+    for D, F in ((85, 131), (1, 7), (62, 260)):
+        x, wg, wu, d = draw(T, D, F, "f16", seed=D)
+        nan = lambda n: torch.full((T, -(-n // 8) * 8 + 8), float("nan"), dtype=x.dtype, device="cuda")
+        xw, dw, ow, dxw = nan(D), nan(F), nan(F), nan(D)
+        xw[:, :D], dw[:, :F] = x, d
+        out, gates = gdn.gdn_glu(x, wg, wu, want_gates=True)
+        o, gates2 = gdn.gdn_glu(xw[:, :D], wg, wu, out=ow[:, :F], want_gates=True)
+        assert torch.equal(o, out) and torch.equal(unpack(gates, F), unpack(gates2, F))
+        want = gdn.gdn_glu_backward(d, x, wg, wu, gates)
+        got = gdn.gdn_glu_backward(dw[:, :F], xw[:, :D], wg, wu, gates, dx=dxw[:, :D])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert bool(ow[:, F:].isnan().all()) and bool(dxw[:, D:].isnan().all())
+
+
+@pytest.mark.gpu
 def test_weights_in_one_tensor_and_at_odd_addresses():
     import gated_delta_rule_gate_gb300 as gdn
     for T in (4, 60):
