@@ -6,9 +6,8 @@
 // 16-bit and 8-bit values a whole word over adjacent lanes; a row is also the block of
 // 8-bit states that shares its scales, so that the largest of a block is a maximum over
 // one warp.  Everything is read once and written once.  Bound by HBM: 4.0e8 bf16 elements
-// with fp32 copies and states (28 bytes each) 1639 us, 6.9 TB/s; with 8-bit states (10 bytes
-// each) 790 us, 5.1 TB/s, where issuing 44 instructions an element takes 470 us and
-// the waits of 24 warps an SM are not all hidden.
+// with fp32 copies and states (28 bytes each) 1636 us, 6.9 TB/s; with 8-bit states (10 bytes
+// each) 676 us, 6.0 TB/s, where the 52 instructions of an element fill 78 % of the issue slots.
 #include <math.h>
 
 #include <cuda_fp8.h>
@@ -117,8 +116,8 @@ __device__ __forceinline__ float2 mix(float a, float2 b, float c, float2 d, floa
     return __fadd2_rn(__ffma2_rn(both(a), b, both(zero)), __ffma2_rn(both(c), d, both(zero)));
 }
 // A root that is up to 2 ulp off, rounded: one step of Newton's method, whose residual
-// v - s^2 an fma gives without error (Markstein 1990).  (With the rounded root of the library
-// 4.0e8 elements took 800 us in place of XX.)
+// v - s^2 an fma gives without error (Markstein 1990).  2^26 bf16 elements with 8-bit states take
+// 116 us so, and 124 with __fsqrt_rn.
 __device__ __forceinline__ float2 rounded_root(float2 s, float2 v) {
     const float2 r = __ffma2_rn(__fmul2_rn(both(-1.f), s), s, v);
     const float2 h = make_float2(reciprocal(fmaxf(s.x, 0x1p-80f)), reciprocal(fmaxf(s.y, 0x1p-80f)));
@@ -180,9 +179,10 @@ __device__ __forceinline__ void put4(void *base, int64_t at, const float2 *v) {
     store_values<T, 4>(static_cast<T *>(base) + at, f);
 }
 
-// Whole rows of 256 elements come through shared memory (cp.async), several on their way
-// a warp, without a register: with the next row in registers 2^26 bf16 elements with
-// 8-bit states took 171 us, for 128 (three rows on their way: 181).  A lane has elements 4 lane + 128 j ... + 3.
+// A whole row of 256 elements; a lane has elements 4 lane + 128 j ... + 3.  With 8-bit states rows
+// come through shared memory (cp.async), several on their way a warp without a register:
+// 2^26 bf16 elements take 174, 137, 116 us with two, three, four of them (and took half as
+// much again with the next row in registers).
 // P, G: the types of parameters and gradients; MASTER: there are fp32 copies.
 template <bool EIGHT, typename P, bool MASTER, typename G>
 struct Whole {
@@ -340,9 +340,9 @@ __device__ __forceinline__ void loose_row(const Step &st, const Factors &f, cons
 
 __device__ __forceinline__ bool whole_row(const Tensor &t, int64_t row) { return t.whole && (row + 1) * kRow <= t.n; }
 
-// A block has a stretch of adjacent rows, which its warps take in turn, and the device
-// as many blocks as there are stretches: SMs are not equally fast (equal shares of a
-// persistent grid: 235 us in place of 218 for 2^26 bf16 elements with fp32 states).
+// A block has a stretch of adjacent rows, which its warps take in turn, and there are as
+// many blocks as stretches: SMs are not equally fast (equal shares of a persistent grid took
+// 235 us in place of 218 for 2^26 bf16 elements with fp32 states).
 template <bool EIGHT, typename P, bool MASTER, typename G, int MAX>
 __global__ void __launch_bounds__(kThreads, EIGHT ? 4 : 2) adamw_kernel(const __grid_constant__ Table<MAX> tab,
                                                                         const __grid_constant__ Step st) {
@@ -391,7 +391,8 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? 4 : 2) adamw_kernel(const __
     };
     if constexpr (EIGHT) {
         const Tensor t = tab.t[i];
-        if (row < stop && whole_row(t, stop - 1 - t.first)) {  // a stretch of one tensor's whole rows
+        if (row < stop && whole_row(t, stop - 1 - t.first)) {
+            // a stretch of one tensor's whole rows, its addresses kept (looked up for each row: 140 us for 116)
             const int rows = (int)((stop - row + kWarps - 1) / kWarps);
             const int64_t r0 = row - t.first;
 #pragma unroll 1
