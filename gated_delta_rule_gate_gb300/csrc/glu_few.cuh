@@ -141,10 +141,11 @@ cudaError_t launch_few_of(const Few &p, cudaStream_t stream) {
 }
 template <typename T>
 cudaError_t launch_few(const Few &p, cudaStream_t stream) {
-    static_assert(kFewTokens == 16, "groups of 8 tokens");
+    static_assert(kFewTokens == 32, "groups of 8 tokens");
     const bool narrow = p.F <= 16 * sm_count();
     if (p.T <= 8) return narrow ? launch_few_of<T, 1, 1>(p, stream) : launch_few_of<T, 1, 2>(p, stream);
-    return narrow ? launch_few_of<T, 2, 1>(p, stream) : launch_few_of<T, 2, 2>(p, stream);
+    if (p.T <= 16) return narrow ? launch_few_of<T, 2, 1>(p, stream) : launch_few_of<T, 2, 2>(p, stream);
+    return narrow ? launch_few_of<T, 4, 1>(p, stream) : launch_few_of<T, 4, 2>(p, stream);
 }
 
 // ---------------------------------------------------------------- gradient, element by element

@@ -79,7 +79,7 @@ struct Joins {
     int count;
 };
 
-constexpr int kFewTokens = 16;
+constexpr int kFewTokens = 32;
 
 cudaError_t launch_forward_f16(const ForwardArgs &p, bool keep, cudaStream_t stream);
 cudaError_t launch_forward_bf16(const ForwardArgs &p, bool keep, cudaStream_t stream);

@@ -3,8 +3,8 @@
 //
 // A pair of blocks on two SMs works on one tile of 256 x 256 (cta_group::2): each has
 // 128 of the tile's rows in its tensor memory and half of either operand in its shared
-// memory, so that a K-step of 64 takes 32 KB of each block for 16.8 MFLOP: half the
-// operand bytes of two single blocks.  Persistent; per block a warp that loads
+// memory, so that a K-step of 64 takes 32 KB of each block (of single blocks on 128 x 256
+// 48).  Persistent; per block a warp that loads
 // (TMA, six stages), a warp whose first thread issues the products (in the pair's first
 // block) and eight warps that take the finished accumulators (two of them, so that the
 // next tile's products run meanwhile) out of tensor memory.
