@@ -211,7 +211,7 @@ void sizes(Job *j, int64_t rows, int cols, int width, int results, int64_t depth
     j->per_part = (pairs * j->blocks_k + parts - 1) / parts;
     j->tiles = (uint32_t)j->tiles_m * (uint32_t)j->tiles_n * (uint32_t)(results * parts);
 }
-// The stretches that K of the gradients' results is cut into: those that make the device's
+// The stretches that K of results is cut into: those that make the device's
 // time least, in K-steps (0.27 us) of a pair of blocks.  A tile costs some six steps beside its
 // own; shares are written and read in fp32, and a launch is added.  Pairs of blocks take
 // tiles in turn, the first job's first, so the longest time is that of the first pair, or of
@@ -264,6 +264,8 @@ gdn_status no_map() { return fail(GDN_ERR_CUDA, "a tensor map could not be made"
 struct ForwardPlan {
     bool few;
     Operand x, wg, wu;
+    int parts;
+    void *shares;
     size_t bytes;
 };
 ForwardPlan plan(const gdn_glu_args *a, void *ws) {
@@ -274,6 +276,13 @@ ForwardPlan plan(const gdn_glu_args *a, void *ws) {
     f.x = operand(a->x, a->rows, a->dim, or_dense(a->x_stride, a->dim), &pieces);
     f.wg = operand(a->w_gate, a->inner, a->dim, a->dim, &pieces);
     f.wu = operand(a->w_up, a->inner, a->dim, a->dim, &pieces);
+    Cut cut;
+    cut.tiles = (a->rows + 255) / 256 * ((a->inner + 127) / 128);
+    cut.steps = (a->dim + 63) / 64;
+    cut.values = 2.0 * (double)a->rows * padded(a->inner);
+    int none;
+    choose_parts(cut, Cut(), &f.parts, &none);
+    f.shares = pieces.take(f.parts > 1 ? 4 * a->rows * padded(a->inner) * f.parts : 0);
     f.bytes = pieces.used;
     return f;
 }
@@ -341,7 +350,7 @@ gdn_status gdn_glu(const gdn_glu_args *a, void *ws, size_t ws_bytes, gdn_stream 
     }
     ForwardArgs p = {};
     Job &j = p.job;
-    sizes(&j, a->rows, a->inner, 128, 1, a->dim, 1, 1);
+    sizes(&j, a->rows, a->inner, 128, 1, a->dim, 1, f.parts);
     p.act = a->activation, p.err = a->error_word;
     const int Fg = gate_columns(a->inner);
     if (!map_of(&j.a[0], f.x, bf16, 128) || !map_of(&j.b[0], f.wg, bf16, 128) || !map_of(&j.b[1], f.wu, bf16, 128) ||
@@ -355,8 +364,17 @@ gdn_status gdn_glu(const gdn_glu_args *a, void *ws, size_t ws_bytes, gdn_stream 
         if (!make_map(&p.lower, gates + 4 * (int64_t)Fg, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, dims, strides, 32))
             return no_map();
     }
+    if (j.parts > 1 && !make_share_map(&j.shares, f.shares, padded(a->inner), a->rows, 2 * j.parts)) return no_map();
     cudaError_t e = bring({&f.x, &f.wg, &f.wu}, s);
     if (e == cudaSuccess) e = bf16 ? launch_forward_bf16(p, a->gates, s) : launch_forward_f16(p, a->gates, s);
+    if (e == cudaSuccess && j.parts > 1) {
+        ForwardJoin q = {};
+        q.shares = static_cast<const float *>(f.shares), q.out = a->out, q.gates = static_cast<unsigned char *>(a->gates);
+        q.rows = a->rows, q.os = os, q.F = a->inner, q.cs = (int)padded(a->inner), q.Fg = Fg;
+        q.parts = j.parts, q.act = a->activation;
+        q.words = a->inner % 4 == 0 && os % 4 == 0 && aligned(a->out, 8);
+        e = bf16 ? launch_forward_join_bf16(q, s) : launch_forward_join_f16(q, s);
+    }
     return gdn::cuda_status(e);
 }
 

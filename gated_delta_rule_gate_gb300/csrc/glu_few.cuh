@@ -246,5 +246,57 @@ cudaError_t launch_join(const Joins &p, cudaStream_t stream) {
     return launch_early(join_kernel<T>, (unsigned)(blocks < most ? blocks : most), 256, 0, stream, p);
 }
 
+// The same of the forward pass: g and u of four columns, then what the product's kernel
+// makes of them.
+template <typename T>
+__global__ void __launch_bounds__(256) forward_join_kernel(const __grid_constant__ ForwardJoin p) {
+    ptx::grid_wait();
+    const int per = p.cs / 4;
+    const int64_t plane = p.rows * p.cs, n = p.rows * per;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / per;
+        const int c = (int)(i - row * per) * 4;
+        float4 g = {}, u = {};
+#pragma unroll 4
+        for (int k = 0; k < p.parts; ++k) {
+            const float *at = p.shares + 2 * k * plane + row * p.cs + c;
+            const float4 a = *reinterpret_cast<const float4 *>(at), b = *reinterpret_cast<const float4 *>(at + plane);
+            g.x += a.x, g.y += a.y, g.z += a.z, g.w += a.w;
+            u.x += b.x, u.y += b.y, u.z += b.z, u.w += b.w;
+        }
+        const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
+        float v[4];
+        with_activation(p.act, [&](auto act) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = activation<act>(gs[e]) * us[e];
+        });
+        T *to = static_cast<T *>(p.out) + row * p.os + c;
+        if (p.words) {
+            if (c < p.F) store_values<T, 4>(to, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < p.F) to[e] = static_cast<T>(v[e]);
+        }
+        if (!p.gates) continue;
+        unsigned char *gates = p.gates + row * gates_row(p.Fg);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(k ? us[e] : gs[e]);
+            *reinterpret_cast<uint2 *>(gates + 2 * (k * p.Fg + c)) =
+                make_uint2(__byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632));
+            *reinterpret_cast<uint32_t *>(gates + lower_at(p.Fg, k, c)) =
+                __byte_perm(__byte_perm(w[0], w[1], 0x0051), __byte_perm(w[2], w[3], 0x0051), 0x5410);
+        }
+    }
+}
+template <typename T>
+cudaError_t launch_forward_join(const ForwardJoin &p, cudaStream_t stream) {
+    const int64_t blocks = (p.rows * (p.cs / 4) + 255) / 256, most = (int64_t)sm_count() * 16;
+    return launch_early(forward_join_kernel<T>, (unsigned)(blocks < most ? blocks : most), 256, 0, stream, p);
+}
+
 }  // namespace glu
 }  // namespace gdn

@@ -19,7 +19,7 @@ struct Result {
 // (result z's are a[z + i], b[i] of pair i).  Tiles of 256 x 256, of 256 x 128 of the forward pass.
 struct Job {
     CUtensorMap a[2], b[2];
-    CUtensorMap shares;  // fp32 [parts x results, rows, cols], where parts > 1
+    CUtensorMap shares;  // fp32 [parts x results (g and u of the forward pass), rows, cols], where parts > 1
     Result c[3];
     int64_t rows;
     uint32_t tiles;                 // of all results and stretches
@@ -28,7 +28,8 @@ struct Job {
     int parts, per_part;            // stretches of K, and theirs
     int a_outer;                    // A has K as its outer dimension
 };
-// The forward pass: out = act(x w_gate^T) (x w_up^T); KEEP: the gates are results too.
+// The forward pass: out = act(x w_gate^T) (x w_up^T); KEEP: the gates are results too;
+// Shares: g and u of stretches of K are the results.
 struct ForwardArgs {
     Job job;           // its results: out, and of kept gates the upper halves of g and u
     CUtensorMap lower; // and the next bytes of both
@@ -37,6 +38,7 @@ struct ForwardArgs {
 };
 template <bool KEEP>
 struct Forward : ForwardArgs {};
+struct ForwardShares : ForwardArgs {};
 // The gradients: dx = d_g w_gate + d_u w_up, and d_w = d^T x of both weights, in one launch.
 struct Backward {
     Job job[2];
@@ -78,6 +80,14 @@ struct Joins {
     Join j[2];
     int count;
 };
+// Those of the forward pass, [parts, g and u, rows, cs], joined before the activation.
+struct ForwardJoin {
+    const float *shares;
+    void *out;
+    unsigned char *gates;  // or null
+    int64_t rows, os;
+    int F, cs, Fg, parts, act, words;  // words: groups of four outputs are
+};
 
 constexpr int kFewTokens = 32;
 
@@ -91,6 +101,8 @@ cudaError_t launch_gate_grad_f16(const GateGrad &p, cudaStream_t stream);
 cudaError_t launch_gate_grad_bf16(const GateGrad &p, cudaStream_t stream);
 cudaError_t launch_join_f16(const Joins &p, cudaStream_t stream);
 cudaError_t launch_join_bf16(const Joins &p, cudaStream_t stream);
+cudaError_t launch_forward_join_f16(const ForwardJoin &p, cudaStream_t stream);
+cudaError_t launch_forward_join_bf16(const ForwardJoin &p, cudaStream_t stream);
 
 }  // namespace glu
 }  // namespace gdn

@@ -46,11 +46,15 @@ constexpr int kStages = 6;
 constexpr int kProductSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kBox + 256;
 template <typename Call>
 struct Shape {
-    static constexpr bool kForward = false, kKeep = false;
+    static constexpr bool kForward = false, kKeep = false, kShares = false;
 };
 template <bool KEEP>
 struct Shape<Forward<KEEP>> {
-    static constexpr bool kForward = true, kKeep = KEEP;
+    static constexpr bool kForward = true, kKeep = KEEP, kShares = false;
+};
+template <>
+struct Shape<ForwardShares> {
+    static constexpr bool kForward = true, kKeep = false, kShares = true;
 };
 constexpr int kGroup = 8;  // tiles along the rows that are taken side by side
 
@@ -164,6 +168,18 @@ __device__ __forceinline__ void put_share(unsigned char *box, int lane, const ui
             make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
 }
 
+__device__ __forceinline__ void send_share(const Job &p, const uint32_t (&r)[32], unsigned char *box, int64_t row,
+                                           int col, int plane, int lane) {
+    reuse(lane);
+    put_share(box, lane, r);
+    ptx::fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        ptx::tma_store_3d(&p.shares, col, (int)row, plane, box);
+        ptx::bulk_commit();
+    }
+}
+
 // An accumulator's 128 columns of one of two groups of warps, `half`: taken into registers,
 // after which it is free for the next tile but one, and sent to their results.
 template <typename T, typename Call>
@@ -175,7 +191,18 @@ __device__ __forceinline__ void take(const Call &call, const Job &p, const TileA
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_cluster(taken);
     };
-    if constexpr (FORWARD) {  // 64 columns of the gate and the same 64 of up
+    if constexpr (Shape<Call>::kShares) {  // 64 columns of the gate and the same of up, not yet joined
+        const int col = t.n * 128 + 64 * half;
+        uint32_t r[4][32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc::ld32_begin(acc + 128 * (k >> 1) + 64 * half + 32 * (k & 1), r[k]);
+        tc::wait_ld(r);
+        release();
+        if (row >= p.rows) return;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (col + 32 * (k & 1) < p.cols) send_share(p, r[k], box, row, col + 32 * (k & 1), 2 * t.part + (k >> 1), lane);
+    } else if constexpr (FORWARD) {  // 64 columns of the gate and the same 64 of up
         const int col = t.n * 128 + 64 * half;
         const bool kept = row < p.rows && col < p.cols;
         Packed v[2];
@@ -248,14 +275,7 @@ __device__ __forceinline__ void take(const Call &call, const Job &p, const TileA
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
                 if (col + 32 * h >= p.cols) return;
-                reuse(lane);
-                put_share(box, lane, r[h]);
-                ptx::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    ptx::tma_store_3d(&p.shares, col + 32 * h, (int)row, t.part * p.results + t.z, box);
-                    ptx::bulk_commit();
-                }
+                send_share(p, r[h], box, row, col + 32 * h, t.part * p.results + t.z, lane);
             }
         } else {
 #pragma unroll
@@ -427,6 +447,7 @@ cudaError_t launch_product(const Call &p, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t launch_forward(const ForwardArgs &p, bool keep, cudaStream_t stream) {
+    if (p.job.parts > 1) return launch_product<T>(ForwardShares{p}, stream);
     return keep ? launch_product<T>(Forward<true>{p}, stream) : launch_product<T>(Forward<false>{p}, stream);
 }
 

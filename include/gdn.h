@@ -587,9 +587,9 @@ typedef enum gdn_activation {
  * aligned to 16 bytes.  A few tokens (serving) take a kernel of their own.  out and gates
  * overlap no input.
  *
- * The workspace is device memory of gdn_glu_workspace_size() bytes, 16-byte aligned (none
- * is needed where rows of x and of the weights are whole words of 16 bytes); its contents
- * are scratch.  dim and inner are at most 2^20.
+ * The workspace is device memory of gdn_glu_workspace_size() bytes, 16-byte aligned (for
+ * operands whose rows are no words of 16 bytes, and for shares of results where they are few);
+ * its contents are scratch.  dim and inner are at most 2^20.
  */
 typedef struct gdn_glu_args {
     int64_t rows;

@@ -118,7 +118,8 @@ def check_backward(got, want, dt):
 # rows, dim, inner: few tokens and many, one tile and several, whole words and odd widths
 SHAPES = [(1, 64, 8), (1, 1, 1), (1, 2048, 96), (3, 517, 1001), (8, 96, 40), (9, 40, 24), (16, 200, 130), (16, 2051, 17),
           (17, 64, 128), (17, 65, 1), (100, 1, 3), (129, 72, 136), (256, 64, 128), (257, 520, 264), (300, 1000, 700),
-          (1001, 517, 1531), (513, 128, 8), (40, 8, 520), (2049, 192, 1288), (700, 12, 600), (90, 20, 4000)]
+          (1001, 517, 1531), (513, 128, 8), (40, 8, 520), (2049, 192, 1288), (700, 12, 600), (90, 20, 4000), (32, 257, 300),
+          (33, 2048, 136), (64, 1536, 1001), (200, 4100, 72), (260, 1030, 515)]
 
 
 @pytest.mark.gpu
@@ -370,7 +371,7 @@ def test_given_workspace():
 # ---------------------------------------------------------------- refusals (no GPU)
 def _forward(**over):
     a = N.GdnGluArgs()
-    a.rows, a.dim, a.inner, a.dtype = 20, 24, 16, N.DTYPE_BF16
+    a.rows, a.dim, a.inner, a.dtype = 40, 24, 16, N.DTYPE_BF16
     for f in ("x", "w_gate", "w_up", "out"):
         setattr(a, f, FAKE)
     for k, v in over.items():
