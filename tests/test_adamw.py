@@ -131,6 +131,7 @@ LISTS = [
     ([100000, 1, 17, 65536, 12345], ("f32", "f16", "bf16"), ("f32", "bf16")),
     ([300 + i for i in range(33)], ("f32", "bf16"), ("f16",)),
     ([64 + i % 7 for i in range(1000)], ("f16", "f32", "bf16"), ("f16", "f32")),
+    ([70 + i % 300 for i in range(900)], ("bf16",), ("f32",)),  # several tables of one kind
     ([5000001], ("f32",), ("f32",)),
     ([9000000, 7], ("bf16",), ("bf16",)),
 ]
@@ -308,6 +309,26 @@ def test_captured_steps_equal_eager_ones(eight):
     torch.cuda.synchronize()
     assert int(step) == 4
     assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a.tensors(), b.tensors()))
+
+
+@pytest.mark.gpu
+def test_a_copy_of_an_fp32_parameter():
+    """It is the copy that the step is taken on; the parameter receives it."""
+    for eight in (False, True):
+        c = Case(14, [700, 30], ("f32",), ("bf16",), eight=eight)
+        c.w = [p + 0.25 for p in c.p]
+        c.before["w"] = [w.clone() for w in c.w]
+        c.p[0].fill_(float("nan"))
+        c.run().check()
+        assert all(torch.equal(p, w) for p, w in zip(c.p, c.w))
+
+
+@pytest.mark.gpu
+def test_empty_lists():
+    import gated_delta_rule_gate_gb300 as g
+    assert g.gdn_adamw([], [], [], [], 1) is None
+    e = torch.zeros(0, device="cuda")
+    assert g.gdn_adamw([e], [e], [e], [e], 1) is None
 
 
 @pytest.mark.gpu

@@ -329,6 +329,51 @@ def test_same_bits_on_any_stream_and_from_a_graph():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(1, 2048, 200), (30, 520, 77), (64, 2048, 136), (90, 63, 41)])
+def test_every_path_from_a_graph(shape):
+    """Few tokens, shares over stretches of K, copied operands: replayed on new inputs, and two
+    graphs of the same call in turn."""
+    import gated_delta_rule_gate_gb300 as gdn
+    x, wg, wu, d = draw(*shape, "bf16", seed=8)
+
+    def all_of():
+        out, gates = gdn.gdn_glu(x, wg, wu, want_gates=True)
+        return [out, *gdn.gdn_glu_backward(d, x, wg, wu, gates)]
+
+    all_of()
+    torch.cuda.synchronize()
+    graphs, results = [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            results.append(all_of())
+    for turn in range(3):
+        x.mul_(-0.5), wg.mul_(1.25), d.add_(0.125)
+        want = all_of()
+        for graph, got in zip(graphs, results):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+def test_largest_values():
+    """fp16 results beyond its range are infinite, gates beyond it are kept as they are."""
+    import gated_delta_rule_gate_gb300 as gdn
+    for T in (4, 50):
+        x = torch.full((T, 64), 60.0, dtype=torch.float16, device="cuda")
+        w = torch.full((24, 64), 60.0, dtype=torch.float16, device="cuda")
+        out, gates = gdn.gdn_glu(x, w, w, want_gates=True)
+        assert bool(out.isinf().all()) and bool((unpack(gates, 24) == 230400.0).all())
+        d = torch.full((T, 24), 2.0 ** -14, dtype=torch.float16, device="cuda")
+        b = gdn.gdn_glu_backward(d, x, w, w, gates)
+        # d_g = d_u = 2^-14 230400 = 14.0625, an fp16 number; the sums are exact in fp32
+        rounded = lambda v: float(torch.tensor(v, dtype=torch.float32).half())
+        assert bool((b.dx == rounded(2 * 24 * 60 * 14.0625)).all())
+        assert bool((b.d_w_gate == rounded(T * 60 * 14.0625)).all()) and torch.equal(b.d_w_gate, b.d_w_up)
+
+
+@pytest.mark.gpu
 def test_two_calls_at_once():
     """On two streams, each with buffers of its own."""
     import gated_delta_rule_gate_gb300 as gdn
