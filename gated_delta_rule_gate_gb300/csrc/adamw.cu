@@ -116,7 +116,8 @@ __device__ __forceinline__ float2 mix(float a, float2 b, float c, float2 d, floa
     return __fadd2_rn(__ffma2_rn(both(a), b, both(zero)), __ffma2_rn(both(c), d, both(zero)));
 }
 // A root that is up to 2 ulp off, rounded: one step of Newton's method, whose residual
-// v - s^2 an fma gives without error (Markstein 1990).  2^26 bf16 elements with 8-bit states take
+// v - s^2 an fma gives without error (Markstein 1990; of v below 2^-104, gradients of 1e-15, the
+// residual is rounded too and the root within an ulp).  2^26 bf16 elements with 8-bit states take
 // 116 us so, and 124 with __fsqrt_rn.
 __device__ __forceinline__ float2 rounded_root(float2 s, float2 v) {
     const float2 r = __ffma2_rn(__fmul2_rn(both(-1.f), s), s, v);

@@ -152,12 +152,12 @@ gdn_status validate_grad(const gdn_glu_grad_args *a) {
     return GDN_OK;
 }
 
-// A workspace given out piece by piece, in multiples of 256 bytes; without memory it counts.
+// A workspace given out piece by piece, in multiples of 256 bytes (before it is known to suffice).
 struct Pieces {
     unsigned char *base;
     size_t used = 0;
     void *take(int64_t values) {
-        void *p = base ? base + used : nullptr;
+        void *p = reinterpret_cast<void *>(reinterpret_cast<uintptr_t>(base) + used);
         used += ((size_t)values * 2 + 255) / 256 * 256;
         return p;
     }
@@ -219,16 +219,22 @@ void sizes(Job *j, int64_t rows, int cols, int width, int results, int64_t depth
 struct Cut {
     int64_t tiles = 0, steps = 0;  // in one stretch
     double values = 0;             // of all results
-    bool into(int n) const { return n == 1 || (steps / n >= 8 && (steps + (steps + n - 1) / n - 1) / ((steps + n - 1) / n) == n); }
+    // into n stretches that are worth it: of eight steps at least, none of them empty, and
+    // not where the tiles alone fill the device four times
+    bool into(int n, int64_t device) const {
+        if (n == 1) return true;
+        const int64_t per = (steps + n - 1) / n;
+        return tiles > 0 && tiles < 4 * device && steps / n >= 8 && (steps + per - 1) / per == n;
+    }
 };
 void choose_parts(const Cut &first, const Cut &second, int *n1, int *n2) {
     static const int counts[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, kMostParts};
     const int64_t device = gdn::sm_count() / 2;
     double least = -1;
     for (const int i : counts) {
-        if (!first.into(i) || (first.tiles == 0 && i > 1)) continue;
+        if (!first.into(i, device)) continue;
         for (const int j : counts) {
-            if (!second.into(j) || (second.tiles == 0 && j > 1)) continue;
+            if (!second.into(j, device)) continue;
             const int64_t a = first.tiles * i, all = a + second.tiles * j;
             const double ta = (double)((first.steps + i - 1) / i + 6), tb = (double)((second.steps + j - 1) / j + 6);
             double longest = 0;
@@ -334,9 +340,9 @@ size_t gdn_glu_workspace_size(const gdn_glu_args *a) {
 gdn_status gdn_glu(const gdn_glu_args *a, void *ws, size_t ws_bytes, gdn_stream stream) {
     gdn_status st = validate(a);
     if (st != GDN_OK) return st;
-    if ((st = check_workspace(ws, ws_bytes, plan(a, nullptr).bytes)) != GDN_OK) return st;
-    if (a->rows == 0) return gdn::ok();
     const ForwardPlan f = plan(a, ws);
+    if ((st = check_workspace(ws, ws_bytes, f.bytes)) != GDN_OK) return st;
+    if (a->rows == 0) return gdn::ok();
     const bool bf16 = a->dtype == GDN_DTYPE_BF16;
     const int64_t os = or_dense(a->out_stride, a->inner);
     cudaStream_t s = (cudaStream_t)stream;
@@ -387,7 +393,8 @@ size_t gdn_glu_backward_workspace_size(const gdn_glu_grad_args *a) {
 gdn_status gdn_glu_backward(const gdn_glu_grad_args *a, void *ws, size_t ws_bytes, gdn_stream stream) {
     gdn_status st = validate_grad(a);
     if (st != GDN_OK) return st;
-    if ((st = check_workspace(ws, ws_bytes, plan_grad(a, nullptr).bytes)) != GDN_OK) return st;
+    const BackwardPlan b = plan_grad(a, ws);
+    if ((st = check_workspace(ws, ws_bytes, b.bytes)) != GDN_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
     const int64_t T = a->rows;
     const int D = a->dim, F = a->inner;
@@ -398,7 +405,6 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *a, void *ws, size_t ws_byte
         if (a->d_w_up && e == cudaSuccess) e = cudaMemsetAsync(a->d_w_up, 0, bytes, s);
         return gdn::cuda_status(e);
     }
-    const BackwardPlan b = plan_grad(a, ws);
     const bool bf16 = a->dtype == GDN_DTYPE_BF16;
     Backward p = {};
     Job &in = p.job[0], &w = p.job[1];
@@ -423,7 +429,8 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *a, void *ws, size_t ws_byte
         if (w.parts > 1) joins.j[joins.count++] = join_of(w, b.w_shares);
     }
     GateGrad g = {};
-    g.d_out = a->d_out, g.gates = static_cast<const unsigned char *>(a->gates), g.dg = const_cast<void *>(b.dg.at), g.du = const_cast<void *>(b.du.at);
+    g.d_out = a->d_out, g.gates = static_cast<const unsigned char *>(a->gates);
+    g.dg = const_cast<void *>(b.dg.at), g.du = const_cast<void *>(b.du.at);
     g.rows = T, g.dos = or_dense(a->d_out_stride, F), g.F = F, g.Fp = (int)padded(F), g.Fg = gate_columns(F);
     g.act = a->activation;
     g.words = F % 8 == 0 && lines(a->d_out, g.dos);

@@ -667,7 +667,8 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *args, void *workspace, size
  * counts (0: skipped) and gdn_dtypes (F32, F16, BF16).  params, exp_avg (m), exp_avg_sq
  * (v) and their scales are updated in place; grads are read.  master (NULL: none, or
  * NULL for a tensor that has none) are fp32 copies of the weights: the step is then
- * taken on the copy, and params[i], which is not read, receives its rounding.
+ * taken on the copy, and params[i], which is not read, receives its rounding.  (A 16-bit
+ * weight without a copy keeps nothing of a step that is less than half its last place.)
  *
  * state_dtype F32 keeps m and v as they are.  E4M3 keeps m and r = sqrt(v) in blocks of
  * GDN_ADAMW_BLOCK elements of a tensor (the last may be short), each with an fp32 scale
