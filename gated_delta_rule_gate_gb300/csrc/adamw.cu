@@ -23,8 +23,8 @@ namespace gdn {
 namespace adamw {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMany = 400, kFew = 32;
-constexpr int kStretch = 8;
+constexpr int kMany = 400, kFew = 32;  // tensors of a table: one of few keeps the launch's argument small
+constexpr int kStretch = 8;            // rows of a warp (16: 119 us for 113, 2^26 elements with 8-bit states)
 constexpr int kRow = GDN_ADAMW_BLOCK;
 constexpr int kGroups = kRow / 128;  // of four adjacent elements a lane
 static_assert(kRow == 256, "a lane's two groups of four");

@@ -215,7 +215,8 @@ void sizes(Job *j, int64_t rows, int cols, int width, int results, int64_t depth
 // time least, in K-steps (0.27 us) of a pair of blocks.  A tile costs some six steps beside its
 // own; shares are written and read in fp32, and a launch is added.  Pairs of blocks take
 // tiles in turn, the first job's first, so the longest time is that of the first pair, or of
-// the first one that has a tile less of the first job.
+// the first one that has a tile less of the first job.  (64 tokens x 4096 x 1024 fp16, 8 tiles: 14.1 us in
+// eight stretches, 24.5 in one; 256 x 4096 x 8192, 64 tiles, stays in one, 31.)
 struct Cut {
     int64_t tiles = 0, steps = 0;  // in one stretch
     double values = 0;             // of all results

@@ -852,6 +852,14 @@ PyObject *py_adamw(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kw
     std::vector<int64_t> sizes(N);
     std::vector<int32_t> ptypes(N), gtypes(N);
     std::vector<const Tensor *> outputs;
+    outputs.reserve(6 * N);
+    // one_device() of lists
+    auto at_home = [&](const Tensor *t, const char *what) {
+        if (t && t->device() != device && t->is_cuda() && device.is_cuda())
+            refuse(PyExc_ValueError, "%s is on %s, not on %s as the rest of the call's device tensors", what,
+                   t->device().str().c_str(), device.str().c_str());
+    };
+    at_home(step, "step"), at_home(lr, "lr"), at_home(norm, "grad_norm"), at_home(err, "error_word");
     auto maybe = [](const std::optional<Sequence> &s, size_t i, const char *what) {
         return s ? tensor(PySequence_Fast_GET_ITEM(s->s, i) == Py_None ? nullptr : PySequence_Fast_GET_ITEM(s->s, i), what)
                  : nullptr;
@@ -862,9 +870,9 @@ PyObject *py_adamw(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kw
         const Tensor *tms = mss ? &mss->at(i, "an exp_avg_scales") : nullptr;
         const Tensor *tvs = vss ? &vss->at(i, "an exp_avg_sq_scales") : nullptr;
         const Tensor *tw = maybe(masters, i, "a master copy");
-        one_device(params.at(0, "a parameter"), {{&tp, "a parameter"}, {&tg, "a gradient"}, {&tm, "an exp_avg"},
-                   {&tv, "an exp_avg_sq"}, {tms, "an exp_avg_scales"}, {tvs, "an exp_avg_sq_scales"},
-                   {tw, "a master copy"}, {step, "step"}, {lr, "lr"}, {norm, "grad_norm"}, {err, "error_word"}});
+        at_home(&tp, "a parameter"), at_home(&tg, "a gradient"), at_home(&tm, "an exp_avg");
+        at_home(&tv, "an exp_avg_sq"), at_home(tms, "an exp_avg_scales"), at_home(tvs, "an exp_avg_sq_scales");
+        at_home(tw, "a master copy");
         const IntArrayRef shape = tp.sizes();
         ptypes[i] = code(tp, "a parameter"), gtypes[i] = code(tg, "a gradient");
         sizes[i] = tp.numel();
