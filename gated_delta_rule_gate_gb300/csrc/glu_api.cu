@@ -312,12 +312,11 @@ BackwardPlan plan_grad(const gdn_glu_grad_args *a, void *ws) {
         b.wg = operand(a->w_gate, F, a->dim, a->dim, &pieces);
         b.wu = operand(a->w_up, F, a->dim, a->dim, &pieces);
     }
-    Cut in, w;
-    if (a->dx) in = cut_of(a->rows, a->dim, 1, F, 2);
-    if (a->d_w_gate) w = cut_of(F, a->dim, 2, a->rows, 1);
-    choose_parts(in, w, &b.in_parts, &b.w_parts);
-    b.in_shares = pieces.take(b.in_parts > 1 ? 2 * a->rows * Dp * b.in_parts : 0);
-    b.w_shares = pieces.take(b.w_parts > 1 ? 4 * F * Dp * b.w_parts : 0);
+    // As if all gradients were wanted, whichever are: the order of a gradient's sum is promised not
+    // to depend on that.
+    choose_parts(cut_of(a->rows, a->dim, 1, F, 2), cut_of(F, a->dim, 2, a->rows, 1), &b.in_parts, &b.w_parts);
+    b.in_shares = pieces.take(a->dx && b.in_parts > 1 ? 2 * a->rows * Dp * b.in_parts : 0);
+    b.w_shares = pieces.take(a->d_w_gate && b.w_parts > 1 ? 4 * F * Dp * b.w_parts : 0);
     b.bytes = pieces.used;
     return b;
 }

@@ -619,7 +619,8 @@ gdn_status gdn_glu(const gdn_glu_args *args, void *workspace, size_t workspace_b
  *     dx = d_g w_gate + d_u w_up,   d_w_gate = d_g^T x,   d_w_up = d_u^T x
  *
  * d_g and d_u are formed in fp32 and rounded to dtype, as operands of the products; sums
- * are fp32, in an order that sizes alone decide.  dx, and d_w_gate with d_w_up, may be NULL
+ * are fp32, in an order that the sizes and the device's number of SMs decide, whichever
+ * gradients are wanted.  dx, and d_w_gate with d_w_up, may be NULL
  * (not wanted; what only they need may then be NULL too).  d_out_stride and dx_stride are
  * elements from row to row (0: without a gap); gates, the weights and their gradients are
  * contiguous.  Without rows the weights' gradients are zero.  Outputs overlap no input.
