@@ -18,8 +18,17 @@ constexpr float kRootHalf = 0.70710678118654752f;    // sqrt(1 / 2)
 constexpr float kPhi0 = 0.39894228040143268f;        // 1 / sqrt(2 pi)
 constexpr float kTanhScale = 1.5957691216057308f;    // 2 sqrt(2 / pi)
 constexpr float kTanhCube = 0.044715f;
+constexpr float kHalfLog2E = 0.72134752044448170f;   // log2(e) / 2
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// 1 / (1 + e^-x) as 2^-24 / (2^-24 + h^2) with h = 2^-12 e^(-x / 2), within 2^-20 of the value for |x| up to
+// 4, 2^-18 down to -87 (the rounding of the exponent), and two steps of 2^-149 below.  The factors are
+// there for x below -87, where 1 + e^-x is above 2^126, of which the fast reciprocal is 0, or no number.
+__device__ __forceinline__ float sigmoid(float x) {
+    float h, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(fmaf(x, -kHalfLog2E, -12.f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(h, h, 0x1p-24f)));
+    return r * 0x1p-24f;
+}
 
 // Calls f with the activation as a constant: chosen once for many values.
 template <typename F>
