@@ -142,13 +142,19 @@ __device__ __forceinline__ float2 update(const Step &st, const Factors &f, float
 struct Scale {
     float s, inv;
 };
+// The larger one, or NaN where there is one: a block with a NaN says so by its scale.
+__device__ __forceinline__ float larger(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 __device__ __forceinline__ Scale scale_of(const float2 (&y)[4]) {
-    float a = 0.f;
+    float a = 0x1p-100f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a = fmaxf(a, fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
-    // numbers that are not negative compare as their bits do
+    for (int i = 0; i < 4; ++i) a = larger(a, larger(fabsf(y[i].x), fabsf(y[i].y)));
+    // numbers that are not negative compare as their bits do, and this NaN (0x7fffffff) is above them
     a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
-    const float s = fmaxf(a, 0x1p-100f) * (1.f / 448.f);
+    const float s = a * (1.f / 448.f);
     return {s, __frcp_rn(s)};
 }
 // y / s as a division rounds it: one product and two fma (Markstein), s.inv being rounded.

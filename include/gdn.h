@@ -679,7 +679,8 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *args, void *workspace, size
  * where there was a gradient.  Each product, sum, root and quotient on the way there is
  * rounded to fp32 (k as max_norm times the reciprocal).  The step itself takes m and v
  * before they are codes.  Codes and scales of zero are states of zero.  (A gradient that is
- * infinite makes its block's states NaN; grad_norm keeps such a step from being taken.)
+ * infinite or NaN makes both states of its block NaN, one whose square is beyond fp32 those of
+ * exp_avg_sq, with a scale that is not finite; grad_norm keeps such a step from being taken.)
  *
  * step_device (or NULL) is the step's number in device memory, in place of `step`, and
  * lr_device the rate, in place of `lr`: a captured graph is replayed with new ones.  A
