@@ -55,9 +55,12 @@ struct Step {
     const float *norm;
     int32_t *err;
 };
-// The same for every element.
+// The same for every element.  The divisor of m is taken 2^24 times as large, and the rate with it: where
+// a root is 0 the divisor is eps, which may be a subnormal number, of which the fast reciprocal
+// is infinite.  (Any other root is above 2^-75.)
+constexpr float kUp = 0x1p24f;
 struct Factors {
-    float clip, rate, decay, unroot, eps;
+    float clip, rate, decay, unroot, eps;  // rate, unroot and eps kUp times as large
 };
 
 template <int MAX>
@@ -103,7 +106,7 @@ __device__ __forceinline__ float root_of(float v) {
     asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
-// Of a number that is not subnormal (a root is above 2^-75, unless it is 0).
+// Of a number that is not subnormal.
 __device__ __forceinline__ float reciprocal(float v) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -373,10 +376,10 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? 4 : 2) adamw_kernel(const __
         c1 = -expm1f(k * st.log_beta1);
         root2 = sqrtf(-expm1f(k * st.log_beta2));
     }
-    f.rate = __fdiv_rn(lr, c1);
+    f.rate = kUp * __fdiv_rn(lr, c1);
     f.decay = lr * st.weight_decay;
-    f.unroot = __fdiv_rn(1.f, root2);
-    f.eps = st.eps;
+    f.unroot = __fdiv_rn(kUp, root2);
+    f.eps = kUp * st.eps;
     using Rows = Whole<EIGHT, P, MASTER, G>;
     constexpr int N = EIGHT ? Rows::kSlots : 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -580,6 +583,7 @@ extern "C" gdn_status gdn_adamw(const gdn_adamw_args *a, gdn_stream stream) {
     s.beta1 = (float)a->beta1, s.rest1 = (float)(1 - a->beta1);
     s.beta2 = (float)a->beta2, s.rest2 = (float)(1 - a->beta2);
     s.lr = (float)a->lr, s.weight_decay = (float)a->weight_decay, s.eps = (float)a->eps;
+    if (a->eps > 0) s.eps = fmaxf(s.eps, 0x1p-149f);  // an eps stays one
     s.zero = -0.f;
     s.max_norm = (float)a->max_norm, s.norm_eps = (float)a->norm_eps;
     // beta = 0 has logarithm -inf, and 1 - beta^t = 1

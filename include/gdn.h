@@ -662,7 +662,7 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *args, void *workspace, size
  * grad_norm is a device float, the norm of all gradients: gdn_grad_clip with the largest
  * max_norm leaves them as they are and gives it, and the clip is then made here, where
  * they are read anyway.  A norm that is not finite leaves every tensor as it is and sets
- * GDN_DEVERR_NONFINITE.
+ * GDN_DEVERR_NONFINITE.  (eps is rounded to fp32, but not to 0 unless it is.)
  *
  * The arrays are HOST memory, read before the call returns: device pointers, element
  * counts (0: skipped) and gdn_dtypes (F32, F16, BF16).  params, exp_avg (m), exp_avg_sq
