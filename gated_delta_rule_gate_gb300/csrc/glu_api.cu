@@ -6,6 +6,7 @@
 
 #include "glu_launch.h"
 #include "launch.h"
+#include "overlap.h"
 #include "ptx.cuh"
 #include "status.h"
 
@@ -321,6 +322,24 @@ BackwardPlan plan_grad(const gdn_glu_grad_args *a, void *ws) {
     return b;
 }
 
+// Results that the kernels write while they still read what they would lie on.
+struct Operands {
+    const char *name;
+    gdn::Span span;
+};
+gdn_status check_apart(std::initializer_list<Operands> results, std::initializer_list<Operands> read) {
+    for (const Operands *r = results.begin(); r != results.end(); ++r) {
+        for (const Operands &o : read)
+            if (gdn::overlap(r->span, o.span)) return fail(GDN_ERR_INVALID, "%s overlaps %s", r->name, o.name);
+        for (const Operands *o = r + 1; o != results.end(); ++o)
+            if (gdn::overlap(r->span, o->span)) return fail(GDN_ERR_INVALID, "%s overlaps %s", r->name, o->name);
+    }
+    return GDN_OK;
+}
+gdn::Span span_of(const void *p, int64_t rows, int64_t stride, int cols) {
+    return {p, rows, 2 * or_dense(stride, cols), 2 * (int64_t)cols};
+}
+
 gdn_status check_workspace(const void *ws, size_t have, size_t need) {
     if (need > 0 && (ws == nullptr || have < need || !aligned(ws, 16)))
         return fail(GDN_ERR_WORKSPACE, "workspace needs %zu bytes, 16-byte aligned (got %zu)", need, have);
@@ -343,6 +362,13 @@ gdn_status gdn_glu(const gdn_glu_args *a, void *ws, size_t ws_bytes, gdn_stream 
     const ForwardPlan f = plan(a, ws);
     if ((st = check_workspace(ws, ws_bytes, f.bytes)) != GDN_OK) return st;
     if (a->rows == 0) return gdn::ok();
+    const int64_t weight = 2 * (int64_t)a->inner * a->dim;
+    st = check_apart({{"out", span_of(a->out, a->rows, a->out_stride, a->inner)},
+                      {"gates", gdn::block_of(a->gates, a->rows * gates_row(gate_columns(a->inner)))}},
+                     {{"x", span_of(a->x, a->rows, a->x_stride, a->dim)},
+                      {"w_gate", gdn::block_of(a->w_gate, weight)},
+                      {"w_up", gdn::block_of(a->w_up, weight)}});
+    if (st != GDN_OK) return st;
     const bool bf16 = a->dtype == GDN_DTYPE_BF16;
     const int64_t os = or_dense(a->out_stride, a->inner);
     cudaStream_t s = (cudaStream_t)stream;
@@ -398,6 +424,15 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *a, void *ws, size_t ws_byte
     cudaStream_t s = (cudaStream_t)stream;
     const int64_t T = a->rows;
     const int D = a->dim, F = a->inner;
+    // d_out and gates have been read before any result is written
+    const int64_t weight = 2 * (int64_t)F * D;
+    st = check_apart({{"dx", span_of(a->dx, T, a->dx_stride, D)},
+                      {"d_w_gate", gdn::block_of(a->d_w_gate, weight)},
+                      {"d_w_up", gdn::block_of(a->d_w_up, weight)}},
+                     {{"x", span_of(a->d_w_gate ? a->x : nullptr, T, a->x_stride, D)},
+                      {"w_gate", gdn::block_of(a->dx && T ? a->w_gate : nullptr, weight)},
+                      {"w_up", gdn::block_of(a->dx && T ? a->w_up : nullptr, weight)}});
+    if (st != GDN_OK) return st;
     cudaError_t e = cudaSuccess;
     if (T == 0) {  // sums over nothing
         const size_t bytes = (size_t)F * D * 2;

@@ -585,7 +585,7 @@ typedef enum gdn_activation {
  * 24 bits (sign, 8 bits of exponent, 15 of fraction; 16 would cost the gradients as much
  * again as their own roundings): GDN_GLU_GATES_ROW(inner) bytes a row, contiguous and
  * aligned to 16 bytes.  A few tokens (serving) take a kernel of their own.  out and gates
- * overlap no input.
+ * overlap no input and not one another (GDN_ERR_INVALID).
  *
  * The workspace is device memory of gdn_glu_workspace_size() bytes, 16-byte aligned (for
  * operands whose rows are no words of 16 bytes, and for shares of results where they are few);
@@ -623,7 +623,9 @@ gdn_status gdn_glu(const gdn_glu_args *args, void *workspace, size_t workspace_b
  * gradients are wanted.  dx, and d_w_gate with d_w_up, may be NULL
  * (not wanted; what only they need may then be NULL too).  d_out_stride and dx_stride are
  * elements from row to row (0: without a gap); gates, the weights and their gradients are
- * contiguous.  Without rows the weights' gradients are zero.  Outputs overlap no input.
+ * contiguous.  Without rows the weights' gradients are zero.  Outputs overlap neither one
+ * another nor what the products read, x, w_gate and w_up (GDN_ERR_INVALID); d_out and gates have been
+ * read before an output is written.
  */
 typedef struct gdn_glu_grad_args {
     int64_t rows;
