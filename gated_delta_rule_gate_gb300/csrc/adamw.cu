@@ -9,9 +9,12 @@
 // with fp32 copies and states (28 bytes each) 1636 us, 6.9 TB/s; with 8-bit states (10 bytes
 // each) 676 us, 6.0 TB/s, where the 52 instructions of an element fill 78 % of the issue slots.
 #include <math.h>
+#include <string.h>
 
 #include <cuda_fp8.h>
 
+#include <memory>
+#include <new>
 #include <utility>
 
 #include "launch.h"
@@ -528,6 +531,51 @@ using gdn::fail;
 
 bool finite_from(double v, double least) { return isfinite(v) && v >= least; }
 
+// No two tensors that a step writes begin at one address: one that is listed twice (tied weights, a state
+// for all) would be stepped by two warps at once.  By a table of the addresses, which costs the
+// host 10 ns a weight; sorting them, to see parts of tensors too, took 50 to 120.
+gdn_status check_apart(const gdn_adamw_args *a) {
+    const struct {
+        const char *name;
+        const void *const *at;
+    } lists[] = {{"params", (const void *const *)a->params},
+                 {"exp_avg", (const void *const *)a->exp_avg},
+                 {"exp_avg_sq", (const void *const *)a->exp_avg_sq},
+                 {"exp_avg_scales", (const void *const *)a->exp_avg_scales},
+                 {"exp_avg_sq_scales", (const void *const *)a->exp_avg_sq_scales},
+                 {"master", (const void *const *)a->master}};
+    int64_t most = 0;
+    for (const auto &l : lists) most += l.at ? a->count : 0;
+    int bits = 6;
+    while ((1LL << bits) < most + most / 2) ++bits;  // places, a third of them empty at least
+    constexpr int kSome = 9;
+    uintptr_t some[1 << kSome], *seen = some;
+    std::unique_ptr<uintptr_t[]> more;
+    if (bits > kSome) {
+        more.reset(new (std::nothrow) uintptr_t[(size_t)1 << bits]);
+        seen = more.get();
+        if (!seen) return fail(GDN_ERR_CUDA, "no host memory for %d tensors", a->count);
+    }
+    memset(seen, 0, sizeof(uintptr_t) << bits);
+    for (const auto &l : lists) {
+        if (!l.at) continue;
+        for (int i = 0; i < a->count; ++i) {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(l.at[i]);
+            if (!at || a->sizes[i] == 0) continue;
+            uint64_t place = (uint64_t)at * 0x9e3779b97f4a7c15u >> (64 - bits);
+            while (seen[place] && seen[place] != at) place = (place + 1) & ((1ull << bits) - 1);
+            if (seen[place]) {
+                for (const auto &o : lists)
+                    for (int k = 0; o.at && k < a->count; ++k)
+                        if (a->sizes[k] > 0 && o.at[k] == l.at[i])
+                            return fail(GDN_ERR_INVALID, "%s[%d] is %s[%d]: one tensor twice", l.name, i, o.name, k);
+            }
+            seen[place] = at;
+        }
+    }
+    return GDN_OK;
+}
+
 gdn_status validate(const gdn_adamw_args *a) {
     if (!a) return fail(GDN_ERR_INVALID, "args is NULL");
     if (a->count < 0) return fail(GDN_ERR_INVALID, "count must be >= 0");
@@ -571,7 +619,7 @@ gdn_status validate(const gdn_adamw_args *a) {
     if (!aligned(a->step_device, 8) || !aligned(a->lr_device, 4) || !aligned(a->grad_norm, 4) ||
         !aligned(a->error_word, 4))
         return fail(GDN_ERR_INVALID, "a pointer is not aligned to its element size");
-    return GDN_OK;
+    return check_apart(a);
 }
 
 }  // namespace

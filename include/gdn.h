@@ -686,7 +686,8 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *args, void *workspace, size
  *
  * step_device (or NULL) is the step's number in device memory, in place of `step`, and
  * lr_device the rate, in place of `lr`: a captured graph is replayed with new ones.  A
- * number below 1 there counts as 1.  No tensor overlaps another.
+ * number below 1 there counts as 1.  No tensor overlaps another (GDN_ERR_INVALID where two
+ * that are updated begin at one address: tied weights listed twice, say).
  */
 typedef struct gdn_adamw_args {
     int32_t count;
