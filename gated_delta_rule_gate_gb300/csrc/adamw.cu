@@ -474,7 +474,8 @@ int fill(const gdn_adamw_args *a, int i, int kind, Table<MAX> *tab) {
         tab->rows += (t.n + kRow - 1) / kRow;
     }
     // rows of a warp: so few that they reach all SMs (six blocks each), up to kStretch
-    int64_t each = (tab->rows + kWarps * 152 * 6 - 1) / (kWarps * 152 * 6);
+    const int64_t warps = (int64_t)kWarps * sm_count() * 6;
+    int64_t each = (tab->rows + warps - 1) / warps;
     each = each < 1 ? 1 : each > kStretch ? kStretch : each;
     while (tab->rows / (each * kWarps) >= 1LL << 31) each *= 2;
     tab->stretch = (int)each * kWarps;
