@@ -15,6 +15,10 @@
 // 16 a block, 4 words    8.7    14.1    22.1
 //  8 a block, 8 words    6.6    14.8    24.8
 //  8 a block, 4 words   10.8    15.5    25.8
+// The same of more tokens, with weights that L2 does not hold, 16 features a block and 8:
+// dim x inner        2048 x 1536  4096 x 2432  4096 x 4864  2048 x 6144  4096 x 8192
+// 16 tokens           6.6   4.7   10.6   8.4   15.5  15.6   13.8  12.0   25.8  27.1
+// 32 tokens           8.8   6.0   12.5  10.2   16.4  19.0   16.0  15.6   28.3  34.6
 // 8 x 4096 x 8192 bf16: 22.4 us, 6.0 TB/s.
 #pragma once
 

@@ -89,8 +89,12 @@ struct ForwardJoin {
     int F, cs, Fg, parts, act, words;  // words: groups of four outputs are
 };
 
-// Up to so many tokens take the kernel of few: 32 x 2048 x 2048 fp16 6.2 us (15.2 in the tensor cores'
-// tiles), x 4096 x 4864 16.6 (25.3), x 4096 x 8192 28.4 (28.4).
+// Up to so many tokens take the kernel of few.  32 tokens, fp16, weights that L2 does not hold, us:
+// dim x inner            2048 x 1536  2048 x 2048  4096 x 1024  4096 x 4864  2048 x 6144  4096 x 8192
+// this kernel                6.0          6.1          9.3          16.4         16.0         28.3
+// the tensor cores' tiles   11.5         12.2         12.8          21.6         16.1         29.0
+// (33 tokens in the tiles   11.7         12.5         13.1          21.8         16.2         29.1)
+// So the border is where wide layers cross; narrow ones would gain from this kernel beyond it.
 constexpr int kFewTokens = 32;
 
 cudaError_t launch_forward_f16(const ForwardArgs &p, bool keep, cudaStream_t stream);

@@ -18,7 +18,7 @@
 //
 // 16384 x 2048 x 6144 bf16: forward 430 us alone (1.92 PFLOP/s) and 496 in a row of them, which
 // the card's power bounds (1.66); the training pass 1764 with its element-wise part.  With few
-// K-steps a tile's results bound it: 32768 x 512 x 1536 72 us (1.43), with kept gates 102
+// K-steps a tile's results bound it: 32768 x 512 x 1536 69 us (1.49), with kept gates 101
 // (they are 300 MB).
 //
 // Where there are few tiles, each is cut into stretches of K, whose sums go to memory in

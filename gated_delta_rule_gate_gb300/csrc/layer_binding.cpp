@@ -1009,8 +1009,8 @@ PyMethodDef methods[] = {
     {"gdn_glu", FAST(py_glu),
      "gdn_glu($module, x, w_gate, w_up, *, activation='silu', want_gates=False, out=None, error_word=None, "
      "workspace=None, stream=None)\n--\n\n"
-     "The gated half of a feed-forward block in one kernel: with g = x w_gate^T and\n"
-     "u = x w_up^T, out = act(g) u.  x is [..., dim] (its rows may be columns of wider\n"
+     "The gated half of a feed-forward block: with g = x w_gate^T and\n"
+     "u = x w_up^T, out = act(g) u, both projections and what joins them in one kernel.  x is [..., dim] (its rows may be columns of wider\n"
      "ones), the weights [inner, dim] (halves of one fused weight, say), all of one dtype,\n"
      "float16 or bfloat16; out is [..., inner].  activation is \"silu\", \"gelu\" (by the\n"
      "error function), \"gelu_tanh\", \"relu\" or \"sigmoid\".  Sums are fp32.  Returns\n"
@@ -1022,7 +1022,7 @@ PyMethodDef methods[] = {
      "want_d_weights=True, dx=None, d_w_gate=None, d_w_up=None, error_word=None, workspace=None, stream=None)\n--\n\n"
      "Gradients of gdn_glu for the gradient d_out of its output, at the gates that it\n"
      "returned: d_g = d_out u act'(g) and d_u = d_out act(g) (rounded to x's dtype as the\n"
-     "products' operands), dx = d_g w_gate + d_u w_up, d_w_gate = d_g^T x, d_w_up = d_u^T x.\n"
+     "products' operands, in float16 with its range), dx = d_g w_gate + d_u w_up, d_w_gate = d_g^T x, d_w_up = d_u^T x.\n"
      "Returns GluGradients(dx, d_w_gate, d_w_up), all in x's dtype; None where not wanted."},
     {"gdn_adamw", FAST(py_adamw),
      "gdn_adamw($module, params, grads, exp_avg, exp_avg_sq, step, *, lr=0.001, beta1=0.9, beta2=0.999, eps=1e-08, "
@@ -1041,7 +1041,8 @@ PyMethodDef methods[] = {
      "gdn_grad_clip(grads, 3e38) leaves them as they are and gives it.  A norm that is not finite leaves\n"
      "everything as it is and sets DEVERR_NONFINITE in error_word.  step (1 at first) may be\n"
      "an int64 tensor and lr a float32 one, of one element on the device, which a captured\n"
-     "graph reads anew at each replay.  All tensors are contiguous and none overlaps another."},
+     "graph reads anew at each replay.  All tensors are contiguous and none overlaps another; one that\n"
+     "is listed twice (tied weights) is refused."},
     {"bind", py_bind, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -63,7 +63,7 @@ typedef enum gdn_dtype {
     GDN_DTYPE_F32 = 0,
     GDN_DTYPE_F16 = 1,
     GDN_DTYPE_BF16 = 2, /* the recurrent-layer operators; the others decline it: GDN_ERR_UNSUPPORTED */
-    GDN_DTYPE_E4M3 = 3  /* 8 bits (4 of exponent, 3 of mantissa, largest 448): output of gdn_rmsnorm only */
+    GDN_DTYPE_E4M3 = 3  /* 8 bits (4 of exponent, 3 of mantissa, largest 448): output of gdn_rmsnorm, states of gdn_adamw */
 } gdn_dtype;
 
 /* "com.microsoft.GatedDeltaNet", Attributes, update_rule; GDN2 is the rule
@@ -574,7 +574,8 @@ typedef enum gdn_activation {
 
 /*
  * gdn_glu -- the gated half of a feed-forward block, both projections and what joins
- * them in one kernel, for each of `rows` tokens:
+ * them in one kernel, for each of `rows` tokens (with a launch before it that copies operands whose
+ * rows are no words of 16 bytes, and one behind it where tiles are so few that K is cut):
  *
  *     g = x w_gate^T,   u = x w_up^T,   out = act(g) u
  *
@@ -618,7 +619,8 @@ gdn_status gdn_glu(const gdn_glu_args *args, void *workspace, size_t workspace_b
  *     d_g = d_out u act'(g),   d_u = d_out act(g)
  *     dx = d_g w_gate + d_u w_up,   d_w_gate = d_g^T x,   d_w_up = d_u^T x
  *
- * d_g and d_u are formed in fp32 and rounded to dtype, as operands of the products; sums
+ * d_g and d_u are formed in fp32 and rounded to dtype, as operands of the products (F16 with its
+ * range: infinite above 65504, with fewer digits below 6e-5); sums
  * are fp32, in an order that the sizes and the device's number of SMs decide, whichever
  * gradients are wanted.  dx, and d_w_gate with d_w_up, may be NULL
  * (not wanted; what only they need may then be NULL too).  d_out_stride and dx_stride are
@@ -663,15 +665,16 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *args, void *workspace, size
  *
  * grad_norm is a device float, the norm of all gradients: gdn_grad_clip with the largest
  * max_norm leaves them as they are and gives it, and the clip is then made here, where
- * they are read anyway.  A norm that is not finite leaves every tensor as it is and sets
- * GDN_DEVERR_NONFINITE.  (eps is rounded to fp32, but not to 0 unless it is.)
+ * they are read anyway.  A norm that is not finite leaves every tensor as it is and, where there
+ * is one to step, sets GDN_DEVERR_NONFINITE.  (eps is rounded to fp32, but not to 0 unless it is.)
  *
  * The arrays are HOST memory, read before the call returns: device pointers, element
  * counts (0: skipped) and gdn_dtypes (F32, F16, BF16).  params, exp_avg (m), exp_avg_sq
  * (v) and their scales are updated in place; grads are read.  master (NULL: none, or
  * NULL for a tensor that has none) are fp32 copies of the weights: the step is then
  * taken on the copy, and params[i], which is not read, receives its rounding.  (A 16-bit
- * weight without a copy keeps nothing of a step that is less than half its last place.)
+ * weight without a copy keeps nothing of a step that is less than half its last place.)  Tensors at
+ * 16-byte addresses go by words; others, parts of a flat buffer say, element by element.
  *
  * state_dtype F32 keeps m and v as they are.  E4M3 keeps m and r = sqrt(v) in blocks of
  * GDN_ADAMW_BLOCK elements of a tensor (the last may be short), each with an fp32 scale
@@ -679,14 +682,16 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *args, void *workspace, size
  * ceil(size / GDN_ADAMW_BLOCK) of them: the code is the quotient by s rounded to e4m3, and
  * of an r above zero at least the smallest, 2^-9, so that no step divides by the eps alone
  * where there was a gradient.  Each product, sum, root and quotient on the way there is
- * rounded to fp32 (k as max_norm times the reciprocal).  The step itself takes m and v
+ * rounded to fp32 (k as max_norm times the reciprocal; a root of v below 2^-104, gradients of
+ * 1e-15, may be off by a step of fp32).  The step itself takes m and v
  * before they are codes.  Codes and scales of zero are states of zero.  (A gradient that is
  * infinite or NaN makes both states of its block NaN, one whose square is beyond fp32 those of
  * exp_avg_sq, with a scale that is not finite; grad_norm keeps such a step from being taken.)
  *
  * step_device (or NULL) is the step's number in device memory, in place of `step`, and
  * lr_device the rate, in place of `lr`: a captured graph is replayed with new ones.  A
- * number below 1 there counts as 1.  No tensor overlaps another (GDN_ERR_INVALID where two
+ * number below 1 there counts as 1.  (1 - beta^t is formed in fp32 of such a number, in 64 bits of
+ * `step`: weights may differ in their last bits, states do not.)  No tensor overlaps another (GDN_ERR_INVALID where two
  * that are updated begin at one address: tied weights listed twice, say).
  */
 typedef struct gdn_adamw_args {
