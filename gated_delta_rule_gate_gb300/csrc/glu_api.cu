@@ -336,8 +336,10 @@ gdn_status check_apart(std::initializer_list<Operands> results, std::initializer
     }
     return GDN_OK;
 }
+// (A distance that no memory has room for stays within 64 bits.)
 gdn::Span span_of(const void *p, int64_t rows, int64_t stride, int cols) {
-    return {p, rows, 2 * or_dense(stride, cols), 2 * (int64_t)cols};
+    const int64_t s = or_dense(stride, cols), most = (1LL << 61) / (rows > 0 ? rows : 1);
+    return {p, rows, 2 * (s < most ? s : most), 2 * (int64_t)cols};
 }
 
 gdn_status check_workspace(const void *ws, size_t have, size_t need) {

@@ -37,6 +37,8 @@ def backward(**over):
     (dict(out=AT + 32 * MB + 16 * 24 * 2 - 2), "out overlaps w_up"),
     (dict(gates=AT), "gates overlaps x"),
     (dict(gates=AT + 48 * MB), "out overlaps gates"),
+    (dict(out=AT, x_stride=1 << 62), "out overlaps x"),
+    (dict(out=AT, out_stride=(1 << 63) - 8), "out overlaps x"),
     # columns of one tensor that have one in common
     (dict(x_stride=48, out=AT + 23 * 2, out_stride=48), "out overlaps x"),
     # rows at unequal distances: the first row of out lies in the second of x
