@@ -565,6 +565,10 @@ gdn_status check_apart(const gdn_adamw_args *a) {
         for (int i = 0; i < a->count; ++i) {
             const uintptr_t at = reinterpret_cast<uintptr_t>(l.at[i]);
             if (!at || a->sizes[i] == 0) continue;
+            // an fp32 weight may be its own copy: both are given the same value by the same thread
+            if (l.at == (const void *const *)a->master && l.at[i] == a->params[i] &&
+                a->param_dtypes[i] == GDN_DTYPE_F32)
+                continue;
             uint64_t place = (uint64_t)at * 0x9e3779b97f4a7c15u >> (64 - bits);
             while (seen[place] && seen[place] != at) place = (place + 1) & ((1ull << bits) - 1);
             if (seen[place]) {

@@ -692,7 +692,8 @@ gdn_status gdn_glu_backward(const gdn_glu_grad_args *args, void *workspace, size
  * lr_device the rate, in place of `lr`: a captured graph is replayed with new ones.  A
  * number below 1 there counts as 1.  (1 - beta^t is formed in fp32 of such a number, in 64 bits of
  * `step`: weights may differ in their last bits, states do not.)  No tensor overlaps another (GDN_ERR_INVALID where two
- * that are updated begin at one address: tied weights listed twice, say).
+ * that are updated begin at one address: tied weights listed twice, say), but an F32 weight may be its own
+ * copy in master.
  */
 typedef struct gdn_adamw_args {
     int32_t count;

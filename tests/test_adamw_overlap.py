@@ -46,6 +46,28 @@ def test_refuses_one_tensor_for_two_parts(first, second):
     assert message == "%s[1] is %s[1]: one tensor twice" % (second, first)
 
 
+def test_a_16_bit_weight_is_not_its_own_copy():
+    at = apart(3)
+    at["master"][2] = at["params"][2]
+    status, message = call(3, [300] * 3, False, at)
+    assert status == N.GDN_ERR_INVALID and message == "master[2] is params[2]: one tensor twice"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("eight", [False, True])
+def test_an_fp32_weight_may_be_its_own_copy(eight):
+    """master = [p.float() for p in params] is that, where params are fp32."""
+    import torch
+    c, d = (adamw.Case(41, [700, 256, 30], ("f32", "bf16", "f32"), eight=eight, master=True) for _ in range(2))
+    c.w = [p if p.dtype == torch.float32 else w for p, w in zip(c.p, c.w)]
+    c.run(), d.run()
+    c.before["w"][0] = c.before["w"][2] = None
+    c.w[0] = c.w[2] = None
+    c.check()
+    for k in ("p", "m", "v"):
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(getattr(c, k), getattr(d, k)))
+
+
 @pytest.mark.gpu
 def test_parts_behind_one_another_are_taken():
     """Flat buffers in any order of their parts, a gradient used twice, and empty tensors anywhere."""
